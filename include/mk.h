@@ -306,6 +306,229 @@ mk_status mk_get_timestamps(mk_layer* layer, uint64_t* host_buf, size_t n);
 mk_status mk_decode_step_noalloc(const mk_layer_config* cfg, const mk_layer_weights* w,
                                  const mk_step_io* io, void* stream);
 
+/* ====================================================================
+ * Batched decoding over a paged KV cache with a shared prefix
+ *
+ * The layer calls above run one sequence over a contiguous cache.  The calls
+ * below are the operators of a step over several requests: mk_build_slots
+ * gives every new token its position and its place in the cache,
+ * mk_rope_apply rotates q and k and writes k and v there, mk_prefix_attn
+ * attends.  A layer that ends with MK_FUSE_NEXT_QKV can be given positions
+ * as well: mk_rope_apply rotates its q_out and the cache rows it wrote in
+ * place, before the next layer (without MK_FIRST_LAYER) starts from them.
+ *
+ * The paged cache is a pool of pages, bf16 or fp16
+ * [n_pages, page_size, n_kv_heads, head_dim] for K and the same for V; a slot
+ * is page * page_size + offset.  A contiguous cache [max_ctx, Hkv, d] of the
+ * layer calls is such a pool.  "Rows" are the new tokens of a step, request
+ * after request: row r belongs to request b iff cu_rows[b] <= r <
+ * cu_rows[b + 1].
+ *
+ * These calls keep no device memory: outputs and workspaces are the
+ * caller's.  They are asynchronous on `stream`, never synchronise, may be
+ * captured into a graph and may run at the same time on several streams as
+ * long as their outputs and workspaces are distinct.  All tensors lie on the
+ * device that is current during the call (MK_ERR_INVALID_ARG where the
+ * library can tell otherwise) and `stream` belongs to it.
+ * ==================================================================== */
+
+typedef enum { MK_BF16 = 0, MK_FP16 = 1 } mk_dtype;
+
+/* Block tables and slot maps from request lengths.
+ *
+ * Request b holds cached_lens[b] tokens of its own in the pages that its row
+ * of block_table names, behind a prefix of prefix_len tokens that is not in
+ * its table, and brings new_lens[b] tokens.  It needs
+ *   ceil((cached + new) / page_size) - ceil(cached / page_size)
+ * pages, which it gets from free_pages[*free_head ..] in batch order.  A
+ * request is refused, and changes nothing of its table, if a length is
+ * negative, cached + new is beyond max_pages pages, its rows end behind
+ * n_rows, or -- where it needs pages -- its pages and those of the requests
+ * before it are more than the list holds.  free_head outside 0..n_free is
+ * taken as the nearer end.
+ *
+ * Outputs: rows keep their place whether a request is refused or not.  For
+ * row i of request b the position is prefix_len + cached + i (at most
+ * INT32_MAX) and the slot
+ * table[b][(cached + i) / page_size] * page_size + (cached + i) % page_size;
+ * the slot is -1 for a refused request and for a page outside 0..n_pages-1.
+ * Rows behind the last request get position 0, slot -1, request -1.
+ * Calling again with the same inputs gives the same outputs; inputs and
+ * outputs (free_head and summary, cached_lens and lens among them) must not
+ * overlap (MK_ERR_INVALID_ARG).  */
+typedef struct mk_slots_io {
+  int32_t n_requests;         /* B, 0 .. 65536                                    */
+  int32_t n_rows;             /* length of the row outputs                        */
+  int32_t page_size;          /* tokens per page, >= 1                            */
+  int32_t max_pages;          /* pages per row of block_table                     */
+  int64_t table_stride;       /* entries between rows of block_table, >= max_pages */
+  int32_t n_pages;            /* pages in the pool                                */
+  int32_t n_free;             /* length of free_pages                             */
+  int32_t prefix_len;         /* >= 0                                             */
+  const int32_t* cached_lens; /* [B]                                              */
+  const int32_t* new_lens;    /* [B]                                              */
+  const int32_t* free_pages;  /* [n_free]; NULL iff n_free is 0                   */
+  const int32_t* free_head;   /* optional [1]: first entry not taken; NULL = 0    */
+  int32_t* block_table;       /* [B, max_pages]: new pages are written            */
+  int32_t* cu_rows;           /* [B + 1]: sums of new_lens (negative ones as 0),
+                                 at most n_rows                                   */
+  int32_t* lens;              /* [B]: cached + new, or cached where refused
+                                 (then brought into 0 .. max_pages * page_size)   */
+  int32_t* positions;         /* [n_rows]                                         */
+  int64_t* slots;             /* [n_rows]                                         */
+  int32_t* row_request;       /* optional [n_rows]                                */
+  int32_t* summary;           /* [4]: free_head after the step; rows in use;
+                                 requests refused; pages that the requests not
+                                 refused for lengths or rows need together (at
+                                 most INT32_MAX)                                  */
+} mk_slots_io;
+mk_status mk_build_slots(const mk_slots_io* io, void* stream);
+
+/* Rotary positions.
+ *
+ * Of each head the first rot_dim values are rotated in pairs i = 0 ..
+ * rot_dim/2 - 1 by the angle position * f_i:
+ *   y_a = m (x_a cos - x_b sin),  y_b = m (x_b cos + x_a sin),
+ * with (a, b) = (i, i + rot_dim/2) (MK_ROPE_HALF) or (2i, 2i + 1)
+ * (MK_ROPE_INTERLEAVED); the other values pass.  f_i = theta^(-2i / rot_dim)
+ * is scaled for contexts beyond the trained orig_ctx by `factor`:
+ *   MK_ROPE_SCALE_NONE    f_i
+ *   MK_ROPE_SCALE_LINEAR  f_i / factor (positions interpolated)
+ *   MK_ROPE_SCALE_BASE    theta' = theta factor^(rot_dim / (rot_dim - 2))
+ *   MK_ROPE_SCALE_PARTS   f_i (g + (1 - g) / factor), where g rises from 0 to 1
+ *                         as the turns over orig_ctx, orig_ctx f_i / 2 pi, go
+ *                         from beta_slow to beta_fast
+ * and m = attn_factor, or where that is 0: 0.1 ln(factor) + 1 for
+ * MK_ROPE_SCALE_PARTS, else 1.  Angles are held as 64-bit fractions of a turn
+ * (exact modulo whole turns at any int32 position), values in 32 bits, and
+ * each result is rounded once. */
+typedef enum { MK_ROPE_HALF = 0, MK_ROPE_INTERLEAVED = 1 } mk_rope_layout;
+typedef enum {
+  MK_ROPE_SCALE_NONE = 0,
+  MK_ROPE_SCALE_LINEAR = 1,
+  MK_ROPE_SCALE_BASE = 2,
+  MK_ROPE_SCALE_PARTS = 3
+} mk_rope_scaling;
+
+typedef struct mk_rope_config {
+  int32_t head_dim;    /* d, a multiple of 8, <= 256                              */
+  int32_t rot_dim;     /* 8 .. d; a multiple of 16 (MK_ROPE_HALF) or 8            */
+  int32_t layout;      /* mk_rope_layout                                          */
+  int32_t scaling;     /* mk_rope_scaling                                         */
+  double theta;        /* >= 1                                                    */
+  double factor;       /* >= 1; 1 for MK_ROPE_SCALE_NONE                          */
+  int32_t orig_ctx;    /* MK_ROPE_SCALE_PARTS: > 0                                */
+  double beta_fast;    /* MK_ROPE_SCALE_PARTS: > beta_slow; both 0 selects 32, 1  */
+  double beta_slow;
+  double attn_factor;  /* m; 0 = the scaling's own                                */
+} mk_rope_config;
+
+typedef struct mk_rope mk_rope;
+
+/* Host memory only: a mk_rope serves every device, stream and thread. */
+mk_status mk_rope_create(const mk_rope_config* cfg, mk_rope** out);
+void mk_rope_destroy(mk_rope* rope);  /* NULL is ignored */
+
+/* Rotates q into q_out and k into the cache and copies v into the cache.
+ * Strides are in elements between rows (heads are contiguous, head_dim values
+ * each), multiples of 8; tensors are 16-byte aligned.  q, k and v may be views
+ * of one projection output.  q_out may be q itself (same stride), and k and v
+ * may be the very cache rows that slots names for them; any other overlap
+ * of an input with an output is not allowed.  A row whose slot is outside
+ * 0 .. n_slots-1 writes nothing to the caches.  Slots are distinct: of rows
+ * with the same slot either one's values stay, in pieces of 16 bytes. */
+typedef struct mk_rope_io {
+  int32_t n_rows;            /* >= 0                                              */
+  int32_t n_q_heads;         /* 0 iff q is NULL                                   */
+  int32_t n_kv_heads;        /* 0 iff k is NULL                                   */
+  int32_t head_dim;          /* d: the one the mk_rope was created for            */
+  int32_t dtype;             /* mk_dtype, of every tensor                         */
+  const void* q;             /* [n_rows, n_q_heads, d]; optional                  */
+  int64_t q_stride;
+  void* q_out;               /* [n_rows, n_q_heads, d]                            */
+  int64_t q_out_stride;
+  const void* k;             /* [n_rows, n_kv_heads, d]; optional                 */
+  int64_t k_stride;
+  const void* v;             /* [n_rows, n_kv_heads, d]; optional: v_cache is
+                                left as it is                                     */
+  int64_t v_stride;
+  const int32_t* positions;  /* [n_rows]                                          */
+  const int64_t* slots;      /* [n_rows]; required with k                         */
+  void* k_cache;             /* [n_slots, n_kv_heads, d]; required with k         */
+  void* v_cache;             /* the same; required with v                         */
+  int64_t n_slots;
+} mk_rope_io;
+mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream);
+
+/* Attention of a batch whose requests share a prefix.
+ *
+ * Request b has n_b = cu_rows[b+1] - cu_rows[b] rows and lens[b] keys of its
+ * own, the last n_b of which are its rows' own; every row sees the
+ * prefix_len keys of the prefix too.  With base = max(0, lens[b] - n_b), row
+ * i has the position p = prefix_len + base + i and sees
+ *   the prefix keys j (at position j),
+ *   its request's keys j < lens[b] with j <= base + i (at prefix_len + j);
+ * with tree_mask p = prefix_len + base + popcount(mask) - 1 and, of the
+ * request's keys, those with j < base and those j >= base whose bit j - base is
+ * set (bits of keys that are not there are ignored);
+ * and of all these, with window > 0, only keys at positions > p - window.
+ *   out = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j exp(scale q.k_j).
+ * A row that sees no key gets out = 0 and lse = -infinity.  Rows from
+ * cu_rows[B] on are left as they are.  Keys that no row sees are never looked
+ * at: they may hold anything.  A key that some row sees must be finite.
+ * The prefix is read once for the whole batch, not once per request.
+ *
+ * Scores and sums are held in 32 bits; the softmax weights are rounded to the
+ * tensors' type before they multiply v.  Two calls on the same inputs give the
+ * same bits.  lens outside 0 .. max_pages * page_size is taken as the nearer
+ * end, cu_rows is taken as rising within 0 .. n_rows, and a page outside
+ * 0 .. n_pages-1 reads as zeros. */
+typedef struct mk_prefix_attn_io {
+  int32_t n_requests;          /* B, 1 .. 65536                                   */
+  int32_t n_rows;              /* rows of q, >= 0                                 */
+  int32_t n_q_heads;           /* a multiple of n_kv_heads, at most 64 per kv head */
+  int32_t n_kv_heads;
+  int32_t head_dim;            /* d: 64 or 128                                    */
+  int32_t dtype;               /* mk_dtype of q, the caches and out               */
+  int32_t page_size;           /* a power of two, 16 .. 65536                     */
+  int32_t n_pages;             /* n_pages * page_size < 2^31                      */
+  int32_t prefix_len;          /* >= 0                                            */
+  int32_t max_pages;           /* pages per row of block_table, >= 0              */
+  int64_t table_stride;        /* entries between rows of block_table             */
+  int32_t window;              /* 0 = every key; with tree_mask 0 or >= 64        */
+  float scale;                 /* of the scores; 0 selects 1 / sqrt(d)            */
+  const void* q;               /* [n_rows, n_q_heads, d], 16-byte aligned         */
+  int64_t q_stride;            /* elements between rows, a multiple of 8          */
+  const void* k_cache;         /* [n_pages, page_size, n_kv_heads, d]             */
+  const void* v_cache;
+  const int32_t* prefix_pages; /* [ceil(prefix_len / page_size)]                  */
+  const int32_t* block_table;  /* [B, max_pages]                                  */
+  const int32_t* lens;         /* [B]                                             */
+  const int32_t* cu_rows;      /* [B + 1]                                         */
+  const uint64_t* tree_mask;   /* optional [n_rows]: bit j of row i's word says
+                                  that it sees row j of its request, itself
+                                  always among them; a request has at most 64
+                                  rows then (a 65th would be seen by none)        */
+  void* out;                   /* [n_rows, n_q_heads, d]; not q                   */
+  int64_t out_stride;          /* elements between rows, a multiple of 8          */
+  float* lse;                  /* optional [n_rows, n_q_heads]                    */
+} mk_prefix_attn_io;
+
+/* Bytes of workspace that mk_prefix_attn needs for every call with these
+ * n_requests, n_rows, heads and head_dim (pointers are not looked at), on the
+ * current device.  Grows with n_rows and n_requests. */
+mk_status mk_prefix_attn_workspace(const mk_prefix_attn_io* io, int64_t* bytes);
+
+/* workspace: device memory, 256-byte aligned, its content does not matter; one
+ * call in flight per workspace. */
+mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t workspace_bytes,
+                         void* stream);
+
+/* Device status of the last mk_prefix_attn that used `workspace`: MK_OK, or
+ * MK_ERR_TIMEOUT if a bounded device-side wait expired (its outputs are then
+ * undefined).  Reads a device word synchronously: call after synchronising. */
+mk_status mk_prefix_attn_status(const void* workspace);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,10 @@ MK_FIRST_LAYER = 0x1
 MK_FUSE_NEXT_QKV = 0x2
 MK_TOPK_RENORM = 0x4
 MK_PREFETCH_NEXT_KV = 0x8
+MK_ERR_INVALID_ARG = 1
+MK_BF16, MK_FP16 = 0, 1
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 _vp = ctypes.c_void_p
 
@@ -83,6 +87,43 @@ class mk_layer_info(ctypes.Structure):
                 ("scratch_bytes", ctypes.c_int64)]
 
 
+_i32, _i64 = ctypes.c_int32, ctypes.c_int64
+
+
+class mk_slots_io(ctypes.Structure):
+    _fields_ = [("n_requests", _i32), ("n_rows", _i32), ("page_size", _i32), ("max_pages", _i32),
+                ("table_stride", _i64), ("n_pages", _i32), ("n_free", _i32), ("prefix_len", _i32),
+                ("cached_lens", _vp), ("new_lens", _vp), ("free_pages", _vp), ("free_head", _vp),
+                ("block_table", _vp), ("cu_rows", _vp), ("lens", _vp), ("positions", _vp),
+                ("slots", _vp), ("row_request", _vp), ("summary", _vp)]
+
+
+class mk_rope_config(ctypes.Structure):
+    _fields_ = [("head_dim", _i32), ("rot_dim", _i32), ("layout", _i32), ("scaling", _i32),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("orig_ctx", _i32),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("attn_factor", ctypes.c_double)]
+
+
+class mk_rope_io(ctypes.Structure):
+    _fields_ = [("n_rows", _i32), ("n_q_heads", _i32), ("n_kv_heads", _i32),
+                ("head_dim", _i32), ("dtype", _i32),
+                ("q", _vp), ("q_stride", _i64), ("q_out", _vp), ("q_out_stride", _i64),
+                ("k", _vp), ("k_stride", _i64), ("v", _vp), ("v_stride", _i64),
+                ("positions", _vp), ("slots", _vp), ("k_cache", _vp), ("v_cache", _vp),
+                ("n_slots", _i64)]
+
+
+class mk_prefix_attn_io(ctypes.Structure):
+    _fields_ = [("n_requests", _i32), ("n_rows", _i32), ("n_q_heads", _i32), ("n_kv_heads", _i32),
+                ("head_dim", _i32), ("dtype", _i32), ("page_size", _i32), ("n_pages", _i32),
+                ("prefix_len", _i32), ("max_pages", _i32), ("table_stride", _i64),
+                ("window", _i32), ("scale", ctypes.c_float), ("q", _vp), ("q_stride", _i64),
+                ("k_cache", _vp), ("v_cache", _vp), ("prefix_pages", _vp), ("block_table", _vp),
+                ("lens", _vp), ("cu_rows", _vp), ("tree_mask", _vp), ("out", _vp),
+                ("out_stride", _i64), ("lse", _vp)]
+
+
 def _sig(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -120,10 +161,22 @@ _lib_mk_decode_step_noalloc = _sig("mk_decode_step_noalloc", _c.c_int,
                                    [_c.POINTER(mk_layer_config), _c.POINTER(mk_layer_weights),
                                     _c.POINTER(mk_step_io), _vp])
 
+_lib_mk_build_slots = _sig("mk_build_slots", _c.c_int, [_c.POINTER(mk_slots_io), _vp])
+_lib_mk_rope_create = _sig("mk_rope_create", _c.c_int, [_c.POINTER(mk_rope_config), _c.POINTER(_vp)])
+_lib_mk_rope_destroy = _sig("mk_rope_destroy", None, [_vp])
+_lib_mk_rope_apply = _sig("mk_rope_apply", _c.c_int, [_vp, _c.POINTER(mk_rope_io), _vp])
+_lib_mk_prefix_attn_workspace = _sig("mk_prefix_attn_workspace", _c.c_int,
+                                     [_c.POINTER(mk_prefix_attn_io), _c.POINTER(_i64)])
+_lib_mk_prefix_attn = _sig("mk_prefix_attn", _c.c_int,
+                           [_c.POINTER(mk_prefix_attn_io), _vp, _i64, _vp])
+_lib_mk_prefix_attn_status = _sig("mk_prefix_attn_status", _c.c_int, [_vp])
+
 EXPORTED = ["mk_layer_create", "mk_decode_step", "mk_decode_step_noalloc", "mk_layer_status", "mk_layer_clear_status",
             "mk_layer_destroy", "mk_stack_create", "mk_stack_step", "mk_stack_status",
             "mk_stack_destroy", "mk_status_string", "mk_layer_get_info", "mk_get_timestamps",
             "mk_layer_prefetch_stats", "mk_stack_prefetch_stats",
+            "mk_build_slots", "mk_rope_create", "mk_rope_destroy", "mk_rope_apply",
+            "mk_prefix_attn_workspace", "mk_prefix_attn", "mk_prefix_attn_status",
             "mk_selftest_quantize", "mk_selftest_mma", "mk_selftest_sync"]
 
 
@@ -321,3 +374,183 @@ def mk_selftest_sync(mode, iters=10000):
     out = _c.c_double()
     _check("mk_selftest_sync", _lib_mk_selftest_sync(m, iters, _c.byref(out)))
     return out.value
+
+
+# ------------------------------------------- batched decoding over a paged cache
+# The library sees addresses only, so that a tensor of another type, on another
+# device or with other strides would be misread: these are refused here, as
+# MK_ERR_INVALID_ARG.
+
+def _refuse(fn):
+    raise MkError(fn, MK_ERR_INVALID_ARG)
+
+
+def _dtype_of(fn, t):
+    import torch
+    if t.dtype is torch.bfloat16:
+        return MK_BF16
+    if t.dtype is torch.float16:
+        return MK_FP16
+    _refuse(fn)
+
+
+def _dense(fn, t, elem, n=None):
+    """Address of a contiguous CUDA tensor of whole numbers or floats of `elem`
+    bytes (None: NULL), with `n` values if given."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.element_size() != elem or not t.is_contiguous() or (
+            n is not None and t.numel() != n):
+        _refuse(fn)
+    return t.data_ptr()
+
+
+def _ints(fn, t, elem, n=None):
+    if t is not None and (t.is_floating_point() or t.is_complex()):
+        _refuse(fn)
+    return _dense(fn, t, elem, n)
+
+
+def _heads(fn, t, like=None):
+    """(address, rows, heads, head_dim, elements between rows) of a tensor
+    [rows, heads, d] whose heads lie side by side."""
+    if not t.is_cuda or t.dim() != 3 or (like is not None and t.dtype != like.dtype):
+        _refuse(fn)
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        _refuse(fn)
+    return t.data_ptr(), n, h, d, s0 if n > 1 else max(s0, h * d)
+
+
+def _pool(fn, t, like):
+    """(address, pages, page size) of a pool [pages, page_size, heads, d]."""
+    if t.dim() != 4 or t.dtype != like.dtype:
+        _refuse(fn)
+    return _dense(fn, t, 2), t.shape[0], t.shape[1]
+
+
+def _table(fn, t):
+    """(address, rows, columns, elements between rows) of an int32 table."""
+    if not t.is_cuda or t.dim() != 2 or t.element_size() != 4 or t.is_floating_point() or (
+            t.shape[1] > 1 and t.stride(1) != 1):
+        _refuse(fn)
+    return t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1])
+
+
+def make_slots_io(cached_lens, new_lens, free_pages, free_head, block_table, cu_rows, lens,
+                  positions, slots, row_request, summary, page_size, n_pages, prefix_len=0):
+    """mk_slots_io of CUDA tensors (int32; slots int64).  free_head and
+    row_request may be None."""
+    fn = "make_slots_io"
+    b, n = cached_lens.numel(), positions.numel()
+    table, rows, cols, stride = _table(fn, block_table)
+    if rows != b:
+        _refuse(fn)
+    return mk_slots_io(b, n, page_size, cols, stride, n_pages, free_pages.numel(), prefix_len,
+                       _ints(fn, cached_lens, 4), _ints(fn, new_lens, 4, b),
+                       _ints(fn, free_pages, 4), _ints(fn, free_head, 4, 1), table,
+                       _ints(fn, cu_rows, 4, b + 1), _ints(fn, lens, 4, b), _ints(fn, positions, 4),
+                       _ints(fn, slots, 8, n), _ints(fn, row_request, 4, n),
+                       _ints(fn, summary, 4, 4))
+
+
+def mk_build_slots(io, stream=None):
+    _check("mk_build_slots", _lib_mk_build_slots(ctypes.byref(io), _stream(stream)))
+
+
+def make_rope_config(head_dim, rot_dim=None, layout="half", theta=10000.0, scaling="none",
+                     factor=1.0, orig_ctx=0, beta_fast=0.0, beta_slow=0.0, attn_factor=0.0):
+    return mk_rope_config(head_dim, head_dim if rot_dim is None else rot_dim, ROPE_LAYOUTS[layout],
+                          ROPE_SCALINGS[scaling], theta, factor, orig_ctx, beta_fast, beta_slow,
+                          attn_factor)
+
+
+def mk_rope_create(cfg):
+    h = _vp()
+    _check("mk_rope_create", _lib_mk_rope_create(ctypes.byref(cfg), ctypes.byref(h)))
+    return h.value
+
+
+def mk_rope_destroy(rope):
+    _lib_mk_rope_destroy(rope)
+
+
+def make_rope_io(q, q_out, k, v, positions, slots, k_cache, v_cache):
+    """mk_rope_io of CUDA tensors: q, q_out [rows, q heads, d], k, v [rows, kv
+    heads, d] (views with a row stride), positions int32, slots int64, caches
+    [pages, page_size, kv heads, d].  q or k (with v) may be None."""
+    fn = "make_rope_io"
+    like = q if q is not None else k
+    if like is None:
+        _refuse(fn)
+    n = like.shape[0]
+    dt = _dtype_of(fn, like)
+    qp = qop = kp = vp = kc = vc = None
+    qs = qos = ks = vs = hq = hk = n_slots = 0
+    if q is not None:
+        qp, _, hq, d, qs = _heads(fn, q)
+        qop, no, ho, do, qos = _heads(fn, q_out, q)
+        if (no, ho, do) != (n, hq, d):
+            _refuse(fn)
+    if k is not None:
+        kp, nk, hk, dk, ks = _heads(fn, k, like)
+        kc, pages, page = _pool(fn, k_cache, like)
+        n_slots = pages * page
+        if nk != n or dk != like.shape[2] or k_cache.shape[2:] != k.shape[1:]:
+            _refuse(fn)
+        if v is not None:
+            vp, _, _, _, vs = _heads(fn, v, like)
+            vc = _pool(fn, v_cache, like)[0]
+            if v.shape != k.shape or v_cache.shape != k_cache.shape:
+                _refuse(fn)
+    elif v is not None:
+        _refuse(fn)
+    return mk_rope_io(n, hq, hk, like.shape[2], dt, qp, qs, qop, qos, kp, ks, vp, vs,
+                      _ints(fn, positions, 4, n), _ints(fn, slots, 8, n), kc, vc, n_slots)
+
+
+def mk_rope_apply(rope, io, stream=None):
+    _check("mk_rope_apply", _lib_mk_rope_apply(rope, ctypes.byref(io), _stream(stream)))
+
+
+def make_prefix_attn_io(q, k_cache, v_cache, out, lens, cu_rows, block_table, prefix_pages=None,
+                        prefix_len=0, window=0, scale=0.0, tree_mask=None, lse=None):
+    """mk_prefix_attn_io of CUDA tensors: q, out [rows, q heads, d] (views with
+    a row stride), caches [pages, page_size, kv heads, d], lens, cu_rows,
+    block_table [requests, pages] and prefix_pages int32, tree_mask int64
+    [rows], lse float32 [rows, q heads]."""
+    fn = "make_prefix_attn_io"
+    qp, n, hq, d, qs = _heads(fn, q)
+    op, no, ho, do, os_ = _heads(fn, out, q)
+    kp, pages, page = _pool(fn, k_cache, q)
+    vp = _pool(fn, v_cache, q)[0]
+    table, b, cols, stride = _table(fn, block_table)
+    if (no, ho, do) != (n, hq, d) or v_cache.shape != k_cache.shape or k_cache.shape[3] != d:
+        _refuse(fn)
+    if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * page < prefix_len):
+        _refuse(fn)
+    if lse is not None and not lse.is_floating_point():
+        _refuse(fn)
+    return mk_prefix_attn_io(b, n, hq, k_cache.shape[2], d, _dtype_of(fn, q), page, pages,
+                             prefix_len, cols, stride, window, scale, qp, qs, kp, vp,
+                             _ints(fn, prefix_pages, 4), table, _ints(fn, lens, 4, b),
+                             _ints(fn, cu_rows, 4, b + 1), _ints(fn, tree_mask, 8, n), op, os_,
+                             _dense(fn, lse, 4, n * hq))
+
+
+def mk_prefix_attn_workspace(io):
+    out = _i64()
+    _check("mk_prefix_attn_workspace",
+           _lib_mk_prefix_attn_workspace(ctypes.byref(io), ctypes.byref(out)))
+    return out.value
+
+
+def mk_prefix_attn(io, workspace, stream=None):
+    _check("mk_prefix_attn", _lib_mk_prefix_attn(
+        ctypes.byref(io), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
+def mk_prefix_attn_status(workspace):
+    return _lib_mk_prefix_attn_status(_ptr(workspace))

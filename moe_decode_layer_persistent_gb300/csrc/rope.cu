@@ -1,0 +1,251 @@
+// rope.cu -- rotary positions with the K/V write (mk_rope_create,
+// mk_rope_apply).
+//
+// Pair (a, b) of a head at position p turns by the angle p f_i:
+//   y_a = m (x_a cos - x_b sin),  y_b = m (x_b cos + x_a sin).
+// The angle is held in 64-bit fixed point as a fraction of a turn: F_i =
+// round(f_i / 2 pi 2^64), and p F_i modulo 2^64 drops the whole turns exactly,
+// so that a position of 2^20 is as exact as one of 16 (in 32-bit floating
+// point its angle would be off by 0.03 rad).  The top 32 bits, as a signed
+// number of half turns, go to sincospif.
+#include <algorithm>
+#include <cmath>
+#include <cuda_fp16.h>
+#include <new>
+
+#include "batch.h"
+#include "ptx.cuh"
+
+struct mk_rope {
+  mk_rope_config cfg;
+  uint64_t turns[128];  // F_i
+  float m;
+};
+
+namespace mk {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+struct RopeParams {
+  mk_rope_io io;
+  int32_t d, rot;
+  float m;
+  uint64_t turns[128];
+};
+
+template <class T> struct Pack;  // two 16-bit values in a word
+template <> struct Pack<__nv_bfloat16> {
+  static MK_DEV float2 get(uint32_t w) {
+    return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
+  }
+  static MK_DEV uint32_t put(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+};
+template <> struct Pack<__half> {
+  static MK_DEV float2 get(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+  static MK_DEV uint32_t put(float a, float b) {
+    __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+};
+
+// Rotates chunk j of a head (of pieces of 16 bytes): for the half layout the 8
+// pairs whose first values are chunk j, for the interleaved one the 4 pairs of
+// chunk j.  Both values of a pair are read before either is written, so src
+// may be dst.  cs: cos and sin of the row's pairs.
+template <class T, int LAYOUT>
+MK_DEV void rotate_chunk(const T* src, T* dst, int j, int rot, const float2* cs) {
+  if (LAYOUT == MK_ROPE_HALF) {
+    uint4 a = reinterpret_cast<const uint4*>(src)[j];
+    uint4 b = reinterpret_cast<const uint4*>(src + rot / 2)[j];
+    uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
+    uint32_t* wb = reinterpret_cast<uint32_t*>(&b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = Pack<T>::get(wa[i]), y = Pack<T>::get(wb[i]);
+      const float2 c0 = cs[8 * j + 2 * i], c1 = cs[8 * j + 2 * i + 1];
+      wa[i] = Pack<T>::put(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
+      wb[i] = Pack<T>::put(y.x * c0.x + x.x * c0.y, y.y * c1.x + x.y * c1.y);
+    }
+    reinterpret_cast<uint4*>(dst)[j] = a;
+    reinterpret_cast<uint4*>(dst + rot / 2)[j] = b;
+  } else {
+    uint4 a = reinterpret_cast<const uint4*>(src)[j];
+    uint32_t* w = reinterpret_cast<uint32_t*>(&a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = Pack<T>::get(w[i]), c = cs[4 * j + i];
+      w[i] = Pack<T>::put(x.x * c.x - x.y * c.y, x.y * c.x + x.x * c.y);
+    }
+    reinterpret_cast<uint4*>(dst)[j] = a;
+  }
+}
+
+// One row per CTA: the row's cosines and sines once, in shared memory, then
+// every head's pieces.
+template <class T, int LAYOUT>
+__global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeParams P) {
+  const mk_rope_io& io = P.io;
+  __shared__ float2 cs[128];
+  const int64_t row = blockIdx.x;
+  const int d = P.d, rot = P.rot;
+  const int64_t pos = io.positions[row];
+  for (int i = threadIdx.x; i < rot / 2; i += kRopeThreads) {
+    const uint64_t phase = static_cast<uint64_t>(pos) * P.turns[i];
+    const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
+    float s, c;
+    sincospif(half_turns, &s, &c);
+    cs[i] = make_float2(c * P.m, s * P.m);
+  }
+  __syncthreads();
+  int64_t slot = -1;
+  if (io.k) {
+    slot = io.slots[row];
+    if (slot >= io.n_slots) slot = -1;
+  }
+  const int turned = LAYOUT == MK_ROPE_HALF ? rot / 16 : rot / 8;  // pieces that turn
+  const int pieces = turned + (d - rot) / 8;
+  const int nq = io.n_q_heads * pieces, nk = slot >= 0 ? io.n_kv_heads * pieces : 0;
+  const int nv = slot >= 0 && io.v ? io.n_kv_heads * (d / 8) : 0;
+  for (int t = threadIdx.x; t < nq + nk + nv; t += kRopeThreads) {
+    if (t < nq + nk) {
+      const bool q = t < nq;
+      const int u = q ? t : t - nq;
+      const int head = u / pieces, j = u % pieces;
+      const T* src = q ? static_cast<const T*>(io.q) + row * io.q_stride
+                       : static_cast<const T*>(io.k) + row * io.k_stride;
+      T* dst = q ? static_cast<T*>(io.q_out) + row * io.q_out_stride
+                 : static_cast<T*>(io.k_cache) + slot * (static_cast<int64_t>(io.n_kv_heads) * d);
+      src += head * d;
+      dst += head * d;
+      if (j < turned) {
+        rotate_chunk<T, LAYOUT>(src, dst, j, rot, cs);
+      } else {
+        const int k = rot / 8 + (j - turned);
+        reinterpret_cast<uint4*>(dst)[k] = reinterpret_cast<const uint4*>(src)[k];
+      }
+    } else {
+      const int u = t - nq - nk;
+      reinterpret_cast<uint4*>(static_cast<T*>(io.v_cache) +
+                               slot * (static_cast<int64_t>(io.n_kv_heads) * d))[u] =
+          reinterpret_cast<const uint4*>(static_cast<const T*>(io.v) + row * io.v_stride)[u];
+    }
+  }
+}
+
+template <class T>
+void launch_rope(int layout, const RopeParams& P, cudaStream_t s) {
+  if (layout == MK_ROPE_HALF)
+    k_rope<T, MK_ROPE_HALF><<<P.io.n_rows, kRopeThreads, 0, s>>>(P);
+  else
+    k_rope<T, MK_ROPE_INTERLEAVED><<<P.io.n_rows, kRopeThreads, 0, s>>>(P);
+}
+
+}  // namespace
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" {
+
+mk_status mk_rope_create(const mk_rope_config* cfg, mk_rope** out) {
+  if (!out) return MK_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!cfg) return MK_ERR_INVALID_ARG;
+  mk_rope_config c = *cfg;
+  if (c.head_dim < 8 || c.head_dim > 256 || c.head_dim % 8) return MK_ERR_UNSUPPORTED;
+  if (c.layout != MK_ROPE_HALF && c.layout != MK_ROPE_INTERLEAVED) return MK_ERR_INVALID_ARG;
+  if (c.rot_dim < 8 || c.rot_dim > c.head_dim) return MK_ERR_INVALID_ARG;
+  if (c.rot_dim % (c.layout == MK_ROPE_HALF ? 16 : 8)) return MK_ERR_UNSUPPORTED;
+  if (c.scaling < MK_ROPE_SCALE_NONE || c.scaling > MK_ROPE_SCALE_PARTS) return MK_ERR_INVALID_ARG;
+  // (the comparisons are false for NaN)
+  if (!(c.theta >= 1.0 && c.theta <= 1e30) || !(c.factor >= 1.0 && c.factor <= 1e9))
+    return MK_ERR_INVALID_ARG;
+  if (c.scaling == MK_ROPE_SCALE_NONE && c.factor != 1.0) return MK_ERR_INVALID_ARG;
+  if (!(c.attn_factor >= 0.0 && c.attn_factor <= 1e9)) return MK_ERR_INVALID_ARG;
+  if (c.scaling == MK_ROPE_SCALE_PARTS) {
+    if (c.beta_fast == 0.0 && c.beta_slow == 0.0) c.beta_fast = 32.0, c.beta_slow = 1.0;
+    if (c.orig_ctx < 1 || !(c.beta_slow >= 0.0 && c.beta_fast > c.beta_slow && c.beta_fast <= 1e9))
+      return MK_ERR_INVALID_ARG;
+  }
+  mk_rope* r = new (std::nothrow) mk_rope();
+  if (!r) return MK_ERR_OOM;
+  r->cfg = c;
+  const double two_pi = 6.283185307179586476925;
+  double theta = c.theta;
+  if (c.scaling == MK_ROPE_SCALE_BASE)
+    theta *= std::pow(c.factor, c.rot_dim / (c.rot_dim - 2.0));
+  for (int i = 0; i < c.rot_dim / 2; ++i) {
+    double f = std::pow(theta, -2.0 * i / c.rot_dim);
+    if (c.scaling == MK_ROPE_SCALE_LINEAR) f /= c.factor;
+    if (c.scaling == MK_ROPE_SCALE_PARTS) {
+      const double g = std::min(
+          1.0, std::max(0.0, (c.orig_ctx * f / two_pi - c.beta_slow) / (c.beta_fast - c.beta_slow)));
+      f *= g + (1.0 - g) / c.factor;
+    }
+    // f <= 1 rad, less than a sixth of a turn
+    r->turns[i] = static_cast<uint64_t>(std::ldexp(f / two_pi, 64));
+  }
+  r->m = static_cast<float>(c.attn_factor != 0.0                ? c.attn_factor
+                            : c.scaling == MK_ROPE_SCALE_PARTS ? 0.1 * std::log(c.factor) + 1.0
+                                                               : 1.0);
+  *out = r;
+  return MK_OK;
+}
+
+void mk_rope_destroy(mk_rope* rope) { delete rope; }
+
+mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream) {
+  if (!rope || !io) return MK_ERR_INVALID_ARG;
+  const int64_t d = rope->cfg.head_dim, n = io->n_rows;
+  if (io->dtype != MK_BF16 && io->dtype != MK_FP16) return MK_ERR_UNSUPPORTED;
+  if (io->head_dim != d) return MK_ERR_INVALID_ARG;
+  if (n < 0 || io->n_q_heads < 0 || io->n_kv_heads < 0) return MK_ERR_INVALID_ARG;
+  if (io->n_q_heads > 4096 || io->n_kv_heads > 4096) return MK_ERR_UNSUPPORTED;
+  if ((io->q != nullptr) != (io->n_q_heads > 0) || (io->k != nullptr) != (io->n_kv_heads > 0))
+    return MK_ERR_INVALID_ARG;
+  if (!io->q && !io->k) return MK_ERR_INVALID_ARG;
+  if (io->q && !io->q_out) return MK_ERR_INVALID_ARG;
+  if (io->k && (!io->slots || !io->k_cache || io->n_slots < 0)) return MK_ERR_INVALID_ARG;
+  if (io->v && (!io->k || !io->v_cache)) return MK_ERR_INVALID_ARG;
+  if (!io->positions) return MK_ERR_INVALID_ARG;
+  const void* ptrs[] = {io->q, io->q_out, io->k, io->v, io->k_cache, io->v_cache};
+  for (const void* p : ptrs)
+    if (misaligned(p, 16)) return MK_ERR_INVALID_ARG;
+  if (misaligned(io->positions, 4) || misaligned(io->slots, 8)) return MK_ERR_INVALID_ARG;
+  const int64_t qw = io->n_q_heads * d, kw = io->n_kv_heads * d;
+  if (io->q && (io->q_stride % 8 || io->q_out_stride % 8 || io->q_stride < qw || io->q_out_stride < qw))
+    return MK_ERR_INVALID_ARG;
+  if (io->k && (io->k_stride % 8 || io->k_stride < kw)) return MK_ERR_INVALID_ARG;
+  if (io->v && (io->v_stride % 8 || io->v_stride < kw)) return MK_ERR_INVALID_ARG;
+  if (io->q) {
+    const int64_t out = span_bytes(n, qw, io->q_out_stride, 2);
+    const bool in_place = io->q == io->q_out && io->q_stride == io->q_out_stride;
+    if (!in_place && overlap(io->q, span_bytes(n, qw, io->q_stride, 2), io->q_out, out))
+      return MK_ERR_INVALID_ARG;
+    if (overlap(io->positions, n * 4, io->q_out, out) ||
+        (io->k && overlap(io->slots, n * 8, io->q_out, out)))
+      return MK_ERR_INVALID_ARG;
+  }
+  if (n == 0) return MK_OK;
+  mk_status st = check_device(io->positions, nullptr, nullptr);
+  if (st != MK_OK) return st;
+  RopeParams P;
+  P.io = *io;
+  P.d = rope->cfg.head_dim;
+  P.rot = rope->cfg.rot_dim;
+  P.m = rope->m;
+  std::copy(rope->turns, rope->turns + 128, P.turns);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (io->dtype == MK_BF16) launch_rope<__nv_bfloat16>(rope->cfg.layout, P, s);
+  else launch_rope<__half>(rope->cfg.layout, P, s);
+  MK_CUDA_TRY(cudaGetLastError());
+  return MK_OK;
+}
+
+}  // extern "C"

@@ -33,4 +33,4 @@ on trained weights has no printed values to pin to: "parity unpinned" for
 real-model numerics, since the pages print no worked example.
 """
 
-from . import numerics, layer  # noqa: F401
+from . import numerics, layer, batch  # noqa: F401
