@@ -10,11 +10,11 @@
 // Each stretch of key tiles leaves (O, m, l); the second kernel joins a row's
 // stretches: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
 //
-// Three launches, chained with programmatic dependent launch:
-//   k_attn_plan   lays all work out on one line (cost units) from the lengths,
-//                 which only the GPU knows;
-//   k_attn_tiles  one CTA per SM takes an equal stretch of that line, whatever
-//                 heads, requests and key ranges it crosses;
+// Two launches, the second one chained with programmatic dependent launch:
+//   k_attn_tiles  lays all work out on one line (cost units) from the lengths,
+//                 which only the GPU knows; one CTA per SM takes an equal
+//                 stretch of it, whatever heads, requests and key ranges it
+//                 crosses;
 //   k_attn_merge  joins the partial results of each row.
 #include <algorithm>
 #include <cfloat>
@@ -43,7 +43,8 @@ constexpr int kTileThreads = 384;
 constexpr float kGrow = 8.f;        // the maximum may lag by 2^8 before O is rescaled
 constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
 
-// What k_attn_plan leaves for the other two kernels.
+// How the line is laid out (every CTA of k_attn_tiles works it out for itself,
+// the first leaves it for k_attn_merge).
 struct Plan {
   int64_t total, share;     // cost of everything, of one CTA
   int64_t prefix_cost;      // the prefix items come first
@@ -73,6 +74,7 @@ struct AttnParams {
   int32_t group;     // G: q heads per KV head
   int32_t tile_tok;  // tokens per row tile: floor(128 / G)
   int32_t box;       // keys per TMA box: min(page_size, 128)
+  int32_t page_shift;
   int32_t ctas;
   Space ws;
 };
@@ -108,74 +110,6 @@ MK_DEV int64_t head_cost(int tiles, int kt) {
   return static_cast<int64_t>(tiles >> 1) * kt * kPairCost + (tiles & 1) * ((kt + 1) >> 1) * kAltCost;
 }
 
-// ------------------------------------------------------------------- plan
-__global__ void __launch_bounds__(1024) k_attn_plan(const __grid_constant__ AttnParams P) {
-  const mk_prefix_attn_io& io = P.io;
-  pdl_launch_dependents();
-  __shared__ int64_t s_sum[32];
-  __shared__ int32_t s_low[32];
-  const int B = io.n_requests, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // the lowest position of any row decides where the prefix starts to be seen
-  int low = INT_MAX;
-  for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    const Req r = read_req(P, b);
-    if (r.n) low = min(low, r.base);
-  }
-  low = __reduce_min_sync(0xffffffffu, low);
-  if (lane == 0) s_low[warp] = low;
-  __syncthreads();
-  low = __reduce_min_sync(0xffffffffu, s_low[lane]);
-  const int n_used = clampi(io.cu_rows[B], 0, io.n_rows);
-  const int64_t lo64 =
-      io.window && low != INT_MAX ? static_cast<int64_t>(io.prefix_len) + low - io.window + 1 : 0;
-  const int lo = clampi(lo64, 0, io.prefix_len);
-  const int kt1 = ceil_div(io.prefix_len, kTileKeys);
-  const int kt0 = lo >= io.prefix_len ? kt1 : lo / kTileKeys;
-  const int tiles = ceil_div(n_used, P.tile_tok);
-  const int64_t prefix_cost = head_cost(tiles, kt1 - kt0) * io.n_kv_heads;
-
-  int64_t at = prefix_cost;
-  for (int a = 0; a < B; a += blockDim.x) {
-    const int b = a + threadIdx.x;
-    int64_t c = 0;
-    if (b < B) {
-      const Req r = read_req(P, b);
-      c = head_cost(ceil_div(r.n, P.tile_tok), r.kt1 - r.kt0) * io.n_kv_heads;
-    }
-    int64_t v = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) s_sum[warp] = v;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += s_sum[w];
-      all += s_sum[w];
-    }
-    __syncthreads();
-    if (b < B) P.ws.cost[b] = at + before + v - c;
-    at += all;
-  }
-  if (threadIdx.x == 0) {
-    P.ws.cost[B] = at;
-    Plan p;
-    p.total = at;
-    // at least one step each, so that every CTA inside an item has a piece of it
-    p.share = max((at + P.ctas - 1) / P.ctas, static_cast<int64_t>(max(kPairCost, kAltCost)));
-    p.prefix_cost = prefix_cost;
-    p.n_used = n_used;
-    p.tiles = tiles;
-    p.kt0 = kt0;
-    p.kt1 = kt1;
-    p.lo = lo;
-    *P.ws.plan = p;
-    *P.ws.status = 0;
-  }
-}
-
 // ------------------------------------------------------------------ tiles
 
 // A stretch of key tiles of one item, as the scheduler warp hands it out.
@@ -188,7 +122,7 @@ struct Piece {
   int32_t kt_a, kt_b;
   int32_t klo, khi;  // keys that some row sees
   int32_t first;     // starts its item: leaves its result by row, else by CTA
-  int32_t cu, base, len;
+  int32_t cu, base;
 };
 
 template <int D>
@@ -196,11 +130,16 @@ struct alignas(1024) TileSmem {
   uint8_t q[2][128 * D * 2];
   uint8_t kv[kStages][128 * D * 2];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t drained;
   uint64_t fifo_full[kFifo], fifo_empty[kFifo];
   Piece fifo[kFifo];
+  Plan plan;
+  int64_t sum[kTileThreads / 32];
+  int32_t low[kTileThreads / 32];
+  int64_t first_at;   // where request `first` starts on the line
+  int32_t first;      // the first request with work for this CTA
   uint32_t tmem;
   uint32_t abort;
 };
@@ -314,73 +253,184 @@ MK_DEV float exp2_approx(float x) {
   return y;
 }
 
+MK_DEV void st_global_8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// The lowest n bits, n clamped to 0 .. 32.
+MK_DEV uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
 // Tile count of a slot in a piece of `tiles` key tiles.
 MK_DEV int slot_tiles(const Piece& w, int slot) {
   const int t = w.kt_b - w.kt_a;
   return !w.alt ? t : (t + 1 - slot) >> 1;
 }
 
+// ---- the line of work, worked out by the whole CTA
+// kReqs consecutive requests per thread and turn: one turn up to 1,536 requests.
+constexpr int kReqs = 4;
+
+template <int D>
+MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
+  const mk_prefix_attn_io& io = P.io;
+  const int B = io.n_requests, lane = lane_id(), warp = threadIdx.x >> 5;
+  constexpr int kTurn = kTileThreads * kReqs;
+  int64_t cost[kReqs], mine = 0;
+  int low = INT_MAX;
+  auto read_costs = [&](int turn) {
+    const int b0 = turn * kTurn + threadIdx.x * kReqs;
+    int32_t cu[kReqs + 1], len[kReqs];
+#pragma unroll
+    for (int i = 0; i <= kReqs; ++i) cu[i] = b0 + i <= B ? io.cu_rows[b0 + i] : 0;
+#pragma unroll
+    for (int i = 0; i < kReqs; ++i) len[i] = b0 + i < B ? io.lens[b0 + i] : 0;
+    int64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < kReqs; ++i) {
+      cost[i] = 0;
+      if (b0 + i < B) {
+        const Req r = make_req(P, cu[i], cu[i + 1], len[i]);
+        cost[i] = head_cost(ceil_div(r.n, P.tile_tok), r.kt1 - r.kt0) * io.n_kv_heads;
+        if (r.n) low = min(low, r.base);
+      }
+      sum += cost[i];
+    }
+    return sum;
+  };
+  const int turns = ceil_div(B, kTurn);
+  int64_t all = 0;
+  for (int t = 0; t < turns; ++t) all += mine = read_costs(t);
+  // the sum of all costs, and the lowest position of any row, which decides
+  // where the prefix starts to be seen
+#pragma unroll
+  for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  low = __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) S.sum[warp] = all, S.low[warp] = low;
+  const int n_used = clampi(io.cu_rows[B], 0, io.n_rows);
+  __syncthreads();
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kTileThreads / 32; ++w) all += S.sum[w], low = min(low, S.low[w]);
+  Plan p;
+  const int64_t lo64 =
+      io.window && low != INT_MAX ? static_cast<int64_t>(io.prefix_len) + low - io.window + 1 : 0;
+  p.n_used = n_used;
+  p.tiles = ceil_div(n_used, P.tile_tok);
+  p.lo = clampi(lo64, 0, io.prefix_len);
+  p.kt1 = ceil_div(io.prefix_len, kTileKeys);
+  p.kt0 = p.lo >= io.prefix_len ? p.kt1 : p.lo / kTileKeys;
+  p.prefix_cost = head_cost(p.tiles, p.kt1 - p.kt0) * io.n_kv_heads;
+  p.total = p.prefix_cost + all;
+  // at least one step each, so that every CTA inside an item has a piece of it
+  p.share = max((p.total + P.ctas - 1) / P.ctas, static_cast<int64_t>(max(kPairCost, kAltCost)));
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * p.share;
+  if (threadIdx.x == 0) {
+    S.plan = p;
+    if (begin < p.prefix_cost) S.first = 0, S.first_at = p.prefix_cost;
+    if (blockIdx.x == 0) *P.ws.plan = p;
+  }
+  // where each request starts: the request of this CTA's beginning, and from
+  // the first CTA all of them
+  if (blockIdx.x != 0 && (begin < p.prefix_cost || begin >= p.total)) return;
+  int64_t at = p.prefix_cost;
+  for (int t = 0; t < turns; ++t) {
+    if (turns > 1) mine = read_costs(t);
+    int64_t v = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) S.sum[warp] = v;
+    __syncthreads();
+    int64_t here = at + v - mine;
+#pragma unroll
+    for (int w = 0; w < kTileThreads / 32; ++w) {
+      if (w < warp) here += S.sum[w];
+      at += S.sum[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kReqs; ++i) {
+      const int b = t * kTurn + threadIdx.x * kReqs + i;
+      if (b < B) {
+        if (blockIdx.x == 0) P.ws.cost[b] = here;
+        if (begin >= here && begin < here + cost[i]) S.first = b, S.first_at = here;
+      }
+      here += cost[i];
+    }
+  }
+}
+
 // ---- scheduler: the CTA's stretch of the line, item by item
 template <int D>
 MK_DEV void run_scheduler(const AttnParams& P, TileSmem<D>& S, const Ctx& c) {
   const mk_prefix_attn_io& io = P.io;
-  const Plan plan = *P.ws.plan;
-  const int Hk = io.n_kv_heads;
+  const Plan plan = S.plan;
+  const int Hk = io.n_kv_heads, lane = lane_id();
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * plan.share;
   const int64_t end = min(plan.total, begin + plan.share);
   int n_out = 0;
   auto push = [&](const Piece& w) -> bool {
     const int k = n_out % kFifo;
-    if (n_out >= kFifo && !wait_bar(c, &S.fifo_empty[k], ((n_out / kFifo) - 1) & 1)) return false;
-    S.fifo[k] = w;
-    mbar_arrive(&S.fifo_full[k]);
+    if (n_out >= kFifo && !wait_warp(c, &S.fifo_empty[k], ((n_out / kFifo) - 1) & 1)) return false;
+    if (lane == 0) {
+      S.fifo[k] = w;
+      mbar_arrive(&S.fifo_full[k]);
+    }
     ++n_out;
     return true;
   };
-  // all items of one row set: tiles row tiles against key tiles [kt0, kt1) for
-  // every head, the first at cost `at` of the line
+  // all items of one row set: `tiles` row tiles against key tiles [kt0, kt1) for
+  // every head, the first at cost `at` of the line, in the order head by head
+  // (the prefix, whose row tiles then share its keys in L2) or row tile by row
+  // tile (a request's own keys)
   auto items = [&](Piece w, int64_t at, int tok, int tiles, int kt0, int kt1, bool heads_outer) -> bool {
     const int kt = kt1 - kt0;
+    if (kt <= 0 || tiles <= 0) return true;
     const int pairs = tiles >> 1, n_items = pairs + (tiles & 1);
     const int64_t pair_cost = static_cast<int64_t>(kt) * kPairCost;
     const int64_t alt_cost = static_cast<int64_t>((kt + 1) >> 1) * kAltCost;
-    const int64_t hc = head_cost(tiles, kt);
-    if (kt <= 0 || tiles <= 0) return true;
-    // order: head by head (the prefix, whose row tiles then share its keys in
-    // L2), or row tile by row tile (a request's own keys); the first item that
-    // ends behind `begin`
-    int64_t i = 0;
+    // the first item that ends behind `begin`
+    int h = 0, p = 0;
+    int64_t s = at;
     if (begin > at) {
       const int64_t off = begin - at;
       if (heads_outer) {
-        const int64_t h = off / hc;
-        i = h * n_items + min((off - h * hc) / pair_cost, static_cast<int64_t>(pairs));
+        const int64_t hc = head_cost(tiles, kt);
+        h = static_cast<int>(off / hc);
+        p = static_cast<int>(min((off - h * hc) / pair_cost, static_cast<int64_t>(pairs)));
+        s = at + h * hc + p * pair_cost;
       } else {
-        const int64_t p = min(off / (pair_cost * Hk), static_cast<int64_t>(pairs));
-        i = p * Hk + (off - p * pair_cost * Hk) / (p < pairs ? pair_cost : alt_cost);
+        p = static_cast<int>(min(off / (pair_cost * Hk), static_cast<int64_t>(pairs)));
+        const int64_t hc = p < pairs ? pair_cost : alt_cost;
+        h = static_cast<int>((off - p * pair_cost * Hk) / hc);
+        s = at + p * pair_cost * Hk + h * hc;
       }
     }
-    for (; i < static_cast<int64_t>(n_items) * Hk; ++i) {
-      const int h = static_cast<int>(heads_outer ? i / n_items : i % Hk);
-      const int p = static_cast<int>(heads_outer ? i % n_items : i / Hk);
-      const int64_t s = heads_outer ? at + h * hc + p * pair_cost
-                                    : at + p * pair_cost * Hk + h * (p < pairs ? pair_cost : alt_cost);
+    while (h < Hk && p < n_items && s < end) {
       const bool alt = p == pairs;
-      const int64_t cost = alt ? alt_cost : pair_cost;
-      const int step = alt ? kAltCost : kPairCost;
-      if (s + cost <= begin) continue;
-      if (s >= end) return true;
-      const int steps = alt ? (kt + 1) >> 1 : kt;
-      const int s0 = s >= begin ? 0 : static_cast<int>((begin - s + step - 1) / step);
-      const int s1 = static_cast<int>(min(static_cast<int64_t>(steps), (end - s + step - 1) / step));
-      if (s0 >= s1) continue;
-      w.alt = alt;
-      w.h = h;
-      w.tok0 = tok + 2 * p * P.tile_tok;
-      w.kt_a = kt0 + (alt ? 2 * s0 : s0);
-      w.kt_b = alt ? min(kt1, kt0 + 2 * s1) : kt0 + s1;
-      w.first = s0 == 0;
-      if (!push(w)) return false;
+      const int step = alt ? kAltCost : kPairCost, steps = alt ? (kt + 1) >> 1 : kt;
+      const int s0 = s >= begin ? 0 : (static_cast<int>(begin - s) + step - 1) / step;
+      const int64_t room = (end - s + step - 1);
+      const int s1 = room >= static_cast<int64_t>(steps) * step ? steps : static_cast<int>(room) / step;
+      if (s0 < s1) {
+        w.alt = alt;
+        w.h = h;
+        w.tok0 = tok + 2 * p * P.tile_tok;
+        w.kt_a = kt0 + (alt ? 2 * s0 : s0);
+        w.kt_b = alt ? min(kt1, kt0 + 2 * s1) : kt0 + s1;
+        w.first = s0 == 0;
+        if (!push(w)) return false;
+      }
+      s += alt ? alt_cost : pair_cost;
+      if (heads_outer) {
+        if (++p == n_items) p = 0, ++h;
+      } else {
+        if (++h == Hk) h = 0, ++p;
+      }
     }
     return true;
   };
@@ -395,25 +445,30 @@ MK_DEV void run_scheduler(const AttnParams& P, TileSmem<D>& S, const Ctx& c) {
     ok = items(w, 0, 0, plan.tiles, plan.kt0, plan.kt1, true);
   }
   if (ok && end > plan.prefix_cost && begin < end) {
-    // the last request that starts at or before `begin`
-    int lo = 0, hi = io.n_requests;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (P.ws.cost[mid] <= begin) lo = mid; else hi = mid;
-    }
     w.kind = 1;
-    for (int b = lo; ok && b < io.n_requests; ++b) {
-      const int64_t at = P.ws.cost[b];
-      if (at >= end) break;
-      const Req r = read_req(P, b);
-      w.b = b;
-      w.cu = r.cu;
-      w.base = r.base;
-      w.len = r.len;
-      w.tok_end = r.cu + r.n;
-      w.klo = io.window ? max(0, clampi(static_cast<int64_t>(r.base) - io.window + 1, 0, r.len)) : 0;
-      w.khi = r.len;
-      ok = items(w, at, r.cu, ceil_div(r.n, P.tile_tok), r.kt0, r.kt1, false);
+    int64_t at = S.first_at;
+    for (int b0 = S.first; ok && at < end && b0 < io.n_requests; b0 += 32) {
+      // 32 requests' lengths at a time
+      Req mine{0, 0, 0, 0, 0, 0};
+      if (b0 + lane < io.n_requests) mine = read_req(P, b0 + lane);
+      for (int i = 0; ok && at < end && i < 32 && b0 + i < io.n_requests; ++i) {
+        Req r;
+        r.cu = __shfl_sync(0xffffffffu, mine.cu, i);
+        r.n = __shfl_sync(0xffffffffu, mine.n, i);
+        r.len = __shfl_sync(0xffffffffu, mine.len, i);
+        r.base = max(0, r.len - r.n);
+        r.kt0 = __shfl_sync(0xffffffffu, mine.kt0, i);
+        r.kt1 = __shfl_sync(0xffffffffu, mine.kt1, i);
+        const int tiles = ceil_div(r.n, P.tile_tok);
+        w.b = b0 + i;
+        w.cu = r.cu;
+        w.base = r.base;
+        w.tok_end = r.cu + r.n;
+        w.klo = io.window ? clampi(static_cast<int64_t>(r.base) - io.window + 1, 0, r.len) : 0;
+        w.khi = r.len;
+        ok = items(w, at, r.cu, tiles, r.kt0, r.kt1, false);
+        at += head_cost(tiles, r.kt1 - r.kt0) * Hk;
+      }
     }
   }
   if (ok) {
@@ -431,128 +486,165 @@ MK_DEV void run_tile_producer(const AttnParams& P, TileSmem<D>& S, const Ctx& c,
   constexpr int kHalves = D / 64;
   const int lane = lane_id();
   const int boxes = kTileKeys / P.box;  // per tile and half
+  const int group_tiles = 32 / boxes;   // key tiles whose pages one lane each holds
   int seq = 0;       // loads into the ring
+  int q_seq = 0;     // loads of row tiles
   int piece = 0;
   bool ok = true;
-  while (ok) {
+  auto next_piece = [&](Piece& w) -> bool {
     const int k = piece % kFifo;
-    if (!(ok = wait_warp(c, &S.fifo_full[k], (piece / kFifo) & 1))) break;
-    const Piece w = S.fifo[k];
+    if (!wait_warp(c, &S.fifo_full[k], (piece / kFifo) & 1)) return false;
+    w = S.fifo[k];
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.fifo_empty[k]);
-    if (w.kind < 0) break;
-    if (piece > 0 && !(ok = wait_warp(c, &S.q_empty, (piece - 1) & 1))) break;
-    const int q_tiles = w.alt ? 1 : 2;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&S.q_full, q_tiles * kHalves * P.group * P.tile_tok * 128);
-      for (int t = 0; t < q_tiles; ++t)
-        for (int f = 0; f < kHalves; ++f)
-          tma_load_3d(S.q[t] + f * 128 * 128, tm_q, &S.q_full, f * 64, w.h * P.group,
-                      w.tok0 + t * P.tile_tok);
-    }
-    __syncwarp();
-    auto load = [&](const CUtensorMap* map, int kt) -> bool {
-      const int st = seq % kStages;
-      if (seq >= kStages && !wait_warp(c, &S.kv_empty[st], ((seq / kStages) - 1) & 1)) return false;
-      // lane = half * boxes + box: the pages that hold a key some row sees
-      const int box = lane % boxes, half = lane / boxes;
-      const int key = kt * kTileKeys + box * P.box;
-      const bool mine = lane < boxes * kHalves && key < w.khi && key + P.box > w.klo;
-      int slot = 0;
-      if (mine) {
-        const int id = w.kind == 0 ? io.prefix_pages[key / io.page_size]
-                                   : io.block_table[w.b * io.table_stride + key / io.page_size];
-        // a page outside the pool: behind the end, where the copy fills zeros
-        slot = id >= 0 && id < io.n_pages ? id * io.page_size + key % io.page_size
-                                          : max(1, io.n_pages * io.page_size);
+    ++piece;
+    return true;
+  };
+  // First slot of box number 32 g + lane of a piece; -1: no row sees its keys.
+  // A page outside the pool: behind the end, where the copy fills in zeros.
+  auto fetch = [&](const Piece& w, int g) -> int {
+    const int box = 32 * g + lane, key = w.kt_a * kTileKeys + box * P.box;
+    if (w.kind < 0 || box >= (w.kt_b - w.kt_a) * boxes || key >= w.khi || key + P.box <= w.klo)
+      return -1;
+    const int page = key >> P.page_shift;
+    const int id = w.kind == 0 ? io.prefix_pages[page] : io.block_table[w.b * io.table_stride + page];
+    return id >= 0 && id < io.n_pages ? (id << P.page_shift) + (key & (io.page_size - 1))
+                                      : max(1, io.n_pages << P.page_shift);
+  };
+  Piece w;
+  ok = next_piece(w);
+  int pages_next = ok ? fetch(w, 0) : -1;
+  while (ok && w.kind >= 0) {
+    // the page numbers are read one group ahead, those of the next piece too:
+    // each read is a round trip to L2 or HBM
+    const Piece me = w;
+    const int t_all = me.kt_b - me.kt_a;
+    int pages = pages_next, pages_ahead = -1, group = 0;
+    if (!(ok = next_piece(w))) break;
+    pages_next = fetch(w, 0);
+    if (t_all > group_tiles) pages_ahead = fetch(me, 1);
+    int pages_old = -1;  // the group before: V follows K by up to two tiles
+    auto load = [&](const CUtensorMap* map, int x) -> bool {
+      const int st = seq % kStages, g = x / group_tiles;
+      if (g > group) {
+        pages_old = pages;
+        pages = pages_ahead;
+        group = g;
+        if (t_all > (g + 1) * group_tiles) pages_ahead = fetch(me, g + 1);
       }
+      // lane = half * boxes + box
+      const int box = lane % boxes, half = lane / boxes;
+      const int slot = __shfl_sync(0xffffffffu, g == group ? pages : pages_old,
+                                   (x % group_tiles) * boxes + box);
+      const bool mine = lane < boxes * kHalves && slot >= 0;
       const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+      if (seq >= kStages && !wait_warp(c, &S.kv_empty[st], ((seq / kStages) - 1) & 1)) return false;
       if (lane == 0) mbar_arrive_expect_tx(&S.kv_full[st], n * P.box * 128);
       __syncwarp();
       if (mine)
         tma_load_3d(S.kv[st] + half * 128 * 128 + box * P.box * 128, map, &S.kv_full[st],
-                    half * 64, w.h, slot);
+                    half * 64, me.h, slot);
       ++seq;
       return true;
     };
-    const int a = w.kt_a, b = w.kt_b;
-    if (!w.alt) {
-      ok = load(tm_k, a);
-      for (int i = a; ok && i < b; ++i) {
-        ok = load(tm_v, i);
-        if (ok && i + 1 < b) ok = load(tm_k, i + 1);
+    ok = load(tm_k, 0);
+    if (ok && me.alt && t_all > 1) ok = load(tm_k, 1);
+    for (int t = 0; ok && t < (me.alt ? 1 : 2); ++t, ++q_seq) {
+      const int q = q_seq & 1;
+      if (q_seq >= 2 && !(ok = wait_warp(c, &S.q_empty[q], ((q_seq >> 1) - 1) & 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&S.q_full[q], kHalves * P.group * P.tile_tok * 128);
+        for (int f = 0; f < kHalves; ++f)
+          tma_load_3d(S.q[q] + f * 128 * 128, tm_q, &S.q_full[q], f * 64, me.h * P.group,
+                      me.tok0 + t * P.tile_tok);
       }
-    } else {
-      ok = load(tm_k, a);
-      if (ok && a + 1 < b) ok = load(tm_k, a + 1);
-      for (int i = a; ok && i < b; ++i) {
-        ok = load(tm_v, i);
-        if (ok && i + 2 < b) ok = load(tm_k, i + 2);
-      }
+      __syncwarp();
     }
-    ++piece;
+    const int lead = me.alt ? 2 : 1;
+    for (int x = 0; ok && x < t_all; ++x) {
+      ok = load(tm_v, x);
+      if (ok && x + lead < t_all) ok = load(tm_k, x + lead);
+    }
   }
   if (!ok) {
     // give up: no copy may land after the CTA has left
     uint32_t none = 0;
     const Ctx drain{&none, c.status};
     for (int s = max(0, seq - kStages); s < seq; ++s)
-      wait_bar(drain, &S.kv_full[s % kStages], (s / kStages) & 1);
+      wait_warp(drain, &S.kv_full[s % kStages], (s / kStages) & 1);
+    for (int s = max(0, q_seq - 2); s < q_seq; ++s)
+      wait_warp(drain, &S.q_full[s & 1], (s >> 1) & 1);
   }
 }
 
-// ---- MMA issuer (one thread); false once a wait has run out
+// ---- MMA issuer: the whole warp walks the pieces, one elected lane issues, so
+// that descriptors and addresses are warp-uniform; false once a wait has run out
 template <class T, int D>
 MK_DEV bool issue_mmas(const AttnParams& P, TileSmem<D>& S, const Ctx& c) {
   constexpr uint32_t kIdS = idesc_of<T>(kTileKeys, false), kIdO = idesc_of<T>(D, true);
   const uint32_t tm = S.tmem;
-  int seq = 0, piece = 0;
+  int seq = 0, q_seq = 0, piece = 0;
   uint32_t p_par[2] = {0, 0};
-  auto wait_stage = [&](int s) { return wait_bar(c, &S.kv_full[s % kStages], (s / kStages) & 1); };
+  auto commit = [&](uint64_t* bar) {
+    if (elect_one()) mma_commit(bar);
+    __syncwarp();
+  };
+  auto wait_stage = [&](int s) { return wait_warp(c, &S.kv_full[s % kStages], (s / kStages) & 1); };
   auto qk = [&](int slot, int q_tile, int s) {
-    const uint32_t qa = smem_u32(S.q[q_tile]), ka = smem_u32(S.kv[s % kStages]);
+    const uint64_t qd = sdesc_kmajor_sw128(smem_u32(S.q[q_tile]));
+    const uint64_t kd = sdesc_kmajor_sw128(smem_u32(S.kv[s % kStages]));
+    if (elect_one()) {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (k >> 2) * 128 * 128 + (k & 3) * 32;
-      mma_bf16(tm + slot * 128, sdesc_kmajor_sw128(qa + off), sdesc_kmajor_sw128(ka + off), kIdS, k);
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t off = ((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4;
+        mma_bf16(tm + slot * 128, qd + off, kd + off, kIdS, k);
+      }
+      mma_commit(&S.s_full[slot]);
     }
-    mma_commit(&S.s_full[slot]);
+    __syncwarp();
   };
   auto pv = [&](int slot, int s, bool first) {
-    const uint32_t va = smem_u32(S.kv[s % kStages]);
+    const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(S.kv[s % kStages]), 128 * 128);
+    if (elect_one()) {
 #pragma unroll
-    for (int k = 0; k < kTileKeys / 16; ++k)
-      mma_ts(tm + 256 + slot * 128, tm + slot * 128 + 8 * k,
-             sdesc_mnmajor_sw128(va + k * 16 * 128, 128 * 128), kIdO, !(first && k == 0));
+      for (int k = 0; k < kTileKeys / 16; ++k)
+        mma_ts(tm + 256 + slot * 128, tm + slot * 128 + 8 * k, vd + k * (16 * 128 >> 4), kIdO,
+               !(first && k == 0));
+    }
+    __syncwarp();
   };
   while (true) {
     const int k = piece % kFifo;
-    if (!wait_bar(c, &S.fifo_full[k], (piece / kFifo) & 1)) return false;
+    if (!wait_warp(c, &S.fifo_full[k], (piece / kFifo) & 1)) return false;
     const Piece w = S.fifo[k];
-    mbar_arrive(&S.fifo_empty[k]);
+    __syncwarp();
+    if (elect_one()) mbar_arrive(&S.fifo_empty[k]);
     if (w.kind < 0) return true;
-    if (!wait_bar(c, &S.q_full, piece & 1)) return false;
     const int n[2] = {slot_tiles(w, 0), slot_tiles(w, 1)};
+    // row tile of each slot
+    const int q_tiles = w.alt ? 1 : 2, q0 = q_seq & 1, q1 = w.alt ? q0 : q0 ^ 1;
+    for (int t = 0; t < q_tiles; ++t)
+      if (!wait_warp(c, &S.q_full[(q_seq + t) & 1], ((q_seq + t) >> 1) & 1)) return false;
+    q_seq += q_tiles;
+    auto free_q = [&] {
+      commit(&S.q_empty[q0]);
+      if (q1 != q0) commit(&S.q_empty[q1]);
+    };
     // scores of the first tiles
     if (!wait_stage(seq)) return false;
     tc_fence_after();
-    qk(0, 0, seq);
-    if (!w.alt) {
-      qk(1, 1, seq);
-      mma_commit(&S.kv_empty[seq % kStages]);
+    qk(0, q0, seq);
+    if (!w.alt) qk(1, q1, seq);
+    commit(&S.kv_empty[seq % kStages]);
+    ++seq;
+    if (w.alt && n[1] > 0) {
+      if (!wait_stage(seq)) return false;
+      tc_fence_after();
+      qk(1, q1, seq);
+      commit(&S.kv_empty[seq % kStages]);
       ++seq;
-    } else {
-      mma_commit(&S.kv_empty[seq % kStages]);
-      ++seq;
-      if (n[1] > 0) {
-        if (!wait_stage(seq)) return false;
-        tc_fence_after();
-        qk(1, 0, seq);
-        mma_commit(&S.kv_empty[seq % kStages]);
-        ++seq;
-      }
     }
-    if (n[0] == 1) mma_commit(&S.q_empty);
+    if (n[0] == 1) free_q();
     for (int j = 0; j < n[0]; ++j) {
       int sv = 0, sk = 0;
       for (int slot = 0; slot < 2; ++slot) {
@@ -565,22 +657,22 @@ MK_DEV bool issue_mmas(const AttnParams& P, TileSmem<D>& S, const Ctx& c) {
           if (more) sk = seq++;
           if (!wait_stage(sv)) return false;
         }
-        if (!wait_bar(c, &S.p_full[slot], p_par[slot])) return false;
+        if (!wait_warp(c, &S.p_full[slot], p_par[slot])) return false;
         p_par[slot] ^= 1;
         tc_fence_after();
         pv(slot, sv, j == 0);
-        if (last_use) mma_commit(&S.kv_empty[sv % kStages]);
+        if (last_use) commit(&S.kv_empty[sv % kStages]);
         if (more) {
           if (fresh && !wait_stage(sk)) return false;
           tc_fence_after();
-          qk(slot, w.alt ? 0 : slot, sk);
-          if (last_use) mma_commit(&S.kv_empty[sk % kStages]);
+          qk(slot, slot ? q1 : q0, sk);
+          if (last_use) commit(&S.kv_empty[sk % kStages]);
         } else {
-          mma_commit(&S.o_done[slot]);
+          commit(&S.o_done[slot]);
         }
       }
       // the last scores are on their way: Q may be replaced once they are done
-      if (n[0] > 1 && j == n[0] - 2) mma_commit(&S.q_empty);
+      if (n[0] > 1 && j == n[0] - 2) free_q();
     }
     ++piece;
   }
@@ -591,8 +683,9 @@ MK_DEV void run_mma(const AttnParams& P, TileSmem<D>& S, const Ctx& c) {
   if (issue_mmas<T, D>(P, S, c)) return;
   // give up: no MMA may run on after the CTA has left
   uint32_t none = 0;
-  mma_commit(&S.drained);
-  wait_bar(Ctx{&none, c.status}, &S.drained, 0);
+  if (elect_one()) mma_commit(&S.drained);
+  __syncwarp();
+  wait_warp(Ctx{&none, c.status}, &S.drained, 0);
 }
 
 // ---- softmax (one warpgroup per slot, one thread per row)
@@ -662,27 +755,27 @@ MK_DEV void run_softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, int s
         tmem_ld_wait();
         const bool edge = klo > k0 || khi < k0 + kTileKeys || tree_at < k0 + kTileKeys;
         if (__any_sync(0xffffffffu, edge)) {
-          const int lo = klo - k0, hi = khi - k0;
-          const int64_t tb = static_cast<int64_t>(tree_at) - k0;
+          const int lo = klo - k0, hi = khi - k0, tb = tree_at - k0;
 #pragma unroll
           for (int q = 0; q < kTileKeys / 32; ++q) {
-            uint32_t see = 0;  // bit i: key k0 + 32 q + i is seen
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int x = 32 * q + i;
-              const bool in = x >= lo && x < hi &&
-                              (x < tb || (x - tb < 64 && ((tree >> (x - tb)) & 1)));
-              see |= in ? 1u << i : 0u;
-            }
+            // bit i: key k0 + 32 q + i is seen
+            uint32_t see = below(hi - 32 * q) & ~below(lo - 32 * q);
+            const int off = tb - 32 * q;
+            if (off < 32)
+              see &= below(off) | (off >= 0 ? static_cast<uint32_t>(tree) << off
+                                   : off > -64 ? static_cast<uint32_t>(tree >> -off) : 0u);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (!((see >> i) & 1)) s[32 * q + i] = -INFINITY;
+              if (!(see & (1u << i))) s[32 * q + i] = -INFINITY;
           }
         }
-        float top = s[0];
+        float t8[8];
 #pragma unroll
-        for (int x = 1; x < kTileKeys; ++x) top = fmaxf(top, s[x]);
-        top *= sl2;
+        for (int x = 0; x < 8; ++x) t8[x] = s[x];
+#pragma unroll
+        for (int x = 8; x < kTileKeys; ++x) t8[x & 7] = fmaxf(t8[x & 7], s[x]);
+        const float top = sl2 * fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])),
+                                      fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
         // rescale only when the maximum has grown by 2^8: until then P is at most
         // 2^8, which its types and the 32-bit sums hold without loss
         const bool grow = valid && top > m + kGrow;
@@ -757,9 +850,10 @@ MK_DEV void run_softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, int s
         tmem_ld32(to + 32 * q, o);
         tmem_ld_wait();
         if (valid) {
-          float4* dst = reinterpret_cast<float4*>(P.ws.o + at * D + 32 * q);
+          // whole sectors: a thread's row is its own
+          float* dst = P.ws.o + at * D + 32 * q;
 #pragma unroll
-          for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          for (int x = 0; x < 32; x += 8) st_global_8(dst + x, o + x);
         }
       }
       tc_fence_before();
@@ -780,10 +874,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&S.kv_full[i], 1);
       mbar_init(&S.kv_empty[i], 1);
     }
-    mbar_init(&S.q_full, 1);
-    mbar_init(&S.q_empty, 1);
     mbar_init(&S.drained, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.q_full[i], 1);
+      mbar_init(&S.q_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_full[i], 4);
       mbar_init(&S.o_done[i], 1);
@@ -802,10 +896,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_alloc(&S.tmem, 512);
     tmem_relinquish();
   }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *P.ws.status = 0;
+  lay_out_work<D>(P, S);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();
   pdl_launch_dependents();
   const Ctx c{&S.abort, P.ws.status};
   // 2 x 128 x 208 + 128 x 72 = 62,464 of the 64,512 registers of the launch; all
@@ -818,8 +913,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else {
     reg_dealloc<72>();
     if (warp == 8) run_tile_producer<D>(P, S, c, &tm_q, &tm_k, &tm_v);
-    else if (warp == 9 && lane_id() == 0) run_mma<T, D>(P, S, c);
-    else if (warp == 10 && lane_id() == 0) run_scheduler<D>(P, S, c);
+    else if (warp == 9) run_mma<T, D>(P, S, c);
+    else if (warp == 10) run_scheduler<D>(P, S, c);
     __syncwarp();
     reg_alloc<168>();
   }
@@ -1002,34 +1097,24 @@ mk_status encode_tmap_3d(CUtensorMap* map, int dtype, const void* base, uint64_t
   return r == CUDA_SUCCESS ? MK_OK : MK_ERR_INVALID_ARG;
 }
 
-template <class... Args>
-mk_status launch_chained(void (*k)(Args...), int grid, int threads, size_t smem, cudaStream_t s,
-                         Args... args) {
+template <class T, int D>
+mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorMap& k,
+                      const CUtensorMap& v, cudaStream_t s) {
+  constexpr int smem = sizeof(TileSmem<D>) + 1024;
+  MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_tiles<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  k_attn_tiles<T, D><<<A.ctas, kTileThreads, smem, s>>>(A, q, k, v);
+  MK_CUDA_TRY(cudaGetLastError());
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(grid);
-  lc.blockDim = dim3(threads);
-  lc.dynamicSmemBytes = smem;
+  lc.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(A.io.n_rows) * A.io.n_q_heads + 7) / 8));
+  lc.blockDim = dim3(256);
   lc.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k, args...));
+  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_attn_merge<T, D>, A));
   return MK_OK;
-}
-
-template <class T, int D>
-mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorMap& k,
-                      const CUtensorMap& v, cudaStream_t s) {
-  constexpr int smem = sizeof(TileSmem<D>) + 1024;
-  MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_tiles<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  k_attn_plan<<<1, 1024, 0, s>>>(A);
-  MK_CUDA_TRY(cudaGetLastError());
-  mk_status st = launch_chained(k_attn_tiles<T, D>, A.ctas, kTileThreads, smem, s, A, q, k, v);
-  if (st != MK_OK) return st;
-  const int64_t items = static_cast<int64_t>(A.io.n_rows) * A.io.n_q_heads;
-  return launch_chained(k_attn_merge<T, D>, static_cast<int>((items + 7) / 8), 256, 0, s, A);
 }
 
 }  // namespace
@@ -1090,6 +1175,7 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   A.group = io->n_q_heads / io->n_kv_heads;
   A.tile_tok = 128 / A.group;
   A.box = static_cast<int>(std::min<int64_t>(P, kTileKeys));
+  A.page_shift = __builtin_ctz(static_cast<uint32_t>(P));
   const uint64_t d = io->head_dim, Hq = io->n_q_heads, Hk = io->n_kv_heads;
   CUtensorMap q, k, v;
   st = encode_tmap_3d(&q, io->dtype, io->q, d, Hq, io->n_rows, d * 2, io->q_stride * 2, A.group, A.tile_tok);
