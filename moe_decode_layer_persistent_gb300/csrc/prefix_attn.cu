@@ -10,12 +10,20 @@
 // Each stretch of key tiles leaves (O, m, l); the second kernel joins a row's
 // stretches: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
 //
+// Work comes in two kinds, each laid out on a line of its own, which every CTA
+// works out from the lengths (only the GPU knows them):
+//   pairs  two row tiles on the same key tiles: bound by the tensor cores.  The
+//          CTAs (one per SM) get an equal stretch of the line each, and a CTA's
+//          two slots take a row tile each;
+//   solos  one row tile (a row set's last one, if their number is odd; most
+//          requests' own rows): bound by the K and V bytes.  The slots of all
+//          CTAs get an equal stretch each.
+// A stretch may begin and end anywhere, whatever heads, requests and keys it
+// crosses.  CTAs with an even number start with their pairs, the others with
+// their solos, so that the tensor cores and HBM are both busy all the time.
 // Two launches, the second one chained with programmatic dependent launch:
-//   k_attn_tiles  lays all work out on one line (cost units) from the lengths,
-//                 which only the GPU knows; one CTA per SM takes an equal
-//                 stretch of it, whatever heads, requests and key ranges it
-//                 crosses;
-//   k_attn_merge  joins the partial results of each row.
+// k_attn_tiles does all that, k_attn_merge joins the partial results of each
+// row.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -30,42 +38,42 @@ namespace mk {
 
 namespace {
 
-// Cost units of a step, in which both softmax warpgroups take one tile each:
-// two row tiles on one key tile (kPairCost), or one row tile on two key tiles
-// (kAltCost), which loads twice the bytes.
-constexpr int kPairCost = 2;
-constexpr int kAltCost = 3;
+constexpr int kPair = 0, kSolo = 1;  // the two kinds of work
+// Cost of a key tile, and what an item (a row set's tile or pair of tiles and
+// a KV head) costs on top of its key tiles: filling the pipeline and writing
+// the result.
+constexpr int kTileCost = 2;
+MK_DEV constexpr int item_over(int kind) { return kind == kPair ? 6 : 3; }
 
 constexpr int kTileKeys = 128;
-constexpr int kStages = 5;          // K and V tiles in flight
+constexpr bool kSplitP = false;
 constexpr int kFifo = 4;            // pieces handed out ahead
 constexpr int kTileThreads = 384;
 constexpr float kGrow = 8.f;        // the maximum may lag by 2^8 before O is rescaled
 constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
 
-// How the line is laid out (every CTA of k_attn_tiles works it out for itself,
-// the first leaves it for k_attn_merge).
+// How the lines are laid out (every CTA of k_attn_tiles works it out for
+// itself, the first leaves it for k_attn_merge).
 struct Plan {
-  int64_t total, share;     // cost of everything, of one CTA
-  int64_t prefix_cost;      // the prefix items come first
-  int32_t n_used;           // rows in use
-  int32_t tiles;            // row tiles of the prefix
-  int32_t kt0, kt1;         // key tiles of the prefix that some row sees
-  int32_t lo;               // first prefix key that some row sees
+  int64_t total[2], share[2];  // cost of everything, of one CTA (pairs) or slot (solos)
+  int64_t prefix_cost[2];      // the prefix items come first
+  int32_t n_used;              // rows in use
+  int32_t tiles;               // row tiles of the prefix
+  int32_t kt0, kt1;            // key tiles of the prefix that some row sees
+  int32_t lo;                  // first prefix key that some row sees
 };
 
 // Workspace layout.
 struct Space {
   uint32_t* status;
   Plan* plan;
-  int64_t* cost;    // [B + 1]: where request b's items start on the line
+  int64_t* cost;    // [2][B]: where request b's items start on each line
   float2* ml;       // (m, l) per partial row
   float* o;         // D values per partial row
-  // first partial row of each region: the prefix's first (or only) slot by row
-  // and head; its second slot (only the last row tile has one) by head; the
-  // requests' own first and second slots by row and head; stretches that start
-  // in the middle of an item, by CTA and slot
-  int64_t pre0, pre1, own0, own1, carry;
+  // first partial row of each region: the prefix's and the requests' own
+  // results by row and head; those of stretches that start in the middle of an
+  // item, [kind][CTA][slot][128]
+  int64_t pre, own, carry;
 };
 
 struct AttnParams {
@@ -105,19 +113,21 @@ MK_DEV Req read_req(const AttnParams& P, int b) {
   return make_req(P, P.io.cu_rows[b], P.io.cu_rows[b + 1], P.io.lens[b]);
 }
 
-// Cost of the items of one head: `tiles` row tiles against `kt` key tiles.
-MK_DEV int64_t head_cost(int tiles, int kt) {
-  return static_cast<int64_t>(tiles >> 1) * kt * kPairCost + (tiles & 1) * ((kt + 1) >> 1) * kAltCost;
+// Items of a row set of `tiles` row tiles for one head: pairs, or the odd tile.
+MK_DEV int items_of(int kind, int tiles) { return kind == kPair ? tiles >> 1 : tiles & 1; }
+MK_DEV int64_t item_cost(int kind, int kt) { return item_over(kind) + static_cast<int64_t>(kt) * kTileCost; }
+// Cost of all of a row set's items against kt key tiles.
+MK_DEV int64_t set_cost(const AttnParams& P, int kind, int tiles, int kt) {
+  return kt > 0 ? items_of(kind, tiles) * item_cost(kind, kt) * P.io.n_kv_heads : 0;
 }
 
 // ------------------------------------------------------------------ tiles
 
-// A stretch of key tiles of one item, as the scheduler warp hands it out.
+// A stretch of key tiles of one item, as a producer hands it out.
 struct Piece {
-  int32_t kind;      // 0 prefix, 1 a request's own keys, -1 no more
-  int32_t alt;       // 1: one row tile, its key tiles by turns to the two slots
+  int32_t own;       // 0 prefix, 1 a request's own keys, -1 no more
   int32_t h, b;
-  int32_t tok0;      // first token (row of q) of slot 0's row tile
+  int32_t tok0;      // first token (row of q) of the (first) row tile
   int32_t tok_end;   // behind the last token of the prefix rows / the request
   int32_t kt_a, kt_b;
   int32_t klo, khi;  // keys that some row sees
@@ -125,21 +135,44 @@ struct Piece {
   int32_t cu, base;
 };
 
-template <int D>
-struct alignas(1024) TileSmem {
-  uint8_t q[2][128 * D * 2];
-  uint8_t kv[kStages][128 * D * 2];
-  uint64_t kv_full[kStages], kv_empty[kStages];
+// Barriers of one ring of K and V tiles, with those of the row tiles and the
+// pieces that go with it.
+constexpr int kMaxStages = 8;
+struct Ring {
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], o_done[2];
-  uint64_t drained;
   uint64_t fifo_full[kFifo], fifo_empty[kFifo];
   Piece fifo[kFifo];
+};
+// A place in a ring: the stage and how often the ring has gone round (mod 2).
+struct Place {
+  int st = 0;
+  uint32_t round = 0;
+  MK_DEV Place next(int stages) const {
+    Place p{st + 1, round};
+    if (p.st == stages) p.st = 0, p.round ^= 1;
+    return p;
+  }
+};
+
+template <int D>
+struct alignas(1024) TileSmem {
+  // K and V tiles in flight: shared by the slots for pairs, a part each for solos
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kSoloStages = D == 128 ? 2 : 4;
+  uint8_t q[2][128 * D * 2];
+  uint8_t kv[kStages][128 * D * 2];
+  Ring ring[3];      // of pairs, of slot 0's solos, of slot 1's
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
+  uint64_t turn;     // both slots' MMAs of the first kind of work are done
+  uint64_t drained[2];
   Plan plan;
-  int64_t sum[kTileThreads / 32];
+  int64_t sum[2][kTileThreads / 32];
   int32_t low[kTileThreads / 32];
-  int64_t first_at;   // where request `first` starts on the line
-  int32_t first;      // the first request with work for this CTA
+  // the first request with work on a line's stretch and where it starts: the
+  // CTA's of pairs, the two slots' of solos
+  int64_t first_at[3];
+  int32_t first[3];
   uint32_t tmem;
   uint32_t abort;
 };
@@ -147,6 +180,22 @@ struct alignas(1024) TileSmem {
 struct Ctx {
   volatile uint32_t* abort;
   uint32_t* status;
+};
+
+// One kind of work as one slot's warps see it.
+template <int D>
+struct View {
+  Ring* ring;
+  uint8_t* kv;       // its part of the buffers
+  int kind, slot, stages;
+  int q_bar;         // the slot's row tile among the ring's
+  MK_DEV View(TileSmem<D>& S, int kind_, int slot_) : kind(kind_), slot(slot_) {
+    const bool pair = kind == kPair;
+    ring = &S.ring[pair ? 0 : 1 + slot];
+    stages = pair ? TileSmem<D>::kStages : TileSmem<D>::kSoloStages;
+    kv = S.kv[pair ? 0 : slot * TileSmem<D>::kSoloStages];
+    q_bar = pair ? slot : 0;
+  }
 };
 
 // Bounded wait: false once any wait of the CTA has run out.
@@ -247,6 +296,28 @@ __host__ __device__ constexpr uint32_t idesc_of(int N, bool b_along_n) {
          (b_along_n ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
 }
 
+// Pairs of float32 operations in one instruction, and the largest of three.
+MK_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+MK_DEV float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+MK_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 MK_DEV float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -262,13 +333,7 @@ MK_DEV void st_global_8(float* p, const float* v) {
 // The lowest n bits, n clamped to 0 .. 32.
 MK_DEV uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
-// Tile count of a slot in a piece of `tiles` key tiles.
-MK_DEV int slot_tiles(const Piece& w, int slot) {
-  const int t = w.kt_b - w.kt_a;
-  return !w.alt ? t : (t + 1 - slot) >> 1;
-}
-
-// ---- the line of work, worked out by the whole CTA
+// ---- the lines of work, worked out by the whole CTA
 // kReqs consecutive requests per thread and turn: one turn up to 1,536 requests.
 constexpr int kReqs = 4;
 
@@ -277,7 +342,7 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   const mk_prefix_attn_io& io = P.io;
   const int B = io.n_requests, lane = lane_id(), warp = threadIdx.x >> 5;
   constexpr int kTurn = kTileThreads * kReqs;
-  int64_t cost[kReqs], mine = 0;
+  int64_t cost[2][kReqs], mine[2], all[2] = {0, 0};
   int low = INT_MAX;
   auto read_costs = [&](int turn) {
     const int b0 = turn * kTurn + threadIdx.x * kReqs;
@@ -286,33 +351,45 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
     for (int i = 0; i <= kReqs; ++i) cu[i] = b0 + i <= B ? io.cu_rows[b0 + i] : 0;
 #pragma unroll
     for (int i = 0; i < kReqs; ++i) len[i] = b0 + i < B ? io.lens[b0 + i] : 0;
-    int64_t sum = 0;
+    mine[0] = mine[1] = 0;
 #pragma unroll
     for (int i = 0; i < kReqs; ++i) {
-      cost[i] = 0;
+      cost[0][i] = cost[1][i] = 0;
       if (b0 + i < B) {
         const Req r = make_req(P, cu[i], cu[i + 1], len[i]);
-        cost[i] = head_cost(ceil_div(r.n, P.tile_tok), r.kt1 - r.kt0) * io.n_kv_heads;
+        const int tiles = ceil_div(r.n, P.tile_tok);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) cost[k][i] = set_cost(P, k, tiles, r.kt1 - r.kt0);
         if (r.n) low = min(low, r.base);
       }
-      sum += cost[i];
+      mine[0] += cost[0][i];
+      mine[1] += cost[1][i];
     }
-    return sum;
   };
   const int turns = ceil_div(B, kTurn);
-  int64_t all = 0;
-  for (int t = 0; t < turns; ++t) all += mine = read_costs(t);
-  // the sum of all costs, and the lowest position of any row, which decides
-  // where the prefix starts to be seen
-#pragma unroll
-  for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  low = __reduce_min_sync(0xffffffffu, low);
-  if (lane == 0) S.sum[warp] = all, S.low[warp] = low;
   const int n_used = clampi(io.cu_rows[B], 0, io.n_rows);
-  __syncthreads();
-  all = 0;
+  for (int t = 0; t < turns; ++t) {
+    read_costs(t);
+    all[0] += mine[0];
+    all[1] += mine[1];
+  }
+  // the sums of all costs, and the lowest position of any row, which decides
+  // where the prefix starts to be seen
+  for (int k = 0; k < 2; ++k) {
 #pragma unroll
-  for (int w = 0; w < kTileThreads / 32; ++w) all += S.sum[w], low = min(low, S.low[w]);
+    for (int o = 16; o; o >>= 1) all[k] += __shfl_xor_sync(0xffffffffu, all[k], o);
+    if (lane == 0) S.sum[k][warp] = all[k];
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) S.low[warp] = low;
+  __syncthreads();
+  all[0] = all[1] = 0;
+#pragma unroll
+  for (int w = 0; w < kTileThreads / 32; ++w) {
+    all[0] += S.sum[0][w];
+    all[1] += S.sum[1][w];
+    low = min(low, S.low[w]);
+  }
   Plan p;
   const int64_t lo64 =
       io.window && low != INT_MAX ? static_cast<int64_t>(io.prefix_len) + low - io.window + 1 : 0;
@@ -321,404 +398,363 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   p.lo = clampi(lo64, 0, io.prefix_len);
   p.kt1 = ceil_div(io.prefix_len, kTileKeys);
   p.kt0 = p.lo >= io.prefix_len ? p.kt1 : p.lo / kTileKeys;
-  p.prefix_cost = head_cost(p.tiles, p.kt1 - p.kt0) * io.n_kv_heads;
-  p.total = p.prefix_cost + all;
-  // at least one step each, so that every CTA inside an item has a piece of it
-  p.share = max((p.total + P.ctas - 1) / P.ctas, static_cast<int64_t>(max(kPairCost, kAltCost)));
-  const int64_t begin = static_cast<int64_t>(blockIdx.x) * p.share;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    p.prefix_cost[k] = set_cost(P, k, p.tiles, p.kt1 - p.kt0);
+    p.total[k] = p.prefix_cost[k] + all[k];
+    const int n = k == kPair ? P.ctas : 2 * P.ctas;
+    // at least one key tile each, so that every stretch inside an item has one
+    p.share[k] = max((p.total[k] + n - 1) / n, static_cast<int64_t>(kTileCost));
+  }
+  const int64_t begin[3] = {blockIdx.x * p.share[kPair], 2ll * blockIdx.x * p.share[kSolo],
+                            (2ll * blockIdx.x + 1) * p.share[kSolo]};
   if (threadIdx.x == 0) {
     S.plan = p;
-    if (begin < p.prefix_cost) S.first = 0, S.first_at = p.prefix_cost;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) S.first[i] = 0, S.first_at[i] = p.prefix_cost[i > 0];
     if (blockIdx.x == 0) *P.ws.plan = p;
   }
-  // where each request starts: the request of this CTA's beginning, and from
+  // where each request starts: the requests of this CTA's stretches, and from
   // the first CTA all of them
-  if (blockIdx.x != 0 && (begin < p.prefix_cost || begin >= p.total)) return;
-  int64_t at = p.prefix_cost;
+  bool need = blockIdx.x == 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    need |= begin[i] >= p.prefix_cost[i > 0] && begin[i] < p.total[i > 0];
+  if (!need) return;
+  int64_t at[2] = {p.prefix_cost[0], p.prefix_cost[1]};
   for (int t = 0; t < turns; ++t) {
-    if (turns > 1) mine = read_costs(t);
-    int64_t v = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
+    if (turns > 1) read_costs(t);
+    int64_t v[2] = {mine[0], mine[1]};
     __syncthreads();
-    if (lane == 31) S.sum[warp] = v;
-    __syncthreads();
-    int64_t here = at + v - mine;
 #pragma unroll
-    for (int w = 0; w < kTileThreads / 32; ++w) {
-      if (w < warp) here += S.sum[w];
-      at += S.sum[w];
-    }
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-    for (int i = 0; i < kReqs; ++i) {
-      const int b = t * kTurn + threadIdx.x * kReqs + i;
-      if (b < B) {
-        if (blockIdx.x == 0) P.ws.cost[b] = here;
-        if (begin >= here && begin < here + cost[i]) S.first = b, S.first_at = here;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v[k], o);
+        if (lane >= o) v[k] += u;
       }
-      here += cost[i];
+      if (lane == 31) S.sum[k][warp] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      int64_t here = at[k] + v[k] - mine[k];
+#pragma unroll
+      for (int w = 0; w < kTileThreads / 32; ++w) {
+        if (w < warp) here += S.sum[k][w];
+        at[k] += S.sum[k][w];
+      }
+#pragma unroll
+      for (int i = 0; i < kReqs; ++i) {
+        const int b = t * kTurn + threadIdx.x * kReqs + i;
+        if (b < B) {
+          if (blockIdx.x == 0) P.ws.cost[static_cast<int64_t>(k) * B + b] = here;
+#pragma unroll
+          for (int j = k; j < (k == kPair ? 1 : 3); ++j)
+            if (begin[j] >= here && begin[j] < here + cost[k][i]) S.first[j] = b, S.first_at[j] = here;
+        }
+        here += cost[k][i];
+      }
     }
   }
 }
 
-// ---- scheduler: the CTA's stretch of the line, item by item
-template <int D>
-MK_DEV void run_scheduler(const AttnParams& P, TileSmem<D>& S, const Ctx& c) {
+// ---- a stretch of a line, piece by piece: emit(Piece) for each
+template <class Emit>
+MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int64_t begin, int first,
+                 int64_t first_at, const Emit& emit) {
   const mk_prefix_attn_io& io = P.io;
-  const Plan plan = S.plan;
-  const int Hk = io.n_kv_heads, lane = lane_id();
-  const int64_t begin = static_cast<int64_t>(blockIdx.x) * plan.share;
-  const int64_t end = min(plan.total, begin + plan.share);
-  int n_out = 0;
-  auto push = [&](const Piece& w) -> bool {
-    const int k = n_out % kFifo;
-    if (n_out >= kFifo && !wait_warp(c, &S.fifo_empty[k], ((n_out / kFifo) - 1) & 1)) return false;
-    if (lane == 0) {
-      S.fifo[k] = w;
-      mbar_arrive(&S.fifo_full[k]);
-    }
-    ++n_out;
-    return true;
-  };
-  // all items of one row set: `tiles` row tiles against key tiles [kt0, kt1) for
-  // every head, the first at cost `at` of the line, in the order head by head
-  // (the prefix, whose row tiles then share its keys in L2) or row tile by row
-  // tile (a request's own keys)
-  auto items = [&](Piece w, int64_t at, int tok, int tiles, int kt0, int kt1, bool heads_outer) -> bool {
-    const int kt = kt1 - kt0;
-    if (kt <= 0 || tiles <= 0) return true;
-    const int pairs = tiles >> 1, n_items = pairs + (tiles & 1);
-    const int64_t pair_cost = static_cast<int64_t>(kt) * kPairCost;
-    const int64_t alt_cost = static_cast<int64_t>((kt + 1) >> 1) * kAltCost;
-    // the first item that ends behind `begin`
-    int h = 0, p = 0;
-    int64_t s = at;
-    if (begin > at) {
-      const int64_t off = begin - at;
-      if (heads_outer) {
-        const int64_t hc = head_cost(tiles, kt);
-        h = static_cast<int>(off / hc);
-        p = static_cast<int>(min((off - h * hc) / pair_cost, static_cast<int64_t>(pairs)));
-        s = at + h * hc + p * pair_cost;
-      } else {
-        p = static_cast<int>(min(off / (pair_cost * Hk), static_cast<int64_t>(pairs)));
-        const int64_t hc = p < pairs ? pair_cost : alt_cost;
-        h = static_cast<int>((off - p * pair_cost * Hk) / hc);
-        s = at + p * pair_cost * Hk + h * hc;
-      }
-    }
-    while (h < Hk && p < n_items && s < end) {
-      const bool alt = p == pairs;
-      const int step = alt ? kAltCost : kPairCost, steps = alt ? (kt + 1) >> 1 : kt;
-      const int s0 = s >= begin ? 0 : (static_cast<int>(begin - s) + step - 1) / step;
-      const int64_t room = (end - s + step - 1);
-      const int s1 = room >= static_cast<int64_t>(steps) * step ? steps : static_cast<int>(room) / step;
+  const int Hk = io.n_kv_heads, lane = lane_id(), over = item_over(kind);
+  const int64_t end = min(plan.total[kind], begin + plan.share[kind]);
+  if (begin >= end) return true;
+  // the items of a row set (row tile by row tile, head by head) from cost `at`
+  auto items = [&](Piece& w, int64_t at, int tok, int tiles, int kt0, int kt1) -> bool {
+    const int kt = kt1 - kt0, count = items_of(kind, tiles) * Hk;
+    if (kt <= 0 || count == 0) return true;
+    const int64_t cost = item_cost(kind, kt);
+    int i = begin > at ? static_cast<int>((begin - at) / cost) : 0;
+    int p = i / Hk, h = i - p * Hk;
+    int64_t s = at + i * cost + over;  // of the item's first key tile
+    for (; i < count && s < end; ++i, s += cost) {
+      const int s0 = s >= begin ? 0 : (static_cast<int>(begin - s) + kTileCost - 1) / kTileCost;
+      const int64_t room = end - s + kTileCost - 1;
+      const int s1 = room >= static_cast<int64_t>(kt) * kTileCost ? kt : static_cast<int>(room) / kTileCost;
       if (s0 < s1) {
-        w.alt = alt;
         w.h = h;
-        w.tok0 = tok + 2 * p * P.tile_tok;
-        w.kt_a = kt0 + (alt ? 2 * s0 : s0);
-        w.kt_b = alt ? min(kt1, kt0 + 2 * s1) : kt0 + s1;
+        w.tok0 = tok + (kind == kPair ? 2 * p : tiles - 1) * P.tile_tok;
+        w.kt_a = kt0 + s0;
+        w.kt_b = kt0 + s1;
         w.first = s0 == 0;
-        if (!push(w)) return false;
+        if (!emit(w)) return false;
       }
-      s += alt ? alt_cost : pair_cost;
-      if (heads_outer) {
-        if (++p == n_items) p = 0, ++h;
-      } else {
-        if (++h == Hk) h = 0, ++p;
-      }
+      if (++h == Hk) h = 0, ++p;
     }
     return true;
   };
   Piece w;
   std::memset(&w, 0, sizeof(w));
-  bool ok = true;
-  if (begin < plan.prefix_cost) {
-    w.kind = 0;
+  if (begin < plan.prefix_cost[kind]) {
     w.tok_end = plan.n_used;
     w.klo = plan.lo;
     w.khi = io.prefix_len;
-    ok = items(w, 0, 0, plan.tiles, plan.kt0, plan.kt1, true);
+    if (!items(w, 0, 0, plan.tiles, plan.kt0, plan.kt1)) return false;
   }
-  if (ok && end > plan.prefix_cost && begin < end) {
-    w.kind = 1;
-    int64_t at = S.first_at;
-    for (int b0 = S.first; ok && at < end && b0 < io.n_requests; b0 += 32) {
-      // 32 requests' lengths at a time
-      Req mine{0, 0, 0, 0, 0, 0};
-      if (b0 + lane < io.n_requests) mine = read_req(P, b0 + lane);
-      for (int i = 0; ok && at < end && i < 32 && b0 + i < io.n_requests; ++i) {
-        Req r;
-        r.cu = __shfl_sync(0xffffffffu, mine.cu, i);
-        r.n = __shfl_sync(0xffffffffu, mine.n, i);
-        r.len = __shfl_sync(0xffffffffu, mine.len, i);
-        r.base = max(0, r.len - r.n);
-        r.kt0 = __shfl_sync(0xffffffffu, mine.kt0, i);
-        r.kt1 = __shfl_sync(0xffffffffu, mine.kt1, i);
-        const int tiles = ceil_div(r.n, P.tile_tok);
-        w.b = b0 + i;
-        w.cu = r.cu;
-        w.base = r.base;
-        w.tok_end = r.cu + r.n;
-        w.klo = io.window ? clampi(static_cast<int64_t>(r.base) - io.window + 1, 0, r.len) : 0;
-        w.khi = r.len;
-        ok = items(w, at, r.cu, tiles, r.kt0, r.kt1, false);
-        at += head_cost(tiles, r.kt1 - r.kt0) * Hk;
-      }
+  w.own = 1;
+  int64_t at = first_at;
+  for (int b0 = first; at < end && b0 < io.n_requests; b0 += 32) {
+    // 32 requests' lengths at a time
+    Req mine{0, 0, 0, 0, 0, 0};
+    if (b0 + lane < io.n_requests) mine = read_req(P, b0 + lane);
+    for (int i = 0; at < end && i < 32 && b0 + i < io.n_requests; ++i) {
+      const int n = __shfl_sync(0xffffffffu, mine.n, i), len = __shfl_sync(0xffffffffu, mine.len, i);
+      const int kt0 = __shfl_sync(0xffffffffu, mine.kt0, i), kt1 = __shfl_sync(0xffffffffu, mine.kt1, i);
+      const int tiles = ceil_div(n, P.tile_tok);
+      w.b = b0 + i;
+      w.cu = __shfl_sync(0xffffffffu, mine.cu, i);
+      w.base = max(0, len - n);
+      w.tok_end = w.cu + n;
+      w.klo = io.window ? clampi(static_cast<int64_t>(w.base) - io.window + 1, 0, len) : 0;
+      w.khi = len;
+      if (!items(w, at, w.cu, tiles, kt0, kt1)) return false;
+      at += set_cost(P, kind, tiles, kt1 - kt0);
     }
   }
-  if (ok) {
-    w.kind = -1;
-    push(w);
-  }
+  return true;
 }
 
-// ---- producer: Q tiles and the ring of K and V tiles
+// ---- producer of one kind of work: hands the pieces out and loads row tiles
+// and K and V tiles (K0 V0 K1 V1 ...)
 template <int D>
-MK_DEV void run_tile_producer(const AttnParams& P, TileSmem<D>& S, const Ctx& c,
-                              const CUtensorMap* tm_q, const CUtensorMap* tm_k,
-                              const CUtensorMap* tm_v) {
+MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const View<D>& V,
+                    const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                    uint64_t* after) {
   const mk_prefix_attn_io& io = P.io;
   constexpr int kHalves = D / 64;
-  const int lane = lane_id();
+  const int lane = lane_id(), kind = V.kind, slot = V.slot, q_tiles = kind == kPair ? 2 : 1;
+  Ring& R = *V.ring;
   const int boxes = kTileKeys / P.box;  // per tile and half
   const int group_tiles = 32 / boxes;   // key tiles whose pages one lane each holds
-  int seq = 0;       // loads into the ring
-  int q_seq = 0;     // loads of row tiles
-  int piece = 0;
-  bool ok = true;
-  auto next_piece = [&](Piece& w) -> bool {
-    const int k = piece % kFifo;
-    if (!wait_warp(c, &S.fifo_full[k], (piece / kFifo) & 1)) return false;
-    w = S.fifo[k];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.fifo_empty[k]);
-    ++piece;
-    return true;
-  };
+  Place at;          // of the next load
+  int loads = 0, n_loaded = 0, n_out = 0;
+  bool ready = after == nullptr;
   // First slot of box number 32 g + lane of a piece; -1: no row sees its keys.
   // A page outside the pool: behind the end, where the copy fills in zeros.
   auto fetch = [&](const Piece& w, int g) -> int {
     const int box = 32 * g + lane, key = w.kt_a * kTileKeys + box * P.box;
-    if (w.kind < 0 || box >= (w.kt_b - w.kt_a) * boxes || key >= w.khi || key + P.box <= w.klo)
-      return -1;
+    if (box >= (w.kt_b - w.kt_a) * boxes || key >= w.khi || key + P.box <= w.klo) return -1;
     const int page = key >> P.page_shift;
-    const int id = w.kind == 0 ? io.prefix_pages[page] : io.block_table[w.b * io.table_stride + page];
+    const int id = w.own ? io.block_table[w.b * io.table_stride + page] : io.prefix_pages[page];
     return id >= 0 && id < io.n_pages ? (id << P.page_shift) + (key & (io.page_size - 1))
                                       : max(1, io.n_pages << P.page_shift);
   };
-  Piece w;
-  ok = next_piece(w);
-  int pages_next = ok ? fetch(w, 0) : -1;
-  while (ok && w.kind >= 0) {
-    // the page numbers are read one group ahead, those of the next piece too:
-    // each read is a round trip to L2 or HBM
-    const Piece me = w;
-    const int t_all = me.kt_b - me.kt_a;
-    int pages = pages_next, pages_ahead = -1, group = 0;
-    if (!(ok = next_piece(w))) break;
-    pages_next = fetch(w, 0);
-    if (t_all > group_tiles) pages_ahead = fetch(me, 1);
-    int pages_old = -1;  // the group before: V follows K by up to two tiles
+  auto push = [&](const Piece& w) -> bool {
+    const int k = n_out % kFifo;
+    if (n_out >= kFifo && !wait_warp(c, &R.fifo_empty[k], ((n_out / kFifo) - 1) & 1)) return false;
+    if (lane == 0) {
+      R.fifo[k] = w;
+      mbar_arrive(&R.fifo_full[k]);
+    }
+    ++n_out;
+    return true;
+  };
+  auto load_piece = [&](const Piece& w, int pages) -> bool {
+    // the buffers belong to the other kind of work until its MMAs are done
+    if (!ready && !wait_warp(c, after, 0)) return false;
+    ready = true;
+    const int n = w.kt_b - w.kt_a;
+    int ahead = n > group_tiles ? fetch(w, 1) : -1, old = -1, group = 0;
     auto load = [&](const CUtensorMap* map, int x) -> bool {
-      const int st = seq % kStages, g = x / group_tiles;
-      if (g > group) {
-        pages_old = pages;
-        pages = pages_ahead;
+      const int g = x / group_tiles;
+      if (g > group) {  // (V follows K by one tile: it may still need the group before)
+        old = pages;
+        pages = ahead;
         group = g;
-        if (t_all > (g + 1) * group_tiles) pages_ahead = fetch(me, g + 1);
+        if (n > (g + 1) * group_tiles) ahead = fetch(w, g + 1);
       }
       // lane = half * boxes + box
       const int box = lane % boxes, half = lane / boxes;
-      const int slot = __shfl_sync(0xffffffffu, g == group ? pages : pages_old,
-                                   (x % group_tiles) * boxes + box);
-      const bool mine = lane < boxes * kHalves && slot >= 0;
-      const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
-      if (seq >= kStages && !wait_warp(c, &S.kv_empty[st], ((seq / kStages) - 1) & 1)) return false;
-      if (lane == 0) mbar_arrive_expect_tx(&S.kv_full[st], n * P.box * 128);
+      const int key = __shfl_sync(0xffffffffu, g == group ? pages : old, (x % group_tiles) * boxes + box);
+      const bool mine = lane < boxes * kHalves && key >= 0;
+      const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, mine));
+      if (loads >= V.stages && !wait_warp(c, &R.empty[at.st], at.round ^ 1)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&R.full[at.st], cnt * P.box * 128);
       __syncwarp();
       if (mine)
-        tma_load_3d(S.kv[st] + half * 128 * 128 + box * P.box * 128, map, &S.kv_full[st],
-                    half * 64, me.h, slot);
-      ++seq;
+        tma_load_3d(V.kv + at.st * (128 * D * 2) + half * 128 * 128 + box * P.box * 128, map,
+                    &R.full[at.st], half * 64, w.h, key);
+      at = at.next(V.stages);
+      ++loads;
       return true;
     };
-    ok = load(tm_k, 0);
-    if (ok && me.alt && t_all > 1) ok = load(tm_k, 1);
-    for (int t = 0; ok && t < (me.alt ? 1 : 2); ++t, ++q_seq) {
-      const int q = q_seq & 1;
-      if (q_seq >= 2 && !(ok = wait_warp(c, &S.q_empty[q], ((q_seq >> 1) - 1) & 1))) break;
+    if (!load(tm_k, 0)) return false;
+    for (int t = 0; t < q_tiles; ++t) {
+      if (n_loaded > 0 && !wait_warp(c, &R.q_empty[t], (n_loaded - 1) & 1)) return false;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&S.q_full[q], kHalves * P.group * P.tile_tok * 128);
+        mbar_arrive_expect_tx(&R.q_full[t], kHalves * P.group * P.tile_tok * 128);
         for (int f = 0; f < kHalves; ++f)
-          tma_load_3d(S.q[q] + f * 128 * 128, tm_q, &S.q_full[q], f * 64, me.h * P.group,
-                      me.tok0 + t * P.tile_tok);
+          tma_load_3d(S.q[slot + t] + f * 128 * 128, tm_q, &R.q_full[t], f * 64, w.h * P.group,
+                      w.tok0 + t * P.tile_tok);
       }
       __syncwarp();
     }
-    const int lead = me.alt ? 2 : 1;
-    for (int x = 0; ok && x < t_all; ++x) {
-      ok = load(tm_v, x);
-      if (ok && x + lead < t_all) ok = load(tm_k, x + lead);
+    ++n_loaded;
+    for (int x = 0; x < n; ++x) {
+      if (!load(tm_v, x)) return false;
+      if (x + 1 < n && !load(tm_k, x + 1)) return false;
     }
+    return true;
+  };
+  // the next piece's pages are read before the piece at hand is loaded: each
+  // read is a round trip to L2 or HBM
+  Piece held;
+  int held_pages = -1;
+  bool have = false;
+  const int line = kind == kPair ? 0 : 1 + slot;
+  const int64_t begin = (kind == kPair ? static_cast<int64_t>(blockIdx.x) : 2ll * blockIdx.x + slot) * S.plan.share[kind];
+  bool ok = walk(P, S.plan, kind, begin, S.first[line], S.first_at[line], [&](const Piece& w) -> bool {
+    if (!push(w)) return false;
+    const int pages = fetch(w, 0);
+    if (have && !load_piece(held, held_pages)) return false;
+    held = w;
+    held_pages = pages;
+    have = true;
+    return true;
+  });
+  if (ok) {
+    Piece none;
+    std::memset(&none, 0, sizeof(none));
+    none.own = -1;
+    ok = push(none) && (!have || load_piece(held, held_pages));
   }
-  if (!ok) {
-    // give up: no copy may land after the CTA has left
-    uint32_t none = 0;
-    const Ctx drain{&none, c.status};
-    for (int s = max(0, seq - kStages); s < seq; ++s)
-      wait_warp(drain, &S.kv_full[s % kStages], (s / kStages) & 1);
-    for (int s = max(0, q_seq - 2); s < q_seq; ++s)
-      wait_warp(drain, &S.q_full[s & 1], (s >> 1) & 1);
-  }
+  if (ok) return true;
+  // give up: no copy may land after the CTA has left
+  uint32_t never = 0;
+  const Ctx drain{&never, c.status};
+  for (int q = max(0, loads - V.stages); q < loads; ++q)
+    wait_warp(drain, &R.full[q % V.stages], (q / V.stages) & 1);
+  for (int t = 0; t < q_tiles && n_loaded > 0; ++t) wait_warp(drain, &R.q_full[t], (n_loaded - 1) & 1);
+  return false;
 }
 
-// ---- MMA issuer: the whole warp walks the pieces, one elected lane issues, so
-// that descriptors and addresses are warp-uniform; false once a wait has run out
+// ---- MMA issuer of one slot: the whole warp walks the pieces, one elected lane
+// issues, so that descriptors and addresses are warp-uniform; false once a wait
+// has run out
+struct SlotParity {
+  uint32_t s = 0, p = 0, o = 0;
+};
+
 template <class T, int D>
-MK_DEV bool issue_mmas(const AttnParams& P, TileSmem<D>& S, const Ctx& c) {
+MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParity& par) {
   constexpr uint32_t kIdS = idesc_of<T>(kTileKeys, false), kIdO = idesc_of<T>(D, true);
-  const uint32_t tm = S.tmem;
-  int seq = 0, q_seq = 0, piece = 0;
-  uint32_t p_par[2] = {0, 0};
+  const int slot = V.slot;
+  const uint32_t ts = S.tmem + slot * 128, to = S.tmem + 256 + slot * 128;
+  Ring& R = *V.ring;
+  const uint64_t qd = sdesc_kmajor_sw128(smem_u32(S.q[slot]));
+  const uint32_t kv = smem_u32(V.kv);
+  Place at;  // of the next K tile
+  int piece = 0;
   auto commit = [&](uint64_t* bar) {
     if (elect_one()) mma_commit(bar);
     __syncwarp();
   };
-  auto wait_stage = [&](int s) { return wait_warp(c, &S.kv_full[s % kStages], (s / kStages) & 1); };
-  auto qk = [&](int slot, int q_tile, int s) {
-    const uint64_t qd = sdesc_kmajor_sw128(smem_u32(S.q[q_tile]));
-    const uint64_t kd = sdesc_kmajor_sw128(smem_u32(S.kv[s % kStages]));
+  auto wait_stage = [&](Place p) { return wait_warp(c, &R.full[p.st], p.round); };
+  // the scores of a tile; its K may be replaced afterwards
+  auto qk = [&](Place p) {
+    const uint64_t kd = sdesc_kmajor_sw128(kv + p.st * (128 * D * 2));
     if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint64_t off = ((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4;
-        mma_bf16(tm + slot * 128, qd + off, kd + off, kIdS, k);
+        mma_bf16(ts, qd + off, kd + off, kIdS, k);
       }
       mma_commit(&S.s_full[slot]);
+      mma_commit(&R.empty[p.st]);
     }
     __syncwarp();
   };
-  auto pv = [&](int slot, int s, bool first) {
-    const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(S.kv[s % kStages]), 128 * 128);
+  auto pv = [&](Place v, int k0, int k1, bool first) {
+    const uint64_t vd = sdesc_mnmajor_sw128(kv + v.st * (128 * D * 2), 128 * 128);
     if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < kTileKeys / 16; ++k)
-        mma_ts(tm + 256 + slot * 128, tm + slot * 128 + 8 * k, vd + k * (16 * 128 >> 4), kIdO,
-               !(first && k == 0));
+      for (int k = k0; k < k1; ++k)
+        mma_ts(to, ts + 8 * k, vd + k * (16 * 128 >> 4), kIdO, !(first && k == 0));
     }
     __syncwarp();
   };
   while (true) {
-    const int k = piece % kFifo;
-    if (!wait_warp(c, &S.fifo_full[k], (piece / kFifo) & 1)) return false;
-    const Piece w = S.fifo[k];
+    const int f = piece % kFifo;
+    if (!wait_warp(c, &R.fifo_full[f], (piece / kFifo) & 1)) return false;
+    const int own = R.fifo[f].own, n = R.fifo[f].kt_b - R.fifo[f].kt_a;
     __syncwarp();
-    if (elect_one()) mbar_arrive(&S.fifo_empty[k]);
-    if (w.kind < 0) return true;
-    const int n[2] = {slot_tiles(w, 0), slot_tiles(w, 1)};
-    // row tile of each slot
-    const int q_tiles = w.alt ? 1 : 2, q0 = q_seq & 1, q1 = w.alt ? q0 : q0 ^ 1;
-    for (int t = 0; t < q_tiles; ++t)
-      if (!wait_warp(c, &S.q_full[(q_seq + t) & 1], ((q_seq + t) >> 1) & 1)) return false;
-    q_seq += q_tiles;
-    auto free_q = [&] {
-      commit(&S.q_empty[q0]);
-      if (q1 != q0) commit(&S.q_empty[q1]);
-    };
-    // scores of the first tiles
-    if (!wait_stage(seq)) return false;
+    if (elect_one()) mbar_arrive(&R.fifo_empty[f]);
+    if (own < 0) return true;
+    if (!wait_warp(c, &R.q_full[V.q_bar], piece & 1) || !wait_stage(at)) return false;
     tc_fence_after();
-    qk(0, q0, seq);
-    if (!w.alt) qk(1, q1, seq);
-    commit(&S.kv_empty[seq % kStages]);
-    ++seq;
-    if (w.alt && n[1] > 0) {
-      if (!wait_stage(seq)) return false;
-      tc_fence_after();
-      qk(1, q1, seq);
-      commit(&S.kv_empty[seq % kStages]);
-      ++seq;
-    }
-    if (n[0] == 1) free_q();
-    for (int j = 0; j < n[0]; ++j) {
-      int sv = 0, sk = 0;
-      for (int slot = 0; slot < 2; ++slot) {
-        if (j >= n[slot]) continue;
-        const bool more = j + 1 < n[slot];
-        const bool fresh = w.alt || slot == 0;   // this slot is the first user of its tiles
-        const bool last_use = w.alt || slot == 1;
-        if (fresh) {
-          sv = seq++;
-          if (more) sk = seq++;
-          if (!wait_stage(sv)) return false;
-        }
-        if (!wait_warp(c, &S.p_full[slot], p_par[slot])) return false;
-        p_par[slot] ^= 1;
+    qk(at);
+    if (n == 1) commit(&R.q_empty[V.q_bar]);
+    for (int j = 0; j < n; ++j) {
+      const Place sv = at.next(V.stages), sk = sv.next(V.stages);
+      const bool more = j + 1 < n;
+      if (!wait_stage(sv) || (more && !wait_stage(sk))) return false;
+      // P V, then the next scores right behind, which take P's place
+      if (kSplitP) {
+        if (!wait_warp(c, &S.p_half[slot], par.p)) return false;
         tc_fence_after();
-        pv(slot, sv, j == 0);
-        if (last_use) commit(&S.kv_empty[sv % kStages]);
-        if (more) {
-          if (fresh && !wait_stage(sk)) return false;
-          tc_fence_after();
-          qk(slot, slot ? q1 : q0, sk);
-          if (last_use) commit(&S.kv_empty[sk % kStages]);
-        } else {
-          commit(&S.o_done[slot]);
-        }
+        pv(sv, 0, kTileKeys / 32, j == 0);
+        if (!wait_warp(c, &S.p_full[slot], par.p)) return false;
+        tc_fence_after();
+        pv(sv, kTileKeys / 32, kTileKeys / 16, false);
+      } else {
+        if (!wait_warp(c, &S.p_full[slot], par.p)) return false;
+        tc_fence_after();
+        pv(sv, 0, kTileKeys / 16, j == 0);
       }
-      // the last scores are on their way: Q may be replaced once they are done
-      if (n[0] > 1 && j == n[0] - 2) free_q();
+      par.p ^= 1;
+      if (more) {
+        qk(sk);
+        if (j == n - 2) commit(&R.q_empty[V.q_bar]);
+      } else {
+        commit(&S.o_done[slot]);
+      }
+      commit(&R.empty[sv.st]);
+      at = sk;
     }
     ++piece;
   }
 }
 
+// ---- softmax of one slot (a warpgroup, one thread per row)
 template <class T, int D>
-MK_DEV void run_mma(const AttnParams& P, TileSmem<D>& S, const Ctx& c) {
-  if (issue_mmas<T, D>(P, S, c)) return;
-  // give up: no MMA may run on after the CTA has left
-  uint32_t none = 0;
-  if (elect_one()) mma_commit(&S.drained);
-  __syncwarp();
-  wait_warp(Ctx{&none, c.status}, &S.drained, 0);
-}
-
-// ---- softmax (one warpgroup per slot, one thread per row)
-template <class T, int D>
-MK_DEV void run_softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, int slot) {
+MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const View<D>& W,
+                    SlotParity& par) {
   const mk_prefix_attn_io& io = P.io;
+  const int slot = W.slot, kind = W.kind;
+  Ring& R = *W.ring;
   const int warp = (threadIdx.x >> 5) & 3, lane = lane_id(), row = warp * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   const uint32_t ts = S.tmem + lanes + slot * 128, to = S.tmem + lanes + 256 + slot * 128;
   const int G = P.group, tok_in_tile = row / G, g = row - tok_in_tile * G;
   const float sl2 = P.scale_log2;
-  int seq = 0, piece = 0;
-  uint32_t s_par = 0, o_par = 0;
+  Place at;  // of the tile's K
+  int piece = 0;
   while (true) {
-    const int k = piece % kFifo;
-    if (!wait_warp(c, &S.fifo_full[k], (piece / kFifo) & 1)) return;
-    const Piece w = S.fifo[k];
+    const int f = piece % kFifo;
+    if (!wait_warp(c, &R.fifo_full[f], (piece / kFifo) & 1)) return false;
+    const Piece w = R.fifo[f];
     __syncwarp();
-    if (lane == 0) mbar_arrive(&S.fifo_empty[k]);
-    if (w.kind < 0) return;
+    if (lane == 0) mbar_arrive(&R.fifo_empty[f]);
+    if (w.own < 0) return true;
     ++piece;
-    const int n = slot_tiles(w, slot);
-    const int seq0 = seq;
-    seq += 2 * (w.kt_b - w.kt_a);
+    const int n = w.kt_b - w.kt_a;
     // this thread's row: its token, and the keys [klo, khi) it sees; of a token
     // tree, the bits of `tree` instead from key `tree_at` on
-    const int tok = w.tok0 + (w.alt ? 0 : slot * P.tile_tok) + tok_in_tile;
+    const int tok = w.tok0 + (kind == kPair ? slot * P.tile_tok : 0) + tok_in_tile;
     const bool valid = tok_in_tile < P.tile_tok && tok < w.tok_end;
     int klo = w.klo, khi = w.khi, tree_at = INT_MAX;
     uint64_t tree = 0;
     if (valid) {
       int base = w.base, i = tok - w.cu;
-      if (w.kind == 0 && io.window) {  // which request is it?
+      if (!w.own && io.window) {  // which request is it?
         int lo = 0, hi = io.n_requests;
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
@@ -732,10 +768,10 @@ MK_DEV void run_softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, int s
       if (io.window) {
         const int depth = io.tree_mask ? max(1, __popcll(tree)) - 1 : i;
         const int64_t low = static_cast<int64_t>(base) + depth - io.window + 1 +
-                            (w.kind == 0 ? io.prefix_len : 0);
+                            (w.own ? 0 : io.prefix_len);
         klo = max(klo, clampi(low, 0, w.khi));
       }
-      if (w.kind == 1) {
+      if (w.own) {
         if (io.tree_mask) tree_at = base;
         else khi = min(khi, clampi(static_cast<int64_t>(base) + i + 1, 0, INT_MAX));
       }
@@ -744,12 +780,12 @@ MK_DEV void run_softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, int s
 
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
-      const int kt = w.kt_a + (w.alt ? 2 * j + slot : j), k0 = kt * kTileKeys;
-      if (!wait_warp(c, &S.s_full[slot], s_par)) return;
-      s_par ^= 1;
+      const int k0 = (w.kt_a + j) * kTileKeys;
+      if (!wait_warp(c, &S.s_full[slot], par.s)) return false;
+      par.s ^= 1;
       tc_fence_after();
+      float s[kTileKeys];
       if (warp_valid) {
-        float s[kTileKeys];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s + 32 * q);
         tmem_ld_wait();
@@ -769,81 +805,88 @@ MK_DEV void run_softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, int s
               if (!(see & (1u << i))) s[32 * q + i] = -INFINITY;
           }
         }
-        float t8[8];
+        float t4[4];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) t8[x] = s[x];
+        for (int y = 0; y < 4; ++y) t4[y] = max3(s[y], s[y + 4], s[y + 8]);
 #pragma unroll
-        for (int x = 8; x < kTileKeys; ++x) t8[x & 7] = fmaxf(t8[x & 7], s[x]);
-        const float top = sl2 * fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])),
-                                      fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
+        for (int x = 12; x < kTileKeys - 4; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) t4[y] = max3(t4[y], s[x + y], s[x + y + 4]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) t4[y] = fmaxf(t4[y], s[kTileKeys - 4 + y]);
+        const float top = sl2 * fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         // rescale only when the maximum has grown by 2^8: until then P is at most
         // 2^8, which its types and the 32-bit sums hold without loss
         const bool grow = valid && top > m + kGrow;
         if (j == 0) {
           m = top;
         } else if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? exp2_approx(m - top) : 1.f;
+          const float x = grow ? exp2_approx(m - top) : 1.f;
           if (grow) m = top;
-          l *= f;
+          l *= x;
 #pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             float o[32];
             tmem_ld32(to + 32 * q, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] *= f;
+            for (int y = 0; y < 32; ++y) o[y] *= x;
             tmem_st32(to + 32 * q, reinterpret_cast<uint32_t*>(o));
           }
         }
-        const float ms = m == -INFINITY ? 0.f : m;
-        uint32_t p[kTileKeys / 2];
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int x = 0; x < kTileKeys; x += 2) {
-          const float a = exp2_approx(fmaf(s[x], sl2, -ms));
-          const float b = exp2_approx(fmaf(s[x + 1], sl2, -ms));
-          sum[(x >> 1) & 3] += a + b;
-          p[x >> 1] = Types<T>::pack(a, b);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st32(ts, p);
-        tmem_st32(ts + 32, p + 32);
-        tmem_st_wait();
       }
       if (k0 < w.klo || k0 + kTileKeys > w.khi) {
         // keys that no row sees may hold anything: their V rows become zeros, so
         // that a weight of zero leaves no NaN behind
-        const int t = w.kt_b - w.kt_a, x = kt - w.kt_a;  // its place among the loads
-        const int v_seq = seq0 + (w.alt ? min(2, t) + x + min(x, max(0, t - 2)) : 1 + 2 * x);
-        if (!wait_warp(c, &S.kv_full[v_seq % kStages], (v_seq / kStages) & 1)) return;
+        const Place sv = at.next(W.stages);
+        if (!wait_warp(c, &R.full[sv.st], sv.round)) return false;
         if (k0 + row < w.klo || k0 + row >= w.khi) {
+          uint8_t* v = W.kv + sv.st * (128 * D * 2) + row * 128;
 #pragma unroll
-          for (int f = 0; f < D / 64; ++f)
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              reinterpret_cast<uint4*>(S.kv[v_seq % kStages] + f * 128 * 128 + row * 128)[x] =
-                  make_uint4(0, 0, 0, 0);
+          for (int x = 0; x < D / 8; ++x)
+            reinterpret_cast<uint4*>(v + (x >> 3) * 128 * 128)[x & 7] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.p_full[slot]);
+      // P = 2^(S - m), 64 keys at a time
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (warp_valid) {
+          const float ms = m == -INFINITY ? 0.f : m;
+          uint32_t p[kTileKeys / 4];
+          float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+          for (int x = 0; x < kTileKeys / 2; x += 2) {
+            float2 y = fma2(make_float2(s[64 * half + x], s[64 * half + x + 1]),
+                            make_float2(sl2, sl2), make_float2(-ms, -ms));
+            y.x = exp2_approx(y.x);
+            y.y = exp2_approx(y.y);
+            sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], y);
+            p[x >> 1] = Types<T>::pack(y.x, y.y);
+          }
+          const float2 both = add2(sum[0], sum[1]);
+          l += both.x + both.y;
+          tmem_st32(ts + 32 * half, p);
+        }
+        if (half || kSplitP) {
+          if (warp_valid) tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(half ? &S.p_full[slot] : &S.p_half[slot]);
+        }
+      }
+      at = at.next(W.stages).next(W.stages);
     }
 
     // the piece's result
-    if (n > 0) {
-      if (!wait_warp(c, &S.o_done[slot], o_par)) return;
-      o_par ^= 1;
-      tc_fence_after();
-    }
-    int64_t at;
-    const int64_t by_row = static_cast<int64_t>(tok) * io.n_q_heads + w.h * G + g;
-    if (!w.first) at = P.ws.carry + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * 128 + row;
-    else if (w.kind == 0) at = w.alt && slot ? P.ws.pre1 + w.h * 128 + row : P.ws.pre0 + by_row;
-    else at = (w.alt && slot ? P.ws.own1 : P.ws.own0) + by_row;
-    if (valid) P.ws.ml[at] = make_float2(m, l);
-    if (n > 0 && warp_valid) {
+    if (!wait_warp(c, &S.o_done[slot], par.o)) return false;
+    par.o ^= 1;
+    tc_fence_after();
+    const int64_t to_row = w.first ? (w.own ? P.ws.own : P.ws.pre) +
+                                     static_cast<int64_t>(tok) * io.n_q_heads + w.h * G + g
+                               : P.ws.carry + ((static_cast<int64_t>(kind) * P.ctas + blockIdx.x) * 2 + slot) * 128 + row;
+    if (valid) P.ws.ml[to_row] = make_float2(m, l);
+    if (warp_valid) {
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         float o[32];
@@ -851,7 +894,7 @@ MK_DEV void run_softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, int s
         tmem_ld_wait();
         if (valid) {
           // whole sectors: a thread's row is its own
-          float* dst = P.ws.o + at * D + 32 * q;
+          float* dst = P.ws.o + to_row * D + 32 * q;
 #pragma unroll
           for (int x = 0; x < 32; x += 8) st_global_8(dst + x, o + x);
         }
@@ -861,6 +904,23 @@ MK_DEV void run_softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, int s
   }
 }
 
+MK_DEV void init_ring(Ring& R, int slots) {
+  for (int i = 0; i < kMaxStages; ++i) {
+    mbar_init(&R.full[i], 1);
+    mbar_init(&R.empty[i], slots);
+  }
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&R.q_full[i], 1);
+    mbar_init(&R.q_empty[i], 1);
+  }
+  for (int i = 0; i < kFifo; ++i) {
+    mbar_init(&R.fifo_full[i], 1);
+    mbar_init(&R.fifo_empty[i], 5 * slots);
+  }
+}
+
+// Warps 0-3 and 4-7: softmax of slot 0 and 1.  Warps 8 and 9: producers (8 for
+// pairs and slot 0's solos, 9 for slot 1's solos).  Warps 10 and 11: MMA issuers.
 template <class T, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
     k_attn_tiles(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap tm_q,
@@ -870,29 +930,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                                    ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&S.kv_full[i], 1);
-      mbar_init(&S.kv_empty[i], 1);
-    }
-    mbar_init(&S.drained, 1);
+    for (int i = 0; i < 3; ++i) init_ring(S.ring[i], i == 0 ? 2 : 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.q_full[i], 1);
-      mbar_init(&S.q_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_half[i], 4);
       mbar_init(&S.p_full[i], 4);
       mbar_init(&S.o_done[i], 1);
+      mbar_init(&S.drained[i], 1);
     }
-    for (int i = 0; i < kFifo; ++i) {
-      mbar_init(&S.fifo_full[i], 1);
-      mbar_init(&S.fifo_empty[i], 10);
-    }
+    mbar_init(&S.turn, 2);
     S.abort = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
-  if (warp == 9) {
+  if (warp == 10) {
     tmem_alloc(&S.tmem, 512);
     tmem_relinquish();
   }
@@ -903,52 +956,79 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   pdl_launch_dependents();
   const Ctx c{&S.abort, P.ws.status};
-  // 2 x 128 x 208 + 128 x 72 = 62,464 of the 64,512 registers of the launch; all
-  // are back at 168 before the common tail
+  // 2 x 128 x 208 + 128 x 88 = 64,512, all registers of the launch; all are back
+  // at 168 before the common tail
+  const int first_kind = blockIdx.x & 1;
   if (warp < 8) {
     reg_alloc<208>();
-    run_softmax<T, D>(P, S, c, warp >> 2);
+    const int slot = warp >> 2;
+    SlotParity par;
+    bool ok = true;
+#pragma unroll 1
+    for (int turn = 0; ok && turn < 2; ++turn)
+      ok = softmax<T, D>(P, S, c, View<D>(S, first_kind ^ turn, slot), par);
     __syncwarp();
     reg_dealloc<168>();
   } else {
-    reg_dealloc<72>();
-    if (warp == 8) run_tile_producer<D>(P, S, c, &tm_q, &tm_k, &tm_v);
-    else if (warp == 9) run_mma<T, D>(P, S, c);
-    else if (warp == 10) run_scheduler<D>(P, S, c);
+    reg_dealloc<88>();
+    const int slot = warp & 1;
+    bool ok = true;
+    if (warp < 10) {
+#pragma unroll 1
+      for (int turn = 0; ok && turn < 2; ++turn)
+        if ((first_kind ^ turn) == kSolo || slot == 0)
+          ok = produce<D>(P, S, c, View<D>(S, first_kind ^ turn, slot), &tm_q, &tm_k, &tm_v,
+                          turn ? &S.turn : nullptr);
+    } else {
+      SlotParity par;
+#pragma unroll 1
+      for (int turn = 0; ok && turn < 2; ++turn) {
+        ok = issue_mmas<T, D>(S, c, View<D>(S, first_kind ^ turn, slot), par);
+        if (ok && turn == 0) {
+          if (elect_one()) mma_commit(&S.turn);
+          __syncwarp();
+        }
+      }
+      if (!ok) {
+        // give up: no MMA may run on after the CTA has left
+        uint32_t never = 0;
+        if (elect_one()) mma_commit(&S.drained[slot]);
+        __syncwarp();
+        wait_warp(Ctx{&never, c.status}, &S.drained[slot], 0);
+      }
+    }
     __syncwarp();
     reg_alloc<168>();
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(S.tmem, 512);
+  if (warp == 10) tmem_dealloc(S.tmem, 512);
 }
 
 // ------------------------------------------------------------------ merge
 
-// The stretches of one item that hold a row: by row (its first piece) and by
-// the CTAs c0 + 1 .. c1, in one slot or both.
+// The stretches of one item that hold a row: its first one, by row, and those
+// of the owners (CTAs or slots) behind it on the line.
 struct Held {
-  int64_t main0, main1, carry;  // partial rows; carry of CTA c0 + 1's slot
-  int32_t ctas, slots;
-  MK_DEV int count() const { return ctas * slots; }
-  MK_DEV int64_t at(int e) const {
-    const int c = slots == 2 ? e >> 1 : e, s = slots == 2 ? e & 1 : 0;
-    return c == 0 ? (s ? main1 : main0) : carry + static_cast<int64_t>(c - 1) * 256 + s * 128;
-  }
+  int64_t first, carry, step;
+  int count;
+  MK_DEV int64_t at(int e) const { return e == 0 ? first : carry + e * step; }
 };
-MK_DEV Held held(const AttnParams& P, int64_t share, int64_t start, int tile, int tiles, int kt,
-                 int64_t main0, int64_t main1, int row) {
+MK_DEV Held held(const AttnParams& P, const Plan& plan, int tile, int tiles, int kt, int h,
+                 int64_t pairs_at, int64_t solos_at, int64_t first, int row) {
+  const int kind = tile == tiles - 1 && (tiles & 1) ? kSolo : kPair;
+  const int64_t s = (kind == kPair ? pairs_at : solos_at) +
+                    (kind == kSolo ? h : (tile >> 1) * P.io.n_kv_heads + h) * item_cost(kind, kt) +
+                    item_over(kind);
+  const int64_t o0 = s / plan.share[kind];
+  const int64_t o1 = (s + static_cast<int64_t>(kt - 1) * kTileCost) / plan.share[kind];
   Held x;
-  const bool alt = tile == tiles - 1 && (tiles & 1);
-  const int steps = alt ? (kt + 1) >> 1 : kt;
-  const int64_t c0 = start / share;
-  const int64_t c1 = (start + static_cast<int64_t>(steps - 1) * (alt ? kAltCost : kPairCost)) / share;
-  x.ctas = steps > 0 ? static_cast<int>(c1 - c0) + 1 : 0;
-  x.slots = alt ? 2 : 1;
-  x.main0 = main0;
-  x.main1 = main1;
-  x.carry = P.ws.carry + (c0 + 1) * 256 + (alt ? 0 : (tile & 1) * 128) + row;
+  x.count = kt > 0 ? static_cast<int>(o1 - o0) + 1 : 0;
+  x.first = first;
+  x.step = kind == kPair ? 256 : 128;
+  x.carry = P.ws.carry + kind * P.ctas * 256ll + o0 * x.step + (kind == kPair ? (tile & 1) * 128 : 0) + row;
   return x;
 }
 
@@ -974,24 +1054,17 @@ __global__ void __launch_bounds__(256) k_attn_merge(const __grid_constant__ Attn
   const int tt = P.tile_tok;
   Held x[2];
   {
-    const int tile = tok / tt, kt = plan.kt1 - plan.kt0;
-    const int row = (tok - tile * tt) * G + g;
-    const int64_t start = h * head_cost(plan.tiles, kt) +
-                          static_cast<int64_t>(tile >> 1) * kt * kPairCost;
-    x[0] = held(P, plan.share, start, tile, plan.tiles, kt, P.ws.pre0 + item,
-                P.ws.pre1 + h * 128 + row, row);
+    const int tile = tok / tt;
+    x[0] = held(P, plan, tile, plan.tiles, plan.kt1 - plan.kt0, h, 0, 0, P.ws.pre + item,
+                (tok - tile * tt) * G + g);
   }
   {
-    const int i = tok - r.cu, tiles = ceil_div(r.n, tt), tile = i / tt, kt = r.kt1 - r.kt0;
-    const int row = (i - tile * tt) * G + g;
-    const int64_t pair_cost = static_cast<int64_t>(kt) * kPairCost;
-    const bool alt = tile == tiles - 1 && (tiles & 1);
-    const int64_t start =
-        P.ws.cost[lo] + (tile >> 1) * pair_cost * io.n_kv_heads +
-        h * (alt ? static_cast<int64_t>((kt + 1) >> 1) * kAltCost : pair_cost);
-    x[1] = held(P, plan.share, start, tile, tiles, kt, P.ws.own0 + item, P.ws.own1 + item, row);
+    const int i = tok - r.cu, tile = i / tt;
+    x[1].count = 0;
+    if (i >= 0 && i < r.n) x[1] = held(P, plan, tile, ceil_div(r.n, tt), r.kt1 - r.kt0, h, P.ws.cost[lo],
+                P.ws.cost[io.n_requests + lo], P.ws.own + item, (i - tile * tt) * G + g);
   }
-  const int n0 = x[0].count(), n = n0 + x[1].count();
+  const int n0 = x[0].count, n = n0 + x[1].count;
   float M = -INFINITY, L = 0.f, acc[V] = {};
   for (int a = 0; a < n; a += 32) {
     const int e = a + lane;
@@ -1061,18 +1134,16 @@ int64_t align256(int64_t v) { return (v + 255) & ~static_cast<int64_t>(255); }
 // Lays the workspace out over `base`; returns its size.
 int64_t lay_out(const mk_prefix_attn_io* io, int ctas, uint8_t* base, Space* s) {
   const int64_t heads = static_cast<int64_t>(io->n_rows) * io->n_q_heads;
-  s->pre0 = 0;
-  s->own0 = heads;
-  s->own1 = 2 * heads;
-  s->pre1 = 3 * heads;
-  s->carry = s->pre1 + io->n_kv_heads * 128ll;
-  const int64_t rows = s->carry + ctas * 256ll;
+  s->pre = 0;
+  s->own = heads;
+  s->carry = 2 * heads;
+  const int64_t rows = s->carry + 2 * ctas * 256ll;
   int64_t at = 0;
   s->status = reinterpret_cast<uint32_t*>(base);
   s->plan = reinterpret_cast<Plan*>(base + 64);
   at = 256;
   s->cost = reinterpret_cast<int64_t*>(base + at);
-  at = align256(at + (io->n_requests + 1) * 8ll);
+  at = align256(at + io->n_requests * 16ll);
   s->ml = reinterpret_cast<float2*>(base + at);
   at = align256(at + rows * 8);
   s->o = reinterpret_cast<float*>(base + at);
