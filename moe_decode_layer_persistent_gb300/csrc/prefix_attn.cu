@@ -15,9 +15,9 @@
 //   pairs  two row tiles on the same key tiles: bound by the tensor cores.  The
 //          CTAs (one per SM) get an equal stretch of the line each, and a CTA's
 //          two slots take a row tile each;
-//   solos  one row tile (a row set's last one, if their number is odd; most
-//          requests' own rows): bound by the K and V bytes.  The slots of all
-//          CTAs get an equal stretch each.
+//   solos  one tile of up to 64 rows (what is left of a row set behind its
+//          pairs, most requests' own rows): bound by the K and V bytes.  The
+//          slots of all CTAs get an equal stretch each.
 // A stretch may begin and end anywhere, whatever heads, requests and keys it
 // crosses.  CTAs with an even number start with their pairs, the others with
 // their solos, so that the tensor cores and HBM are both busy all the time.
@@ -46,29 +46,33 @@ constexpr int kTileCost = 2;
 MK_DEV constexpr int item_over(int kind) { return kind == kPair ? 6 : 3; }
 
 constexpr int kTileKeys = 128;
-constexpr bool kSplitP = false;
 constexpr int kFifo = 4;            // pieces handed out ahead
 constexpr int kTileThreads = 384;
 constexpr float kGrow = 8.f;        // the maximum may lag by 2^8 before O is rescaled
 constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
 
-// How the lines are laid out (every CTA of k_attn_tiles works it out for
-// itself, the first leaves it for k_attn_merge).
+// How the lines are laid out (every CTA of k_attn_tiles works it out for itself).
 struct Plan {
   int64_t total[2], share[2];  // cost of everything, of one CTA (pairs) or slot (solos)
   int64_t prefix_cost[2];      // the prefix items come first
   int32_t n_used;              // rows in use
-  int32_t tiles;               // row tiles of the prefix
   int32_t kt0, kt1;            // key tiles of the prefix that some row sees
   int32_t lo;                  // first prefix key that some row sees
 };
 
+// One row's result of one stretch of key tiles; its O is beside it.
+struct Partial {
+  float m, l;
+  // of an item's first stretch: 2 * (stretches behind it) + kind, and the row's
+  // place in this stretch's part of the carry region, from which those of the
+  // stretches behind it follow
+  int32_t more, carry;
+};
+
 // Workspace layout.
 struct Space {
-  uint32_t* status;
-  Plan* plan;
-  int64_t* cost;    // [2][B]: where request b's items start on each line
-  float2* ml;       // (m, l) per partial row
+  uint32_t* status;  // [0] the status, [1] whether any row sees a prefix key
+  Partial* part;
   float* o;         // D values per partial row
   // first partial row of each region: the prefix's and the requests' own
   // results by row and head; those of stretches that start in the middle of an
@@ -81,6 +85,7 @@ struct AttnParams {
   float scale_log2;  // scale * log2(e)
   int32_t group;     // G: q heads per KV head
   int32_t tile_tok;  // tokens per row tile: floor(128 / G)
+  int32_t half_tok;  // tokens per solo: floor(64 / G)
   int32_t box;       // keys per TMA box: min(page_size, 128)
   int32_t page_shift;
   int32_t ctas;
@@ -113,12 +118,16 @@ MK_DEV Req read_req(const AttnParams& P, int b) {
   return make_req(P, P.io.cu_rows[b], P.io.cu_rows[b + 1], P.io.lens[b]);
 }
 
-// Items of a row set of `tiles` row tiles for one head: pairs, or the odd tile.
-MK_DEV int items_of(int kind, int tiles) { return kind == kPair ? tiles >> 1 : tiles & 1; }
+// Items of a row set of n tokens for one head: pairs of row tiles, the last one
+// of what is left if that is more than 64 rows; a solo of what is left otherwise.
+MK_DEV int items_of(const AttnParams& P, int kind, int n) {
+  const int full = n / (2 * P.tile_tok), left = n - full * 2 * P.tile_tok;
+  return kind == kPair ? full + (left > P.half_tok) : left > 0 && left <= P.half_tok;
+}
 MK_DEV int64_t item_cost(int kind, int kt) { return item_over(kind) + static_cast<int64_t>(kt) * kTileCost; }
 // Cost of all of a row set's items against kt key tiles.
-MK_DEV int64_t set_cost(const AttnParams& P, int kind, int tiles, int kt) {
-  return kt > 0 ? items_of(kind, tiles) * item_cost(kind, kt) * P.io.n_kv_heads : 0;
+MK_DEV int64_t set_cost(const AttnParams& P, int kind, int n, int kt) {
+  return kt > 0 ? items_of(P, kind, n) * item_cost(kind, kt) * P.io.n_kv_heads : 0;
 }
 
 // ------------------------------------------------------------------ tiles
@@ -132,6 +141,8 @@ struct Piece {
   int32_t kt_a, kt_b;
   int32_t klo, khi;  // keys that some row sees
   int32_t first;     // starts its item: leaves its result by row, else by CTA
+  int32_t more;      // stretches of the item behind this one (of a first one)
+  int32_t split;     // tokens of slot 0's row tile of a pair
   int32_t cu, base;
 };
 
@@ -157,13 +168,18 @@ struct Place {
 
 template <int D>
 struct alignas(1024) TileSmem {
-  // K and V tiles in flight: shared by the slots for pairs, a part each for solos
+  // Row tiles and K and V tiles in flight.  Pairs: two row tiles, then kStages
+  // tiles.  Solos: for each slot its row tile of 64 rows, then kSoloStages tiles.  (A solo's MMA reads 128 rows: those behind the 64
+  // are whatever lies there, and so are the rows of the result that nobody
+  // reads.)  Three stages per slot instead of two keep a K or V tile on its way
+  // while the two before it are in use.
+  static constexpr int kTile = 128 * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr int kSoloStages = D == 128 ? 2 : 4;
-  uint8_t q[2][128 * D * 2];
-  uint8_t kv[kStages][128 * D * 2];
+  static constexpr int kSoloStages = D == 128 ? 3 : 6;
+  static constexpr int kArena = (kStages + 2 > 2 * kSoloStages + 1 ? kStages + 2 : 2 * kSoloStages + 1) * kTile;
+  uint8_t arena[kArena];
   Ring ring[3];      // of pairs, of slot 0's solos, of slot 1's
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
+  uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t turn;     // both slots' MMAs of the first kind of work are done
   uint64_t drained[2];
   Plan plan;
@@ -187,13 +203,17 @@ template <int D>
 struct View {
   Ring* ring;
   uint8_t* kv;       // its part of the buffers
+  uint8_t* q;        // the slot's row tile
   int kind, slot, stages;
   int q_bar;         // the slot's row tile among the ring's
   MK_DEV View(TileSmem<D>& S, int kind_, int slot_) : kind(kind_), slot(slot_) {
     const bool pair = kind == kPair;
     ring = &S.ring[pair ? 0 : 1 + slot];
     stages = pair ? TileSmem<D>::kStages : TileSmem<D>::kSoloStages;
-    kv = S.kv[pair ? 0 : slot * TileSmem<D>::kSoloStages];
+    constexpr int kTile = TileSmem<D>::kTile;
+    uint8_t* part = S.arena + slot * (kTile / 2 + TileSmem<D>::kSoloStages * kTile);  // of a solo's slot
+    kv = pair ? S.arena + 2 * kTile : part + kTile / 2;
+    q = pair ? S.arena + slot * kTile : part;
     q_bar = pair ? slot : 0;
   }
 };
@@ -357,9 +377,8 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
       cost[0][i] = cost[1][i] = 0;
       if (b0 + i < B) {
         const Req r = make_req(P, cu[i], cu[i + 1], len[i]);
-        const int tiles = ceil_div(r.n, P.tile_tok);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) cost[k][i] = set_cost(P, k, tiles, r.kt1 - r.kt0);
+        for (int k = 0; k < 2; ++k) cost[k][i] = set_cost(P, k, r.n, r.kt1 - r.kt0);
         if (r.n) low = min(low, r.base);
       }
       mine[0] += cost[0][i];
@@ -374,33 +393,42 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
     all[1] += mine[1];
   }
   // the sums of all costs, and the lowest position of any row, which decides
-  // where the prefix starts to be seen
+  // where the prefix starts to be seen; in the same turn the running sums over
+  // the warp
+  int64_t v[2] = {all[0], all[1]};
+#pragma unroll
   for (int k = 0; k < 2; ++k) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) all[k] += __shfl_xor_sync(0xffffffffu, all[k], o);
-    if (lane == 0) S.sum[k][warp] = all[k];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v[k], o);
+      if (lane >= o) v[k] += u;
+    }
+    if (lane == 31) S.sum[k][warp] = v[k];
   }
   low = __reduce_min_sync(0xffffffffu, low);
   if (lane == 0) S.low[warp] = low;
   __syncthreads();
+  int64_t before[2] = {0, 0};
   all[0] = all[1] = 0;
 #pragma unroll
   for (int w = 0; w < kTileThreads / 32; ++w) {
-    all[0] += S.sum[0][w];
-    all[1] += S.sum[1][w];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (w < warp) before[k] += S.sum[k][w];
+      all[k] += S.sum[k][w];
+    }
     low = min(low, S.low[w]);
   }
   Plan p;
   const int64_t lo64 =
       io.window && low != INT_MAX ? static_cast<int64_t>(io.prefix_len) + low - io.window + 1 : 0;
   p.n_used = n_used;
-  p.tiles = ceil_div(n_used, P.tile_tok);
   p.lo = clampi(lo64, 0, io.prefix_len);
   p.kt1 = ceil_div(io.prefix_len, kTileKeys);
   p.kt0 = p.lo >= io.prefix_len ? p.kt1 : p.lo / kTileKeys;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    p.prefix_cost[k] = set_cost(P, k, p.tiles, p.kt1 - p.kt0);
+    p.prefix_cost[k] = set_cost(P, k, p.n_used, p.kt1 - p.kt0);
     p.total[k] = p.prefix_cost[k] + all[k];
     const int n = k == kPair ? P.ctas : 2 * P.ctas;
     // at least one key tile each, so that every stretch inside an item has one
@@ -411,20 +439,36 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   if (threadIdx.x == 0) {
     S.plan = p;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) S.first[i] = 0, S.first_at[i] = p.prefix_cost[i > 0];
-    if (blockIdx.x == 0) *P.ws.plan = p;
+    for (int i = 0; i < 3; ++i)
+      if (begin[i] < p.prefix_cost[i > 0] || begin[i] >= p.total[i > 0])
+        S.first[i] = 0, S.first_at[i] = p.prefix_cost[i > 0];
+    if (blockIdx.x == 0) {
+      P.ws.status[0] = 0;
+      P.ws.status[1] = p.kt1 > p.kt0;
+    }
   }
-  // where each request starts: the requests of this CTA's stretches, and from
-  // the first CTA all of them
-  bool need = blockIdx.x == 0;
+  // the requests that this CTA's stretches start in
+  auto find = [&](int t, int64_t here0, int64_t here1) {
+    int64_t here[2] = {here0, here1};
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    need |= begin[i] >= p.prefix_cost[i > 0] && begin[i] < p.total[i > 0];
-  if (!need) return;
+    for (int i = 0; i < kReqs; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int j = k; j < (k == kPair ? 1 : 3); ++j)
+          if (begin[j] >= here[k] && begin[j] < here[k] + cost[k][i])
+            S.first[j] = t * kTurn + threadIdx.x * kReqs + i, S.first_at[j] = here[k];
+        here[k] += cost[k][i];
+      }
+  };
+  if (turns == 1) {
+    find(0, p.prefix_cost[0] + before[0] + v[0] - mine[0], p.prefix_cost[1] + before[1] + v[1] - mine[1]);
+    return;
+  }
   int64_t at[2] = {p.prefix_cost[0], p.prefix_cost[1]};
   for (int t = 0; t < turns; ++t) {
-    if (turns > 1) read_costs(t);
-    int64_t v[2] = {mine[0], mine[1]};
+    read_costs(t);
+    v[0] = mine[0], v[1] = mine[1];
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -436,26 +480,13 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
       if (lane == 31) S.sum[k][warp] = v[k];
     }
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      int64_t here = at[k] + v[k] - mine[k];
-#pragma unroll
-      for (int w = 0; w < kTileThreads / 32; ++w) {
-        if (w < warp) here += S.sum[k][w];
+    int64_t here[2] = {at[0] + v[0] - mine[0], at[1] + v[1] - mine[1]};
+    for (int w = 0; w < kTileThreads / 32; ++w)
+      for (int k = 0; k < 2; ++k) {
+        if (w < warp) here[k] += S.sum[k][w];
         at[k] += S.sum[k][w];
       }
-#pragma unroll
-      for (int i = 0; i < kReqs; ++i) {
-        const int b = t * kTurn + threadIdx.x * kReqs + i;
-        if (b < B) {
-          if (blockIdx.x == 0) P.ws.cost[static_cast<int64_t>(k) * B + b] = here;
-#pragma unroll
-          for (int j = k; j < (k == kPair ? 1 : 3); ++j)
-            if (begin[j] >= here && begin[j] < here + cost[k][i]) S.first[j] = b, S.first_at[j] = here;
-        }
-        here += cost[k][i];
-      }
-    }
+    find(t, here[0], here[1]);
   }
 }
 
@@ -467,10 +498,12 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int64_t begin,
   const int Hk = io.n_kv_heads, lane = lane_id(), over = item_over(kind);
   const int64_t end = min(plan.total[kind], begin + plan.share[kind]);
   if (begin >= end) return true;
-  // the items of a row set (row tile by row tile, head by head) from cost `at`
-  auto items = [&](Piece& w, int64_t at, int tok, int tiles, int kt0, int kt1) -> bool {
-    const int kt = kt1 - kt0, count = items_of(kind, tiles) * Hk;
+  // the items of a row set of n tokens (row tile by row tile, head by head) from
+  // cost `at`
+  auto items = [&](Piece& w, int64_t at, int tok, int n, int kt0, int kt1) -> bool {
+    const int kt = kt1 - kt0, rows = items_of(P, kind, n), count = rows * Hk;
     if (kt <= 0 || count == 0) return true;
+    const int left = n - (rows - 1) * 2 * P.tile_tok;  // of the last pair
     const int64_t cost = item_cost(kind, kt);
     int i = begin > at ? static_cast<int>((begin - at) / cost) : 0;
     int p = i / Hk, h = i - p * Hk;
@@ -481,10 +514,14 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int64_t begin,
       const int s1 = room >= static_cast<int64_t>(kt) * kTileCost ? kt : static_cast<int>(room) / kTileCost;
       if (s0 < s1) {
         w.h = h;
-        w.tok0 = tok + (kind == kPair ? 2 * p : tiles - 1) * P.tile_tok;
+        // (behind its pairs the row set's solo)
+        w.tok0 = tok + 2 * P.tile_tok * (kind == kPair ? p : n / (2 * P.tile_tok));
+        w.split = kind == kPair && p == rows - 1 && left <= 2 * P.half_tok ? P.half_tok : P.tile_tok;
         w.kt_a = kt0 + s0;
         w.kt_b = kt0 + s1;
         w.first = s0 == 0;
+        const int64_t last = s + static_cast<int64_t>(kt - 1) * kTileCost - begin;
+        w.more = last < plan.share[kind] ? 0 : static_cast<int>(last / plan.share[kind]);
         if (!emit(w)) return false;
       }
       if (++h == Hk) h = 0, ++p;
@@ -497,7 +534,7 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int64_t begin,
     w.tok_end = plan.n_used;
     w.klo = plan.lo;
     w.khi = io.prefix_len;
-    if (!items(w, 0, 0, plan.tiles, plan.kt0, plan.kt1)) return false;
+    if (!items(w, 0, 0, plan.n_used, plan.kt0, plan.kt1)) return false;
   }
   w.own = 1;
   int64_t at = first_at;
@@ -508,15 +545,14 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int64_t begin,
     for (int i = 0; at < end && i < 32 && b0 + i < io.n_requests; ++i) {
       const int n = __shfl_sync(0xffffffffu, mine.n, i), len = __shfl_sync(0xffffffffu, mine.len, i);
       const int kt0 = __shfl_sync(0xffffffffu, mine.kt0, i), kt1 = __shfl_sync(0xffffffffu, mine.kt1, i);
-      const int tiles = ceil_div(n, P.tile_tok);
       w.b = b0 + i;
       w.cu = __shfl_sync(0xffffffffu, mine.cu, i);
       w.base = max(0, len - n);
       w.tok_end = w.cu + n;
       w.klo = io.window ? clampi(static_cast<int64_t>(w.base) - io.window + 1, 0, len) : 0;
       w.khi = len;
-      if (!items(w, at, w.cu, tiles, kt0, kt1)) return false;
-      at += set_cost(P, kind, tiles, kt1 - kt0);
+      if (!items(w, at, w.cu, n, kt0, kt1)) return false;
+      at += set_cost(P, kind, n, kt1 - kt0);
     }
   }
   return true;
@@ -539,7 +575,7 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   bool ready = after == nullptr;
   // First slot of box number 32 g + lane of a piece; -1: no row sees its keys.
   // A page outside the pool: behind the end, where the copy fills in zeros.
-  auto fetch = [&](const Piece& w, int g) -> int {
+  auto fetch = [&](const volatile Piece& w, int g) -> int {
     const int box = 32 * g + lane, key = w.kt_a * kTileKeys + box * P.box;
     if (box >= (w.kt_b - w.kt_a) * boxes || key >= w.khi || key + P.box <= w.klo) return -1;
     const int page = key >> P.page_shift;
@@ -554,10 +590,13 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
       R.fifo[k] = w;
       mbar_arrive(&R.fifo_full[k]);
     }
+    __syncwarp();
     ++n_out;
     return true;
   };
-  auto load_piece = [&](const Piece& w, int pages) -> bool {
+  // (a piece is read in the fifo's place, which nobody but this warp reuses:
+  // registers are short here)
+  auto load_piece = [&](const volatile Piece& w, int pages) -> bool {
     // the buffers belong to the other kind of work until its MMAs are done
     if (!ready && !wait_warp(c, after, 0)) return false;
     ready = true;
@@ -590,10 +629,11 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     for (int t = 0; t < q_tiles; ++t) {
       if (n_loaded > 0 && !wait_warp(c, &R.q_empty[t], (n_loaded - 1) & 1)) return false;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&R.q_full[t], kHalves * P.group * P.tile_tok * 128);
+        const int toks = kind == kPair ? P.tile_tok : P.half_tok;
+        mbar_arrive_expect_tx(&R.q_full[t], kHalves * P.group * toks * 128);
         for (int f = 0; f < kHalves; ++f)
-          tma_load_3d(S.q[slot + t] + f * 128 * 128, tm_q, &R.q_full[t], f * 64, w.h * P.group,
-                      w.tok0 + t * P.tile_tok);
+          tma_load_3d(V.q + t * TileSmem<D>::kTile + f * (kind == kPair ? 128 : 64) * 128, tm_q,
+                      &R.q_full[t], f * 64, w.h * P.group, w.tok0 + t * w.split);
       }
       __syncwarp();
     }
@@ -606,25 +646,21 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   };
   // the next piece's pages are read before the piece at hand is loaded: each
   // read is a round trip to L2 or HBM
-  Piece held;
   int held_pages = -1;
-  bool have = false;
   const int line = kind == kPair ? 0 : 1 + slot;
   const int64_t begin = (kind == kPair ? static_cast<int64_t>(blockIdx.x) : 2ll * blockIdx.x + slot) * S.plan.share[kind];
   bool ok = walk(P, S.plan, kind, begin, S.first[line], S.first_at[line], [&](const Piece& w) -> bool {
     if (!push(w)) return false;
     const int pages = fetch(w, 0);
-    if (have && !load_piece(held, held_pages)) return false;
-    held = w;
+    if (n_out > 1 && !load_piece(R.fifo[(n_out - 2) % kFifo], held_pages)) return false;
     held_pages = pages;
-    have = true;
     return true;
   });
   if (ok) {
     Piece none;
     std::memset(&none, 0, sizeof(none));
     none.own = -1;
-    ok = push(none) && (!have || load_piece(held, held_pages));
+    ok = push(none) && (n_out < 2 || load_piece(R.fifo[(n_out - 2) % kFifo], held_pages));
   }
   if (ok) return true;
   // give up: no copy may land after the CTA has left
@@ -649,7 +685,8 @@ MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParit
   const int slot = V.slot;
   const uint32_t ts = S.tmem + slot * 128, to = S.tmem + 256 + slot * 128;
   Ring& R = *V.ring;
-  const uint64_t qd = sdesc_kmajor_sw128(smem_u32(S.q[slot]));
+  const uint64_t qd = sdesc_kmajor_sw128(smem_u32(V.q));
+  const uint32_t q_half = (V.kind == kPair ? 128 : 64) * 128 >> 4;  // to a row's second 64 values
   const uint32_t kv = smem_u32(V.kv);
   Place at;  // of the next K tile
   int piece = 0;
@@ -664,19 +701,19 @@ MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParit
     if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint64_t off = ((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4;
-        mma_bf16(ts, qd + off, kd + off, kIdS, k);
+        mma_bf16(ts, qd + (k >> 2) * q_half + (k & 3) * 2, kd + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2,
+                 kIdS, k);
       }
       mma_commit(&S.s_full[slot]);
       mma_commit(&R.empty[p.st]);
     }
     __syncwarp();
   };
-  auto pv = [&](Place v, int k0, int k1, bool first) {
+  auto pv = [&](Place v, bool first) {
     const uint64_t vd = sdesc_mnmajor_sw128(kv + v.st * (128 * D * 2), 128 * 128);
     if (elect_one()) {
 #pragma unroll
-      for (int k = k0; k < k1; ++k)
+      for (int k = 0; k < kTileKeys / 16; ++k)
         mma_ts(to, ts + 8 * k, vd + k * (16 * 128 >> 4), kIdO, !(first && k == 0));
     }
     __syncwarp();
@@ -697,18 +734,9 @@ MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParit
       const bool more = j + 1 < n;
       if (!wait_stage(sv) || (more && !wait_stage(sk))) return false;
       // P V, then the next scores right behind, which take P's place
-      if (kSplitP) {
-        if (!wait_warp(c, &S.p_half[slot], par.p)) return false;
-        tc_fence_after();
-        pv(sv, 0, kTileKeys / 32, j == 0);
-        if (!wait_warp(c, &S.p_full[slot], par.p)) return false;
-        tc_fence_after();
-        pv(sv, kTileKeys / 32, kTileKeys / 16, false);
-      } else {
-        if (!wait_warp(c, &S.p_full[slot], par.p)) return false;
-        tc_fence_after();
-        pv(sv, 0, kTileKeys / 16, j == 0);
-      }
+      if (!wait_warp(c, &S.p_full[slot], par.p)) return false;
+      tc_fence_after();
+      pv(sv, j == 0);
       par.p ^= 1;
       if (more) {
         qk(sk);
@@ -748,8 +776,8 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     const int n = w.kt_b - w.kt_a;
     // this thread's row: its token, and the keys [klo, khi) it sees; of a token
     // tree, the bits of `tree` instead from key `tree_at` on
-    const int tok = w.tok0 + (kind == kPair ? slot * P.tile_tok : 0) + tok_in_tile;
-    const bool valid = tok_in_tile < P.tile_tok && tok < w.tok_end;
+    const int tok = w.tok0 + (kind == kPair ? slot * w.split : 0) + tok_in_tile;
+    const bool valid = tok_in_tile < (kind == kPair ? (slot ? P.tile_tok : w.split) : P.half_tok) && tok < w.tok_end;
     int klo = w.klo, khi = w.khi, tree_at = INT_MAX;
     uint64_t tree = 0;
     if (valid) {
@@ -781,6 +809,19 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
       const int k0 = (w.kt_a + j) * kTileKeys;
+      if (k0 < w.klo || k0 + kTileKeys > w.khi) {
+        // keys that no row sees may hold anything: their V rows become zeros, so
+        // that a weight of zero leaves no NaN behind
+        const Place sv = at.next(W.stages);
+        if (!wait_warp(c, &R.full[sv.st], sv.round)) return false;
+        if (k0 + row < w.klo || k0 + row >= w.khi) {
+          uint8_t* v = W.kv + sv.st * (128 * D * 2) + row * 128;
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x)
+            reinterpret_cast<uint4*>(v + (x >> 3) * 128 * 128)[x & 7] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
       if (!wait_warp(c, &S.s_full[slot], par.s)) return false;
       par.s ^= 1;
       tc_fence_after();
@@ -835,46 +876,31 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
           }
         }
       }
-      if (k0 < w.klo || k0 + kTileKeys > w.khi) {
-        // keys that no row sees may hold anything: their V rows become zeros, so
-        // that a weight of zero leaves no NaN behind
-        const Place sv = at.next(W.stages);
-        if (!wait_warp(c, &R.full[sv.st], sv.round)) return false;
-        if (k0 + row < w.klo || k0 + row >= w.khi) {
-          uint8_t* v = W.kv + sv.st * (128 * D * 2) + row * 128;
+      // P = 2^(S - m)
+      if (warp_valid) {
+        const float ms = m == -INFINITY ? 0.f : m;
+        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-          for (int x = 0; x < D / 8; ++x)
-            reinterpret_cast<uint4*>(v + (x >> 3) * 128 * 128)[x & 7] = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-      }
-      // P = 2^(S - m), 64 keys at a time
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (warp_valid) {
-          const float ms = m == -INFINITY ? 0.f : m;
+        for (int q = 0; q < 2; ++q) {
           uint32_t p[kTileKeys / 4];
-          float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
           for (int x = 0; x < kTileKeys / 2; x += 2) {
-            float2 y = fma2(make_float2(s[64 * half + x], s[64 * half + x + 1]),
-                            make_float2(sl2, sl2), make_float2(-ms, -ms));
+            float2 y = fma2(make_float2(s[64 * q + x], s[64 * q + x + 1]), make_float2(sl2, sl2),
+                            make_float2(-ms, -ms));
             y.x = exp2_approx(y.x);
             y.y = exp2_approx(y.y);
             sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], y);
             p[x >> 1] = Types<T>::pack(y.x, y.y);
           }
-          const float2 both = add2(sum[0], sum[1]);
-          l += both.x + both.y;
-          tmem_st32(ts + 32 * half, p);
+          tmem_st32(ts + 32 * q, p);
         }
-        if (half || kSplitP) {
-          if (warp_valid) tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(half ? &S.p_full[slot] : &S.p_half[slot]);
-        }
+        const float2 all = add2(sum[0], sum[1]);
+        l += all.x + all.y;
+        tmem_st_wait();
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_full[slot]);
       at = at.next(W.stages).next(W.stages);
     }
 
@@ -882,10 +908,11 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     if (!wait_warp(c, &S.o_done[slot], par.o)) return false;
     par.o ^= 1;
     tc_fence_after();
+    const int32_t carry = ((kind * P.ctas + blockIdx.x) * 2 + slot) * 128 + row;
     const int64_t to_row = w.first ? (w.own ? P.ws.own : P.ws.pre) +
-                                     static_cast<int64_t>(tok) * io.n_q_heads + w.h * G + g
-                               : P.ws.carry + ((static_cast<int64_t>(kind) * P.ctas + blockIdx.x) * 2 + slot) * 128 + row;
-    if (valid) P.ws.ml[to_row] = make_float2(m, l);
+                                         static_cast<int64_t>(tok) * io.n_q_heads + w.h * G + g
+                                   : P.ws.carry + carry;
+    if (valid) P.ws.part[to_row] = Partial{m, l, 2 * w.more + kind, carry};
     if (warp_valid) {
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
@@ -904,52 +931,53 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   }
 }
 
-MK_DEV void init_ring(Ring& R, int slots) {
-  for (int i = 0; i < kMaxStages; ++i) {
-    mbar_init(&R.full[i], 1);
-    mbar_init(&R.empty[i], slots);
-  }
-  for (int i = 0; i < 2; ++i) {
-    mbar_init(&R.q_full[i], 1);
-    mbar_init(&R.q_empty[i], 1);
-  }
-  for (int i = 0; i < kFifo; ++i) {
-    mbar_init(&R.fifo_full[i], 1);
-    mbar_init(&R.fifo_empty[i], 5 * slots);
-  }
-}
-
 // Warps 0-3 and 4-7: softmax of slot 0 and 1.  Warps 8 and 9: producers (8 for
 // pairs and slot 0's solos, 9 for slot 1's solos).  Warps 10 and 11: MMA issuers.
 template <class T, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
     k_attn_tiles(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap tm_q,
-                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+                 const __grid_constant__ CUtensorMap tm_q64, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v) {
   extern __shared__ uint8_t smem_raw[];
   TileSmem<D>& S = *reinterpret_cast<TileSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                    ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) init_ring(S.ring[i], i == 0 ? 2 : 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_half[i], 4);
-      mbar_init(&S.p_full[i], 4);
-      mbar_init(&S.o_done[i], 1);
-      mbar_init(&S.drained[i], 1);
+  if (warp == 11) {
+    // one barrier per lane and turn
+    for (int i = lane_id(); i < 3 * kMaxStages; i += 32) {
+      mbar_init(&S.ring[i / kMaxStages].full[i % kMaxStages], 1);
+      mbar_init(&S.ring[i / kMaxStages].empty[i % kMaxStages], i < kMaxStages ? 2 : 1);
     }
-    mbar_init(&S.turn, 2);
-    S.abort = 0;
+    for (int i = lane_id(); i < 3 * kFifo; i += 32) {
+      mbar_init(&S.ring[i / kFifo].fifo_full[i % kFifo], 1);
+      mbar_init(&S.ring[i / kFifo].fifo_empty[i % kFifo], i < kFifo ? 10 : 5);
+    }
+    if (lane_id() < 6) {
+      mbar_init(&S.ring[lane_id() >> 1].q_full[lane_id() & 1], 1);
+      mbar_init(&S.ring[lane_id() >> 1].q_empty[lane_id() & 1], 1);
+    }
+    if (lane_id() < 2) {
+      mbar_init(&S.s_full[lane_id()], 1);
+      mbar_init(&S.p_full[lane_id()], 4);
+      mbar_init(&S.o_done[lane_id()], 1);
+      mbar_init(&S.drained[lane_id()], 1);
+    }
+    if (lane_id() == 0) {
+      mbar_init(&S.turn, 2);
+      S.abort = 0;
+    }
     fence_mbar_init();
-    prefetch_tensormap(&tm_q);
-    prefetch_tensormap(&tm_k);
-    prefetch_tensormap(&tm_v);
   }
   if (warp == 10) {
     tmem_alloc(&S.tmem, 512);
     tmem_relinquish();
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *P.ws.status = 0;
+  if (warp == 9 && lane_id() == 0) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_q64);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
   lay_out_work<D>(P, S);
   tc_fence_before();
   __syncthreads();
@@ -977,8 +1005,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
       for (int turn = 0; ok && turn < 2; ++turn)
         if ((first_kind ^ turn) == kSolo || slot == 0)
-          ok = produce<D>(P, S, c, View<D>(S, first_kind ^ turn, slot), &tm_q, &tm_k, &tm_v,
-                          turn ? &S.turn : nullptr);
+          ok = produce<D>(P, S, c, View<D>(S, first_kind ^ turn, slot), (first_kind ^ turn) == kSolo ? &tm_q64 : &tm_q,
+                          &tm_k, &tm_v, turn ? &S.turn : nullptr);
     } else {
       SlotParity par;
 #pragma unroll 1
@@ -1009,79 +1037,87 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // ------------------------------------------------------------------ merge
 
-// The stretches of one item that hold a row: its first one, by row, and those
-// of the owners (CTAs or slots) behind it on the line.
-struct Held {
-  int64_t first, carry, step;
-  int count;
-  MK_DEV int64_t at(int e) const { return e == 0 ? first : carry + e * step; }
+// V values of one row's O per lane.
+template <int V>
+struct Vals {
+  float v[V];
 };
-MK_DEV Held held(const AttnParams& P, const Plan& plan, int tile, int tiles, int kt, int h,
-                 int64_t pairs_at, int64_t solos_at, int64_t first, int row) {
-  const int kind = tile == tiles - 1 && (tiles & 1) ? kSolo : kPair;
-  const int64_t s = (kind == kPair ? pairs_at : solos_at) +
-                    (kind == kSolo ? h : (tile >> 1) * P.io.n_kv_heads + h) * item_cost(kind, kt) +
-                    item_over(kind);
-  const int64_t o0 = s / plan.share[kind];
-  const int64_t o1 = (s + static_cast<int64_t>(kt - 1) * kTileCost) / plan.share[kind];
-  Held x;
-  x.count = kt > 0 ? static_cast<int>(o1 - o0) + 1 : 0;
-  x.first = first;
-  x.step = kind == kPair ? 256 : 128;
-  x.carry = P.ws.carry + kind * P.ctas * 256ll + o0 * x.step + (kind == kPair ? (tile & 1) * 128 : 0) + row;
+template <int V>
+MK_DEV Vals<V> load_vals(const float* p) {
+  Vals<V> x;
+  if (V == 4) {
+    const float4 y = *reinterpret_cast<const float4*>(p);
+    x.v[0] = y.x, x.v[1] = y.y, x.v[V - 2] = y.z, x.v[V - 1] = y.w;
+  } else {
+    const float2 y = *reinterpret_cast<const float2*>(p);
+    x.v[0] = y.x, x.v[1] = y.y;
+  }
   return x;
 }
 
+// One warp per row and q head.  What does not depend on the tiles (the row's
+// request) comes before the wait for them; behind it the first stretches'
+// results of the prefix and of the request's own keys, by row, and then those
+// of the stretches that carried on.
 template <class T, int D>
 __global__ void __launch_bounds__(256) k_attn_merge(const __grid_constant__ AttnParams P) {
   const mk_prefix_attn_io& io = P.io;
   constexpr int V = D / 32;
-  pdl_wait();
-  const Plan plan = *P.ws.plan;
-  const int lane = lane_id(), Hq = io.n_q_heads, G = P.group;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t tok64 = item / Hq;
-  if (tok64 >= plan.n_used) return;
-  const int tok = static_cast<int>(tok64), hq = static_cast<int>(item - tok64 * Hq);
-  const int h = hq / G, g = hq - h * G;
-  // its request
-  int lo = 0, hi = io.n_requests;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (io.cu_rows[mid] <= tok) lo = mid; else hi = mid;
-  }
-  const Req r = read_req(P, lo);
-  const int tt = P.tile_tok;
-  Held x[2];
-  {
-    const int tile = tok / tt;
-    x[0] = held(P, plan, tile, plan.tiles, plan.kt1 - plan.kt0, h, 0, 0, P.ws.pre + item,
-                (tok - tile * tt) * G + g);
-  }
-  {
-    const int i = tok - r.cu, tile = i / tt;
-    x[1].count = 0;
-    if (i >= 0 && i < r.n) x[1] = held(P, plan, tile, ceil_div(r.n, tt), r.kt1 - r.kt0, h, P.ws.cost[lo],
-                P.ws.cost[io.n_requests + lo], P.ws.own + item, (i - tile * tt) * G + g);
-  }
-  const int n0 = x[0].count, n = n0 + x[1].count;
-  float M = -INFINITY, L = 0.f, acc[V] = {};
-  for (int a = 0; a < n; a += 32) {
-    const int e = a + lane;
-    int64_t at = 0;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (e < n) {
-      at = e < n0 ? x[0].at(e) : x[1].at(e - n0);
-      ml = P.ws.ml[at];
+  const int lane = lane_id(), Hq = io.n_q_heads;
+  const uint32_t item = blockIdx.x * 8u + (threadIdx.x >> 5);
+  const int tok = static_cast<int>(item / static_cast<uint32_t>(Hq));
+  const bool in = tok < clampi(io.cu_rows[io.n_requests], 0, io.n_rows);
+  bool own = false;
+  if (in) {
+    int lo = 0, hi = io.n_requests;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (io.cu_rows[mid] <= tok) lo = mid; else hi = mid;
     }
-    float top = ml.x;
+    const Req r = read_req(P, lo);
+    own = r.kt1 > r.kt0;
+  }
+  pdl_wait();
+  if (!in) return;
+  const Partial* part = P.ws.part;
+  Partial first[2];
+  Vals<V> x[2];
+  const bool pre = P.ws.status[1] != 0;
+  first[0] = part[P.ws.pre + item];
+  first[1] = part[P.ws.own + item];
+  x[0] = load_vals<V>(P.ws.o + (P.ws.pre + item) * D + lane * V);
+  x[1] = load_vals<V>(P.ws.o + (P.ws.own + item) * D + lane * V);
+  if (!pre) first[0] = Partial{-INFINITY, 0.f, 0, 0};
+  if (!own) first[1] = Partial{-INFINITY, 0.f, 0, 0};
+  float M = fmaxf(first[0].m, first[1].m), L = 0.f, acc[V] = {};
+  if (M != -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float w = first[i].m == -INFINITY ? 0.f : exp2f(first[i].m - M);
+      if (w != 0.f) {  // (what was not written may hold anything)
+        L += w * first[i].l;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += w * x[i].v[v];
+      }
+    }
+  }
+  const int most = 2 * P.ctas;  // (a wrong cu_rows must not lead out of the workspace)
+  const int n0 = clampi(first[0].more >> 1, 0, most), n = n0 + clampi(first[1].more >> 1, 0, most);
+  for (int a = 0; a < n; a += 32) {
+    const int e = a + lane, k0 = e < n0 ? e : e - n0;
+    const int kind = (e < n0 ? first[0].more : first[1].more) & 1;
+    const int64_t c = (e < n0 ? first[0].carry : first[1].carry) + static_cast<int64_t>(k0 + 1) * (kind == kPair ? 256 : 128);
+    const bool ok = e < n && c >= 0 && c < 512ll * P.ctas;
+    const int64_t at = P.ws.carry + (ok ? c : 0);
+    Partial mine{-INFINITY, 0.f, 0, 0};
+    if (ok) mine = part[at];
+    float top = mine.m;
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = fmaxf(top, M);
     if (top == -INFINITY) continue;
-    const float old = exp2f(M - top);
-    float wgt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-    float sum = wgt * ml.y;
+    const float old = exp2f(M - top), w = mine.m == -INFINITY ? 0.f : exp2f(mine.m - top);
+    float sum = w * mine.l;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     L = L * old + sum;
@@ -1089,25 +1125,28 @@ __global__ void __launch_bounds__(256) k_attn_merge(const __grid_constant__ Attn
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= old;
     const int cnt = min(32, n - a);
-#pragma unroll 4
-    for (int k = 0; k < cnt; ++k) {
-      const float f = __shfl_sync(0xffffffffu, wgt, k);
-      const int64_t p = __shfl_sync(0xffffffffu, at, k);
-      if (f == 0.f) continue;
-      const float* src = P.ws.o + p * D + lane * V;
-      if (V == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(src);
-        acc[0] += f * y.x, acc[1] += f * y.y, acc[V - 2] += f * y.z, acc[V - 1] += f * y.w;
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(src);
-        acc[0] += f * y.x, acc[1] += f * y.y;
+    for (int k = 0; k < cnt; k += 4) {  // four rows on their way at once
+      Vals<V> y[4];
+      float f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        f[u] = __shfl_sync(0xffffffffu, w, (k + u) & 31);
+        const int64_t p = __shfl_sync(0xffffffffu, at, (k + u) & 31);
+        if (k + u >= cnt) f[u] = 0.f;
+        y[u] = load_vals<V>(P.ws.o + p * D + lane * V);
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (f[u] != 0.f)
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] += f[u] * y[u].v[v];
     }
   }
   const float inv = L != 0.f ? 1.f / L : 0.f;  // no key, or NaN as it comes
   uint32_t out[V / 2];
 #pragma unroll
   for (int v = 0; v < V; v += 2) out[v >> 1] = Types<T>::pack(acc[v] * inv, acc[v + 1] * inv);
+  const int hq = static_cast<int>(item) - tok * Hq;
   T* dst = static_cast<T*>(io.out) + tok * io.out_stride + hq * D + lane * V;
   if (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[V / 2 - 1]);
   else *reinterpret_cast<uint32_t*>(dst) = out[0];
@@ -1140,12 +1179,9 @@ int64_t lay_out(const mk_prefix_attn_io* io, int ctas, uint8_t* base, Space* s) 
   const int64_t rows = s->carry + 2 * ctas * 256ll;
   int64_t at = 0;
   s->status = reinterpret_cast<uint32_t*>(base);
-  s->plan = reinterpret_cast<Plan*>(base + 64);
   at = 256;
-  s->cost = reinterpret_cast<int64_t*>(base + at);
-  at = align256(at + io->n_requests * 16ll);
-  s->ml = reinterpret_cast<float2*>(base + at);
-  at = align256(at + rows * 8);
+  s->part = reinterpret_cast<Partial*>(base + at);
+  at = align256(at + rows * static_cast<int64_t>(sizeof(Partial)));
   s->o = reinterpret_cast<float*>(base + at);
   return align256(at + rows * io->head_dim * 4);
 }
@@ -1169,11 +1205,11 @@ mk_status encode_tmap_3d(CUtensorMap* map, int dtype, const void* base, uint64_t
 }
 
 template <class T, int D>
-mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorMap& k,
-                      const CUtensorMap& v, cudaStream_t s) {
+mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorMap& q64,
+                      const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
   constexpr int smem = sizeof(TileSmem<D>) + 1024;
   MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_tiles<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  k_attn_tiles<T, D><<<A.ctas, kTileThreads, smem, s>>>(A, q, k, v);
+  k_attn_tiles<T, D><<<A.ctas, kTileThreads, smem, s>>>(A, q, q64, k, v);
   MK_CUDA_TRY(cudaGetLastError());
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(A.io.n_rows) * A.io.n_q_heads + 7) / 8));
@@ -1245,11 +1281,14 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   A.scale_log2 = scale * 1.4426950408889634f;
   A.group = io->n_q_heads / io->n_kv_heads;
   A.tile_tok = 128 / A.group;
+  A.half_tok = 64 / A.group;
   A.box = static_cast<int>(std::min<int64_t>(P, kTileKeys));
   A.page_shift = __builtin_ctz(static_cast<uint32_t>(P));
   const uint64_t d = io->head_dim, Hq = io->n_q_heads, Hk = io->n_kv_heads;
-  CUtensorMap q, k, v;
+  CUtensorMap q, q64, k, v;
   st = encode_tmap_3d(&q, io->dtype, io->q, d, Hq, io->n_rows, d * 2, io->q_stride * 2, A.group, A.tile_tok);
+  if (st != MK_OK) return st;
+  st = encode_tmap_3d(&q64, io->dtype, io->q, d, Hq, io->n_rows, d * 2, io->q_stride * 2, A.group, A.half_tok);
   if (st != MK_OK) return st;
   // a pool without pages is never read
   const uint64_t slots = std::max<int64_t>(1, io->n_pages * P);
@@ -1261,10 +1300,10 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   if (st != MK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (io->dtype == MK_BF16)
-    return io->head_dim == 128 ? launch_attn<__nv_bfloat16, 128>(A, q, k, v, s)
-                               : launch_attn<__nv_bfloat16, 64>(A, q, k, v, s);
-  return io->head_dim == 128 ? launch_attn<__half, 128>(A, q, k, v, s)
-                             : launch_attn<__half, 64>(A, q, k, v, s);
+    return io->head_dim == 128 ? launch_attn<__nv_bfloat16, 128>(A, q, q64, k, v, s)
+                               : launch_attn<__nv_bfloat16, 64>(A, q, q64, k, v, s);
+  return io->head_dim == 128 ? launch_attn<__half, 128>(A, q, q64, k, v, s)
+                             : launch_attn<__half, 64>(A, q, q64, k, v, s);
 }
 
 mk_status mk_prefix_attn_status(const void* workspace) {
