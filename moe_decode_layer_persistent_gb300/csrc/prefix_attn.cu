@@ -10,17 +10,18 @@
 // Each stretch of key tiles leaves (O, m, l); the second kernel joins a row's
 // stretches: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
 //
-// Work comes in two kinds, each laid out on a line of its own, which every CTA
-// works out from the lengths (only the GPU knows them):
-//   pairs  two row tiles on the same key tiles: bound by the tensor cores.  The
-//          CTAs (one per SM) get an equal stretch of the line each, and a CTA's
-//          two slots take a row tile each;
+// Work comes in two kinds:
+//   pairs  two row tiles on the same key tiles: bound by the tensor cores; a
+//          CTA's two slots take a row tile each;
 //   solos  one tile of up to 64 rows (what is left of a row set behind its
-//          pairs, most requests' own rows): bound by the K and V bytes.  The
-//          slots of all CTAs get an equal stretch each.
-// A stretch may begin and end anywhere, whatever heads, requests and keys it
-// crosses.  CTAs with an even number start with their pairs, the others with
-// their solos, so that the tensor cores and HBM are both busy all the time.
+//          pairs, most requests' own rows): bound by the K and V bytes; each slot
+//          takes one.
+// All pairs lie on one line and all solos on another, measured in time; every CTA
+// works them out from the lengths (only the GPU knows them).  With A and B their
+// lengths, each of the C CTAs (one per SM) gets the time T = (A + B / 2) / C: the
+// first A / T of them take the pairs, the others' slots the solos, whatever
+// heads, requests and keys a stretch crosses.  So the tensor cores and HBM are
+// both busy from beginning to end.
 // Two launches, the second one chained with programmatic dependent launch:
 // k_attn_tiles does all that, k_attn_merge joins the partial results of each
 // row.
@@ -39,11 +40,12 @@ namespace mk {
 namespace {
 
 constexpr int kPair = 0, kSolo = 1;  // the two kinds of work
-// Cost of a key tile, and what an item (a row set's tile or pair of tiles and
-// a KV head) costs on top of its key tiles: filling the pipeline and writing
-// the result.
-constexpr int kTileCost = 2;
-MK_DEV constexpr int item_over(int kind) { return kind == kPair ? 6 : 3; }
+// Time of a key tile, and what an item (a row set's tile or pair of tiles and a
+// KV head) takes on top of its key tiles: filling the pipeline and writing the
+// result.  In units of about 0.2 us.
+constexpr int kMaxTileCost = 10;
+MK_DEV constexpr int tile_cost(int kind) { return kind == kPair ? 8 : 10; }
+MK_DEV constexpr int item_over(int kind) { return kind == kPair ? 24 : 12; }
 
 constexpr int kTileKeys = 128;
 constexpr int kFifo = 4;            // pieces handed out ahead
@@ -53,11 +55,31 @@ constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
 
 // How the lines are laid out (every CTA of k_attn_tiles works it out for itself).
 struct Plan {
-  int64_t total[2], share[2];  // cost of everything, of one CTA (pairs) or slot (solos)
-  int64_t prefix_cost[2];      // the prefix items come first
-  int32_t n_used;              // rows in use
-  int32_t kt0, kt1;            // key tiles of the prefix that some row sees
-  int32_t lo;                  // first prefix key that some row sees
+  int64_t total[2];        // of each line
+  int64_t share;           // T
+  int64_t prefix_cost[2];  // the prefix items come first
+  int32_t n_used;          // rows in use
+  int32_t kt0, kt1;        // key tiles of the prefix that some row sees
+  int32_t lo;              // first prefix key that some row sees
+  // The solos start in CTA solo_cta, whose slots have solo_len of them each; of
+  // the CTAs behind it each slot has `share`.
+  int32_t solo_cta;
+  int64_t solo_len;
+  MK_DEV int64_t begin(int kind, int slot) const {
+    const int c = static_cast<int>(blockIdx.x);
+    if (kind == kPair) return c * share;
+    if (c <= solo_cta) return c < solo_cta ? total[kSolo] : slot * solo_len;
+    return 2 * solo_len + (2ll * (c - solo_cta - 1) + slot) * share;
+  }
+  MK_DEV int64_t length(int kind) const {
+    return kind == kSolo && static_cast<int>(blockIdx.x) == solo_cta ? solo_len : share;
+  }
+  // The owner (CTA of pairs, slot of solos) of a place on a line, counted from
+  // the line's first.
+  MK_DEV int owner(int kind, int64_t at) const {
+    if (kind == kPair) return static_cast<int>(at / share);
+    return at < 2 * solo_len ? at >= solo_len : 2 + static_cast<int>((at - 2 * solo_len) / share);
+  }
 };
 
 // One row's result of one stretch of key tiles; its O is beside it.
@@ -124,7 +146,9 @@ MK_DEV int items_of(const AttnParams& P, int kind, int n) {
   const int full = n / (2 * P.tile_tok), left = n - full * 2 * P.tile_tok;
   return kind == kPair ? full + (left > P.half_tok) : left > 0 && left <= P.half_tok;
 }
-MK_DEV int64_t item_cost(int kind, int kt) { return item_over(kind) + static_cast<int64_t>(kt) * kTileCost; }
+MK_DEV int64_t item_cost(int kind, int kt) {
+  return item_over(kind) + static_cast<int64_t>(kt) * tile_cost(kind);
+}
 // Cost of all of a row set's items against kt key tiles.
 MK_DEV int64_t set_cost(const AttnParams& P, int kind, int n, int kt) {
   return kt > 0 ? items_of(P, kind, n) * item_cost(kind, kt) * P.io.n_kv_heads : 0;
@@ -205,7 +229,6 @@ struct View {
   uint8_t* kv;       // its part of the buffers
   uint8_t* q;        // the slot's row tile
   int kind, slot, stages;
-  int q_bar;         // the slot's row tile among the ring's
   MK_DEV View(TileSmem<D>& S, int kind_, int slot_) : kind(kind_), slot(slot_) {
     const bool pair = kind == kPair;
     ring = &S.ring[pair ? 0 : 1 + slot];
@@ -214,7 +237,6 @@ struct View {
     uint8_t* part = S.arena + slot * (kTile / 2 + TileSmem<D>::kSoloStages * kTile);  // of a solo's slot
     kv = pair ? S.arena + 2 * kTile : part + kTile / 2;
     q = pair ? S.arena + slot * kTile : part;
-    q_bar = pair ? slot : 0;
   }
 };
 
@@ -353,73 +375,45 @@ MK_DEV void st_global_8(float* p, const float* v) {
 // The lowest n bits, n clamped to 0 .. 32.
 MK_DEV uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
-// ---- the lines of work, worked out by the whole CTA
-// kReqs consecutive requests per thread and turn: one turn up to 1,536 requests.
-constexpr int kReqs = 4;
-
+// ---- the lines of work, worked out by the whole CTA: each thread takes
+// consecutive requests (one, up to 384 of them)
 template <int D>
 MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   const mk_prefix_attn_io& io = P.io;
   const int B = io.n_requests, lane = lane_id(), warp = threadIdx.x >> 5;
-  constexpr int kTurn = kTileThreads * kReqs;
-  int64_t cost[2][kReqs], mine[2], all[2] = {0, 0};
-  int low = INT_MAX;
-  auto read_costs = [&](int turn) {
-    const int b0 = turn * kTurn + threadIdx.x * kReqs;
-    int32_t cu[kReqs + 1], len[kReqs];
-#pragma unroll
-    for (int i = 0; i <= kReqs; ++i) cu[i] = b0 + i <= B ? io.cu_rows[b0 + i] : 0;
-#pragma unroll
-    for (int i = 0; i < kReqs; ++i) len[i] = b0 + i < B ? io.lens[b0 + i] : 0;
-    mine[0] = mine[1] = 0;
-#pragma unroll
-    for (int i = 0; i < kReqs; ++i) {
-      cost[0][i] = cost[1][i] = 0;
-      if (b0 + i < B) {
-        const Req r = make_req(P, cu[i], cu[i + 1], len[i]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) cost[k][i] = set_cost(P, k, r.n, r.kt1 - r.kt0);
-        if (r.n) low = min(low, r.base);
-      }
-      mine[0] += cost[0][i];
-      mine[1] += cost[1][i];
-    }
-  };
-  const int turns = ceil_div(B, kTurn);
+  const int each = ceil_div(B, kTileThreads), b0 = threadIdx.x * each, b1 = min(B, b0 + each);
   const int n_used = clampi(io.cu_rows[B], 0, io.n_rows);
-  for (int t = 0; t < turns; ++t) {
-    read_costs(t);
-    all[0] += mine[0];
-    all[1] += mine[1];
+  int64_t mine[2] = {0, 0};
+  int low = INT_MAX;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const Req r = read_req(P, b);
+    for (int k = 0; k < 2; ++k) mine[k] += set_cost(P, k, r.n, r.kt1 - r.kt0);
+    if (r.n) low = min(low, r.base);
   }
-  // the sums of all costs, and the lowest position of any row, which decides
-  // where the prefix starts to be seen; in the same turn the running sums over
-  // the warp
-  int64_t v[2] = {all[0], all[1]};
+  int64_t v[2] = {mine[0], mine[1]};
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int k = 0; k < 2; ++k) {
       const int64_t u = __shfl_up_sync(0xffffffffu, v[k], o);
       if (lane >= o) v[k] += u;
     }
-    if (lane == 31) S.sum[k][warp] = v[k];
-  }
+  if (lane == 31) S.sum[0][warp] = v[0], S.sum[1][warp] = v[1];
   low = __reduce_min_sync(0xffffffffu, low);
   if (lane == 0) S.low[warp] = low;
   __syncthreads();
-  int64_t before[2] = {0, 0};
-  all[0] = all[1] = 0;
-#pragma unroll
+  Plan p;
+  p.total[0] = p.total[1] = 0;
+#pragma unroll 1
   for (int w = 0; w < kTileThreads / 32; ++w) {
-#pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (w < warp) before[k] += S.sum[k][w];
-      all[k] += S.sum[k][w];
+      if (w < warp) v[k] += S.sum[k][w];
+      p.total[k] += S.sum[k][w];
     }
     low = min(low, S.low[w]);
   }
-  Plan p;
+  // the lowest position of any row decides where the prefix starts to be seen
   const int64_t lo64 =
       io.window && low != INT_MAX ? static_cast<int64_t>(io.prefix_len) + low - io.window + 1 : 0;
   p.n_used = n_used;
@@ -429,74 +423,53 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     p.prefix_cost[k] = set_cost(P, k, p.n_used, p.kt1 - p.kt0);
-    p.total[k] = p.prefix_cost[k] + all[k];
-    const int n = k == kPair ? P.ctas : 2 * P.ctas;
-    // at least one key tile each, so that every stretch inside an item has one
-    p.share[k] = max((p.total[k] + n - 1) / n, static_cast<int64_t>(kTileCost));
+    p.total[k] += p.prefix_cost[k];
   }
-  const int64_t begin[3] = {blockIdx.x * p.share[kPair], 2ll * blockIdx.x * p.share[kSolo],
-                            (2ll * blockIdx.x + 1) * p.share[kSolo]};
+  // At least one key tile each, so that every stretch inside an item has one: what
+  // is left of the last pairs' CTA is used only if it holds one (the sum has room
+  // for what then is not).
+  p.share = max((p.total[kPair] + (p.total[kSolo] + 1) / 2 + kMaxTileCost + P.ctas - 1) / P.ctas,
+                static_cast<int64_t>(kMaxTileCost));
+  p.solo_cta = static_cast<int>(p.total[kPair] / p.share);
+  p.solo_len = (p.solo_cta + 1) * p.share - p.total[kPair];
+  if (p.solo_len < kMaxTileCost) ++p.solo_cta, p.solo_len = p.share;
   if (threadIdx.x == 0) {
     S.plan = p;
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (begin[i] < p.prefix_cost[i > 0] || begin[i] >= p.total[i > 0])
-        S.first[i] = 0, S.first_at[i] = p.prefix_cost[i > 0];
     if (blockIdx.x == 0) {
       P.ws.status[0] = 0;
       P.ws.status[1] = p.kt1 > p.kt0;
     }
   }
   // the requests that this CTA's stretches start in
-  auto find = [&](int t, int64_t here0, int64_t here1) {
-    int64_t here[2] = {here0, here1};
 #pragma unroll
-    for (int i = 0; i < kReqs; ++i)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int j = k; j < (k == kPair ? 1 : 3); ++j)
-          if (begin[j] >= here[k] && begin[j] < here[k] + cost[k][i])
-            S.first[j] = t * kTurn + threadIdx.x * kReqs + i, S.first_at[j] = here[k];
-        here[k] += cost[k][i];
+  for (int j = 0; j < 3; ++j) {
+    const int k = j > 0;
+    const int64_t begin = p.begin(k, j - 1);
+    int64_t here = p.prefix_cost[k] + v[k] - mine[k];
+    if (threadIdx.x == 0 && begin < here) S.first[j] = 0, S.first_at[j] = here;
+    if (begin >= here && begin < here + mine[k]) {
+      int b = b0;
+#pragma unroll 1
+      for (; b < b1 - 1; ++b) {
+        const Req r = read_req(P, b);
+        const int64_t next = here + set_cost(P, k, r.n, r.kt1 - r.kt0);
+        if (begin < next) break;
+        here = next;
       }
-  };
-  if (turns == 1) {
-    find(0, p.prefix_cost[0] + before[0] + v[0] - mine[0], p.prefix_cost[1] + before[1] + v[1] - mine[1]);
-    return;
-  }
-  int64_t at[2] = {p.prefix_cost[0], p.prefix_cost[1]};
-  for (int t = 0; t < turns; ++t) {
-    read_costs(t);
-    v[0] = mine[0], v[1] = mine[1];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v[k], o);
-        if (lane >= o) v[k] += u;
-      }
-      if (lane == 31) S.sum[k][warp] = v[k];
+      S.first[j] = b;
+      S.first_at[j] = here;
     }
-    __syncthreads();
-    int64_t here[2] = {at[0] + v[0] - mine[0], at[1] + v[1] - mine[1]};
-    for (int w = 0; w < kTileThreads / 32; ++w)
-      for (int k = 0; k < 2; ++k) {
-        if (w < warp) here[k] += S.sum[k][w];
-        at[k] += S.sum[k][w];
-      }
-    find(t, here[0], here[1]);
   }
 }
 
 // ---- a stretch of a line, piece by piece: emit(Piece) for each
 template <class Emit>
-MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int64_t begin, int first,
+MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int slot, int first,
                  int64_t first_at, const Emit& emit) {
   const mk_prefix_attn_io& io = P.io;
-  const int Hk = io.n_kv_heads, lane = lane_id(), over = item_over(kind);
-  const int64_t end = min(plan.total[kind], begin + plan.share[kind]);
+  const int Hk = io.n_kv_heads, lane = lane_id(), step = tile_cost(kind);
+  const int64_t begin = plan.begin(kind, slot);
+  const int64_t end = min(plan.total[kind], begin + plan.length(kind));
   if (begin >= end) return true;
   // the items of a row set of n tokens (row tile by row tile, head by head) from
   // cost `at`
@@ -507,11 +480,11 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int64_t begin,
     const int64_t cost = item_cost(kind, kt);
     int i = begin > at ? static_cast<int>((begin - at) / cost) : 0;
     int p = i / Hk, h = i - p * Hk;
-    int64_t s = at + i * cost + over;  // of the item's first key tile
+    int64_t s = at + i * cost + item_over(kind);  // of the item's first key tile
     for (; i < count && s < end; ++i, s += cost) {
-      const int s0 = s >= begin ? 0 : (static_cast<int>(begin - s) + kTileCost - 1) / kTileCost;
-      const int64_t room = end - s + kTileCost - 1;
-      const int s1 = room >= static_cast<int64_t>(kt) * kTileCost ? kt : static_cast<int>(room) / kTileCost;
+      const int s0 = s >= begin ? 0 : (static_cast<int>(begin - s) + step - 1) / step;
+      const int64_t room = end - s + step - 1;
+      const int s1 = room >= static_cast<int64_t>(kt) * step ? kt : static_cast<int>(room) / step;
       if (s0 < s1) {
         w.h = h;
         // (behind its pairs the row set's solo)
@@ -520,8 +493,8 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int64_t begin,
         w.kt_a = kt0 + s0;
         w.kt_b = kt0 + s1;
         w.first = s0 == 0;
-        const int64_t last = s + static_cast<int64_t>(kt - 1) * kTileCost - begin;
-        w.more = last < plan.share[kind] ? 0 : static_cast<int>(last / plan.share[kind]);
+        const int64_t last = s + static_cast<int64_t>(kt - 1) * step;
+        w.more = last < end ? 0 : plan.owner(kind, last) - plan.owner(kind, s);
         if (!emit(w)) return false;
       }
       if (++h == Hk) h = 0, ++p;
@@ -540,13 +513,13 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int64_t begin,
   int64_t at = first_at;
   for (int b0 = first; at < end && b0 < io.n_requests; b0 += 32) {
     // 32 requests' lengths at a time
-    Req mine{0, 0, 0, 0, 0, 0};
-    if (b0 + lane < io.n_requests) mine = read_req(P, b0 + lane);
+    Req req{0, 0, 0, 0, 0, 0};
+    if (b0 + lane < io.n_requests) req = read_req(P, b0 + lane);
     for (int i = 0; at < end && i < 32 && b0 + i < io.n_requests; ++i) {
-      const int n = __shfl_sync(0xffffffffu, mine.n, i), len = __shfl_sync(0xffffffffu, mine.len, i);
-      const int kt0 = __shfl_sync(0xffffffffu, mine.kt0, i), kt1 = __shfl_sync(0xffffffffu, mine.kt1, i);
+      const int n = __shfl_sync(0xffffffffu, req.n, i), len = __shfl_sync(0xffffffffu, req.len, i);
+      const int kt0 = __shfl_sync(0xffffffffu, req.kt0, i), kt1 = __shfl_sync(0xffffffffu, req.kt1, i);
       w.b = b0 + i;
-      w.cu = __shfl_sync(0xffffffffu, mine.cu, i);
+      w.cu = __shfl_sync(0xffffffffu, req.cu, i);
       w.base = max(0, len - n);
       w.tok_end = w.cu + n;
       w.klo = io.window ? clampi(static_cast<int64_t>(w.base) - io.window + 1, 0, len) : 0;
@@ -648,8 +621,7 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   // read is a round trip to L2 or HBM
   int held_pages = -1;
   const int line = kind == kPair ? 0 : 1 + slot;
-  const int64_t begin = (kind == kPair ? static_cast<int64_t>(blockIdx.x) : 2ll * blockIdx.x + slot) * S.plan.share[kind];
-  bool ok = walk(P, S.plan, kind, begin, S.first[line], S.first_at[line], [&](const Piece& w) -> bool {
+  bool ok = walk(P, S.plan, kind, slot, S.first[line], S.first_at[line], [&](const Piece& w) -> bool {
     if (!push(w)) return false;
     const int pages = fetch(w, 0);
     if (n_out > 1 && !load_piece(R.fifo[(n_out - 2) % kFifo], held_pages)) return false;
@@ -672,22 +644,24 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   return false;
 }
 
-// ---- MMA issuer of one slot: the whole warp walks the pieces, one elected lane
-// issues, so that descriptors and addresses are warp-uniform; false once a wait
-// has run out
+// ---- MMA issuer: the whole warp walks the pieces, one elected lane issues, so
+// that descriptors and addresses are warp-uniform; false once a wait has run out.
+// Of a solo each slot has its own; of a pair slot 0's issues for both, slot by
+// slot: with the products of both slots mixed, slots that make their P at the same
+// time go on doing so, and a tile takes 2.5 us instead of 1.6.
 struct SlotParity {
   uint32_t s = 0, p = 0, o = 0;
+  int cold = 1;  // nothing has run yet
 };
 
 template <class T, int D>
 MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParity& par) {
   constexpr uint32_t kIdS = idesc_of<T>(kTileKeys, false), kIdO = idesc_of<T>(D, true);
-  const int slot = V.slot;
-  const uint32_t ts = S.tmem + slot * 128, to = S.tmem + 256 + slot * 128;
+  const bool pair = V.kind == kPair, issue = !pair || V.slot == 0;
+  const int from = V.slot, to = pair ? 2 : V.slot + 1;  // slots
   Ring& R = *V.ring;
-  const uint64_t qd = sdesc_kmajor_sw128(smem_u32(V.q));
-  const uint32_t q_half = (V.kind == kPair ? 128 : 64) * 128 >> 4;  // to a row's second 64 values
-  const uint32_t kv = smem_u32(V.kv);
+  const uint32_t q = smem_u32(V.q), kv = smem_u32(V.kv);
+  const uint32_t q_half = (pair ? 128 : 64) * 128 >> 4;  // to a row's second 64 values
   Place at;  // of the next K tile
   int piece = 0;
   auto commit = [&](uint64_t* bar) {
@@ -695,28 +669,31 @@ MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParit
     __syncwarp();
   };
   auto wait_stage = [&](Place p) { return wait_warp(c, &R.full[p.st], p.round); };
-  // the scores of a tile; its K may be replaced afterwards
-  auto qk = [&](Place p) {
-    const uint64_t kd = sdesc_kmajor_sw128(kv + p.st * (128 * D * 2));
+  // the scores of a tile
+  auto qk = [&](int slot, Place p) {
+    const uint64_t qd = sdesc_kmajor_sw128(q + (slot - from) * TileSmem<D>::kTile);
+    const uint64_t kd = sdesc_kmajor_sw128(kv + p.st * TileSmem<D>::kTile);
     if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        mma_bf16(ts, qd + (k >> 2) * q_half + (k & 3) * 2, kd + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2,
-                 kIdS, k);
-      }
+      for (int k = 0; k < D / 16; ++k)
+        mma_bf16(S.tmem + slot * 128, qd + (k >> 2) * q_half + (k & 3) * 2,
+                 kd + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, kIdS, k);
       mma_commit(&S.s_full[slot]);
-      mma_commit(&R.empty[p.st]);
     }
     __syncwarp();
   };
-  auto pv = [&](Place v, bool first) {
-    const uint64_t vd = sdesc_mnmajor_sw128(kv + v.st * (128 * D * 2), 128 * 128);
+  auto pv = [&](int slot, Place v, bool first) {
+    const uint64_t vd = sdesc_mnmajor_sw128(kv + v.st * TileSmem<D>::kTile, 128 * 128);
     if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < kTileKeys / 16; ++k)
-        mma_ts(to, ts + 8 * k, vd + k * (16 * 128 >> 4), kIdO, !(first && k == 0));
+        mma_ts(S.tmem + 256 + slot * 128, S.tmem + slot * 128 + 8 * k, vd + k * (16 * 128 >> 4), kIdO,
+               !(first && k == 0));
     }
     __syncwarp();
+  };
+  auto free_q = [&] {
+    for (int slot = from; slot < to; ++slot) commit(&R.q_empty[slot - from]);
   };
   while (true) {
     const int f = piece % kFifo;
@@ -725,29 +702,38 @@ MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParit
     __syncwarp();
     if (elect_one()) mbar_arrive(&R.fifo_empty[f]);
     if (own < 0) return true;
-    if (!wait_warp(c, &R.q_full[V.q_bar], piece & 1) || !wait_stage(at)) return false;
+    ++piece;
+    if (!issue) {
+      par.p ^= n & 1;
+      continue;
+    }
+    for (int slot = from; slot < to; ++slot)
+      if (!wait_warp(c, &R.q_full[slot - from], (piece - 1) & 1)) return false;
+    if (!wait_stage(at)) return false;
     tc_fence_after();
-    qk(at);
-    if (n == 1) commit(&R.q_empty[V.q_bar]);
+    for (int slot = from; slot < to; ++slot) qk(slot, at);
+    commit(&R.empty[at.st]);
+    if (n == 1) free_q();
     for (int j = 0; j < n; ++j) {
       const Place sv = at.next(V.stages), sk = sv.next(V.stages);
       const bool more = j + 1 < n;
       if (!wait_stage(sv) || (more && !wait_stage(sk))) return false;
-      // P V, then the next scores right behind, which take P's place
-      if (!wait_warp(c, &S.p_full[slot], par.p)) return false;
-      tc_fence_after();
-      pv(sv, j == 0);
+      for (int slot = from; slot < to; ++slot) {
+        // P V, then the next scores right behind, which take P's place
+        if (!wait_warp(c, &S.p_full[slot], par.p)) return false;
+        tc_fence_after();
+        pv(slot, sv, j == 0);
+        if (more) qk(slot, sk);
+        else commit(&S.o_done[slot]);
+      }
       par.p ^= 1;
       if (more) {
-        qk(sk);
-        if (j == n - 2) commit(&R.q_empty[V.q_bar]);
-      } else {
-        commit(&S.o_done[slot]);
+        commit(&R.empty[sk.st]);
+        if (j == n - 2) free_q();
       }
       commit(&R.empty[sv.st]);
       at = sk;
     }
-    ++piece;
   }
 }
 
@@ -806,10 +792,13 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     }
     const bool warp_valid = __any_sync(0xffffffffu, valid);
 
+    // (The CTA's first tile goes through the motions on what lies in tensor memory,
+    // without waiting or leaving anything, while its scores are being made: this
+    // code then is in the instruction cache.)
     float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < n; ++j) {
+    for (int j = par.cold ? -1 : 0; j < n; ++j) {
       const int k0 = (w.kt_a + j) * kTileKeys;
-      if (k0 < w.klo || k0 + kTileKeys > w.khi) {
+      if (j >= 0 && (k0 < w.klo || k0 + kTileKeys > w.khi)) {
         // keys that no row sees may hold anything: their V rows become zeros, so
         // that a weight of zero leaves no NaN behind
         const Place sv = at.next(W.stages);
@@ -822,15 +811,17 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
         }
         fence_proxy_async_smem();
       }
-      if (!wait_warp(c, &S.s_full[slot], par.s)) return false;
-      par.s ^= 1;
-      tc_fence_after();
+      if (j >= 0) {
+        if (!wait_warp(c, &S.s_full[slot], par.s)) return false;
+        par.s ^= 1;
+        tc_fence_after();
+      }
       float s[kTileKeys];
       if (warp_valid) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s + 32 * q);
         tmem_ld_wait();
-        const bool edge = klo > k0 || khi < k0 + kTileKeys || tree_at < k0 + kTileKeys;
+        const bool edge = klo > k0 || khi < k0 + kTileKeys || tree_at < k0 + kTileKeys || j < 0;
         if (__any_sync(0xffffffffu, edge)) {
           const int lo = klo - k0, hi = khi - k0, tb = tree_at - k0;
 #pragma unroll
@@ -859,8 +850,9 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
         // rescale only when the maximum has grown by 2^8: until then P is at most
         // 2^8, which its types and the 32-bit sums hold without loss
         const bool grow = valid && top > m + kGrow;
-        if (j == 0) {
+        if (j <= 0) {
           m = top;
+          l = 0.f;
         } else if (__any_sync(0xffffffffu, grow)) {
           const float x = grow ? exp2_approx(m - top) : 1.f;
           if (grow) m = top;
@@ -892,17 +884,21 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
             sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], y);
             p[x >> 1] = Types<T>::pack(y.x, y.y);
           }
-          tmem_st32(ts + 32 * q, p);
+          if (j >= 0) tmem_st32(ts + 32 * q, p);
+          else par.cold += p[0] == 1u && p[31] == 1u;  // (keeps the work)
         }
         const float2 all = add2(sum[0], sum[1]);
         l += all.x + all.y;
         tmem_st_wait();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.p_full[slot]);
-      at = at.next(W.stages).next(W.stages);
+      if (j >= 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[slot]);
+        at = at.next(W.stages).next(W.stages);
+      }
     }
+    par.cold = 0;
 
     // the piece's result
     if (!wait_warp(c, &S.o_done[slot], par.o)) return false;
@@ -946,7 +942,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // one barrier per lane and turn
     for (int i = lane_id(); i < 3 * kMaxStages; i += 32) {
       mbar_init(&S.ring[i / kMaxStages].full[i % kMaxStages], 1);
-      mbar_init(&S.ring[i / kMaxStages].empty[i % kMaxStages], i < kMaxStages ? 2 : 1);
+      mbar_init(&S.ring[i / kMaxStages].empty[i % kMaxStages], 1);
     }
     for (int i = lane_id(); i < 3 * kFifo; i += 32) {
       mbar_init(&S.ring[i / kFifo].fifo_full[i % kFifo], 1);
@@ -986,7 +982,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const Ctx c{&S.abort, P.ws.status};
   // 2 x 128 x 208 + 128 x 88 = 64,512, all registers of the launch; all are back
   // at 168 before the common tail
-  const int first_kind = blockIdx.x & 1;
   if (warp < 8) {
     reg_alloc<208>();
     const int slot = warp >> 2;
@@ -994,7 +989,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
 #pragma unroll 1
     for (int turn = 0; ok && turn < 2; ++turn)
-      ok = softmax<T, D>(P, S, c, View<D>(S, first_kind ^ turn, slot), par);
+      ok = softmax<T, D>(P, S, c, View<D>(S, turn, slot), par);
     __syncwarp();
     reg_dealloc<168>();
   } else {
@@ -1004,14 +999,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp < 10) {
 #pragma unroll 1
       for (int turn = 0; ok && turn < 2; ++turn)
-        if ((first_kind ^ turn) == kSolo || slot == 0)
-          ok = produce<D>(P, S, c, View<D>(S, first_kind ^ turn, slot), (first_kind ^ turn) == kSolo ? &tm_q64 : &tm_q,
+        if (turn == kSolo || slot == 0)
+          ok = produce<D>(P, S, c, View<D>(S, turn, slot), turn == kSolo ? &tm_q64 : &tm_q,
                           &tm_k, &tm_v, turn ? &S.turn : nullptr);
     } else {
       SlotParity par;
 #pragma unroll 1
       for (int turn = 0; ok && turn < 2; ++turn) {
-        ok = issue_mmas<T, D>(S, c, View<D>(S, first_kind ^ turn, slot), par);
+        ok = issue_mmas<T, D>(S, c, View<D>(S, turn, slot), par);
         if (ok && turn == 0) {
           if (elect_one()) mma_commit(&S.turn);
           __syncwarp();
@@ -1125,18 +1120,18 @@ __global__ void __launch_bounds__(256) k_attn_merge(const __grid_constant__ Attn
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= old;
     const int cnt = min(32, n - a);
-    for (int k = 0; k < cnt; k += 4) {  // four rows on their way at once
-      Vals<V> y[4];
-      float f[4];
+    for (int k = 0; k < cnt; k += 8) {  // eight rows on their way at once
+      Vals<V> y[8];
+      float f[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
         f[u] = __shfl_sync(0xffffffffu, w, (k + u) & 31);
         const int64_t p = __shfl_sync(0xffffffffu, at, (k + u) & 31);
         if (k + u >= cnt) f[u] = 0.f;
         y[u] = load_vals<V>(P.ws.o + p * D + lane * V);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 8; ++u)
         if (f[u] != 0.f)
 #pragma unroll
           for (int v = 0; v < V; ++v) acc[v] += f[u] * y[u].v[v];
