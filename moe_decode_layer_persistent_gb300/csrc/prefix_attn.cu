@@ -204,6 +204,7 @@ struct alignas(1024) TileSmem {
   uint8_t arena[kArena];
   Ring ring[3];      // of pairs, of slot 0's solos, of slot 1's
   uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t turn_of[2];  // pairs: the other slot's issuer has had its turn
   uint64_t turn;     // both slots' MMAs of the first kind of work are done
   uint64_t drained[2];
   Plan plan;
@@ -240,11 +241,15 @@ struct View {
   }
 };
 
-// Bounded wait: false once any wait of the CTA has run out.
+// Bounded waits: false once any wait of the CTA has run out.  The clock is read
+// now and then only: reading it takes longer than a hand-off.
 MK_DEV bool wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
     if (*c.abort) return false;
     if (globaltimer() - t0 > kWaitNs) {
       *c.abort = 1;
@@ -252,7 +257,6 @@ MK_DEV bool wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity) {
       return false;
     }
   }
-  return true;
 }
 MK_DEV bool wait_warp(const Ctx& c, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait_bar(c, bar, parity));
@@ -644,11 +648,14 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   return false;
 }
 
-// ---- MMA issuer: the whole warp walks the pieces, one elected lane issues, so
-// that descriptors and addresses are warp-uniform; false once a wait has run out.
-// Of a solo each slot has its own; of a pair slot 0's issues for both, slot by
-// slot: with the products of both slots mixed, slots that make their P at the same
-// time go on doing so, and a tile takes 2.5 us instead of 1.6.
+// ---- MMA issuer of a slot: the whole warp walks the pieces, one elected lane
+// issues, so that descriptors and addresses are warp-uniform; false once a wait
+// has run out.  The issuers of a pair's slots take turns, a tile's P V and the next
+// tile's scores at a time: with the products of both slots mixed, slots that make
+// their P at the same time go on doing so, and a tile takes 2.5 us; with one warp
+// issuing for both, its waits and commits (0.1 us each) make it 1.8.  For the
+// commits' sake only scores and results are announced by one; what they tell about
+// the buffers, the softmax warps that wait for them pass on.
 struct SlotParity {
   uint32_t s = 0, p = 0, o = 0;
   int cold = 1;  // nothing has run yet
@@ -657,43 +664,29 @@ struct SlotParity {
 template <class T, int D>
 MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParity& par) {
   constexpr uint32_t kIdS = idesc_of<T>(kTileKeys, false), kIdO = idesc_of<T>(D, true);
-  const bool pair = V.kind == kPair, issue = !pair || V.slot == 0;
-  const int from = V.slot, to = pair ? 2 : V.slot + 1;  // slots
+  const bool pair = V.kind == kPair;
+  const int slot = V.slot;
+  const uint32_t ts = S.tmem + slot * 128, to = S.tmem + 256 + slot * 128;
   Ring& R = *V.ring;
-  const uint32_t q = smem_u32(V.q), kv = smem_u32(V.kv);
+  uint64_t* const q_full = &R.q_full[pair ? slot : 0];
+  const uint64_t qd = sdesc_kmajor_sw128(smem_u32(V.q));
   const uint32_t q_half = (pair ? 128 : 64) * 128 >> 4;  // to a row's second 64 values
+  const uint32_t kv = smem_u32(V.kv);
   Place at;  // of the next K tile
   int piece = 0;
-  auto commit = [&](uint64_t* bar) {
-    if (elect_one()) mma_commit(bar);
-    __syncwarp();
-  };
+  uint32_t turns = 0;
   auto wait_stage = [&](Place p) { return wait_warp(c, &R.full[p.st], p.round); };
+  auto my_turn = [&]() -> bool {
+    const uint32_t k = turns++ + slot;  // turns of the other slot that come first
+    return !pair || k == 0 || wait_warp(c, &S.turn_of[slot], (k - 1) & 1);
+  };
   // the scores of a tile
-  auto qk = [&](int slot, Place p) {
-    const uint64_t qd = sdesc_kmajor_sw128(q + (slot - from) * TileSmem<D>::kTile);
+  auto qk = [&](Place p) {
     const uint64_t kd = sdesc_kmajor_sw128(kv + p.st * TileSmem<D>::kTile);
-    if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_bf16(S.tmem + slot * 128, qd + (k >> 2) * q_half + (k & 3) * 2,
-                 kd + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, kIdS, k);
-      mma_commit(&S.s_full[slot]);
-    }
-    __syncwarp();
-  };
-  auto pv = [&](int slot, Place v, bool first) {
-    const uint64_t vd = sdesc_mnmajor_sw128(kv + v.st * TileSmem<D>::kTile, 128 * 128);
-    if (elect_one()) {
-#pragma unroll
-      for (int k = 0; k < kTileKeys / 16; ++k)
-        mma_ts(S.tmem + 256 + slot * 128, S.tmem + slot * 128 + 8 * k, vd + k * (16 * 128 >> 4), kIdO,
-               !(first && k == 0));
-    }
-    __syncwarp();
-  };
-  auto free_q = [&] {
-    for (int slot = from; slot < to; ++slot) commit(&R.q_empty[slot - from]);
+    for (int k = 0; k < D / 16; ++k)
+      mma_bf16(ts, qd + (k >> 2) * q_half + (k & 3) * 2, kd + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2,
+               kIdS, k);
   };
   while (true) {
     const int f = piece % kFifo;
@@ -702,38 +695,35 @@ MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParit
     __syncwarp();
     if (elect_one()) mbar_arrive(&R.fifo_empty[f]);
     if (own < 0) return true;
-    ++piece;
-    if (!issue) {
-      par.p ^= n & 1;
-      continue;
-    }
-    for (int slot = from; slot < to; ++slot)
-      if (!wait_warp(c, &R.q_full[slot - from], (piece - 1) & 1)) return false;
-    if (!wait_stage(at)) return false;
+    if (!wait_warp(c, q_full, piece & 1) || !wait_stage(at) || !my_turn()) return false;
     tc_fence_after();
-    for (int slot = from; slot < to; ++slot) qk(slot, at);
-    commit(&R.empty[at.st]);
-    if (n == 1) free_q();
+    if (elect_one()) {
+      qk(at);
+      if (pair) mbar_arrive(&S.turn_of[slot ^ 1]);
+      mma_commit(&S.s_full[slot]);
+    }
+    __syncwarp();
     for (int j = 0; j < n; ++j) {
       const Place sv = at.next(V.stages), sk = sv.next(V.stages);
       const bool more = j + 1 < n;
       if (!wait_stage(sv) || (more && !wait_stage(sk))) return false;
-      for (int slot = from; slot < to; ++slot) {
-        // P V, then the next scores right behind, which take P's place
-        if (!wait_warp(c, &S.p_full[slot], par.p)) return false;
-        tc_fence_after();
-        pv(slot, sv, j == 0);
-        if (more) qk(slot, sk);
-        else commit(&S.o_done[slot]);
-      }
+      if (!wait_warp(c, &S.p_full[slot], par.p) || !my_turn()) return false;
       par.p ^= 1;
-      if (more) {
-        commit(&R.empty[sk.st]);
-        if (j == n - 2) free_q();
+      tc_fence_after();
+      const uint64_t vd = sdesc_mnmajor_sw128(kv + sv.st * TileSmem<D>::kTile, 128 * 128);
+      if (elect_one()) {
+        // P V, then the next scores right behind, which take P's place
+#pragma unroll
+        for (int k = 0; k < kTileKeys / 16; ++k)
+          mma_ts(to, ts + 8 * k, vd + k * (16 * 128 >> 4), kIdO, j > 0 || k > 0);
+        if (more) qk(sk);
+        if (pair) mbar_arrive(&S.turn_of[slot ^ 1]);
+        mma_commit(more ? &S.s_full[slot] : &S.o_done[slot]);
       }
-      commit(&R.empty[sv.st]);
+      __syncwarp();
       at = sk;
     }
+    ++piece;
   }
 }
 
@@ -815,6 +805,14 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
         if (!wait_warp(c, &S.s_full[slot], par.s)) return false;
         par.s ^= 1;
         tc_fence_after();
+        // These scores are done, and so is all that this slot's issuer sent before
+        // them: the slot no longer needs the tile's K, the V of the tile before and,
+        // with the last tile, its row tile.
+        if (warp == 0 && lane == 0) {
+          mbar_arrive(&R.empty[at.st]);
+          if (j > 0) mbar_arrive(&R.empty[at.st == 0 ? W.stages - 1 : at.st - 1]);
+          if (j == n - 1) mbar_arrive(&R.q_empty[kind == kPair ? slot : 0]);
+        }
       }
       float s[kTileKeys];
       if (warp_valid) {
@@ -904,6 +902,8 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     if (!wait_warp(c, &S.o_done[slot], par.o)) return false;
     par.o ^= 1;
     tc_fence_after();
+    if (warp == 0 && lane == 0)  // the last V
+      mbar_arrive(&R.empty[at.st == 0 ? W.stages - 1 : at.st - 1]);
     const int32_t carry = ((kind * P.ctas + blockIdx.x) * 2 + slot) * 128 + row;
     const int64_t to_row = w.first ? (w.own ? P.ws.own : P.ws.pre) +
                                          static_cast<int64_t>(tok) * io.n_q_heads + w.h * G + g
@@ -913,6 +913,7 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         float o[32];
+        __syncwarp();  // (loads from tensor memory are for whole warps)
         tmem_ld32(to + 32 * q, o);
         tmem_ld_wait();
         if (valid) {
@@ -942,7 +943,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // one barrier per lane and turn
     for (int i = lane_id(); i < 3 * kMaxStages; i += 32) {
       mbar_init(&S.ring[i / kMaxStages].full[i % kMaxStages], 1);
-      mbar_init(&S.ring[i / kMaxStages].empty[i % kMaxStages], 1);
+      mbar_init(&S.ring[i / kMaxStages].empty[i % kMaxStages], i < kMaxStages ? 2 : 1);
     }
     for (int i = lane_id(); i < 3 * kFifo; i += 32) {
       mbar_init(&S.ring[i / kFifo].fifo_full[i % kFifo], 1);
@@ -957,6 +958,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&S.p_full[lane_id()], 4);
       mbar_init(&S.o_done[lane_id()], 1);
       mbar_init(&S.drained[lane_id()], 1);
+      mbar_init(&S.turn_of[lane_id()], 1);
     }
     if (lane_id() == 0) {
       mbar_init(&S.turn, 2);
