@@ -8,6 +8,7 @@ library has not been built -- there is no CPU fallback.
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmk.so")
@@ -379,63 +380,73 @@ def mk_selftest_sync(mode, iters=10000):
 # ------------------------------------------- batched decoding over a paged cache
 # The library sees addresses only, so that a tensor of another type, on another
 # device or with other strides would be misread: these are refused here, as
-# MK_ERR_INVALID_ARG.
+# MK_ERR_INVALID_ARG.  A serving loop makes these structs in every step: each
+# tensor is looked at once, and the fields are packed together.
+
+_torch = None
+_pack_slots = struct.Struct("@4iqiii11P").pack
+_pack_rope = struct.Struct("@5iPqPqPqPqPPPPq").pack
+_pack_attn = struct.Struct("@10iqifPqPPPPPPPPqP").pack
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
 
 def _refuse(fn):
     raise MkError(fn, MK_ERR_INVALID_ARG)
 
 
-def _dtype_of(fn, t):
-    import torch
-    if t.dtype is torch.bfloat16:
-        return MK_BF16
-    if t.dtype is torch.float16:
-        return MK_FP16
-    _refuse(fn)
+def _device_of(fn, t):
+    d = t.get_device()
+    if d < 0:
+        _refuse(fn)
+    return d
 
 
-def _dense(fn, t, elem, n=None):
-    """Address of a contiguous CUDA tensor of whole numbers or floats of `elem`
-    bytes (None: NULL), with `n` values if given."""
+def _vec(fn, t, dtype, dev, n=None):
+    """Address of a contiguous tensor of `dtype` on CUDA device `dev` (None: 0),
+    with `n` values if given."""
     if t is None:
-        return None
-    if not t.is_cuda or t.element_size() != elem or not t.is_contiguous() or (
+        return 0
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (
             n is not None and t.numel() != n):
         _refuse(fn)
     return t.data_ptr()
 
 
-def _ints(fn, t, elem, n=None):
-    if t is not None and (t.is_floating_point() or t.is_complex()):
-        _refuse(fn)
-    return _dense(fn, t, elem, n)
+def _kind(fn, T, t):
+    if t.dtype is T.bfloat16:
+        return MK_BF16
+    if t.dtype is T.float16:
+        return MK_FP16
+    _refuse(fn)
 
 
-def _heads(fn, t, like=None):
-    """(address, rows, heads, head_dim, elements between rows) of a tensor
-    [rows, heads, d] whose heads lie side by side."""
-    if not t.is_cuda or t.dim() != 3 or (like is not None and t.dtype != like.dtype):
+def _rows(fn, t, shape, dtype, dev):
+    """(address, elements between rows) of a tensor [rows, heads, d] whose heads
+    lie side by side."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
         _refuse(fn)
-    n, h, d = t.shape
+    n, h, d = shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         _refuse(fn)
-    return t.data_ptr(), n, h, d, s0 if n > 1 else max(s0, h * d)
+    return t.data_ptr(), s0 if n > 1 else max(s0, h * d)
 
 
-def _pool(fn, t, like):
-    """(address, pages, page size) of a pool [pages, page_size, heads, d]."""
-    if t.dim() != 4 or t.dtype != like.dtype:
+def _table(fn, t, dtype, dev):
+    """(address, rows, columns, elements between rows) of a table."""
+    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev:
         _refuse(fn)
-    return _dense(fn, t, 2), t.shape[0], t.shape[1]
-
-
-def _table(fn, t):
-    """(address, rows, columns, elements between rows) of an int32 table."""
-    if not t.is_cuda or t.dim() != 2 or t.element_size() != 4 or t.is_floating_point() or (
-            t.shape[1] > 1 and t.stride(1) != 1):
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
         _refuse(fn)
-    return t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1])
+    return t.data_ptr(), rows, cols, max(s0, cols)
 
 
 def make_slots_io(cached_lens, new_lens, free_pages, free_head, block_table, cu_rows, lens,
@@ -443,16 +454,19 @@ def make_slots_io(cached_lens, new_lens, free_pages, free_head, block_table, cu_
     """mk_slots_io of CUDA tensors (int32; slots int64).  free_head and
     row_request may be None."""
     fn = "make_slots_io"
+    T = _torch or _load_torch()
+    i32, dev = T.int32, _device_of(fn, cu_rows)
     b, n = cached_lens.numel(), positions.numel()
-    table, rows, cols, stride = _table(fn, block_table)
+    table, rows, cols, stride = _table(fn, block_table, i32, dev)
     if rows != b:
         _refuse(fn)
-    return mk_slots_io(b, n, page_size, cols, stride, n_pages, free_pages.numel(), prefix_len,
-                       _ints(fn, cached_lens, 4), _ints(fn, new_lens, 4, b),
-                       _ints(fn, free_pages, 4), _ints(fn, free_head, 4, 1), table,
-                       _ints(fn, cu_rows, 4, b + 1), _ints(fn, lens, 4, b), _ints(fn, positions, 4),
-                       _ints(fn, slots, 8, n), _ints(fn, row_request, 4, n),
-                       _ints(fn, summary, 4, 4))
+    return mk_slots_io.from_buffer_copy(_pack_slots(
+        b, n, page_size, cols, stride, n_pages, free_pages.numel(), prefix_len,
+        _vec(fn, cached_lens, i32, dev), _vec(fn, new_lens, i32, dev, b),
+        _vec(fn, free_pages, i32, dev), _vec(fn, free_head, i32, dev, 1), table,
+        _vec(fn, cu_rows, i32, dev, b + 1), _vec(fn, lens, i32, dev, b),
+        _vec(fn, positions, i32, dev), _vec(fn, slots, T.int64, dev, n),
+        _vec(fn, row_request, i32, dev, n), _vec(fn, summary, i32, dev, 4)))
 
 
 def mk_build_slots(io, stream=None):
@@ -481,33 +495,34 @@ def make_rope_io(q, q_out, k, v, positions, slots, k_cache, v_cache):
     heads, d] (views with a row stride), positions int32, slots int64, caches
     [pages, page_size, kv heads, d].  q or k (with v) may be None."""
     fn = "make_rope_io"
+    T = _torch or _load_torch()
     like = q if q is not None else k
-    if like is None:
+    if like is None or like.dim() != 3 or (k is None and v is not None):
         _refuse(fn)
-    n = like.shape[0]
-    dt = _dtype_of(fn, like)
-    qp = qop = kp = vp = kc = vc = None
-    qs = qos = ks = vs = hq = hk = n_slots = 0
+    dt, dev = like.dtype, _device_of(fn, like)
+    n, hq, d = like.shape
+    qp = qop = kp = vp = kc = vc = qs = qos = ks = vs = hk = n_slots = 0
     if q is not None:
-        qp, _, hq, d, qs = _heads(fn, q)
-        qop, no, ho, do, qos = _heads(fn, q_out, q)
-        if (no, ho, do) != (n, hq, d):
-            _refuse(fn)
+        qp, qs = _rows(fn, q, q.shape, dt, dev)
+        qop, qos = _rows(fn, q_out, q.shape, dt, dev)
+    else:
+        hq = 0
     if k is not None:
-        kp, nk, hk, dk, ks = _heads(fn, k, like)
-        kc, pages, page = _pool(fn, k_cache, like)
-        n_slots = pages * page
-        if nk != n or dk != like.shape[2] or k_cache.shape[2:] != k.shape[1:]:
+        hk = k.shape[1]
+        kp, ks = _rows(fn, k, (n, hk, d), dt, dev)
+        kc = _vec(fn, k_cache, dt, dev)
+        pool = k_cache.shape
+        if len(pool) != 4 or pool[2] != hk or pool[3] != d:
             _refuse(fn)
+        n_slots = pool[0] * pool[1]
         if v is not None:
-            vp, _, _, _, vs = _heads(fn, v, like)
-            vc = _pool(fn, v_cache, like)[0]
-            if v.shape != k.shape or v_cache.shape != k_cache.shape:
+            vp, vs = _rows(fn, v, (n, hk, d), dt, dev)
+            vc = _vec(fn, v_cache, dt, dev)
+            if v_cache.shape != pool:
                 _refuse(fn)
-    elif v is not None:
-        _refuse(fn)
-    return mk_rope_io(n, hq, hk, like.shape[2], dt, qp, qs, qop, qos, kp, ks, vp, vs,
-                      _ints(fn, positions, 4, n), _ints(fn, slots, 8, n), kc, vc, n_slots)
+    return mk_rope_io.from_buffer_copy(_pack_rope(
+        n, hq, hk, d, _kind(fn, T, like), qp, qs, qop, qos, kp, ks, vp, vs,
+        _vec(fn, positions, T.int32, dev, n), _vec(fn, slots, T.int64, dev, n), kc, vc, n_slots))
 
 
 def mk_rope_apply(rope, io, stream=None):
@@ -521,22 +536,26 @@ def make_prefix_attn_io(q, k_cache, v_cache, out, lens, cu_rows, block_table, pr
     block_table [requests, pages] and prefix_pages int32, tree_mask int64
     [rows], lse float32 [rows, q heads]."""
     fn = "make_prefix_attn_io"
-    qp, n, hq, d, qs = _heads(fn, q)
-    op, no, ho, do, os_ = _heads(fn, out, q)
-    kp, pages, page = _pool(fn, k_cache, q)
-    vp = _pool(fn, v_cache, q)[0]
-    table, b, cols, stride = _table(fn, block_table)
-    if (no, ho, do) != (n, hq, d) or v_cache.shape != k_cache.shape or k_cache.shape[3] != d:
+    T = _torch or _load_torch()
+    i32, dt, dev = T.int32, q.dtype, _device_of(fn, q)
+    shape, pool = q.shape, k_cache.shape
+    if len(shape) != 3 or len(pool) != 4:
+        _refuse(fn)
+    n, hq, d = shape
+    pages, page, hk, dk = pool
+    qp, qs = _rows(fn, q, shape, dt, dev)
+    op, os_ = _rows(fn, out, shape, dt, dev)
+    table, b, cols, stride = _table(fn, block_table, i32, dev)
+    if v_cache.shape != pool or dk != d:
         _refuse(fn)
     if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * page < prefix_len):
         _refuse(fn)
-    if lse is not None and not lse.is_floating_point():
-        _refuse(fn)
-    return mk_prefix_attn_io(b, n, hq, k_cache.shape[2], d, _dtype_of(fn, q), page, pages,
-                             prefix_len, cols, stride, window, scale, qp, qs, kp, vp,
-                             _ints(fn, prefix_pages, 4), table, _ints(fn, lens, 4, b),
-                             _ints(fn, cu_rows, 4, b + 1), _ints(fn, tree_mask, 8, n), op, os_,
-                             _dense(fn, lse, 4, n * hq))
+    return mk_prefix_attn_io.from_buffer_copy(_pack_attn(
+        b, n, hq, hk, d, _kind(fn, T, q), page, pages, prefix_len, cols, stride, window, scale,
+        qp, qs, _vec(fn, k_cache, dt, dev), _vec(fn, v_cache, dt, dev),
+        _vec(fn, prefix_pages, i32, dev), table, _vec(fn, lens, i32, dev, b),
+        _vec(fn, cu_rows, i32, dev, b + 1), _vec(fn, tree_mask, T.int64, dev, n), op, os_,
+        _vec(fn, lse, T.float32, dev, n * hq)))
 
 
 def mk_prefix_attn_workspace(io):

@@ -8,6 +8,7 @@
 // so the whole of it is two exclusive scans over the batch and a write per row
 // and per page.  Bound by launch latency at every batch size in use.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "batch.h"
@@ -228,18 +229,27 @@ __global__ void __launch_bounds__(kSlotThreads)
 }  // namespace
 
 mk_status check_device(const void* p, int* device, int* sm_count) {
-  int dev = -1, major = 0, minor = 0;
+  // SM count of each device once asked, -1 for another architecture (a fact of the
+  // machine; asking takes longer than the rest of a call)
+  static std::atomic<int> known[64];
+  int dev = -1;
   MK_CUDA_TRY(cudaGetDevice(&dev));
-  MK_CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
-  MK_CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
-  if (major != 10 || minor != 3) return MK_ERR_UNSUPPORTED;
-  if (sm_count) MK_CUDA_TRY(cudaDeviceGetAttribute(sm_count, cudaDevAttrMultiProcessorCount, dev));
+  int sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (sms == 0) {
+    int major = 0, minor = 0;
+    MK_CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
+    MK_CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
+    MK_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    if (major != 10 || minor != 3) sms = -1;
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  }
+  if (sms < 0) return MK_ERR_UNSUPPORTED;
   cudaPointerAttributes at;
   MK_CUDA_TRY(cudaPointerGetAttributes(&at, p));
+  if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return MK_ERR_INVALID_ARG;
   if (at.type == cudaMemoryTypeDevice && at.device != dev) return MK_ERR_INVALID_ARG;
-  if (at.type == cudaMemoryTypeHost || at.type == cudaMemoryTypeUnregistered)
-    return MK_ERR_INVALID_ARG;
   if (device) *device = dev;
+  if (sm_count) *sm_count = sms;
   return MK_OK;
 }
 

@@ -157,8 +157,33 @@ def test_attention_workspace_refusals(mk):
 def test_binding_refuses_what_the_library_would_misread(mk):
     import torch
     t = torch.zeros(4, dtype=torch.int32)           # host memory
-    refused(mk, lambda: mk._ints("f", t, 4), INVALID)
-    refused(mk, lambda: mk._dtype_of("f", torch.zeros(1)), INVALID)
+    q = torch.zeros(2, 2, 16, dtype=torch.bfloat16)
+    pool = torch.zeros(2, 16, 2, 16, dtype=torch.bfloat16)
+    refused(mk, lambda: mk.make_slots_io(t, t, t, None, t[None], t, t, t, t.long(), None, t, 16, 8), INVALID)
+    refused(mk, lambda: mk.make_rope_io(q, q, q, q, t, t.long(), pool, pool), INVALID)
     refused(mk, lambda: mk.make_rope_io(None, None, None, None, t, t, None, None), INVALID)
-    refused(mk, lambda: mk._heads("f", torch.zeros(2, 2, 2)), INVALID)
-    refused(mk, lambda: mk._table("f", t[None]), INVALID)
+    refused(mk, lambda: mk.make_rope_io(q[0], q, None, None, t, t, None, None), INVALID)
+    refused(mk, lambda: mk.make_prefix_attn_io(q, pool, pool, q, t, t, t[None], t, 4), INVALID)
+    # one thing at a time, with the device taken as given
+    refused(mk, lambda: mk._vec("f", t, torch.int64, -1), INVALID)
+    refused(mk, lambda: mk._vec("f", t, torch.int32, 0), INVALID)
+    refused(mk, lambda: mk._vec("f", t, torch.int32, -1, 5), INVALID)
+    refused(mk, lambda: mk._vec("f", t[::2], torch.int32, -1), INVALID)
+    refused(mk, lambda: mk._rows("f", q.transpose(0, 1), (2, 2, 16), q.dtype, -1), INVALID)
+    refused(mk, lambda: mk._rows("f", q, (2, 2, 32), q.dtype, -1), INVALID)
+    refused(mk, lambda: mk._rows("f", q.half(), (2, 2, 16), q.dtype, -1), INVALID)
+    refused(mk, lambda: mk._table("f", t.repeat(4, 1).t(), torch.int32, -1), INVALID)
+    refused(mk, lambda: mk._table("f", t, torch.int32, -1), INVALID)
+    refused(mk, lambda: mk._kind("f", torch, torch.zeros(1)), INVALID)
+    assert mk._vec("f", None, torch.int32, 0) == 0
+    assert mk._rows("f", q[:, :1], (2, 1, 16), q.dtype, -1) == (q.data_ptr(), 32)
+
+
+def test_packed_fields_are_the_structs(mk):
+    """The packed layouts are those of the ctypes structs, field by field."""
+    import struct
+    for cls, fmt in ((mk.mk_slots_io, "@4iqiii11P"), (mk.mk_rope_io, "@5iPqPqPqPqPPPPq"),
+                     (mk.mk_prefix_attn_io, "@10iqifPqPPPPPPPPqP")):
+        values = [i + 1 for i in range(len(cls._fields_))]
+        got = cls.from_buffer_copy(struct.Struct(fmt).pack(*values))
+        assert [getattr(got, f) for f, _ in cls._fields_] == values
