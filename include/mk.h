@@ -360,7 +360,8 @@ typedef struct mk_slots_io {
   int32_t n_requests;         /* B, 0 .. 65536                                    */
   int32_t n_rows;             /* length of the row outputs                        */
   int32_t page_size;          /* tokens per page, >= 1                            */
-  int32_t max_pages;          /* pages per row of block_table                     */
+  int32_t max_pages;          /* pages per row of block_table;
+                                 prefix_len + (max_pages + 1) * page_size < 2^31   */
   int64_t table_stride;       /* entries between rows of block_table, >= max_pages */
   int32_t n_pages;            /* pages in the pool                                */
   int32_t n_free;             /* length of free_pages                             */

@@ -53,86 +53,104 @@ template <> struct Pack<__half> {
   }
 };
 
-// Rotates chunk j of a head (of pieces of 16 bytes): for the half layout the 8
-// pairs whose first values are chunk j, for the interleaved one the 4 pairs of
-// chunk j.  Both values of a pair are read before either is written, so src
-// may be dst.  cs: cos and sin of the row's pairs.
+// A piece of work: 16 bytes of a head that turn with 16 others (half layout) or
+// among themselves (interleaved), or that pass.
+struct Piece {
+  uint4 a, b;
+};
+
+// Turns piece j of a head: for the half layout the 8 pairs whose first values are
+// a and second ones b, for the interleaved one the 4 pairs of a.  cs: cos and sin
+// of the row's pairs.
 template <class T, int LAYOUT>
-MK_DEV void rotate_chunk(const T* src, T* dst, int j, int rot, const float2* cs) {
-  if (LAYOUT == MK_ROPE_HALF) {
-    uint4 a = reinterpret_cast<const uint4*>(src)[j];
-    uint4 b = reinterpret_cast<const uint4*>(src + rot / 2)[j];
-    uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
-    uint32_t* wb = reinterpret_cast<uint32_t*>(&b);
+MK_DEV void turn_piece(Piece& x, int j, const float2* cs) {
+  uint32_t* wa = reinterpret_cast<uint32_t*>(&x.a);
+  uint32_t* wb = reinterpret_cast<uint32_t*>(&x.b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = Pack<T>::get(wa[i]), y = Pack<T>::get(wb[i]);
+  for (int i = 0; i < 4; ++i) {
+    if (LAYOUT == MK_ROPE_HALF) {
+      const float2 u = Pack<T>::get(wa[i]), v = Pack<T>::get(wb[i]);
       const float2 c0 = cs[8 * j + 2 * i], c1 = cs[8 * j + 2 * i + 1];
-      wa[i] = Pack<T>::put(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
-      wb[i] = Pack<T>::put(y.x * c0.x + x.x * c0.y, y.y * c1.x + x.y * c1.y);
+      wa[i] = Pack<T>::put(u.x * c0.x - v.x * c0.y, u.y * c1.x - v.y * c1.y);
+      wb[i] = Pack<T>::put(v.x * c0.x + u.x * c0.y, v.y * c1.x + u.y * c1.y);
+    } else {
+      const float2 u = Pack<T>::get(wa[i]), c = cs[4 * j + i];
+      wa[i] = Pack<T>::put(u.x * c.x - u.y * c.y, u.y * c.x + u.x * c.y);
     }
-    reinterpret_cast<uint4*>(dst)[j] = a;
-    reinterpret_cast<uint4*>(dst + rot / 2)[j] = b;
-  } else {
-    uint4 a = reinterpret_cast<const uint4*>(src)[j];
-    uint32_t* w = reinterpret_cast<uint32_t*>(&a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = Pack<T>::get(w[i]), c = cs[4 * j + i];
-      w[i] = Pack<T>::put(x.x * c.x - x.y * c.y, x.y * c.x + x.x * c.y);
-    }
-    reinterpret_cast<uint4*>(dst)[j] = a;
   }
 }
 
-// One row per CTA: the row's cosines and sines once, in shared memory, then
-// every head's pieces.
+// One row per CTA: the row's cosines and sines once, in shared memory, then every
+// head's pieces, kPieces per thread at a time.  The first ones are on their way
+// while the angles are being made, so that a CTA's life is one trip to memory and
+// back; HBM bounds it with many rows (403 MB of a 16,384-row prompt, half layout,
+// 32 + 2 x 8 heads of 128: @PROMPT@), the launch with few (16 rows: @VERIFY@).
 template <class T, int LAYOUT>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeParams P) {
   const mk_rope_io& io = P.io;
+  constexpr int kPieces = 2;
   __shared__ float2 cs[128];
   const int64_t row = blockIdx.x;
   const int d = P.d, rot = P.rot;
-  const int64_t pos = io.positions[row];
-  for (int i = threadIdx.x; i < rot / 2; i += kRopeThreads) {
-    const uint64_t phase = static_cast<uint64_t>(pos) * P.turns[i];
-    const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    cs[i] = make_float2(c * P.m, s * P.m);
-  }
-  __syncthreads();
+  const int32_t pos = io.positions[row];
   int64_t slot = -1;
   if (io.k) {
     slot = io.slots[row];
     if (slot >= io.n_slots) slot = -1;
   }
-  const int turned = LAYOUT == MK_ROPE_HALF ? rot / 16 : rot / 8;  // pieces that turn
-  const int pieces = turned + (d - rot) / 8;
-  const int nq = io.n_q_heads * pieces, nk = slot >= 0 ? io.n_kv_heads * pieces : 0;
-  const int nv = slot >= 0 && io.v ? io.n_kv_heads * (d / 8) : 0;
-  for (int t = threadIdx.x; t < nq + nk + nv; t += kRopeThreads) {
-    if (t < nq + nk) {
-      const bool q = t < nq;
-      const int u = q ? t : t - nq;
-      const int head = u / pieces, j = u % pieces;
-      const T* src = q ? static_cast<const T*>(io.q) + row * io.q_stride
-                       : static_cast<const T*>(io.k) + row * io.k_stride;
-      T* dst = q ? static_cast<T*>(io.q_out) + row * io.q_out_stride
-                 : static_cast<T*>(io.k_cache) + slot * (static_cast<int64_t>(io.n_kv_heads) * d);
-      src += head * d;
-      dst += head * d;
-      if (j < turned) {
-        rotate_chunk<T, LAYOUT>(src, dst, j, rot, cs);
+  const uint32_t turned = LAYOUT == MK_ROPE_HALF ? rot / 16 : rot / 8;  // pieces that turn
+  const uint32_t pieces = turned + (d - rot) / 8;
+  const uint32_t nq = io.n_q_heads * pieces, nk = io.n_kv_heads * pieces;
+  const uint32_t n = nq + nk + (io.v ? io.n_kv_heads * (d / 8) : 0);
+  const int64_t cache_row = slot * (static_cast<int64_t>(io.n_kv_heads) * d);
+  for (uint32_t t0 = threadIdx.x; t0 == threadIdx.x || t0 < n; t0 += kPieces * kRopeThreads) {
+    Piece x[kPieces];
+    T* dst[kPieces];
+    int j[kPieces];  // piece that turns; -1: passes
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t t = t0 + i * kRopeThreads;
+      dst[i] = nullptr;
+      j[i] = -1;
+      if (t >= n) continue;
+      const T* src;
+      if (t < nq + nk) {
+        const bool q = t < nq;
+        const uint32_t u = q ? t : t - nq, head = u / pieces, p = u - head * pieces;
+        src = q ? static_cast<const T*>(io.q) + row * io.q_stride
+                : static_cast<const T*>(io.k) + row * io.k_stride;
+        T* to = q ? static_cast<T*>(io.q_out) + row * io.q_out_stride
+                  : static_cast<T*>(io.k_cache) + cache_row;
+        const uint32_t at = head * d + (p < turned ? p * 8 : rot + (p - turned) * 8);
+        src += at;
+        if (q || slot >= 0) dst[i] = to + at;
+        if (p < turned) j[i] = static_cast<int>(p);
       } else {
-        const int k = rot / 8 + (j - turned);
-        reinterpret_cast<uint4*>(dst)[k] = reinterpret_cast<const uint4*>(src)[k];
+        const uint32_t at = (t - nq - nk) * 8;
+        src = static_cast<const T*>(io.v) + row * io.v_stride + at;
+        if (slot >= 0) dst[i] = static_cast<T*>(io.v_cache) + cache_row + at;
       }
-    } else {
-      const int u = t - nq - nk;
-      reinterpret_cast<uint4*>(static_cast<T*>(io.v_cache) +
-                               slot * (static_cast<int64_t>(io.n_kv_heads) * d))[u] =
-          reinterpret_cast<const uint4*>(static_cast<const T*>(io.v) + row * io.v_stride)[u];
+      x[i].a = *reinterpret_cast<const uint4*>(src);
+      if (LAYOUT == MK_ROPE_HALF && j[i] >= 0) x[i].b = *reinterpret_cast<const uint4*>(src + rot / 2);
+    }
+    if (t0 == threadIdx.x) {
+      for (int i = threadIdx.x; i < rot / 2; i += kRopeThreads) {
+        const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[i];
+        const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
+        float s, c;
+        sincospif(half_turns, &s, &c);
+        cs[i] = make_float2(c * P.m, s * P.m);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      if (!dst[i]) continue;
+      if (j[i] >= 0) {
+        turn_piece<T, LAYOUT>(x[i], j[i], cs);
+        if (LAYOUT == MK_ROPE_HALF) *reinterpret_cast<uint4*>(dst[i] + rot / 2) = x[i].b;
+      }
+      *reinterpret_cast<uint4*>(dst[i]) = x[i].a;
     }
   }
 }

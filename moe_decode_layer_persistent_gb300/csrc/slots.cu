@@ -5,8 +5,10 @@
 //   cu_b    = sum_{a<b} n_a                      rows of request b
 //   need_b  = ceil((c_b+n_b)/P) - ceil(c_b/P)    pages it gets
 //   first_b = head + sum_{a<b} need_a            their place in the free list
-// so the whole of it is two exclusive scans over the batch and a write per row
-// and per page.  Bound by launch latency at every batch size in use.
+// so the whole of it is two exclusive sums over the batch and a write per row and
+// per page.  Each CTA sums the lengths before its own requests itself, in one
+// launch: reading the batch again from L2 costs less than a second launch or a
+// wait for other CTAs.  A handful of dependent reads bounds it, not the bytes.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -18,141 +20,178 @@ namespace mk {
 
 namespace {
 
-constexpr int kSlotThreads = 256;
+constexpr int kSlotThreads = 512;
+
+// Quotients of numbers below 2^31 by a fixed divisor: with 2^(s-1) < d <= 2^s and
+// m = floor(2^(31+s) / d) + 1, floor(x m / 2^(31+s)) = floor(x / d), since the error
+// x (m - 2^(31+s) / d) / 2^(31+s) <= x / 2^(31+s) < 1 / d.
+struct Divisor {
+  uint32_t d, m, shift;
+};
+Divisor make_divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t{1} << s) < d) ++s;
+  return Divisor{d, static_cast<uint32_t>((uint64_t{1} << (31 + s)) / d + 1), 31 + s};
+}
+MK_DEV uint32_t quotient(uint32_t x, const Divisor& v) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(x) * v.m) >> v.shift);
+}
 
 struct SlotsParams {
   mk_slots_io io;
+  Divisor page;
   int32_t per_cta;  // requests of one CTA
 };
 
-// Lengths of one request as every CTA reads them.
+// Sums over a batch, or a part of it.
+struct Sums {
+  int64_t rows, need;
+};
+
+// One request's lengths.
 struct Request {
-  int64_t rows;  // rows in the row layout
-  int64_t need;  // pages, if its rows fit
+  int32_t cached, rows, need;  // need: pages, if its rows fit
   bool lengths_ok;
 };
 
-MK_DEV int64_t pages_of(int64_t tokens, int32_t page) { return (tokens + page - 1) / page; }
-
-MK_DEV Request read_request(const mk_slots_io& io, int b) {
-  const int64_t c = io.cached_lens[b], n = io.new_lens[b];
+MK_DEV Request read_request(const SlotsParams& P, int b) {
+  const mk_slots_io& io = P.io;
+  const int32_t c = io.cached_lens[b], n = io.new_lens[b];
   Request r;
-  r.rows = n > 0 ? n : 0;
-  r.lengths_ok = c >= 0 && n >= 0 && c + n <= static_cast<int64_t>(io.max_pages) * io.page_size;
-  r.need = r.lengths_ok ? pages_of(c + n, io.page_size) - pages_of(c, io.page_size) : 0;
+  r.cached = c;
+  r.rows = max(n, 0);
+  // (max_pages * page_size is below 2^31)
+  r.lengths_ok = c >= 0 && n >= 0 && static_cast<int64_t>(c) + n <= io.max_pages * io.page_size;
+  r.need = 0;
+  if (r.lengths_ok)
+    r.need = quotient(c + n + io.page_size - 1u, P.page) - quotient(c + io.page_size - 1u, P.page);
   return r;
 }
 
-// Inclusive sums of one value per thread over the CTA; *total = the sum of all.
-MK_DEV int64_t cta_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+// Inclusive sums of a value pair per thread over the CTA; *total = those of all.
+MK_DEV Sums cta_scan(Sums v, Sums* warp_sums, Sums* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+    const int64_t a = __shfl_up_sync(0xffffffffu, v.rows, o), b = __shfl_up_sync(0xffffffffu, v.need, o);
+    if (lane >= o) v.rows += a, v.need += b;
   }
+  __syncthreads();
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  int64_t before = 0, all = 0;
+  Sums before{0, 0}, all{0, 0};
 #pragma unroll
   for (int w = 0; w < kSlotThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    all += warp_sums[w];
+    const Sums x = warp_sums[w];
+    if (w < warp) before.rows += x.rows, before.need += x.need;
+    all.rows += x.rows, all.need += x.need;
   }
-  __syncthreads();
   *total = all;
-  return v + before;
+  return Sums{v.rows + before.rows, v.need + before.need};
 }
 
-MK_DEV int64_t cta_sum(int64_t v, int64_t* warp_sums) {
-  int64_t total;
-  cta_scan(v, warp_sums, &total);
-  return total;
+MK_DEV int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
-// Each CTA owns per_cta consecutive requests.  It sums the lengths of the
-// requests before its own (and of all, for the end of the rows) itself:
-// reading the batch's lengths again costs less than a second launch or a wait
-// for the CTAs before it.
 __global__ void __launch_bounds__(kSlotThreads)
     k_build_slots(const __grid_constant__ SlotsParams P) {
   const mk_slots_io& io = P.io;
-  __shared__ int64_t warp_sums[kSlotThreads / 32];
-  __shared__ int64_t s_cu[kSlotThreads + 1];     // first row of each request of the chunk
-  __shared__ int64_t s_need[kSlotThreads + 1];   // pages before each request of the chunk
+  __shared__ Sums warp_sums[kSlotThreads / 32];
+  __shared__ int64_t part[kSlotThreads / 32][5];
+  __shared__ int64_t s_cu[kSlotThreads];    // first row of each request of the chunk
+  __shared__ int64_t s_need[kSlotThreads];  // pages before each request of the chunk
   __shared__ int32_t s_cached[kSlotThreads];
   __shared__ uint8_t s_granted[kSlotThreads];
 
-  const int B = io.n_requests, page = io.page_size;
+  const int B = io.n_requests, page = io.page_size, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b0 = min(B, static_cast<int>(blockIdx.x) * P.per_cta), b1 = min(B, b0 + P.per_cta);
   int64_t head = io.free_head ? *io.free_head : 0;
   head = head < 0 ? 0 : head > io.n_free ? io.n_free : head;
   const int64_t avail = io.n_free - head;
 
-  // sums over the requests before b0 and over all
-  int64_t rows_before = 0, rows_all = 0, need_before = 0, need_all = 0;
+  // sums over the requests before b0 and over all, and how many lengths are wrong
+  Sums before{0, 0}, all{0, 0};
+  int64_t wrong = 0;
+#pragma unroll 4
   for (int b = threadIdx.x; b < B; b += kSlotThreads) {
-    const Request r = read_request(io, b);
-    rows_all += r.rows;
-    need_all += r.need;
-    if (b < b0) rows_before += r.rows, need_before += r.need;
+    const Request r = read_request(P, b);
+    all.rows += r.rows, all.need += r.need;
+    if (b < b0) before.rows += r.rows, before.need += r.need;
+    wrong += !r.lengths_ok;
   }
-  rows_before = cta_sum(rows_before, warp_sums);
-  rows_all = cta_sum(rows_all, warp_sums);
-  need_before = cta_sum(need_before, warp_sums);
-  need_all = cta_sum(need_all, warp_sums);
-  if (rows_all > io.n_rows) {
-    // some request's rows do not fit: it and those behind it need no pages, so
-    // the page sums have to go by each request's last row
-    int64_t row = 0;
-    need_before = need_all = 0;
+  {
+    const int64_t v[5] = {warp_sum(before.rows), warp_sum(before.need), warp_sum(all.rows),
+                          warp_sum(all.need), warp_sum(wrong)};
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < 5; ++i) part[warp][i] = v[i];
+    __syncthreads();
+    int64_t sum[5] = {0, 0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kSlotThreads / 32; ++w)
+#pragma unroll
+      for (int i = 0; i < 5; ++i) sum[i] += part[w][i];
+    before = Sums{sum[0], sum[1]};
+    all = Sums{sum[2], sum[3]};
+    wrong = sum[4];
+  }
+  const int64_t rows_all = all.rows;
+  const int64_t rows_used = rows_all < io.n_rows ? rows_all : io.n_rows;
+  int64_t taken = all.need, refused = wrong;
+  if (rows_all > io.n_rows || all.need > avail) {
+    // Some request's rows or pages do not fit.  One whose rows do not needs no
+    // pages, nor do those behind it, so that the page sums go by each one's last
+    // row: a pass over the batch in order.
+    Sums at{0, 0};
+    before.need = taken = refused = 0;
     for (int a = 0; a < B; a += kSlotThreads) {
       const int b = a + threadIdx.x;
-      Request r{0, 0, false};
-      if (b < B) r = read_request(io, b);
-      int64_t rows, need;
-      const int64_t end = row + cta_scan(r.rows, warp_sums, &rows);
-      cta_scan(end <= io.n_rows ? r.need : 0, warp_sums, &need);
-      need_all += need;
-      if (b1 > b0) need_before += cta_sum(b < b0 && end <= io.n_rows ? r.need : 0, warp_sums);
-      row += rows;
+      Request r{0, 0, 0, false};
+      if (b < B) r = read_request(P, b);
+      Sums total;
+      const int64_t end = at.rows + cta_scan(Sums{r.rows, 0}, warp_sums, &total).rows;
+      at.rows += total.rows;
+      const bool fits = b < B && r.lengths_ok && end <= io.n_rows;
+      const int64_t want = fits ? r.need : 0;
+      const int64_t need_end = at.need + cta_scan(Sums{0, want}, warp_sums, &total).need;
+      at.need += total.need;
+      const bool granted = fits && (want == 0 || need_end <= avail);
+      cta_scan(Sums{granted ? want : 0, b < B && !granted}, warp_sums, &total);
+      taken += total.rows;
+      refused += total.need;
+      cta_scan(Sums{0, b < b0 ? want : 0}, warp_sums, &total);
+      before.need += total.need;
     }
+    all.need = at.need;
   }
-  const int64_t rows_used = rows_all < io.n_rows ? rows_all : io.n_rows;
 
   for (int a = b0; a < b1; a += kSlotThreads) {
     const int m = min(kSlotThreads, b1 - a), i = threadIdx.x, b = a + i;
-    Request r{0, 0, false};
-    int64_t c = 0, n = 0;
-    if (i < m) {
-      r = read_request(io, b);
-      c = io.cached_lens[b];
-      n = r.rows;
-    }
-    int64_t rows, need;
-    const int64_t row_end = rows_before + cta_scan(r.rows, warp_sums, &rows);
+    Request r{0, 0, 0, false};
+    if (i < m) r = read_request(P, b);
+    // (the rows first: whether they fit decides about the pages)
+    Sums total, need_total;
+    const int64_t row_end = before.rows + cta_scan(Sums{r.rows, 0}, warp_sums, &total).rows;
     const bool fits = i < m && r.lengths_ok && row_end <= io.n_rows;
     const int64_t want = fits ? r.need : 0;
-    const int64_t need_end = need_before + cta_scan(want, warp_sums, &need);
+    const int64_t need_end = before.need + cta_scan(Sums{0, want}, warp_sums, &need_total).need;
     const bool granted = fits && (want == 0 || need_end <= avail);
     if (i < m) {
-      const int64_t cap = static_cast<int64_t>(io.max_pages) * page;
       io.cu_rows[b] = static_cast<int32_t>(min(row_end - r.rows, static_cast<int64_t>(io.n_rows)));
-      io.lens[b] = static_cast<int32_t>(granted ? c + n : c < 0 ? 0 : min(c, cap));
-      s_cached[i] = static_cast<int32_t>(c);
+      io.lens[b] = granted ? r.cached + r.rows : max(0, min(r.cached, io.max_pages * page));
+      s_cached[i] = r.cached;
       s_granted[i] = granted;
     }
     s_cu[i] = row_end - r.rows;
     s_need[i] = need_end - want;
-    if (i == kSlotThreads - 1) {
-      s_cu[kSlotThreads] = row_end;
-      s_need[kSlotThreads] = need_end;
-    }
     __syncthreads();
 
     // the new pages of the chunk's requests, one thread per page
-    for (int64_t e = need_before + threadIdx.x; e < need_before + need && e < avail;
-         e += kSlotThreads) {
+    const int64_t e1 = min(before.need + need_total.need, avail);
+    for (int64_t e = before.need + threadIdx.x; e < e1; e += kSlotThreads) {
       int lo = 0, hi = m;  // the last request with s_need <= e, which has a page at e
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -160,12 +199,13 @@ __global__ void __launch_bounds__(kSlotThreads)
       }
       if (s_granted[lo])
         io.block_table[static_cast<int64_t>(a + lo) * io.table_stride +
-                       pages_of(s_cached[lo], page) + (e - s_need[lo])] = io.free_pages[head + e];
+                       quotient(s_cached[lo] + page - 1u, P.page) + (e - s_need[lo])] =
+            io.free_pages[head + e];
     }
     // the chunk's rows, one thread per row; a row takes its page from where it
     // is handed out, not from the table, which this CTA is writing
-    const int64_t r1 = min(rows_before + rows, static_cast<int64_t>(io.n_rows));
-    for (int64_t row = rows_before + threadIdx.x; row < r1; row += kSlotThreads) {
+    const int64_t r1 = min(before.rows + total.rows, static_cast<int64_t>(io.n_rows));
+    for (int64_t row = before.rows + threadIdx.x; row < r1; row += kSlotThreads) {
       int lo = 0, hi = m;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -174,18 +214,19 @@ __global__ void __launch_bounds__(kSlotThreads)
       const int64_t at = static_cast<int64_t>(s_cached[lo]) + (row - s_cu[lo]);
       int64_t slot = -1;
       if (s_granted[lo]) {
-        const int64_t col = at / page, held = pages_of(s_cached[lo], page);
+        const uint32_t t = static_cast<uint32_t>(at), col = quotient(t, P.page);
+        const uint32_t held = quotient(s_cached[lo] + page - 1u, P.page);
         const int32_t id =
             col < held ? io.block_table[static_cast<int64_t>(a + lo) * io.table_stride + col]
                        : io.free_pages[head + s_need[lo] + (col - held)];
-        if (id >= 0 && id < io.n_pages) slot = static_cast<int64_t>(id) * page + at % page;
+        if (id >= 0 && id < io.n_pages) slot = static_cast<int64_t>(id) * page + (t - col * page);
       }
       io.positions[row] = static_cast<int32_t>(min(io.prefix_len + at, static_cast<int64_t>(INT_MAX)));
       io.slots[row] = slot;
       if (io.row_request) io.row_request[row] = a + lo;
     }
-    rows_before += rows;
-    need_before += need;
+    before.rows += total.rows;
+    before.need += need_total.need;
     __syncthreads();
   }
 
@@ -196,33 +237,12 @@ __global__ void __launch_bounds__(kSlotThreads)
     io.slots[row] = -1;
     if (io.row_request) io.row_request[row] = -1;
   }
-  if (blockIdx.x == gridDim.x - 1) {
-    // what was taken and refused: a pass over the batch in order
-    int64_t row = 0, upto = 0, taken = 0, refused = 0;
-    for (int a = 0; a < B; a += kSlotThreads) {
-      const int b = a + threadIdx.x;
-      Request r{0, 0, false};
-      if (b < B) r = read_request(io, b);
-      int64_t rows, need;
-      const int64_t end = row + cta_scan(r.rows, warp_sums, &rows);
-      const bool fits = b < B && r.lengths_ok && end <= io.n_rows;
-      const int64_t want = fits ? r.need : 0;
-      const int64_t need_end = upto + cta_scan(want, warp_sums, &need);
-      const bool granted = fits && (want == 0 || need_end <= avail);
-      taken += granted ? want : 0;
-      refused += b < B && !granted;
-      row += rows;
-      upto += need;
-    }
-    taken = cta_sum(taken, warp_sums);
-    refused = cta_sum(refused, warp_sums);
-    if (threadIdx.x == 0) {
-      io.cu_rows[B] = static_cast<int32_t>(rows_used);
-      io.summary[0] = static_cast<int32_t>(head + taken);
-      io.summary[1] = static_cast<int32_t>(rows_used);
-      io.summary[2] = static_cast<int32_t>(refused);
-      io.summary[3] = static_cast<int32_t>(need_all < INT_MAX ? need_all : INT_MAX);
-    }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    io.cu_rows[B] = static_cast<int32_t>(rows_used);
+    io.summary[0] = static_cast<int32_t>(head + taken);
+    io.summary[1] = static_cast<int32_t>(rows_used);
+    io.summary[2] = static_cast<int32_t>(refused);
+    io.summary[3] = static_cast<int32_t>(all.need < INT_MAX ? all.need : INT_MAX);
   }
 }
 
@@ -264,8 +284,7 @@ extern "C" mk_status mk_build_slots(const mk_slots_io* io, void* stream) {
       io->n_free < 0 || io->prefix_len < 0 || io->table_stride < io->max_pages)
     return MK_ERR_INVALID_ARG;
   const int64_t B = io->n_requests;
-  if (static_cast<int64_t>(io->max_pages) * io->page_size > INT32_MAX - io->prefix_len)
-    return MK_ERR_INVALID_ARG;
+  if ((io->max_pages + 1ll) * io->page_size > INT32_MAX - io->prefix_len) return MK_ERR_INVALID_ARG;
   if (!io->cu_rows || !io->summary) return MK_ERR_INVALID_ARG;
   if (B && (!io->cached_lens || !io->new_lens || !io->lens)) return MK_ERR_INVALID_ARG;
   if (B && io->max_pages && !io->block_table) return MK_ERR_INVALID_ARG;
@@ -301,6 +320,7 @@ extern "C" mk_status mk_build_slots(const mk_slots_io* io, void* stream) {
   if (st != MK_OK) return st;
   SlotsParams P;
   P.io = *io;
+  P.page = make_divisor(static_cast<uint32_t>(io->page_size));
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((B + 31) / 32, 2 * sms));
   P.per_cta = static_cast<int32_t>((B + grid - 1) / grid);
   k_build_slots<<<static_cast<unsigned>(grid), kSlotThreads, 0, static_cast<cudaStream_t>(stream)>>>(P);
