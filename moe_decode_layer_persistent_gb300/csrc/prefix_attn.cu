@@ -26,6 +26,7 @@
 // k_attn_tiles does all that, k_attn_merge joins the partial results of each
 // row.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -976,6 +977,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
+  pdl_wait();  // (what lies before it overlaps the end of the kernel before)
   lay_out_work<D>(P, S);
   tc_fence_before();
   __syncthreads();
@@ -1034,7 +1036,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // ------------------------------------------------------------------ merge
 
-// V values of one row's O per lane.
+constexpr int kMergeThreads = 256;
+
 template <int V>
 struct Vals {
   float v[V];
@@ -1042,26 +1045,34 @@ struct Vals {
 template <int V>
 MK_DEV Vals<V> load_vals(const float* p) {
   Vals<V> x;
-  if (V == 4) {
-    const float4 y = *reinterpret_cast<const float4*>(p);
-    x.v[0] = y.x, x.v[1] = y.y, x.v[V - 2] = y.z, x.v[V - 1] = y.w;
-  } else {
+  if (V == 2) {
     const float2 y = *reinterpret_cast<const float2*>(p);
     x.v[0] = y.x, x.v[1] = y.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i + 3 < V; i += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(p + i);
+      x.v[i] = y.x, x.v[i + 1] = y.y, x.v[i + 2] = y.z, x.v[i + 3] = y.w;
+    }
   }
   return x;
 }
 
-// One warp per row and q head.  What does not depend on the tiles (the row's
-// request) comes before the wait for them; behind it the first stretches'
-// results of the prefix and of the request's own keys, by row, and then those
-// of the stretches that carried on.
-template <class T, int D>
-__global__ void __launch_bounds__(256) k_attn_merge(const __grid_constant__ AttnParams P) {
+// What does not depend on the tiles (the row's request) comes before the wait for
+// them; behind it the first stretches' results of the prefix and of the request's
+// own keys, by row, and then those of the stretches that carried on.  Each is a
+// round trip to L2; they and the launch bound it.  A row and head has N lanes: 32,
+// or 16 where there are so many rows that they come in waves (64 requests of 8
+// tokens, 32 heads of 128: 10 us behind the tiles instead of 18; with 32 tokens and
+// 20 results each 16 lanes would take 6 us longer).
+template <class T, int D, int N>
+__global__ void __launch_bounds__(kMergeThreads) k_attn_merge(const __grid_constant__ AttnParams P) {
   const mk_prefix_attn_io& io = P.io;
-  constexpr int V = D / 32;
-  const int lane = lane_id(), Hq = io.n_q_heads;
-  const uint32_t item = blockIdx.x * 8u + (threadIdx.x >> 5);
+  constexpr int V = D / N, kAtOnce = N == 32 ? 8 : 4;
+  const int lane = threadIdx.x % N, Hq = io.n_q_heads;
+  // the item's lanes
+  const uint32_t lanes = N == 32 ? 0xffffffffu : (threadIdx.x & 16) ? 0xffff0000u : 0xffffu;
+  const uint32_t item = blockIdx.x * static_cast<uint32_t>(kMergeThreads / N) + threadIdx.x / N;
   const int tok = static_cast<int>(item / static_cast<uint32_t>(Hq));
   const bool in = tok < clampi(io.cu_rows[io.n_requests], 0, io.n_rows);
   bool own = false;
@@ -1100,7 +1111,7 @@ __global__ void __launch_bounds__(256) k_attn_merge(const __grid_constant__ Attn
   }
   const int most = 2 * P.ctas;  // (a wrong cu_rows must not lead out of the workspace)
   const int n0 = clampi(first[0].more >> 1, 0, most), n = n0 + clampi(first[1].more >> 1, 0, most);
-  for (int a = 0; a < n; a += 32) {
+  for (int a = 0; a < n; a += N) {
     const int e = a + lane, k0 = e < n0 ? e : e - n0;
     const int kind = (e < n0 ? first[0].more : first[1].more) & 1;
     const int64_t c = (e < n0 ? first[0].carry : first[1].carry) + static_cast<int64_t>(k0 + 1) * (kind == kPair ? 256 : 128);
@@ -1110,30 +1121,30 @@ __global__ void __launch_bounds__(256) k_attn_merge(const __grid_constant__ Attn
     if (ok) mine = part[at];
     float top = mine.m;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = N / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
     top = fmaxf(top, M);
     if (top == -INFINITY) continue;
     const float old = exp2f(M - top), w = mine.m == -INFINITY ? 0.f : exp2f(mine.m - top);
     float sum = w * mine.l;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = N / 2; o; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
     L = L * old + sum;
     M = top;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= old;
-    const int cnt = min(32, n - a);
-    for (int k = 0; k < cnt; k += 8) {  // eight rows on their way at once
-      Vals<V> y[8];
-      float f[8];
+    const int cnt = min(N, n - a);
+    for (int k = 0; k < cnt; k += kAtOnce) {  // that many rows on their way at once
+      Vals<V> y[kAtOnce];
+      float f[kAtOnce];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        f[u] = __shfl_sync(0xffffffffu, w, (k + u) & 31);
-        const int64_t p = __shfl_sync(0xffffffffu, at, (k + u) & 31);
+      for (int u = 0; u < kAtOnce; ++u) {
+        f[u] = __shfl_sync(lanes, w, (k + u) & (N - 1), N);
+        const int64_t p = __shfl_sync(lanes, at, (k + u) & (N - 1), N);
         if (k + u >= cnt) f[u] = 0.f;
         y[u] = load_vals<V>(P.ws.o + p * D + lane * V);
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
+      for (int u = 0; u < kAtOnce; ++u)
         if (f[u] != 0.f)
 #pragma unroll
           for (int v = 0; v < V; ++v) acc[v] += f[u] * y[u].v[v];
@@ -1145,7 +1156,8 @@ __global__ void __launch_bounds__(256) k_attn_merge(const __grid_constant__ Attn
   for (int v = 0; v < V; v += 2) out[v >> 1] = Types<T>::pack(acc[v] * inv, acc[v + 1] * inv);
   const int hq = static_cast<int>(item) - tok * Hq;
   T* dst = static_cast<T*>(io.out) + tok * io.out_stride + hq * D + lane * V;
-  if (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[V / 2 - 1]);
+  if (V == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[V / 8], out[V / 4], out[V / 2 - 1]);
+  else if (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[V / 2 - 1]);
   else *reinterpret_cast<uint32_t*>(dst) = out[0];
   if (lane == 0 && io.lse)
     io.lse[item] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
@@ -1203,21 +1215,33 @@ mk_status encode_tmap_3d(CUtensorMap* map, int dtype, const void* base, uint64_t
 
 template <class T, int D>
 mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorMap& q64,
-                      const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+                      const CUtensorMap& k, const CUtensorMap& v, int device, cudaStream_t s) {
   constexpr int smem = sizeof(TileSmem<D>) + 1024;
-  MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_tiles<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  k_attn_tiles<T, D><<<A.ctas, kTileThreads, smem, s>>>(A, q, q64, k, v);
-  MK_CUDA_TRY(cudaGetLastError());
+  // (once per device: it takes as long as a launch)
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_tiles<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(A.io.n_rows) * A.io.n_q_heads + 7) / 8));
-  lc.blockDim = dim3(256);
-  lc.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_attn_merge<T, D>, A));
+  lc.stream = s;
+  lc.gridDim = dim3(A.ctas);
+  lc.blockDim = dim3(kTileThreads);
+  lc.dynamicSmemBytes = smem;
+  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_attn_tiles<T, D>, A, q, q64, k, v));
+  const int64_t items = static_cast<int64_t>(A.io.n_rows) * A.io.n_q_heads;
+  const int n = items > 32ll * A.ctas ? 16 : 32;
+  lc.gridDim = dim3(static_cast<unsigned>((items * n + kMergeThreads - 1) / kMergeThreads));
+  lc.blockDim = dim3(kMergeThreads);
+  lc.dynamicSmemBytes = 0;
+  if (n == 32) MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_attn_merge<T, D, 32>, A));
+  else MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_attn_merge<T, D, 16>, A));
   return MK_OK;
 }
 
@@ -1270,7 +1294,8 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   if (io->n_rows == 0) return MK_OK;
   AttnParams A;
   A.io = *io;
-  st = check_device(workspace, nullptr, &A.ctas);
+  int device = 0;
+  st = check_device(workspace, &device, &A.ctas);
   if (st != MK_OK) return st;
   if (workspace_bytes < lay_out(io, A.ctas, static_cast<uint8_t*>(workspace), &A.ws))
     return MK_ERR_INVALID_ARG;
@@ -1297,10 +1322,10 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   if (st != MK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (io->dtype == MK_BF16)
-    return io->head_dim == 128 ? launch_attn<__nv_bfloat16, 128>(A, q, q64, k, v, s)
-                               : launch_attn<__nv_bfloat16, 64>(A, q, q64, k, v, s);
-  return io->head_dim == 128 ? launch_attn<__half, 128>(A, q, q64, k, v, s)
-                             : launch_attn<__half, 64>(A, q, q64, k, v, s);
+    return io->head_dim == 128 ? launch_attn<__nv_bfloat16, 128>(A, q, q64, k, v, device, s)
+                               : launch_attn<__nv_bfloat16, 64>(A, q, q64, k, v, device, s);
+  return io->head_dim == 128 ? launch_attn<__half, 128>(A, q, q64, k, v, device, s)
+                             : launch_attn<__half, 64>(A, q, q64, k, v, device, s);
 }
 
 mk_status mk_prefix_attn_status(const void* workspace) {

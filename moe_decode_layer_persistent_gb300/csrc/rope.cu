@@ -26,8 +26,6 @@ namespace mk {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-
 struct RopeParams {
   mk_rope_io io;
   int32_t d, rot;
@@ -81,14 +79,17 @@ MK_DEV void turn_piece(Piece& x, int j, const float2* cs) {
 }
 
 // One row per CTA: the row's cosines and sines once, in shared memory, then every
-// head's pieces, kPieces per thread at a time.  The first ones are on their way
-// while the angles are being made, so that a CTA's life is one trip to memory and
-// back; HBM bounds it with many rows (403 MB of a 16,384-row prompt, half layout,
-// 32 + 2 x 8 heads of 128: @PROMPT@), the launch with few (16 rows: @VERIFY@).
-template <class T, int LAYOUT>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeParams P) {
+// head's pieces, one per thread at a time.  The first ones are on their way while
+// the angles are being made, so that a CTA's life is one trip to memory and back.
+// HBM bounds it with many rows: 128 threads per CTA and 32 registers leave room for
+// 16 rows per SM (403 MB of a 16,384-row prompt, half layout, 32 + 2 x 8 heads of
+// 128: 63.5 us, 6.3 TB/s; with 256 threads and two pieces at a time 72 us).  With
+// few rows the launch does: there 256 threads take each (16 such rows: 2.7 us; with
+// 128 threads 3.4 us).
+template <class T, int LAYOUT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS)
+    k_rope(const __grid_constant__ RopeParams P) {
   const mk_rope_io& io = P.io;
-  constexpr int kPieces = 2;
   __shared__ float2 cs[128];
   const int64_t row = blockIdx.x;
   const int d = P.d, rot = P.rot;
@@ -103,16 +104,11 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ R
   const uint32_t nq = io.n_q_heads * pieces, nk = io.n_kv_heads * pieces;
   const uint32_t n = nq + nk + (io.v ? io.n_kv_heads * (d / 8) : 0);
   const int64_t cache_row = slot * (static_cast<int64_t>(io.n_kv_heads) * d);
-  for (uint32_t t0 = threadIdx.x; t0 == threadIdx.x || t0 < n; t0 += kPieces * kRopeThreads) {
-    Piece x[kPieces];
-    T* dst[kPieces];
-    int j[kPieces];  // piece that turns; -1: passes
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const uint32_t t = t0 + i * kRopeThreads;
-      dst[i] = nullptr;
-      j[i] = -1;
-      if (t >= n) continue;
+  for (uint32_t t = threadIdx.x; t == threadIdx.x || t < n; t += THREADS) {
+    Piece x;
+    T* dst = nullptr;
+    int j = -1;  // piece that turns; -1: passes
+    if (t < n) {
       const T* src;
       if (t < nq + nk) {
         const bool q = t < nq;
@@ -123,18 +119,18 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ R
                   : static_cast<T*>(io.k_cache) + cache_row;
         const uint32_t at = head * d + (p < turned ? p * 8 : rot + (p - turned) * 8);
         src += at;
-        if (q || slot >= 0) dst[i] = to + at;
-        if (p < turned) j[i] = static_cast<int>(p);
+        if (q || slot >= 0) dst = to + at;
+        if (p < turned) j = static_cast<int>(p);
       } else {
         const uint32_t at = (t - nq - nk) * 8;
         src = static_cast<const T*>(io.v) + row * io.v_stride + at;
-        if (slot >= 0) dst[i] = static_cast<T*>(io.v_cache) + cache_row + at;
+        if (slot >= 0) dst = static_cast<T*>(io.v_cache) + cache_row + at;
       }
-      x[i].a = *reinterpret_cast<const uint4*>(src);
-      if (LAYOUT == MK_ROPE_HALF && j[i] >= 0) x[i].b = *reinterpret_cast<const uint4*>(src + rot / 2);
+      x.a = __ldcs(reinterpret_cast<const uint4*>(src));
+      if (LAYOUT == MK_ROPE_HALF && j >= 0) x.b = __ldcs(reinterpret_cast<const uint4*>(src + rot / 2));
     }
-    if (t0 == threadIdx.x) {
-      for (int i = threadIdx.x; i < rot / 2; i += kRopeThreads) {
+    if (t == threadIdx.x) {
+      for (int i = threadIdx.x; i < rot / 2; i += THREADS) {
         const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[i];
         const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
         float s, c;
@@ -143,24 +139,19 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ R
       }
       __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      if (!dst[i]) continue;
-      if (j[i] >= 0) {
-        turn_piece<T, LAYOUT>(x[i], j[i], cs);
-        if (LAYOUT == MK_ROPE_HALF) *reinterpret_cast<uint4*>(dst[i] + rot / 2) = x[i].b;
-      }
-      *reinterpret_cast<uint4*>(dst[i]) = x[i].a;
+    if (!dst) continue;
+    if (j >= 0) {
+      turn_piece<T, LAYOUT>(x, j, cs);
+      if (LAYOUT == MK_ROPE_HALF) *reinterpret_cast<uint4*>(dst + rot / 2) = x.b;
     }
+    *reinterpret_cast<uint4*>(dst) = x.a;
   }
 }
 
-template <class T>
-void launch_rope(int layout, const RopeParams& P, cudaStream_t s) {
-  if (layout == MK_ROPE_HALF)
-    k_rope<T, MK_ROPE_HALF><<<P.io.n_rows, kRopeThreads, 0, s>>>(P);
-  else
-    k_rope<T, MK_ROPE_INTERLEAVED><<<P.io.n_rows, kRopeThreads, 0, s>>>(P);
+template <class T, int LAYOUT>
+void launch_rope(const RopeParams& P, int sms, cudaStream_t s) {
+  if (P.io.n_rows < 4 * sms) k_rope<T, LAYOUT, 256><<<P.io.n_rows, 256, 0, s>>>(P);
+  else k_rope<T, LAYOUT, 128><<<P.io.n_rows, 128, 0, s>>>(P);
 }
 
 }  // namespace
@@ -251,7 +242,8 @@ mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream)
       return MK_ERR_INVALID_ARG;
   }
   if (n == 0) return MK_OK;
-  mk_status st = check_device(io->positions, nullptr, nullptr);
+  int sms = 0;
+  mk_status st = check_device(io->positions, nullptr, &sms);
   if (st != MK_OK) return st;
   RopeParams P;
   P.io = *io;
@@ -260,8 +252,14 @@ mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream)
   P.m = rope->m;
   std::copy(rope->turns, rope->turns + 128, P.turns);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (io->dtype == MK_BF16) launch_rope<__nv_bfloat16>(rope->cfg.layout, P, s);
-  else launch_rope<__half>(rope->cfg.layout, P, s);
+  const bool half = rope->cfg.layout == MK_ROPE_HALF;
+  if (io->dtype == MK_BF16) {
+    if (half) launch_rope<__nv_bfloat16, MK_ROPE_HALF>(P, sms, s);
+    else launch_rope<__nv_bfloat16, MK_ROPE_INTERLEAVED>(P, sms, s);
+  } else {
+    if (half) launch_rope<__half, MK_ROPE_HALF>(P, sms, s);
+    else launch_rope<__half, MK_ROPE_INTERLEAVED>(P, sms, s);
+  }
   MK_CUDA_TRY(cudaGetLastError());
   return MK_OK;
 }
