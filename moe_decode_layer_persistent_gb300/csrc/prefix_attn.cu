@@ -5,7 +5,7 @@
 // one matrix Q against the prefix, and each request's rows one against its own
 // keys.  Both are the same computation on a row tile (up to 128 rows) and a
 // range of 128-key tiles, with running maximum m and sum l (log2 units):
-//   S = Q K^T,  m' = max(m, rowmax S),  P = 2^(S - m'),
+//   S = Q K^T,  m' >= m near the maximum so far,  P = 2^(S - m'),
 //   l' = l 2^(m - m') + rowsum P,  O' = O 2^(m - m') + P V.
 // Each stretch of key tiles leaves (O, m, l); the second kernel joins a row's
 // stretches: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
@@ -51,7 +51,7 @@ MK_DEV constexpr int item_over(int kind) { return kind == kPair ? 24 : 12; }
 constexpr int kTileKeys = 128;
 constexpr int kFifo = 4;            // pieces handed out ahead
 constexpr int kTileThreads = 384;
-constexpr float kGrow = 8.f;        // the maximum may lag by 2^8 before O is rescaled
+constexpr float kMost = 16384.f;    // a row's sum of P over a tile, in units of 2^m, at most
 constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
 
 // How the lines are laid out (every CTA of k_attn_tiles works it out for itself).
@@ -708,7 +708,7 @@ MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParit
       const Place sv = at.next(V.stages), sk = sv.next(V.stages);
       const bool more = j + 1 < n;
       if (!wait_stage(sv) || (more && !wait_stage(sk))) return false;
-      if (!wait_warp(c, &S.p_full[slot], par.p) || !my_turn()) return false;
+      if (!my_turn() || !wait_warp(c, &S.p_full[slot], par.p)) return false;
       par.p ^= 1;
       tc_fence_after();
       const uint64_t vd = sdesc_mnmajor_sw128(kv + sv.st * TileSmem<D>::kTile, 128 * 128);
@@ -815,80 +815,94 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
           if (j == n - 1) mbar_arrive(&R.q_empty[kind == kPair ? slot : 0]);
         }
       }
-      float s[kTileKeys];
       if (warp_valid) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s + 32 * q);
-        tmem_ld_wait();
-        const bool edge = klo > k0 || khi < k0 + kTileKeys || tree_at < k0 + kTileKeys || j < 0;
-        if (__any_sync(0xffffffffu, edge)) {
-          const int lo = klo - k0, hi = khi - k0, tb = tree_at - k0;
-#pragma unroll
-          for (int q = 0; q < kTileKeys / 32; ++q) {
-            // bit i: key k0 + 32 q + i is seen
-            uint32_t see = below(hi - 32 * q) & ~below(lo - 32 * q);
-            const int off = tb - 32 * q;
-            if (off < 32)
-              see &= below(off) | (off >= 0 ? static_cast<uint32_t>(tree) << off
-                                   : off > -64 ? static_cast<uint32_t>(tree >> -off) : 0u);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(see & (1u << i))) s[32 * q + i] = -INFINITY;
-          }
-        }
-        float t4[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) t4[y] = max3(s[y], s[y + 4], s[y + 8]);
-#pragma unroll
-        for (int x = 12; x < kTileKeys - 4; x += 8)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) t4[y] = max3(t4[y], s[x + y], s[x + y + 4]);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) t4[y] = fmaxf(t4[y], s[kTileKeys - 4 + y]);
-        const float top = sl2 * fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-        // rescale only when the maximum has grown by 2^8: until then P is at most
-        // 2^8, which its types and the 32-bit sums hold without loss
-        const bool grow = valid && top > m + kGrow;
-        if (j <= 0) {
-          m = top;
-          l = 0.f;
-        } else if (__any_sync(0xffffffffu, grow)) {
-          const float x = grow ? exp2_approx(m - top) : 1.f;
-          if (grow) m = top;
-          l *= x;
+        // P = 2^(S - m), with the m of the tiles before as long as the row's sum
+        // stays below 2^14 (which the weights' types and the 32-bit sums hold
+        // without loss): the maximum itself is looked for only in a piece's first
+        // tile and where that fails, in a second pass over the scores (they lie in
+        // tensor memory until P is stored).  Taking it in every tile is 0.19 us of
+        // the 1.6 that a tile takes.
+        bool look = j <= 0 || __any_sync(0xffffffffu, valid && m == -INFINITY);
+        uint32_t p[kTileKeys / 2];
+        float total;
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            float o[32];
-            tmem_ld32(to + 32 * q, o);
-            tmem_ld_wait();
+        while (true) {
+          float s[kTileKeys];
 #pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] *= x;
-            tmem_st32(to + 32 * q, reinterpret_cast<uint32_t*>(o));
+          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s + 32 * q);
+          tmem_ld_wait();
+          const bool edge = klo > k0 || khi < k0 + kTileKeys || tree_at < k0 + kTileKeys || j < 0;
+          if (__any_sync(0xffffffffu, edge)) {
+            const int lo = klo - k0, hi = khi - k0, tb = tree_at - k0;
+#pragma unroll
+            for (int q = 0; q < kTileKeys / 32; ++q) {
+              // bit i: key k0 + 32 q + i is seen
+              uint32_t see = below(hi - 32 * q) & ~below(lo - 32 * q);
+              const int off = tb - 32 * q;
+              if (off < 32)
+                see &= below(off) | (off >= 0 ? static_cast<uint32_t>(tree) << off
+                                     : off > -64 ? static_cast<uint32_t>(tree >> -off) : 0u);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(see & (1u << i))) s[32 * q + i] = -INFINITY;
+            }
           }
-        }
-      }
-      // P = 2^(S - m)
-      if (warp_valid) {
-        const float ms = m == -INFINITY ? 0.f : m;
-        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          if (look) {
+            float t4[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t p[kTileKeys / 4];
+            for (int y = 0; y < 4; ++y) t4[y] = max3(s[y], s[y + 4], s[y + 8]);
 #pragma unroll
-          for (int x = 0; x < kTileKeys / 2; x += 2) {
-            float2 y = fma2(make_float2(s[64 * q + x], s[64 * q + x + 1]), make_float2(sl2, sl2),
-                            make_float2(-ms, -ms));
+            for (int x = 12; x < kTileKeys - 4; x += 8)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) t4[y] = max3(t4[y], s[x + y], s[x + y + 4]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) t4[y] = fmaxf(t4[y], s[kTileKeys - 4 + y]);
+            const float top = sl2 * fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+            if (j <= 0) {
+              m = top;
+              l = 0.f;
+            } else {
+              const bool grow = valid && top > m;
+              const float x = grow ? exp2_approx(m - top) : 1.f;
+              if (grow) m = top;
+              l *= x;
+              if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                  float o[32];
+                  tmem_ld32(to + 32 * q, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int y = 0; y < 32; ++y) o[y] *= x;
+                  tmem_st32(to + 32 * q, reinterpret_cast<uint32_t*>(o));
+                }
+              }
+            }
+          }
+          const float ms = m == -INFINITY ? 0.f : m;
+          float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+          for (int x = 0; x < kTileKeys; x += 2) {
+            float2 y = fma2(make_float2(s[x], s[x + 1]), make_float2(sl2, sl2), make_float2(-ms, -ms));
             y.x = exp2_approx(y.x);
             y.y = exp2_approx(y.y);
             sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], y);
             p[x >> 1] = Types<T>::pack(y.x, y.y);
           }
-          if (j >= 0) tmem_st32(ts + 32 * q, p);
-          else par.cold += p[0] == 1u && p[31] == 1u;  // (keeps the work)
+          const float2 both = add2(sum[0], sum[1]);
+          total = both.x + both.y;
+          // (the comparison is false for NaN)
+          if (look || !__any_sync(0xffffffffu, valid && !(total <= kMost))) break;
+          look = true;
         }
-        const float2 all = add2(sum[0], sum[1]);
-        l += all.x + all.y;
-        tmem_st_wait();
+        l += total;
+        if (j >= 0) {
+          tmem_st32(ts, p);
+          tmem_st32(ts + 32, p + 32);
+          tmem_st_wait();
+        } else {
+          par.cold += p[0] == 1u && p[63] == 1u;  // (keeps the work)
+        }
       }
       if (j >= 0) {
         tc_fence_before();
