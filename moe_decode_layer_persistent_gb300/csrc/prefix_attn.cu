@@ -52,7 +52,9 @@ constexpr int kTileKeys = 128;
 constexpr int kFifo = 4;            // pieces handed out ahead
 constexpr int kTileThreads = 384;
 constexpr float kMost = 16384.f;    // a row's sum of P over a tile, in units of 2^m, at most
-constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
+// Limits of the waits: for a hand-off, and for what may take as long as a CTA's
+// whole work (a wait that runs out ends that work, too).
+constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000, kLongWaitNs = 100 * kWaitNs;
 
 // How the lines are laid out (every CTA of k_attn_tiles works it out for itself).
 struct Plan {
@@ -244,7 +246,7 @@ struct View {
 
 // Bounded waits: false once any wait of the CTA has run out.  The clock is read
 // now and then only: reading it takes longer than a hand-off.
-MK_DEV bool wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity) {
+MK_DEV bool wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity, uint64_t limit) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   while (true) {
@@ -252,15 +254,15 @@ MK_DEV bool wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity) {
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*c.abort) return false;
-    if (globaltimer() - t0 > kWaitNs) {
+    if (globaltimer() - t0 > limit) {
       *c.abort = 1;
       atomicExch(c.status, 1u);
       return false;
     }
   }
 }
-MK_DEV bool wait_warp(const Ctx& c, uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_bar(c, bar, parity));
+MK_DEV bool wait_warp(const Ctx& c, uint64_t* bar, uint32_t parity, uint64_t limit = kWaitNs) {
+  return __all_sync(0xffffffffu, wait_bar(c, bar, parity, limit));
 }
 
 MK_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -563,7 +565,8 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   };
   auto push = [&](const Piece& w) -> bool {
     const int k = n_out % kFifo;
-    if (n_out >= kFifo && !wait_warp(c, &R.fifo_empty[k], ((n_out / kFifo) - 1) & 1)) return false;
+    if (n_out >= kFifo && !wait_warp(c, &R.fifo_empty[k], ((n_out / kFifo) - 1) & 1, kLongWaitNs))
+      return false;
     if (lane == 0) {
       R.fifo[k] = w;
       mbar_arrive(&R.fifo_full[k]);
@@ -576,7 +579,7 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   // registers are short here)
   auto load_piece = [&](const volatile Piece& w, int pages) -> bool {
     // the buffers belong to the other kind of work until its MMAs are done
-    if (!ready && !wait_warp(c, after, 0)) return false;
+    if (!ready && !wait_warp(c, after, 0, kLongWaitNs)) return false;
     ready = true;
     const int n = w.kt_b - w.kt_a;
     int ahead = n > group_tiles ? fetch(w, 1) : -1, old = -1, group = 0;
@@ -1290,7 +1293,7 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
       io->table_stride < io->max_pages || io->window < 0)
     return MK_ERR_INVALID_ARG;
   if (cap + io->prefix_len > INT32_MAX - 256) return MK_ERR_INVALID_ARG;
-  if (!(io->scale >= 0.f && io->scale <= FLT_MAX)) return MK_ERR_INVALID_ARG;
+  if (!(io->scale >= 0.f && io->scale <= FLT_MAX / 2)) return MK_ERR_INVALID_ARG;
   if (io->tree_mask && io->window > 0 && io->window < 64) return MK_ERR_UNSUPPORTED;
   if (!io->lens || !io->cu_rows || !workspace) return MK_ERR_INVALID_ARG;
   if (io->max_pages && !io->block_table) return MK_ERR_INVALID_ARG;
@@ -1305,7 +1308,6 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
       misaligned(io->cu_rows, 4) || misaligned(io->block_table, 4) ||
       misaligned(io->prefix_pages, 4) || misaligned(io->tree_mask, 8) || misaligned(io->lse, 4))
     return MK_ERR_INVALID_ARG;
-  if (io->n_rows == 0) return MK_OK;
   AttnParams A;
   A.io = *io;
   int device = 0;
@@ -1313,6 +1315,10 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   if (st != MK_OK) return st;
   if (workspace_bytes < lay_out(io, A.ctas, static_cast<uint8_t*>(workspace), &A.ws))
     return MK_ERR_INVALID_ARG;
+  if (io->n_rows == 0) {
+    MK_CUDA_TRY(cudaMemsetAsync(A.ws.status, 0, sizeof(uint32_t), static_cast<cudaStream_t>(stream)));
+    return MK_OK;
+  }
   const float scale = io->scale != 0.f ? io->scale : 1.f / std::sqrt(static_cast<float>(io->head_dim));
   A.scale_log2 = scale * 1.4426950408889634f;
   A.group = io->n_q_heads / io->n_kv_heads;

@@ -137,7 +137,7 @@ def attn(mk, io, workspace=16 * A, size=1 << 40):
     (dict(table_stride=7), INVALID), (dict(max_pages=1 << 27, table_stride=1 << 27), INVALID),
     (dict(window=-1), INVALID), (dict(window=63, tree_mask=10 * A), UNSUPPORTED),
     (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
-    (dict(scale=float("inf")), INVALID), (dict(q=0), INVALID), (dict(out=0), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(scale=3e38), INVALID), (dict(q=0), INVALID), (dict(out=0), INVALID),
     (dict(out=A), INVALID), (dict(k_cache=0), INVALID), (dict(v_cache=0), INVALID),
     (dict(lens=0), INVALID), (dict(cu_rows=0), INVALID), (dict(block_table=0), INVALID),
     (dict(prefix_pages=0), INVALID), (dict(q_stride=1020), INVALID), (dict(q_stride=1016), INVALID),

@@ -359,7 +359,7 @@ def check_attn(mk, a, scale=None):
     assert np.all(err <= tol), ("out", (err / np.maximum(tol, 1e-300)).max())
     empty = np.isinf(lse)
     assert np.array_equal(np.isinf(got_lse), empty) and np.all(got_lse[empty] < 0)
-    e = np.abs(got_lse - lse)[~empty]
+    e = np.abs(got_lse[~empty] - lse[~empty])
     assert np.all(e <= e_s + (keys + 64) * V + 4 * V * np.abs(lse[~empty])), ("lse", e.max())
     # rows behind the last request and the values beside out are left as they were
     assert bool((a["whole"][n:] == CANARY).all()) and bool((a["whole"][:, a["hq"]:] == CANARY).all())
@@ -395,6 +395,13 @@ ATTN = {
     "large_scores": ([100, 60], [4, 4], 400, 8, 2, 128, "bf16", 16, dict(q_scale=6.0, ramp=4.0)),
     "large_scores_fp16": ([100, 60], [4, 4], 400, 8, 2, 64, "fp16", 16, dict(q_scale=6.0, ramp=4.0)),
     "many_requests": ([(7 * i) % 90 + 1 for i in range(300)], [1] * 300, 90, 4, 1, 64, "bf16", 16, {}),
+    "many_items": ([(3 * i) % 11 + 1 for i in range(300)], [1] * 300, 3, 32, 8, 64, "bf16", 16, {}),
+    "many_items_128": ([(3 * i) % 7 + 1 for i in range(160)], [1] * 160, 2, 32, 4, 128, "fp16", 16, {}),
+    "requests_900": ([(5 * i) % 200 + 1 for i in range(900)], [i % 3 for i in range(900)], 40, 2, 1, 64,
+                     "bf16", 16, {}),
+    "rows_65": ([70, 40], [33, 1], 300, 2, 1, 128, "bf16", 16, {}),
+    "rows_64_65_128_129": ([40, 41, 70, 90], [32, 33, 64, 65], 0, 2, 1, 64, "bf16", 16, {}),
+    "prefix_in_many_pieces": ([3, 2], [3, 2], 6000, 4, 2, 64, "bf16", 64, {}),
     "long": ([1500, 40, 700], [2, 2, 1], 2100, 4, 1, 128, "bf16", 1024, {}),
 }
 
@@ -444,6 +451,53 @@ def test_prefix_attn_workspace_too_small(cuda_lib):
     with pytest.raises(cuda_lib.MkError) as e:
         cuda_lib.mk_prefix_attn(a["io"], a["workspace"][:-1])
     assert e.value.status == 1
+
+
+def test_prefix_attn_no_rows(cuda_lib):
+    """Nothing to attend to: outputs stay, the status is that of a call."""
+    a = make_attn(np.random.default_rng(5), [30], [0], 40, 4, 1, 64, "bf16", 16, extra_rows=0)
+    a["q"] = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    a["hq"] = 4
+    io = cuda_lib.make_prefix_attn_io(a["q"], a["k"], a["v"], torch.empty_like(a["q"]), dev([30]), dev([0, 0]),
+                                      dev(a["table"]), dev(a["prefix_pages"]), 40)
+    ws = torch.full((cuda_lib.mk_prefix_attn_workspace(io),), 0xFF, dtype=torch.uint8, device="cuda")
+    cuda_lib.mk_prefix_attn(io, ws)
+    torch.cuda.synchronize()
+    assert cuda_lib.mk_prefix_attn_status(ws) == 0
+
+
+def test_prefix_attn_far_pages(cuda_lib):
+    """Slots whose byte offset passes 32 bits: a pool of 4.6 GB per cache, keys at
+    its end."""
+    rng = np.random.default_rng(6)
+    a = make_attn(rng, [100, 17], [2, 1], 70, 4, 2, 128, "bf16", 64)
+    pages = 140000
+    big = {}
+    for name in ("k", "v"):
+        pool = torch.zeros(pages, 64, 2, 128, dtype=torch.bfloat16, device="cuda")
+        pool[-a[name].shape[0]:] = a[name]
+        big[name] = pool
+    shift = pages - a["k"].shape[0]
+    far = dict(a, k=big["k"], v=big["v"], table=np.where(a["table"] < a["k"].shape[0], a["table"] + shift, -1),
+               prefix_pages=a["prefix_pages"] + shift)
+    call_attn(cuda_lib, a)
+    call_attn(cuda_lib, far)
+    check_attn(cuda_lib, a)
+    assert torch.equal(far["out"][:a["n"]], a["out"][:a["n"]]) and torch.equal(far["lse"], a["lse"])
+
+
+def test_rope_far_slots(cuda_lib):
+    """Cache rows whose byte offset passes 32 bits."""
+    rope = cuda_lib.mk_rope_create(cuda_lib.make_rope_config(64))
+    pages = 140000
+    kc, vc = (torch.zeros(pages, 64, 2, 128, dtype=torch.bfloat16, device="cuda").view(pages, 64, 4, 64) for _ in range(2))
+    _, k = rounded(np.random.default_rng(7), (3, 4, 64), "bf16")
+    at = pages * 64 - 3
+    io = cuda_lib.make_rope_io(None, None, k, k, dev([0, 0, 0]), dev([at, at + 1, at + 2], torch.int64), kc, vc)
+    cuda_lib.mk_rope_apply(rope, io)
+    torch.cuda.synchronize()
+    cuda_lib.mk_rope_destroy(rope)
+    assert torch.equal(kc.view(-1, 4, 64)[-3:], k) and torch.equal(vc.view(-1, 4, 64)[-3:], k)   # position 0
 
 
 # ------------------------------------------- together, streams and graphs
