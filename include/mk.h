@@ -481,7 +481,9 @@ mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream)
  *
  * Scores and sums are held in 32 bits; the softmax weights are rounded to the
  * tensors' type before they multiply v.  Two calls on the same inputs give the
- * same bits.  lens outside 0 .. max_pages * page_size is taken as the nearer
+ * same bits.  Work is planned in 32 bits: MK_ERR_UNSUPPORTED where n_kv_heads *
+ * (n_rows / (256 / group) + n_requests) * (128-key tiles of prefix and table
+ * together) comes to 2^29 or more.  lens outside 0 .. max_pages * page_size is taken as the nearer
  * end, cu_rows is taken as rising within 0 .. n_rows, and a page outside
  * 0 .. n_pages-1 reads as zeros. */
 typedef struct mk_prefix_attn_io {

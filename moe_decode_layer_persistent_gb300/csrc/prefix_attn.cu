@@ -43,10 +43,9 @@ namespace {
 constexpr int kPair = 0, kSolo = 1;  // the two kinds of work
 // Time of a key tile, and what an item (a row set's tile or pair of tiles and a
 // KV head) takes on top of its key tiles: filling the pipeline and writing the
-// result.  In units of about 0.2 us.
-constexpr int kMaxTileCost = 10;
-MK_DEV constexpr int tile_cost(int kind) { return kind == kPair ? 8 : 10; }
-MK_DEV constexpr int item_over(int kind) { return kind == kPair ? 24 : 12; }
+// result.  In units of about 0.2 us (of 0.4, 0.8 or 1.6 us in calls so large that
+// the lines would not fit into 32 bits).
+constexpr int kTileCost[2] = {8, 10}, kItemCost[2] = {24, 12};
 
 constexpr int kTileKeys = 128;
 constexpr int kFifo = 4;            // pieces handed out ahead
@@ -58,30 +57,30 @@ constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000, kLongWaitNs = 100 * kWaitNs;
 
 // How the lines are laid out (every CTA of k_attn_tiles works it out for itself).
 struct Plan {
-  int64_t total[2];        // of each line
-  int64_t share;           // T
-  int64_t prefix_cost[2];  // the prefix items come first
+  int32_t total[2];        // of each line
+  int32_t share;           // T
+  int32_t prefix_cost[2];  // the prefix items come first
   int32_t n_used;          // rows in use
   int32_t kt0, kt1;        // key tiles of the prefix that some row sees
   int32_t lo;              // first prefix key that some row sees
   // The solos start in CTA solo_cta, whose slots have solo_len of them each; of
   // the CTAs behind it each slot has `share`.
   int32_t solo_cta;
-  int64_t solo_len;
-  MK_DEV int64_t begin(int kind, int slot) const {
+  int32_t solo_len;
+  MK_DEV int32_t begin(int kind, int slot) const {
     const int c = static_cast<int>(blockIdx.x);
     if (kind == kPair) return c * share;
     if (c <= solo_cta) return c < solo_cta ? total[kSolo] : slot * solo_len;
-    return 2 * solo_len + (2ll * (c - solo_cta - 1) + slot) * share;
+    return 2 * solo_len + (2 * (c - solo_cta - 1) + slot) * share;
   }
-  MK_DEV int64_t length(int kind) const {
+  MK_DEV int32_t length(int kind) const {
     return kind == kSolo && static_cast<int>(blockIdx.x) == solo_cta ? solo_len : share;
   }
   // The owner (CTA of pairs, slot of solos) of a place on a line, counted from
   // the line's first.
-  MK_DEV int owner(int kind, int64_t at) const {
-    if (kind == kPair) return static_cast<int>(at / share);
-    return at < 2 * solo_len ? at >= solo_len : 2 + static_cast<int>((at - 2 * solo_len) / share);
+  MK_DEV int owner(int kind, int32_t at) const {
+    if (kind == kPair) return at / share;
+    return at < 2 * solo_len ? at >= solo_len : 2 + (at - 2 * solo_len) / share;
   }
 };
 
@@ -114,6 +113,7 @@ struct AttnParams {
   int32_t box;       // keys per TMA box: min(page_size, 128)
   int32_t page_shift;
   int32_t ctas;
+  int32_t tile_cost[2], item_cost[2];  // kTileCost, kItemCost in this call's units
   Space ws;
 };
 
@@ -149,12 +149,12 @@ MK_DEV int items_of(const AttnParams& P, int kind, int n) {
   const int full = n / (2 * P.tile_tok), left = n - full * 2 * P.tile_tok;
   return kind == kPair ? full + (left > P.half_tok) : left > 0 && left <= P.half_tok;
 }
-MK_DEV int64_t item_cost(int kind, int kt) {
-  return item_over(kind) + static_cast<int64_t>(kt) * tile_cost(kind);
+MK_DEV int32_t item_cost(const AttnParams& P, int kind, int kt) {
+  return P.item_cost[kind] + kt * P.tile_cost[kind];
 }
 // Cost of all of a row set's items against kt key tiles.
-MK_DEV int64_t set_cost(const AttnParams& P, int kind, int n, int kt) {
-  return kt > 0 ? items_of(P, kind, n) * item_cost(kind, kt) * P.io.n_kv_heads : 0;
+MK_DEV int32_t set_cost(const AttnParams& P, int kind, int n, int kt) {
+  return kt > 0 ? items_of(P, kind, n) * item_cost(P, kind, kt) * P.io.n_kv_heads : 0;
 }
 
 // ------------------------------------------------------------------ tiles
@@ -211,11 +211,11 @@ struct alignas(1024) TileSmem {
   uint64_t turn;     // both slots' MMAs of the first kind of work are done
   uint64_t drained[2];
   Plan plan;
-  int64_t sum[2][kTileThreads / 32];
+  int32_t sum[2][kTileThreads / 32];
   int32_t low[kTileThreads / 32];
   // the first request with work on a line's stretch and where it starts: the
   // CTA's of pairs, the two slots' of solos
-  int64_t first_at[3];
+  int32_t first_at[3];
   int32_t first[3];
   uint32_t tmem;
   uint32_t abort;
@@ -390,7 +390,7 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   const int B = io.n_requests, lane = lane_id(), warp = threadIdx.x >> 5;
   const int each = ceil_div(B, kTileThreads), b0 = threadIdx.x * each, b1 = min(B, b0 + each);
   const int n_used = clampi(io.cu_rows[B], 0, io.n_rows);
-  int64_t mine[2] = {0, 0};
+  int32_t mine[2] = {0, 0};
   int low = INT_MAX;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
@@ -398,12 +398,12 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
     for (int k = 0; k < 2; ++k) mine[k] += set_cost(P, k, r.n, r.kt1 - r.kt0);
     if (r.n) low = min(low, r.base);
   }
-  int64_t v[2] = {mine[0], mine[1]};
+  int32_t v[2] = {mine[0], mine[1]};
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, v[k], o);
+      const int32_t u = __shfl_up_sync(0xffffffffu, v[k], o);
       if (lane >= o) v[k] += u;
     }
   if (lane == 31) S.sum[0][warp] = v[0], S.sum[1][warp] = v[1];
@@ -412,11 +412,13 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   __syncthreads();
   Plan p;
   p.total[0] = p.total[1] = 0;
-#pragma unroll 1
+#pragma unroll
   for (int w = 0; w < kTileThreads / 32; ++w) {
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (w < warp) v[k] += S.sum[k][w];
-      p.total[k] += S.sum[k][w];
+      const int32_t x = S.sum[k][w];
+      if (w < warp) v[k] += x;
+      p.total[k] += x;
     }
     low = min(low, S.low[w]);
   }
@@ -435,11 +437,11 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   // At least one key tile each, so that every stretch inside an item has one: what
   // is left of the last pairs' CTA is used only if it holds one (the sum has room
   // for what then is not).
-  p.share = max((p.total[kPair] + (p.total[kSolo] + 1) / 2 + kMaxTileCost + P.ctas - 1) / P.ctas,
-                static_cast<int64_t>(kMaxTileCost));
-  p.solo_cta = static_cast<int>(p.total[kPair] / p.share);
+  const int32_t most = max(P.tile_cost[0], P.tile_cost[1]);
+  p.share = max((p.total[kPair] + ((p.total[kSolo] + 1) >> 1) + most + P.ctas - 1) / P.ctas, most);
+  p.solo_cta = p.total[kPair] / p.share;
   p.solo_len = (p.solo_cta + 1) * p.share - p.total[kPair];
-  if (p.solo_len < kMaxTileCost) ++p.solo_cta, p.solo_len = p.share;
+  if (p.solo_len < most) ++p.solo_cta, p.solo_len = p.share;
   if (threadIdx.x == 0) {
     S.plan = p;
     if (blockIdx.x == 0) {
@@ -451,15 +453,15 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
 #pragma unroll
   for (int j = 0; j < 3; ++j) {
     const int k = j > 0;
-    const int64_t begin = p.begin(k, j - 1);
-    int64_t here = p.prefix_cost[k] + v[k] - mine[k];
+    const int32_t begin = p.begin(k, j - 1);
+    int32_t here = p.prefix_cost[k] + v[k] - mine[k];
     if (threadIdx.x == 0 && begin < here) S.first[j] = 0, S.first_at[j] = here;
     if (begin >= here && begin < here + mine[k]) {
       int b = b0;
 #pragma unroll 1
       for (; b < b1 - 1; ++b) {
         const Req r = read_req(P, b);
-        const int64_t next = here + set_cost(P, k, r.n, r.kt1 - r.kt0);
+        const int32_t next = here + set_cost(P, k, r.n, r.kt1 - r.kt0);
         if (begin < next) break;
         here = next;
       }
@@ -472,26 +474,25 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
 // ---- a stretch of a line, piece by piece: emit(Piece) for each
 template <class Emit>
 MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int slot, int first,
-                 int64_t first_at, const Emit& emit) {
+                 int32_t first_at, const Emit& emit) {
   const mk_prefix_attn_io& io = P.io;
-  const int Hk = io.n_kv_heads, lane = lane_id(), step = tile_cost(kind);
-  const int64_t begin = plan.begin(kind, slot);
-  const int64_t end = min(plan.total[kind], begin + plan.length(kind));
+  const int Hk = io.n_kv_heads, lane = lane_id(), step = P.tile_cost[kind];
+  const int32_t begin = plan.begin(kind, slot);
+  const int32_t end = min(plan.total[kind], begin + plan.length(kind));
   if (begin >= end) return true;
   // the items of a row set of n tokens (row tile by row tile, head by head) from
   // cost `at`
-  auto items = [&](Piece& w, int64_t at, int tok, int n, int kt0, int kt1) -> bool {
+  auto items = [&](Piece& w, int32_t at, int tok, int n, int kt0, int kt1) -> bool {
     const int kt = kt1 - kt0, rows = items_of(P, kind, n), count = rows * Hk;
     if (kt <= 0 || count == 0) return true;
     const int left = n - (rows - 1) * 2 * P.tile_tok;  // of the last pair
-    const int64_t cost = item_cost(kind, kt);
-    int i = begin > at ? static_cast<int>((begin - at) / cost) : 0;
+    const int32_t cost = item_cost(P, kind, kt);
+    int i = begin > at ? (begin - at) / cost : 0;
     int p = i / Hk, h = i - p * Hk;
-    int64_t s = at + i * cost + item_over(kind);  // of the item's first key tile
+    int32_t s = at + i * cost + P.item_cost[kind];  // of the item's first key tile
     for (; i < count && s < end; ++i, s += cost) {
-      const int s0 = s >= begin ? 0 : (static_cast<int>(begin - s) + step - 1) / step;
-      const int64_t room = end - s + step - 1;
-      const int s1 = room >= static_cast<int64_t>(kt) * step ? kt : static_cast<int>(room) / step;
+      const int s0 = s >= begin ? 0 : (begin - s + step - 1) / step;
+      const int s1 = min(kt, (end - s + step - 1) / step);
       if (s0 < s1) {
         w.h = h;
         // (behind its pairs the row set's solo)
@@ -500,7 +501,7 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int slot, int 
         w.kt_a = kt0 + s0;
         w.kt_b = kt0 + s1;
         w.first = s0 == 0;
-        const int64_t last = s + static_cast<int64_t>(kt - 1) * step;
+        const int32_t last = s + (kt - 1) * step;
         w.more = last < end ? 0 : plan.owner(kind, last) - plan.owner(kind, s);
         if (!emit(w)) return false;
       }
@@ -517,7 +518,7 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int slot, int 
     if (!items(w, 0, 0, plan.n_used, plan.kt0, plan.kt1)) return false;
   }
   w.own = 1;
-  int64_t at = first_at;
+  int32_t at = first_at;
   for (int b0 = first; at < end && b0 < io.n_requests; b0 += 32) {
     // 32 requests' lengths at a time
     Req req{0, 0, 0, 0, 0, 0};
@@ -1310,6 +1311,27 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
     return MK_ERR_INVALID_ARG;
   AttnParams A;
   A.io = *io;
+  A.group = io->n_q_heads / io->n_kv_heads;
+  A.tile_tok = 128 / A.group;
+  A.half_tok = 64 / A.group;
+  // the longest that the lines of work can be, by the capacity of the tables
+  const int64_t pairs = io->n_rows / (2 * A.tile_tok) + 1;
+  const int64_t own = pairs + std::min(io->n_requests, io->n_rows);
+  const int64_t kt = (io->prefix_len + kTileKeys - 1) / kTileKeys, own_kt = (cap + kTileKeys - 1) / kTileKeys;
+  int unit = 0;
+  for (;; ++unit) {
+    int64_t t = 1, i = 1;
+    for (int k = 0; k < 2; ++k) {
+      A.tile_cost[k] = std::max(1, kTileCost[k] >> unit);
+      A.item_cost[k] = std::max(1, kItemCost[k] >> unit);
+      t = std::max<int64_t>(t, A.tile_cost[k]);
+      i = std::max<int64_t>(i, A.item_cost[k]);
+    }
+    const double most = static_cast<double>(io->n_kv_heads) *
+                        (static_cast<double>(pairs) * (kt * t + i) + static_cast<double>(own) * (own_kt * t + i));
+    if (most < 1 << 29) break;
+    if (unit == 3) return MK_ERR_UNSUPPORTED;
+  }
   int device = 0;
   st = check_device(workspace, &device, &A.ctas);
   if (st != MK_OK) return st;
@@ -1321,9 +1343,6 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   }
   const float scale = io->scale != 0.f ? io->scale : 1.f / std::sqrt(static_cast<float>(io->head_dim));
   A.scale_log2 = scale * 1.4426950408889634f;
-  A.group = io->n_q_heads / io->n_kv_heads;
-  A.tile_tok = 128 / A.group;
-  A.half_tok = 64 / A.group;
   A.box = static_cast<int>(std::min<int64_t>(P, kTileKeys));
   A.page_shift = __builtin_ctz(static_cast<uint32_t>(P));
   const uint64_t d = io->head_dim, Hq = io->n_q_heads, Hk = io->n_kv_heads;

@@ -135,6 +135,7 @@ def attn(mk, io, workspace=16 * A, size=1 << 40):
     (dict(page_size=1 << 17), UNSUPPORTED), (dict(n_pages=-1), INVALID),
     (dict(n_pages=1 << 27), INVALID), (dict(prefix_len=-1), INVALID), (dict(max_pages=-1), INVALID),
     (dict(table_stride=7), INVALID), (dict(max_pages=1 << 27, table_stride=1 << 27), INVALID),
+    (dict(n_requests=65536, n_rows=65536, max_pages=1 << 20, table_stride=1 << 20), UNSUPPORTED),
     (dict(window=-1), INVALID), (dict(window=63, tree_mask=10 * A), UNSUPPORTED),
     (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(scale=3e38), INVALID), (dict(q=0), INVALID), (dict(out=0), INVALID),
