@@ -474,8 +474,8 @@ mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream)
  * set (bits of keys that are not there are ignored);
  * and of all these, with window > 0, only keys at positions > p - window.
  *   out = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j exp(scale q.k_j).
- * A row that sees no key gets out = 0 and lse = -infinity.  Rows from
- * cu_rows[B] on are left as they are.  Keys that no row sees are never looked
+ * A row that sees no key gets out = 0 and lse = -infinity.  Rows before
+ * cu_rows[0] and from cu_rows[B] on are left as they are.  Keys that no row sees are never looked
  * at: they may hold anything.  A key that some row sees must be finite.
  * The prefix is read once for the whole batch, not once per request.
  *
@@ -483,9 +483,10 @@ mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream)
  * tensors' type before they multiply v.  Two calls on the same inputs give the
  * same bits.  Work is planned in 32 bits: MK_ERR_UNSUPPORTED where n_kv_heads *
  * (n_rows / (256 / group) + n_requests) * (128-key tiles of prefix and table
- * together) comes to 2^29 or more.  lens outside 0 .. max_pages * page_size is taken as the nearer
- * end, cu_rows is taken as rising within 0 .. n_rows, and a page outside
- * 0 .. n_pages-1 reads as zeros. */
+ * together) comes to 2^29 or more.  lens outside 0 .. max_pages * page_size
+ * and cu_rows outside 0 .. n_rows are taken as the nearer end, and a page
+ * outside 0 .. n_pages-1 reads as zeros.  A cu_rows that falls leaves out and
+ * lse undefined: see mk_prefix_attn_status. */
 typedef struct mk_prefix_attn_io {
   int32_t n_requests;          /* B, 1 .. 65536                                   */
   int32_t n_rows;              /* rows of q, >= 0                                 */
@@ -528,8 +529,8 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
                          void* stream);
 
 /* Device status of the last mk_prefix_attn that used `workspace`: MK_OK, or
- * MK_ERR_TIMEOUT if a bounded device-side wait expired (its outputs are then
- * undefined).  Reads a device word synchronously: call after synchronising. */
+ * MK_ERR_TIMEOUT if a bounded device-side wait expired, MK_ERR_INVALID_ARG if its
+ * cu_rows falls (its outputs are then undefined).  Reads a device word synchronously: call after synchronising. */
 mk_status mk_prefix_attn_status(const void* workspace);
 
 #ifdef __cplusplus

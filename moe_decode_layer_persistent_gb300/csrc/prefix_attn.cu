@@ -48,6 +48,7 @@ constexpr int kPair = 0, kSolo = 1;  // the two kinds of work
 constexpr int kTileCost[2] = {8, 10}, kItemCost[2] = {24, 12};
 
 constexpr int kTileKeys = 128;
+constexpr uint32_t kTimeout = 1, kFalling = 2;  // values of the status word
 constexpr int kFifo = 4;            // pieces handed out ahead
 constexpr int kTileThreads = 384;
 constexpr float kMost = 16384.f;    // a row's sum of P over a tile, in units of 2^m, at most
@@ -97,7 +98,7 @@ struct Partial {
 struct Space {
   uint32_t* status;  // [0] the status, [1] whether any row sees a prefix key
   Partial* part;
-  float* o;         // D values per partial row
+  float* o;          // D values per partial row
   // first partial row of each region: the prefix's and the requests' own
   // results by row and head; those of stretches that start in the middle of an
   // item, [kind][CTA][slot][128]
@@ -196,9 +197,9 @@ struct Place {
 template <int D>
 struct alignas(1024) TileSmem {
   // Row tiles and K and V tiles in flight.  Pairs: two row tiles, then kStages
-  // tiles.  Solos: for each slot its row tile of 64 rows, then kSoloStages tiles.  (A solo's MMA reads 128 rows: those behind the 64
-  // are whatever lies there, and so are the rows of the result that nobody
-  // reads.)  Three stages per slot instead of two keep a K or V tile on its way
+  // tiles.  Solos: for each slot its row tile of 64 rows, then kSoloStages tiles.
+  // (A solo's MMA reads 128 rows: those behind the 64 are whatever lies there, and
+  // so are the rows of the result that nobody reads.)  Three stages per slot instead of two keep a K or V tile on its way
   // while the two before it are in use.
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 8;
@@ -256,7 +257,7 @@ MK_DEV bool wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity, uint64_t limi
     if (*c.abort) return false;
     if (globaltimer() - t0 > limit) {
       *c.abort = 1;
-      atomicExch(c.status, 1u);
+      atomicExch(c.status, kTimeout);
       return false;
     }
   }
@@ -392,9 +393,11 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   const int n_used = clampi(io.cu_rows[B], 0, io.n_rows);
   int32_t mine[2] = {0, 0};
   int low = INT_MAX;
+  bool falls = false;  // the lines are measured for rows that belong to one request each
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const Req r = read_req(P, b);
+    falls |= io.cu_rows[b + 1] < io.cu_rows[b];
     for (int k = 0; k < 2; ++k) mine[k] += set_cost(P, k, r.n, r.kt1 - r.kt0);
     if (r.n) low = min(low, r.base);
   }
@@ -409,7 +412,7 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   if (lane == 31) S.sum[0][warp] = v[0], S.sum[1][warp] = v[1];
   low = __reduce_min_sync(0xffffffffu, low);
   if (lane == 0) S.low[warp] = low;
-  __syncthreads();
+  falls = __syncthreads_or(falls);
   Plan p;
   p.total[0] = p.total[1] = 0;
 #pragma unroll
@@ -433,6 +436,7 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   for (int k = 0; k < 2; ++k) {
     p.prefix_cost[k] = set_cost(P, k, p.n_used, p.kt1 - p.kt0);
     p.total[k] += p.prefix_cost[k];
+    if (falls) p.total[k] = 0;
   }
   // At least one key tile each, so that every stretch inside an item has one: what
   // is left of the last pairs' CTA is used only if it holds one (the sum has room
@@ -445,7 +449,7 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   if (threadIdx.x == 0) {
     S.plan = p;
     if (blockIdx.x == 0) {
-      P.ws.status[0] = 0;
+      P.ws.status[0] = falls ? kFalling : 0;
       P.ws.status[1] = p.kt1 > p.kt0;
     }
   }
@@ -758,7 +762,8 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     // this thread's row: its token, and the keys [klo, khi) it sees; of a token
     // tree, the bits of `tree` instead from key `tree_at` on
     const int tok = w.tok0 + (kind == kPair ? slot * w.split : 0) + tok_in_tile;
-    const bool valid = tok_in_tile < (kind == kPair ? (slot ? P.tile_tok : w.split) : P.half_tok) && tok < w.tok_end;
+    const int toks = kind == kSolo ? P.half_tok : slot ? P.tile_tok : w.split;
+    const bool valid = tok_in_tile < toks && tok < w.tok_end;
     int klo = w.klo, khi = w.khi, tree_at = INT_MAX;
     uint64_t tree = 0;
     if (valid) {
@@ -1092,7 +1097,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_attn_merge(const __grid_const
   const uint32_t lanes = N == 32 ? 0xffffffffu : (threadIdx.x & 16) ? 0xffff0000u : 0xffffu;
   const uint32_t item = blockIdx.x * static_cast<uint32_t>(kMergeThreads / N) + threadIdx.x / N;
   const int tok = static_cast<int>(item / static_cast<uint32_t>(Hq));
-  const bool in = tok < clampi(io.cu_rows[io.n_requests], 0, io.n_rows);
+  const bool in = tok >= io.cu_rows[0] && tok < clampi(io.cu_rows[io.n_requests], 0, io.n_rows);
   bool own = false;
   if (in) {
     int lo = 0, hi = io.n_requests;
@@ -1132,7 +1137,8 @@ __global__ void __launch_bounds__(kMergeThreads) k_attn_merge(const __grid_const
   for (int a = 0; a < n; a += N) {
     const int e = a + lane, k0 = e < n0 ? e : e - n0;
     const int kind = (e < n0 ? first[0].more : first[1].more) & 1;
-    const int64_t c = (e < n0 ? first[0].carry : first[1].carry) + static_cast<int64_t>(k0 + 1) * (kind == kPair ? 256 : 128);
+    const int64_t c = (e < n0 ? first[0].carry : first[1].carry) +
+                      static_cast<int64_t>(k0 + 1) * (kind == kPair ? 256 : 128);
     const bool ok = e < n && c >= 0 && c < 512ll * P.ctas;
     const int64_t at = P.ws.carry + (ok ? c : 0);
     Partial mine{-INFINITY, 0.f, 0, 0};
@@ -1371,7 +1377,7 @@ mk_status mk_prefix_attn_status(const void* workspace) {
   if (!workspace) return MK_ERR_INVALID_ARG;
   uint32_t s = 0;
   MK_CUDA_TRY(cudaMemcpy(&s, workspace, sizeof(s), cudaMemcpyDeviceToHost));
-  return s == 0 ? MK_OK : MK_ERR_TIMEOUT;
+  return s == 0 ? MK_OK : s == kFalling ? MK_ERR_INVALID_ARG : MK_ERR_TIMEOUT;
 }
 
 }  // extern "C"

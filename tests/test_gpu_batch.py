@@ -466,6 +466,37 @@ def test_prefix_attn_no_rows(cuda_lib):
     assert cuda_lib.mk_prefix_attn_status(ws) == 0
 
 
+def test_prefix_attn_rows_before_the_first_request(cuda_lib):
+    a = make_attn(np.random.default_rng(8), [30, 9, 40], [2, 1, 3], 100, 4, 2, 64, "bf16", 16)
+    a["cu"] = np.array([2, 2, 3, 6])
+    call_attn(cuda_lib, a)
+    b = dict(a, n=4, cu=a["cu"] - 2)
+    for name in ("q0", "whole", "out", "lse"):
+        b[name] = a[name][2:]
+    check_attn(cuda_lib, b)
+    assert bool((a["whole"][:2] == CANARY).all()) and bool((a["lse"][:2] == CANARY).all())
+
+
+@pytest.mark.parametrize("cu", [[0, 3, 1, 6], [6, 0, 6, 0], [2 ** 31 - 1, 0, -2 ** 31, 6]])
+def test_prefix_attn_falling_rows(cuda_lib, cu):
+    """Rows that would belong to several requests: the status says so, nothing
+    beside the outputs is touched, and the next call is well again."""
+    a = make_attn(np.random.default_rng(9), [30, 9, 40], [2, 1, 3], 100, 4, 2, 64, "bf16", 16)
+    right = a["cu"]
+    call_attn(cuda_lib, a)
+    size = a["workspace"].numel()
+    room = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    b = dict(a, cu=np.array(cu))
+    call_attn(cuda_lib, b, workspace=room[:size])
+    torch.cuda.synchronize()
+    assert cuda_lib.mk_prefix_attn_status(room) == 1
+    assert bool((room[size:] == 0x5A).all()) and bool((b["whole"][:, b["hq"]:] == CANARY).all())
+    assert bool((b["whole"][6:] == CANARY).all())
+    a["cu"] = right
+    call_attn(cuda_lib, a, workspace=room[:size])
+    check_attn(cuda_lib, a)
+
+
 def test_prefix_attn_far_pages(cuda_lib):
     """Slots whose byte offset passes 32 bits: a pool of 4.6 GB per cache, keys at
     its end."""
