@@ -128,12 +128,21 @@ def _code_only(text):
     return "".join(text.split())
 
 
-def kernel_source_hash(files=None):
-    """Hash of the kernel sources' code (comments and layout do not count)."""
+# sources of the batched operators, no part of the layer kernel
+BATCH_SOURCES = {"batch.h", "slots.cu", "rope.cu", "prefix_attn.cu"}
+
+
+def layer_sources():
     import glob
+    files = sorted(glob.glob(os.path.join(ROOT, "moe_decode_layer_persistent_gb300", "csrc", "*")))
+    return [f for f in files if os.path.basename(f) not in BATCH_SOURCES]
+
+
+def kernel_source_hash(files=None):
+    """Hash of the layer kernel sources' code (comments and layout do not count)."""
     import hashlib
     if files is None:
-        files = sorted(glob.glob(os.path.join(ROOT, "moe_decode_layer_persistent_gb300", "csrc", "*")))
+        files = layer_sources()
     h = hashlib.sha256()
     for f in files:
         h.update(_code_only(open(f, encoding="utf-8").read()).encode())

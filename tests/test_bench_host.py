@@ -62,6 +62,17 @@ def test_source_hash_ignores_comments_and_layout(tmp_path):
     assert h([str(a)]) != h([str(c)])
 
 
+def test_layer_sources_are_those_the_layer_is_built_from():
+    """The batched operators' sources do not decide whether a profile of the layer
+    kernel still holds, and no source of the layer includes one of them."""
+    files = bench.layer_sources()
+    names = {os.path.basename(f) for f in files}
+    assert {"layer.cu", "layer.h", "api.cu", "ptx.cuh", "quant.cuh"} <= names
+    assert not names & bench.BATCH_SOURCES
+    for f in files:
+        assert not any('#include "%s"' % b in open(f).read() for b in bench.BATCH_SOURCES)
+
+
 def test_profiled_traffic_only_for_matching_sources(tmp_path, monkeypatch):
     prof = tmp_path / "profiles"
     prof.mkdir()
