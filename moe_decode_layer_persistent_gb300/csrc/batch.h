@@ -26,4 +26,19 @@ inline int64_t span_bytes(int64_t rows, int64_t width, int64_t stride, int64_t e
 // that device is a compute-capability 10.3 GPU; its number and SM count.
 mk_status check_device(const void* p, int* device, int* sm_count);
 
+// Quotients of numbers below 2^31 by a fixed divisor: with 2^(s-1) < d <= 2^s and
+// m = floor(2^(31+s) / d) + 1, floor(x m / 2^(31+s)) = floor(x / d), since the error
+// x (m - 2^(31+s) / d) / 2^(31+s) <= x / 2^(31+s) < 1 / d.
+struct Divisor {
+  uint32_t d, m, shift;
+};
+inline Divisor make_divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t{1} << s) < d) ++s;
+  return Divisor{d, static_cast<uint32_t>((uint64_t{1} << (31 + s)) / d + 1), 31 + s};
+}
+__device__ __forceinline__ uint32_t quotient(uint32_t x, const Divisor& v) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(x) * v.m) >> v.shift);
+}
+
 }  // namespace mk

@@ -68,6 +68,7 @@ struct Plan {
   // the CTAs behind it each slot has `share`.
   int32_t solo_cta;
   int32_t solo_len;
+  int32_t first;           // kind of work that this CTA starts with
   MK_DEV int32_t begin(int kind, int slot) const {
     const int c = static_cast<int>(blockIdx.x);
     if (kind == kPair) return c * share;
@@ -77,11 +78,16 @@ struct Plan {
   MK_DEV int32_t length(int kind) const {
     return kind == kSolo && static_cast<int>(blockIdx.x) == solo_cta ? solo_len : share;
   }
-  // The owner (CTA of pairs, slot of solos) of a place on a line, counted from
-  // the line's first.
-  MK_DEV int owner(int kind, int32_t at) const {
-    if (kind == kPair) return at / share;
-    return at < 2 * solo_len ? at >= solo_len : 2 + (at - 2 * solo_len) / share;
+  // How many stretches behind this one (a CTA's of pairs, a slot's of solos) the
+  // one with a place on the line is.
+  MK_DEV int behind(int kind, int slot, int32_t at) const {
+    uint32_t past = at - begin(kind, slot);
+    if (kind == kSolo && static_cast<int>(blockIdx.x) == solo_cta) {
+      past = at - 2 * solo_len;  // (from the next CTA on, or negative)
+      if (at < 2 * solo_len) return at >= solo_len && slot == 0;
+      return 2 - slot + past / share;
+    }
+    return past / share;
   }
 };
 
@@ -111,10 +117,13 @@ struct AttnParams {
   int32_t group;     // G: q heads per KV head
   int32_t tile_tok;  // tokens per row tile: floor(128 / G)
   int32_t half_tok;  // tokens per solo: floor(64 / G)
-  int32_t box;       // keys per TMA box: min(page_size, 128)
+  int32_t box, box_shift;  // keys per TMA box: min(page_size, 128) = 128 >> box_shift
   int32_t page_shift;
   int32_t ctas;
   int32_t tile_cost[2], item_cost[2];  // kTileCost, kItemCost in this call's units
+  // quotients without divisions, whose code, run for the first time at a CTA's
+  // start, delays its first loads
+  Divisor by_pair, by_heads, by_ctas, by_cost[2];
   Space ws;
 };
 
@@ -147,7 +156,7 @@ MK_DEV Req read_req(const AttnParams& P, int b) {
 // Items of a row set of n tokens for one head: pairs of row tiles, the last one
 // of what is left if that is more than 64 rows; a solo of what is left otherwise.
 MK_DEV int items_of(const AttnParams& P, int kind, int n) {
-  const int full = n / (2 * P.tile_tok), left = n - full * 2 * P.tile_tok;
+  const int full = quotient(n, P.by_pair), left = n - full * 2 * P.tile_tok;
   return kind == kPair ? full + (left > P.half_tok) : left > 0 && left <= P.half_tok;
 }
 MK_DEV int32_t item_cost(const AttnParams& P, int kind, int kt) {
@@ -414,17 +423,14 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   if (lane == 0) S.low[warp] = low;
   falls = __syncthreads_or(falls);
   Plan p;
-  p.total[0] = p.total[1] = 0;
+  const bool some = lane < kTileThreads / 32;  // a lane per warp
 #pragma unroll
-  for (int w = 0; w < kTileThreads / 32; ++w) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int32_t x = S.sum[k][w];
-      if (w < warp) v[k] += x;
-      p.total[k] += x;
-    }
-    low = min(low, S.low[w]);
+  for (int k = 0; k < 2; ++k) {
+    const int32_t x = some ? S.sum[k][lane] : 0;
+    v[k] += __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+    p.total[k] = __reduce_add_sync(0xffffffffu, x);
   }
+  low = __reduce_min_sync(0xffffffffu, some ? S.low[lane] : INT_MAX);
   // the lowest position of any row decides where the prefix starts to be seen
   const int64_t lo64 =
       io.window && low != INT_MAX ? static_cast<int64_t>(io.prefix_len) + low - io.window + 1 : 0;
@@ -442,10 +448,11 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   // is left of the last pairs' CTA is used only if it holds one (the sum has room
   // for what then is not).
   const int32_t most = max(P.tile_cost[0], P.tile_cost[1]);
-  p.share = max((p.total[kPair] + ((p.total[kSolo] + 1) >> 1) + most + P.ctas - 1) / P.ctas, most);
-  p.solo_cta = p.total[kPair] / p.share;
+  p.share = max(static_cast<int32_t>(quotient(p.total[kPair] + ((p.total[kSolo] + 1) >> 1) + most + P.ctas - 1, P.by_ctas)), most);
+  p.solo_cta = static_cast<uint32_t>(p.total[kPair]) / static_cast<uint32_t>(p.share);
   p.solo_len = (p.solo_cta + 1) * p.share - p.total[kPair];
   if (p.solo_len < most) ++p.solo_cta, p.solo_len = p.share;
+  p.first = p.begin(kPair, 0) < p.total[kPair] ? kPair : kSolo;
   if (threadIdx.x == 0) {
     S.plan = p;
     if (blockIdx.x == 0) {
@@ -454,13 +461,13 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
     }
   }
   // the requests that this CTA's stretches start in
-#pragma unroll
+#pragma unroll 1
   for (int j = 0; j < 3; ++j) {
     const int k = j > 0;
-    const int32_t begin = p.begin(k, j - 1);
-    int32_t here = p.prefix_cost[k] + v[k] - mine[k];
+    const int32_t begin = p.begin(k, j - 1), cost = k ? mine[1] : mine[0];
+    int32_t here = (k ? p.prefix_cost[1] + v[1] : p.prefix_cost[0] + v[0]) - cost;
     if (threadIdx.x == 0 && begin < here) S.first[j] = 0, S.first_at[j] = here;
-    if (begin >= here && begin < here + mine[k]) {
+    if (begin >= here && begin < here + cost) {
       int b = b0;
 #pragma unroll 1
       for (; b < b1 - 1; ++b) {
@@ -491,22 +498,22 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int slot, int 
     if (kt <= 0 || count == 0) return true;
     const int left = n - (rows - 1) * 2 * P.tile_tok;  // of the last pair
     const int32_t cost = item_cost(P, kind, kt);
-    int i = begin > at ? (begin - at) / cost : 0;
-    int p = i / Hk, h = i - p * Hk;
+    int i = begin > at ? static_cast<uint32_t>(begin - at) / static_cast<uint32_t>(cost) : 0;
+    int p = quotient(i, P.by_heads), h = i - p * Hk;
     int32_t s = at + i * cost + P.item_cost[kind];  // of the item's first key tile
     for (; i < count && s < end; ++i, s += cost) {
-      const int s0 = s >= begin ? 0 : (begin - s + step - 1) / step;
-      const int s1 = min(kt, (end - s + step - 1) / step);
+      const int s0 = s >= begin ? 0 : quotient(begin - s + step - 1, P.by_cost[kind]);
+      const int s1 = min(kt, static_cast<int>(quotient(end - s + step - 1, P.by_cost[kind])));
       if (s0 < s1) {
         w.h = h;
         // (behind its pairs the row set's solo)
-        w.tok0 = tok + 2 * P.tile_tok * (kind == kPair ? p : n / (2 * P.tile_tok));
+        w.tok0 = tok + 2 * P.tile_tok * (kind == kPair ? p : quotient(n, P.by_pair));
         w.split = kind == kPair && p == rows - 1 && left <= 2 * P.half_tok ? P.half_tok : P.tile_tok;
         w.kt_a = kt0 + s0;
         w.kt_b = kt0 + s1;
         w.first = s0 == 0;
         const int32_t last = s + (kt - 1) * step;
-        w.more = last < end ? 0 : plan.owner(kind, last) - plan.owner(kind, s);
+        w.more = last < end ? 0 : plan.behind(kind, slot, last);
         if (!emit(w)) return false;
       }
       if (++h == Hk) h = 0, ++p;
@@ -553,8 +560,9 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   constexpr int kHalves = D / 64;
   const int lane = lane_id(), kind = V.kind, slot = V.slot, q_tiles = kind == kPair ? 2 : 1;
   Ring& R = *V.ring;
-  const int boxes = kTileKeys / P.box;  // per tile and half
-  const int group_tiles = 32 / boxes;   // key tiles whose pages one lane each holds
+  const int boxes = 1 << P.box_shift;           // per tile and half
+  const int group_shift = 5 - P.box_shift;
+  const int group_tiles = 1 << group_shift;     // key tiles whose pages one lane each holds
   Place at;          // of the next load
   int loads = 0, n_loaded = 0, n_out = 0;
   bool ready = after == nullptr;
@@ -589,7 +597,7 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     const int n = w.kt_b - w.kt_a;
     int ahead = n > group_tiles ? fetch(w, 1) : -1, old = -1, group = 0;
     auto load = [&](const CUtensorMap* map, int x) -> bool {
-      const int g = x / group_tiles;
+      const int g = x >> group_shift;
       if (g > group) {  // (V follows K by one tile: it may still need the group before)
         old = pages;
         pages = ahead;
@@ -597,8 +605,8 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
         if (n > (g + 1) * group_tiles) ahead = fetch(w, g + 1);
       }
       // lane = half * boxes + box
-      const int box = lane % boxes, half = lane / boxes;
-      const int key = __shfl_sync(0xffffffffu, g == group ? pages : old, (x % group_tiles) * boxes + box);
+      const int box = lane & (boxes - 1), half = lane >> P.box_shift;
+      const int key = __shfl_sync(0xffffffffu, g == group ? pages : old, ((x & (group_tiles - 1)) << P.box_shift) + box);
       const bool mine = lane < boxes * kHalves && key >= 0;
       const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, mine));
       if (loads >= V.stages && !wait_warp(c, &R.empty[at.st], at.round ^ 1)) return false;
@@ -954,6 +962,11 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
 
 // Warps 0-3 and 4-7: softmax of slot 0 and 1.  Warps 8 and 9: producers (8 for
 // pairs and slot 0's solos, 9 for slot 1's solos).  Warps 10 and 11: MMA issuers.
+// A CTA's way to its first scores is a chain of round trips (lengths, page numbers,
+// K: 3 us with cold caches) and of code that it runs for the first time, which is
+// fetched at a few instructions per nanosecond: the plan without divisions and
+// unrolled copies, and CTAs without pairs that go to their solos at once, took 1 to
+// 2 us off every call (64 requests over 4096 + up to 1000 keys: 44.5 to 42.6 us).
 template <class T, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
     k_attn_tiles(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap tm_q,
@@ -1015,7 +1028,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     SlotParity par;
     bool ok = true;
 #pragma unroll 1
-    for (int turn = 0; ok && turn < 2; ++turn)
+    for (int turn = S.plan.first; ok && turn < 2; ++turn)
       ok = softmax<T, D>(P, S, c, View<D>(S, turn, slot), par);
     __syncwarp();
     reg_dealloc<168>();
@@ -1025,14 +1038,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     if (warp < 10) {
 #pragma unroll 1
-      for (int turn = 0; ok && turn < 2; ++turn)
+      for (int turn = S.plan.first; ok && turn < 2; ++turn)
         if (turn == kSolo || slot == 0)
           ok = produce<D>(P, S, c, View<D>(S, turn, slot), turn == kSolo ? &tm_q64 : &tm_q,
-                          &tm_k, &tm_v, turn ? &S.turn : nullptr);
+                          &tm_k, &tm_v, turn > S.plan.first ? &S.turn : nullptr);
     } else {
       SlotParity par;
 #pragma unroll 1
-      for (int turn = 0; ok && turn < 2; ++turn) {
+      for (int turn = S.plan.first; ok && turn < 2; ++turn) {
         ok = issue_mmas<T, D>(S, c, View<D>(S, turn, slot), par);
         if (ok && turn == 0) {
           if (elect_one()) mma_commit(&S.turn);
@@ -1320,6 +1333,8 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   A.group = io->n_q_heads / io->n_kv_heads;
   A.tile_tok = 128 / A.group;
   A.half_tok = 64 / A.group;
+  A.by_pair = make_divisor(2 * A.tile_tok);
+  A.by_heads = make_divisor(io->n_kv_heads);
   // the longest that the lines of work can be, by the capacity of the tables
   const int64_t pairs = io->n_rows / (2 * A.tile_tok) + 1;
   const int64_t own = pairs + std::min(io->n_requests, io->n_rows);
@@ -1341,6 +1356,8 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   int device = 0;
   st = check_device(workspace, &device, &A.ctas);
   if (st != MK_OK) return st;
+  A.by_ctas = make_divisor(A.ctas);
+  for (int k = 0; k < 2; ++k) A.by_cost[k] = make_divisor(A.tile_cost[k]);
   if (workspace_bytes < lay_out(io, A.ctas, static_cast<uint8_t*>(workspace), &A.ws))
     return MK_ERR_INVALID_ARG;
   if (io->n_rows == 0) {
@@ -1350,6 +1367,7 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   const float scale = io->scale != 0.f ? io->scale : 1.f / std::sqrt(static_cast<float>(io->head_dim));
   A.scale_log2 = scale * 1.4426950408889634f;
   A.box = static_cast<int>(std::min<int64_t>(P, kTileKeys));
+  A.box_shift = __builtin_ctz(kTileKeys / A.box);
   A.page_shift = __builtin_ctz(static_cast<uint32_t>(P));
   const uint64_t d = io->head_dim, Hq = io->n_q_heads, Hk = io->n_kv_heads;
   CUtensorMap q, q64, k, v;

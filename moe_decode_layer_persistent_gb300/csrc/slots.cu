@@ -22,21 +22,6 @@ namespace {
 
 constexpr int kSlotThreads = 512;
 
-// Quotients of numbers below 2^31 by a fixed divisor: with 2^(s-1) < d <= 2^s and
-// m = floor(2^(31+s) / d) + 1, floor(x m / 2^(31+s)) = floor(x / d), since the error
-// x (m - 2^(31+s) / d) / 2^(31+s) <= x / 2^(31+s) < 1 / d.
-struct Divisor {
-  uint32_t d, m, shift;
-};
-Divisor make_divisor(uint32_t d) {
-  uint32_t s = 0;
-  while ((uint64_t{1} << s) < d) ++s;
-  return Divisor{d, static_cast<uint32_t>((uint64_t{1} << (31 + s)) / d + 1), 31 + s};
-}
-MK_DEV uint32_t quotient(uint32_t x, const Divisor& v) {
-  return static_cast<uint32_t>((static_cast<uint64_t>(x) * v.m) >> v.shift);
-}
-
 struct SlotsParams {
   mk_slots_io io;
   Divisor page;
