@@ -964,7 +964,7 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
 // pairs and slot 0's solos, 9 for slot 1's solos).  Warps 10 and 11: MMA issuers.
 // A CTA's way to its first scores is a chain of round trips (lengths, page numbers,
 // K: 3 us with cold caches) and of code that it runs for the first time, which is
-// fetched at a few instructions per nanosecond: the plan without divisions and
+// slower to fetch than to run: the plan without divisions and
 // unrolled copies, and CTAs without pairs that go to their solos at once, took 1 to
 // 2 us off every call (64 requests over 4096 + up to 1000 keys: 44.5 to 42.6 us).
 template <class T, int D>
@@ -1072,7 +1072,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // ------------------------------------------------------------------ merge
 
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 256, kMergePerSm = 5;
+constexpr int kMergeSmem = 220 * 1024;  // less than an SM has
 
 template <int V>
 struct Vals {
@@ -1097,14 +1098,20 @@ MK_DEV Vals<V> load_vals(const float* p) {
 // What does not depend on the tiles (the row's request) comes before the wait for
 // them; behind it the first stretches' results of the prefix and of the request's
 // own keys, by row, and then those of the stretches that carried on.  Each is a
-// round trip to L2; they and the launch bound it.  A row and head has N lanes: 32,
-// or 16 where there are so many rows that they come in waves (64 requests of 8
-// tokens, 32 heads of 128: 10 us behind the tiles instead of 18; with 32 tokens and
-// 20 results each 16 lanes would take 6 us longer).
+// round trip to L2; they and the launch bound it (3 to 4 us behind the last tile).
+// Its CTAs become resident on the SMs that are done first, as many as fit, so that
+// registers are kept low (a CTA that has to wait for others' end costs 3 us) and no
+// SM takes more than its even share: 16 requests of up to 16 tokens over 16384 keys
+// 45.4 us instead of 47.3, of 2 tokens over 32768 keys 44.4 instead of 46.2 (and
+// 47.6 with low registers alone).  A row and head has N lanes: 32, or 16 where
+// there are so many rows that they come in waves (64 requests of 8 tokens, 32 heads
+// of 128: 10 us less; with 32 tokens and 20 results each 16 lanes would take 6 us
+// longer).
 template <class T, int D, int N>
-__global__ void __launch_bounds__(kMergeThreads) k_attn_merge(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(kMergeThreads, kMergePerSm)
+    k_attn_merge(const __grid_constant__ AttnParams P) {
   const mk_prefix_attn_io& io = P.io;
-  constexpr int V = D / N, kAtOnce = N == 32 ? 8 : 4;
+  constexpr int V = D / N, kAtOnce = N == 32 ? 4 : 2;
   const int lane = threadIdx.x % N, Hq = io.n_q_heads;
   // the item's lanes
   const uint32_t lanes = N == 32 ? 0xffffffffu : (threadIdx.x & 16) ? 0xffff0000u : 0xffffu;
@@ -1113,10 +1120,14 @@ __global__ void __launch_bounds__(kMergeThreads) k_attn_merge(const __grid_const
   const bool in = tok >= io.cu_rows[0] && tok < clampi(io.cu_rows[io.n_requests], 0, io.n_rows);
   bool own = false;
   if (in) {
-    int lo = 0, hi = io.n_requests;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (io.cu_rows[mid] <= tok) lo = mid; else hi = mid;
+    // its request: the lanes look at N places at once
+    int lo = 0;
+    for (int n = io.n_requests; n > 1;) {
+      const int step = (n + N - 1) / N, at = lane * step;
+      const uint32_t below = __ballot_sync(lanes, at < n && io.cu_rows[lo + at] <= tok) & lanes;
+      const int skip = max(0, __popc(below) - 1) * step;
+      lo += skip;
+      n = min(step, n - skip);
     }
     const Req r = read_req(P, lo);
     own = r.kt1 > r.kt0;
@@ -1259,6 +1270,8 @@ mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorM
   const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
     MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_tiles<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_merge<T, D, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem));
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_merge<T, D, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem));
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t lc = {};
@@ -1276,7 +1289,9 @@ mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorM
   const int n = items > 32ll * A.ctas ? 16 : 32;
   lc.gridDim = dim3(static_cast<unsigned>((items * n + kMergeThreads - 1) / kMergeThreads));
   lc.blockDim = dim3(kMergeThreads);
-  lc.dynamicSmemBytes = 0;
+  // (shared memory that nobody uses: no SM takes more than its share of the CTAs)
+  const int share = static_cast<int>((lc.gridDim.x + A.ctas - 1) / A.ctas);
+  lc.dynamicSmemBytes = share < kMergePerSm ? kMergeSmem / share - 1024 : 0;
   if (n == 32) MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_attn_merge<T, D, 32>, A));
   else MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_attn_merge<T, D, 16>, A));
   return MK_OK;
