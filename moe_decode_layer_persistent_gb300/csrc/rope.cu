@@ -4,7 +4,7 @@
 // Pair (a, b) of a head at position p turns by the angle p f_i:
 //   y_a = m (x_a cos - x_b sin),  y_b = m (x_b cos + x_a sin).
 // The angle is held in 64-bit fixed point as a fraction of a turn: F_i =
-// round(f_i / 2 pi 2^64), and p F_i modulo 2^64 drops the whole turns exactly,
+// floor(f_i / 2 pi 2^64), and p F_i modulo 2^64 drops the whole turns exactly,
 // so that a position of 2^20 is as exact as one of 16 (in 32-bit floating
 // point its angle would be off by 0.03 rad).  The top 32 bits, as a signed
 // number of half turns, go to sincospif.
