@@ -531,6 +531,41 @@ def test_rope_far_slots(cuda_lib):
     assert torch.equal(kc.view(-1, 4, 64)[-3:], k) and torch.equal(vc.view(-1, 4, 64)[-3:], k)   # position 0
 
 
+def test_largest_batch(cuda_lib):
+    """65536 requests of one token each: every row sees its own key alone, so that
+    its output is that key's value to the bit and its lse the key's score."""
+    B, page, hq, d = 65536, 16, 2, 64
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    zero, one = (torch.full((B,), x, dtype=torch.int32, device="cuda") for x in (0, 1))
+    free = torch.randperm(B, generator=gen, device="cuda").int()
+    table = torch.full((B, 1), -1, dtype=torch.int32, device="cuda")
+    cu, lens, positions, request = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (B + 1, B, B, B))
+    slots, summary = torch.empty(B, dtype=torch.int64, device="cuda"), torch.empty(4, dtype=torch.int32, device="cuda")
+    cuda_lib.mk_build_slots(cuda_lib.make_slots_io(zero, one, free, None, table, cu, lens, positions, slots, request,
+                                                   summary, page, B))
+    q, k, v = (torch.randn(B, h, d, generator=gen, device="cuda").bfloat16() for h in (hq, 1, 1))
+    kc, vc = (torch.full((B, page, 1, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rope = cuda_lib.mk_rope_create(cuda_lib.make_rope_config(d))
+    qr, out = torch.empty_like(q), torch.empty_like(q)
+    cuda_lib.mk_rope_apply(rope, cuda_lib.make_rope_io(q, qr, k, v, positions, slots, kc, vc))
+    lse = torch.empty(B, hq, device="cuda")
+    io = cuda_lib.make_prefix_attn_io(qr, kc, vc, out, lens, cu, table, lse=lse)
+    ws = torch.empty(cuda_lib.mk_prefix_attn_workspace(io), dtype=torch.uint8, device="cuda")
+    cuda_lib.mk_prefix_attn(io, ws)
+    torch.cuda.synchronize()
+    cuda_lib.mk_rope_destroy(rope)
+    assert cuda_lib.mk_prefix_attn_status(ws) == 0
+    assert summary.tolist() == [B, B, 0, B]
+    assert torch.equal(slots, free.long() * page) and torch.equal(cu, torch.arange(B + 1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(qr, q)                                    # position 0
+    assert torch.equal(out, v.expand(B, hq, d))
+    # 64 partial sums, each off by 2 V of the absolute sum; scale, log2(e), their product
+    # with it and ln(2) round the score six times; exp2 and log2 of a sum near 1
+    score = (q.double() * k.double()).sum(-1) / 8
+    size = (q.double() * k.double()).abs().sum(-1) / 8
+    assert bool(((lse.double() - score).abs() <= 64 * 2 * V * size + 6 * V * score.abs() + 2.0 ** -21).all())
+
+
 # ------------------------------------------- together, streams and graphs
 
 def _step(mk, rng, B, page, prefix, hq, hk, d, dtype, n_rows):
