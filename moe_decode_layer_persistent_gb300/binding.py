@@ -446,7 +446,7 @@ def _table(fn, t, dtype, dev):
     s0, s1 = t.stride()
     if cols > 1 and s1 != 1:
         _refuse(fn)
-    return t.data_ptr(), rows, cols, max(s0, cols)
+    return t.data_ptr(), rows, cols, s0 if rows > 1 else max(s0, cols)
 
 
 def make_slots_io(cached_lens, new_lens, free_pages, free_head, block_table, cu_rows, lens,

@@ -188,3 +188,30 @@ def test_packed_fields_are_the_structs(mk):
         values = [i + 1 for i in range(len(cls._fields_))]
         got = cls.from_buffer_copy(struct.Struct(fmt).pack(*values))
         assert [getattr(got, f) for f, _ in cls._fields_] == values
+
+
+@pytest.mark.parametrize("make", [
+    lambda t: t[:8].expand(4, 8), lambda t: t.as_strided((4, 8), (3, 1)), lambda t: t[:1].expand(4, 1),
+    lambda t: t.as_strided((4, 8), (7, 1))])
+def test_tables_whose_rows_overlap(mk, make):
+    """Rows that share memory keep their stride, which the library refuses: a
+    stride of its own would lead it behind the table."""
+    import torch
+    table = make(torch.zeros(64, dtype=torch.int32))
+    _, rows, cols, stride = mk._table("f", table, torch.int32, -1)
+    assert (rows, cols, stride) == (*table.shape, table.stride(0))
+    refused(mk, lambda: attn(mk, attn_io(mk, max_pages=cols, table_stride=stride)), INVALID)
+    refused(mk, lambda: mk.mk_build_slots(slots_io(mk, max_pages=cols, table_stride=stride)), INVALID)
+
+
+def test_tables_of_one_row_or_column(mk):
+    """A single row has no stride to respect; a table's rows may have gaps."""
+    import torch
+    t = torch.zeros(64, dtype=torch.int32)
+    assert mk._table("f", t[None], torch.int32, -1)[1:] == (1, 64, 64)
+    assert mk._table("f", t[:8].expand(1, 8), torch.int32, -1)[1:] == (1, 8, 8)
+    assert mk._table("f", t.as_strided((1, 8), (2, 1)), torch.int32, -1)[1:] == (1, 8, 8)
+    assert mk._table("f", t.view(8, 8)[:, :5], torch.int32, -1)[1:] == (8, 5, 8)
+    assert mk._table("f", t.view(8, 8)[:, 3:4], torch.int32, -1)[1:] == (8, 1, 8)
+    assert mk._table("f", t.view(8, 8)[:, :0], torch.int32, -1)[1:] == (8, 0, 8)
+    assert mk._table("f", t[:0].view(0, 8), torch.int32, -1)[1:] == (0, 8, 8)
