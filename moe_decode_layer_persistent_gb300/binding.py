@@ -550,12 +550,14 @@ def make_prefix_attn_io(q, k_cache, v_cache, out, lens, cu_rows, block_table, pr
         _refuse(fn)
     if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * page < prefix_len):
         _refuse(fn)
-    return mk_prefix_attn_io.from_buffer_copy(_pack_attn(
+    io = mk_prefix_attn_io.from_buffer_copy(_pack_attn(
         b, n, hq, hk, d, _kind(fn, T, q), page, pages, prefix_len, cols, stride, window, scale,
         qp, qs, _vec(fn, k_cache, dt, dev), _vec(fn, v_cache, dt, dev),
         _vec(fn, prefix_pages, i32, dev), table, _vec(fn, lens, i32, dev, b),
         _vec(fn, cu_rows, i32, dev, b + 1), _vec(fn, tree_mask, T.int64, dev, n), op, os_,
         _vec(fn, lse, T.float32, dev, n * hq)))
+    io.device = dev  # (an attribute beside the fields: the workspace has to be there too)
+    return io
 
 
 def mk_prefix_attn_workspace(io):
@@ -566,6 +568,8 @@ def mk_prefix_attn_workspace(io):
 
 
 def mk_prefix_attn(io, workspace, stream=None):
+    if not workspace.is_contiguous() or workspace.get_device() != getattr(io, "device", workspace.get_device()):
+        _refuse("mk_prefix_attn")
     _check("mk_prefix_attn", _lib_mk_prefix_attn(
         ctypes.byref(io), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _stream(stream)))

@@ -215,3 +215,16 @@ def test_tables_of_one_row_or_column(mk):
     assert mk._table("f", t.view(8, 8)[:, 3:4], torch.int32, -1)[1:] == (8, 1, 8)
     assert mk._table("f", t.view(8, 8)[:, :0], torch.int32, -1)[1:] == (8, 0, 8)
     assert mk._table("f", t[:0].view(0, 8), torch.int32, -1)[1:] == (0, 8, 8)
+
+
+def test_workspace_refusals_of_the_binding(mk):
+    """A workspace is one stretch of memory, on the device of the tensors it is
+    for: its address and its number of values do not tell."""
+    import torch
+    room = torch.zeros(1 << 16, dtype=torch.uint8)
+    room = room[-room.data_ptr() % 256:]            # aligned as a workspace has to be
+    for bad in (room[:1].expand(1 << 30), room[::2], room[:1 << 14].view(128, 128).t()):
+        refused(mk, lambda: mk.mk_prefix_attn(attn_io(mk), bad), INVALID)
+    io = attn_io(mk)
+    io.device = 1                                   # as make_prefix_attn_io leaves it
+    refused(mk, lambda: mk.mk_prefix_attn(io, room), INVALID)
