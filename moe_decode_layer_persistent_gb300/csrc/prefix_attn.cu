@@ -846,6 +846,7 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
           if (j > 0) mbar_arrive(&R.empty[at.st == 0 ? W.stages - 1 : at.st - 1]);
           if (j == n - 1) mbar_arrive(&R.q_empty[kind == kPair ? slot : 0]);
         }
+        __syncwarp();  // (loads from tensor memory are for whole warps)
       }
       if (warp_valid) {
         // P = 2^(S - m), with the m of the tiles before as long as the row's sum
