@@ -610,18 +610,17 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     if (!ready && !wait_warp(c, after, 0, kLongWaitNs)) return false;
     ready = true;
     const int n = w.kt_b - w.kt_a;
-    int ahead = n > group_tiles ? fetch(w, 1) : -1, old = -1, group = 0;
+    int ahead = n > group_tiles ? fetch(w, 1) : -1, group = 0;
     auto load = [&](const CUtensorMap* map, int x) -> bool {
       const int g = x >> group_shift;
-      if (g > group) {  // (V follows K by one tile: it may still need the group before)
-        old = pages;
+      if (g > group) {  // (K is loaded before V of the same tile: x never falls)
         pages = ahead;
         group = g;
         if (n > (g + 1) * group_tiles) ahead = fetch(w, g + 1);
       }
       // lane = half * boxes + box
       const int box = lane & (boxes - 1), half = lane >> P.box_shift;
-      const int key = __shfl_sync(0xffffffffu, g == group ? pages : old, ((x & (group_tiles - 1)) << P.box_shift) + box);
+      const int key = __shfl_sync(0xffffffffu, pages, ((x & (group_tiles - 1)) << P.box_shift) + box);
       const bool mine = lane < boxes * kHalves && key >= 0;
       const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, mine));
       if (loads >= V.stages && !wait_warp(c, &R.empty[at.st], at.round ^ 1)) return false;
