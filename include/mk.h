@@ -529,8 +529,10 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
                          void* stream);
 
 /* Device status of the last mk_prefix_attn that used `workspace`: MK_OK, or
- * MK_ERR_TIMEOUT if a bounded device-side wait expired, MK_ERR_INVALID_ARG if its
- * cu_rows falls (its outputs are then undefined).  Reads a device word synchronously: call after synchronising. */
+ * MK_ERR_TIMEOUT if a bounded device-side wait expired (2 s for a hand-off),
+ * MK_ERR_INVALID_ARG if its cu_rows falls; out and lse are then undefined, and the
+ * next call on the workspace is well.  Reads a device word synchronously: call
+ * after synchronising. */
 mk_status mk_prefix_attn_status(const void* workspace);
 
 #ifdef __cplusplus

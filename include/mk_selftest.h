@@ -39,6 +39,17 @@ mk_status mk_selftest_mma(int32_t fp4, const void* a, const void* a_scales, cons
  * allocates and frees its own 256 bytes. */
 mk_status mk_selftest_sync(int32_t mode, int32_t iters, double* ns_per_op);
 
+/* mk_prefix_attn (bf16, head_dim 64) with its waits for hand-offs limited to
+ * `wait_ns` (1 .. 2e9; 2e9 in mk_prefix_attn itself) and, in every CTA, one
+ * hand-off withheld, so that the waits for it run out and the kernel gives up:
+ * withhold 1, the scores of each slot's tile number `which`; 2, the weights of
+ * that tile; 3, the row tile of slot which % 2 after its piece which / 2; 4, the
+ * buffers after the pairs of slot `which`; 0, nothing.  Synchronous; returns
+ * mk_prefix_attn_status: MK_ERR_TIMEOUT where some CTA came that far. */
+mk_status mk_selftest_attn_waits(const mk_prefix_attn_io* io, void* workspace,
+                                 int64_t workspace_bytes, uint64_t wait_ns, int32_t withhold,
+                                 int32_t which, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

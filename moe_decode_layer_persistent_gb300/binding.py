@@ -171,6 +171,9 @@ _lib_mk_prefix_attn_workspace = _sig("mk_prefix_attn_workspace", _c.c_int,
 _lib_mk_prefix_attn = _sig("mk_prefix_attn", _c.c_int,
                            [_c.POINTER(mk_prefix_attn_io), _vp, _i64, _vp])
 _lib_mk_prefix_attn_status = _sig("mk_prefix_attn_status", _c.c_int, [_vp])
+_lib_mk_selftest_attn_waits = _sig("mk_selftest_attn_waits", _c.c_int,
+                                   [_c.POINTER(mk_prefix_attn_io), _vp, _i64, _c.c_uint64, _i32,
+                                    _i32, _vp])
 
 EXPORTED = ["mk_layer_create", "mk_decode_step", "mk_decode_step_noalloc", "mk_layer_status", "mk_layer_clear_status",
             "mk_layer_destroy", "mk_stack_create", "mk_stack_step", "mk_stack_status",
@@ -178,7 +181,7 @@ EXPORTED = ["mk_layer_create", "mk_decode_step", "mk_decode_step_noalloc", "mk_l
             "mk_layer_prefetch_stats", "mk_stack_prefetch_stats",
             "mk_build_slots", "mk_rope_create", "mk_rope_destroy", "mk_rope_apply",
             "mk_prefix_attn_workspace", "mk_prefix_attn", "mk_prefix_attn_status",
-            "mk_selftest_quantize", "mk_selftest_mma", "mk_selftest_sync"]
+            "mk_selftest_quantize", "mk_selftest_mma", "mk_selftest_sync", "mk_selftest_attn_waits"]
 
 
 def _ptr(t):
@@ -577,3 +580,15 @@ def mk_prefix_attn(io, workspace, stream=None):
 
 def mk_prefix_attn_status(workspace):
     return _lib_mk_prefix_attn_status(_ptr(workspace))
+
+
+WITHHOLD = {"nothing": 0, "scores": 1, "weights": 2, "row_tile": 3, "buffers": 4}
+
+
+def mk_selftest_attn_waits(io, workspace, wait_ns, withhold="nothing", which=0, stream=None):
+    """mk_prefix_attn with short waits and a hand-off withheld; returns the status."""
+    if not workspace.is_contiguous():
+        _refuse("mk_selftest_attn_waits")
+    return _lib_mk_selftest_attn_waits(
+        ctypes.byref(io), workspace.data_ptr(), workspace.numel() * workspace.element_size(), wait_ns,
+        WITHHOLD[withhold], which, _stream(stream))

@@ -33,6 +33,7 @@
 #include <cstring>
 #include <cuda_fp16.h>
 
+#include "../../include/mk_selftest.h"
 #include "batch.h"
 #include "ptx.cuh"
 
@@ -54,9 +55,14 @@ constexpr uint32_t kTimeout = 1, kFalling = 2;  // values of the status word
 constexpr int kFifo = 4;            // pieces handed out ahead
 constexpr int kTileThreads = 384;
 constexpr float kMost = 16384.f;    // a row's sum of P over a tile, in units of 2^m, at most
-// Limits of the waits: for a hand-off, and for what may take as long as a CTA's
-// whole work (a wait that runs out ends that work, too).
-constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000, kLongWaitNs = 100 * kWaitNs;
+// Limits of the waits: for a hand-off, and so many times that for what may take as
+// long as a CTA's whole work (a wait that runs out ends that work, too).
+constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
+constexpr int kLongWait = 100;
+
+// Hand-offs that a self-test withholds, so that waits run out: a tile's scores, a
+// tile's weights, a slot's row tile after use, the buffers after a slot's pairs.
+enum Withhold { kNothing = 0, kScores = 1, kWeights = 2, kRowTile = 3, kBuffers = 4 };
 
 // How the lines are laid out (every CTA of k_attn_tiles works it out for itself).
 struct Plan {
@@ -128,6 +134,10 @@ struct AttnParams {
   // start, delays its first loads
   Divisor by_pair, by_heads, by_ctas, by_cost[2];
   Space ws;
+  // of a self-test: limit of a wait for a hand-off; which hand-off to withhold, and
+  // the how manieth
+  uint64_t wait_ns;
+  int32_t withhold, withhold_at;
 };
 
 MK_DEV int clampi(int64_t v, int lo, int hi) {
@@ -194,6 +204,9 @@ struct Ring {
   uint64_t q_full[2], q_empty[2];
   uint64_t fifo_full[kFifo], fifo_empty[kFifo];
   Piece fifo[kFifo];
+  // Once the producer is done: the K and V tiles whose copies were issued, how often
+  // those of all row tiles were, and how many row tiles' once more.
+  int32_t loads, q_rounds, q_more;
 };
 // A place in a ring: the stage and how often the ring has gone round (mod 2).
 struct Place {
@@ -231,12 +244,18 @@ struct alignas(1024) TileSmem {
   int32_t first_at[3];
   int32_t first[3];
   uint32_t tmem;
-  uint32_t abort;
+  // some wait of the CTA has run out: while it works, while it drains what it gave up
+  uint32_t abort, drain_abort;
 };
 
+template <bool kTest>
 struct Ctx {
   volatile uint32_t* abort;
   uint32_t* status;
+  uint64_t wait_ns;  // of a self-test
+  MK_DEV uint64_t limit(int work) const {
+    return (kTest ? wait_ns : kWaitNs) * (work ? kLongWait : 1);
+  }
 };
 
 // One kind of work as one slot's warps see it.
@@ -258,8 +277,11 @@ struct View {
 };
 
 // Bounded waits: false once any wait of the CTA has run out.  The clock is read
-// now and then only: reading it takes longer than a hand-off.
-MK_DEV bool wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity, uint64_t limit) {
+// now and then only: reading it takes longer than a hand-off.  (With limits that come
+// from memory ragged verify steps take 1.2 us longer: 16 requests of up to 16 tokens
+// over 16384 keys 47.6 instead of 46.4.)
+template <bool kTest>
+MK_DEV bool wait_bar(const Ctx<kTest>& c, uint64_t* bar, uint32_t parity, int work) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   while (true) {
@@ -267,15 +289,27 @@ MK_DEV bool wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity, uint64_t limi
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*c.abort) return false;
-    if (globaltimer() - t0 > limit) {
+    if (globaltimer() - t0 > c.limit(work)) {
       *c.abort = 1;
       atomicExch(c.status, kTimeout);
       return false;
     }
   }
 }
-MK_DEV bool wait_warp(const Ctx& c, uint64_t* bar, uint32_t parity, uint64_t limit = kWaitNs) {
-  return __all_sync(0xffffffffu, wait_bar(c, bar, parity, limit));
+template <bool kTest>
+MK_DEV bool wait_warp(const Ctx<kTest>& c, uint64_t* bar, uint32_t parity, int work = 0) {
+  return __all_sync(0xffffffffu, wait_bar(c, bar, parity, work));
+}
+
+// Of work that was given up: waits for the copies into a ring that may still be on
+// their way, the last one into each stage and each row tile.
+MK_DEV void drain_ring(const Ctx<false>& c, Ring& R, int stages, int q_tiles) {
+  for (int q = max(0, R.loads - stages); q < R.loads; ++q)
+    wait_warp(c, &R.full[q % stages], (q / stages) & 1);
+  for (int t = 0; t < q_tiles; ++t) {
+    const int n = R.q_rounds + (t < R.q_more);
+    if (n > 0) wait_warp(c, &R.q_full[t], (n - 1) & 1);
+  }
 }
 
 MK_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -567,8 +601,8 @@ MK_DEV bool walk(const AttnParams& P, const Plan& plan, int kind, int slot, int 
 
 // ---- producer of one kind of work: hands the pieces out and loads row tiles
 // and K and V tiles (K0 V0 K1 V1 ...)
-template <int D>
-MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const View<D>& V,
+template <int D, bool kTest>
+MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx<kTest>& c, const View<D>& V,
                     const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                     uint64_t* after) {
   const mk_prefix_attn_io& io = P.io;
@@ -580,7 +614,6 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   const int group_tiles = 1 << group_shift;     // key tiles whose pages one lane each holds
   Place at;          // of the next load
   int loads = 0, n_loaded = 0, n_out = 0;
-  bool ready = after == nullptr;
   // First slot of box number 32 g + lane of a piece; -1: no row sees its keys.
   // A page outside the pool: behind the end, where the copy fills in zeros.
   auto fetch = [&](const volatile Piece& w, int g) -> int {
@@ -593,7 +626,7 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   };
   auto push = [&](const Piece& w) -> bool {
     const int k = n_out % kFifo;
-    if (n_out >= kFifo && !wait_warp(c, &R.fifo_empty[k], ((n_out / kFifo) - 1) & 1, kLongWaitNs))
+    if (n_out >= kFifo && !wait_warp(c, &R.fifo_empty[k], ((n_out / kFifo) - 1) & 1, 1))
       return false;
     if (lane == 0) {
       R.fifo[k] = w;
@@ -607,8 +640,8 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
   // registers are short here)
   auto load_piece = [&](const volatile Piece& w, int pages) -> bool {
     // the buffers belong to the other kind of work until its MMAs are done
-    if (!ready && !wait_warp(c, after, 0, kLongWaitNs)) return false;
-    ready = true;
+    if (after && !wait_warp(c, after, 0, 1)) return false;
+    after = nullptr;
     const int n = w.kt_b - w.kt_a;
     int ahead = n > group_tiles ? fetch(w, 1) : -1, group = 0;
     auto load = [&](const CUtensorMap* map, int x) -> bool {
@@ -635,7 +668,10 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     };
     if (!load(tm_k, 0)) return false;
     for (int t = 0; t < q_tiles; ++t) {
-      if (n_loaded > 0 && !wait_warp(c, &R.q_empty[t], (n_loaded - 1) & 1)) return false;
+      if (n_loaded > 0 && !wait_warp(c, &R.q_empty[t], (n_loaded - 1) & 1)) {
+        if (lane == 0) R.q_more = t;
+        return false;
+      }
       if (lane == 0) {
         const int toks = kind == kPair ? P.tile_tok : P.half_tok;
         mbar_arrive_expect_tx(&R.q_full[t], kHalves * P.group * toks * 128);
@@ -669,14 +705,8 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
     none.own = -1;
     ok = push(none) && (n_out < 2 || load_piece(R.fifo[(n_out - 2) % kFifo], held_pages));
   }
-  if (ok) return true;
-  // give up: no copy may land after the CTA has left
-  uint32_t never = 0;
-  const Ctx drain{&never, c.status};
-  for (int q = max(0, loads - V.stages); q < loads; ++q)
-    wait_warp(drain, &R.full[q % V.stages], (q / V.stages) & 1);
-  for (int t = 0; t < q_tiles && n_loaded > 0; ++t) wait_warp(drain, &R.q_full[t], (n_loaded - 1) & 1);
-  return false;
+  if (lane == 0) R.loads = loads, R.q_rounds = n_loaded;
+  return ok;
 }
 
 // ---- MMA issuer of a slot: the whole warp walks the pieces, one elected lane
@@ -690,10 +720,17 @@ MK_DEV bool produce(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
 struct SlotParity {
   uint32_t s = 0, p = 0, o = 0;
   int cold = 1;  // nothing has run yet
+  int tile = 0;  // (counted in a self-test only)
 };
 
-template <class T, int D>
-MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParity& par) {
+// Whether a self-test withholds this hand-off.
+template <bool kTest>
+MK_DEV bool withheld(const AttnParams& P, Withhold what, int tile) {
+  return kTest && P.withhold == what && P.withhold_at == tile;
+}
+
+template <class T, int D, bool kTest>
+MK_DEV bool issue_mmas(const AttnParams& P, TileSmem<D>& S, const Ctx<kTest>& c, const View<D>& V, SlotParity& par) {
   constexpr uint32_t kIdS = idesc_of<T>(kTileKeys, false), kIdO = idesc_of<T>(D, true);
   const bool pair = V.kind == kPair;
   const int slot = V.slot;
@@ -731,8 +768,9 @@ MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParit
     if (elect_one()) {
       qk(at);
       if (pair) mbar_arrive(&S.turn_of[slot ^ 1]);
-      mma_commit(&S.s_full[slot]);
+      if (!withheld<kTest>(P, kScores, par.tile)) mma_commit(&S.s_full[slot]);
     }
+    if (kTest) ++par.tile;
     __syncwarp();
     for (int j = 0; j < n; ++j) {
       const Place sv = at.next(V.stages), sk = sv.next(V.stages);
@@ -749,9 +787,10 @@ MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParit
           mma_ts(to, ts + 8 * k, vd + k * (16 * 128 >> 4), kIdO, j > 0 || k > 0);
         if (more) qk(sk);
         if (pair) mbar_arrive(&S.turn_of[slot ^ 1]);
-        mma_commit(more ? &S.s_full[slot] : &S.o_done[slot]);
+        if (!more || !withheld<kTest>(P, kScores, par.tile)) mma_commit(more ? &S.s_full[slot] : &S.o_done[slot]);
       }
       __syncwarp();
+      if (kTest && more) ++par.tile;
       at = sk;
     }
     ++piece;
@@ -759,8 +798,8 @@ MK_DEV bool issue_mmas(TileSmem<D>& S, const Ctx& c, const View<D>& V, SlotParit
 }
 
 // ---- softmax of one slot (a warpgroup, one thread per row)
-template <class T, int D>
-MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const View<D>& W,
+template <class T, int D, bool kTest>
+MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx<kTest>& c, const View<D>& W,
                     SlotParity& par) {
   const mk_prefix_attn_io& io = P.io;
   const int slot = W.slot, kind = W.kind;
@@ -843,7 +882,7 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
         if (warp == 0 && lane == 0) {
           mbar_arrive(&R.empty[at.st]);
           if (j > 0) mbar_arrive(&R.empty[at.st == 0 ? W.stages - 1 : at.st - 1]);
-          if (j == n - 1) mbar_arrive(&R.q_empty[kind == kPair ? slot : 0]);
+          if (j == n - 1 && !withheld<kTest>(P, kRowTile, 2 * (piece - 1) + slot)) mbar_arrive(&R.q_empty[kind == kPair ? slot : 0]);
         }
         __syncwarp();  // (loads from tensor memory are for whole warps)
       }
@@ -939,7 +978,8 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
       if (j >= 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full[slot]);
+        if (lane == 0 && !withheld<kTest>(P, kWeights, par.tile)) mbar_arrive(&S.p_full[slot]);
+        if (kTest) ++par.tile;
         at = at.next(W.stages).next(W.stages);
       }
     }
@@ -997,7 +1037,7 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx& c, const Vie
 // Measured, 32 q heads on 8 KV heads of 128, bf16: 64 x 8 rows over a prefix of
 // 32768 keys run at 1,180 TFLOP/s (a pair of tiles takes 1.55 us, its products alone
 // 1.05); 256 requests' own keys at 6.1 TB/s, 90 % of a plain copy.
-template <class T, int D>
+template <class T, int D, bool kTest>
 __global__ void __launch_bounds__(kTileThreads, 1)
     k_attn_tiles(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap tm_q,
                  const __grid_constant__ CUtensorMap tm_q64, const __grid_constant__ CUtensorMap tm_k,
@@ -1016,6 +1056,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&S.ring[i / kFifo].fifo_full[i % kFifo], 1);
       mbar_init(&S.ring[i / kFifo].fifo_empty[i % kFifo], i < kFifo ? 10 : 5);
     }
+    if (lane_id() < 3) {
+      Ring& R = S.ring[lane_id()];
+      R.loads = R.q_rounds = R.q_more = 0;
+    }
     if (lane_id() < 6) {
       mbar_init(&S.ring[lane_id() >> 1].q_full[lane_id() & 1], 1);
       mbar_init(&S.ring[lane_id() >> 1].q_empty[lane_id() & 1], 1);
@@ -1029,7 +1073,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     if (lane_id() == 0) {
       mbar_init(&S.turn, 2);
-      S.abort = 0;
+      S.abort = S.drain_abort = 0;
     }
     fence_mbar_init();
   }
@@ -1049,7 +1093,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();
-  const Ctx c{&S.abort, P.ws.status};
+  const Ctx<kTest> c{&S.abort, P.ws.status, P.wait_ns};
   // 2 x 128 x 208 + 128 x 88 = 64,512, all registers of the launch; all are back
   // at 168 before the common tail
   if (warp < 8) {
@@ -1059,7 +1103,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
 #pragma unroll 1
     for (int turn = S.plan.first; ok && turn < 2; ++turn)
-      ok = softmax<T, D>(P, S, c, View<D>(S, turn, slot), par);
+      ok = softmax<T, D, kTest>(P, S, c, View<D>(S, turn, slot), par);
     __syncwarp();
     reg_dealloc<168>();
   } else {
@@ -1070,24 +1114,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
       for (int turn = S.plan.first; ok && turn < 2; ++turn)
         if (turn == kSolo || slot == 0)
-          ok = produce<D>(P, S, c, View<D>(S, turn, slot), turn == kSolo ? &tm_q64 : &tm_q,
+          ok = produce<D, kTest>(P, S, c, View<D>(S, turn, slot), turn == kSolo ? &tm_q64 : &tm_q,
                           &tm_k, &tm_v, turn > S.plan.first ? &S.turn : nullptr);
     } else {
       SlotParity par;
 #pragma unroll 1
       for (int turn = S.plan.first; ok && turn < 2; ++turn) {
-        ok = issue_mmas<T, D>(S, c, View<D>(S, turn, slot), par);
+        ok = issue_mmas<T, D, kTest>(P, S, c, View<D>(S, turn, slot), par);
         if (ok && turn == 0) {
-          if (elect_one()) mma_commit(&S.turn);
+          if (elect_one() && !withheld<kTest>(P, kBuffers, slot)) mma_commit(&S.turn);
           __syncwarp();
         }
-      }
-      if (!ok) {
-        // give up: no MMA may run on after the CTA has left
-        uint32_t never = 0;
-        if (elect_one()) mma_commit(&S.drained[slot]);
-        __syncwarp();
-        wait_warp(Ctx{&never, c.status}, &S.drained[slot], 0);
       }
     }
     __syncwarp();
@@ -1097,6 +1134,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (S.abort) {
+    // A wait has run out (none behind the barrier writes the word).  Whichever it was,
+    // and whoever was done by then: no copy may land and no product run on after the
+    // CTA has left.
+    const Ctx<false> last{&S.drain_abort, c.status, 0};
+    if (warp == 8) drain_ring(last, S.ring[0], TileSmem<D>::kStages, 2);
+    if (warp == 8 || warp == 9) drain_ring(last, S.ring[warp - 7], TileSmem<D>::kSoloStages, 1);
+    if (warp >= 10) {
+      if (elect_one()) mma_commit(&S.drained[warp & 1]);
+      __syncwarp();
+      wait_warp(last, &S.drained[warp & 1], 0);
+    }
+    __syncthreads();
+  }
   if (warp == 10) tmem_dealloc(S.tmem, 512);
 }
 
@@ -1304,7 +1355,7 @@ mk_status encode_tmap_3d(CUtensorMap* map, int dtype, const void* base, uint64_t
   return r == CUDA_SUCCESS ? MK_OK : MK_ERR_INVALID_ARG;
 }
 
-template <class T, int D>
+template <class T, int D, bool kTest = false>
 mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorMap& q64,
                       const CUtensorMap& k, const CUtensorMap& v, int device, cudaStream_t s) {
   constexpr int smem = sizeof(TileSmem<D>) + 1024;
@@ -1312,7 +1363,7 @@ mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorM
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_tiles<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_tiles<T, D, kTest>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_merge<T, D, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem));
     MK_CUDA_TRY(cudaFuncSetAttribute(k_attn_merge<T, D, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem));
     ready.fetch_or(bit, std::memory_order_relaxed);
@@ -1327,7 +1378,7 @@ mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorM
   lc.gridDim = dim3(A.ctas);
   lc.blockDim = dim3(kTileThreads);
   lc.dynamicSmemBytes = smem;
-  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_attn_tiles<T, D>, A, q, q64, k, v));
+  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_attn_tiles<T, D, kTest>, A, q, q64, k, v));
   const int64_t items = static_cast<int64_t>(A.io.n_rows) * A.io.n_q_heads;
   const int n = items > 32ll * A.ctas ? 16 : 32;
   lc.gridDim = dim3(static_cast<unsigned>((items * n + kMergeThreads - 1) / kMergeThreads));
@@ -1340,29 +1391,14 @@ mk_status launch_attn(const AttnParams& A, const CUtensorMap& q, const CUtensorM
   return MK_OK;
 }
 
-}  // namespace
+// What a self-test sets about the waits.
+struct Waits {
+  uint64_t ns;
+  int32_t withhold, which;
+};
 
-}  // namespace mk
-
-using namespace mk;
-
-extern "C" {
-
-mk_status mk_prefix_attn_workspace(const mk_prefix_attn_io* io, int64_t* bytes) {
-  if (!bytes) return MK_ERR_INVALID_ARG;
-  *bytes = 0;
-  mk_status st = check_shapes(io);
-  if (st != MK_OK) return st;
-  int dev = -1, sms = 0;
-  MK_CUDA_TRY(cudaGetDevice(&dev));
-  MK_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  Space s;
-  *bytes = lay_out(io, sms, nullptr, &s);
-  return MK_OK;
-}
-
-mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t workspace_bytes,
-                         void* stream) {
+mk_status attn(const mk_prefix_attn_io* io, void* workspace, int64_t workspace_bytes, void* stream,
+               const Waits* test) {
   mk_status st = check_shapes(io);
   if (st != MK_OK) return st;
   const int64_t P = io->page_size, cap = static_cast<int64_t>(io->max_pages) * P;
@@ -1388,6 +1424,9 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
     return MK_ERR_INVALID_ARG;
   AttnParams A;
   A.io = *io;
+  A.wait_ns = test ? test->ns : kWaitNs;
+  A.withhold = test ? test->withhold : kNothing;
+  A.withhold_at = test ? test->which : 0;
   A.group = io->n_q_heads / io->n_kv_heads;
   A.tile_tok = 128 / A.group;
   A.half_tok = 64 / A.group;
@@ -1442,11 +1481,50 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
   st = encode_tmap_3d(&v, io->dtype, vp, d, Hk, slots, d * 2, Hk * d * 2, 1, A.box);
   if (st != MK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (test) return launch_attn<__nv_bfloat16, 64, true>(A, q, q64, k, v, device, s);
   if (io->dtype == MK_BF16)
     return io->head_dim == 128 ? launch_attn<__nv_bfloat16, 128>(A, q, q64, k, v, device, s)
                                : launch_attn<__nv_bfloat16, 64>(A, q, q64, k, v, device, s);
   return io->head_dim == 128 ? launch_attn<__half, 128>(A, q, q64, k, v, device, s)
                              : launch_attn<__half, 64>(A, q, q64, k, v, device, s);
+}
+
+}  // namespace
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" {
+
+mk_status mk_prefix_attn_workspace(const mk_prefix_attn_io* io, int64_t* bytes) {
+  if (!bytes) return MK_ERR_INVALID_ARG;
+  *bytes = 0;
+  mk_status st = check_shapes(io);
+  if (st != MK_OK) return st;
+  int dev = -1, sms = 0;
+  MK_CUDA_TRY(cudaGetDevice(&dev));
+  MK_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  Space s;
+  *bytes = lay_out(io, sms, nullptr, &s);
+  return MK_OK;
+}
+
+mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t workspace_bytes,
+                         void* stream) {
+  return attn(io, workspace, workspace_bytes, stream, nullptr);
+}
+
+mk_status mk_selftest_attn_waits(const mk_prefix_attn_io* io, void* workspace, int64_t workspace_bytes,
+                                 uint64_t wait_ns, int32_t withhold, int32_t which, void* stream) {
+  if (!io || !wait_ns || wait_ns > kWaitNs || withhold < kNothing || withhold > kBuffers || which < 0)
+    return MK_ERR_INVALID_ARG;
+  if (io->dtype != MK_BF16 || io->head_dim != 64) return MK_ERR_UNSUPPORTED;
+  const Waits w{wait_ns, withhold, which};
+  const mk_status st = attn(io, workspace, workspace_bytes, stream, &w);
+  if (st != MK_OK) return st;
+  MK_CUDA_TRY(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
+  return mk_prefix_attn_status(workspace);
 }
 
 mk_status mk_prefix_attn_status(const void* workspace) {

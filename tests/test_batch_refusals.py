@@ -228,3 +228,13 @@ def test_workspace_refusals_of_the_binding(mk):
     io = attn_io(mk)
     io.device = 1                                   # as make_prefix_attn_io leaves it
     refused(mk, lambda: mk.mk_prefix_attn(io, room), INVALID)
+
+
+@pytest.mark.parametrize("over,args,status", [
+    ({}, (0, 1, 0), INVALID), ({}, (2 * 10 ** 9 + 1, 1, 0), INVALID), ({}, (10 ** 6, 5, 0), INVALID),
+    ({}, (10 ** 6, -1, 0), INVALID), ({}, (10 ** 6, 1, -1), INVALID),
+    (dict(dtype=1), (10 ** 6, 1, 0), UNSUPPORTED), ({}, (10 ** 6, 1, 0), UNSUPPORTED),   # head_dim 128
+    (dict(head_dim=64, lens=0), (10 ** 6, 1, 0), INVALID)])
+def test_attention_waits_selftest_refusals(mk, over, args, status):
+    assert mk._lib_mk_selftest_attn_waits(attn_io(mk, **over), 16 * A, 1 << 40, *args, None) == status
+    assert mk._lib_mk_selftest_attn_waits(None, 16 * A, 1 << 40, 10 ** 6, 1, 0, None) == INVALID

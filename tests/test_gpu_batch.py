@@ -727,3 +727,54 @@ def test_layer_chain_with_positions(cuda_lib):
     r = ol.layer_forward(oio.oracle_cfg(c), oio.np_weights(work["Ws"][0]), np64(x1), np64(nkc), np64(nvc), ctx,
                          q_in=np64(q), first_layer=False)
     H.assert_close("x_out", np64(x2), r["x_out"])
+
+
+# ------------------------------------------------------- waits that run out
+
+@pytest.fixture(scope="module")
+def waiting(cuda_lib):
+    """A call whose CTAs hold pairs of row tiles, solos, or both, several pieces
+    each: 64 requests of one token, 8 heads on 2, behind 40,000 keys (on 152 SMs
+    the pairs' work ends in the middle of a CTA's)."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    B, prefix, page, hq, hk, d = 64, 40000, 64, 8, 2, 64
+    first, held = prefix // page, 5
+    pages = first + B * held
+    q = torch.randn(B, hq, d, generator=gen, device="cuda").bfloat16()
+    kc, vc = (torch.randn(pages, page, hk, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    ids = torch.randperm(pages, generator=gen, device="cuda").int()
+    out = torch.full((B, hq, d), CANARY, dtype=torch.bfloat16, device="cuda")
+    lens, cu = torch.full((B,), 300, dtype=torch.int32, device="cuda"), torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    io = cuda_lib.make_prefix_attn_io(q, kc, vc, out, lens, cu, ids[first:].view(B, held), ids[:first], prefix)
+    size = cuda_lib.mk_prefix_attn_workspace(io)
+    room = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    cuda_lib.mk_prefix_attn(io, room[:size])
+    torch.cuda.synchronize()
+    assert cuda_lib.mk_prefix_attn_status(room) == 0
+    return dict(io=io, ws=room[:size], guard=room[size:], out=out, want=out.clone(),
+                keep=(q, kc, vc, ids, lens, cu), kept=(kc.clone(), vc.clone()))
+
+
+def test_attention_waits_that_do_not_run_out(cuda_lib, waiting):
+    waiting["out"].fill_(CANARY)
+    assert cuda_lib.mk_selftest_attn_waits(waiting["io"], waiting["ws"], 2 * 10 ** 9) == 0
+    assert torch.equal(waiting["out"], waiting["want"])
+
+
+@pytest.mark.parametrize("what,which", [("scores", 0), ("scores", 3), ("weights", 0), ("weights", 2),
+                                        ("row_tile", 0), ("row_tile", 1), ("buffers", 0), ("buffers", 1)])
+def test_attention_gives_up_and_recovers(cuda_lib, waiting, what, which):
+    """A hand-off that never comes: within the limit (1 ms) every warp of the CTA
+    gives up, its copies and products are waited for, the status says so, nothing
+    beside outputs and workspace is touched; the next call on the same workspace
+    is well, to the bit."""
+    status = cuda_lib.mk_selftest_attn_waits(waiting["io"], waiting["ws"], 10 ** 6, what, which)
+    assert cuda_lib.STATUS_NAMES[status] == "MK_ERR_TIMEOUT"
+    assert cuda_lib.mk_prefix_attn_status(waiting["ws"]) == status
+    assert bool((waiting["guard"] == 0x5A).all())
+    assert all(torch.equal(a, b) for a, b in zip(waiting["keep"][1:3], waiting["kept"]))
+    waiting["out"].fill_(CANARY)
+    cuda_lib.mk_prefix_attn(waiting["io"], waiting["ws"])
+    torch.cuda.synchronize()
+    assert cuda_lib.mk_prefix_attn_status(waiting["ws"]) == 0
+    assert torch.equal(waiting["out"], waiting["want"])
