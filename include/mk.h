@@ -476,7 +476,8 @@ mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream)
  *   out = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j exp(scale q.k_j).
  * A row that sees no key gets out = 0 and lse = -infinity.  Rows before
  * cu_rows[0] and from cu_rows[B] on are left as they are.  Keys that no row sees are never looked
- * at: they may hold anything.  A key that some row sees must be finite.
+ * at: they may hold anything.  A key that some row sees must be finite.  A row
+ * of q that holds a NaN gets NaN, if it sees a key, and no other row does.
  * The prefix is read once for the whole batch, not once per request.
  *
  * Scores and sums are held in 32 bits; the softmax weights are rounded to the

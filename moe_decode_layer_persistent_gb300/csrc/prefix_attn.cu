@@ -426,6 +426,12 @@ MK_DEV float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// The larger one, or NaN if either is.
+MK_DEV float max_or_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 MK_DEV float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -995,7 +1001,8 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx<kTest>& c, co
     const int64_t to_row = w.first ? (w.own ? P.ws.own : P.ws.pre) +
                                          static_cast<int64_t>(tok) * io.n_q_heads + w.h * G + g
                                    : P.ws.carry + carry;
-    if (valid) P.ws.part[to_row] = Partial{m, l, 2 * w.more + kind, carry};
+    // (a NaN among the scores is in l, while the maximum passes it by)
+    if (valid) P.ws.part[to_row] = Partial{l == l ? m : l, l, 2 * w.more + kind, carry};
     if (warp_valid) {
       // Four threads write 128 bytes of a row, 8 values each as they come from tensor
       // memory: of 16 pairs of columns, pair 4 i + c lies in place 4 c + i.  (With a
@@ -1226,7 +1233,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergePerSm)
   x[1] = load_vals<V>(P.ws.o + (P.ws.own + item) * D + lane * V);
   if (!pre) first[0] = Partial{-INFINITY, 0.f, 0, 0};
   if (!own) first[1] = Partial{-INFINITY, 0.f, 0, 0};
-  float M = fmaxf(first[0].m, first[1].m), L = 0.f, acc[V] = {};
+  float M = max_or_nan(first[0].m, first[1].m), L = 0.f, acc[V] = {};
   if (M != -INFINITY) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -1251,8 +1258,8 @@ __global__ void __launch_bounds__(kMergeThreads, kMergePerSm)
     if (ok) mine = part[at];
     float top = mine.m;
 #pragma unroll
-    for (int o = N / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
-    top = fmaxf(top, M);
+    for (int o = N / 2; o; o >>= 1) top = max_or_nan(top, __shfl_xor_sync(lanes, top, o));
+    top = max_or_nan(top, M);
     if (top == -INFINITY) continue;
     const float old = exp2f(M - top), w = mine.m == -INFINITY ? 0.f : exp2f(mine.m - top);
     float sum = w * mine.l;

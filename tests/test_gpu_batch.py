@@ -420,6 +420,27 @@ def test_prefix_attn_scale(cuda_lib):
     check_attn(cuda_lib, a, scale=0.03125)
 
 
+@pytest.mark.parametrize("name", ["one_key", "prefix_only", "no_key", "tile_ends", "chunk", "window_40", "tree_window",
+                                  "prefix_in_many_pieces", "long"])
+def test_prefix_attn_rows_of_nan(cuda_lib, name):
+    """A row whose q holds a NaN: out and lse are NaN as the formula has it (a row
+    without keys still gets 0 and -inf), and no other row's result is."""
+    lens, news, prefix, hq, hk, d, dtype, page, more = ATTN[name]
+    a = make_attn(np.random.default_rng(len(name)), lens, news, prefix, hq, hk, d, dtype, page, **more)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+    out, lse = a["out"].clone(), a["lse"].clone()
+    bad = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+    bad[:a["n"]:3, ::2] = True                    # some rows, some of their heads
+    a["q"][:, :, 5][bad] = float("nan")
+    call_attn(cuda_lib, a)
+    torch.cuda.synchronize()
+    keys = bad & ~torch.isinf(lse)
+    assert bool(torch.isnan(a["out"][keys]).all()) and bool(torch.isnan(a["lse"][keys]).all())
+    a["out"][keys], a["lse"][keys] = out[keys], lse[keys]
+    check_attn(cuda_lib, a)                       # the others, and those without keys
+
+
 def test_prefix_attn_bad_tables_and_lengths(cuda_lib):
     """Pages outside the pool read as zeros; lengths are cut to the table."""
     a = make_attn(np.random.default_rng(2), [40, 9, 60], [2, 1, 4], 100, 4, 2, 64, "bf16", 16)
