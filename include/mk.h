@@ -439,7 +439,7 @@ void mk_rope_destroy(mk_rope* rope);  /* NULL is ignored */
  * 0 .. n_slots-1 writes nothing to the caches.  Slots are distinct: of rows
  * with the same slot either one's values stay, in pieces of 16 bytes. */
 typedef struct mk_rope_io {
-  int32_t n_rows;            /* >= 0                                              */
+  int32_t n_rows;            /* >= 0; with 0 every pointer may be NULL            */
   int32_t n_q_heads;         /* 0 iff q is NULL                                   */
   int32_t n_kv_heads;        /* 0 iff k is NULL                                   */
   int32_t head_dim;          /* d: the one the mk_rope was created for            */

@@ -216,6 +216,7 @@ mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream)
   if (io->head_dim != d) return MK_ERR_INVALID_ARG;
   if (n < 0 || io->n_q_heads < 0 || io->n_kv_heads < 0) return MK_ERR_INVALID_ARG;
   if (io->n_q_heads > 4096 || io->n_kv_heads > 4096) return MK_ERR_UNSUPPORTED;
+  if (n == 0) return MK_OK;  // (tensors without rows may have no address)
   if ((io->q != nullptr) != (io->n_q_heads > 0) || (io->k != nullptr) != (io->n_kv_heads > 0))
     return MK_ERR_INVALID_ARG;
   if (!io->q && !io->k) return MK_ERR_INVALID_ARG;
@@ -241,7 +242,6 @@ mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream)
         (io->k && overlap(io->slots, n * 8, io->q_out, out)))
       return MK_ERR_INVALID_ARG;
   }
-  if (n == 0) return MK_OK;
   int sms = 0;
   mk_status st = check_device(io->positions, nullptr, &sms);
   if (st != MK_OK) return st;

@@ -238,3 +238,18 @@ def test_workspace_refusals_of_the_binding(mk):
 def test_attention_waits_selftest_refusals(mk, over, args, status):
     assert mk._lib_mk_selftest_attn_waits(attn_io(mk, **over), 16 * A, 1 << 40, *args, None) == status
     assert mk._lib_mk_selftest_attn_waits(None, 16 * A, 1 << 40, 10 ** 6, 1, 0, None) == INVALID
+
+
+def test_rope_without_rows(mk):
+    """Tensors without rows have no address; what does not depend on rows is still checked."""
+    r = mk.mk_rope_create(mk.make_rope_config(128))
+    empty = dict(n_rows=0, q=0, q_out=0, k=0, v=0, positions=0, slots=0)
+    try:
+        mk.mk_rope_apply(r, rope_io(mk, **empty))
+        mk.mk_rope_apply(r, rope_io(mk, **empty, q_stride=0, q_out_stride=0, k_stride=0, v_stride=0))
+        mk.mk_rope_apply(r, rope_io(mk, **empty, n_kv_heads=0, k_cache=0, v_cache=0, n_slots=0))
+        for over, status in ((dict(dtype=2), UNSUPPORTED), (dict(head_dim=64), INVALID),
+                             (dict(n_q_heads=-1), INVALID), (dict(n_kv_heads=5000), UNSUPPORTED)):
+            refused(mk, lambda: mk.mk_rope_apply(r, rope_io(mk, **empty, **over)), status)
+    finally:
+        mk.mk_rope_destroy(r)

@@ -799,3 +799,18 @@ def test_attention_gives_up_and_recovers(cuda_lib, waiting, what, which):
     torch.cuda.synchronize()
     assert cuda_lib.mk_prefix_attn_status(waiting["ws"]) == 0
     assert torch.equal(waiting["out"], waiting["want"])
+
+
+def test_rope_of_an_idle_step(cuda_lib):
+    """A step without rows, through the binding: nothing happens."""
+    pool = torch.full((2, 16, 2, 64), CANARY, dtype=torch.bfloat16, device="cuda")
+    qkv = torch.empty(0, 8, 64, dtype=torch.bfloat16, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    rope = cuda_lib.mk_rope_create(cuda_lib.make_rope_config(64))
+    for q in (qkv[:, :4], None):
+        io = cuda_lib.make_rope_io(q, None if q is None else torch.empty_like(q), qkv[:, 4:6], qkv[:, 6:], none, none.long(), pool, pool.clone())
+        cuda_lib.mk_rope_apply(rope, io)
+    cuda_lib.mk_rope_apply(rope, cuda_lib.make_rope_io(qkv, torch.empty_like(qkv), None, None, none, None, None, None))
+    torch.cuda.synchronize()
+    cuda_lib.mk_rope_destroy(rope)
+    assert bool((pool == CANARY).all())
