@@ -160,6 +160,21 @@ def test_slots_edges(cuda_lib, what):
     check_slots(cuda_lib, cached, new, free, head, table, n_rows, page, n_pages, **kw)
 
 
+@pytest.mark.parametrize("cached,new,spare", [
+    ([5], [131072], 0), ([0, 63, 64, 1000], [70001, 0, 64, 30000], 9), ([100] * 32, [4096] * 32, 1),
+    ([10, 20], [3, 5], 100000)])
+def test_slots_few_requests_many_rows(cuda_lib, cached, new, spare):
+    page = 64
+    held = [-(-c // page) for c in cached]
+    width = max(-(-(c + n) // page) for c, n in zip(cached, new)) + 1
+    n_pages = sum(held) + sum(new) // page + 2 * len(new)
+    ids = np.random.default_rng(sum(new)).permutation(n_pages)
+    table = np.full((len(cached), width), -1)
+    for b, h in enumerate(held):
+        table[b, :h] = ids[sum(held[:b]):sum(held[:b + 1])]
+    check_slots(cuda_lib, cached, new, ids[sum(held):], 0, table, sum(new) + spare, page, n_pages, prefix=7)
+
+
 def test_slots_empty_batch(cuda_lib):
     got = check_slots(cuda_lib, np.zeros(0, int), np.zeros(0, int), np.arange(4), 1,
                       np.zeros((0, 3), int), 5, 16, 10)
@@ -439,6 +454,26 @@ def test_prefix_attn_rows_of_nan(cuda_lib, name):
     assert bool(torch.isnan(a["out"][keys]).all()) and bool(torch.isnan(a["lse"][keys]).all())
     a["out"][keys], a["lse"][keys] = out[keys], lse[keys]
     check_attn(cuda_lib, a)                       # the others, and those without keys
+
+
+def test_prefix_attn_table_with_gaps(cuda_lib):
+    """A block table whose rows are wider than the pages in use (table_stride >
+    max_pages), as a view: the entries beside it are not read."""
+    a = make_attn(np.random.default_rng(12), [300, 45, 1, 700], [8, 3, 1, 2], 130, 8, 2, 128, "bf16", 16)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+    want, lse = a["out"].clone(), a["lse"].clone()
+    rows, cols = a["table"].shape
+    wide = torch.full((rows + 2, cols + 5), 2 ** 30, dtype=torch.int32, device="cuda")
+    view = wide[1:rows + 1, 2:cols + 2]
+    view.copy_(a["keep"][2])
+    io = cuda_lib.make_prefix_attn_io(a["q"], a["k"], a["v"], a["out"], a["keep"][0], a["keep"][1], view, a["keep"][3],
+                                      a["prefix"], lse=a["lse"])
+    assert (io.max_pages, io.table_stride) == (cols, cols + 5)
+    a["whole"].fill_(CANARY)
+    cuda_lib.mk_prefix_attn(io, a["workspace"])
+    check_attn(cuda_lib, a)
+    assert torch.equal(a["out"], want) and torch.equal(a["lse"], lse)
 
 
 def test_prefix_attn_bad_tables_and_lengths(cuda_lib):
