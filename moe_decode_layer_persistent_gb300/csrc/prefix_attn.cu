@@ -239,6 +239,7 @@ struct alignas(1024) TileSmem {
   Plan plan;
   int32_t sum[2][kTileThreads / 32];
   int32_t low[kTileThreads / 32];
+  int32_t low_cu;    // first row of the (last) request with the lowest position of all
   // the first request with work on a line's stretch and where it starts: the
   // CTA's of pairs, the two slots' of solos
   int32_t first_at[3];
@@ -389,9 +390,11 @@ template <> struct Types<__nv_bfloat16> {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&v);
   }
+  static constexpr uint32_t kExponent = 0x7f80;  // all ones: infinity or NaN
 };
 template <> struct Types<__half> {
   static constexpr uint32_t kFormat = 0;
+  static constexpr uint32_t kExponent = 0x7c00;
   static MK_DEV uint32_t pack(float a, float b) {
     __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&v);
@@ -456,15 +459,16 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
   const int each = ceil_div(B, kTileThreads), b0 = threadIdx.x * each, b1 = min(B, b0 + each);
   const int n_used = clampi(io.cu_rows[B], 0, io.n_rows);
   int32_t mine[2] = {0, 0};
-  int low = INT_MAX;
+  int low = INT_MAX, low_cu = 0;
   bool falls = false;  // the lines are measured for rows that belong to one request each
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const Req r = read_req(P, b);
     falls |= io.cu_rows[b + 1] < io.cu_rows[b];
     for (int k = 0; k < 2; ++k) mine[k] += set_cost(P, k, r.n, r.kt1 - r.kt0);
-    if (r.n) low = min(low, r.base);
+    if (r.n && r.base < low) low = r.base, low_cu = r.cu;
   }
+  const int my_low = low;
   int32_t v[2] = {mine[0], mine[1]};
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1)
@@ -486,6 +490,7 @@ MK_DEV void lay_out_work(const AttnParams& P, TileSmem<D>& S) {
     p.total[k] = __reduce_add_sync(0xffffffffu, x);
   }
   low = __reduce_min_sync(0xffffffffu, some ? S.low[lane] : INT_MAX);
+  if (my_low == low) atomicMax(&S.low_cu, low_cu);
   // the lowest position of any row decides where the prefix starts to be seen
   const int64_t lo64 =
       io.window && low != INT_MAX ? static_cast<int64_t>(io.prefix_len) + low - io.window + 1 : 0;
@@ -804,6 +809,22 @@ MK_DEV bool issue_mmas(const AttnParams& P, TileSmem<D>& S, const Ctx<kTest>& c,
 }
 
 // ---- softmax of one slot (a warpgroup, one thread per row)
+// Whether a row of V in shared memory holds an infinity or a NaN.  (A call: inlined, it
+// costs every softmax 2 %.)
+template <class T, int D>
+__device__ __noinline__ bool row_not_finite(const uint8_t* v, int row) {
+  constexpr uint32_t kLow = Types<T>::kExponent, kHigh = kLow << 16;
+  bool found = false;
+#pragma unroll 1
+  for (int x = 0; x < D / 8; ++x) {  // (neighbouring rows start at different banks)
+    const uint4 u = reinterpret_cast<const uint4*>(v + (x >> 3) * 128 * 128)[(x ^ row) & 7];
+    const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) found |= (words[i] & kLow) == kLow || (words[i] & kHigh) == kHigh;
+  }
+  return found;
+}
+
 template <class T, int D, bool kTest>
 MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx<kTest>& c, const View<D>& W,
                     SlotParity& par) {
@@ -858,6 +879,11 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx<kTest>& c, co
       }
     }
     const bool warp_valid = __any_sync(0xffffffffu, valid);
+    // So many keys from klo on may be seen by no row: klo is the window of a row with
+    // no bit but its own, and if the first row of the request that it belongs to is not
+    // one, all windows may start later.
+    const int late =
+        io.tree_mask && io.window && __popcll(io.tree_mask[w.own ? w.cu : S.low_cu]) > 1 ? 63 : 0;
 
     // (The CTA's first tile goes through the motions on what lies in tensor memory,
     // without waiting or leaving anything, while its scores are being made: this
@@ -865,13 +891,16 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx<kTest>& c, co
     float m = -INFINITY, l = 0.f;
     for (int j = par.cold ? -1 : 0; j < n; ++j) {
       const int k0 = (w.kt_a + j) * kTileKeys;
-      if (j >= 0 && (k0 < w.klo || k0 + kTileKeys > w.khi)) {
+      if (j >= 0 && (k0 < w.klo + late || k0 + kTileKeys > w.khi)) {
         // keys that no row sees may hold anything: their V rows become zeros, so
         // that a weight of zero leaves no NaN behind
         const Place sv = at.next(W.stages);
         if (!wait_warp(c, &R.full[sv.st], sv.round)) return false;
-        if (k0 + row < w.klo || k0 + row >= w.khi) {
-          uint8_t* v = W.kv + sv.st * (128 * D * 2) + row * 128;
+        uint8_t* v = W.kv + sv.st * (128 * D * 2) + row * 128;
+        bool unseen = k0 + row < w.klo || k0 + row >= w.khi;
+        // (one that may be seen has to be finite)
+        if (!unseen && k0 + row < w.klo + late) unseen = row_not_finite<T, D>(v, row);
+        if (unseen) {
 #pragma unroll
           for (int x = 0; x < D / 8; ++x)
             reinterpret_cast<uint4*>(v + (x >> 3) * 128 * 128)[x & 7] = make_uint4(0, 0, 0, 0);
@@ -1081,6 +1110,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (lane_id() == 0) {
       mbar_init(&S.turn, 2);
       S.abort = S.drain_abort = 0;
+      S.low_cu = 0;
     }
     fence_mbar_init();
   }

@@ -456,6 +456,30 @@ def test_prefix_attn_rows_of_nan(cuda_lib, name):
     check_attn(cuda_lib, a)                       # the others, and those without keys
 
 
+@pytest.mark.parametrize("window,dtype,d", [(64, "bf16", 64), (100, "fp16", 128), (300, "bf16", 128)])
+def test_prefix_attn_window_of_rows_that_see_one_another(cuda_lib, window, dtype, d):
+    """Tree words in which every row sees rows behind it too, so that no row has
+    depth 0 and the windows of all start later: keys below the lowest window
+    hold NaN, in the prefix and among the requests' own."""
+    a = make_attn(np.random.default_rng(window), [140, 300, 20, 90], [16, 9, 5, 64], 200, 4, 1, d, dtype, 16,
+                  window=window, tree=True)
+    news = [int(m) for m in np.diff(a["cu"])]
+    a["words"] = [(1 << m) - 1 for m in news for _ in range(m)] + [0] * (len(a["words"]) - a["n"])
+    pages, page = a["k"].shape[:2]
+    seen = np.zeros((pages, page), bool)
+    for b, m in enumerate(news):
+        for i in range(m):
+            pre, own = ob.visible(i, m, int(a["lens"][b]), a["prefix"], window, a["words"][int(a["cu"][b]) + i])
+            for j in pre:
+                seen[a["prefix_pages"][j // page], j % page] = True
+            for j in own:
+                seen[a["table"][b, j // page], j % page] = True
+    hide = torch.from_numpy(~seen).cuda()
+    a["k"][hide], a["v"][hide] = float("nan"), float("nan")
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+
+
 def test_prefix_attn_table_with_gaps(cuda_lib):
     """A block table whose rows are wider than the pages in use (table_stride >
     max_pages), as a view: the entries beside it are not read."""
