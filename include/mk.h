@@ -475,13 +475,16 @@ mk_status mk_rope_apply(const mk_rope* rope, const mk_rope_io* io, void* stream)
  * and of all these, with window > 0, only keys at positions > p - window.
  *   out = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j exp(scale q.k_j).
  * A row that sees no key gets out = 0 and lse = -infinity.  Rows before
- * cu_rows[0] and from cu_rows[B] on are left as they are.  Keys that no row sees are never looked
- * at: they may hold anything.  A key that some row sees must be finite.  A row
- * of q that holds a NaN gets NaN, if it sees a key, and no other row does.
- * The prefix is read once for the whole batch, not once per request.
+ * cu_rows[0] and from cu_rows[B] on are left as they are.  Keys that no row sees
+ * do not count: they may hold anything.  A key that some row sees must be finite.
+ * A row of q that holds a NaN gets NaN, if it sees a key, and no other row does.
+ * The prefix is read once per kv head and 256 / group rows of the batch, whichever
+ * requests they are of, not once per request (and from HBM once as long as it fits
+ * the L2 cache).
  *
- * Scores and sums are held in 32 bits; the softmax weights are rounded to the
- * tensors' type before they multiply v.  Two calls on the same inputs give the
+ * Scores and sums are held in 32 bits, for scores scale q.k up to 2^26; the
+ * softmax weights are rounded to the tensors' type before they multiply v (the
+ * layer calls keep 16 bits of them).  Two calls on the same inputs give the
  * same bits.  Work is planned in 32 bits: MK_ERR_UNSUPPORTED where n_kv_heads *
  * (n_rows / (256 / group) + n_requests) * (128-key tiles of prefix and table
  * together) comes to 2^29 or more.  lens outside 0 .. max_pages * page_size

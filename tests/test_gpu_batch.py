@@ -480,6 +480,38 @@ def test_prefix_attn_window_of_rows_that_see_one_another(cuda_lib, window, dtype
     check_attn(cuda_lib, a)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("top", [0, 100, 299, 300, 431])
+def test_prefix_attn_largest_scores(cuda_lib, dtype, top):
+    """Scores up to 2^26, one far above the others: that key's value alone.  Its
+    weight is 2^e, with e the rounding of the row's maximum, and goes into the
+    product rounded, into the sum not; the output is rounded once more.  The score
+    is exact, its product with scale log2(e), the way back and that factor itself
+    round to 32 bits."""
+    a = make_attn(np.random.default_rng(top), [132, 132], [1, 2], 300, 2, 1, 64, dtype, 16)
+    c = np.random.default_rng(top).integers(0, 255, 432)
+    c[top] = 255
+    keys = torch.from_numpy(c * 2.0 ** 8).to(a["k"])           # score: 2^13 * 2^8 c / 8 = 2^18 c
+    a["q"].zero_()
+    a["q"][:, :, 3] = 2.0 ** 13
+    for b in range(2):
+        for j in range(432):
+            page = a["prefix_pages"][j // 16] if j < 300 else a["table"][b, (j - 300) // 16]
+            at = (int(page), j % 16 if j < 300 else (j - 300) % 16)
+            a["k"][at] = 0
+            a["k"][at][0, 3] = keys[j]
+    call_attn(cuda_lib, a)
+    torch.cuda.synchronize()
+    assert cuda_lib.mk_prefix_attn_status(a["workspace"]) == 0
+    for row, b in ((0, 0), (2, 1)) if top == 431 else ((0, 0), (1, 1), (2, 1)):
+        page = a["prefix_pages"][top // 16] if top < 300 else a["table"][b, (top - 300) // 16]
+        v = a["v0"][int(page), top % 16 if top < 300 else (top - 300) % 16, 0]
+        err = np.abs(np64(a["out"])[row] - v)
+        assert np.all(err <= 2.1 * U[dtype] * np.abs(v) + TINY[dtype]), err.max()
+        lse = np64(a["lse"])[row]
+        assert np.all(np.abs(lse - 255 * 2.0 ** 18) <= 8 * V * 255 * 2.0 ** 18), lse
+
+
 def test_prefix_attn_table_with_gaps(cuda_lib):
     """A block table whose rows are wider than the pages in use (table_stride >
     max_pages), as a view: the entries beside it are not read."""
