@@ -987,6 +987,11 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx<kTest>& c, co
           }
           const float ms = m == -INFINITY ? 0.f : m;
           float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          // P goes into the product rounded to the tensors' type, which is all that operand
+          // A takes; its sum is of the 32-bit values. A low part beside it, as the layer
+          // kernel keeps one, would double P V (a pair's products 1.05 -> 1.57 us). Without
+          // it out is off by 0.0023 of its norm in bf16 (0.00029 in fp16), where rounding
+          // out itself leaves 0.0017 (0.00021).
 #pragma unroll
           for (int x = 0; x < kTileKeys; x += 2) {
             float2 y = fma2(make_float2(s[x], s[x + 1]), make_float2(sl2, sl2), make_float2(-ms, -ms));
@@ -1071,8 +1076,9 @@ MK_DEV bool softmax(const AttnParams& P, TileSmem<D>& S, const Ctx<kTest>& c, co
 // unrolled copies, and CTAs without pairs that go to their solos at once, took 1 to
 // 2 us off every call (64 requests over 4096 + up to 1000 keys: 44.5 to 42.6 us).
 // Measured, 32 q heads on 8 KV heads of 128, bf16: 64 x 8 rows over a prefix of
-// 32768 keys run at 1,180 TFLOP/s (a pair of tiles takes 1.55 us, its products alone
-// 1.05); 256 requests' own keys at 6.1 TB/s, 90 % of a plain copy.
+// 32768 keys run at 1,160 TFLOP/s (237 us; a pair of tiles takes 1.55 us, its products
+// alone 1.05); one row of each of 256 requests over 1000 to 2000 keys of its own, 16
+// to a page (1.6 GB), at 6.2 TB/s (255 us), 91 % of a plain copy.
 template <class T, int D, bool kTest>
 __global__ void __launch_bounds__(kTileThreads, 1)
     k_attn_tiles(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap tm_q,
