@@ -26,13 +26,13 @@ def listed():
         # a long prompt, positions scaled by parts, into 4 bits
         dict(name="append-prompt", op="append", rows=8192, q_heads=32, kv_heads=8, dim=128, rot=128, layout="half", scaling="parts", norm=True, bits=4, dtype="bf16", positions=131072, page=64),
         # two short requests on the tiny layer's heads: latency
-        dict(name="kv4-tiny", op="attn", requests=2, new=1, ragged=False, tree=False, own_lo=100, own_hi=500, window=0, q_heads=4, kv_heads=1, dim=64, dtype="bf16", page=16),
+        dict(name="kvq-tiny", op="attn", requests=2, new=1, ragged=False, tree=False, own_lo=100, own_hi=500, window=0, q_heads=4, kv_heads=1, dim=64, dtype="bf16", page=16),
         # plain decoding, one token per request, lengths all over the range
-        dict(name="kv4-decode", op="attn", requests=64, new=1, ragged=False, tree=False, own_lo=32, own_hi=8192, window=0, q_heads=32, kv_heads=8, dim=128, dtype="bf16", page=64),
+        dict(name="kvq-decode", op="attn", requests=64, new=1, ragged=False, tree=False, own_lo=32, own_hi=8192, window=0, q_heads=32, kv_heads=8, dim=128, dtype="bf16", page=64),
         # ragged token trees of 16 requests over the stack's context
-        dict(name="kv4-tree", op="attn", requests=16, new=16, ragged=True, tree=True, own_lo=16, own_hi=16384, window=0, q_heads=32, kv_heads=8, dim=128, dtype="fp16", page=32),
+        dict(name="kvq-tree", op="attn", requests=16, new=16, ragged=True, tree=True, own_lo=16, own_hi=16384, window=0, q_heads=32, kv_heads=8, dim=128, dtype="fp16", page=32),
         # few requests with very long contexts
-        dict(name="kv4-long", op="attn", requests=3, new=2, ragged=True, tree=False, own_lo=60000, own_hi=131072, window=0, q_heads=32, kv_heads=8, dim=128, dtype="bf16", page=128),
+        dict(name="kvq-long", op="attn", requests=3, new=2, ragged=True, tree=False, own_lo=60000, own_hi=131072, window=0, q_heads=32, kv_heads=8, dim=128, dtype="bf16", page=128),
         # the tiny layer's projection of one verify step: latency
         dict(name="linear-tiny", op="linear", rows=2, n_in=256, n_out=384, bias=True, act="none", residual=False, dtype="bf16"),
         # the projection to q, k and v of a decode batch
@@ -194,7 +194,7 @@ def prepare(case, seed):
         s["out"], s["lse"] = torch.empty_like(s["q"]), torch.empty(n, hq, device="cuda", dtype=torch.float32)
         if own:  # the workspace that a program keeps
             from moe_decode_layer_persistent_gb300 import binding as mk
-            s["workspace"] = torch.empty(mk.mk_kv4_attn_workspace(_attn_io(mk, s)), device="cuda", dtype=torch.uint8)
+            s["workspace"] = torch.empty(mk.mk_kvq_attn_workspace(_attn_io(mk, s)), device="cuda", dtype=torch.uint8)
     else:
         m, n, k = c["rows"], c["n_out"], c["n_in"]
         s["x"], s["w"] = rand(m, k), rand(n, k, by=k ** -0.5)
@@ -207,12 +207,12 @@ def prepare(case, seed):
     return s
 
 
-def _kv4(mk, s):
-    return mk.make_kv4_cache(s["kc"], s["ks"], s["vc"], s["vs"], s["k_exp"], s["v_exp"])
+def _kvq(mk, s):
+    return mk.make_kvq_cache(s["kc"], s["ks"], s["vc"], s["vs"], s["k_exp"], s["v_exp"])
 
 
 def _attn_io(mk, s):
-    return mk.make_kv4_attn_io(s["q"], _kv4(mk, s), s["out"], s["lens"], s["cu"], s["table"], window=s["case"]["window"], tree_mask=s["mask"], lse=s["lse"])
+    return mk.make_kvq_attn_io(s["q"], _kvq(mk, s), s["out"], s["lens"], s["cu"], s["table"], window=s["case"]["window"], tree_mask=s["mask"], lse=s["lse"])
 
 
 def _linear_io(mk, s):
@@ -231,13 +231,13 @@ def run(state):
                                            k_cache=s["k_cache"], v_cache=s["v_cache"])
                 mk.mk_qkv_append(s["handle"], io, stream)
                 return {"q_out": s["q_out"], "k": s["k_cache"], "v": s["v_cache"]}
-            kv4 = _kv4(mk, s)
-            io = mk.make_qkv_append_io(s["q"], s["q_out"], s["k"], s["v"], s["positions"], s["slots"], q_norm=s["q_norm"], k_norm=s["k_norm"], kv4=kv4)
+            kvq = _kvq(mk, s)
+            io = mk.make_qkv_append_io(s["q"], s["q_out"], s["k"], s["v"], s["positions"], s["slots"], q_norm=s["q_norm"], k_norm=s["k_norm"], kvq=kvq)
             mk.mk_qkv_append(s["handle"], io, stream)
-            mk.mk_kv4_read(mk.make_kv4_read_io(kv4, None, s["k_values"], s["v_values"]), stream)
+            mk.mk_kvq_read(mk.make_kvq_read_io(kvq, None, s["k_values"], s["v_values"]), stream)
             return {"q_out": s["q_out"], "k": s["k_values"], "v": s["v_values"]}
         if op == "attn":
-            mk.mk_kv4_attn(_attn_io(mk, s), s["workspace"], stream)
+            mk.mk_kvq_attn(_attn_io(mk, s), s["workspace"], stream)
             return {"out": s["out"], "lse": s["lse"]}
         mk.mk_linear(_linear_io(mk, s), s["workspace"], stream)
         return s["out"]
