@@ -129,7 +129,8 @@ def _code_only(text):
 
 
 # sources of the batched operators, no part of the layer kernel
-BATCH_SOURCES = {"batch.h", "slots.cu", "rope.cu", "prefix_attn.cu"}
+BATCH_SOURCES = {"batch.h", "rope.h", "kvq.cuh", "slots.cu", "rope.cu", "prefix_attn.cu", "qkv_append.cu",
+                 "kvq_attn.cu", "linear.cu"}
 
 
 def layer_sources():

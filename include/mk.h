@@ -539,6 +539,194 @@ mk_status mk_prefix_attn(const mk_prefix_attn_io* io, void* workspace, int64_t w
  * after synchronising. */
 mk_status mk_prefix_attn_status(const void* workspace);
 
+/* ====================================================================
+ * The attention half of a batched layer over a paged cache in 4 bits
+ *
+ * mk_linear makes q, k and v of the batch's rows, mk_qkv_append norms and
+ * rotates them and writes k and v into a paged cache, mk_kvq_attn attends,
+ * mk_linear projects back onto the residual stream.  Slots, positions, lens,
+ * cu_rows and block tables are those of mk_build_slots (prefix_len 0: a prefix
+ * that requests share stands in each of their tables).  The conventions are
+ * those of the batched calls above.
+ *
+ * A cache in 4 bits: of each token and kv head the head_dim values lie in groups
+ * of 16; each group has an E4M3 scale s, each head a power of two 2^e, and the
+ * code n (0 .. 15) stands for (n - 8) s 2^e.  Pools, in order of
+ *   codes   uint8 [n_pages, n_kv_heads, page_size, head_dim / 2], value 2i in the
+ *           low nibble of byte i
+ *   scales  uint8 [n_pages, n_kv_heads, page_size, head_dim / 16]
+ * The slot page * page_size + offset is the row (page, :, offset).
+ * ==================================================================== */
+
+typedef struct mk_kvq_cache {
+  int32_t n_pages;        /* n_pages * page_size < 2^31                           */
+  int32_t page_size;      /* a power of two, 16 .. 65536                          */
+  int32_t n_kv_heads;     /* <= 4096                                              */
+  int32_t head_dim;       /* d: a multiple of 16, <= 256                          */
+  void* k_codes;          /* the pools; 16-byte aligned                           */
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  const int32_t* k_exp;   /* optional [n_kv_heads]: e of each head's keys, -64 ..
+                             64 (others count as the nearer end); NULL = 0        */
+  const int32_t* v_exp;   /* the same of its values                               */
+} mk_kvq_cache;
+
+/* Norms of q and k, rotary positions and the K/V write in one pass.
+ *
+ * Of each head x (with a norm weight w):
+ *   n_i = x_i w_i / sqrt(mean_j x_j^2 + eps),
+ * then the rotation of mk_rope_apply by the row's position (rope NULL: none).
+ * q goes to q_out, rounded once.  k and v (v as it is) go to the row's slot: with
+ * bits 16 into k_cache and v_cache as in mk_rope_apply, rounded once; with bits 4
+ * into kvq: of each group z_i = y_i 2^-e of 16 values
+ *   s = E4M3(max |z| / 7) to nearest even, at most 448,
+ *   n_i = min(max(rint(z_i / s), -8), 7) + 8   (8 where s is 0).
+ * These are the codes of the formula: sums and angles are held in 32 bits, and
+ * where a value comes so near a border between two codes or scales that this
+ * could tell, the group is worked out again in 64 bits.  A group that holds a NaN
+ * gets the scale NaN (0x7F) and the codes 8; infinities saturate.
+ * A row whose slot is outside the pool writes nothing there; slots are distinct.
+ * q_out may be q itself (same stride); any other overlap of inputs and outputs is
+ * not allowed, k and v in the very cache rows that slots names (bits 16) apart. */
+typedef struct mk_qkv_append_io {
+  int32_t n_rows;            /* >= 0; with 0 every tensor of rows may be NULL      */
+  int32_t n_q_heads;         /* 0 iff q is NULL; <= 4096                           */
+  int32_t n_kv_heads;        /* 0 iff k is NULL; <= 4096                           */
+  int32_t head_dim;          /* d: a multiple of 8 (bits 4: 16), <= 256            */
+  int32_t dtype;             /* mk_dtype of q, k, v, the norm weights, the caches
+                                in 16 bits                                         */
+  int32_t bits;              /* 16 or 4: the cache's                               */
+  float eps;                 /* >= 0; looked at with a norm weight only            */
+  const void* q;             /* [n_rows, n_q_heads, d]; optional                   */
+  int64_t q_stride;          /* elements between rows, a multiple of 8             */
+  void* q_out;               /* [n_rows, n_q_heads, d]                             */
+  int64_t q_out_stride;
+  const void* k;             /* [n_rows, n_kv_heads, d]; optional                  */
+  int64_t k_stride;
+  const void* v;             /* [n_rows, n_kv_heads, d]; optional: the cache's
+                                values are left as they are                        */
+  int64_t v_stride;
+  const int32_t* positions;  /* [n_rows]; required with rope                       */
+  const int64_t* slots;      /* [n_rows]; required with k                          */
+  const void* q_norm;        /* optional [d]: w of the q heads                     */
+  const void* k_norm;        /* optional [d]: w of the k heads                     */
+  void* k_cache;             /* bits 16: [n_slots, n_kv_heads, d]                  */
+  void* v_cache;
+  int64_t n_slots;           /* bits 16                                            */
+  mk_kvq_cache kvq;          /* bits 4                                             */
+} mk_qkv_append_io;
+mk_status mk_qkv_append(const mk_rope* rope, const mk_qkv_append_io* io, void* stream);
+
+/* The values that rows of a cache in 4 bits stand for, in 16 bits: row i of k_out
+ * and v_out is slot slots[i], or slot i where slots is NULL (then n_rows is at most
+ * the pool's slots).  A slot outside the pool reads as zeros.  bf16 holds every
+ * (n - 8) s exactly, fp16 as well; 2^e may round or overflow there. */
+typedef struct mk_kvq_read_io {
+  mk_kvq_cache kvq;
+  int32_t n_rows;            /* >= 0                                               */
+  int32_t dtype;             /* mk_dtype of k_out and v_out                        */
+  const int64_t* slots;      /* optional [n_rows]                                  */
+  void* k_out;               /* [n_rows, n_kv_heads, d], contiguous; optional       */
+  void* v_out;               /* the same; optional                                 */
+} mk_kvq_read_io;
+mk_status mk_kvq_read(const mk_kvq_read_io* io, void* stream);
+
+/* Attention over a paged cache in 4 bits.
+ *
+ * Request b has n_b = cu_rows[b+1] - cu_rows[b] rows and lens[b] keys, the last
+ * n_b of which are its rows' own.  With base = max(0, lens[b] - n_b) its row i has
+ * the position p = base + i and sees the keys j < lens[b] with j <= p; with
+ * tree_mask p = base + popcount(mask) - 1 and it sees the keys j < base and those
+ * j >= base whose bit j - base is set (bits of keys that are not there are
+ * ignored); and of all these, with window > 0, only keys at positions > p - window
+ * (key j is at position j).
+ *   out = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j exp(scale q.k_j).
+ * A row that sees no key gets out = 0 and lse = -infinity.  Rows before cu_rows[0]
+ * and from cu_rows[B] on are left as they are.  Keys that no row sees do not count:
+ * their codes and scales may be anything.  A key that some row sees must have
+ * finite scales.  A row of q that holds a NaN gets NaN, if it sees a key, and no
+ * other row does.
+ *
+ * Keys and values come into the products exactly; q is held in 11 bits relative to
+ * its row's largest value or better; the softmax weights are rounded to fp16 (11
+ * bits) before they multiply v; scores, maxima, sums and out are held in 32 bits
+ * and out is rounded once.  Two calls on the same inputs give the same bits.
+ * lens outside 0 .. max_pages * page_size and cu_rows outside 0 .. n_rows are
+ * taken as the nearer end, and a page outside 0 .. n_pages-1 reads as zeros.  A
+ * cu_rows that falls leaves out and lse undefined. */
+typedef struct mk_kvq_attn_io {
+  int32_t n_requests;          /* B, 1 .. 65536                                   */
+  int32_t n_rows;              /* rows of q, >= 0                                 */
+  int32_t n_q_heads;           /* a multiple of kvq.n_kv_heads, at most 64 per kv
+                                  head                                            */
+  int32_t dtype;               /* mk_dtype of q and out                           */
+  int32_t max_pages;           /* pages per row of block_table, >= 0              */
+  int32_t window;              /* 0 = every key; with tree_mask 0 or >= 64        */
+  float scale;                 /* of the scores; 0 selects 1 / sqrt(d)            */
+  int64_t table_stride;        /* entries between rows of block_table             */
+  mk_kvq_cache kvq;            /* head_dim 64 or 128                              */
+  const void* q;               /* [n_rows, n_q_heads, d], 16-byte aligned         */
+  int64_t q_stride;            /* elements between rows, a multiple of 8          */
+  const int32_t* block_table;  /* [B, max_pages]                                  */
+  const int32_t* lens;         /* [B]                                             */
+  const int32_t* cu_rows;      /* [B + 1]                                         */
+  const uint64_t* tree_mask;   /* optional [n_rows], as for mk_prefix_attn        */
+  void* out;                   /* [n_rows, n_q_heads, d]; not q                   */
+  int64_t out_stride;          /* elements between rows, a multiple of 8          */
+  float* lse;                  /* optional [n_rows, n_q_heads]                    */
+} mk_kvq_attn_io;
+
+/* Bytes of workspace for every call with these n_requests, n_rows, heads and
+ * head_dim (pointers are not looked at), on the current device. */
+mk_status mk_kvq_attn_workspace(const mk_kvq_attn_io* io, int64_t* bytes);
+
+/* workspace: device memory, 256-byte aligned, its content does not matter; one
+ * call in flight per workspace. */
+mk_status mk_kvq_attn(const mk_kvq_attn_io* io, void* workspace, int64_t workspace_bytes,
+                      void* stream);
+
+/* Device status of the last mk_kvq_attn that used `workspace`: MK_OK, or
+ * MK_ERR_TIMEOUT if a bounded device-side wait expired (out and lse are then
+ * undefined).  Reads a device word synchronously: call after synchronising. */
+mk_status mk_kvq_attn_status(const void* workspace);
+
+/* Projection with bias, activation and residual:
+ *   out = act(x w^T + bias) + residual,
+ * summed in 32 bits and rounded once.  MK_ACT_SILU: y / (1 + e^-y);
+ * MK_ACT_GELU: y (1 + erf(y / sqrt 2)) / 2; MK_ACT_GELU_TANH: y (1 + tanh(sqrt(2 / pi)
+ * (y + 0.044715 y^3))) / 2.  residual may be out itself (same stride); any other
+ * overlap of an input with out is not allowed.  Two calls on the same inputs give
+ * the same bits. */
+typedef enum { MK_ACT_NONE = 0, MK_ACT_SILU = 1, MK_ACT_GELU = 2, MK_ACT_GELU_TANH = 3 } mk_act;
+
+typedef struct mk_linear_io {
+  int32_t n_rows;          /* >= 0; with 0 x, residual and out may be NULL        */
+  int32_t n_in;            /* a multiple of 8, >= 8                               */
+  int32_t n_out;           /* >= 1                                                */
+  int32_t dtype;           /* mk_dtype, of every tensor                           */
+  int32_t act;             /* mk_act                                              */
+  const void* x;           /* [n_rows, n_in], 16-byte aligned                     */
+  int64_t x_stride;        /* elements between rows, a multiple of 8              */
+  const void* w;           /* [n_out, n_in], 16-byte aligned                      */
+  int64_t w_stride;        /* the same                                            */
+  const void* bias;        /* optional [n_out]                                    */
+  const void* residual;    /* optional [n_rows, n_out]                            */
+  int64_t residual_stride; /* elements between rows, >= n_out                     */
+  void* out;               /* [n_rows, n_out]                                     */
+  int64_t out_stride;      /* elements between rows, >= n_out                     */
+} mk_linear_io;
+
+/* Bytes of workspace for every call with these sizes (pointers and strides are not
+ * looked at), on the current device. */
+mk_status mk_linear_workspace(const mk_linear_io* io, int64_t* bytes);
+
+/* workspace: as for mk_kvq_attn. */
+mk_status mk_linear(const mk_linear_io* io, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Device status of the last mk_linear that used `workspace`: as mk_kvq_attn_status. */
+mk_status mk_linear_status(const void* workspace);
+
 #ifdef __cplusplus
 }
 #endif

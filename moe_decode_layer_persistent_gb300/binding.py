@@ -30,6 +30,7 @@ MK_ERR_INVALID_ARG = 1
 MK_BF16, MK_FP16 = 0, 1
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
 
 _vp = ctypes.c_void_p
 
@@ -125,6 +126,40 @@ class mk_prefix_attn_io(ctypes.Structure):
                 ("out_stride", _i64), ("lse", _vp)]
 
 
+class mk_kvq_cache(ctypes.Structure):
+    _fields_ = [("n_pages", _i32), ("page_size", _i32), ("n_kv_heads", _i32), ("head_dim", _i32),
+                ("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp),
+                ("k_exp", _vp), ("v_exp", _vp)]
+
+
+class mk_qkv_append_io(ctypes.Structure):
+    _fields_ = [("n_rows", _i32), ("n_q_heads", _i32), ("n_kv_heads", _i32), ("head_dim", _i32),
+                ("dtype", _i32), ("bits", _i32), ("eps", ctypes.c_float),
+                ("q", _vp), ("q_stride", _i64), ("q_out", _vp), ("q_out_stride", _i64),
+                ("k", _vp), ("k_stride", _i64), ("v", _vp), ("v_stride", _i64),
+                ("positions", _vp), ("slots", _vp), ("q_norm", _vp), ("k_norm", _vp),
+                ("k_cache", _vp), ("v_cache", _vp), ("n_slots", _i64), ("kvq", mk_kvq_cache)]
+
+
+class mk_kvq_read_io(ctypes.Structure):
+    _fields_ = [("kvq", mk_kvq_cache), ("n_rows", _i32), ("dtype", _i32), ("slots", _vp),
+                ("k_out", _vp), ("v_out", _vp)]
+
+
+class mk_kvq_attn_io(ctypes.Structure):
+    _fields_ = [("n_requests", _i32), ("n_rows", _i32), ("n_q_heads", _i32), ("dtype", _i32),
+                ("max_pages", _i32), ("window", _i32), ("scale", ctypes.c_float),
+                ("table_stride", _i64), ("kvq", mk_kvq_cache), ("q", _vp), ("q_stride", _i64),
+                ("block_table", _vp), ("lens", _vp), ("cu_rows", _vp), ("tree_mask", _vp),
+                ("out", _vp), ("out_stride", _i64), ("lse", _vp)]
+
+
+class mk_linear_io(ctypes.Structure):
+    _fields_ = [("n_rows", _i32), ("n_in", _i32), ("n_out", _i32), ("dtype", _i32), ("act", _i32),
+                ("x", _vp), ("x_stride", _i64), ("w", _vp), ("w_stride", _i64), ("bias", _vp),
+                ("residual", _vp), ("residual_stride", _i64), ("out", _vp), ("out_stride", _i64)]
+
+
 def _sig(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -174,6 +209,16 @@ _lib_mk_prefix_attn_status = _sig("mk_prefix_attn_status", _c.c_int, [_vp])
 _lib_mk_selftest_attn_waits = _sig("mk_selftest_attn_waits", _c.c_int,
                                    [_c.POINTER(mk_prefix_attn_io), _vp, _i64, _c.c_uint64, _i32,
                                     _i32, _vp])
+_lib_mk_qkv_append = _sig("mk_qkv_append", _c.c_int, [_vp, _c.POINTER(mk_qkv_append_io), _vp])
+_lib_mk_kvq_read = _sig("mk_kvq_read", _c.c_int, [_c.POINTER(mk_kvq_read_io), _vp])
+_lib_mk_kvq_attn_workspace = _sig("mk_kvq_attn_workspace", _c.c_int,
+                                  [_c.POINTER(mk_kvq_attn_io), _c.POINTER(_i64)])
+_lib_mk_kvq_attn = _sig("mk_kvq_attn", _c.c_int, [_c.POINTER(mk_kvq_attn_io), _vp, _i64, _vp])
+_lib_mk_kvq_attn_status = _sig("mk_kvq_attn_status", _c.c_int, [_vp])
+_lib_mk_linear_workspace = _sig("mk_linear_workspace", _c.c_int,
+                                [_c.POINTER(mk_linear_io), _c.POINTER(_i64)])
+_lib_mk_linear = _sig("mk_linear", _c.c_int, [_c.POINTER(mk_linear_io), _vp, _i64, _vp])
+_lib_mk_linear_status = _sig("mk_linear_status", _c.c_int, [_vp])
 
 EXPORTED = ["mk_layer_create", "mk_decode_step", "mk_decode_step_noalloc", "mk_layer_status", "mk_layer_clear_status",
             "mk_layer_destroy", "mk_stack_create", "mk_stack_step", "mk_stack_status",
@@ -181,6 +226,8 @@ EXPORTED = ["mk_layer_create", "mk_decode_step", "mk_decode_step_noalloc", "mk_l
             "mk_layer_prefetch_stats", "mk_stack_prefetch_stats",
             "mk_build_slots", "mk_rope_create", "mk_rope_destroy", "mk_rope_apply",
             "mk_prefix_attn_workspace", "mk_prefix_attn", "mk_prefix_attn_status",
+            "mk_qkv_append", "mk_kvq_read", "mk_kvq_attn_workspace", "mk_kvq_attn", "mk_kvq_attn_status",
+            "mk_linear_workspace", "mk_linear", "mk_linear_status",
             "mk_selftest_quantize", "mk_selftest_mma", "mk_selftest_sync", "mk_selftest_attn_waits"]
 
 
@@ -390,6 +437,12 @@ _torch = None
 _pack_slots = struct.Struct("@4iqiii11P").pack
 _pack_rope = struct.Struct("@5iPqPqPqPqPPPPq").pack
 _pack_attn = struct.Struct("@10iqifPqPPPPPPPPqP").pack
+# (those of mk_kvq_cache, 4i6P, inside the others' without padding: 8-byte aligned)
+_pack_kvq = struct.Struct("@4i6P").pack
+_pack_append = struct.Struct("@6if" + "Pq" * 4 + "6Pq64s").pack
+_pack_read = struct.Struct("@64s2i3P").pack
+_pack_kvq_attn = struct.Struct("@6ifq64sPq5PqP").pack
+_pack_linear = struct.Struct("@5iPqPqPPqPq").pack
 
 
 def _load_torch():
@@ -592,3 +645,190 @@ def mk_selftest_attn_waits(io, workspace, wait_ns, withhold="nothing", which=0, 
     return _lib_mk_selftest_attn_waits(
         ctypes.byref(io), workspace.data_ptr(), workspace.numel() * workspace.element_size(), wait_ns,
         WITHHOLD[withhold], which, _stream(stream))
+
+
+# ------------------------- the attention half of a layer over a cache in 4 bits
+
+def make_kvq_cache(k_codes, k_scales, v_codes, v_scales, k_exp=None, v_exp=None):
+    """mk_kvq_cache of CUDA tensors: codes uint8 [pages, kv heads, page_size, d/2],
+    scales uint8 [pages, kv heads, page_size, d/16], exps int32 [kv heads] or None."""
+    fn = "make_kvq_cache"
+    T = _torch or _load_torch()
+    u8, dev = T.uint8, _device_of(fn, k_codes)
+    shape = k_codes.shape
+    if len(shape) != 4:
+        _refuse(fn)
+    pages, heads, page, half = shape
+    groups = (pages, heads, page, half // 8)
+    if half % 8 or v_codes.shape != shape or k_scales.shape != groups or v_scales.shape != groups:
+        _refuse(fn)
+    c = mk_kvq_cache.from_buffer_copy(_pack_kvq(
+        pages, page, heads, 2 * half, _vec(fn, k_codes, u8, dev), _vec(fn, k_scales, u8, dev),
+        _vec(fn, v_codes, u8, dev), _vec(fn, v_scales, u8, dev), _vec(fn, k_exp, T.int32, dev, heads),
+        _vec(fn, v_exp, T.int32, dev, heads)))
+    c.device = dev  # (an attribute beside the fields: other tensors have to be there too)
+    return c
+
+
+def _kvq_on(fn, kvq, dev):
+    if getattr(kvq, "device", dev) != dev:
+        _refuse(fn)
+    return bytes(kvq)
+
+
+def make_qkv_append_io(q, q_out, k, v, positions, slots, q_norm=None, k_norm=None, eps=1e-6,
+                       k_cache=None, v_cache=None, kvq=None):
+    """mk_qkv_append_io of CUDA tensors: q, q_out [rows, q heads, d], k, v [rows, kv
+    heads, d] (views with a row stride), positions int32 (None without a rotation),
+    slots int64, norms [d]; the cache as [pages, page_size, kv heads, d] tensors or
+    as a mk_kvq_cache.  q or k (with v) may be None."""
+    fn = "make_qkv_append_io"
+    T = _torch or _load_torch()
+    like = q if q is not None else k
+    if like is None or like.dim() != 3 or (k is None and v is not None):
+        _refuse(fn)
+    dt, dev = like.dtype, _device_of(fn, like)
+    n, hq, d = like.shape
+    qp = qop = kp = vp = kc = vc = qs = qos = ks = vs = hk = n_slots = 0
+    bits, four = 16, bytes(64)
+    if q is not None:
+        qp, qs = _rows(fn, q, q.shape, dt, dev)
+        qop, qos = _rows(fn, q_out, q.shape, dt, dev)
+    else:
+        hq = 0
+    if k is not None:
+        hk = k.shape[1]
+        kp, ks = _rows(fn, k, (n, hk, d), dt, dev)
+        if v is not None:
+            vp, vs = _rows(fn, v, (n, hk, d), dt, dev)
+        if kvq is not None:
+            bits, four = 4, _kvq_on(fn, kvq, dev)
+            if kvq.n_kv_heads != hk or kvq.head_dim != d or k_cache is not None or v_cache is not None:
+                _refuse(fn)
+        else:
+            kc = _vec(fn, k_cache, dt, dev)
+            pool = k_cache.shape if k_cache is not None else ()
+            if len(pool) != 4 or pool[2] != hk or pool[3] != d:
+                _refuse(fn)
+            n_slots = pool[0] * pool[1]
+            if v is not None:
+                vc = _vec(fn, v_cache, dt, dev)
+                if v_cache is None or v_cache.shape != pool:
+                    _refuse(fn)
+    return mk_qkv_append_io.from_buffer_copy(_pack_append(
+        n, hq, hk, d, _kind(fn, T, like), bits, eps, qp, qs, qop, qos, kp, ks, vp, vs,
+        _vec(fn, positions, T.int32, dev, n), _vec(fn, slots, T.int64, dev, n),
+        _vec(fn, q_norm, dt, dev, d), _vec(fn, k_norm, dt, dev, d), kc, vc, n_slots, four))
+
+
+def mk_qkv_append(rope, io, stream=None):
+    """rope: of mk_rope_create, or None (no rotation)."""
+    _check("mk_qkv_append", _lib_mk_qkv_append(rope, ctypes.byref(io), _stream(stream)))
+
+
+def make_kvq_read_io(kvq, slots, k_out, v_out):
+    """mk_kvq_read_io: rows `slots` (int64; None: all, in order) of the cache as
+    k_out, v_out [rows, kv heads, d], bf16 or fp16; either may be None."""
+    fn = "make_kvq_read_io"
+    T = _torch or _load_torch()
+    like = k_out if k_out is not None else v_out
+    if like is None:
+        _refuse(fn)
+    dt, dev = like.dtype, _device_of(fn, like)
+    n = kvq.n_pages * kvq.page_size if slots is None else slots.numel()
+    size = n * kvq.n_kv_heads * kvq.head_dim
+    return mk_kvq_read_io.from_buffer_copy(_pack_read(
+        _kvq_on(fn, kvq, dev), n, _kind(fn, T, like), _vec(fn, slots, T.int64, dev),
+        _vec(fn, k_out, dt, dev, size), _vec(fn, v_out, dt, dev, size)))
+
+
+def mk_kvq_read(io, stream=None):
+    _check("mk_kvq_read", _lib_mk_kvq_read(ctypes.byref(io), _stream(stream)))
+
+
+def make_kvq_attn_io(q, kvq, out, lens, cu_rows, block_table, window=0, scale=0.0, tree_mask=None,
+                     lse=None):
+    """mk_kvq_attn_io of CUDA tensors: q, out [rows, q heads, d] (views with a row
+    stride), lens, cu_rows, block_table [requests, pages] int32, tree_mask int64
+    [rows], lse float32 [rows, q heads]."""
+    fn = "make_kvq_attn_io"
+    T = _torch or _load_torch()
+    i32, dt, dev = T.int32, q.dtype, _device_of(fn, q)
+    shape = q.shape
+    if len(shape) != 3 or kvq.head_dim != shape[2]:
+        _refuse(fn)
+    n, hq, _ = shape
+    qp, qs = _rows(fn, q, shape, dt, dev)
+    op, os_ = _rows(fn, out, shape, dt, dev)
+    table, b, cols, stride = _table(fn, block_table, i32, dev)
+    io = mk_kvq_attn_io.from_buffer_copy(_pack_kvq_attn(
+        b, n, hq, _kind(fn, T, q), cols, window, scale, stride, _kvq_on(fn, kvq, dev), qp, qs, table,
+        _vec(fn, lens, i32, dev, b), _vec(fn, cu_rows, i32, dev, b + 1),
+        _vec(fn, tree_mask, T.int64, dev, n), op, os_, _vec(fn, lse, T.float32, dev, n * hq)))
+    io.device = dev
+    return io
+
+
+def _with_workspace(fn, call, io, workspace, stream):
+    if not workspace.is_contiguous() or workspace.get_device() != getattr(io, "device", workspace.get_device()):
+        _refuse(fn)
+    _check(fn, call(ctypes.byref(io), workspace.data_ptr(),
+                    workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def mk_kvq_attn_workspace(io):
+    out = _i64()
+    _check("mk_kvq_attn_workspace",
+           _lib_mk_kvq_attn_workspace(ctypes.byref(io), ctypes.byref(out)))
+    return out.value
+
+
+def mk_kvq_attn(io, workspace, stream=None):
+    _with_workspace("mk_kvq_attn", _lib_mk_kvq_attn, io, workspace, stream)
+
+
+def mk_kvq_attn_status(workspace):
+    return _lib_mk_kvq_attn_status(_ptr(workspace))
+
+
+def _matrix(fn, t, rows, cols, dtype, dev):
+    """(address, elements between rows) of a [rows, cols] matrix with contiguous rows."""
+    if t.shape != (rows, cols) or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(fn)
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        _refuse(fn)
+    return t.data_ptr(), s0 if rows > 1 else max(s0, -(-cols // 8) * 8)
+
+
+def make_linear_io(x, w, out, bias=None, act="none", residual=None):
+    """mk_linear_io of CUDA tensors: x [rows, in], w [out, in], out and residual
+    [rows, out] (views with a row stride), bias [out]."""
+    fn = "make_linear_io"
+    T = _torch or _load_torch()
+    dt, dev = x.dtype, _device_of(fn, x)
+    if x.dim() != 2 or w.dim() != 2:
+        _refuse(fn)
+    (m, k), n = x.shape, w.shape[0]
+    xp, xs = _matrix(fn, x, m, k, dt, dev)
+    wp, ws = _matrix(fn, w, n, k, dt, dev)
+    op, os_ = _matrix(fn, out, m, n, dt, dev)
+    rp, rs = _matrix(fn, residual, m, n, dt, dev) if residual is not None else (0, 0)
+    io = mk_linear_io.from_buffer_copy(_pack_linear(
+        m, k, n, _kind(fn, T, x), ACTS[act], xp, xs, wp, ws, _vec(fn, bias, dt, dev, n), rp, rs, op, os_))
+    io.device = dev
+    return io
+
+
+def mk_linear_workspace(io):
+    out = _i64()
+    _check("mk_linear_workspace", _lib_mk_linear_workspace(ctypes.byref(io), ctypes.byref(out)))
+    return out.value
+
+
+def mk_linear(io, workspace, stream=None):
+    _with_workspace("mk_linear", _lib_mk_linear, io, workspace, stream)
+
+
+def mk_linear_status(workspace):
+    return _lib_mk_linear_status(_ptr(workspace))

@@ -1,0 +1,560 @@
+// qkv_append.cu -- norms of q and k, rotary positions and the write into a paged
+// cache of 16 or 4 bits in one pass (mk_qkv_append), and rows of a cache in 4 bits
+// as values again (mk_kvq_read).
+//
+// Of a head x, with r = 1 / sqrt(mean x^2 + eps), weights w and the angle t of a
+// pair (a, b):
+//   y_a = r (x_a (w_a m cos t) - x_b (w_b m sin t)),
+//   y_b = r (x_b (w_b m cos t) + x_a (w_a m sin t)).
+// A team of lanes holds a head, 8 values each, so that the brackets are the same
+// for every head of a row that a thread works on: they are made once per row.
+#include <algorithm>
+#include <climits>
+#include <math_constants.h>
+
+#include "kvq.cuh"
+#include "rope.h"
+
+namespace mk {
+
+namespace {
+
+struct AppendParams {
+  mk_qkv_append_io io;
+  int32_t d, rot;     // rot 0: no rotation
+  int32_t team;       // lanes per head: the power of two from d / 8 on
+  int32_t page_shift;
+  float m, by_d;  // by_d: 1 / d
+  double m64;
+  uint64_t turns[128];
+};
+
+// Cosine and sine of phase / 2^64 turns.  The nearest quarter turn is taken off
+// first: what is left is at most 2^-25 rad off in 32 bits.
+MK_DEV float2 cos_sin(uint64_t phase) {
+  const uint32_t u = static_cast<uint32_t>(phase >> 32);
+  const uint32_t quarter = (u + (1u << 29)) >> 30;
+  const float half_turns = static_cast<float>(static_cast<int32_t>(u - (quarter << 30))) * 0x1p-31f;
+  float s, c;
+  sincospif(half_turns, &s, &c);
+  const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+  return make_float2((quarter + 1) & 2 ? -x : x, quarter & 2 ? -y : y);
+}
+
+template <class T>
+MK_DEV void unpack8(const uint4& raw, float (&x)[8]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = Pack<T>::get(w[i]);
+    x[2 * i] = v.x;
+    x[2 * i + 1] = v.y;
+  }
+}
+template <class T>
+MK_DEV uint4 pack8(const float (&y)[8]) {
+  return make_uint4(Pack<T>::put(y[0], y[1]), Pack<T>::put(y[2], y[3]), Pack<T>::put(y[4], y[5]),
+                    Pack<T>::put(y[6], y[7]));
+}
+
+// What 8 values of every q head, or of every k head, of a row are multiplied with:
+// themselves by a, their partners by b.
+struct Turn {
+  float a[8], b[8];
+  bool turns;
+  float top, partner_top;  // bounds of |a| and |b|
+};
+
+template <class T, int LAYOUT>
+MK_DEV Turn make_turn(const AppendParams& P, const void* weights, const float2* cs, int l, int from) {
+  Turn t;
+  float w[8], wp[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = wp[i] = 1.f;
+  const bool turns = t.turns = l < P.rot / 8;
+  if (weights && l * 8 < P.d) {
+    unpack8<T>(reinterpret_cast<const uint4*>(weights)[l], w);
+    if (LAYOUT == MK_ROPE_HALF) unpack8<T>(reinterpret_cast<const uint4*>(weights)[from], wp);
+  }
+  if (LAYOUT == MK_ROPE_INTERLEAVED)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wp[i] = w[i ^ 1];
+  t.top = t.partner_top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t.top = fmaxf(t.top, fabsf(w[i]));
+    t.partner_top = fmaxf(t.partner_top, fabsf(wp[i]));
+    t.a[i] = w[i];
+    t.b[i] = 0.f;
+    if (!turns) continue;
+    const bool second = LAYOUT == MK_ROPE_HALF ? l >= P.rot / 16 : i & 1;
+    const float2 c = cs[LAYOUT == MK_ROPE_HALF ? (second ? l - P.rot / 16 : l) * 8 + i : l * 4 + i / 2];
+    t.a[i] = w[i] * c.x;
+    t.b[i] = second ? wp[i] * c.y : -wp[i] * c.y;
+  }
+  if (turns) t.top *= P.m, t.partner_top *= P.m;
+  else t.partner_top = 0.f;
+  return t;
+}
+
+// The 8 values z of lane l (of two that hold a group) in 64 bits.
+template <class T, int LAYOUT>
+__device__ __noinline__ void exact_values(const AppendParams& P, const T* x, const T* w, int32_t pos, int l,
+                                          int e, double* z) {
+  double r = 1.0;
+  if (w) {
+    double sum = 0.0;
+    for (int i = 0; i < P.d; ++i) {
+      const double v = static_cast<float>(x[i]);
+      sum += v * v;
+    }
+    r = 1.0 / sqrt(sum / P.d + static_cast<double>(P.io.eps));
+  }
+  const double unit = r * static_cast<double>(pow2(-e));
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const int at = l * 8 + i;
+    const double own = static_cast<double>(static_cast<float>(x[at])) * (w ? static_cast<double>(static_cast<float>(w[at])) : 1.0);
+    if (at >= P.rot) {
+      z[i] = own * unit;
+      continue;
+    }
+    const bool half = LAYOUT == MK_ROPE_HALF;
+    const bool second = half ? at >= P.rot / 2 : at & 1;
+    const int to = half ? (second ? at - P.rot / 2 : at + P.rot / 2) : at ^ 1;
+    const int pair = half ? min(at, to) : at / 2;
+    const double other = static_cast<double>(static_cast<float>(x[to])) * (w ? static_cast<double>(static_cast<float>(w[to])) : 1.0);
+    const int64_t phase = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[pair]);
+    double s, c;
+    sincospi(static_cast<double>(phase) * 0x1p-63, &s, &c);
+    z[i] = (own * c + (second ? other : -other) * s) * P.m64 * unit;
+  }
+}
+
+// A double to the E4M3 scale nearest to a seventh of it: through a float that is
+// odd where it is not exact, so that it is rounded once.
+MK_DEV uint32_t exact_scale(double top) {
+  const double q = top / 7.0;
+  float f = __double2float_rz(q);
+  if (static_cast<double>(f) != q) f = __uint_as_float(__float_as_uint(f) | 1u);
+  return floats_to_e4m3x2(f, 0.f) & 0xFFu;
+}
+
+// Codes of 8 values (value i in bits 4i ..) and the scale of their group; the
+// lane's neighbour has the group's other 8.
+template <class T, int LAYOUT, bool MADE>
+MK_DEV uint2 quantise(const AppendParams& P, float (&z)[8], float off, const T* x, const T* w, int32_t pos, int l,
+                      int e) {
+  float top = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    nan |= z[i] != z[i];
+    top = fmaxf(top, fabsf(z[i]));
+  }
+  if (nan) top = CUDART_NAN_F;
+  const float other = __shfl_xor_sync(0xffffffffu, top, 1);
+  nan |= other != other;
+  top = fmaxf(top, other);
+  const float seventh = __fdiv_rn(top, 7.f);
+  uint32_t scale = floats_to_e4m3x2(seventh, 0.f) & 0xFFu;
+  const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_half2(scale) & 0xFFFFu)));
+  uint32_t word = 0;
+  bool near = false;
+  if (MADE) {
+    off = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, 1));
+    const uint32_t both = floats_to_e4m3x2(seventh - off, seventh + off);
+    near = (both & 0xFFu) != (both >> 8);
+  }
+  const float room = MADE && s > 0.f ? 0.5f - __fdividef(off, s) - 0x1p-20f : 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = s > 0.f ? __fdiv_rn(z[i], s) : 0.f;
+    const float n = rintf(t);
+    if (MADE) near |= s > 0.f && !(fabsf(t - n) <= room) && fabsf(t) < 9.f;
+    word |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(n, -8.f), 7.f)) + 8) << (4 * i);
+  }
+  if (MADE) {
+    // (about one row of 40 has such a group)
+    near = near && !nan;
+    near = __shfl_xor_sync(0xffffffffu, static_cast<int>(near), 1) || near;
+    if (near) {
+      double y[8], big = 0.0;
+      exact_values<T, LAYOUT>(P, x, w, pos, l, e, y);
+      for (int i = 0; i < 8; ++i) big = fmax(big, fabs(y[i]));
+      big = fmax(big, __shfl_xor_sync(3u << (lane_id() & 30), big, 1));
+      scale = exact_scale(big);
+      const double u = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_half2(scale) & 0xFFFFu)));
+      word = 0;
+      for (int i = 0; i < 8; ++i) {
+        const double n = u > 0.0 ? rint(y[i] / u) : 0.0;
+        word |= static_cast<uint32_t>(static_cast<int>(fmin(fmax(n, -8.0), 7.0)) + 8) << (4 * i);
+      }
+    }
+  }
+  if (nan) return make_uint2(0x88888888u, 0x7Fu);
+  return make_uint2(word, scale);
+}
+
+// Where the slot's row of a kv head starts in the pools of codes and scales, in rows.
+MK_DEV int64_t kvq_row(const mk_kvq_cache& c, int page_shift, int64_t slot, int head) {
+  return (((slot >> page_shift) * c.n_kv_heads + head) << page_shift) + (slot & (c.page_size - 1));
+}
+
+// One row per CTA (gridDim.y 3: a CTA each for its q, k and v heads).
+template <class T, int LAYOUT, int BITS, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid_constant__ AppendParams P) {
+  const mk_qkv_append_io& io = P.io;
+  __shared__ float2 cs[128];
+  const int64_t row = blockIdx.x;
+  const int d = P.d, team = P.team;
+  const int l = threadIdx.x & (team - 1), first = threadIdx.x / team, teams = THREADS / team;
+  const bool some = l * 8 < d;
+  const int parts = gridDim.y == 3 ? 1 << blockIdx.y : 7;
+  const int32_t pos = P.rot ? io.positions[row] : 0;
+  int64_t slot = -1;
+  if (io.k && (parts & 6)) {
+    slot = io.slots[row];
+    const int64_t most = BITS == 4 ? static_cast<int64_t>(io.kvq.n_pages) << P.page_shift : io.n_slots;
+    if (slot >= most) slot = -1;
+  }
+  constexpr int kAhead = 4;
+  uint4 next[kAhead];
+  // the first loads are on their way while the angles are made
+  const T* q = static_cast<const T*>(io.q) + row * io.q_stride + l * 8;
+  if (parts & 1)
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (some && first + u * teams < io.n_q_heads) next[u] = __ldcs(reinterpret_cast<const uint4*>(q + (first + u * teams) * d));
+  for (int i = threadIdx.x; i < P.rot / 2 && (parts & 3); i += THREADS) {
+    const float2 c = cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[i]);
+    cs[i] = make_float2(c.x * P.m, c.y * P.m);
+  }
+  __syncthreads();
+  // lane of the partners
+  const int h16 = P.rot / 16;
+  const int from = LAYOUT == MK_ROPE_HALF && l < 2 * h16 ? (l < h16 ? l + h16 : l - h16) : l;
+
+  // The normed and rotated values of a head; for a cache in 4 bits how far they
+  // may be off: the angle's and the sine's rounding (2^-23.4 of the pair), those of
+  // the brackets and products (3 x 2^-24) and of r (2^-21.7 of the value), together
+  // below 2^-20.5 (|n_a| + |n_b|) m.
+  auto turned = [&](const uint4& raw, const Turn& t, bool norm, float (&y)[8], float* off) {
+    float x[8], p[8];
+    unpack8<T>(raw, x);
+    float r = 1.f;
+    if (norm) {
+      float ss[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ss[i] = x[2 * i] * x[2 * i] + x[2 * i + 1] * x[2 * i + 1];
+      float sum = (ss[0] + ss[1]) + (ss[2] + ss[3]);
+      for (int o = team / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      r = __frsqrt_rn(sum * P.by_d + io.eps);
+    }
+    if (LAYOUT == MK_ROPE_HALF) {
+      uint4 other;
+      other.x = __shfl_sync(0xffffffffu, raw.x, from, team);
+      other.y = __shfl_sync(0xffffffffu, raw.y, from, team);
+      other.z = __shfl_sync(0xffffffffu, raw.z, from, team);
+      other.w = __shfl_sync(0xffffffffu, raw.w, from, team);
+      unpack8<T>(other, p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
+    }
+    if (off) {
+      float top = 0.f, ptop = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i])), ptop = fmaxf(ptop, fabsf(p[i]));
+      *off = 0x1p-20f * r * (top * t.top + ptop * t.partner_top);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = (t.turns ? x[i] * t.a[i] + p[i] * t.b[i] : x[i] * t.a[i]) * r;
+  };
+
+  if (parts & 1) {
+    T* out = static_cast<T*>(io.q_out) + row * io.q_out_stride + l * 8;
+    const Turn t = make_turn<T, LAYOUT>(P, io.q_norm, cs, l, from);
+    // (the loop is the same for a whole warp: its teams meet in the shuffles)
+    const int warp_first = (threadIdx.x & ~31) / team;
+    for (int at = 0; warp_first + at < io.n_q_heads; at += kAhead * teams) {
+      uint4 raw[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) raw[u] = next[u];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int h = first + at + (kAhead + u) * teams;
+        if (some && h < io.n_q_heads) next[u] = __ldcs(reinterpret_cast<const uint4*>(q + h * d));
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int h = first + at + u * teams;
+        if (!some || h >= io.n_q_heads) raw[u] = make_uint4(0, 0, 0, 0);
+        if (warp_first + at + u * teams >= io.n_q_heads) break;
+        float y[8];
+        turned(raw[u], t, io.q_norm != nullptr, y, nullptr);
+        if (some && h < io.n_q_heads) *reinterpret_cast<uint4*>(out + h * d) = pack8<T>(y);
+      }
+    }
+  }
+#pragma unroll 1
+  for (int part = 1; part < 3; ++part) {
+    const bool is_k = part == 1;
+    const T* src = static_cast<const T*>(is_k ? io.k : io.v);
+    if (!(parts >> part & 1) || !src || slot < 0) continue;
+    src += row * (is_k ? io.k_stride : io.v_stride);
+    const int warp_first = (threadIdx.x & ~31) / team;
+    Turn t;
+    if (is_k) t = make_turn<T, LAYOUT>(P, io.k_norm, cs, l, from);
+    for (int at = 0; warp_first + at < io.n_kv_heads; at += teams) {
+      const int h = first + at;
+      const bool mine = some && h < io.n_kv_heads;
+      uint4 raw = make_uint4(0, 0, 0, 0);
+      if (mine) raw = __ldcs(reinterpret_cast<const uint4*>(src + h * d + l * 8));
+      if (BITS == 16) {
+        if (is_k) {
+          float y[8];
+          turned(raw, t, io.k_norm != nullptr, y, nullptr);
+          raw = pack8<T>(y);
+        }
+        if (mine)
+          *reinterpret_cast<uint4*>(static_cast<T*>(is_k ? io.k_cache : io.v_cache) +
+                                    (slot * io.n_kv_heads + h) * d + l * 8) = raw;
+        continue;
+      }
+      const int32_t* exps = is_k ? io.kvq.k_exp : io.kvq.v_exp;
+      const int e = exps && mine ? clamp_exp(exps[h]) : 0;
+      const float unit = pow2(-e);
+      float z[8];
+      uint2 code;
+      if (is_k) {
+        float off;
+        turned(raw, t, io.k_norm != nullptr, z, &off);
+        off *= unit;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] *= unit;
+        if (P.rot || io.k_norm)
+          code = quantise<T, LAYOUT, true>(P, z, off, src + h * d, static_cast<const T*>(io.k_norm), pos, l, e);
+        else
+          code = quantise<T, LAYOUT, false>(P, z, 0.f, nullptr, nullptr, 0, l, e);
+      } else {
+        unpack8<T>(raw, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] *= unit;
+        code = quantise<T, LAYOUT, false>(P, z, 0.f, nullptr, nullptr, 0, l, e);
+      }
+      if (!mine) continue;
+      const int64_t to = kvq_row(io.kvq, P.page_shift, slot, h);
+      uint8_t* codes = static_cast<uint8_t*>(is_k ? io.kvq.k_codes : io.kvq.v_codes);
+      uint8_t* scales = static_cast<uint8_t*>(is_k ? io.kvq.k_scales : io.kvq.v_scales);
+      *reinterpret_cast<uint32_t*>(codes + to * (d / 2) + l * 4) = code.x;
+      if (!(l & 1)) scales[to * (d / 16) + l / 2] = static_cast<uint8_t>(code.y);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ values again
+
+struct ReadParams {
+  mk_kvq_read_io io;
+  int32_t page_shift;
+  int64_t groups;  // of 16 values, of K and of V
+};
+
+// A thread per group, in the order of the pools where every slot is read.
+template <class T>
+__global__ void __launch_bounds__(256) k_read(const __grid_constant__ ReadParams P) {
+  const mk_kvq_read_io& io = P.io;
+  const mk_kvq_cache& c = io.kvq;
+  const int per = c.head_dim / 16;
+  const bool is_k = blockIdx.y == 0;
+  T* out = static_cast<T*>(is_k ? io.k_out : io.v_out);
+  if (!out) return;
+  const uint8_t* codes = static_cast<const uint8_t*>(is_k ? c.k_codes : c.v_codes);
+  const uint8_t* scales = static_cast<const uint8_t*>(is_k ? c.k_scales : c.v_scales);
+  const int32_t* exps = is_k ? c.k_exp : c.v_exp;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < P.groups; i += gridDim.x * 256ll) {
+    const int64_t r = i / per;
+    const int g = static_cast<int>(i - r * per);
+    int64_t row, slot;
+    int h;
+    if (io.slots) {
+      row = r / c.n_kv_heads;
+      h = static_cast<int>(r - row * c.n_kv_heads);
+      slot = io.slots[row];
+    } else {
+      const int64_t block = r >> P.page_shift, page = block / c.n_kv_heads;
+      h = static_cast<int>(block - page * c.n_kv_heads);
+      row = slot = (page << P.page_shift) + (r & (c.page_size - 1));
+      if (row >= io.n_rows) continue;
+    }
+    uint2 word = make_uint2(0x88888888u, 0x88888888u);
+    float s = 0.f;
+    if (slot >= 0 && slot < static_cast<int64_t>(c.n_pages) << P.page_shift) {
+      const int64_t at = kvq_row(c, P.page_shift, slot, h);
+      word = *reinterpret_cast<const uint2*>(codes + at * (c.head_dim / 2) + g * 8);
+      s = e4m3_to_float(scales[at * per + g]) * pow2(exps ? clamp_exp(exps[h]) : 0);
+    }
+    uint4 y[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (static_cast<int>(((k ? word.y : word.x) >> (4 * j)) & 15u) - 8) * s;
+      y[k] = pack8<T>(v);
+    }
+    uint4* to = reinterpret_cast<uint4*>(out + (row * c.n_kv_heads + h) * c.head_dim + g * 16);
+    to[0] = y[0];
+    to[1] = y[1];
+  }
+}
+
+template <class T, int LAYOUT, int BITS>
+void launch_append(const AppendParams& P, int sms, cudaStream_t s) {
+  const unsigned n = static_cast<unsigned>(P.io.n_rows);
+  if (P.io.n_rows < 2 * sms) k_append<T, LAYOUT, BITS, 256><<<dim3(n, 3), 256, 0, s>>>(P);
+  else k_append<T, LAYOUT, BITS, 128><<<n, 128, 0, s>>>(P);
+}
+template <class T>
+void launch_append(const AppendParams& P, bool half, int sms, cudaStream_t s) {
+  if (P.io.bits == 16) {
+    if (half) launch_append<T, MK_ROPE_HALF, 16>(P, sms, s);
+    else launch_append<T, MK_ROPE_INTERLEAVED, 16>(P, sms, s);
+  } else {
+    if (half) launch_append<T, MK_ROPE_HALF, 4>(P, sms, s);
+    else launch_append<T, MK_ROPE_INTERLEAVED, 4>(P, sms, s);
+  }
+}
+
+}  // namespace
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" {
+
+mk_status mk_qkv_append(const mk_rope* rope, const mk_qkv_append_io* io, void* stream) {
+  if (!io) return MK_ERR_INVALID_ARG;
+  const int64_t d = io->head_dim, n = io->n_rows;
+  if (io->dtype != MK_BF16 && io->dtype != MK_FP16) return MK_ERR_UNSUPPORTED;
+  if (io->bits != 16 && io->bits != 4) return MK_ERR_UNSUPPORTED;
+  if (n < 0 || io->n_q_heads < 0 || io->n_kv_heads < 0) return MK_ERR_INVALID_ARG;
+  if (d < 8 || d > 256 || d % 8) return MK_ERR_UNSUPPORTED;
+  if (rope && rope->cfg.head_dim != d) return MK_ERR_INVALID_ARG;
+  if (io->n_q_heads > 4096 || io->n_kv_heads > 4096) return MK_ERR_UNSUPPORTED;
+  if (!(io->eps >= 0.f && io->eps <= 1e30f)) return MK_ERR_INVALID_ARG;
+  if (io->bits == 4 && io->n_kv_heads) {
+    const mk_status st = check_kvq(io->kvq, true);
+    if (st != MK_OK) return st;
+    if (io->kvq.head_dim != d || io->kvq.n_kv_heads != io->n_kv_heads) return MK_ERR_INVALID_ARG;
+  }
+  if (n == 0) return MK_OK;  // (tensors without rows may have no address)
+  if ((io->q != nullptr) != (io->n_q_heads > 0) || (io->k != nullptr) != (io->n_kv_heads > 0))
+    return MK_ERR_INVALID_ARG;
+  if (!io->q && !io->k) return MK_ERR_INVALID_ARG;
+  if (io->q && !io->q_out) return MK_ERR_INVALID_ARG;
+  if (io->k && !io->slots) return MK_ERR_INVALID_ARG;
+  if (io->v && !io->k) return MK_ERR_INVALID_ARG;
+  if (io->k && io->bits == 16 && (!io->k_cache || (io->v && !io->v_cache) || io->n_slots < 0))
+    return MK_ERR_INVALID_ARG;
+  if (rope && !io->positions) return MK_ERR_INVALID_ARG;
+  const void* ptrs[] = {io->q, io->q_out, io->k, io->v, io->k_cache, io->v_cache, io->q_norm, io->k_norm};
+  for (const void* p : ptrs)
+    if (misaligned(p, 16)) return MK_ERR_INVALID_ARG;
+  if (misaligned(io->positions, 4) || misaligned(io->slots, 8)) return MK_ERR_INVALID_ARG;
+  const int64_t qw = io->n_q_heads * d, kw = io->n_kv_heads * d;
+  if (io->q && (io->q_stride % 8 || io->q_out_stride % 8 || io->q_stride < qw || io->q_out_stride < qw))
+    return MK_ERR_INVALID_ARG;
+  if (io->k && (io->k_stride % 8 || io->k_stride < kw)) return MK_ERR_INVALID_ARG;
+  if (io->v && (io->v_stride % 8 || io->v_stride < kw)) return MK_ERR_INVALID_ARG;
+  // what is written, against what is read (k and v may lie between the rows of q_out)
+  const int64_t q_out = io->q ? span_bytes(n, qw, io->q_out_stride, 2) : 0;
+  const int64_t q_in = io->q ? span_bytes(n, qw, io->q_stride, 2) : 0;
+  const int64_t k_in = io->k ? span_bytes(n, kw, io->k_stride, 2) : 0;
+  const int64_t v_in = io->v ? span_bytes(n, kw, io->v_stride, 2) : 0;
+  struct Range { const void* p; int64_t n; };
+  const bool in_place = io->q == io->q_out && io->q_stride == io->q_out_stride;
+  const Range in[] = {{in_place ? nullptr : io->q, q_in}, {rope ? io->positions : nullptr, n * 4},
+                      {io->k ? io->slots : nullptr, n * 8}, {io->q_norm, d * 2}, {io->k ? io->k_norm : nullptr, d * 2}};
+  Range out[5] = {{io->q_out, q_out}, {}, {}, {}, {}};
+  if (io->k && io->bits == 4) {
+    const int64_t rows = static_cast<int64_t>(io->kvq.n_pages) * io->kvq.page_size * io->n_kv_heads;
+    out[1] = {io->kvq.k_codes, rows * (d / 2)};
+    out[2] = {io->kvq.k_scales, rows * (d / 16)};
+    if (io->v) {
+      out[3] = {io->kvq.v_codes, rows * (d / 2)};
+      out[4] = {io->kvq.v_scales, rows * (d / 16)};
+    }
+    for (int a = 1; a < 5; ++a) {
+      const Range more[] = {{io->kvq.k_exp, io->n_kv_heads * 4ll}, {io->kvq.v_exp, io->n_kv_heads * 4ll},
+                            {io->q, q_in}, {io->q_out, q_out}, {io->k, k_in}, {io->v, v_in}};
+      for (const Range& r : more)
+        if (overlap(r.p, r.n, out[a].p, out[a].n)) return MK_ERR_INVALID_ARG;
+      for (int b = a + 1; b < 5; ++b)
+        if (overlap(out[a].p, out[a].n, out[b].p, out[b].n)) return MK_ERR_INVALID_ARG;
+    }
+  }
+  for (const Range& r : in)
+    for (const Range& w : out)
+      if (overlap(r.p, r.n, w.p, w.n)) return MK_ERR_INVALID_ARG;
+  int sms = 0;
+  const mk_status st = check_device(io->q ? io->q_out : io->slots, nullptr, &sms);
+  if (st != MK_OK) return st;
+  AppendParams P;
+  P.io = *io;
+  P.d = static_cast<int32_t>(d);
+  P.by_d = 1.f / static_cast<float>(d);
+  P.rot = rope ? rope->cfg.rot_dim : 0;
+  P.team = 1;
+  while (P.team * 8 < d) P.team *= 2;
+  if (io->bits == 4) P.team = std::max(P.team, 2);
+  P.page_shift = io->bits == 4 && io->n_kv_heads ? __builtin_ctz(static_cast<uint32_t>(io->kvq.page_size)) : 0;
+  P.m = rope ? rope->m : 1.f;
+  P.m64 = rope ? rope->m64 : 1.0;
+  std::fill(P.turns, P.turns + 128, 0);
+  if (rope) std::copy(rope->turns, rope->turns + 128, P.turns);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool half = !rope || rope->cfg.layout == MK_ROPE_HALF;
+  if (io->dtype == MK_BF16) launch_append<__nv_bfloat16>(P, half, sms, s);
+  else launch_append<__half>(P, half, sms, s);
+  MK_CUDA_TRY(cudaGetLastError());
+  return MK_OK;
+}
+
+mk_status mk_kvq_read(const mk_kvq_read_io* io, void* stream) {
+  if (!io) return MK_ERR_INVALID_ARG;
+  if (io->dtype != MK_BF16 && io->dtype != MK_FP16) return MK_ERR_UNSUPPORTED;
+  mk_status st = check_kvq(io->kvq, true);
+  if (st != MK_OK) return st;
+  const mk_kvq_cache& c = io->kvq;
+  const int64_t slots = static_cast<int64_t>(c.n_pages) * c.page_size, n = io->n_rows;
+  if (n < 0 || (!io->slots && n > slots)) return MK_ERR_INVALID_ARG;
+  if (n == 0) return MK_OK;
+  if (!io->k_out && !io->v_out) return MK_ERR_INVALID_ARG;
+  if (misaligned(io->k_out, 16) || misaligned(io->v_out, 16) || misaligned(io->slots, 8)) return MK_ERR_INVALID_ARG;
+  const int64_t out = n * c.n_kv_heads * c.head_dim * 2, rows = slots * c.n_kv_heads;
+  if (overlap(io->k_out, out, io->v_out, out)) return MK_ERR_INVALID_ARG;
+  for (const void* p : {io->k_out, io->v_out})
+    if (overlap(p, out, io->slots, n * 8) || overlap(p, out, c.k_codes, rows * (c.head_dim / 2)) ||
+        overlap(p, out, c.v_codes, rows * (c.head_dim / 2)) || overlap(p, out, c.k_scales, rows * (c.head_dim / 16)) ||
+        overlap(p, out, c.v_scales, rows * (c.head_dim / 16)) || overlap(p, out, c.k_exp, c.n_kv_heads * 4ll) ||
+        overlap(p, out, c.v_exp, c.n_kv_heads * 4ll))
+      return MK_ERR_INVALID_ARG;
+  int sms = 0;
+  st = check_device(io->k_out ? io->k_out : io->v_out, nullptr, &sms);
+  if (st != MK_OK) return st;
+  ReadParams P;
+  P.io = *io;
+  P.page_shift = __builtin_ctz(static_cast<uint32_t>(c.page_size));
+  // (every slot: whole pages, of which the last may stand out)
+  const int64_t r = io->slots ? n : (n + c.page_size - 1) / c.page_size * c.page_size;
+  P.groups = r * c.n_kv_heads * (c.head_dim / 16);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((P.groups + 255) / 256, 16ll * sms)), 2);
+  if (io->dtype == MK_BF16) k_read<__nv_bfloat16><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(P);
+  else k_read<__half><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(P);
+  MK_CUDA_TRY(cudaGetLastError());
+  return MK_OK;
+}
+
+}  // extern "C"

@@ -10,17 +10,9 @@
 // number of half turns, go to sincospif.
 #include <algorithm>
 #include <cmath>
-#include <cuda_fp16.h>
 #include <new>
 
-#include "batch.h"
-#include "ptx.cuh"
-
-struct mk_rope {
-  mk_rope_config cfg;
-  uint64_t turns[128];  // F_i
-  float m;
-};
+#include "rope.h"
 
 namespace mk {
 
@@ -31,24 +23,6 @@ struct RopeParams {
   int32_t d, rot;
   float m;
   uint64_t turns[128];
-};
-
-template <class T> struct Pack;  // two 16-bit values in a word
-template <> struct Pack<__nv_bfloat16> {
-  static MK_DEV float2 get(uint32_t w) {
-    return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
-  }
-  static MK_DEV uint32_t put(float a, float b) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&v);
-  }
-};
-template <> struct Pack<__half> {
-  static MK_DEV float2 get(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
-  static MK_DEV uint32_t put(float a, float b) {
-    __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&v);
-  }
 };
 
 // A piece of work: 16 bytes of a head that turn with 16 others (half layout) or
@@ -200,9 +174,10 @@ mk_status mk_rope_create(const mk_rope_config* cfg, mk_rope** out) {
     // f <= 1 rad, less than a sixth of a turn
     r->turns[i] = static_cast<uint64_t>(std::ldexp(f / two_pi, 64));
   }
-  r->m = static_cast<float>(c.attn_factor != 0.0                ? c.attn_factor
-                            : c.scaling == MK_ROPE_SCALE_PARTS ? 0.1 * std::log(c.factor) + 1.0
-                                                               : 1.0);
+  r->m64 = c.attn_factor != 0.0               ? c.attn_factor
+           : c.scaling == MK_ROPE_SCALE_PARTS ? 0.1 * std::log(c.factor) + 1.0
+                                              : 1.0;
+  r->m = static_cast<float>(r->m64);
   *out = r;
   return MK_OK;
 }

@@ -1,0 +1,645 @@
+"""GPU parity of the attention half of a batched layer over a cache in 4 bits
+(mk_linear, mk_qkv_append, mk_kvq_read, mk_kvq_attn) with the float64 oracle,
+through the binding.
+
+Tolerances, from the arithmetic, with u = eps / 2 of the tensors' type, tiny = half
+the spacing of its subnormals and v = 2^-24, half a step of float32:
+
+append: what a value is made from is off by less than 2^-20 of its pair's
+  magnitude (the angle 2^-25 rad, sine and cosine 2 ulp, weight, factor and
+  products 4 v, the root of the mean 6 v):
+    |err| <= (|n_a| + |n_b|) m 2^-20 + u |y| + tiny.
+  Codes and scales are the oracle's: what is near a border is worked out in 64 bits.
+attention: a score is a sum of d exact products in float32, each partial sum off by
+  2 v, and sum |q_i k_i| <= |q| |k|; q is off by 2^-25 of its row's largest value:
+  with e_s = scale 3 d v max|q| max|k| + 2^-19 (exp2, its argument, the reference's
+  rounding) a weight is relatively off by e_s; rounding it to fp16 adds 2^-11, or,
+  where it underflows, 2^-25 against a largest weight of at least 2^-10.  A
+  quotient doubles e_s.  Sums of n keys in chunks of 16 and of the partial results
+  add (n / 16 + 64) 2 v.  With W = sum_j w_j |v_j| over the softmax weights:
+    |out err| <= W (2^-11 + 2 e_s + (n / 16 + 64) 2 v) + n 2^-15 2^-10 max|v| + u |out| + tiny,
+    |lse err| <= e_s + (n + 64) v + 4 v |lse|.
+linear: products are exact in float32, sums of n_in in chunks of 16 and of up to 64
+  parts off by (n_in / 16 + 64) 2 v of S = |x| |w|^T; an activation has a slope of
+  at most 1.13 and adds 2^-20 (1 + |y|):
+    |err| <= 1.13 S (n_in / 16 + 64) 2 v + 2^-20 (1 + |y|) + u |y| + tiny.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import batch as ob
+from oracle import kvq as ok
+
+pytestmark = pytest.mark.gpu
+
+TORCH = {"bf16": torch.bfloat16, "fp16": torch.float16}
+U = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}               # torch.finfo(t).eps / 2
+TINY = {"bf16": 2.0 ** -134, "fp16": 2.0 ** -25}
+V = 2.0 ** -24
+CANARY = -1152.0                                          # exact in bf16 and fp16
+
+
+def dev(x, dtype=torch.int32):
+    return torch.as_tensor(np.asarray(x)).to(dtype).cuda()
+
+
+def np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def rounded(rng, shape, dtype, scale=1.0):
+    """N(0, scale^2) values of the type, as float64, and the CUDA tensor."""
+    t = torch.from_numpy(rng.standard_normal(shape) * scale).to(TORCH[dtype])
+    return t.double().numpy(), t.cuda()
+
+
+# ----------------------------------------------------------------- append
+
+def pool(rng, pages, heads, page, d):
+    """Pools of any codes and scales that are numbers."""
+    return [torch.from_numpy(x).cuda() for x in (
+        rng.integers(0, 256, (pages, heads, page, d // 2), dtype=np.uint8),
+        rng.integers(0, 126, (pages, heads, page, d // 16), dtype=np.uint8))]
+
+
+def check_append(mk, rng, n, hq, hk, d, rot, layout, dtype, positions, bits, norm=True, page=16, scaling="none",
+                 factor=1.0, orig_ctx=0, eps=1e-6, in_place=False, no_v=False, no_q=False, no_k=False, exps=True,
+                 stream=None, by=1.0, change=None):
+    pages = n // page + 3
+    x, qkv = rounded(rng, (n, hq + 2 * hk + 1, d), dtype, by)   # one head more: the rows have a gap
+    if change is not None:
+        change(x)
+        qkv.copy_(torch.from_numpy(x))
+        x = np64(qkv)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:hq + 2 * hk]
+    slots = rng.permutation(pages * page)[:n]
+    if n > 3:
+        slots[[1, n - 1]] = [-1, pages * page]              # rows without a place
+    live = (slots >= 0) & (slots < pages * page)
+    wq, wk = [rounded(rng, (d,), dtype) if norm else (None, None) for _ in range(2)]
+    out = torch.full((n, hq + 1, d), CANARY, dtype=TORCH[dtype], device="cuda")
+    q_out = q if in_place else out[:, :hq]
+    rope = mk.mk_rope_create(mk.make_rope_config(d, rot, layout=layout, scaling=scaling, factor=factor,
+                                                 orig_ctx=orig_ctx)) if rot else None
+    e = [rng.integers(-3, 4, hk) if exps else np.zeros(hk, int) for _ in range(2)]
+    kw = dict(q_norm=wq[1], k_norm=wk[1], eps=eps)
+    if bits == 16:
+        caches = [rounded(rng, (pages, page, hk, d), dtype)[1] for _ in range(2)]
+        kw.update(k_cache=None if no_k else caches[0], v_cache=None if no_v or no_k else caches[1])
+    else:
+        caches = pool(rng, pages, hk, page, d) + pool(rng, pages, hk, page, d)
+        ex = [dev(a) if exps else None for a in e]
+        if not no_k:
+            kw.update(kvq=mk.make_kvq_cache(*caches, *ex))
+    kept = [c.clone() for c in caches]
+    pos, at = dev(positions) if rot else None, None if no_k else dev(slots, torch.int64)
+    io = mk.make_qkv_append_io(None if no_q else q, None if no_q else q_out, None if no_k else k,
+                               None if no_v or no_k else v, pos, at, **kw)
+    mk.mk_qkv_append(rope, io, stream)
+    torch.cuda.synchronize()
+    mk.mk_rope_destroy(rope)
+    f, m = ob.rope_frequencies(rot or 16, scaling=scaling, factor=factor, orig_ctx=orig_ctx)
+
+    def want(src, w):
+        with np.errstate(invalid="ignore"):
+            return ok.norm_rope(src, w, eps, positions, rot, layout, f, m)
+
+    def close(got, wanted):
+        y, mag = wanted
+        tol = mag * 2.0 ** -20 + U[dtype] * np.abs(y) + TINY[dtype]
+        assert np.all(np.abs(got - y) <= tol), (np.abs(got - y) / np.maximum(tol, 1e-300)).max()
+
+    if not no_q:
+        close(np64(q_out), want(x[:, :hq], wq[0]))
+        if not in_place:
+            assert bool((out[:, hq] == CANARY).all())
+    if not in_place:                                        # the inputs are as they were
+        assert np.array_equal(np64(qkv), x, equal_nan=True)
+    if no_k:
+        return
+    at = slots[live]
+    others = np.setdiff1d(np.arange(pages * page), at)
+    yk = want(x[:, hq:hq + hk], wk[0])
+    if bits == 16:
+        flat = [c.view(pages * page, hk, d) for c in caches]
+        close(np64(flat[0])[at], [a[live] for a in yk])
+        old = [c.view(pages * page, hk, d) for c in kept]
+        assert torch.equal(flat[1][at], old[1][at] if no_v else v[torch.from_numpy(live).cuda()])
+    else:
+        flat = [c.transpose(1, 2).reshape(pages * page, hk, -1) for c in caches]
+        old = [c.transpose(1, 2).reshape(pages * page, hk, -1) for c in kept]
+        for (y, a) in ((yk[0], 0), (x[:, hq + hk:hq + 2 * hk], 2)):
+            codes, scales = ok.encode(y[live], e[a // 2][None])
+            if a and no_v:
+                codes, scales = old[2][at].cpu().numpy(), old[3][at].cpu().numpy()
+            assert np.array_equal(flat[a + 1][at].cpu().numpy(), scales)
+            assert np.array_equal(flat[a][at].cpu().numpy(), codes)
+    for a, b in zip(flat, old):
+        assert torch.equal(a[others], b[others])
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("n,hq,hk,d,rot,dtype", [
+    (1, 4, 1, 64, 64, "bf16"), (16, 32, 8, 128, 128, "bf16"), (5, 6, 2, 64, 16, "fp16"),
+    (37, 8, 8, 128, 32, "bf16"), (3, 1, 1, 256, 256, "fp16"), (9, 5, 5, 80, 48, "bf16"),
+    (700, 3, 1, 32, 16, "fp16"), (2, 33, 17, 16, 16, "bf16"), (400, 32, 8, 128, 128, "fp16")])
+def test_append(cuda_lib, bits, layout, n, hq, hk, d, rot, dtype):
+    rng = np.random.default_rng(n)
+    check_append(cuda_lib, rng, n, hq, hk, d, rot, layout, dtype, rng.integers(0, 40000, n), bits)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("kw", [
+    dict(norm=False), dict(norm=False, rot=0), dict(rot=0), dict(scaling="linear", factor=8.0),
+    dict(scaling="base", factor=4.0), dict(scaling="parts", factor=16.0, orig_ctx=4096), dict(eps=0.5),
+    dict(in_place=True), dict(no_v=True), dict(no_q=True), dict(no_k=True), dict(exps=False), dict(page=256),
+    dict(in_place=True, layout="interleaved"), dict(by=1e-3), dict(by=300.0), dict(by=1e-3, norm=False)])
+def test_append_variants(cuda_lib, bits, kw):
+    kw = dict(dict(layout="half", rot=64), **kw)
+    rng = np.random.default_rng(11)
+    check_append(cuda_lib, rng, 50, 8, 2, 128, dtype="bf16", positions=rng.integers(0, 1 << 20, 50), bits=bits, **kw)
+
+
+def test_append_head_of_eight(cuda_lib):
+    rng = np.random.default_rng(2)
+    check_append(cuda_lib, rng, 70, 5, 3, 8, 8, "interleaved", "bf16", rng.integers(0, 4000, 70), 16)
+
+
+def test_append_many_codes(cuda_lib):
+    """Codes of a million values, some hundred of which lie near a border in 32 bits."""
+    rng = np.random.default_rng(3)
+    check_append(cuda_lib, rng, 1000, 1, 8, 128, 128, "half", "bf16", rng.integers(0, 1 << 20, 1000), 4,
+                 scaling="parts", factor=8.0, orig_ctx=8192)
+
+
+def test_append_ties_infinities_and_nan(cuda_lib):
+    """Values on borders between codes and scales (without a rotation they stay
+    there), zeros, infinities; a NaN takes its group along."""
+    def change(x):
+        r = np.random.default_rng(4)
+        x[:] = np.round(x * 8) / 4                                       # multiples of a quarter
+        x[::3, :, ::16] = 7 * 2.0 ** r.integers(-3, 3, x[::3, :, ::16].shape)  # a power of two as scale
+        x[1::7] = 0
+        x[2::7, :, :16] = 7 * 17 / 16 * 2.0 ** -2                        # ties between scales
+        x[3::7, :, 5], x[4::7, :, 40] = np.inf, -np.inf
+        x[5::7, :, 20] = np.nan
+    for dtype in ("bf16", "fp16"):
+        rng = np.random.default_rng(5)
+        check_append(cuda_lib, rng, 90, 1, 4, 64, 0, "half", dtype, None, 4, norm=False, no_q=True, change=change)
+
+
+def test_read(cuda_lib):
+    rng = np.random.default_rng(6)
+    for dtype, d, page, heads, pages in (("bf16", 128, 64, 8, 5), ("fp16", 64, 16, 3, 7), ("bf16", 80, 32, 1, 1)):
+        pools = pool(rng, pages, heads, page, d) + pool(rng, pages, heads, page, d)
+        for s in pools[1::2]:
+            s.copy_(torch.from_numpy(rng.integers(40, 80, s.shape, dtype=np.uint8)))
+        exps = [rng.integers(-3, 4, heads) for _ in range(2)]
+        on_gpu = [dev(e) for e in exps]
+        kvq = cuda_lib.make_kvq_cache(*pools, *on_gpu)
+        n = pages * page
+        want = [ok.decode_pool(pools[i].cpu().numpy(), pools[i + 1].cpu().numpy(), exps[i // 2]).reshape(n, heads, d)
+                for i in (0, 2)]
+        slots = rng.integers(-2, n + 2, 45)
+        for sl in (None, slots):
+            rows = n if sl is None else len(sl)
+            out = [torch.full((rows, heads, d), CANARY, dtype=TORCH[dtype], device="cuda") for _ in range(2)]
+            at = None if sl is None else dev(sl, torch.int64)
+            cuda_lib.mk_kvq_read(cuda_lib.make_kvq_read_io(kvq, at, *out))
+            for got, w in zip(out, want):
+                if sl is not None:
+                    w = np.where(((sl >= 0) & (sl < n))[:, None, None], w[np.clip(sl, 0, n - 1)], 0)
+                assert np.array_equal(np64(got), w)
+        one = torch.zeros(n, heads, d, dtype=TORCH[dtype], device="cuda")
+        cuda_lib.mk_kvq_read(cuda_lib.make_kvq_read_io(kvq, None, None, one))
+        assert np.array_equal(np64(one), want[1])
+
+
+# -------------------------------------------------------------- attention
+
+def make_attn(rng, lens, news, hq, hk, d, dtype, page, window=0, tree=False, q_scale=1.0, extra_rows=2, exps=True,
+              k_scale=1.0):
+    """Inputs of one call; what no row sees has NaN scales."""
+    B = len(lens)
+    n = int(sum(news))
+    width = max(1, max(-(-max(a, 1) // page) for a in lens))
+    held = [-(-max(a, 0) // page) for a in lens]
+    n_pages = sum(held) + 2
+    ids = rng.permutation(n_pages)
+    table = np.full((B, width), n_pages + 99)
+    at = 0
+    for b in range(B):
+        table[b, :held[b]] = ids[at:at + held[b]]
+        at += held[b]
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(int)
+    q0, q = rounded(rng, (n + extra_rows, hq + 1, d), dtype, q_scale)
+    e = [rng.integers(-2, 2, hk) if exps else np.zeros(hk, int) for _ in range(2)]
+    pools = []
+    for by in (k_scale, 1.0):
+        pools += list(ok.encode(rng.standard_normal((n_pages, hk, page, d)) * by))
+    words = None
+    if tree:
+        words = []
+        for m in news:
+            mine = []
+            for i in range(m):
+                up = int(rng.integers(-1, i)) if i else -1
+                mine.append((1 << i) | (mine[up] if up >= 0 else 0))
+            words += mine
+        words += [0] * extra_rows
+    a = dict(n=n, q0=q0[:, :hq], q=q[:, :hq], table=table, lens=np.array(lens), cu=cu, window=window, words=words,
+             dtype=dtype, d=d, hq=hq, hk=hk, page=page, pools=pools, exps=e, news=list(news))
+    hide_unseen(a)
+    return a
+
+
+def hide_unseen(a):
+    pages, _, page, _ = a["pools"][0].shape
+    seen = np.zeros((pages, page), bool)
+    for b in range(len(a["lens"])):
+        for i in range(a["news"][b]):
+            _, own = ob.visible(i, a["news"][b], min(max(int(a["lens"][b]), 0), a["table"].shape[1] * page), 0, a["window"],
+                                None if a["words"] is None else a["words"][a["cu"][b] + i])
+            for j in own:
+                seen[a["table"][b, j // page], j % page] = True
+    p, r = np.nonzero(~seen)
+    for scales in a["pools"][1::2]:
+        scales[p, :, r] = np.where(np.arange(a["d"] // 16) % 2, 0xFF, 0x7F)
+
+
+def call_attn(mk, a, stream=None, workspace=None, scale=0.0, lse=True):
+    rows = a["q"].shape[0]
+    whole = torch.full((rows, a["hq"] + 1, a["d"]), CANARY, dtype=a["q"].dtype, device="cuda")
+    a["whole"], a["out"] = whole, whole[:, :a["hq"]]
+    a["lse"] = torch.full((rows, a["hq"]), CANARY, dtype=torch.float32, device="cuda")
+    words = None if a["words"] is None else torch.tensor(
+        [w - (1 << 64) if w >> 63 else w for w in a["words"]], dtype=torch.int64, device="cuda")
+    a["dev"] = [torch.from_numpy(x).cuda() for x in a["pools"]] + [dev(e) for e in a["exps"]]
+    a["keep"] = (dev(a["lens"]), dev(a["cu"]), dev(a["table"]), words)
+    kvq = mk.make_kvq_cache(*a["dev"])
+    io = mk.make_kvq_attn_io(a["q"], kvq, a["out"], *a["keep"][:3], window=a["window"], tree_mask=words,
+                             lse=a["lse"] if lse else None, scale=scale)
+    if workspace is None:
+        workspace = torch.empty(mk.mk_kvq_attn_workspace(io), dtype=torch.uint8, device="cuda")
+    a["workspace"], a["io"], a["kvq"] = workspace, io, kvq
+    mk.mk_kvq_attn(io, workspace, stream)
+
+
+def check_attn(mk, a, scale=None, skip=None):
+    torch.cuda.synchronize()
+    assert mk.mk_kvq_attn_status(a["workspace"]) == 0
+    n, d, dt = a["n"], a["d"], a["dtype"]
+    k, v = (ok.decode_pool(a["pools"][i], a["pools"][i + 1], a["exps"][i // 2]) for i in (0, 2))
+    want, lse, weight = ob.prefix_attn(a["q0"][:n], k, v, [], 0, a["table"], a["lens"], a["cu"], a["window"], scale,
+                                       a["words"])
+    sc = 1.0 / math.sqrt(d) if scale is None else scale
+    keys = max(0, int(np.minimum(a["lens"], a["table"].shape[1] * a["page"]).max(initial=0)))
+    top = lambda x: float(np.sqrt(np.max(np.nansum(x * x, axis=-1), initial=0.0)))  # noqa: E731
+    e_s = sc * 3 * d * V * top(a["q0"]) * top(k) + 2.0 ** -19
+    vmax = np.nanmax(np.abs(v), initial=0.0)
+    tol = (weight * (2.0 ** -11 + 2 * e_s + (keys / 16 + 64) * 2 * V) + keys * 2.0 ** -25 * vmax
+           + U[dt] * np.abs(want) + TINY[dt])
+    got, got_lse = np64(a["out"])[:n], np64(a["lse"])[:n]
+    use = np.ones(n, bool) if skip is None else ~skip[:n]
+    got, got_lse, want, lse, tol = got[use], got_lse[use], want[use], lse[use], tol[use]
+    assert np.all(np.isfinite(got))
+    err = np.abs(got - want)
+    assert np.all(err <= tol), ("out", (err / np.maximum(tol, 1e-300)).max())
+    empty = np.isinf(lse)
+    assert np.array_equal(np.isinf(got_lse), empty) and np.all(got_lse[empty] < 0)
+    e = np.abs(got_lse[~empty] - lse[~empty])
+    assert np.all(e <= e_s + (keys + 64) * V + 4 * V * np.abs(lse[~empty])), ("lse", e.max())
+    # rows behind the last request and the values beside out are left as they were
+    assert bool((a["whole"][n:] == CANARY).all()) and bool((a["whole"][:, a["hq"]:] == CANARY).all())
+    assert bool((a["lse"][n:] == CANARY).all())
+
+
+ATTN = {
+    # name: lens, news, hq, hk, d, dtype, page, more
+    "one_key": ([1], [1], 4, 1, 64, "bf16", 16, {}),
+    "no_key": ([0, 3, 0], [1, 1, 2], 2, 1, 64, "bf16", 16, {}),
+    "idle_requests": ([20, 0, 33, 5, 40], [0, 0, 2, 0, 1], 4, 1, 128, "bf16", 16, {}),
+    "all_idle": ([20, 7], [0, 0], 4, 1, 128, "bf16", 16, {}),
+    "tile_ends": ([15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129], [1] * 6 + [2] * 3 + [3] * 3, 8, 2, 128,
+                  "bf16", 64, {}),
+    "tile_ends_64": ([15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129], [1] * 12, 8, 1, 64, "fp16", 16, {}),
+    "mha": ([30, 90, 200], [3, 1, 2], 3, 3, 128, "fp16", 128, {}),
+    "group_6": ([60, 61, 300], [5, 7, 16], 12, 2, 64, "bf16", 16, {}),
+    "group_7": ([60, 61, 140], [19, 7, 37], 7, 1, 128, "bf16", 32, {}),
+    "group_9": ([60, 161], [1, 2], 9, 1, 128, "fp16", 32, {}),
+    "group_64": ([40, 9], [4, 3], 64, 1, 64, "bf16", 16, {}),
+    "group_64_128": ([70, 300], [1, 1], 128, 2, 128, "bf16", 16, {}),
+    "rows_8_9": ([100, 101, 40], [2, 2, 3], 8, 2, 128, "bf16", 16, {}),
+    "chunk": ([350, 20], [300, 3], 4, 2, 128, "bf16", 64, {}),
+    "chunk_fp16": ([200, 130], [140, 130], 2, 1, 64, "fp16", 256, {}),
+    "few_keys_for_rows": ([3, 0, 8], [7, 2, 8], 4, 1, 128, "bf16", 16, {}),
+    "window_1": ([20, 5, 300], [4, 5, 2], 4, 2, 64, "bf16", 16, dict(window=1)),
+    "window_40": ([20, 50, 300, 41], [4, 5, 2, 1], 4, 2, 128, "bf16", 16, dict(window=40)),
+    "window_200": ([20, 250, 700], [4, 16, 2], 4, 2, 64, "fp16", 32, dict(window=200)),
+    "window_wide": ([20, 50], [4, 5], 4, 2, 64, "bf16", 16, dict(window=100000)),
+    "tree": ([40, 300, 16], [16, 9, 16], 8, 2, 128, "bf16", 16, dict(tree=True)),
+    "tree_64": ([64, 100], [64, 64], 4, 1, 64, "fp16", 16, dict(tree=True)),
+    "tree_window": ([140, 300, 20], [16, 9, 5], 4, 1, 128, "bf16", 16, dict(tree=True, window=64)),
+    "large_scores": ([100, 460], [4, 4], 8, 2, 128, "bf16", 16, dict(q_scale=16.0)),
+    "large_scores_fp16": ([100, 460], [4, 4], 8, 2, 64, "fp16", 16, dict(q_scale=16.0)),
+    "small_q": ([100, 60], [4, 4], 8, 2, 128, "bf16", 16, dict(q_scale=1e-20)),
+    "large_keys": ([100, 60], [2, 1], 8, 2, 128, "bf16", 16, dict(q_scale=2.0 ** -12, k_scale=500.0)),
+    "many_requests": ([(7 * i) % 90 + 1 for i in range(300)], [1] * 300, 4, 1, 64, "bf16", 16, {}),
+    "many_items": ([(3 * i) % 11 + 1 for i in range(300)], [1] * 300, 32, 8, 64, "bf16", 16, {}),
+    "requests_900": ([(5 * i) % 200 + 1 for i in range(900)], [i % 3 for i in range(900)], 2, 1, 64, "bf16", 16, {}),
+    "long": ([1500, 40, 3700], [2, 2, 1], 4, 1, 128, "bf16", 1024, {}),
+    "long_64": ([9000], [1], 8, 1, 64, "fp16", 64, {}),
+    "verify": ([600, 555, 91, 16], [16, 9, 13, 16], 8, 2, 128, "bf16", 16, {}),
+    "rows_32_33": ([200, 300, 64], [8, 9, 16], 4, 1, 128, "fp16", 16, {}),
+    "rows_64_65_128_129": ([240, 141, 270, 290], [32, 33, 64, 65], 2, 1, 64, "bf16", 16, {}),
+}
+
+
+@pytest.mark.parametrize("name", list(ATTN))
+def test_attn(cuda_lib, name):
+    lens, news, hq, hk, d, dtype, page, more = ATTN[name]
+    a = make_attn(np.random.default_rng(len(name)), lens, news, hq, hk, d, dtype, page, **more)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+
+
+def test_attn_scale_and_no_lse(cuda_lib):
+    a = make_attn(np.random.default_rng(1), [30, 109], [2, 1], 4, 2, 64, "bf16", 16, exps=False)
+    call_attn(cuda_lib, a, scale=0.03125)
+    check_attn(cuda_lib, a, scale=0.03125)
+    out, lse = a["out"].clone(), a["lse"].clone()
+    call_attn(cuda_lib, a, scale=0.03125, lse=False)
+    torch.cuda.synchronize()
+    assert torch.equal(a["out"], out) and bool((a["lse"] == CANARY).all())
+
+
+@pytest.mark.parametrize("name", ["one_key", "no_key", "tile_ends", "chunk", "window_40", "tree_window", "long", "verify"])
+def test_attn_rows_of_nan(cuda_lib, name):
+    """A row whose q holds a NaN: out and lse are NaN (a row without keys still gets
+    0 and -inf), and no other row's result is."""
+    lens, news, hq, hk, d, dtype, page, more = ATTN[name]
+    a = make_attn(np.random.default_rng(len(name)), lens, news, hq, hk, d, dtype, page, **more)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+    out, lse = a["out"].clone(), a["lse"].clone()
+    bad = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+    bad[:a["n"]:3, ::2] = True                    # some rows, some of their heads
+    a["q"][:, :, 5][bad] = float("nan")
+    call_attn(cuda_lib, a)
+    torch.cuda.synchronize()
+    keys = bad & ~torch.isinf(lse)
+    assert bool(torch.isnan(a["out"][keys]).all()) and bool(torch.isnan(a["lse"][keys]).all())
+    a["out"][keys], a["lse"][keys] = out[keys], lse[keys]
+    check_attn(cuda_lib, a)                       # the others, and those without keys
+
+
+@pytest.mark.parametrize("window,dtype,d", [(64, "bf16", 64), (100, "fp16", 128), (300, "bf16", 128)])
+def test_attn_window_of_rows_that_see_one_another(cuda_lib, window, dtype, d):
+    """Tree words in which every row sees rows behind it too, so that no row has
+    depth 0 and the windows of all start later: what lies below has NaN scales."""
+    a = make_attn(np.random.default_rng(window), [140, 300, 20, 90], [16, 9, 5, 64], 4, 1, d, dtype, 16, window=window,
+                  tree=True)
+    a["words"] = [(1 << m) - 1 for m in a["news"] for _ in range(m)] + [0] * 2
+    hide_unseen(a)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+
+
+def test_attn_rising_scores(cuda_lib):
+    """Scores that rise along the keys by far more than fp16 holds: the reference
+    that weights are taken against moves all the time."""
+    for d, new in ((128, 1), (64, 3), (128, 16)):
+        a = make_attn(np.random.default_rng(d), [700, 333], [new, 1], 4, 1, d, "bf16", 16, exps=False)
+        codes, scales = a["pools"][:2]
+        for b in range(2):
+            for j in range(a["lens"][b]):
+                page = a["table"][b, j // 16]
+                scales[page, :, j % 16] = ok.e4m3(0.01 + j / 90.0)
+        a["q"].abs_()
+        a["q0"] = np64(a["q"])
+        codes[:] = codes | 0x88
+        call_attn(cuda_lib, a)
+        check_attn(cuda_lib, a)
+
+
+def test_attn_bad_tables_and_lengths(cuda_lib):
+    """Pages outside the pool read as zeros; lengths are cut to the table."""
+    a = make_attn(np.random.default_rng(2), [40, 9, 60], [2, 1, 4], 4, 2, 64, "bf16", 16)
+    for s in a["pools"][1::2]:
+        s[:] = 56
+    a["table"][0, 1], a["table"][2, 0] = -1, 2 ** 31 - 1
+    a["table"][1] = a["table"][2]
+    a["lens"] = np.array([40, 10 ** 9, -7])
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+
+
+def test_attn_table_with_gaps(cuda_lib):
+    a = make_attn(np.random.default_rng(12), [300, 45, 1, 700], [8, 3, 1, 2], 8, 2, 128, "bf16", 16)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+    want, lse = a["out"].clone(), a["lse"].clone()
+    rows, cols = a["table"].shape
+    wide = torch.full((rows + 2, cols + 5), 2 ** 30, dtype=torch.int32, device="cuda")
+    view = wide[1:rows + 1, 2:cols + 2]
+    view.copy_(a["keep"][2])
+    io = cuda_lib.make_kvq_attn_io(a["q"], a["kvq"], a["out"], a["keep"][0], a["keep"][1], view, lse=a["lse"])
+    a["whole"].fill_(CANARY)
+    cuda_lib.mk_kvq_attn(io, a["workspace"])
+    check_attn(cuda_lib, a)
+    assert torch.equal(a["out"], want) and torch.equal(a["lse"], lse)
+
+
+def test_attn_is_repeatable_and_needs_no_clean_workspace(cuda_lib):
+    a = make_attn(np.random.default_rng(3), [300, 45, 1700, 2], [8, 3, 1, 2], 8, 2, 128, "bf16", 16)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+    first, lse = a["out"].clone(), a["lse"].clone()
+    a["workspace"].fill_(0xFF)
+    cuda_lib.mk_kvq_attn(a["io"], a["workspace"])
+    torch.cuda.synchronize()
+    assert torch.equal(a["out"], first) and torch.equal(a["lse"], lse)
+
+
+def test_attn_rows_before_the_first_request(cuda_lib):
+    a = make_attn(np.random.default_rng(13), [30, 90], [3, 2], 4, 2, 64, "bf16", 16)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+    want = a["out"].clone()
+    a["keep"][1][0] = 2                              # the first request has one row left, its last
+    a["whole"].fill_(CANARY)
+    cuda_lib.mk_kvq_attn(a["io"], a["workspace"])
+    torch.cuda.synchronize()
+    assert bool((a["whole"][:2] == CANARY).all()) and torch.equal(a["out"][2:5], want[2:5])
+
+
+def test_attn_on_streams_and_in_graphs(cuda_lib):
+    calls = [make_attn(np.random.default_rng(20 + i), [400 + i, 77], [1 + 2 * i, 1], 8, 2, 128, "bf16", 16) for i in range(3)]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for a, s in zip(calls, streams):
+        with torch.cuda.stream(s):
+            call_attn(cuda_lib, a, stream=s)
+    for a in calls:
+        check_attn(cuda_lib, a)
+    for a in calls:
+        a["want"] = a["out"].clone(), a["lse"].clone()
+        a["whole"].fill_(CANARY)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cuda_lib.mk_kvq_attn(a["io"], a["workspace"], torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        assert bool((a["whole"] == CANARY).all())
+        for _ in range(2):
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a["out"], a["want"][0])
+        a["keep"][0][0] -= 9                         # other lengths in the same graph
+        a["lens"][0] -= 9
+        g.replay()
+        hide = [s.copy() for s in a["pools"][1::2]]
+        check_attn(cuda_lib, a)
+        del hide
+
+
+# ----------------------------------------------------------------- linear
+
+def check_linear(mk, rng, m, k, n, dtype, bias=False, act="none", residual=False, in_place=False, gap=8, stream=None,
+                 by=1.0):
+    x0, x = rounded(rng, (m, k + gap), dtype, by)
+    w0, w = rounded(rng, (n, k + gap), dtype, k ** -0.5)
+    x[:, k:], w[:, k:] = float("nan"), float("nan")          # what lies between the rows is not read
+    b0, b = rounded(rng, (n,), dtype) if bias else (None, None)
+    whole = torch.full((m + 1, n + 3), CANARY, dtype=TORCH[dtype], device="cuda")
+    out = whole[:m, :n]
+    r0, r = rounded(rng, (m, n + 5), dtype) if residual else (None, None)
+    if residual:
+        r0, r = r0[:, :n], r[:, :n]
+        if in_place:
+            out.copy_(r)
+            r = out
+    io = mk.make_linear_io(x[:, :k], w[:, :k], out, bias=b, act=act, residual=r)
+    ws = torch.full((mk.mk_linear_workspace(io),), 0xFF, dtype=torch.uint8, device="cuda")
+    mk.mk_linear(io, ws, stream)
+    torch.cuda.synchronize()
+    assert mk.mk_linear_status(ws) == 0
+    want, s = ok.linear(x0[:, :k], w0[:, :k], b0, act, r0)
+    tol = 1.13 * s * (k / 16 + 64) * 2 * V + 2.0 ** -20 * (1 + np.abs(want)) + U[dtype] * np.abs(want) + TINY[dtype]
+    err = np.abs(np64(out) - want)
+    assert np.all(err <= tol), (err / tol).max()
+    assert bool((whole[m:] == CANARY).all()) and bool((whole[:, n:] == CANARY).all())
+    if not in_place:
+        first = out.clone()
+        ws.fill_(0x55)
+        mk.mk_linear(io, ws, stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,k,n", [
+    (1, 8, 1), (1, 64, 128), (2, 256, 384), (3, 72, 130), (16, 4096, 256), (17, 1000, 129), (31, 136, 100),
+    (64, 2048, 640), (65, 520, 255), (100, 4096, 257), (127, 64, 127), (128, 128, 256), (129, 192, 513),
+    (250, 1024, 1031), (256, 320, 999), (257, 8, 7), (600, 264, 300), (1000, 512, 1500)])
+def test_linear(cuda_lib, dtype, m, k, n):
+    check_linear(cuda_lib, np.random.default_rng(m + k + n), m, k, n, dtype, bias=bool(n & 1), residual=bool(m & 1))
+
+
+@pytest.mark.parametrize("m,k,n", [(5, 200, 77), (300, 200, 264)])
+@pytest.mark.parametrize("kw", [
+    dict(act="silu"), dict(act="gelu"), dict(act="gelu_tanh"), dict(act="silu", bias=True, residual=True),
+    dict(residual=True, in_place=True), dict(residual=True, in_place=True, act="gelu"), dict(gap=0),
+    dict(act="silu", by=100.0), dict(act="gelu_tanh", by=100.0)])
+def test_linear_variants(cuda_lib, m, k, n, kw):
+    check_linear(cuda_lib, np.random.default_rng(9), m, k, n, "bf16", **kw)
+
+
+def test_linear_takes_infinities_and_nan_as_they_come(cuda_lib):
+    x = torch.zeros(40, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(200, 64, dtype=torch.bfloat16, device="cuda")
+    x[3, 5], x[4, 6], x[7, 0] = float("inf"), float("nan"), 2.0
+    out = torch.empty(40, 200, dtype=torch.bfloat16, device="cuda")
+    for act in ("none", "silu", "gelu", "gelu_tanh"):
+        io = cuda_lib.make_linear_io(x, w, out, act=act)
+        ws = torch.empty(cuda_lib.mk_linear_workspace(io), dtype=torch.uint8, device="cuda")
+        cuda_lib.mk_linear(io, ws)
+        torch.cuda.synchronize()
+        assert bool(torch.isinf(out[3]).all()) and bool(torch.isnan(out[4]).all()) and bool((out[0] == 0).all())
+        assert bool((out[7] > 1.7).all()) and bool(torch.isfinite(out[5:]).all())
+
+
+# ---------------------------------------------------------- all of them
+
+def test_a_step_through_all_operators(cuda_lib):
+    """Projection, slots, norms with rotation and cache write, attention, projection
+    onto the residual stream, twice: the second step attends to the first one's keys.
+    The oracle goes on from what each operator was given, so that each is held to its
+    own tolerance."""
+    mk = cuda_lib
+    rng = np.random.default_rng(30)
+    H, hq, hk, d, page, B, width = 512, 8, 2, 64, 16, 5, 8
+    n_pages = B * width
+    w_qkv0, w_qkv = rounded(rng, ((hq + 2 * hk) * d, H), "bf16", H ** -0.5)
+    w_o0, w_o = rounded(rng, (H, hq * d), "bf16", (hq * d) ** -0.5)
+    b0, bias = rounded(rng, ((hq + 2 * hk) * d,), "bf16", 0.1)
+    (wq0, wq), (wk0, wk) = (rounded(rng, (d,), "bf16") for _ in range(2))
+    pools = [torch.zeros(n_pages, hk, page, w, dtype=torch.uint8, device="cuda") for w in (d // 2, d // 16) * 2]
+    exps = np.array([1, -1]), np.array([0, 2])
+    on_gpu = [dev(e) for e in exps]
+    kvq = mk.make_kvq_cache(*pools, *on_gpu)
+    table, head = dev(np.full((B, width), -1)), dev([0])
+    free = dev(rng.permutation(n_pages))
+    lens = dev([0] * B)
+    rope = mk.mk_rope_create(mk.make_rope_config(d))
+    f, m = ob.rope_frequencies(d)
+    for news in ([5, 33, 0, 1, 16], [1, 1, 4, 1, 2]):
+        n = sum(news)
+        cu, new_lens, summary = dev([0] * (B + 1)), dev([0] * B), dev([0] * 4)
+        positions, slots = dev([0] * n), dev([0] * n, torch.int64)
+        new = dev(news)
+        mk.mk_build_slots(mk.make_slots_io(lens, new, free, head, table, cu, new_lens, positions, slots, None,
+                                           summary, page, n_pages))
+        x0, x = rounded(rng, (n, H), "bf16")
+        qkv = torch.empty(n, hq + 2 * hk, d, dtype=torch.bfloat16, device="cuda")
+        io = mk.make_linear_io(x, w_qkv, qkv.view(n, -1), bias=bias)
+        ws = torch.empty(mk.mk_linear_workspace(io), dtype=torch.uint8, device="cuda")
+        mk.mk_linear(io, ws)
+        made = np64(qkv)
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+        mk.mk_qkv_append(rope, mk.make_qkv_append_io(q, q, k, v, positions, slots, q_norm=wq, k_norm=wk, kvq=kvq))
+        out = torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda")
+        aio = mk.make_kvq_attn_io(q, kvq, out, new_lens, cu, table)
+        aws = torch.empty(mk.mk_kvq_attn_workspace(aio), dtype=torch.uint8, device="cuda")
+        mk.mk_kvq_attn(aio, aws)
+        x_out = torch.empty_like(x)
+        oio = mk.make_linear_io(out.view(n, -1), w_o, x_out, residual=x)
+        ows = torch.empty(mk.mk_linear_workspace(oio), dtype=torch.uint8, device="cuda")
+        mk.mk_linear(oio, ows)
+        torch.cuda.synchronize()
+        lens, head = new_lens, summary[:1].clone()
+        assert mk.mk_linear_status(ws) == mk.mk_kvq_attn_status(aws) == mk.mk_linear_status(ows) == 0
+
+        want, s = ok.linear(x0, w_qkv0, b0)
+        assert np.all(np.abs(made.reshape(n, -1) - want) <= s * (H / 16 + 64) * 2 * V + U["bf16"] * np.abs(want) + 1e-6)
+        pos, sl = positions.cpu().numpy(), slots.cpu().numpy()
+        yq, mag = ok.norm_rope(made[:, :hq], wq0, 1e-6, pos, d, "half", f, m)
+        assert np.all(np.abs(np64(q) - yq) <= mag * 2.0 ** -20 + U["bf16"] * np.abs(yq))
+        yk, _ = ok.norm_rope(made[:, hq:hq + hk], wk0, 1e-6, pos, d, "half", f, m)
+        for i, y in ((0, yk), (2, made[:, hq + hk:])):
+            codes, scales = ok.encode(y, exps[i // 2][None])
+            got = [p.transpose(1, 2).reshape(n_pages * page, hk, -1)[slots].cpu().numpy() for p in pools[i:i + 2]]
+            assert np.array_equal(got[0], codes) and np.array_equal(got[1], scales)
+        kd, vd = (ok.decode_pool(pools[i].cpu().numpy(), pools[i + 1].cpu().numpy(), exps[i // 2]) for i in (0, 2))
+        ao, _, weight = ob.prefix_attn(np64(q), kd, vd, [], 0, table.cpu().numpy(), lens.cpu().numpy(), cu.cpu().numpy())
+        e_s = 3 * d ** 0.5 * V * np.abs(np64(q)).max() * d * np.abs(kd).max() + 2.0 ** -19
+        assert np.all(np.abs(np64(out) - ao) <= weight * (2.0 ** -11 + 2 * e_s + 2.0 ** -15) + U["bf16"] * np.abs(ao) + 2.0 ** -18)
+        want, s = ok.linear(np64(out).reshape(n, -1), w_o0, residual=x0)
+        assert np.all(np.abs(np64(x_out) - want) <= s * (hq * d / 16 + 64) * 2 * V + U["bf16"] * np.abs(want) + 1e-6)
+        assert np.array_equal(sl, slots.cpu().numpy())
+    mk.mk_rope_destroy(rope)
