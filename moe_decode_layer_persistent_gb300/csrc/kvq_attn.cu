@@ -1,8 +1,32 @@
 // kvq_attn.cu -- attention over a paged cache in 4 bits (mk_kvq_attn).
+//
+// Of a request's rows (token, q head of the group) those of one kv head form row
+// tiles of 8 or 16.  With a row tile's Q and 16 keys a step is
+//   S^T = K Q^T,  P = 2^(S - r),  l += P,  O^T += V^T P^T
+// in units of log2, r a reference near the maximum of each row so far.  K and V are
+// the products' first operands, 16 keys or 16 dimensions by 8 rows: with 4 rows per
+// kv head, as in plain decoding, half of the tensor core's work counts and not a
+// quarter or less, and the codes become operands in the registers of the thread
+// that needs them, without a second trip through shared memory.
+//
+// A key takes 144 bytes and 256 conversions per kv head (d = 128), so that the
+// conversions cost as much as HBM does.  What keeps them cheap: the dimensions of a
+// head may be summed over in any order, so each thread takes 32 neighbouring ones of
+// a key (16 bytes) and Q is laid out to match; a mask turns two codes into two fp16
+// 1024 + n, a fused multiply-add with the scale into values, exactly; for V, two
+// keys' words are interleaved by halves first, so that the pairs are pairs of keys.
+//
+// All key tiles of all items (request, kv head, row tile) lie on one line, of which
+// every warp takes an equal stretch, whatever the lengths are; each warp works by
+// itself, its copies in flight in a ring of its own.  A stretch that holds a whole
+// item writes its result, the others (O, r, l), which a second kernel, chained with
+// programmatic dependent launch, joins in the order of the line.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "kvq.cuh"
 #include "rope.h"
@@ -11,81 +35,663 @@ namespace mk {
 
 namespace {
 
+constexpr int kStep = 16;      // keys of a step
+constexpr int kTileSteps = 2;  // steps of a key tile, the unit of the line
+constexpr int kStages = 4;     // steps of a warp's ring
+// Weights are 2^(score - r) in fp16: r is set so that a row's largest is 2^6 and
+// moves when one passes 2^15; those below 2^-25 of the type vanish, 2^-31 of the
+// largest at most.
+constexpr float kRefBelow = 6.f, kRefMost = 15.f;
+constexpr float kNoRef = -1e30f;
+
+// An item whose stretches lie in several warps, as the warp with the first says.
+struct Split {
+  int32_t parts;     // 0: none
+  int32_t cu, rows;  // first row of the request, its rows of this kv head
+  int32_t first;     // first of these in the tile
+  int32_t h;
+};
+
 struct KvqParams {
   mk_kvq_attn_io io;
-  float scale_log2;  // scale * log2(e)
+  float scale_log2;  // scale * log2(e), times 8 (see Scales)
   int32_t group;
   int32_t page_shift;
+  int32_t workers;
+  Divisor by_group;
   uint32_t* status;
+  Split* split;      // [workers]
+  float2* stat;      // (r, l) of the rows of part 2 w (begins inside an item), 2 w + 1
+  float* o;          // [2 workers][rows][D]
 };
 
 MK_DEV int clampi(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : static_cast<int>(v); }
 
-// One row and q head per CTA, a key per warp at a time.
-template <class T, int D>
-__global__ void __launch_bounds__(128) k_kvq_simple(const __grid_constant__ KvqParams P) {
+// One request's lengths, made safe, and its place on the line.
+struct Req {
+  int32_t cu, n, len, base;
+  int32_t step0, tiles;  // first step and key tiles of its items
+  int32_t row_tiles;
+  MK_DEV int64_t cost(int heads) const { return static_cast<int64_t>(tiles) * row_tiles * heads; }
+};
+template <int R>
+MK_DEV Req read_req(const KvqParams& P, int b) {
+  const mk_kvq_attn_io& io = P.io;
+  Req r;
+  r.cu = clampi(io.cu_rows[b], 0, io.n_rows);
+  r.n = clampi(io.cu_rows[b + 1], r.cu, io.n_rows) - r.cu;
+  r.len = clampi(io.lens[b], 0, io.max_pages << P.page_shift);
+  r.base = max(0, r.len - r.n);
+  const int low = io.window ? max(0, r.base - io.window + 1) : 0;
+  r.step0 = low / kStep;
+  // (at least one, so that rows without keys are written)
+  r.tiles = max(1, ((r.len + kStep - 1) / kStep - r.step0 + kTileSteps - 1) / kTileSteps);
+  r.row_tiles = static_cast<int>((static_cast<int64_t>(r.n) * P.group + R - 1) / R);
+  return r;
+}
+
+MK_DEV void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+MK_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+MK_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// D += A B, 16 x 8 by 16.
+MK_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+MK_DEV uint32_t transposed8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+MK_DEV float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+MK_DEV uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+MK_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+MK_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+MK_DEV uint32_t and_or(uint32_t a, uint32_t mask, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(c));
+  return d;
+}
+
+// Factors for a pair of scales s: of codes in the low nibbles, 1024 + n, and the
+// high ones, 1024 + 16 n.  All in eighths, so that 1032 times the largest scale is
+// still an fp16; every factor and every result is exact.
+struct Scales {
+  uint32_t lo, hi, lo_off, hi_off;
+};
+MK_DEV Scales make_scales(uint32_t pair) {  // two E4M3 bytes
+  const uint32_t s = e4m3x2_to_half2(pair);
+  return {hmul2(s, 0x30003000u), hmul2(s, 0x20002000u), hmul2(s, 0xD808D808u), hmul2(s, 0xC880C880u)};
+}
+// x the low (I = 0) or the high byte's nibble pair of a word: two values.
+template <int HIGH>
+MK_DEV uint32_t values(uint32_t word, uint32_t lo, uint32_t off) {
+  return hfma2(and_or(word, HIGH ? 0x00F000F0u : 0x000F000Fu, 0x64006400u), lo, off);
+}
+
+template <int D>
+struct Layout {
+  static constexpr int kCodes = kStep * D / 2, kScales = kStep * D / 16;
+  static constexpr int kK = 0, kV = kCodes, kKs = 2 * kCodes, kVs = 2 * kCodes + kScales;
+  static constexpr int kStage = 2 * (kCodes + kScales);
+  // Key of row 2 t + 1 (the even rows' are t): chosen so that neither K's rows nor
+  // V's pairs of keys meet in a bank.
+  static constexpr int kFlip = D == 128 ? 1 : 2;
+};
+
+template <int WARPS>
+struct PlanSmem {
+  int64_t sum[WARPS];
+  int64_t first_at[WARPS];
+  int32_t first[WARPS];
+};
+
+// Warps per CTA (one CTA per SM): as many as registers allow.
+template <int NT>
+constexpr int kWarps = NT == 1 ? 16 : 12;
+
+template <class T, int D, int NT>
+__global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_constant__ KvqParams P) {
+  constexpr int R = 8 * NT, W = kWarps<NT>, TH = W * 32;
+  constexpr int KS = D / 16;   // products per 16 keys for the scores
+  constexpr int MT = D / 16;   // and for the values
+  using L = Layout<D>;
   const mk_kvq_attn_io& io = P.io;
   const mk_kvq_cache& c = io.kvq;
-  constexpr int V = D / 32;
-  __shared__ float part[4][D + 2];
-  const int row = blockIdx.x / io.n_q_heads, hq = blockIdx.x % io.n_q_heads, h = hq / P.group;
-  const int lane = lane_id(), warp = threadIdx.x / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ PlanSmem<W> plan;
+  const int lane = lane_id(), warp = threadIdx.x / 32, Hk = c.n_kv_heads;
+  const int worker = warp * gridDim.x + blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
-  int lo = 0, hi = io.n_requests;  // last b with cu_rows[b] <= row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (io.cu_rows[mid] <= row) lo = mid;
-    else hi = mid;
+
+  // The line: each thread adds up the requests of a stretch of the batch.
+  const int per = (io.n_requests + TH - 1) / TH;
+  const int b0 = min(io.n_requests, static_cast<int>(threadIdx.x) * per), b1 = min(io.n_requests, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += read_req<R>(P, b).cost(Hk);
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
   }
-  if (io.cu_rows[lo] > row || io.cu_rows[lo + 1] <= row) return;
-  const int cu = clampi(io.cu_rows[lo], 0, io.n_rows), n = clampi(io.cu_rows[lo + 1], cu, io.n_rows) - cu;
-  const int len = clampi(io.lens[lo], 0, io.max_pages << P.page_shift);
-  const int base = max(0, len - n), i = row - cu;
-  const uint64_t mask = io.tree_mask ? io.tree_mask[row] : 0;
-  const int p = base + (io.tree_mask ? __popcll(mask) - 1 : i);
-  const int first = io.window ? max(0, p - io.window + 1) : 0;
-  const int last = io.tree_mask ? len : min(len, base + i + 1);
-  const T* q = static_cast<const T*>(io.q) + row * io.q_stride + hq * D + lane * V;
-  float x[V], acc[V] = {}, m = -INFINITY, sum = 0.f;
-  const float unit_k = pow2(c.k_exp ? clamp_exp(c.k_exp[h]) : 0), unit_v = pow2(c.v_exp ? clamp_exp(c.v_exp[h]) : 0);
-  for (int v = 0; v < V; ++v) x[v] = static_cast<float>(q[v]);
-  for (int j = first + warp; j < last; j += 4) {
-    if (io.tree_mask && j >= base && !(j - base < 64 && mask >> (j - base) & 1)) continue;
-    const int page = io.block_table[lo * io.table_stride + (j >> P.page_shift)];
-    float kv[2][V] = {};
-    if (page >= 0 && page < c.n_pages) {
-      const int64_t at = ((static_cast<int64_t>(page) * c.n_kv_heads + h) << P.page_shift) + (j & (c.page_size - 1));
+  if (lane == 31) plan.sum[warp] = upto;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w == warp) upto += total;
+    total += plan.sum[w];
+  }
+  const int64_t share = max(static_cast<int64_t>(1), (total + P.workers - 1) / P.workers);
+  if (mine) {
+    for (int w = 0; w < W; ++w) {
+      const int64_t at = (static_cast<int64_t>(w) * gridDim.x + blockIdx.x) * share;
+      if (at < upto - mine || at >= upto) continue;
+      int64_t begin = upto - mine;
+      int b = b0;
+      for (; b < b1 - 1; ++b) {
+        const int64_t cost = read_req<R>(P, b).cost(Hk);
+        if (at < begin + cost) break;
+        begin += cost;
+      }
+      plan.first[w] = b;
+      plan.first_at[w] = begin;
+    }
+  }
+  __syncthreads();
+  int64_t pos = worker * share;
+  const int64_t end = min(total, pos + share);
+  if (lane == 0) P.split[worker].parts = 0;
+  if (pos >= end) return;
+  int b = plan.first[warp];
+  int64_t begin = plan.first_at[warp];
+
+  uint8_t* ring = smem + warp * (kStages * L::kStage);
+  const uint32_t ring32 = smem_u32(ring);
+  const int g = lane >> 2, t = lane & 3;
+  const int key_even = g >> 1, key_g = g & 1 ? 4 + (key_even ^ L::kFlip) : key_even;  // of row g of K
+  const int key_0 = t, key_1 = 4 + (t ^ L::kFlip);                                    // of V's pair
+  while (pos < end) {
+    const Req rq = read_req<R>(P, b);
+    const int64_t cost = rq.cost(Hk);
+    if (pos >= begin + cost) {
+      begin += cost;
+      ++b;
+      continue;
+    }
+    const int64_t off = pos - begin, item = off / rq.tiles;
+    const int h = static_cast<int>(item / rq.row_tiles), rt = static_cast<int>(item - static_cast<int64_t>(h) * rq.row_tiles);
+    const int ta = static_cast<int>(off - item * rq.tiles);
+    const int tb = static_cast<int>(min(static_cast<int64_t>(rq.tiles), ta + (end - pos)));
+    pos += tb - ta;
+    const int rows = rq.n * P.group;  // (checked by the host to be an int)
+
+    // Q of this thread's column of the second operand: row g of each 8
+    uint32_t qf[NT][KS][2];
+    float c_row[NT][2];            // factor on the scores of rows 2 t, 2 t + 1
+    int lo[NT][2], hi[NT][2];      // keys that they see (of a tree: before its own)
+    int klo = INT_MAX, khi = 0, full_lo = 0, full_hi = INT_MAX;
+    const float unit_k = pow2(c.k_exp ? clamp_exp(c.k_exp[h]) : 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int f = rt * R + nt * 8 + g;
+      const bool valid = f < rows;
+      const int i = quotient(valid ? f : 0, P.by_group), hq = h * P.group + (valid ? f - i * P.group : 0);
+      const int64_t row = rq.cu + i;
+      // dimensions 32 t .. (64: 16 t ..), 8 at a time: two words of pairs (x, x + 4)
+      float factor = 1.f;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(io.q) + row * io.q_stride + hq * D + t * (D / 4));
+      uint4 raw[D / 32];
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) raw[j] = valid ? src[j] : make_uint4(0, 0, 0, 0);
+      if (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+        // bf16 into fp16, relative to the row's largest value
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[j].x & 0x7FFF7FFFu, raw[j].y & 0x7FFF7FFFu),
+                                       __vmaxu2(raw[j].z & 0x7FFF7FFFu, raw[j].w & 0x7FFF7FFFu)));
+        top = max(top & 0xFFFFu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = min(max(static_cast<int>(top >> 7), 1), 253);  // biased; up to 2 * 2^e
+        factor = top < 0x7F80u ? __int_as_float(e << 23) : 1.f;
+        const float inv = top < 0x7F80u ? __int_as_float((254 - e) << 23) : 1.f;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(&raw[j]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = Pack<T>::get(w[k]);
+            w[k] = half2_bits(x.x * inv, x.y * inv);
+          }
+        }
+      }
+      // words (0,1)(2,3)(4,5)(6,7) into (0,4)(1,5)(2,6)(3,7)
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        qf[nt][2 * j][0] = __byte_perm(raw[j].x, raw[j].z, 0x5410);
+        qf[nt][2 * j][1] = __byte_perm(raw[j].x, raw[j].z, 0x7632);
+        qf[nt][2 * j + 1][0] = __byte_perm(raw[j].y, raw[j].w, 0x5410);
+        qf[nt][2 * j + 1][1] = __byte_perm(raw[j].y, raw[j].w, 0x7632);
+      }
+      // the keys of row g, then those of rows 2 t and 2 t + 1
+      int my_lo = 0, my_hi = 0;
+      if (valid) {
+        const int p = rq.base + (io.tree_mask ? __popcll(io.tree_mask[row]) - 1 : i);
+        my_lo = io.window ? max(0, p - io.window + 1) : 0;
+        my_hi = io.tree_mask ? min(rq.len, rq.base) : min(rq.len, rq.base + i + 1);
+        klo = min(klo, my_lo);
+        khi = max(khi, io.tree_mask ? min(rq.len, rq.base + 64) : my_hi);
+        full_lo = max(full_lo, my_lo);
+        full_hi = min(full_hi, my_hi);
+      }
+#pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const uint8_t* codes = static_cast<const uint8_t*>(k ? c.v_codes : c.k_codes) + at * (D / 2) + lane * V / 2;
-        const float s = e4m3_to_float((static_cast<const uint8_t*>(k ? c.v_scales : c.k_scales) + at * (D / 16))[lane * V / 16]);
-        for (int v = 0; v < V; ++v) kv[k][v] = (static_cast<int>(codes[v / 2] >> (4 * (v & 1)) & 15) - 8) * s;
+        c_row[nt][k] = P.scale_log2 * __shfl_sync(0xffffffffu, factor, 8 * t + 4 * k) * unit_k;
+        lo[nt][k] = __shfl_sync(0xffffffffu, my_lo, 8 * t + 4 * k);
+        hi[nt][k] = __shfl_sync(0xffffffffu, my_hi, 8 * t + 4 * k);
       }
     }
-    float dot = 0.f;
-    for (int v = 0; v < V; ++v) dot += x[v] * kv[0][v];
-    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    const float s = dot * unit_k * P.scale_log2, top = s > m ? s : m != m ? m : s != s ? s : m;
-    const float old = exp2f(m - top), w = exp2f(s - top);
-    sum = sum * old + w;
-    for (int v = 0; v < V; ++v) acc[v] = acc[v] * old + w * kv[1][v];
-    m = top;
+    klo = __reduce_min_sync(0xffffffffu, klo);
+    khi = __reduce_max_sync(0xffffffffu, khi);
+    full_lo = __reduce_max_sync(0xffffffffu, full_lo);
+    full_hi = __reduce_min_sync(0xffffffffu, full_hi);
+
+    float o[NT][MT][4];
+    float ref[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      ref[nt][0] = ref[nt][1] = kNoRef;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.f;
+    }
+
+    const int s_a = max(rq.step0 + ta * kTileSteps, min(klo, khi) / kStep);
+    const int s_b = min(rq.step0 + tb * kTileSteps, (khi + kStep - 1) / kStep);
+    const int32_t* table = io.block_table + b * io.table_stride;
+    // pages of 32 steps from `pages_at` on, one per lane
+    int pages_at = s_a;
+    auto page_of = [&](int s) { return s < s_b ? table[s * kStep >> P.page_shift] : -1; };
+    int pages = s_a < s_b ? page_of(s_a + lane) : -1, pages_next = s_a + 32 < s_b ? page_of(s_a + 32 + lane) : -1;
+    const int64_t head_row = static_cast<int64_t>(h) << P.page_shift;
+    auto issue = [&](int s) {
+      if (s < s_b) {
+        if (s - pages_at >= 32) {
+          pages_at += 32;
+          pages = pages_next;
+          pages_next = page_of(s + 32 + lane);
+        }
+        const int page = __shfl_sync(0xffffffffu, pages, s - pages_at);
+        const bool there = page >= 0 && page < c.n_pages;
+        const int64_t row = there ? ((static_cast<int64_t>(page) * Hk) << P.page_shift) + head_row + ((s * kStep) & (c.page_size - 1)) : 0;
+        const uint32_t at = ring32 + ((s - s_a) & (kStages - 1)) * L::kStage;
+        const uint8_t* k = static_cast<const uint8_t*>(c.k_codes) + row * (D / 2) + lane * 16;
+        const uint8_t* v = static_cast<const uint8_t*>(c.v_codes) + row * (D / 2) + lane * 16;
+        if (D == 128) {
+          const uint32_t turn = (lane >> 3 & 1) << 5;  // see the loads of V
+          cp_async16(at + L::kK + lane * 16, k, there);
+          cp_async16(at + L::kK + 512 + lane * 16, k + 512, there);
+          cp_async16(at + L::kV + ((lane * 16) ^ turn), v, there);
+          cp_async16(at + L::kV + 512 + ((lane * 16) ^ turn), v + 512, there);
+        } else {
+          cp_async16(at + L::kK + lane * 16, k, there);
+          cp_async16(at + L::kV + lane * 16, v, there);
+        }
+        constexpr int n = L::kScales / 16;
+        if (lane < 2 * n) {
+          const uint8_t* sc = static_cast<const uint8_t*>(lane < n ? c.k_scales : c.v_scales) + row * (D / 16) + (lane & (n - 1)) * 16;
+          cp_async16(at + L::kKs + lane * 16, sc, there);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(s_a + i);
+#pragma unroll 1
+    for (int s = s_a; s < s_b; ++s) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      issue(s + kStages - 1);
+      const uint8_t* st = ring + ((s - s_a) & (kStages - 1)) * L::kStage;
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc[nt][k] = 0.f;
+      // scores: rows g and g + 8 are the keys key_g and key_g + 8
+      {
+        constexpr int WORDS = D / 32;  // of 8 codes, of this thread's dimensions of a key
+        uint32_t w[2][WORDS];
+        Scales f[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int key = key_g + 8 * k;
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(st + L::kK + key * 64 + t * 16);
+            w[k][0] = x.x, w[k][1] = x.y, w[k][2 % WORDS] = x.z, w[k][3 % WORDS] = x.w;
+            f[k] = make_scales(*reinterpret_cast<const uint16_t*>(st + L::kKs + key * 8 + t * 2));
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(st + L::kK + key * 32 + t * 8);
+            w[k][0] = x.x, w[k][1] = x.y;
+            const uint32_t one = st[L::kKs + key * 4 + t];
+            f[k] = make_scales(one | one << 8);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < WORDS; ++j) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            Scales x = f[k];
+            if (D == 128) {  // words 0, 1 are of the first group of 16, 2, 3 of the second
+              const uint32_t sel = j < 2 ? 0x1010u : 0x3232u;
+              x.lo = __byte_perm(x.lo, 0, sel);
+              x.hi = __byte_perm(x.hi, 0, sel);
+              x.lo_off = __byte_perm(x.lo_off, 0, sel);
+              x.hi_off = __byte_perm(x.hi_off, 0, sel);
+            }
+            const uint32_t up = w[k][j] >> 8;
+            a[k][0] = values<0>(w[k][j], x.lo, x.lo_off);
+            a[k][1] = values<1>(w[k][j], x.hi, x.hi_off);
+            a[k][2] = values<0>(up, x.lo, x.lo_off);
+            a[k][3] = values<1>(up, x.hi, x.hi_off);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(sc[nt], a[0][0], a[1][0], a[0][1], a[1][1], qf[nt][2 * j][0], qf[nt][2 * j][1]);
+            mma16816(sc[nt], a[0][2], a[1][2], a[0][3], a[1][3], qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+          }
+        }
+      }
+      const int j0 = s * kStep;
+      const bool edge = j0 < full_lo || j0 + kStep > full_hi;
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc[nt][k] *= c_row[nt][k & 1];
+        if (edge) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = j0 + key_g + (k & 2) * 4;
+            bool see = j >= lo[nt][k & 1] && j < hi[nt][k & 1];
+            if (io.tree_mask && j >= rq.base && j < khi) {
+              const int fr = rt * R + nt * 8 + 2 * t + (k & 1);
+              see = fr < rows && (io.tree_mask[rq.cu + quotient(fr, P.by_group)] >> (j - rq.base) & 1);
+            }
+            if (!see) sc[nt][k] = -INFINITY;
+          }
+        }
+        over |= fmaxf(sc[nt][0], sc[nt][2]) - ref[nt][0] > kRefMost || fmaxf(sc[nt][1], sc[nt][3]) - ref[nt][1] > kRefMost;
+      }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float top = fmaxf(sc[nt][k], sc[nt][k + 2]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float next = top - ref[nt][k] > kRefMost ? top - kRefBelow : ref[nt][k];
+            const float old = exp2_approx(ref[nt][k] - next);
+            ref[nt][k] = next;
+            l[nt][k] *= old;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              o[nt][i][k] *= old;
+              o[nt][i][k + 2] *= old;
+            }
+          }
+      }
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = exp2_approx(sc[nt][k] - ref[nt][k & 1]);
+        l[nt][0] += p[0] + p[2];
+        l[nt][1] += p[1] + p[3];
+        pf[nt][0] = transposed8x8(half2_bits(p[0], p[1]));
+        pf[nt][1] = transposed8x8(half2_bits(p[2], p[3]));
+      }
+      // values: of 16 keys the pairs (key_0, key_1) and 8 further on
+      {
+        constexpr int WORDS = D / 64;  // of this thread's dimensions of a key
+        uint32_t w[4][WORDS];
+        Scales f[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int ka = key_0 + 8 * k, kb = key_1 + 8 * k;
+          uint32_t sa, sb;
+          if (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(st + L::kV + ((ka * 64 + g * 8) ^ ((ka >> 1 & 1) << 5)));
+            const uint2 y = *reinterpret_cast<const uint2*>(st + L::kV + ((kb * 64 + g * 8) ^ ((kb >> 1 & 1) << 5)));
+            w[2 * k][0] = x.x, w[2 * k][1 % WORDS] = x.y;
+            w[2 * k + 1][0] = y.x, w[2 * k + 1][1 % WORDS] = y.y;
+            sa = st[L::kVs + ka * 8 + g], sb = st[L::kVs + kb * 8 + g];
+          } else {
+            w[2 * k][0] = *reinterpret_cast<const uint32_t*>(st + L::kV + ka * 32 + g * 4);
+            w[2 * k + 1][0] = *reinterpret_cast<const uint32_t*>(st + L::kV + kb * 32 + g * 4);
+            sa = st[L::kVs + ka * 4 + g / 2], sb = st[L::kVs + kb * 4 + g / 2];
+          }
+          if (edge) {  // keys that no row sees may hold anything
+            if (j0 + ka < klo || j0 + ka >= khi) sa = 0;
+            if (j0 + kb < klo || j0 + kb >= khi) sb = 0;
+          }
+          f[k] = make_scales(sa | sb << 8);
+        }
+#pragma unroll
+        for (int j = 0; j < WORDS; ++j) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // dimensions 8 j + 4 half ..
+            uint32_t a[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t x = __byte_perm(w[2 * k][j], w[2 * k + 1][j], half ? 0x7632 : 0x5410), up = x >> 8;
+              a[k][0] = values<0>(x, f[k].lo, f[k].lo_off);
+              a[k][1] = values<1>(x, f[k].hi, f[k].hi_off);
+              a[k][2] = values<0>(up, f[k].lo, f[k].lo_off);
+              a[k][3] = values<1>(up, f[k].hi, f[k].hi_off);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(o[nt][4 * j + 2 * half], a[0][0], a[0][1], a[1][0], a[1][1], pf[nt][0], pf[nt][1]);
+              mma16816(o[nt][4 * j + 2 * half + 1], a[0][2], a[0][3], a[1][2], a[1][3], pf[nt][0], pf[nt][1]);
+            }
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+
+    // this thread's: rows 2 t and 2 t + 1, dimensions D / 8 g .. (o[i][k]: 2 i, o[i][k + 2]: 2 i + 1)
+    const bool whole = ta == 0 && tb == rq.tiles;
+    const float unit_v = 8.f * pow2(c.v_exp ? clamp_exp(c.v_exp[h]) : 0);
+    if (lane == 0 && ta == 0 && !whole) {
+      // (the item starts at pos - (tb - ta) and its last tile lies in this worker's stretch or a later one)
+      const int64_t last = (pos - tb + rq.tiles - 1) / share;
+      P.split[worker] = {static_cast<int32_t>(last - worker + 1), rq.cu, rows, rt * R, h};
+    }
+    const int64_t part = 2ll * worker + (ta == 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float sum = l[nt][k];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int r = nt * 8 + 2 * t + k, fr = rt * R + r;
+        if (fr >= rows) continue;
+        if (!whole) {
+          float* to = P.o + (part * R + r) * D + g * (D / 8);
+#pragma unroll
+          for (int i = 0; i < MT; i += 2)
+            *reinterpret_cast<float4*>(to + 2 * i) = make_float4(o[nt][i][k] * unit_v, o[nt][i][k + 2] * unit_v, o[nt][i + 1][k] * unit_v, o[nt][i + 1][k + 2] * unit_v);
+          if (g == 0) P.stat[part * R + r] = make_float2(ref[nt][k], sum);
+          continue;
+        }
+        const int i = quotient(fr, P.by_group), hq = h * P.group + fr - i * P.group;
+        const int64_t row = rq.cu + i;
+        const float inv = sum != 0.f ? unit_v / sum : 0.f;
+        uint32_t y[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) y[m] = Pack<T>::put(o[nt][m][k] * inv, o[nt][m][k + 2] * inv);
+        uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(io.out) + row * io.out_stride + hq * D + g * (D / 8));
+#pragma unroll
+        for (int m = 0; m < MT / 4; ++m) to[m] = make_uint4(y[4 * m], y[4 * m + 1], y[4 * m + 2], y[4 * m + 3]);
+        if (g == 0 && io.lse)
+          io.lse[row * io.n_q_heads + hq] = sum != 0.f ? (ref[nt][k] + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      }
   }
-  for (int v = 0; v < V; ++v) part[warp][lane * V + v] = acc[v];
-  if (lane == 0) part[warp][D] = m, part[warp][D + 1] = sum;
-  __syncthreads();
-  if (warp) return;
-  float top = -INFINITY;
-  for (int w = 0; w < 4; ++w) top = part[w][D] > top || part[w][D] != part[w][D] ? part[w][D] : top;
-  float all = 0.f, out[V] = {};
-  for (int w = 0; w < 4; ++w) {
-    const float f = part[w][D] == -INFINITY ? 0.f : exp2f(part[w][D] - top);
-    all += f * part[w][D + 1];
-    for (int v = 0; v < V; ++v) out[v] += f * part[w][lane * V + v];
+}
+
+// Joins the parts of a split item: part 2 w + 1 of the worker with the first and
+// parts 2 (w + 1), ... of those behind it.  A CTA takes R / gridDim.y of its rows;
+// its warps share out the parts.
+constexpr int kJoinWarps = 8;
+template <class T, int D, int R>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_kvq_join(const __grid_constant__ KvqParams P) {
+  constexpr int V = D / 32;
+  __shared__ float sum_o[kJoinWarps][D];
+  __shared__ float2 sum_l[kJoinWarps];
+  const mk_kvq_attn_io& io = P.io;
+  const int lane = lane_id(), warp = threadIdx.x / 32, worker = blockIdx.x;
+  pdl_wait();
+  const Split sp = P.split[worker];
+  if (sp.parts == 0) return;
+  const int rows = R / gridDim.y;
+  for (int r = blockIdx.y * rows; r < static_cast<int>(blockIdx.y + 1) * rows; ++r) {
+    const int fr = sp.first + r;
+    if (fr >= sp.rows) return;
+    float acc[V] = {}, top = kNoRef, all = 0.f;
+#pragma unroll 4
+    for (int p = warp; p < sp.parts; p += kJoinWarps) {
+      const int64_t at = (p ? 2ll * (worker + p) : 2ll * worker + 1) * R + r;
+      const float2 x = P.stat[at];
+      const float* o = P.o + at * D + lane * V;
+      float y[V];
+      if (V == 4) *reinterpret_cast<float4*>(y) = __ldcs(reinterpret_cast<const float4*>(o));
+      else *reinterpret_cast<float2*>(y) = __ldcs(reinterpret_cast<const float2*>(o));
+      const float next = fmaxf(top, x.x), old = exp2f(top - next), f = exp2f(x.x - next);
+      top = next;
+      all = all * old + x.y * f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = acc[v] * old + y[v] * f;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum_o[warp][lane * V + v] = acc[v];
+    if (lane == 0) sum_l[warp] = make_float2(top, all);
+    __syncthreads();
+    if (warp == 0) {
+      const int n = min(kJoinWarps, sp.parts);
+      float m = kNoRef, s = 0.f, out[V] = {};
+      for (int w = 0; w < n; ++w) m = fmaxf(m, sum_l[w].x);
+      for (int w = 0; w < n; ++w) {
+        const float f = exp2f(sum_l[w].x - m);
+        s += sum_l[w].y * f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] += sum_o[w][lane * V + v] * f;
+      }
+      const float inv = s != 0.f ? 1.f / s : 0.f;
+      const int i = quotient(fr, P.by_group), hq = sp.h * P.group + fr - i * P.group;
+      const int64_t row = sp.cu + i;
+      uint32_t y[V / 2];
+#pragma unroll
+      for (int v = 0; v < V; v += 2) y[v / 2] = Pack<T>::put(out[v] * inv, out[v + 1] * inv);
+      uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<T*>(io.out) + row * io.out_stride + hq * D + lane * V);
+#pragma unroll
+      for (int v = 0; v < V / 2; ++v) to[v] = y[v];
+      if (lane == 0 && io.lse)
+        io.lse[row * io.n_q_heads + hq] = s != 0.f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
+    }
+    __syncthreads();
   }
-  T* to = static_cast<T*>(io.out) + row * io.out_stride + hq * D + lane * V;
-  const float inv = all != 0.f ? unit_v / all : 0.f;
-  for (int v = 0; v < V; ++v) to[v] = static_cast<T>(out[v] * inv);
-  if (lane == 0 && io.lse) io.lse[static_cast<int64_t>(row) * io.n_q_heads + hq] = all != 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY;
+}
+
+int64_t align256(int64_t v) { return (v + 255) & ~static_cast<int64_t>(255); }
+
+// Lays the workspace out for `workers` over `base`; returns its size.
+int64_t lay_out(int workers, int rows, int d, uint8_t* base, KvqParams* P) {
+  int64_t at = 256;
+  P->status = reinterpret_cast<uint32_t*>(base);
+  P->split = reinterpret_cast<Split*>(base + at);
+  at = align256(at + workers * static_cast<int64_t>(sizeof(Split)));
+  P->stat = reinterpret_cast<float2*>(base + at);
+  at = align256(at + 2ll * workers * rows * 8);
+  P->o = reinterpret_cast<float*>(base + at);
+  return align256(at + 2ll * workers * rows * d * 4);
+}
+
+// Rows per tile: 16 where 8 would be passed on average.
+int rows_of_tile(const mk_kvq_attn_io* io) {
+  const int64_t group = io->n_q_heads / io->kvq.n_kv_heads;
+  return io->n_rows * group > 8ll * io->n_requests ? 16 : 8;
+}
+int workers_of(int rows, int sms) { return sms * (rows == 8 ? kWarps<1> : kWarps<2>); }
+
+template <class T, int D, int NT>
+mk_status launch(const KvqParams& P, int device, int sms, cudaStream_t s) {
+  constexpr int R = 8 * NT, smem = kWarps<NT> * kStages * Layout<D>::kStage;
+  static std::atomic<uint64_t> ready{0};  // (once per device: it takes as long as a launch)
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_kvq_attn<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  lc.stream = s;
+  lc.gridDim = dim3(sms);
+  lc.blockDim = dim3(kWarps<NT> * 32);
+  lc.dynamicSmemBytes = smem;
+  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_attn<T, D, NT>, P));
+  // few items, many parts each: rows on CTAs of their own
+  const int64_t items = (static_cast<int64_t>(P.io.n_rows) * P.group / R + P.io.n_requests) * P.io.kvq.n_kv_heads;
+  lc.gridDim = dim3(P.workers, items * 16 < P.workers ? R : 1);
+  lc.blockDim = dim3(kJoinWarps * 32);
+  lc.dynamicSmemBytes = 0;
+  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_join<T, D, R>, P));
+  return MK_OK;
+}
+template <class T, int D>
+mk_status launch(const KvqParams& P, int rows, int device, int sms, cudaStream_t s) {
+  return rows == 8 ? launch<T, D, 1>(P, device, sms, s) : launch<T, D, 2>(P, device, sms, s);
 }
 
 mk_status check_shapes(const mk_kvq_attn_io* io) {
@@ -114,7 +720,12 @@ mk_status mk_kvq_attn_workspace(const mk_kvq_attn_io* io, int64_t* bytes) {
   *bytes = 0;
   const mk_status st = check_shapes(io);
   if (st != MK_OK) return st;
-  *bytes = 256;
+  int dev = -1, sms = 0;
+  MK_CUDA_TRY(cudaGetDevice(&dev));
+  MK_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  KvqParams P;
+  const int rows = rows_of_tile(io);
+  *bytes = lay_out(workers_of(rows, sms), rows, io->kvq.head_dim, nullptr, &P);
   return MK_OK;
 }
 
@@ -156,30 +767,27 @@ mk_status mk_kvq_attn(const mk_kvq_attn_io* io, void* workspace, int64_t workspa
     for (int b = a + 1; b < 3; ++b)
       if (overlap(out[a].p, out[a].n, out[b].p, out[b].n)) return MK_ERR_INVALID_ARG;
   }
-  if (workspace_bytes < 256) return MK_ERR_INVALID_ARG;
-  st = check_device(workspace, nullptr, nullptr);
+  int device = 0, sms = 0;
+  st = check_device(workspace, &device, &sms);
   if (st != MK_OK) return st;
+  const int tile = rows_of_tile(io);
+  KvqParams P;
+  P.workers = workers_of(tile, sms);
+  if (workspace_bytes < lay_out(P.workers, tile, static_cast<int>(d), static_cast<uint8_t*>(workspace), &P))
+    return MK_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n == 0) {
     MK_CUDA_TRY(cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s));
     return MK_OK;
   }
-  KvqParams P;
   P.io = *io;
-  P.scale_log2 = (io->scale != 0.f ? io->scale : 1.f / std::sqrt(static_cast<float>(d))) * 1.4426950408889634f;
+  P.scale_log2 = (io->scale != 0.f ? io->scale : 1.f / std::sqrt(static_cast<float>(d))) * (8.f * 1.4426950408889634f);
   P.group = io->n_q_heads / c.n_kv_heads;
+  P.by_group = make_divisor(P.group);
   P.page_shift = __builtin_ctz(static_cast<uint32_t>(c.page_size));
-  P.status = static_cast<uint32_t*>(workspace);
-  const unsigned grid = static_cast<unsigned>(n * io->n_q_heads);
-  if (io->dtype == MK_BF16) {
-    if (d == 128) k_kvq_simple<__nv_bfloat16, 128><<<grid, 128, 0, s>>>(P);
-    else k_kvq_simple<__nv_bfloat16, 64><<<grid, 128, 0, s>>>(P);
-  } else {
-    if (d == 128) k_kvq_simple<__half, 128><<<grid, 128, 0, s>>>(P);
-    else k_kvq_simple<__half, 64><<<grid, 128, 0, s>>>(P);
-  }
-  MK_CUDA_TRY(cudaGetLastError());
-  return MK_OK;
+  if (io->dtype == MK_BF16)
+    return d == 128 ? launch<__nv_bfloat16, 128>(P, tile, device, sms, s) : launch<__nv_bfloat16, 64>(P, tile, device, sms, s);
+  return d == 128 ? launch<__half, 128>(P, tile, device, sms, s) : launch<__half, 64>(P, tile, device, sms, s);
 }
 
 mk_status mk_kvq_attn_status(const void* workspace) {
