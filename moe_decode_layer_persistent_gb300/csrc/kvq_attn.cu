@@ -1,7 +1,7 @@
 // kvq_attn.cu -- attention over a paged cache in 4 bits (mk_kvq_attn).
 //
 // Of a request's rows (token, q head of the group) those of one kv head form row
-// tiles of 8 or 16.  With a row tile's Q and 16 keys a step is
+// tiles of 8 or 16.  With a row tile's Q and 32 keys a step is
 //   S^T = K Q^T,  P = 2^(S - r),  l += P,  O^T += V^T P^T
 // in units of log2, r a reference near the maximum of each row so far.  K and V are
 // the products' first operands, 16 keys or 16 dimensions by 8 rows: with 4 rows per
@@ -35,9 +35,8 @@ namespace mk {
 
 namespace {
 
-constexpr int kStep = 16;      // keys of a step
-constexpr int kTileSteps = 2;  // steps of a key tile, the unit of the line
-constexpr int kStages = 4;     // steps of a warp's ring
+constexpr int kKeys = 32;   // of a key tile: a step of a warp, and the unit of the line
+constexpr int kStages = 3;  // key tiles of a warp's ring
 // Weights are 2^(score - r) in fp16: r is set so that a row's largest is 2^6 and
 // moves when one passes 2^15; those below 2^-25 of the type vanish, 2^-31 of the
 // largest at most.
@@ -57,6 +56,7 @@ struct KvqParams {
   float scale_log2;  // scale * log2(e), times 8 (see Scales)
   int32_t group;
   int32_t page_shift;
+  uint32_t page_bytes;  // of codes
   int32_t workers;
   Divisor by_group;
   uint32_t* status;
@@ -70,7 +70,7 @@ MK_DEV int clampi(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi 
 // One request's lengths, made safe, and its place on the line.
 struct Req {
   int32_t cu, n, len, base;
-  int32_t step0, tiles;  // first step and key tiles of its items
+  int32_t tile0, tiles;  // first key tile of its items and how many they have
   int32_t row_tiles;
   MK_DEV int64_t cost(int heads) const { return static_cast<int64_t>(tiles) * row_tiles * heads; }
 };
@@ -83,9 +83,9 @@ MK_DEV Req read_req(const KvqParams& P, int b) {
   r.len = clampi(io.lens[b], 0, io.max_pages << P.page_shift);
   r.base = max(0, r.len - r.n);
   const int low = io.window ? max(0, r.base - io.window + 1) : 0;
-  r.step0 = low / kStep;
+  r.tile0 = low / kKeys;
   // (at least one, so that rows without keys are written)
-  r.tiles = max(1, ((r.len + kStep - 1) / kStep - r.step0 + kTileSteps - 1) / kTileSteps);
+  r.tiles = max(1, (r.len + kKeys - 1) / kKeys - r.tile0);
   r.row_tiles = static_cast<int>((static_cast<int64_t>(r.n) * P.group + R - 1) / R);
   return r;
 }
@@ -119,16 +119,7 @@ MK_DEV uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-MK_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-MK_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
+MK_DEV __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 MK_DEV uint32_t and_or(uint32_t a, uint32_t mask, uint32_t c) {
   uint32_t d;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(c));
@@ -139,38 +130,61 @@ MK_DEV uint32_t and_or(uint32_t a, uint32_t mask, uint32_t c) {
 // high ones, 1024 + 16 n.  All in eighths, so that 1032 times the largest scale is
 // still an fp16; every factor and every result is exact.
 struct Scales {
-  uint32_t lo, hi, lo_off, hi_off;
+  __half2 lo, hi, lo_off, hi_off;
+  MK_DEV Scales first() const { return {__low2half2(lo), __low2half2(hi), __low2half2(lo_off), __low2half2(hi_off)}; }
+  MK_DEV Scales second() const { return {__high2half2(lo), __high2half2(hi), __high2half2(lo_off), __high2half2(hi_off)}; }
 };
 MK_DEV Scales make_scales(uint32_t pair) {  // two E4M3 bytes
-  const uint32_t s = e4m3x2_to_half2(pair);
-  return {hmul2(s, 0x30003000u), hmul2(s, 0x20002000u), hmul2(s, 0xD808D808u), hmul2(s, 0xC880C880u)};
+  const __half2 s = as_half2(e4m3x2_to_half2(pair));
+  return {__hmul2(s, as_half2(0x30003000u)), __hmul2(s, as_half2(0x20002000u)), __hmul2(s, as_half2(0xD808D808u)),
+          __hmul2(s, as_half2(0xC880C880u))};
 }
-// x the low (I = 0) or the high byte's nibble pair of a word: two values.
-template <int HIGH>
-MK_DEV uint32_t values(uint32_t word, uint32_t lo, uint32_t off) {
-  return hfma2(and_or(word, HIGH ? 0x00F000F0u : 0x000F000Fu, 0x64006400u), lo, off);
+// Eight codes, as four pairs (x, x + 4).
+MK_DEV void values(uint32_t word, const Scales& f, uint32_t (&y)[4]) {
+  const uint32_t up = word >> 8;
+  const __half2 v[4] = {__hfma2(as_half2(and_or(word, 0x000F000Fu, 0x64006400u)), f.lo, f.lo_off),
+                        __hfma2(as_half2(and_or(word, 0x00F000F0u, 0x64006400u)), f.hi, f.hi_off),
+                        __hfma2(as_half2(and_or(up, 0x000F000Fu, 0x64006400u)), f.lo, f.lo_off),
+                        __hfma2(as_half2(and_or(up, 0x00F000F0u, 0x64006400u)), f.hi, f.hi_off)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const uint32_t*>(&v[i]);
 }
 
+// A stage of a warp's ring: two blocks of 16 keys, each K's codes, V's codes, K's
+// scales, V's scales (a page may hold no more than 16 keys).
 template <int D>
 struct Layout {
-  static constexpr int kCodes = kStep * D / 2, kScales = kStep * D / 16;
+  static constexpr int kCodes = 16 * D / 2, kScales = 16 * D / 16;
   static constexpr int kK = 0, kV = kCodes, kKs = 2 * kCodes, kVs = 2 * kCodes + kScales;
-  static constexpr int kStage = 2 * (kCodes + kScales);
+  static constexpr int kBlock = 2 * (kCodes + kScales);
+  static constexpr int kStage = 2 * kBlock;
   // Key of row 2 t + 1 (the even rows' are t): chosen so that neither K's rows nor
   // V's pairs of keys meet in a bank.
   static constexpr int kFlip = D == 128 ? 1 : 2;
 };
 
-template <int WARPS>
+// What a warp knows of its stretch, out of its registers while it works: they are
+// what bounds the number of warps.
+template <int R>
+struct Stretch {
+  int64_t pos, begin, part;
+  int32_t b, h, cu, rows, first, base, whole, klo, khi;
+  int32_t lo[R], hi[R];  // keys that each row sees (of a tree: those before its own)
+};
+template <int WARPS, int R>
 struct PlanSmem {
   int64_t sum[WARPS];
   int64_t first_at[WARPS];
   int32_t first[WARPS];
+  Stretch<R> at[WARPS];
 };
 
 // Warps per CTA (one CTA per SM): as many as registers allow.
 template <int NT>
-constexpr int kWarps = NT == 1 ? 16 : 12;
+#ifndef MKW
+#define MKW 16
+#endif
+constexpr int kWarps = NT == 1 ? MKW : 12;
 
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_constant__ KvqParams P) {
@@ -181,7 +195,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
   const mk_kvq_attn_io& io = P.io;
   const mk_kvq_cache& c = io.kvq;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ PlanSmem<W> plan;
+  __shared__ PlanSmem<W, R> plan;
   const int lane = lane_id(), warp = threadIdx.x / 32, Hk = c.n_kv_heads;
   const int worker = warp * gridDim.x + blockIdx.x;
   pdl_launch_dependents();
@@ -224,104 +238,133 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
     }
   }
   __syncthreads();
-  int64_t pos = worker * share;
-  const int64_t end = min(total, pos + share);
-  if (lane == 0) P.split[worker].parts = 0;
-  if (pos >= end) return;
-  int b = plan.first[warp];
-  int64_t begin = plan.first_at[warp];
+  {
+    const int64_t pos = worker * share;
+    if (lane == 0) P.split[worker].parts = 0;
+    if (pos >= total) return;
+    if (lane == 0) {
+      plan.at[warp].pos = pos;
+      plan.at[warp].begin = plan.first_at[warp];
+      plan.at[warp].b = plan.first[warp];
+    }
+    __syncwarp();
+  }
+  volatile Stretch<R>& at = plan.at[warp];
 
   uint8_t* ring = smem + warp * (kStages * L::kStage);
   const uint32_t ring32 = smem_u32(ring);
+  // this lane's 16 bytes of each copy: of 16 keys' codes, and of their scales
+  constexpr int kScaleLanes = L::kScales / 16;
+  const uint8_t* k_lane = static_cast<const uint8_t*>(c.k_codes) + lane * 16;
+  const uint8_t* v_lane = static_cast<const uint8_t*>(c.v_codes) + lane * 16;
+  const uint8_t* s_lane = static_cast<const uint8_t*>(lane < kScaleLanes ? c.k_scales : c.v_scales) + (lane & (kScaleLanes - 1)) * 16;
   const int g = lane >> 2, t = lane & 3;
   const int key_even = g >> 1, key_g = g & 1 ? 4 + (key_even ^ L::kFlip) : key_even;  // of row g of K
   const int key_0 = t, key_1 = 4 + (t ^ L::kFlip);                                    // of V's pair
-  while (pos < end) {
-    const Req rq = read_req<R>(P, b);
-    const int64_t cost = rq.cost(Hk);
-    if (pos >= begin + cost) {
-      begin += cost;
-      ++b;
-      continue;
-    }
-    const int64_t off = pos - begin, item = off / rq.tiles;
-    const int h = static_cast<int>(item / rq.row_tiles), rt = static_cast<int>(item - static_cast<int64_t>(h) * rq.row_tiles);
-    const int ta = static_cast<int>(off - item * rq.tiles);
-    const int tb = static_cast<int>(min(static_cast<int64_t>(rq.tiles), ta + (end - pos)));
-    pos += tb - ta;
-    const int rows = rq.n * P.group;  // (checked by the host to be an int)
-
-    // Q of this thread's column of the second operand: row g of each 8
-    uint32_t qf[NT][KS][2];
-    float c_row[NT][2];            // factor on the scores of rows 2 t, 2 t + 1
-    int lo[NT][2], hi[NT][2];      // keys that they see (of a tree: before its own)
-    int klo = INT_MAX, khi = 0, full_lo = 0, full_hi = INT_MAX;
-    const float unit_k = pow2(c.k_exp ? clamp_exp(c.k_exp[h]) : 0);
+  while (true) {
+    uint32_t qf[NT][KS][2];    // Q of this thread's column of the second operand: row g of each 8
+    float c_row[NT][2];        // factor on the scores of rows 2 t, 2 t + 1
+    int full_lo = 0, full_hi = INT_MAX;  // keys that every row sees
+    int tile, tile_end, h;
+    const int32_t* table;
+    {
+      int64_t pos = at.pos, begin = at.begin;
+      const int64_t end = min(total, static_cast<int64_t>(worker + 1) * share);
+      if (pos >= end) return;
+      int b = at.b;
+      Req rq = read_req<R>(P, b);
+      for (int64_t cost; pos >= begin + (cost = rq.cost(Hk)); rq = read_req<R>(P, b)) {
+        begin += cost;
+        ++b;
+      }
+      const int64_t off = pos - begin, item = off / rq.tiles;
+      h = static_cast<int>(item / rq.row_tiles);
+      const int rt = static_cast<int>(item - static_cast<int64_t>(h) * rq.row_tiles);
+      const int ta = static_cast<int>(off - item * rq.tiles);
+      const int tb = static_cast<int>(min(static_cast<int64_t>(rq.tiles), ta + (end - pos)));
+      const int rows = rq.n * P.group;  // (checked by the host to be an int)
+      int klo = INT_MAX, khi = 0;
+      const float unit_k = pow2(c.k_exp ? clamp_exp(c.k_exp[h]) : 0);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int f = rt * R + nt * 8 + g;
-      const bool valid = f < rows;
-      const int i = quotient(valid ? f : 0, P.by_group), hq = h * P.group + (valid ? f - i * P.group : 0);
-      const int64_t row = rq.cu + i;
-      // dimensions 32 t .. (64: 16 t ..), 8 at a time: two words of pairs (x, x + 4)
-      float factor = 1.f;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(io.q) + row * io.q_stride + hq * D + t * (D / 4));
-      uint4 raw[D / 32];
+      for (int nt = 0; nt < NT; ++nt) {
+        const int f = rt * R + nt * 8 + g;
+        const bool valid = f < rows;
+        const int i = quotient(valid ? f : 0, P.by_group), hq = h * P.group + (valid ? f - i * P.group : 0);
+        const int64_t row = rq.cu + i;
+        // dimensions 32 t .. (64: 16 t ..), 8 at a time: two words of pairs (x, x + 4)
+        float factor = 1.f;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(io.q) + row * io.q_stride + hq * D + t * (D / 4));
+        uint4 raw[D / 32];
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) raw[j] = valid ? src[j] : make_uint4(0, 0, 0, 0);
-      if (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
-        // bf16 into fp16, relative to the row's largest value
-        uint32_t top = 0;
+        for (int j = 0; j < D / 32; ++j) raw[j] = valid ? src[j] : make_uint4(0, 0, 0, 0);
+        if (!std::is_same<T, __half>::value) {
+          // bf16 into fp16, relative to the row's largest value
+          uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j)
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[j].x & 0x7FFF7FFFu, raw[j].y & 0x7FFF7FFFu),
-                                       __vmaxu2(raw[j].z & 0x7FFF7FFFu, raw[j].w & 0x7FFF7FFFu)));
-        top = max(top & 0xFFFFu, top >> 16);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = min(max(static_cast<int>(top >> 7), 1), 253);  // biased; up to 2 * 2^e
-        factor = top < 0x7F80u ? __int_as_float(e << 23) : 1.f;
-        const float inv = top < 0x7F80u ? __int_as_float((254 - e) << 23) : 1.f;
+          for (int j = 0; j < D / 32; ++j)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[j].x & 0x7FFF7FFFu, raw[j].y & 0x7FFF7FFFu),
+                                         __vmaxu2(raw[j].z & 0x7FFF7FFFu, raw[j].w & 0x7FFF7FFFu)));
+          top = max(top & 0xFFFFu, top >> 16);
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = min(max(static_cast<int>(top >> 7), 1), 253);  // biased; up to 2 * 2^e
+          factor = top < 0x7F80u ? __int_as_float(e << 23) : 1.f;
+          const float inv = top < 0x7F80u ? __int_as_float((254 - e) << 23) : 1.f;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(&raw[j]);
+          for (int j = 0; j < D / 32; ++j) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&raw[j]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 x = Pack<T>::get(w[k]);
-            w[k] = half2_bits(x.x * inv, x.y * inv);
+            for (int k = 0; k < 4; ++k) {
+              const float2 x = Pack<T>::get(w[k]);
+              w[k] = half2_bits(x.x * inv, x.y * inv);
+            }
           }
         }
-      }
-      // words (0,1)(2,3)(4,5)(6,7) into (0,4)(1,5)(2,6)(3,7)
+        // words (0,1)(2,3)(4,5)(6,7) into (0,4)(1,5)(2,6)(3,7)
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        qf[nt][2 * j][0] = __byte_perm(raw[j].x, raw[j].z, 0x5410);
-        qf[nt][2 * j][1] = __byte_perm(raw[j].x, raw[j].z, 0x7632);
-        qf[nt][2 * j + 1][0] = __byte_perm(raw[j].y, raw[j].w, 0x5410);
-        qf[nt][2 * j + 1][1] = __byte_perm(raw[j].y, raw[j].w, 0x7632);
-      }
-      // the keys of row g, then those of rows 2 t and 2 t + 1
-      int my_lo = 0, my_hi = 0;
-      if (valid) {
-        const int p = rq.base + (io.tree_mask ? __popcll(io.tree_mask[row]) - 1 : i);
-        my_lo = io.window ? max(0, p - io.window + 1) : 0;
-        my_hi = io.tree_mask ? min(rq.len, rq.base) : min(rq.len, rq.base + i + 1);
-        klo = min(klo, my_lo);
-        khi = max(khi, io.tree_mask ? min(rq.len, rq.base + 64) : my_hi);
-        full_lo = max(full_lo, my_lo);
-        full_hi = min(full_hi, my_hi);
-      }
+        for (int j = 0; j < D / 32; ++j) {
+          qf[nt][2 * j][0] = __byte_perm(raw[j].x, raw[j].z, 0x5410);
+          qf[nt][2 * j][1] = __byte_perm(raw[j].x, raw[j].z, 0x7632);
+          qf[nt][2 * j + 1][0] = __byte_perm(raw[j].y, raw[j].w, 0x5410);
+          qf[nt][2 * j + 1][1] = __byte_perm(raw[j].y, raw[j].w, 0x7632);
+        }
+        int my_lo = 0, my_hi = 0;
+        if (valid) {
+          const int p = rq.base + (io.tree_mask ? __popcll(io.tree_mask[row]) - 1 : i);
+          my_lo = io.window ? max(0, p - io.window + 1) : 0;
+          my_hi = io.tree_mask ? min(rq.len, rq.base) : min(rq.len, rq.base + i + 1);
+          klo = min(klo, my_lo);
+          khi = max(khi, io.tree_mask ? min(rq.len, rq.base + 64) : my_hi);
+          full_lo = max(full_lo, my_lo);
+          full_hi = min(full_hi, my_hi);
+        }
+        if (t == 0) at.lo[nt * 8 + g] = my_lo, at.hi[nt * 8 + g] = my_hi;
+        // (not 0, which a masked score, -infinity, must not meet)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        c_row[nt][k] = P.scale_log2 * __shfl_sync(0xffffffffu, factor, 8 * t + 4 * k) * unit_k;
-        lo[nt][k] = __shfl_sync(0xffffffffu, my_lo, 8 * t + 4 * k);
-        hi[nt][k] = __shfl_sync(0xffffffffu, my_hi, 8 * t + 4 * k);
+        for (int k = 0; k < 2; ++k)
+          c_row[nt][k] = fmaxf(P.scale_log2 * __shfl_sync(0xffffffffu, factor, 8 * t + 4 * k) * unit_k, FLT_MIN);
       }
+      klo = __reduce_min_sync(0xffffffffu, klo);
+      khi = __reduce_max_sync(0xffffffffu, khi);
+      full_lo = __reduce_max_sync(0xffffffffu, full_lo);
+      full_hi = __reduce_min_sync(0xffffffffu, full_hi);
+      tile = max(rq.tile0 + ta, min(klo, khi) / kKeys);
+      tile_end = min(rq.tile0 + tb, (khi + kKeys - 1) / kKeys);
+      table = io.block_table + b * io.table_stride;
+      if (lane == 0) {
+        const bool whole = ta == 0 && tb == rq.tiles;
+        at.pos = pos + (tb - ta);
+        at.begin = begin;
+        at.b = b, at.h = h, at.cu = rq.cu, at.rows = rows, at.first = rt * R, at.base = rq.base;
+        at.whole = whole, at.klo = klo, at.khi = khi;
+        at.part = 2ll * worker + (ta == 0);
+        if (ta == 0 && !whole) {
+          const int64_t last = (pos + rq.tiles - 1) / share;  // the warp with the item's last tile
+          P.split[worker] = {static_cast<int32_t>(last - worker + 1), rq.cu, rows, rt * R, h};
+        }
+      }
+      __syncwarp();
     }
-    klo = __reduce_min_sync(0xffffffffu, klo);
-    khi = __reduce_max_sync(0xffffffffu, khi);
-    full_lo = __reduce_max_sync(0xffffffffu, full_lo);
-    full_hi = __reduce_min_sync(0xffffffffu, full_hi);
 
     float o[NT][MT][4];
     float ref[NT][2], l[NT][2];
@@ -335,134 +378,134 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
         for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.f;
     }
 
-    const int s_a = max(rq.step0 + ta * kTileSteps, min(klo, khi) / kStep);
-    const int s_b = min(rq.step0 + tb * kTileSteps, (khi + kStep - 1) / kStep);
-    const int32_t* table = io.block_table + b * io.table_stride;
-    // pages of 32 steps from `pages_at` on, one per lane
-    int pages_at = s_a;
-    auto page_of = [&](int s) { return s < s_b ? table[s * kStep >> P.page_shift] : -1; };
-    int pages = s_a < s_b ? page_of(s_a + lane) : -1, pages_next = s_a + 32 < s_b ? page_of(s_a + 32 + lane) : -1;
-    const int64_t head_row = static_cast<int64_t>(h) << P.page_shift;
-    auto issue = [&](int s) {
-      if (s < s_b) {
-        if (s - pages_at >= 32) {
-          pages_at += 32;
+    // Pages of 32 blocks of 16 keys, one per lane, and those of the next 32.
+    const uint32_t head_bytes = static_cast<uint32_t>(h << P.page_shift) * (D / 2);
+    const int blocks_end = 2 * tile_end;
+    int block = 2 * tile, pages_at = block;
+    auto page_of = [&](int x) { return x < blocks_end && x * 16 < at.khi ? table[x * 16 >> P.page_shift] : -1; };
+    int pages = page_of(block + lane), pages_next = page_of(block + 32 + lane);
+    auto issue = [&](uint32_t to) {
+      if (block < blocks_end) {
+        if (block - pages_at == 32) {
+          pages_at = block;
           pages = pages_next;
-          pages_next = page_of(s + 32 + lane);
+          pages_next = page_of(block + 32 + lane);
         }
-        const int page = __shfl_sync(0xffffffffu, pages, s - pages_at);
-        const bool there = page >= 0 && page < c.n_pages;
-        const int64_t row = there ? ((static_cast<int64_t>(page) * Hk) << P.page_shift) + head_row + ((s * kStep) & (c.page_size - 1)) : 0;
-        const uint32_t at = ring32 + ((s - s_a) & (kStages - 1)) * L::kStage;
-        const uint8_t* k = static_cast<const uint8_t*>(c.k_codes) + row * (D / 2) + lane * 16;
-        const uint8_t* v = static_cast<const uint8_t*>(c.v_codes) + row * (D / 2) + lane * 16;
-        if (D == 128) {
-          const uint32_t turn = (lane >> 3 & 1) << 5;  // see the loads of V
-          cp_async16(at + L::kK + lane * 16, k, there);
-          cp_async16(at + L::kK + 512 + lane * 16, k + 512, there);
-          cp_async16(at + L::kV + ((lane * 16) ^ turn), v, there);
-          cp_async16(at + L::kV + 512 + ((lane * 16) ^ turn), v + 512, there);
-        } else {
-          cp_async16(at + L::kK + lane * 16, k, there);
-          cp_async16(at + L::kV + lane * 16, v, there);
-        }
-        constexpr int n = L::kScales / 16;
-        if (lane < 2 * n) {
-          const uint8_t* sc = static_cast<const uint8_t*>(lane < n ? c.k_scales : c.v_scales) + row * (D / 16) + (lane & (n - 1)) * 16;
-          cp_async16(at + L::kKs + lane * 16, sc, there);
+#pragma unroll
+        for (int half = 0; half < 2; ++half, ++block) {
+          const int page = __shfl_sync(0xffffffffu, pages, block - pages_at);
+          const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(c.n_pages);
+          // (a page's codes are less than 2^31 bytes)
+          const int64_t off = there ? static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(page)) * P.page_bytes +
+                                                           (head_bytes + ((block * 16) & (c.page_size - 1)) * (D / 2)))
+                                    : 0;
+          const uint32_t st = to + half * L::kBlock + lane * 16;
+          const uint8_t *k = k_lane + off, *v = v_lane + off;
+          cp_async16(st + L::kK, k, there);
+          if (D == 128) {
+            const uint32_t turned = st ^ ((lane >> 3 & 1) << 5);  // see the loads of V
+            cp_async16(st + L::kK + 512, k + 512, there);
+            cp_async16(turned + L::kV, v, there);
+            cp_async16(turned + L::kV + 512, v + 512, there);
+          } else {
+            cp_async16(st + L::kV, v, there);
+          }
+          if (lane < 2 * kScaleLanes) cp_async16(st + L::kKs, s_lane + (off >> 3), there);
         }
       }
       cp_async_commit();
     };
+    uint32_t stage = 0, stage_in = 0;  // offsets in the ring: of the tile at hand, of the next copy
+    auto next_stage = [](uint32_t x) { return x == (kStages - 1) * L::kStage ? 0u : x + L::kStage; };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(s_a + i);
+    for (int i = 0; i < kStages - 1; ++i) {
+      issue(ring32 + stage_in);
+      stage_in = next_stage(stage_in);
+    }
 #pragma unroll 1
-    for (int s = s_a; s < s_b; ++s) {
+    for (; tile < tile_end; ++tile) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
-      issue(s + kStages - 1);
-      const uint8_t* st = ring + ((s - s_a) & (kStages - 1)) * L::kStage;
-      float sc[NT][4];
+      issue(ring32 + stage_in);
+      stage_in = next_stage(stage_in);
+      const uint8_t* st = ring + stage;
+      stage = next_stage(stage);
+      float sc[2][NT][4];
+      // scores: of each block rows g and g + 8 are the keys key_g and key_g + 8
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[nt][k] = 0.f;
-      // scores: rows g and g + 8 are the keys key_g and key_g + 8
-      {
+      for (int blk = 0; blk < 2; ++blk) {
         constexpr int WORDS = D / 32;  // of 8 codes, of this thread's dimensions of a key
+        const uint8_t* sb = st + blk * L::kBlock;
         uint32_t w[2][WORDS];
         Scales f[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int key = key_g + 8 * k;
           if (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(st + L::kK + key * 64 + t * 16);
+            const uint4 x = *reinterpret_cast<const uint4*>(sb + L::kK + key * 64 + t * 16);
             w[k][0] = x.x, w[k][1] = x.y, w[k][2 % WORDS] = x.z, w[k][3 % WORDS] = x.w;
-            f[k] = make_scales(*reinterpret_cast<const uint16_t*>(st + L::kKs + key * 8 + t * 2));
+            f[k] = make_scales(*reinterpret_cast<const uint16_t*>(sb + L::kKs + key * 8 + t * 2));
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(st + L::kK + key * 32 + t * 8);
+            const uint2 x = *reinterpret_cast<const uint2*>(sb + L::kK + key * 32 + t * 8);
             w[k][0] = x.x, w[k][1] = x.y;
-            const uint32_t one = st[L::kKs + key * 4 + t];
+            const uint32_t one = sb[L::kKs + key * 4 + t];
             f[k] = make_scales(one | one << 8);
           }
         }
 #pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[blk][nt][k] = 0.f;
+#pragma unroll
         for (int j = 0; j < WORDS; ++j) {
           uint32_t a[2][4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            Scales x = f[k];
-            if (D == 128) {  // words 0, 1 are of the first group of 16, 2, 3 of the second
-              const uint32_t sel = j < 2 ? 0x1010u : 0x3232u;
-              x.lo = __byte_perm(x.lo, 0, sel);
-              x.hi = __byte_perm(x.hi, 0, sel);
-              x.lo_off = __byte_perm(x.lo_off, 0, sel);
-              x.hi_off = __byte_perm(x.hi_off, 0, sel);
-            }
-            const uint32_t up = w[k][j] >> 8;
-            a[k][0] = values<0>(w[k][j], x.lo, x.lo_off);
-            a[k][1] = values<1>(w[k][j], x.hi, x.hi_off);
-            a[k][2] = values<0>(up, x.lo, x.lo_off);
-            a[k][3] = values<1>(up, x.hi, x.hi_off);
-          }
+          for (int k = 0; k < 2; ++k)  // (d 128: words 0, 1 are of the first group of 16, 2, 3 of the second)
+            values(w[k][j], D == 64 || j < 2 ? f[k].first() : f[k].second(), a[k]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma16816(sc[nt], a[0][0], a[1][0], a[0][1], a[1][1], qf[nt][2 * j][0], qf[nt][2 * j][1]);
-            mma16816(sc[nt], a[0][2], a[1][2], a[0][3], a[1][3], qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+            mma16816(sc[blk][nt], a[0][0], a[1][0], a[0][1], a[1][1], qf[nt][2 * j][0], qf[nt][2 * j][1]);
+            mma16816(sc[blk][nt], a[0][2], a[1][2], a[0][3], a[1][3], qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
           }
         }
       }
-      const int j0 = s * kStep;
-      const bool edge = j0 < full_lo || j0 + kStep > full_hi;
-      bool over = false;
+      const bool edge = tile * kKeys < full_lo || tile * kKeys + kKeys > full_hi;
+      if (edge) {
+#pragma unroll 1
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[nt][k] *= c_row[nt][k & 1];
-        if (edge) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int j = j0 + key_g + (k & 2) * 4;
-            bool see = j >= lo[nt][k & 1] && j < hi[nt][k & 1];
-            if (io.tree_mask && j >= rq.base && j < khi) {
-              const int fr = rt * R + nt * 8 + 2 * t + (k & 1);
-              see = fr < rows && (io.tree_mask[rq.cu + quotient(fr, P.by_group)] >> (j - rq.base) & 1);
+          for (int x = 0; x < 8; ++x) {
+            const int k = x & 3, j = tile * kKeys + (x >> 2) * 16 + key_g + (k & 2) * 4, r = nt * 8 + 2 * t + (k & 1);
+            bool see = j >= at.lo[r] && j < at.hi[r];
+            if (io.tree_mask && j >= at.base && j < at.khi) {
+              const int fr = at.first + r;
+              see = fr < at.rows && (io.tree_mask[at.cu + quotient(fr, P.by_group)] >> (j - at.base) & 1);
             }
-            if (!see) sc[nt][k] = -INFINITY;
+#pragma unroll
+            for (int m = 0; m < NT; ++m)
+              if (m == nt && !see) sc[x >> 2][m][k] = -INFINITY;
           }
-        }
-        over |= fmaxf(sc[nt][0], sc[nt][2]) - ref[nt][0] > kRefMost || fmaxf(sc[nt][1], sc[nt][3]) - ref[nt][1] > kRefMost;
       }
+      bool over = false;
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          top[nt][k] = fmaxf(fmaxf(sc[0][nt][k], sc[0][nt][k + 2]), fmaxf(sc[1][nt][k], sc[1][nt][k + 2]));
+          over |= fmaf(top[nt][k], c_row[nt][k], -ref[nt][k]) > kRefMost;
+        }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float top = fmaxf(sc[nt][k], sc[nt][k + 2]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float next = top - ref[nt][k] > kRefMost ? top - kRefBelow : ref[nt][k];
+            float x = top[nt][k];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            x *= c_row[nt][k];
+            const float next = x - ref[nt][k] > kRefMost ? x - kRefBelow : ref[nt][k];
             const float old = exp2_approx(ref[nt][k] - next);
             ref[nt][k] = next;
             l[nt][k] *= old;
@@ -473,77 +516,73 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
             }
           }
       }
-      uint32_t pf[NT][2];
+      uint32_t pf[2][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
+      for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = exp2_approx(sc[nt][k] - ref[nt][k & 1]);
-        l[nt][0] += p[0] + p[2];
-        l[nt][1] += p[1] + p[3];
-        pf[nt][0] = transposed8x8(half2_bits(p[0], p[1]));
-        pf[nt][1] = transposed8x8(half2_bits(p[2], p[3]));
-      }
-      // values: of 16 keys the pairs (key_0, key_1) and 8 further on
-      {
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) p[k] = exp2_approx(fmaf(sc[blk][nt][k], c_row[nt][k & 1], -ref[nt][k & 1]));
+          l[nt][0] += p[0] + p[2];
+          l[nt][1] += p[1] + p[3];
+          pf[blk][nt][0] = transposed8x8(half2_bits(p[0], p[1]));
+          pf[blk][nt][1] = transposed8x8(half2_bits(p[2], p[3]));
+        }
+      // values: of each block the pairs of keys (key_0, key_1) and 8 further on
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
         constexpr int WORDS = D / 64;  // of this thread's dimensions of a key
+        const uint8_t* sb = st + blk * L::kBlock;
         uint32_t w[4][WORDS];
         Scales f[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int ka = key_0 + 8 * k, kb = key_1 + 8 * k;
-          uint32_t sa, sb;
+          uint32_t sa, sb8;
           if (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(st + L::kV + ((ka * 64 + g * 8) ^ ((ka >> 1 & 1) << 5)));
-            const uint2 y = *reinterpret_cast<const uint2*>(st + L::kV + ((kb * 64 + g * 8) ^ ((kb >> 1 & 1) << 5)));
+            const uint2 x = *reinterpret_cast<const uint2*>(sb + L::kV + ((ka * 64 + g * 8) ^ ((ka >> 1 & 1) << 5)));
+            const uint2 y = *reinterpret_cast<const uint2*>(sb + L::kV + ((kb * 64 + g * 8) ^ ((kb >> 1 & 1) << 5)));
             w[2 * k][0] = x.x, w[2 * k][1 % WORDS] = x.y;
             w[2 * k + 1][0] = y.x, w[2 * k + 1][1 % WORDS] = y.y;
-            sa = st[L::kVs + ka * 8 + g], sb = st[L::kVs + kb * 8 + g];
+            sa = sb[L::kVs + ka * 8 + g], sb8 = sb[L::kVs + kb * 8 + g];
           } else {
-            w[2 * k][0] = *reinterpret_cast<const uint32_t*>(st + L::kV + ka * 32 + g * 4);
-            w[2 * k + 1][0] = *reinterpret_cast<const uint32_t*>(st + L::kV + kb * 32 + g * 4);
-            sa = st[L::kVs + ka * 4 + g / 2], sb = st[L::kVs + kb * 4 + g / 2];
+            w[2 * k][0] = *reinterpret_cast<const uint32_t*>(sb + L::kV + ka * 32 + g * 4);
+            w[2 * k + 1][0] = *reinterpret_cast<const uint32_t*>(sb + L::kV + kb * 32 + g * 4);
+            sa = sb[L::kVs + ka * 4 + g / 2], sb8 = sb[L::kVs + kb * 4 + g / 2];
           }
           if (edge) {  // keys that no row sees may hold anything
-            if (j0 + ka < klo || j0 + ka >= khi) sa = 0;
-            if (j0 + kb < klo || j0 + kb >= khi) sb = 0;
+            const int j0 = tile * kKeys + blk * 16, lo = at.klo, hi = at.khi;
+            if (j0 + ka < lo || j0 + ka >= hi) sa = 0;
+            if (j0 + kb < lo || j0 + kb >= hi) sb8 = 0;
           }
-          f[k] = make_scales(sa | sb << 8);
+          f[k] = make_scales(sa | sb8 << 8);
         }
 #pragma unroll
-        for (int j = 0; j < WORDS; ++j) {
+        for (int j = 0; j < WORDS; ++j)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {  // dimensions 8 j + 4 half ..
             uint32_t a[2][4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t x = __byte_perm(w[2 * k][j], w[2 * k + 1][j], half ? 0x7632 : 0x5410), up = x >> 8;
-              a[k][0] = values<0>(x, f[k].lo, f[k].lo_off);
-              a[k][1] = values<1>(x, f[k].hi, f[k].hi_off);
-              a[k][2] = values<0>(up, f[k].lo, f[k].lo_off);
-              a[k][3] = values<1>(up, f[k].hi, f[k].hi_off);
-            }
+            for (int k = 0; k < 2; ++k)
+              values(__byte_perm(w[2 * k][j], w[2 * k + 1][j], half ? 0x7632 : 0x5410), f[k], a[k]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma16816(o[nt][4 * j + 2 * half], a[0][0], a[0][1], a[1][0], a[1][1], pf[nt][0], pf[nt][1]);
-              mma16816(o[nt][4 * j + 2 * half + 1], a[0][2], a[0][3], a[1][2], a[1][3], pf[nt][0], pf[nt][1]);
+              mma16816(o[nt][4 * j + 2 * half], a[0][0], a[0][1], a[1][0], a[1][1], pf[blk][nt][0], pf[blk][nt][1]);
+              mma16816(o[nt][4 * j + 2 * half + 1], a[0][2], a[0][3], a[1][2], a[1][3], pf[blk][nt][0], pf[blk][nt][1]);
             }
           }
-        }
       }
     }
     cp_async_wait<0>();
     __syncwarp();
 
     // this thread's: rows 2 t and 2 t + 1, dimensions D / 8 g .. (o[i][k]: 2 i, o[i][k + 2]: 2 i + 1)
-    const bool whole = ta == 0 && tb == rq.tiles;
+    h = at.h;
     const float unit_v = 8.f * pow2(c.v_exp ? clamp_exp(c.v_exp[h]) : 0);
-    if (lane == 0 && ta == 0 && !whole) {
-      // (the item starts at pos - (tb - ta) and its last tile lies in this worker's stretch or a later one)
-      const int64_t last = (pos - tb + rq.tiles - 1) / share;
-      P.split[worker] = {static_cast<int32_t>(last - worker + 1), rq.cu, rows, rt * R, h};
-    }
-    const int64_t part = 2ll * worker + (ta == 0);
+    const int64_t part = at.part;
+    const int rows = at.rows, first = at.first, cu = at.cu;
+    const bool whole = at.whole;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -552,7 +591,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
         sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int r = nt * 8 + 2 * t + k, fr = rt * R + r;
+        const int r = nt * 8 + 2 * t + k, fr = first + r;
         if (fr >= rows) continue;
         if (!whole) {
           float* to = P.o + (part * R + r) * D + g * (D / 8);
@@ -563,7 +602,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
           continue;
         }
         const int i = quotient(fr, P.by_group), hq = h * P.group + fr - i * P.group;
-        const int64_t row = rq.cu + i;
+        const int64_t row = cu + i;
         const float inv = sum != 0.f ? unit_v / sum : 0.f;
         uint32_t y[MT];
 #pragma unroll
@@ -574,6 +613,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
         if (g == 0 && io.lse)
           io.lse[row * io.n_q_heads + hq] = sum != 0.f ? (ref[nt][k] + log2f(sum)) * 0.6931471805599453f : -INFINITY;
       }
+    __syncwarp();
   }
 }
 
@@ -736,6 +776,8 @@ mk_status mk_kvq_attn(const mk_kvq_attn_io* io, void* workspace, int64_t workspa
   if (st != MK_OK) return st;
   const mk_kvq_cache& c = io->kvq;
   const int64_t d = c.head_dim, n = io->n_rows, slots = static_cast<int64_t>(c.n_pages) * c.page_size;
+  const int64_t page_bytes = static_cast<int64_t>(c.n_kv_heads) * c.page_size * (d / 2);
+  if (page_bytes > INT32_MAX) return MK_ERR_UNSUPPORTED;
   if (io->max_pages < 0 || io->table_stride < io->max_pages || io->window < 0) return MK_ERR_INVALID_ARG;
   if (static_cast<int64_t>(io->max_pages) * c.page_size > INT32_MAX - 256) return MK_ERR_INVALID_ARG;
   if (!(io->scale >= 0.f && io->scale <= FLT_MAX / 2)) return MK_ERR_INVALID_ARG;
@@ -785,6 +827,7 @@ mk_status mk_kvq_attn(const mk_kvq_attn_io* io, void* workspace, int64_t workspa
   P.group = io->n_q_heads / c.n_kv_heads;
   P.by_group = make_divisor(P.group);
   P.page_shift = __builtin_ctz(static_cast<uint32_t>(c.page_size));
+  P.page_bytes = static_cast<uint32_t>(page_bytes);
   if (io->dtype == MK_BF16)
     return d == 128 ? launch<__nv_bfloat16, 128>(P, tile, device, sms, s) : launch<__nv_bfloat16, 64>(P, tile, device, sms, s);
   return d == 128 ? launch<__half, 128>(P, tile, device, sms, s) : launch<__half, 64>(P, tile, device, sms, s);

@@ -97,38 +97,33 @@ MK_DEV Turn make_turn(const AppendParams& P, const void* weights, const float2* 
   return t;
 }
 
-// The 8 values z of lane l (of two that hold a group) in 64 bits.
+// Value i = lane % 16 of a group in 64 bits (z, and the codes' unit); the lanes of a
+// warp share out the sum of squares.  x, w: the head's values and weights (or null).
 template <class T, int LAYOUT>
-__device__ __noinline__ void exact_values(const AppendParams& P, const T* x, const T* w, int32_t pos, int l,
-                                          int e, double* z) {
+MK_DEV double exact_value(const AppendParams& P, const T* x, const T* w, int32_t pos, int group, int e) {
   double r = 1.0;
   if (w) {
     double sum = 0.0;
-    for (int i = 0; i < P.d; ++i) {
+    for (int i = lane_id(); i < P.d; i += 32) {
       const double v = static_cast<float>(x[i]);
       sum += v * v;
     }
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     r = 1.0 / sqrt(sum / P.d + static_cast<double>(P.io.eps));
   }
   const double unit = r * static_cast<double>(pow2(-e));
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    const int at = l * 8 + i;
-    const double own = static_cast<double>(static_cast<float>(x[at])) * (w ? static_cast<double>(static_cast<float>(w[at])) : 1.0);
-    if (at >= P.rot) {
-      z[i] = own * unit;
-      continue;
-    }
-    const bool half = LAYOUT == MK_ROPE_HALF;
-    const bool second = half ? at >= P.rot / 2 : at & 1;
-    const int to = half ? (second ? at - P.rot / 2 : at + P.rot / 2) : at ^ 1;
-    const int pair = half ? min(at, to) : at / 2;
-    const double other = static_cast<double>(static_cast<float>(x[to])) * (w ? static_cast<double>(static_cast<float>(w[to])) : 1.0);
-    const int64_t phase = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[pair]);
-    double s, c;
-    sincospi(static_cast<double>(phase) * 0x1p-63, &s, &c);
-    z[i] = (own * c + (second ? other : -other) * s) * P.m64 * unit;
-  }
+  const int at = group * 16 + (lane_id() & 15);
+  const double own = static_cast<double>(static_cast<float>(x[at])) * (w ? static_cast<double>(static_cast<float>(w[at])) : 1.0);
+  if (at >= P.rot) return own * unit;
+  const bool half = LAYOUT == MK_ROPE_HALF;
+  const bool second = half ? at >= P.rot / 2 : at & 1;
+  const int to = half ? (second ? at - P.rot / 2 : at + P.rot / 2) : at ^ 1;
+  const int pair = half ? min(at, to) : at / 2;
+  const double other = static_cast<double>(static_cast<float>(x[to])) * (w ? static_cast<double>(static_cast<float>(w[to])) : 1.0);
+  const int64_t phase = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[pair]);
+  double s, c;
+  sincospi(static_cast<double>(phase) * 0x1p-63, &s, &c);
+  return (own * c + (second ? other : -other) * s) * P.m64 * unit;
 }
 
 // A double to the E4M3 scale nearest to a seventh of it: through a float that is
@@ -140,11 +135,27 @@ MK_DEV uint32_t exact_scale(double top) {
   return floats_to_e4m3x2(f, 0.f) & 0xFFu;
 }
 
-// Codes of 8 values (value i in bits 4i ..) and the scale of their group; the
-// lane's neighbour has the group's other 8.
-template <class T, int LAYOUT, bool MADE>
-MK_DEV uint2 quantise(const AppendParams& P, float (&z)[8], float off, const T* x, const T* w, int32_t pos, int l,
-                      int e) {
+// One group's codes (value i in bits 4 i of 64) and scale, in 64 bits, by a whole warp.
+template <class T, int LAYOUT>
+__device__ __noinline__ uint3 exact_group(const AppendParams& P, const T* x, const T* w, int32_t pos, int group, int e) {
+  const double z = exact_value<T, LAYOUT>(P, x, w, pos, group, e);
+  double top = fabs(z);
+  for (int o = 8; o; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const uint32_t scale = exact_scale(top);
+  const double u = e4m3_to_float(scale);
+  const double n = u > 0.0 ? rint(z / u) : 0.0;
+  const uint32_t code = static_cast<uint32_t>(static_cast<int>(fmin(fmax(n, -8.0), 7.0)) + 8);
+  const int i = lane_id() & 15;
+  const uint32_t lo = __reduce_or_sync(0xffffffffu, i < 8 ? code << (4 * i) : 0u);
+  const uint32_t hi = __reduce_or_sync(0xffffffffu, i >= 8 ? code << (4 * i - 32) : 0u);
+  return make_uint3(lo, hi, scale);
+}
+
+// Codes of 8 values (value i in bits 4 i) and the scale of their group; the lane's
+// neighbour has the group's other 8.  MADE: the values were computed, and are off by
+// `off` at most; near: this could tell.
+template <bool MADE>
+MK_DEV uint2 quantise(const float (&z)[8], float off, bool* near_border) {
   float top = 0.f;
   bool nan = false;
 #pragma unroll
@@ -157,8 +168,8 @@ MK_DEV uint2 quantise(const AppendParams& P, float (&z)[8], float off, const T* 
   nan |= other != other;
   top = fmaxf(top, other);
   const float seventh = __fdiv_rn(top, 7.f);
-  uint32_t scale = floats_to_e4m3x2(seventh, 0.f) & 0xFFu;
-  const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_half2(scale) & 0xFFFFu)));
+  const uint32_t scale = floats_to_e4m3x2(seventh, 0.f) & 0xFFu;
+  const float s = e4m3_to_float(scale);
   uint32_t word = 0;
   bool near = false;
   if (MADE) {
@@ -166,31 +177,21 @@ MK_DEV uint2 quantise(const AppendParams& P, float (&z)[8], float off, const T* 
     const uint32_t both = floats_to_e4m3x2(seventh - off, seventh + off);
     near = (both & 0xFFu) != (both >> 8);
   }
-  const float room = MADE && s > 0.f ? 0.5f - __fdividef(off, s) - 0x1p-20f : 0.f;
+  // Given values are divided, as ties between codes are frequent among them; computed
+  // ones near a tie are worked out again anyway (a product with 1 / s is off by 2^-22
+  // of up to 8).
+  const float inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
+  const float room = 0.5f - off * inv - 0x1p-19f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = s > 0.f ? __fdiv_rn(z[i], s) : 0.f;
+    const float t = MADE ? z[i] * inv : s > 0.f ? __fdiv_rn(z[i], s) : 0.f;
     const float n = rintf(t);
-    if (MADE) near |= s > 0.f && !(fabsf(t - n) <= room) && fabsf(t) < 9.f;
+    if (MADE) near |= !(fabsf(t - n) <= room) && fabsf(t) < 9.f;
     word |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(n, -8.f), 7.f)) + 8) << (4 * i);
   }
   if (MADE) {
-    // (about one row of 40 has such a group)
     near = near && !nan;
-    near = __shfl_xor_sync(0xffffffffu, static_cast<int>(near), 1) || near;
-    if (near) {
-      double y[8], big = 0.0;
-      exact_values<T, LAYOUT>(P, x, w, pos, l, e, y);
-      for (int i = 0; i < 8; ++i) big = fmax(big, fabs(y[i]));
-      big = fmax(big, __shfl_xor_sync(3u << (lane_id() & 30), big, 1));
-      scale = exact_scale(big);
-      const double u = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_half2(scale) & 0xFFFFu)));
-      word = 0;
-      for (int i = 0; i < 8; ++i) {
-        const double n = u > 0.0 ? rint(y[i] / u) : 0.0;
-        word |= static_cast<uint32_t>(static_cast<int>(fmin(fmax(n, -8.0), 7.0)) + 8) << (4 * i);
-      }
-    }
+    *near_border = __shfl_xor_sync(0xffffffffu, static_cast<int>(near), 1) || near;
   }
   if (nan) return make_uint2(0x88888888u, 0x7Fu);
   return make_uint2(word, scale);
@@ -333,15 +334,26 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid
         off *= unit;
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] *= unit;
-        if (P.rot || io.k_norm)
-          code = quantise<T, LAYOUT, true>(P, z, off, src + h * d, static_cast<const T*>(io.k_norm), pos, l, e);
-        else
-          code = quantise<T, LAYOUT, false>(P, z, 0.f, nullptr, nullptr, 0, l, e);
+        bool near = false;
+        if (P.rot || io.k_norm) code = quantise<true>(z, off, &near);
+        else code = quantise<false>(z, 0.f, nullptr);
+        // groups near a border, one after the other (about one row of 40 has one)
+        uint32_t todo = __ballot_sync(0xffffffffu, near && mine && !(l & 1));
+        while (todo) {
+          const int from_lane = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int gh = __shfl_sync(0xffffffffu, h, from_lane), gl = __shfl_sync(0xffffffffu, l, from_lane);
+          const int ge = __shfl_sync(0xffffffffu, e, from_lane);
+          const uint3 x = exact_group<T, LAYOUT>(P, src + gh * d, static_cast<const T*>(io.k_norm), pos, gl / 2, ge);
+          const int mine_too = static_cast<int>(lane_id()) - from_lane;
+          if (mine_too == 0) code = make_uint2(x.x, x.z);
+          if (mine_too == 1) code = make_uint2(x.y, x.z);
+        }
       } else {
         unpack8<T>(raw, z);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] *= unit;
-        code = quantise<T, LAYOUT, false>(P, z, 0.f, nullptr, nullptr, 0, l, e);
+        code = quantise<false>(z, 0.f, nullptr);
       }
       if (!mine) continue;
       const int64_t to = kvq_row(io.kvq, P.page_shift, slot, h);
