@@ -40,6 +40,7 @@ struct LinearParams {
   int32_t stages;
   int32_t tmem_cols;   // allocated; two tiles' where a CTA has several
   uint32_t idesc;
+  int32_t vec;         // out and residual take four values at a time
 };
 
 struct LinearBars {
@@ -77,12 +78,69 @@ MK_DEV bool wait_bar(const LinearParams& P, LinearBars& B, uint64_t* bar, uint32
 MK_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
-MK_DEV float load_cluster(uint32_t addr, uint32_t rank) {
+MK_DEV float4 load_cluster(uint32_t addr, uint32_t rank) {
   uint32_t a;
-  float v;
+  float4 v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
+}
+
+// Of a split tile: adds up the ranks' sums of rows c0 .. c1-1 (four outputs per
+// lane, a row per warp at a time, kRows rows on their way) and writes the results.
+template <class T, bool VEC>
+MK_DEV void join_sums(const LinearParams& P, uint32_t sums, int feat0, int row0, int c0, int c1) {
+  constexpr int kRows = 4, kWarps = kThreads / 32;
+  const mk_linear_io& io = P.io;
+  const int warp = threadIdx.x / 32, feat = feat0 + static_cast<int>(lane_id()) * 4;
+  const int mine = min(4, io.n_out - feat);  // outputs of this lane
+  float bias[4] = {};
+  if (io.bias)
+    for (int j = 0; j < mine; ++j) bias[j] = static_cast<float>(static_cast<const T*>(io.bias)[feat + j]);
+  for (int col = c0 + warp; col < c1; col += kRows * kWarps) {
+    float4 y[kRows];
+    float r[kRows][4];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int at = col + i * kWarps;
+      const T* res = static_cast<const T*>(io.residual) + static_cast<int64_t>(row0 + at) * io.residual_stride + feat;
+      const bool there = io.residual && at < c1;
+      if (VEC) {
+        uint2 w = make_uint2(0, 0);
+        if (there && mine == 4) w = *reinterpret_cast<const uint2*>(res);
+        const float2 a = Pack<T>::get(w.x), b = Pack<T>::get(w.y);
+        r[i][0] = a.x, r[i][1] = a.y, r[i][2] = b.x, r[i][3] = b.y;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[i][j] = there && j < mine ? static_cast<float>(res[j]) : 0.f;
+      }
+      y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int k = 0; k < P.split; ++k)
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float4 v = load_cluster(sums + min(col + i * kWarps, c1 - 1) * (kFeat * 4) + lane_id() * 16, k);
+        y[i].x += v.x, y[i].y += v.y, y[i].z += v.z, y[i].w += v.w;
+      }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int at = col + i * kWarps;
+      if (at >= c1) continue;
+      T* out = static_cast<T*>(io.out) + static_cast<int64_t>(row0 + at) * io.out_stride + feat;
+      const float z[4] = {activated(y[i].x + bias[0], io.act) + r[i][0], activated(y[i].y + bias[1], io.act) + r[i][1],
+                          activated(y[i].z + bias[2], io.act) + r[i][2], activated(y[i].w + bias[3], io.act) + r[i][3]};
+      if (VEC) {
+        if (mine == 4) *reinterpret_cast<uint2*>(out) = make_uint2(Pack<T>::put(z[0], z[1]), Pack<T>::put(z[2], z[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < mine) out[j] = static_cast<T>(z[j]);
+      }
+    }
+  }
 }
 
 template <class T>
@@ -227,29 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_sync();
     // (a CTA of a cluster has one tile)
-    if (warp >= 2 && !*const_cast<volatile uint32_t*>(&B.abort)) {
-      const int quad = warp & 3, tile = first;
-      const int feat = tile / P.row_tiles * kFeat + quad * 32 + lane;
-      const int row0 = tile % P.row_tiles * P.cols, rows = min(P.cols, io.n_rows - row0);
+    if (!*const_cast<volatile uint32_t*>(&B.abort)) {
+      const int feat0 = first / P.row_tiles * kFeat;
+      const int row0 = first % P.row_tiles * P.cols, rows = min(P.cols, io.n_rows - row0);
       const int c0 = rows * rank / P.split, c1 = rows * (rank + 1) / P.split;
-      const bool mine = feat < io.n_out;
-      const float bias = io.bias && mine ? static_cast<float>(static_cast<const T*>(io.bias)[feat]) : 0.f;
-      const uint32_t at = smem_u32(smem) + (quad * 32 + lane) * 4;
-      for (int col = c0; col < c1; col += 4) {
-        float y[4], r[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[i] = 0.f;
-          r[i] = io.residual && mine && col + i < c1 ? static_cast<float>(static_cast<const T*>(io.residual)[static_cast<int64_t>(row0 + col + i) * io.residual_stride + feat]) : 0.f;
-        }
-        for (int k = 0; k < P.split; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] += load_cluster(at + min(col + i, c1 - 1) * (kFeat * 4), k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (mine && col + i < c1)
-            static_cast<T*>(io.out)[static_cast<int64_t>(row0 + col + i) * io.out_stride + feat] = static_cast<T>(activated(y[i] + bias, io.act) + r[i]);
-      }
+      if (P.vec) join_sums<T, true>(P, smem_u32(smem), feat0, row0, c0, c1);
+      else join_sums<T, false>(P, smem_u32(smem), feat0, row0, c0, c1);
     }
     __syncwarp();
     cluster_sync();  // no CTA leaves while another one reads its sums
@@ -387,6 +428,8 @@ mk_status mk_linear(const mk_linear_io* io, void* workspace, int64_t workspace_b
   choose(&P, sms);
   // M 128, N the tile's columns; fp16 is type 0, bf16 type 1
   P.idesc = io->dtype == MK_BF16 ? idesc_bf16(kFeat, P.cols) : idesc_bf16(kFeat, P.cols) & ~((1u << 7) | (1u << 10));
+  P.vec = n % 4 == 0 && io->out_stride % 4 == 0 && !misaligned(io->out, 8) &&
+          (!io->residual || (io->residual_stride % 4 == 0 && !misaligned(io->residual, 8)));
   CUtensorMap w, x;
   st = encode_tmap(&w, io->dtype, io->w, k, n, io->w_stride, kFeat);
   if (st != MK_OK) return st;
