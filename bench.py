@@ -130,7 +130,7 @@ def _code_only(text):
 
 # sources of the batched operators, no part of the layer kernel
 BATCH_SOURCES = {"batch.h", "rope.h", "kvq.cuh", "slots.cu", "rope.cu", "prefix_attn.cu", "qkv_append.cu",
-                 "kvq_attn.cu", "linear.cu"}
+                 "kvq_attn.cu", "kvq_attn.cuh", "kvq_wide.cu", "attn_ptx.cuh", "linear.cu"}
 
 
 def layer_sources():

@@ -28,8 +28,7 @@
 #include <cmath>
 #include <type_traits>
 
-#include "kvq.cuh"
-#include "rope.h"
+#include "kvq_attn.cuh"
 
 namespace mk {
 
@@ -37,118 +36,6 @@ namespace {
 
 constexpr int kKeys = 32;   // of a key tile: a step of a warp, and the unit of the line
 constexpr int kStages = 3;  // key tiles of a warp's ring
-// Weights are 2^(score - r) in fp16: r is set so that a row's largest is 2^6 and
-// moves when one passes 2^15; those below 2^-25 of the type vanish, 2^-31 of the
-// largest at most.
-constexpr float kRefBelow = 6.f, kRefMost = 15.f;
-constexpr float kNoRef = -1e30f;
-
-// An item whose stretches lie in several warps, as the warp with the first says.
-struct Split {
-  int32_t parts;     // 0: none
-  int32_t cu, rows;  // first row of the request, its rows of this kv head
-  int32_t first;     // first of these in the tile
-  int32_t h;
-};
-
-struct KvqParams {
-  mk_kvq_attn_io io;
-  float scale_log2;  // scale * log2(e), times 8 (see Scales)
-  int32_t group;
-  int32_t page_shift;
-  uint32_t page_bytes;  // of codes
-  int32_t workers;
-  Divisor by_group;
-  uint32_t* status;
-  Split* split;      // [workers]
-  float2* stat;      // (r, l) of the rows of part 2 w (begins inside an item), 2 w + 1
-  float* o;          // [2 workers][rows][D]
-};
-
-MK_DEV int clampi(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : static_cast<int>(v); }
-
-// One request's lengths, made safe, and its place on the line.
-struct Req {
-  int32_t cu, n, len, base;
-  int32_t tile0, tiles;  // first key tile of its items and how many they have
-  int32_t row_tiles;
-  MK_DEV int64_t cost(int heads) const { return static_cast<int64_t>(tiles) * row_tiles * heads; }
-};
-template <int R>
-MK_DEV Req read_req(const KvqParams& P, int b) {
-  const mk_kvq_attn_io& io = P.io;
-  Req r;
-  r.cu = clampi(io.cu_rows[b], 0, io.n_rows);
-  r.n = clampi(io.cu_rows[b + 1], r.cu, io.n_rows) - r.cu;
-  r.len = clampi(io.lens[b], 0, io.max_pages << P.page_shift);
-  r.base = max(0, r.len - r.n);
-  const int low = io.window ? max(0, r.base - io.window + 1) : 0;
-  r.tile0 = low / kKeys;
-  // (at least one, so that rows without keys are written)
-  r.tiles = max(1, (r.len + kKeys - 1) / kKeys - r.tile0);
-  r.row_tiles = static_cast<int>((static_cast<int64_t>(r.n) * P.group + R - 1) / R);
-  return r;
-}
-
-MK_DEV void cp_async16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
-               : "memory");
-}
-MK_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-MK_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// D += A B, 16 x 8 by 16.
-MK_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-MK_DEV uint32_t transposed8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-MK_DEV float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-MK_DEV uint32_t half2_bits(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-MK_DEV __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
-MK_DEV uint32_t and_or(uint32_t a, uint32_t mask, uint32_t c) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(c));
-  return d;
-}
-
-// Factors for a pair of scales s: of codes in the low nibbles, 1024 + n, and the
-// high ones, 1024 + 16 n.  All in eighths, so that 1032 times the largest scale is
-// still an fp16; every factor and every result is exact.
-struct Scales {
-  __half2 lo, hi, lo_off, hi_off;
-  MK_DEV Scales first() const { return {__low2half2(lo), __low2half2(hi), __low2half2(lo_off), __low2half2(hi_off)}; }
-  MK_DEV Scales second() const { return {__high2half2(lo), __high2half2(hi), __high2half2(lo_off), __high2half2(hi_off)}; }
-};
-MK_DEV Scales make_scales(uint32_t pair) {  // two E4M3 bytes
-  const __half2 s = as_half2(e4m3x2_to_half2(pair));
-  return {__hmul2(s, as_half2(0x30003000u)), __hmul2(s, as_half2(0x20002000u)), __hmul2(s, as_half2(0xD808D808u)),
-          __hmul2(s, as_half2(0xC880C880u))};
-}
-// Eight codes, as four pairs (x, x + 4).
-MK_DEV void values(uint32_t word, const Scales& f, uint32_t (&y)[4]) {
-  const uint32_t up = word >> 8;
-  const __half2 v[4] = {__hfma2(as_half2(and_or(word, 0x000F000Fu, 0x64006400u)), f.lo, f.lo_off),
-                        __hfma2(as_half2(and_or(word, 0x00F000F0u, 0x64006400u)), f.hi, f.hi_off),
-                        __hfma2(as_half2(and_or(up, 0x000F000Fu, 0x64006400u)), f.lo, f.lo_off),
-                        __hfma2(as_half2(and_or(up, 0x00F000F0u, 0x64006400u)), f.hi, f.hi_off)};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const uint32_t*>(&v[i]);
-}
 
 // A stage of a warp's ring: two blocks of 16 keys, each K's codes, V's codes, K's
 // scales, V's scales (a page may hold no more than 16 keys).
@@ -179,12 +66,10 @@ struct PlanSmem {
   Stretch<R> at[WARPS];
 };
 
-// Warps per CTA (one CTA per SM): as many as registers allow.
+// Warps per CTA (one CTA per SM).  With 16 of 128 registers each and with 8 the same
+// work takes 5 to 7 % longer (64 requests, one token, up to 8192 keys: 91 and 91 us, 12: 85).
 template <int NT>
-#ifndef MKW
-#define MKW 16
-#endif
-constexpr int kWarps = NT == 1 ? MKW : 12;
+constexpr int kWarps = 12;
 
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_constant__ KvqParams P) {
@@ -206,7 +91,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
   const int per = (io.n_requests + TH - 1) / TH;
   const int b0 = min(io.n_requests, static_cast<int>(threadIdx.x) * per), b1 = min(io.n_requests, b0 + per);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += read_req<R>(P, b).cost(Hk);
+  for (int b = b0; b < b1; ++b) mine += read_req<R, kKeys>(P, b).cost(Hk);
   int64_t upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -229,7 +114,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
       int64_t begin = upto - mine;
       int b = b0;
       for (; b < b1 - 1; ++b) {
-        const int64_t cost = read_req<R>(P, b).cost(Hk);
+        const int64_t cost = read_req<R, kKeys>(P, b).cost(Hk);
         if (at < begin + cost) break;
         begin += cost;
       }
@@ -272,8 +157,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
       const int64_t end = min(total, static_cast<int64_t>(worker + 1) * share);
       if (pos >= end) return;
       int b = at.b;
-      Req rq = read_req<R>(P, b);
-      for (int64_t cost; pos >= begin + (cost = rq.cost(Hk)); rq = read_req<R>(P, b)) {
+      Req rq = read_req<R, kKeys>(P, b);
+      for (int64_t cost; pos >= begin + (cost = rq.cost(Hk)); rq = read_req<R, kKeys>(P, b)) {
         begin += cost;
         ++b;
       }
@@ -618,9 +503,10 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
 }
 
 // Joins the parts of a split item: part 2 w + 1 of the worker with the first and
-// parts 2 (w + 1), ... of those behind it.  A CTA takes R / gridDim.y of its rows;
-// its warps share out the parts.
-constexpr int kJoinWarps = 8;
+// parts 2 (w + 1), ... of those behind it.  A CTA takes R / gridDim.y of its rows: a
+// row per warp, or where there are many parts all warps one row after the other, the
+// parts shared out among them.
+constexpr int kJoinWarps = 8, kFewParts = 12;
 template <class T, int D, int R>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_kvq_join(const __grid_constant__ KvqParams P) {
   constexpr int V = D / 32;
@@ -631,13 +517,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kvq_join(const __grid_const
   pdl_wait();
   const Split sp = P.split[worker];
   if (sp.parts == 0) return;
-  const int rows = R / gridDim.y;
-  for (int r = blockIdx.y * rows; r < static_cast<int>(blockIdx.y + 1) * rows; ++r) {
-    const int fr = sp.first + r;
-    if (fr >= sp.rows) return;
-    float acc[V] = {}, top = kNoRef, all = 0.f;
+  const int rows = R / gridDim.y, r0 = blockIdx.y * rows;
+  // adds up parts from, from + step, ...
+  auto add = [&](int r, int from, int step, float& top, float& all, float (&acc)[V]) {
+    top = kNoRef, all = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
 #pragma unroll 4
-    for (int p = warp; p < sp.parts; p += kJoinWarps) {
+    for (int p = from; p < sp.parts; p += step) {
       const int64_t at = (p ? 2ll * (worker + p) : 2ll * worker + 1) * R + r;
       const float2 x = P.stat[at];
       const float* o = P.o + at * D + lane * V;
@@ -650,31 +537,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kvq_join(const __grid_const
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = acc[v] * old + y[v] * f;
     }
+  };
+  auto write = [&](int fr, float top, float all, const float (&acc)[V]) {
+    const float inv = all != 0.f ? 1.f / all : 0.f;
+    const int i = quotient(fr, P.by_group), hq = sp.h * P.group + fr - i * P.group;
+    const int64_t row = sp.cu + i;
+    uint32_t y[V / 2];
+#pragma unroll
+    for (int v = 0; v < V; v += 2) y[v / 2] = Pack<T>::put(acc[v] * inv, acc[v + 1] * inv);
+    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<T*>(io.out) + row * io.out_stride + hq * D + lane * V);
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) to[v] = y[v];
+    if (lane == 0 && io.lse)
+      io.lse[row * io.n_q_heads + hq] = all != 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY;
+  };
+  float acc[V], top, all;
+  if (sp.parts <= kFewParts) {
+    for (int r = r0 + warp; r < r0 + rows && sp.first + r < sp.rows; r += kJoinWarps) {
+      add(r, 0, 1, top, all, acc);
+      write(sp.first + r, top, all, acc);
+    }
+    return;
+  }
+  for (int r = r0; r < r0 + rows && sp.first + r < sp.rows; ++r) {
+    add(r, warp, kJoinWarps, top, all, acc);
 #pragma unroll
     for (int v = 0; v < V; ++v) sum_o[warp][lane * V + v] = acc[v];
     if (lane == 0) sum_l[warp] = make_float2(top, all);
     __syncthreads();
     if (warp == 0) {
-      const int n = min(kJoinWarps, sp.parts);
       float m = kNoRef, s = 0.f, out[V] = {};
-      for (int w = 0; w < n; ++w) m = fmaxf(m, sum_l[w].x);
-      for (int w = 0; w < n; ++w) {
+      for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sum_l[w].x);
+      for (int w = 0; w < kJoinWarps; ++w) {
         const float f = exp2f(sum_l[w].x - m);
         s += sum_l[w].y * f;
 #pragma unroll
         for (int v = 0; v < V; ++v) out[v] += sum_o[w][lane * V + v] * f;
       }
-      const float inv = s != 0.f ? 1.f / s : 0.f;
-      const int i = quotient(fr, P.by_group), hq = sp.h * P.group + fr - i * P.group;
-      const int64_t row = sp.cu + i;
-      uint32_t y[V / 2];
-#pragma unroll
-      for (int v = 0; v < V; v += 2) y[v / 2] = Pack<T>::put(out[v] * inv, out[v + 1] * inv);
-      uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<T*>(io.out) + row * io.out_stride + hq * D + lane * V);
-#pragma unroll
-      for (int v = 0; v < V / 2; ++v) to[v] = y[v];
-      if (lane == 0 && io.lse)
-        io.lse[row * io.n_q_heads + hq] = s != 0.f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
+      write(sp.first + r, m, s, out);
     }
     __syncthreads();
   }
@@ -694,22 +594,15 @@ int64_t lay_out(int workers, int rows, int d, uint8_t* base, KvqParams* P) {
   return align256(at + 2ll * workers * rows * d * 4);
 }
 
-// Rows per tile: 16 where 8 would be passed on average.
+// Rows per tile, by what the requests' rows of a kv head are on average.
 int rows_of_tile(const mk_kvq_attn_io* io) {
-  const int64_t group = io->n_q_heads / io->kvq.n_kv_heads;
-  return io->n_rows * group > 8ll * io->n_requests ? 16 : 8;
+  const int64_t group = io->n_q_heads / io->kvq.n_kv_heads, rows = io->n_rows * group;
+  return rows > 16ll * io->n_requests ? kWideRows : rows > 8ll * io->n_requests ? 16 : 8;
 }
-int workers_of(int rows, int sms) { return sms * (rows == 8 ? kWarps<1> : kWarps<2>); }
+int workers_of(int rows, int sms) { return rows == kWideRows ? sms : sms * (rows == 8 ? kWarps<1> : kWarps<2>); }
 
-template <class T, int D, int NT>
+template <class T, int D, int R>
 mk_status launch(const KvqParams& P, int device, int sms, cudaStream_t s) {
-  constexpr int R = 8 * NT, smem = kWarps<NT> * kStages * Layout<D>::kStage;
-  static std::atomic<uint64_t> ready{0};  // (once per device: it takes as long as a launch)
-  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
-  if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    MK_CUDA_TRY(cudaFuncSetAttribute(k_kvq_attn<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -717,13 +610,25 @@ mk_status launch(const KvqParams& P, int device, int sms, cudaStream_t s) {
   lc.attrs = attr;
   lc.numAttrs = 1;
   lc.stream = s;
-  lc.gridDim = dim3(sms);
-  lc.blockDim = dim3(kWarps<NT> * 32);
-  lc.dynamicSmemBytes = smem;
-  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_attn<T, D, NT>, P));
+  if (R == kWideRows) {
+    const mk_status st = launch_kvq_wide(P, device, sms, s);
+    if (st != MK_OK) return st;
+  } else {
+    constexpr int NT = R == 16 ? 2 : 1, smem = kWarps<NT> * kStages * Layout<D>::kStage;
+    static std::atomic<uint64_t> ready{0};  // (once per device: it takes as long as a launch)
+    const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+      MK_CUDA_TRY(cudaFuncSetAttribute(k_kvq_attn<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+      ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    lc.gridDim = dim3(sms);
+    lc.blockDim = dim3(kWarps<NT> * 32);
+    lc.dynamicSmemBytes = smem;
+    MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_attn<T, D, NT>, P));
+  }
   // few items, many parts each: rows on CTAs of their own
   const int64_t items = (static_cast<int64_t>(P.io.n_rows) * P.group / R + P.io.n_requests) * P.io.kvq.n_kv_heads;
-  lc.gridDim = dim3(P.workers, items * 16 < P.workers ? R : 1);
+  lc.gridDim = dim3(P.workers, items * 16 < P.workers ? R : R == kWideRows ? R / 8 : 1);
   lc.blockDim = dim3(kJoinWarps * 32);
   lc.dynamicSmemBytes = 0;
   MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_join<T, D, R>, P));
@@ -731,7 +636,9 @@ mk_status launch(const KvqParams& P, int device, int sms, cudaStream_t s) {
 }
 template <class T, int D>
 mk_status launch(const KvqParams& P, int rows, int device, int sms, cudaStream_t s) {
-  return rows == 8 ? launch<T, D, 1>(P, device, sms, s) : launch<T, D, 2>(P, device, sms, s);
+  return rows == 8    ? launch<T, D, 8>(P, device, sms, s)
+         : rows == 16 ? launch<T, D, 16>(P, device, sms, s)
+                      : launch<T, D, kWideRows>(P, device, sms, s);
 }
 
 mk_status check_shapes(const mk_kvq_attn_io* io) {

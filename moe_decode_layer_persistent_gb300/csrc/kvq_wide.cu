@@ -1,0 +1,612 @@
+// kvq_wide.cu -- attention over a paged cache in 4 bits for row tiles of up to 128
+// rows, on the 5th-generation tensor cores.
+//
+// The steps of kvq_attn.cu with the rows as operand A: S = Q K^T (128 rows by 128
+// keys), P = 2^(S - r) over S's place in tensor memory, O += P V.  With 16 rows the
+// conversions of the codes cost more than the products; here every key is converted
+// once for all of a tile's rows:
+//   8 warps  bring 16 keys of each tile into a ring of their own, turn their codes
+//            into fp16 and store them as operand B (K along the dimensions, V along
+//            the keys: both are rows of a key's dimensions in shared memory);
+//   4 warps  keep a row per thread: they bring Q, turn scores into weights, and write
+//            the results;
+//   1 warp   (of a fourth warpgroup) issues the products, the scores of the next tile before P V.
+// Two buffers of K, of V and of S keep the three busy at the same time.  Key tiles of
+// all items lie on one line, of which each CTA (one per SM) takes an equal stretch;
+// k_kvq_join joins what lies in several.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "kvq_attn.cuh"
+
+namespace mk {
+
+namespace {
+
+constexpr int kKeys = 128;       // of a key tile
+constexpr int kRows = kWideRows;
+constexpr int kConvert = 8;      // warps that convert: 16 keys of a tile each
+constexpr int kThreads = 512;    // four warpgroups: rows, two that convert, products
+constexpr int kStages = 3;       // tiles of a converting warp's ring
+constexpr float kMost = 32768.f; // a row's sum of weights over a tile
+constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
+constexpr uint32_t kTimeout = 1;
+
+template <int D>
+struct alignas(1024) WideSmem {
+  static constexpr int kTile = kKeys * D * 2;
+  static constexpr int kCodes = 16 * D / 2, kScales = 16 * D / 16, kStage = 2 * (kCodes + kScales);
+  uint8_t q[kTile], k[2][kTile], v[2][kTile];
+  uint8_t raw[kConvert][kStages][kStage];  // of each 16 keys: K's codes, V's, K's scales, V's
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], q_full, drained;
+  int64_t sum[kThreads / 32];
+  int64_t first_at;
+  int32_t first;
+  uint32_t tmem, abort;
+};
+
+// fp16 operands, f32 sums, M 128; b_along_n: operand B runs along N.
+__host__ __device__ constexpr uint32_t idesc_fp16(int N, bool b_along_n) {
+  return (1u << 4) | (b_along_n ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+
+// Bounded waits of whole warps: false once any wait of the CTA has run out.
+template <int D>
+MK_DEV bool wait_bar(const KvqParams& P, WideSmem<D>& S, uint64_t* bar, uint32_t parity) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer();
+    while (true) {
+#pragma unroll 1
+      for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+      if (ok || *const_cast<volatile uint32_t*>(&S.abort)) break;
+      if (globaltimer() - t0 > kWaitNs) {
+        *const_cast<volatile uint32_t*>(&S.abort) = 1;
+        atomicExch(P.status, kTimeout);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// A stretch of one item's key tiles, as every warp works it out.
+struct Item {
+  int32_t b, h, cu, n, base, len, rows, first;  // rows of the kv head, the tile's first
+  int32_t tile, tile_end;                       // key tiles to go through
+  int32_t klo, khi;                             // keys that some row sees
+  bool whole, starts;
+};
+struct Walk {
+  int64_t pos, end, begin, share;
+  int32_t b;
+  // The next stretch (for whole warps); false if there is none.
+  MK_DEV bool next(const KvqParams& P, Item& it) {
+    if (pos >= end) return false;
+    const mk_kvq_attn_io& io = P.io;
+    const int Hk = io.kvq.n_kv_heads;
+    Req rq = read_req<kRows, kKeys>(P, b);
+    for (int64_t cost; pos >= begin + (cost = rq.cost(Hk)); rq = read_req<kRows, kKeys>(P, b)) {
+      begin += cost;
+      ++b;
+    }
+    const int64_t off = pos - begin, item = off / rq.tiles;
+    it.h = static_cast<int>(item / rq.row_tiles);
+    const int rt = static_cast<int>(item - static_cast<int64_t>(it.h) * rq.row_tiles);
+    const int ta = static_cast<int>(off - item * rq.tiles);
+    const int tb = static_cast<int>(min(static_cast<int64_t>(rq.tiles), ta + (end - pos)));
+    it.b = b, it.cu = rq.cu, it.n = rq.n, it.base = rq.base, it.len = rq.len;
+    it.rows = rq.n * P.group;
+    it.first = rt * kRows;
+    it.starts = ta == 0;
+    it.whole = ta == 0 && tb == rq.tiles;
+    const int i0 = quotient(it.first, P.by_group), i1 = quotient(min(it.rows, it.first + kRows) - 1, P.by_group);
+    int depth = i0;
+    it.khi = min(rq.len, rq.base + i1 + 1);
+    if (io.tree_mask) {
+      // (a row sees its own key and no row the 65th; the lowest window is that of the
+      // row with the fewest bits)
+      it.khi = min(rq.len, rq.base + 64);
+      depth = 0;
+      if (io.window) {
+        int least = 63;
+        for (int i = i0 + static_cast<int>(lane_id()); i <= i1; i += 32) least = min(least, __popcll(io.tree_mask[rq.cu + i]) - 1);
+        depth = __reduce_min_sync(0xffffffffu, least);
+      }
+    }
+    it.klo = io.window ? max(0, rq.base + depth - io.window + 1) : 0;
+    it.tile = max(rq.tile0 + ta, min(it.klo, it.khi) / kKeys);
+    it.tile_end = min(rq.tile0 + tb, (it.khi + kKeys - 1) / kKeys);
+    pos += tb - ta;
+    return true;
+  }
+};
+
+// ---- converting warps
+template <int D>
+MK_DEV void convert(const KvqParams& P, WideSmem<D>& S, Walk walk, int w) {
+  using L = WideSmem<D>;
+  const mk_kvq_attn_io& io = P.io;
+  const mk_kvq_cache& c = io.kvq;
+  constexpr int kChunks = D / 32;           // of 32 codes (16 bytes) of a key
+  constexpr int kPer = 16 * kChunks / 32;   // of a lane
+  const int lane = lane_id(), key = lane & 15, row = w * 16 + key;
+  const uint32_t ring = smem_u32(S.raw[w]);
+  constexpr int kScaleLanes = L::kScales / 16;
+  // this lane's 16 bytes of each copy, and their place: the chunks of a key are turned
+  // so that eight keys' meet no bank twice when they are read
+  const int ck = lane / kChunks, cc = lane % kChunks;
+  const uint32_t place = ck * (D / 2) + ((cc ^ (D == 128 ? ck >> 1 & 3 : ck >> 2 & 1)) << 4);
+  const uint8_t* k_lane = static_cast<const uint8_t*>(c.k_codes) + lane * 16;
+  const uint8_t* v_lane = static_cast<const uint8_t*>(c.v_codes) + lane * 16;
+  const uint8_t* s_lane = static_cast<const uint8_t*>(lane < kScaleLanes ? c.k_scales : c.v_scales) + (lane & (kScaleLanes - 1)) * 16;
+  int done = 0;  // tiles of this CTA
+  Item it;
+  while (walk.next(P, it)) {
+    const int32_t* table = io.block_table + it.b * io.table_stride;
+    const uint32_t head_bytes = static_cast<uint32_t>(it.h << P.page_shift) * (D / 2);
+    // pages of this warp's keys of 32 tiles, one per lane, and those of the next 32
+    auto page_of = [&](int tile) {
+      const int j = tile * kKeys + w * 16;
+      return tile < it.tile_end && j < it.khi ? table[j >> P.page_shift] : -1;
+    };
+    int load = it.tile, pages_at = load;
+    int pages = page_of(load + lane), pages_next = page_of(load + 32 + lane);
+    auto issue = [&](int stage) {
+      if (load < it.tile_end) {
+        if (load - pages_at == 32) {
+          pages_at = load;
+          pages = pages_next;
+          pages_next = page_of(load + 32 + lane);
+        }
+        const int page = __shfl_sync(0xffffffffu, pages, load - pages_at);
+        const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(c.n_pages);
+        const int64_t off = there ? static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(page)) * P.page_bytes +
+                                                         (head_bytes + ((load * kKeys + w * 16) & (c.page_size - 1)) * (D / 2)))
+                                  : 0;
+        const uint32_t st = ring + stage * L::kStage;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          cp_async16(st + place + i * 512, k_lane + off + i * 512, there);
+          cp_async16(st + L::kCodes + place + i * 512, v_lane + off + i * 512, there);
+        }
+        if (lane < 2 * kScaleLanes) cp_async16(st + 2 * L::kCodes + lane * 16, s_lane + (off >> 3), there);
+        ++load;
+      }
+      cp_async_commit();
+    };
+    int stage = 0, stage_in = 0;
+    auto after = [](int x) { return x == kStages - 1 ? 0 : x + 1; };
+    for (int i = 0; i < kStages - 1; ++i, stage_in = after(stage_in)) issue(stage_in);
+    for (int tile = it.tile; tile < it.tile_end; ++tile, ++done, stage = after(stage)) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      issue(stage_in);
+      stage_in = after(stage_in);
+      const int buf = done & 1;
+      const uint8_t* st = S.raw[w][stage];
+      const int j = tile * kKeys + row;
+      const bool seen = j >= it.klo && j < it.khi;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint64_t* empty = kv ? &S.v_empty[buf] : &S.k_empty[buf];
+        if (done >= 2 && !wait_bar(P, S, empty, ((done >> 1) - 1) & 1)) {
+          cp_async_wait<0>();
+          return;
+        }
+        uint8_t* to = (kv ? S.v[buf] : S.k[buf]) + row * 128;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int chunk = (lane >> 4) + 2 * i;
+          const uint4 x = *reinterpret_cast<const uint4*>(st + kv * L::kCodes + key * (D / 2) + ((chunk ^ (D == 128 ? key >> 1 & 3 : key >> 2 & 1)) << 4));
+          uint32_t pair = *reinterpret_cast<const uint16_t*>(st + 2 * L::kCodes + kv * L::kScales + key * (D / 16) + chunk * 2);
+          // keys that no row sees may hold anything: a weight of 0 must meet a number
+          if (kv && !seen) pair = 0;
+          const Scales f = make_scales(pair);
+          const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            uint32_t y[4];
+            values(words[n], n < 2 ? f.first() : f.second(), y);
+            const int unit = chunk * 4 + n;  // of 8 dimensions; 8 of them to a panel
+            *reinterpret_cast<uint4*>(to + (unit >> 3) * (kKeys * 128) + (((unit & 7) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv ? &S.v_full[buf] : &S.k_full[buf]);
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+  }
+}
+
+// ---- the products' issuer
+template <int D>
+MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
+  constexpr uint32_t kIdS = idesc_fp16(kKeys, false), kIdO = idesc_fp16(D, true);
+  const uint32_t tmem = S.tmem, to = tmem + 256;
+  const uint64_t qd = sdesc_kmajor_sw128(smem_u32(S.q));
+  int done = 0, items = 0;
+  // O += P V of a tile
+  auto pv = [&](int at, bool first) {
+    const int buf = at & 1;
+    if (!wait_bar(P, S, &S.v_full[buf], (at >> 1) & 1) || !wait_bar(P, S, &S.p_full[buf], (at >> 1) & 1)) return false;
+    tc_fence_after();
+    if (elect_one()) {
+      const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(S.v[buf]), kKeys * 128);
+#pragma unroll
+      for (int k = 0; k < kKeys / 16; ++k)
+        mma_ts(to, tmem + buf * 128 + 8 * k, vd + k * (16 * 128 >> 4), kIdO, !first || k > 0);
+      mma_commit(&S.v_empty[buf]);
+    }
+    __syncwarp();
+    return true;
+  };
+  Item it;
+  while (walk.next(P, it)) {
+    const int n = it.tile_end - it.tile;
+    if (n <= 0) continue;
+    if (!wait_bar(P, S, &S.q_full, items++ & 1)) return false;
+    for (int t = 0; t < n; ++t, ++done) {
+      const int buf = done & 1;
+      if (!wait_bar(P, S, &S.k_full[buf], (done >> 1) & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t kd = sdesc_kmajor_sw128(smem_u32(S.k[buf]));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t at = (k >> 2) * (kKeys * 128 >> 4) + (k & 3) * 2;
+          mma_bf16(tmem + buf * 128, qd + at, kd + at, kIdS, k);
+        }
+        mma_commit(&S.s_full[buf]);
+        mma_commit(&S.k_empty[buf]);
+      }
+      __syncwarp();
+      if (t && !pv(done - 1, t == 1)) return false;
+    }
+    if (!pv(done - 1, n == 1)) return false;
+  }
+  return true;
+}
+
+// ---- a row per thread
+template <class T, int D>
+MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
+  const mk_kvq_attn_io& io = P.io;
+  const mk_kvq_cache& c = io.kvq;
+  const int lane = lane_id(), warp = threadIdx.x / 32, row = threadIdx.x;
+  const uint32_t lanes = S.tmem + (static_cast<uint32_t>(warp * 32) << 16), to = lanes + 256;
+  int done = 0;
+  Item it;
+  while (walk.next(P, it)) {
+    const int f = it.first + row;
+    const bool valid = f < it.rows;
+    const int i = quotient(valid ? f : 0, P.by_group), hq = it.h * P.group + (valid ? f - i * P.group : 0);
+    const int64_t at_row = it.cu + i;
+    // Q, in fp16 relative to the row's largest value, its pairs as the codes' are
+    float c_row = P.scale_log2 * pow2(c.k_exp ? clamp_exp(c.k_exp[it.h]) : 0);
+    const int n = it.tile_end - it.tile;
+    if (n > 0) {  // (no products of the item before are on their way: its last scores have come)
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(io.q) + at_row * io.q_stride + hq * D);
+      uint4 raw[D / 8];
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) raw[j] = valid ? src[j] : make_uint4(0, 0, 0, 0);
+      if (!std::is_same<T, __half>::value) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[j].x & 0x7FFF7FFFu, raw[j].y & 0x7FFF7FFFu),
+                                       __vmaxu2(raw[j].z & 0x7FFF7FFFu, raw[j].w & 0x7FFF7FFFu)));
+        top = max(top & 0xFFFFu, top >> 16);
+        const int e = min(max(static_cast<int>(top >> 7), 1), 253);
+        const float inv = top < 0x7F80u ? __int_as_float((254 - e) << 23) : 1.f;
+        c_row *= top < 0x7F80u ? __int_as_float(e << 23) : 1.f;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          uint32_t* x = reinterpret_cast<uint32_t*>(&raw[j]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 y = Pack<T>::get(x[k]);
+            x[k] = half2_bits(y.x * inv, y.y * inv);
+          }
+        }
+      }
+      c_row = fmaxf(c_row, FLT_MIN);  // (a masked score, -infinity, must not meet 0)
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j)
+        *reinterpret_cast<uint4*>(S.q + (j >> 3) * (kRows * 128) + row * 128 + (((j & 7) ^ (row & 7)) << 4)) =
+            make_uint4(__byte_perm(raw[j].x, raw[j].z, 0x5410), __byte_perm(raw[j].x, raw[j].z, 0x7632),
+                       __byte_perm(raw[j].y, raw[j].w, 0x5410), __byte_perm(raw[j].y, raw[j].w, 0x7632));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.q_full);
+    }
+
+    // the keys that the row sees: lo .. hi-1 and, of a tree, bits from base on
+    int lo = 0, hi = 0;
+    uint64_t tree = 0;
+    if (valid) {
+      if (io.tree_mask) tree = io.tree_mask[at_row];
+      const int p = it.base + (io.tree_mask ? __popcll(tree) - 1 : i);
+      lo = io.window ? max(0, p - io.window + 1) : 0;
+      hi = io.tree_mask ? min(it.len, it.base) : min(it.len, it.base + i + 1);
+    }
+    const bool warp_valid = __any_sync(0xffffffffu, valid);
+    float ref = kNoRef, l = 0.f;
+    for (int t = 0; t < n; ++t, ++done) {
+      const int buf = done & 1, k0 = (it.tile + t) * kKeys;
+      if (!wait_bar(P, S, &S.s_full[buf], (done >> 1) & 1)) return;
+      tc_fence_after();
+      if (warp_valid) {
+        const uint32_t ts = lanes + buf * 128;
+        const bool edge = __any_sync(0xffffffffu, valid && (k0 < lo || k0 + kKeys > hi));
+        auto scores = [&](int half, float (&s)[64]) {
+          tmem_ld32(ts + half * 64, s);
+          tmem_ld32(ts + half * 64 + 32, s + 32);
+          tmem_ld_wait();
+          if (!edge) return;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int at = k0 + half * 64 + q * 32;
+            uint32_t see = below(hi - at) & ~below(lo - at);
+            if (io.tree_mask) {
+              // bit x: key at + x, of which those from base on follow the row's word
+              const int off = it.base - at;
+              see |= (off >= 32 ? 0u : off >= 0 ? static_cast<uint32_t>(tree) << off : off > -64 ? static_cast<uint32_t>(tree >> -off) : 0u) & below(it.khi - at);
+            }
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!(see >> x & 1)) s[32 * q + x] = -INFINITY;
+          }
+        };
+        uint32_t p[64];
+        float total;
+        bool look = __any_sync(0xffffffffu, valid && ref == kNoRef);
+#pragma unroll 1
+        while (true) {
+          if (look) {
+            // the row's largest score: the reference moves if it is far above it
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              float s[64];
+              scores(half, s);
+#pragma unroll
+              for (int x = 0; x < 64; x += 2) top = max3(top, s[x], s[x + 1]);
+            }
+            top *= c_row;
+            const float next = valid && top - ref > kRefBelow ? top - kRefBelow : ref;
+            const float old = exp2_approx(ref - next);
+            l *= old;
+            ref = next;
+            if (t && __any_sync(0xffffffffu, old != 1.f)) {
+              // (the tile before is in O when its V is free)
+              if (!wait_bar(P, S, &S.v_empty[(done - 1) & 1], ((done - 1) >> 1) & 1)) return;
+              tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                float o[32];
+                tmem_ld32(to + 32 * q, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int y = 0; y < 32; ++y) o[y] *= old;
+                tmem_st32(to + 32 * q, reinterpret_cast<uint32_t*>(o));
+              }
+              tmem_st_wait();
+            }
+          }
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float s[64];
+            scores(half, s);
+#pragma unroll
+            for (int x = 0; x < 64; x += 2) {
+              float2 y = fma2(make_float2(s[x], s[x + 1]), make_float2(c_row, c_row), make_float2(-ref, -ref));
+              y.x = exp2_approx(y.x);
+              y.y = exp2_approx(y.y);
+              sum = add2(sum, y);
+              p[half * 32 + x / 2] = half2_bits(y.x, y.y);
+            }
+          }
+          total = sum.x + sum.y;
+          // (the comparison is false for NaN)
+          if (look || !__any_sync(0xffffffffu, valid && total > kMost)) break;
+          look = true;
+        }
+        l += total;
+        tmem_st32(ts, p);
+        tmem_st32(ts + 32, p + 32);
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_full[buf]);
+    }
+    if (n > 0) {
+      if (!wait_bar(P, S, &S.v_empty[(done - 1) & 1], ((done - 1) >> 1) & 1)) return;
+      tc_fence_after();
+    }
+    if (!warp_valid) continue;
+
+    const float unit_v = 8.f * pow2(c.v_exp ? clamp_exp(c.v_exp[it.h]) : 0);
+    const int64_t part = 2ll * blockIdx.x + it.starts;
+    const float inv = it.whole ? (l != 0.f ? unit_v / l : 0.f) : unit_v;
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+      float o[32];
+      if (n > 0) {
+        tmem_ld32(to + 32 * q, o);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = 0.f;
+      }
+      if (!valid) continue;
+      // eight columns are the dimensions 0 4 1 5 2 6 3 7
+      if (it.whole) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(io.out) + at_row * io.out_stride + hq * D + 32 * q);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float* y = o + 8 * x;
+          dst[x] = make_uint4(Pack<T>::put(y[0] * inv, y[2] * inv), Pack<T>::put(y[4] * inv, y[6] * inv),
+                              Pack<T>::put(y[1] * inv, y[3] * inv), Pack<T>::put(y[5] * inv, y[7] * inv));
+        }
+      } else {
+        float4* dst = reinterpret_cast<float4*>(P.o + (part * kRows + row) * D + 32 * q);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float* y = o + 8 * x;
+          dst[2 * x] = make_float4(y[0] * inv, y[2] * inv, y[4] * inv, y[6] * inv);
+          dst[2 * x + 1] = make_float4(y[1] * inv, y[3] * inv, y[5] * inv, y[7] * inv);
+        }
+      }
+    }
+    tc_fence_before();
+    if (valid && !it.whole) P.stat[part * kRows + row] = make_float2(ref, l);
+    if (valid && it.whole && io.lse)
+      io.lse[at_row * io.n_q_heads + hq] = l != 0.f ? (ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant__ KvqParams P) {
+  extern __shared__ uint8_t raw_smem[];
+  WideSmem<D>& S = *reinterpret_cast<WideSmem<D>*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
+  const mk_kvq_attn_io& io = P.io;
+  const int warp = threadIdx.x / 32, lane = lane_id(), Hk = io.kvq.n_kv_heads;
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.k_full[i], kConvert);
+      mbar_init(&S.v_full[i], kConvert);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 4);
+    }
+    mbar_init(&S.q_full, 4);
+    mbar_init(&S.drained, 1);
+    S.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    __syncwarp();
+    tmem_alloc(&S.tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
+
+  // The line: each thread adds up the requests of a stretch of the batch.
+  const int per = (io.n_requests + kThreads - 1) / kThreads;
+  const int b0 = min(io.n_requests, static_cast<int>(threadIdx.x) * per), b1 = min(io.n_requests, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += read_req<kRows, kKeys>(P, b).cost(Hk);
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) S.sum[warp] = upto;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) upto += total;
+    total += S.sum[w];
+  }
+  Walk walk;
+  walk.share = max(static_cast<int64_t>(1), (total + P.workers - 1) / P.workers);
+  walk.pos = blockIdx.x * walk.share;
+  walk.end = min(total, walk.pos + walk.share);
+  if (walk.pos >= upto - mine && walk.pos < upto) {
+    int64_t begin = upto - mine;
+    int b = b0;
+    for (; b < b1 - 1; ++b) {
+      const int64_t cost = read_req<kRows, kKeys>(P, b).cost(Hk);
+      if (walk.pos < begin + cost) break;
+      begin += cost;
+    }
+    S.first = b;
+    S.first_at = begin;
+  }
+  if (threadIdx.x == 0) P.split[blockIdx.x].parts = 0;
+  __syncthreads();
+  walk.b = S.first;
+  walk.begin = S.first_at;
+
+  if (walk.pos < walk.end) {
+    if (warp < 4) {
+      reg_alloc<208>();
+      rows<T, D>(P, S, walk);
+    } else if (warp < 4 + kConvert) {
+      reg_dealloc<120>();
+      convert<D>(P, S, walk, warp - 4);
+    } else {
+      reg_dealloc<64>();
+      if (warp == 12) {
+      const bool ok = issue_mmas<D>(P, S, walk);
+      // of work that was given up: the products on their way
+      if (!ok) {
+        if (elect_one()) mma_commit(&S.drained);
+        __syncwarp();
+        mbar_wait_bounded(&S.drained, 0, kWaitNs);
+      } else {
+        // an item that ends in a later CTA
+        Item it;
+        while (walk.next(P, it)) {
+          if (!it.starts || it.whole || lane) continue;
+          const Req rq = read_req<kRows, kKeys>(P, it.b);
+          const int64_t start = walk.begin + (static_cast<int64_t>(it.h) * rq.row_tiles + it.first / kRows) * rq.tiles;
+          const int64_t last = (start + rq.tiles - 1) / walk.share;
+          P.split[blockIdx.x] = {static_cast<int32_t>(last - blockIdx.x + 1), it.cu, it.rows, it.first, it.h};
+        }
+      }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) tmem_dealloc(S.tmem, 512);
+}
+
+template <class T, int D>
+mk_status launch(const KvqParams& P, int device, int sms, cudaStream_t s) {
+  constexpr int smem = sizeof(WideSmem<D>) + 1024;
+  static std::atomic<uint64_t> ready{0};  // (once per device: it takes as long as a launch)
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_kvq_wide<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  lc.stream = s;
+  lc.gridDim = dim3(sms);
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = smem;
+  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_wide<T, D>, P));
+  return MK_OK;
+}
+
+}  // namespace
+
+mk_status launch_kvq_wide(const KvqParams& P, int device, int sms, cudaStream_t s) {
+  const bool d128 = P.io.kvq.head_dim == 128;
+  if (P.io.dtype == MK_BF16)
+    return d128 ? launch<__nv_bfloat16, 128>(P, device, sms, s) : launch<__nv_bfloat16, 64>(P, device, sms, s);
+  return d128 ? launch<__half, 128>(P, device, sms, s) : launch<__half, 64>(P, device, sms, s);
+}
+
+}  // namespace mk
