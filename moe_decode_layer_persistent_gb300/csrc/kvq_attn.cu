@@ -162,11 +162,18 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
         begin += cost;
         ++b;
       }
-      const int64_t off = pos - begin, item = off / rq.tiles;
+      const int64_t off = pos - begin, item = off / (rq.tiles + rq.lead);
       h = static_cast<int>(item / rq.row_tiles);
       const int rt = static_cast<int>(item - static_cast<int64_t>(h) * rq.row_tiles);
-      const int ta = static_cast<int>(off - item * rq.tiles);
-      const int tb = static_cast<int>(min(static_cast<int64_t>(rq.tiles), ta + (end - pos)));
+      const int64_t start = begin + item * (rq.tiles + rq.lead), to = min(end, start + rq.tiles + rq.lead);
+      const Piece piece = piece_of(rq, pos - start, to - start);
+      const int ta = piece.a, tb = piece.b;
+      if (ta >= tb) {  // (what an item takes on top of its key tiles)
+        __syncwarp();
+        if (lane == 0) at.pos = to, at.begin = begin, at.b = b;
+        __syncwarp();
+        continue;
+      }
       const int rows = rq.n * P.group;  // (checked by the host to be an int)
       int klo = INT_MAX, khi = 0;
       const float unit_k = pow2(c.k_exp ? clamp_exp(c.k_exp[h]) : 0);
@@ -238,15 +245,12 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
       table = io.block_table + b * io.table_stride;
       if (lane == 0) {
         const bool whole = ta == 0 && tb == rq.tiles;
-        at.pos = pos + (tb - ta);
+        at.pos = to;
         at.begin = begin;
         at.b = b, at.h = h, at.cu = rq.cu, at.rows = rows, at.first = rt * R, at.base = rq.base;
         at.whole = whole, at.klo = klo, at.khi = khi;
         at.part = 2ll * worker + (ta == 0);
-        if (ta == 0 && !whole) {
-          const int64_t last = (pos + rq.tiles - 1) / share;  // the warp with the item's last tile
-          P.split[worker] = {static_cast<int32_t>(last - worker + 1), rq.cu, rows, rt * R, h};
-        }
+        if (ta == 0 && !whole) P.split[worker] = {parts_of(rq, start, share), 0, rq.cu, rows, rt * R, h};
       }
       __syncwarp();
     }
@@ -517,15 +521,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kvq_join(const __grid_const
   pdl_wait();
   const Split sp = P.split[worker];
   if (sp.parts == 0) return;
-  const int rows = R / gridDim.y, r0 = blockIdx.y * rows;
+  const int rows = R / gridDim.y, r0 = blockIdx.y * rows, n = sp.parts << sp.folded;
   // adds up parts from, from + step, ...
   auto add = [&](int r, int from, int step, float& top, float& all, float (&acc)[V]) {
     top = kNoRef, all = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
 #pragma unroll 4
-    for (int p = from; p < sp.parts; p += step) {
-      const int64_t at = (p ? 2ll * (worker + p) : 2ll * worker + 1) * R + r;
+    for (int k = from; k < n; k += step) {
+      const int p = k >> sp.folded;
+      const int64_t at = (p ? 2ll * (worker + p) : 2ll * worker + 1) * R + r + (sp.folded & k) * (R / 2);
       const float2 x = P.stat[at];
       const float* o = P.o + at * D + lane * V;
       float y[V];
@@ -552,7 +557,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kvq_join(const __grid_const
       io.lse[row * io.n_q_heads + hq] = all != 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY;
   };
   float acc[V], top, all;
-  if (sp.parts <= kFewParts) {
+  if (n <= kFewParts) {
     for (int r = r0 + warp; r < r0 + rows && sp.first + r < sp.rows; r += kJoinWarps) {
       add(r, 0, 1, top, all, acc);
       write(sp.first + r, top, all, acc);

@@ -15,10 +15,17 @@ namespace mk {
 // largest at most.
 constexpr float kRefBelow = 6.f, kRefMost = 15.f;
 constexpr float kNoRef = -1e30f;
+#ifndef LEAD
+#define LEAD 3
+#define WLEAD 4
+#endif
+constexpr int kLead = LEAD, kWideLead = WLEAD;
 
-// An item whose stretches lie in several warps, as the warp with the first says.
+// An item that is joined, as the worker with its first key tile says: one whose
+// stretches lie in several workers, or whose rows a worker holds twice.
 struct Split {
   int32_t parts;     // 0: none
+  int32_t folded;    // row r lies in rows r and r + kWideRows / 2 of each part
   int32_t cu, rows;  // first row of the request, its rows of this kv head
   int32_t first;     // first of these in the tile
   int32_t h;
@@ -40,13 +47,28 @@ struct KvqParams {
 
 MK_DEV int clampi(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : static_cast<int>(v); }
 
-// One request's lengths, made safe, and its place on the line.
+// One request's lengths, made safe, and its place on the line: for each kv head and
+// row tile an item of its key tiles, in front of them `lead` units for what an item
+// takes on top (Q, the first copies, the results).
 struct Req {
   int32_t cu, n, len, base;
   int32_t tile0, tiles;  // first key tile of its items and how many they have
   int32_t row_tiles;
-  MK_DEV int64_t cost(int heads) const { return static_cast<int64_t>(tiles) * row_tiles * heads; }
+  int32_t lead;
+  MK_DEV int64_t cost(int heads) const { return static_cast<int64_t>(tiles + lead) * row_tiles * heads; }
 };
+// The part of an item that lies between two places of it: key tiles [a, b).
+struct Piece {
+  int32_t a, b;
+};
+MK_DEV Piece piece_of(const Req& r, int64_t from, int64_t to) {
+  return {static_cast<int32_t>(max(from - r.lead, static_cast<int64_t>(0))),
+          static_cast<int32_t>(max(min(to - r.lead, static_cast<int64_t>(r.tiles)), static_cast<int64_t>(0)))};
+}
+// How many workers share the key tiles of an item that starts at a place of the line.
+MK_DEV int parts_of(const Req& r, int64_t start, int64_t share) {
+  return static_cast<int>((start + r.lead + r.tiles - 1) / share - (start + r.lead) / share + 1);
+}
 template <int R, int KEYS>
 MK_DEV Req read_req(const KvqParams& P, int b) {
   const mk_kvq_attn_io& io = P.io;
@@ -57,6 +79,7 @@ MK_DEV Req read_req(const KvqParams& P, int b) {
   r.base = max(0, r.len - r.n);
   const int low = io.window ? max(0, r.base - io.window + 1) : 0;
   r.tile0 = low / KEYS;
+  r.lead = KEYS == 32 ? kLead : kWideLead;
   // (at least one, so that rows without keys are written)
   r.tiles = max(1, (r.len + KEYS - 1) / KEYS - r.tile0);
   r.row_tiles = static_cast<int>((static_cast<int64_t>(r.n) * P.group + R - 1) / R);

@@ -76,31 +76,45 @@ struct Item {
   int32_t b, h, cu, n, base, len, rows, first;  // rows of the kv head, the tile's first
   int32_t tile, tile_end;                       // key tiles to go through
   int32_t klo, khi;                             // keys that some row sees
-  bool whole, starts;
+  int32_t parts;                                // workers that share it
+  bool starts;                                  // this one has its first key tile
+  // No more than half of the tile's rows: they are there twice, and the first half of
+  // the threads takes the even key tiles, the second the odd ones.  (The other half's
+  // weights are zeros.)  The weights of a tile are otherwise what takes longest.
+  bool folded;
 };
 struct Walk {
   int64_t pos, end, begin, share;
   int32_t b;
   // The next stretch (for whole warps); false if there is none.
   MK_DEV bool next(const KvqParams& P, Item& it) {
-    if (pos >= end) return false;
     const mk_kvq_attn_io& io = P.io;
     const int Hk = io.kvq.n_kv_heads;
-    Req rq = read_req<kRows, kKeys>(P, b);
-    for (int64_t cost; pos >= begin + (cost = rq.cost(Hk)); rq = read_req<kRows, kKeys>(P, b)) {
-      begin += cost;
-      ++b;
-    }
-    const int64_t off = pos - begin, item = off / rq.tiles;
+    Req rq;
+    Piece piece;
+    int64_t item, start;
+    do {
+      if (pos >= end) return false;
+      rq = read_req<kRows, kKeys>(P, b);
+      for (int64_t cost; pos >= begin + (cost = rq.cost(Hk)); rq = read_req<kRows, kKeys>(P, b)) {
+        begin += cost;
+        ++b;
+      }
+      item = (pos - begin) / (rq.tiles + rq.lead);
+      start = begin + item * (rq.tiles + rq.lead);
+      const int64_t to = min(end, start + rq.tiles + rq.lead);
+      piece = piece_of(rq, pos - start, to - start);
+      pos = to;
+    } while (piece.a >= piece.b);  // (what an item takes on top of its key tiles)
     it.h = static_cast<int>(item / rq.row_tiles);
     const int rt = static_cast<int>(item - static_cast<int64_t>(it.h) * rq.row_tiles);
-    const int ta = static_cast<int>(off - item * rq.tiles);
-    const int tb = static_cast<int>(min(static_cast<int64_t>(rq.tiles), ta + (end - pos)));
+    const int ta = piece.a, tb = piece.b;
     it.b = b, it.cu = rq.cu, it.n = rq.n, it.base = rq.base, it.len = rq.len;
     it.rows = rq.n * P.group;
     it.first = rt * kRows;
     it.starts = ta == 0;
-    it.whole = ta == 0 && tb == rq.tiles;
+    it.parts = parts_of(rq, start, share);
+    it.folded = it.rows - it.first <= kRows / 2;
     const int i0 = quotient(it.first, P.by_group), i1 = quotient(min(it.rows, it.first + kRows) - 1, P.by_group);
     int depth = i0;
     it.khi = min(rq.len, rq.base + i1 + 1);
@@ -118,7 +132,6 @@ struct Walk {
     it.klo = io.window ? max(0, rq.base + depth - io.window + 1) : 0;
     it.tile = max(rq.tile0 + ta, min(it.klo, it.khi) / kKeys);
     it.tile_end = min(rq.tile0 + tb, (it.khi + kKeys - 1) / kKeys);
-    pos += tb - ta;
     return true;
   }
 };
@@ -273,76 +286,100 @@ MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
 }
 
 // ---- a row per thread
+// What a thread knows of its row of an item.
+struct Row {
+  Item it;
+  int64_t at;     // row of q
+  uint64_t tree;  // bits of the keys from it.base on
+  int32_t hq, lo, hi;
+  float c;        // factor on its scores
+  bool valid;
+};
+
+// Brings the row's Q into shared memory, in fp16 relative to its largest value, the
+// pairs in the order of the codes'.
+template <class T, int D>
+MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r) {
+  const mk_kvq_attn_io& io = P.io;
+  const mk_kvq_cache& c = io.kvq;
+  const Item& it = r.it;
+  const int row = threadIdx.x, f = it.first + (it.folded ? row & (kRows / 2 - 1) : row);
+  r.valid = f < it.rows;
+  const int i = quotient(r.valid ? f : 0, P.by_group);
+  r.hq = it.h * P.group + (r.valid ? f - i * P.group : 0);
+  r.at = it.cu + i;
+  r.c = P.scale_log2 * pow2(c.k_exp ? clamp_exp(c.k_exp[it.h]) : 0);
+  r.lo = r.hi = 0;
+  r.tree = 0;
+  if (r.valid) {
+    if (io.tree_mask) r.tree = io.tree_mask[r.at];
+    const int p = it.base + (io.tree_mask ? __popcll(r.tree) - 1 : i);
+    r.lo = io.window ? max(0, p - io.window + 1) : 0;
+    r.hi = io.tree_mask ? min(it.len, it.base) : min(it.len, it.base + i + 1);
+  }
+  if (it.tile >= it.tile_end) return;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(io.q) + r.at * io.q_stride + r.hq * D);
+  uint4 raw[D / 8];
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j) raw[j] = r.valid ? src[j] : make_uint4(0, 0, 0, 0);
+  if (!std::is_same<T, __half>::value) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[j].x & 0x7FFF7FFFu, raw[j].y & 0x7FFF7FFFu),
+                                   __vmaxu2(raw[j].z & 0x7FFF7FFFu, raw[j].w & 0x7FFF7FFFu)));
+    top = max(top & 0xFFFFu, top >> 16);
+    const int e = min(max(static_cast<int>(top >> 7), 1), 253);
+    const float inv = top < 0x7F80u ? __int_as_float((254 - e) << 23) : 1.f;
+    r.c *= top < 0x7F80u ? __int_as_float(e << 23) : 1.f;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) {
+      uint32_t* x = reinterpret_cast<uint32_t*>(&raw[j]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 y = Pack<T>::get(x[k]);
+        x[k] = half2_bits(y.x * inv, y.y * inv);
+      }
+    }
+  }
+  r.c = fmaxf(r.c, FLT_MIN);  // (a masked score, -infinity, must not meet 0)
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j)
+    *reinterpret_cast<uint4*>(S.q + (j >> 3) * (kRows * 128) + row * 128 + (((j & 7) ^ (row & 7)) << 4)) =
+        make_uint4(__byte_perm(raw[j].x, raw[j].z, 0x5410), __byte_perm(raw[j].x, raw[j].z, 0x7632),
+                   __byte_perm(raw[j].y, raw[j].w, 0x5410), __byte_perm(raw[j].y, raw[j].w, 0x7632));
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane_id() == 0) mbar_arrive(&S.q_full);
+}
+
 template <class T, int D>
 MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   const mk_kvq_attn_io& io = P.io;
-  const mk_kvq_cache& c = io.kvq;
   const int lane = lane_id(), warp = threadIdx.x / 32, row = threadIdx.x;
   const uint32_t lanes = S.tmem + (static_cast<uint32_t>(warp * 32) << 16), to = lanes + 256;
   int done = 0;
-  Item it;
-  while (walk.next(P, it)) {
-    const int f = it.first + row;
-    const bool valid = f < it.rows;
-    const int i = quotient(valid ? f : 0, P.by_group), hq = it.h * P.group + (valid ? f - i * P.group : 0);
-    const int64_t at_row = it.cu + i;
-    // Q, in fp16 relative to the row's largest value, its pairs as the codes' are
-    float c_row = P.scale_log2 * pow2(c.k_exp ? clamp_exp(c.k_exp[it.h]) : 0);
-    const int n = it.tile_end - it.tile;
-    if (n > 0) {  // (no products of the item before are on their way: its last scores have come)
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(io.q) + at_row * io.q_stride + hq * D);
-      uint4 raw[D / 8];
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) raw[j] = valid ? src[j] : make_uint4(0, 0, 0, 0);
-      if (!std::is_same<T, __half>::value) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[j].x & 0x7FFF7FFFu, raw[j].y & 0x7FFF7FFFu),
-                                       __vmaxu2(raw[j].z & 0x7FFF7FFFu, raw[j].w & 0x7FFF7FFFu)));
-        top = max(top & 0xFFFFu, top >> 16);
-        const int e = min(max(static_cast<int>(top >> 7), 1), 253);
-        const float inv = top < 0x7F80u ? __int_as_float((254 - e) << 23) : 1.f;
-        c_row *= top < 0x7F80u ? __int_as_float(e << 23) : 1.f;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          uint32_t* x = reinterpret_cast<uint32_t*>(&raw[j]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 y = Pack<T>::get(x[k]);
-            x[k] = half2_bits(y.x * inv, y.y * inv);
-          }
-        }
-      }
-      c_row = fmaxf(c_row, FLT_MIN);  // (a masked score, -infinity, must not meet 0)
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-        *reinterpret_cast<uint4*>(S.q + (j >> 3) * (kRows * 128) + row * 128 + (((j & 7) ^ (row & 7)) << 4)) =
-            make_uint4(__byte_perm(raw[j].x, raw[j].z, 0x5410), __byte_perm(raw[j].x, raw[j].z, 0x7632),
-                       __byte_perm(raw[j].y, raw[j].w, 0x5410), __byte_perm(raw[j].y, raw[j].w, 0x7632));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.q_full);
-    }
-
-    // the keys that the row sees: lo .. hi-1 and, of a tree, bits from base on
-    int lo = 0, hi = 0;
-    uint64_t tree = 0;
-    if (valid) {
-      if (io.tree_mask) tree = io.tree_mask[at_row];
-      const int p = it.base + (io.tree_mask ? __popcll(tree) - 1 : i);
-      lo = io.window ? max(0, p - io.window + 1) : 0;
-      hi = io.tree_mask ? min(it.len, it.base) : min(it.len, it.base + i + 1);
-    }
-    const bool warp_valid = __any_sync(0xffffffffu, valid);
+  Row r;
+  bool more = walk.next(P, r.it);
+  if (more) take_row<T, D>(P, S, r);
+  while (more) {
+    const bool warp_valid = __any_sync(0xffffffffu, r.valid);
+    const int n = r.it.tile_end - r.it.tile;
     float ref = kNoRef, l = 0.f;
     for (int t = 0; t < n; ++t, ++done) {
-      const int buf = done & 1, k0 = (it.tile + t) * kKeys;
+      const int buf = done & 1, k0 = (r.it.tile + t) * kKeys;
       if (!wait_bar(P, S, &S.s_full[buf], (done >> 1) & 1)) return;
       tc_fence_after();
-      if (warp_valid) {
-        const uint32_t ts = lanes + buf * 128;
-        const bool edge = __any_sync(0xffffffffu, valid && (k0 < lo || k0 + kKeys > hi));
+      const uint32_t ts = lanes + buf * 128;
+      if (warp_valid && r.it.folded && (t & 1) != warp >> 1) {
+        uint32_t p[32];
+#pragma unroll
+        for (int x = 0; x < 32; ++x) p[x] = 0;
+        tmem_st32(ts, p);
+        tmem_st32(ts + 32, p);
+        tmem_st_wait();
+      } else if (warp_valid) {
+        const bool edge = __any_sync(0xffffffffu, r.valid && (k0 < r.lo || k0 + kKeys > r.hi));
         auto scores = [&](int half, float (&s)[64]) {
           tmem_ld32(ts + half * 64, s);
           tmem_ld32(ts + half * 64 + 32, s + 32);
@@ -351,11 +388,15 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int at = k0 + half * 64 + q * 32;
-            uint32_t see = below(hi - at) & ~below(lo - at);
+            uint32_t see = below(r.hi - at) & ~below(r.lo - at);
             if (io.tree_mask) {
               // bit x: key at + x, of which those from base on follow the row's word
-              const int off = it.base - at;
-              see |= (off >= 32 ? 0u : off >= 0 ? static_cast<uint32_t>(tree) << off : off > -64 ? static_cast<uint32_t>(tree >> -off) : 0u) & below(it.khi - at);
+              const int off = r.it.base - at;
+              see |= (off >= 32    ? 0u
+                      : off >= 0   ? static_cast<uint32_t>(r.tree) << off
+                      : off > -64 ? static_cast<uint32_t>(r.tree >> -off)
+                                   : 0u) &
+                     below(r.it.khi - at);
             }
 #pragma unroll
             for (int x = 0; x < 32; ++x)
@@ -364,7 +405,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
         };
         uint32_t p[64];
         float total;
-        bool look = __any_sync(0xffffffffu, valid && ref == kNoRef);
+        bool look = __any_sync(0xffffffffu, r.valid && ref == kNoRef);
 #pragma unroll 1
         while (true) {
           if (look) {
@@ -377,8 +418,8 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
 #pragma unroll
               for (int x = 0; x < 64; x += 2) top = max3(top, s[x], s[x + 1]);
             }
-            top *= c_row;
-            const float next = valid && top - ref > kRefBelow ? top - kRefBelow : ref;
+            top *= r.c;
+            const float next = r.valid && top - ref > kRefBelow ? top - kRefBelow : ref;
             const float old = exp2_approx(ref - next);
             l *= old;
             ref = next;
@@ -405,7 +446,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
             scores(half, s);
 #pragma unroll
             for (int x = 0; x < 64; x += 2) {
-              float2 y = fma2(make_float2(s[x], s[x + 1]), make_float2(c_row, c_row), make_float2(-ref, -ref));
+              float2 y = fma2(make_float2(s[x], s[x + 1]), make_float2(r.c, r.c), make_float2(-ref, -ref));
               y.x = exp2_approx(y.x);
               y.y = exp2_approx(y.y);
               sum = add2(sum, y);
@@ -414,7 +455,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
           }
           total = sum.x + sum.y;
           // (the comparison is false for NaN)
-          if (look || !__any_sync(0xffffffffu, valid && total > kMost)) break;
+          if (look || !__any_sync(0xffffffffu, r.valid && total > kMost)) break;
           look = true;
         }
         l += total;
@@ -426,15 +467,21 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.p_full[buf]);
     }
+
+    // The next item's Q goes its way before this one's results: Q's last products, the
+    // last tile's scores, are there.
+    const Row mine = r;
+    more = walk.next(P, r.it);
+    if (more) take_row<T, D>(P, S, r);
     if (n > 0) {
       if (!wait_bar(P, S, &S.v_empty[(done - 1) & 1], ((done - 1) >> 1) & 1)) return;
       tc_fence_after();
     }
     if (!warp_valid) continue;
-
-    const float unit_v = 8.f * pow2(c.v_exp ? clamp_exp(c.v_exp[it.h]) : 0);
-    const int64_t part = 2ll * blockIdx.x + it.starts;
-    const float inv = it.whole ? (l != 0.f ? unit_v / l : 0.f) : unit_v;
+    const float unit_v = 8.f * pow2(io.kvq.v_exp ? clamp_exp(io.kvq.v_exp[mine.it.h]) : 0);
+    const int64_t part = 2ll * blockIdx.x + mine.it.starts;
+    const bool whole = mine.it.parts == 1 && !mine.it.folded;
+    const float inv = whole ? (l != 0.f ? unit_v / l : 0.f) : unit_v;
 #pragma unroll 1
     for (int q = 0; q < D / 32; ++q) {
       float o[32];
@@ -445,30 +492,32 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
 #pragma unroll
         for (int x = 0; x < 32; ++x) o[x] = 0.f;
       }
-      if (!valid) continue;
-      // eight columns are the dimensions 0 4 1 5 2 6 3 7
-      if (it.whole) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(io.out) + at_row * io.out_stride + hq * D + 32 * q);
+      if (mine.valid) {
+        // eight columns are the dimensions 0 4 1 5 2 6 3 7
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(io.out) + mine.at * io.out_stride + mine.hq * D + 32 * q);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float* y = o + 8 * x;
-          dst[x] = make_uint4(Pack<T>::put(y[0] * inv, y[2] * inv), Pack<T>::put(y[4] * inv, y[6] * inv),
-                              Pack<T>::put(y[1] * inv, y[3] * inv), Pack<T>::put(y[5] * inv, y[7] * inv));
-        }
-      } else {
-        float4* dst = reinterpret_cast<float4*>(P.o + (part * kRows + row) * D + 32 * q);
+          for (int x = 0; x < 4; ++x) {
+            const float* y = o + 8 * x;
+            dst[x] = make_uint4(Pack<T>::put(y[0] * inv, y[2] * inv), Pack<T>::put(y[4] * inv, y[6] * inv),
+                                Pack<T>::put(y[1] * inv, y[3] * inv), Pack<T>::put(y[5] * inv, y[7] * inv));
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(P.o + (part * kRows + row) * D + 32 * q);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float* y = o + 8 * x;
-          dst[2 * x] = make_float4(y[0] * inv, y[2] * inv, y[4] * inv, y[6] * inv);
-          dst[2 * x + 1] = make_float4(y[1] * inv, y[3] * inv, y[5] * inv, y[7] * inv);
+          for (int x = 0; x < 4; ++x) {
+            const float* y = o + 8 * x;
+            dst[2 * x] = make_float4(y[0] * inv, y[2] * inv, y[4] * inv, y[6] * inv);
+            dst[2 * x + 1] = make_float4(y[1] * inv, y[3] * inv, y[5] * inv, y[7] * inv);
+          }
         }
       }
+      __syncwarp();
     }
     tc_fence_before();
-    if (valid && !it.whole) P.stat[part * kRows + row] = make_float2(ref, l);
-    if (valid && it.whole && io.lse)
-      io.lse[at_row * io.n_q_heads + hq] = l != 0.f ? (ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (mine.valid && !whole) P.stat[part * kRows + row] = make_float2(ref, l);
+    if (mine.valid && whole && io.lse)
+      io.lse[mine.at * io.n_q_heads + mine.hq] = l != 0.f ? (ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
 }
 
@@ -559,14 +608,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant_
         __syncwarp();
         mbar_wait_bounded(&S.drained, 0, kWaitNs);
       } else {
-        // an item that ends in a later CTA
+        // an item to join
         Item it;
         while (walk.next(P, it)) {
-          if (!it.starts || it.whole || lane) continue;
-          const Req rq = read_req<kRows, kKeys>(P, it.b);
-          const int64_t start = walk.begin + (static_cast<int64_t>(it.h) * rq.row_tiles + it.first / kRows) * rq.tiles;
-          const int64_t last = (start + rq.tiles - 1) / walk.share;
-          P.split[blockIdx.x] = {static_cast<int32_t>(last - blockIdx.x + 1), it.cu, it.rows, it.first, it.h};
+          if (it.starts && (it.parts > 1 || it.folded) && lane == 0)
+            P.split[blockIdx.x] = {it.parts, it.folded, it.cu, it.rows, it.first, it.h};
         }
       }
       }
