@@ -28,6 +28,7 @@ constexpr int kMaxStages = 12;
 constexpr int kThreads = 192;     // producer, MMA issuer, four warps of results
 constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
 constexpr uint32_t kTimeout = 1;
+constexpr int kSmem = 222 * 1024;  // of a CTA, at most: one per SM
 
 struct LinearParams {
   mk_linear_io io;
@@ -36,7 +37,8 @@ struct LinearParams {
   int32_t row_tiles;   // tiles along the rows of x
   int32_t tiles;       // all tiles
   int32_t blocks;      // of inputs
-  int32_t split;       // CTAs per tile
+  int32_t split;       // CTAs (pairs of CTAs) per tile
+  int32_t pair;        // a tile is 256 outputs, of two CTAs
   int32_t stages;
   int32_t tmem_cols;   // allocated; two tiles' where a CTA has several
   uint32_t idesc;
@@ -50,12 +52,20 @@ struct LinearBars {
   uint32_t tmem, abort;
 };
 
-MK_DEV float activated(float y, int act) {
-  if (act == MK_ACT_SILU) return y / (1.f + expf(-y));
-  if (act == MK_ACT_GELU) return 0.5f * y * (1.f + erff(y * 0.7071067811865476f));
-  if (act == MK_ACT_GELU_TANH)
-    return 0.5f * y * (1.f + tanhf(0.7978845608028654f * (y + 0.044715f * y * y * y)));
-  return y;
+// y = act(y) of N values (the choice outside of the loop, so that their chains overlap).
+template <int N>
+MK_DEV void activate(float (&y)[N], int act) {
+  if (act == MK_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = __fdividef(y[i], 1.f + __expf(-y[i]));
+  } else if (act == MK_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = 0.5f * y[i] * (1.f + erff(y[i] * 0.7071067811865476f));
+  } else if (act == MK_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      y[i] = 0.5f * y[i] * (1.f + tanhf(0.7978845608028654f * (y[i] + 0.044715f * y[i] * y[i] * y[i])));
+  }
 }
 
 // Bounded wait: false once any wait of the CTA has run out.
@@ -75,6 +85,70 @@ MK_DEV bool wait_bar(const LinearParams& P, LinearBars& B, uint64_t* bar, uint32
   }
 }
 
+// Pairs of CTAs: each holds half of a tile's outputs and brings half of the rows of x;
+// the first one's issuer multiplies for both.
+MK_DEV uint32_t address_in(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+template <bool PAIR>
+MK_DEV void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, uint64_t policy, uint32_t leader) {
+  if (!PAIR) {
+    tma_load_2d(dst, map, bar, x, y, policy);
+    return;
+  }
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(address_in(bar, leader)), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+template <bool PAIR>
+MK_DEV void multiply(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  if (!PAIR) {
+    mma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
+    return;
+  }
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on `bar` (of both CTAs of a pair, whose ranks `mask` names) when the products
+// issued so far are done.
+template <bool PAIR>
+MK_DEV void commit(uint64_t* bar, uint32_t mask) {
+  if (!PAIR) {
+    mma_commit(bar);
+    return;
+  }
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(mask))
+      : "memory");
+}
+template <bool PAIR>
+MK_DEV void alloc_columns(uint32_t* to, uint32_t cols) {
+  if (!PAIR) {
+    tmem_alloc(to, cols);
+    tmem_relinquish();
+    return;
+  }
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(to)), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+template <bool PAIR>
+MK_DEV void free_columns(uint32_t at, uint32_t cols) {
+  if (!PAIR) tmem_dealloc(at, cols);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
+}
+MK_DEV void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 MK_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -92,7 +166,7 @@ MK_DEV float4 load_cluster(uint32_t addr, uint32_t rank) {
 // Of a split tile: adds up the ranks' sums of rows c0 .. c1-1 (four outputs per
 // lane, a row per warp at a time, kRows rows on their way) and writes the results.
 template <class T, bool VEC>
-MK_DEV void join_sums(const LinearParams& P, uint32_t sums, int feat0, int row0, int c0, int c1) {
+MK_DEV void join_sums(const LinearParams& P, uint32_t sums, int feat0, int row0, int c0, int c1, int half) {
   constexpr int kRows = 4, kWarps = kThreads / 32;
   const mk_linear_io& io = P.io;
   const int warp = threadIdx.x / 32, feat = feat0 + static_cast<int>(lane_id()) * 4;
@@ -122,7 +196,7 @@ MK_DEV void join_sums(const LinearParams& P, uint32_t sums, int feat0, int row0,
     for (int k = 0; k < P.split; ++k)
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const float4 v = load_cluster(sums + min(col + i * kWarps, c1 - 1) * (kFeat * 4) + lane_id() * 16, k);
+        const float4 v = load_cluster(sums + min(col + i * kWarps, c1 - 1) * (kFeat * 4) + lane_id() * 16, P.pair ? 2 * k + half : k);
         y[i].x += v.x, y[i].y += v.y, y[i].z += v.z, y[i].w += v.w;
       }
 #pragma unroll
@@ -130,8 +204,10 @@ MK_DEV void join_sums(const LinearParams& P, uint32_t sums, int feat0, int row0,
       const int at = col + i * kWarps;
       if (at >= c1) continue;
       T* out = static_cast<T*>(io.out) + static_cast<int64_t>(row0 + at) * io.out_stride + feat;
-      const float z[4] = {activated(y[i].x + bias[0], io.act) + r[i][0], activated(y[i].y + bias[1], io.act) + r[i][1],
-                          activated(y[i].z + bias[2], io.act) + r[i][2], activated(y[i].w + bias[3], io.act) + r[i][3]};
+      float z[4] = {y[i].x + bias[0], y[i].y + bias[1], y[i].z + bias[2], y[i].w + bias[3]};
+      activate(z, io.act);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] += r[i][j];
       if (VEC) {
         if (mine == 4) *reinterpret_cast<uint2*>(out) = make_uint2(Pack<T>::put(z[0], z[1]), Pack<T>::put(z[2], z[3]));
       } else {
@@ -143,7 +219,7 @@ MK_DEV void join_sums(const LinearParams& P, uint32_t sums, int feat0, int row0,
   }
 }
 
-template <class T>
+template <class T, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear(const __grid_constant__ LinearParams P, const __grid_constant__ CUtensorMap wmap,
              const __grid_constant__ CUtensorMap xmap) {
@@ -152,9 +228,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const mk_linear_io& io = P.io;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
   const int warp = threadIdx.x / 32, lane = lane_id();
-  const uint32_t stage_bytes = kFeat * 128 + P.cols * 128;
-  const int rank = blockIdx.x % P.split;
-  const int first = blockIdx.x / P.split, step = gridDim.x / P.split;
+  constexpr int kCtas = PAIR ? 2 : 1, kTileFeat = kFeat * kCtas;
+  const int x_rows = P.cols / kCtas;  // that this CTA brings
+  const uint32_t stage_bytes = kFeat * 128 + x_rows * 128;
+  const int in_cluster = blockIdx.x % (P.split * kCtas), rank = in_cluster / kCtas, half = in_cluster % kCtas;
+  const uint32_t leader = in_cluster - half, both = 3u << leader;
+  const int first = blockIdx.x / (P.split * kCtas), step = gridDim.x / (P.split * kCtas);
   // this CTA's blocks of every tile
   const int k0 = static_cast<int>(static_cast<int64_t>(P.blocks) * rank / P.split);
   const int k1 = static_cast<int>(static_cast<int64_t>(P.blocks) * (rank + 1) / P.split);
@@ -165,16 +244,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&wmap);
     prefetch_tensormap(&xmap);
     for (int i = 0; i < P.stages; ++i) mbar_init(&B.full[i], 1), mbar_init(&B.empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&B.acc_full[i], 1), mbar_init(&B.acc_empty[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&B.acc_full[i], 1), mbar_init(&B.acc_empty[i], 4 * kCtas);
     mbar_init(&B.drained, 1);
     B.abort = 0;
     fence_mbar_init();
   }
   __syncwarp();
-  if (warp == 1) {
-    tmem_alloc(&B.tmem, P.tmem_cols);
-    tmem_relinquish();
-  }
+  if (PAIR) cluster_sync();  // (barriers that the other CTA arrives at)
+  if (warp == 1) alloc_columns<PAIR>(&B.tmem, P.tmem_cols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -188,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t keep = policy_evict_normal(), once = P.row_tiles == 1 ? policy_evict_first() : keep;
       bool ok = true;
       for (int tile = first; tile < P.tiles && ok; tile += step) {
-        const int f = tile / P.row_tiles * kFeat, r = tile % P.row_tiles * P.cols;
+        const int f = tile / P.row_tiles * kTileFeat + half * kFeat, r = tile % P.row_tiles * P.cols + half * x_rows;
         for (int k = k0; k < k1; ++k, ++loads) {
           const int st = loads % P.stages, round = loads / P.stages;
           if (round && !wait_bar(P, B, &B.empty[st], (round - 1) & 1)) {
@@ -196,18 +273,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           uint8_t* a = smem + st * stage_bytes;
-          mbar_arrive_expect_tx(&B.full[st], stage_bytes);
-          tma_load_2d(a, &wmap, &B.full[st], k * kBlock, f, once);
-          tma_load_2d(a + kFeat * 128, &xmap, &B.full[st], k * kBlock, r, keep);
+          if (half == 0) mbar_arrive_expect_tx(&B.full[st], stage_bytes * kCtas);
+          load_box<PAIR>(a, &wmap, &B.full[st], k * kBlock, f, once, leader);
+          load_box<PAIR>(a + kFeat * 128, &xmap, &B.full[st], k * kBlock, r, keep, leader);
         }
       }
       // of work that was given up: the copies on their way, the last one into each stage
-      if (!ok)
+      // (the second of a pair: the first one's barriers count its copies; it has waited long)
+      if (!ok && half == 0)
         for (int i = max(0, loads - P.stages); i < loads; ++i) mbar_wait_bounded(&B.full[i % P.stages], (i / P.stages) & 1, kWaitNs);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (elect_one()) {
+    if (half == 0 && elect_one()) {
       bool ok = true;
       int used = 0, n = 0;
       for (int tile = first; tile < P.tiles && ok; tile += step, ++n) {
@@ -228,13 +306,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t ad = sdesc_kmajor_sw128(a), bd = sdesc_kmajor_sw128(a + kFeat * 128);
 #pragma unroll
           for (int i = 0; i < kBlock / 16; ++i)  // 16 inputs: 32 bytes on in the swizzled rows
-            mma_bf16(tmem + buf * acc_cols, ad + 2 * i, bd + 2 * i, P.idesc, k > k0 || i > 0);
-          mma_commit(&B.empty[st]);
+            multiply<PAIR>(tmem + buf * acc_cols, ad + 2 * i, bd + 2 * i, P.idesc, k > k0 || i > 0);
+          commit<PAIR>(&B.empty[st], both);
         }
-        if (ok) mma_commit(&B.acc_full[buf]);
+        if (ok) commit<PAIR>(&B.acc_full[buf], both);
       }
       if (!ok) {
-        mma_commit(&B.drained);
+        commit<PAIR>(&B.drained, both);
         mbar_wait_bounded(&B.drained, 0, kWaitNs);
       }
     }
@@ -247,21 +325,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* sums = reinterpret_cast<float*>(smem);  // of a split tile: [cols][128]
     for (int tile = first; tile < P.tiles; tile += step, ++n) {
       const int buf = n & 1;
-      ok = __all_sync(0xffffffffu, wait_bar(P, B, &B.acc_full[buf], (n >> 1) & 1));
-      if (!ok) break;
-      tc_fence_after();
-      const int feat = tile / P.row_tiles * kFeat + quad * 32 + lane;
+      const int feat = tile / P.row_tiles * kTileFeat + half * kFeat + quad * 32 + lane;
       const int row0 = tile % P.row_tiles * P.cols, rows = min(P.cols, io.n_rows - row0);
       const bool mine = feat < io.n_out;
       const float bias = io.bias && mine ? static_cast<float>(static_cast<const T*>(io.bias)[feat]) : 0.f;
       const T* res = static_cast<const T*>(io.residual) + static_cast<int64_t>(row0) * io.residual_stride + feat;
       T* out = static_cast<T*>(io.out) + static_cast<int64_t>(row0) * io.out_stride + feat;
+      // (the residual of the columns behind the next ones is on its way)
+      T ahead[2][16];
+      auto fetch = [&](int col, T (&to)[16]) {
+        if (!io.residual || P.split > 1) return;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          to[i] = mine && col + i < rows ? res[static_cast<int64_t>(col + i) * io.residual_stride] : static_cast<T>(0.f);
+      };
+      fetch(0, ahead[0]);
+      fetch(16, ahead[1]);
+      ok = __all_sync(0xffffffffu, wait_bar(P, B, &B.acc_full[buf], (n >> 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
       for (int col = 0; col < rows; col += 16) {
         float v[16], r[16];
-        if (io.residual && P.split == 1)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            r[i] = mine && col + i < rows ? static_cast<float>(res[static_cast<int64_t>(col + i) * io.residual_stride]) : 0.f;
+        for (int i = 0; i < 16; ++i) {
+          r[i] = static_cast<float>(ahead[0][i]);
+          ahead[0][i] = ahead[1][i];
+        }
+        fetch(col + 32, ahead[1]);
         tmem_ld16(tmem + lane_at + buf * acc_cols + col, v);
         if (P.split > 1) {
 #pragma unroll
@@ -269,16 +359,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (!mine || col + i >= rows) continue;
-          float y = activated(v[i] + bias, io.act);
-          if (io.residual) y += r[i];
-          out[static_cast<int64_t>(col + i) * io.out_stride] = static_cast<T>(y);
+        for (int i = 0; i < 16; ++i) v[i] += bias;
+        activate(v, io.act);
+        if (io.residual)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += r[i];
+        T* to = out + static_cast<int64_t>(col) * io.out_stride;
+        if (mine && col + 16 <= rows) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i, to += io.out_stride) *to = static_cast<T>(v[i]);
+        } else if (mine) {
+          for (int i = 0; i < 16; ++i, to += io.out_stride)
+            if (col + i < rows) *to = static_cast<T>(v[i]);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&B.acc_empty[buf]);
+      if (lane == 0) {
+        if (half == 0) mbar_arrive(&B.acc_empty[buf]);
+        else arrive_at(address_in(&B.acc_empty[buf], leader));
+      }
     }
   }
   if (P.split > 1) {
@@ -286,18 +386,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     // (a CTA of a cluster has one tile)
     if (!*const_cast<volatile uint32_t*>(&B.abort)) {
-      const int feat0 = first / P.row_tiles * kFeat;
+      const int feat0 = first / P.row_tiles * kTileFeat + half * kFeat;
       const int row0 = first % P.row_tiles * P.cols, rows = min(P.cols, io.n_rows - row0);
       const int c0 = rows * rank / P.split, c1 = rows * (rank + 1) / P.split;
-      if (P.vec) join_sums<T, true>(P, smem_u32(smem), feat0, row0, c0, c1);
-      else join_sums<T, false>(P, smem_u32(smem), feat0, row0, c0, c1);
+      if (P.vec) join_sums<T, true>(P, smem_u32(smem), feat0, row0, c0, c1, half);
+      else join_sums<T, false>(P, smem_u32(smem), feat0, row0, c0, c1, half);
     }
     __syncwarp();
-    cluster_sync();  // no CTA leaves while another one reads its sums
   }
+  // no CTA leaves while another one reads its sums or arrives at its barriers
   tc_fence_before();
+  if (PAIR || P.split > 1) cluster_sync();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, P.tmem_cols);
+  if (warp == 1) free_columns<PAIR>(tmem, P.tmem_cols);
 }
 
 // 2-D map over [rows][inner] 16-bit values, box of 64 x box_rows, 128-byte swizzle;
@@ -317,47 +418,109 @@ mk_status encode_tmap(CUtensorMap* map, int dtype, const void* base, uint64_t in
   return r == CUDA_SUCCESS ? MK_OK : MK_ERR_INVALID_ARG;
 }
 
-// Sizes of the tiles and how many CTAs share one.
-void choose(LinearParams* P, int sms) {
-  const int64_t m = P->io.n_rows;
-  const int64_t row_tiles = (m + 255) / 256, each = (m + row_tiles - 1) / row_tiles;
-  P->cols = static_cast<int32_t>((each + 15) / 16 * 16);
-  P->row_tiles = static_cast<int32_t>((m + P->cols - 1) / P->cols);
-  P->tiles = P->row_tiles * static_cast<int32_t>((P->io.n_out + kFeat - 1) / kFeat);
-  P->blocks = (P->io.n_in + kBlock - 1) / kBlock;
-  P->split = 1;
-  if (P->tiles < sms) P->split = std::max(1, std::min({8, sms / P->tiles, P->blocks / 4}));
-  const int stage = (kFeat + P->cols) * 128;
-  P->stages = std::min({kMaxStages, 220 * 1024 / stage, std::max(2, P->blocks / P->split + 1)});
-  const int acc = P->cols <= 32 ? 32 : P->cols <= 64 ? 64 : P->cols <= 128 ? 128 : 256;
-  P->tmem_cols = 2 * acc;
+// How many clusters of 2 .. 8 CTAs, one CTA per SM, run at the same time: less than
+// the SMs divided by their size, as a cluster's SMs lie side by side.
+template <class T>
+mk_status max_clusters(int device, int sms, int (&most)[9]) {
+  static std::atomic<int> known[64][9];
+  for (int c = 1; c <= 8; ++c) {
+    int n = c == 1 ? sms : device < 64 ? known[device][c].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+      cudaLaunchConfig_t lc = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = c;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      lc.attrs = attr;
+      lc.numAttrs = 1;
+      lc.gridDim = dim3(c * sms);
+      lc.blockDim = dim3(kThreads);
+      lc.dynamicSmemBytes = kSmem;
+      MK_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_linear<T, false>, &lc));
+      if (device < 64) known[device][c].store(n, std::memory_order_relaxed);
+    }
+    most[c] = n;
+  }
+  return MK_OK;
 }
 
-template <class T>
-mk_status launch(const LinearParams& P, const CUtensorMap& w, const CUtensorMap& x, int device, int sms, cudaStream_t s) {
-  static std::atomic<uint64_t> ready{0};  // (once per device: it takes as long as a launch)
-  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
-  if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    MK_CUDA_TRY(cudaFuncSetAttribute(k_linear<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 221 * 1024 + 1024));
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
+int columns_of(int cols) { return cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256; }
+
+// Sizes of the tiles and how many CTAs share one; returns how many CTAs work.
+int choose(LinearParams* P, const int (&most)[9], int ctas) {
+  const int64_t m = P->io.n_rows, n = P->io.n_out;
+  const int64_t row_tiles = (m + 255) / 256, each = (m + row_tiles - 1) / row_tiles;
+  const int unit = 16 * ctas, feat = kFeat * ctas;
+  P->pair = ctas == 2;
+  P->blocks = (P->io.n_in + kBlock - 1) / kBlock;
+  P->cols = static_cast<int32_t>((each + unit - 1) / unit * unit);
+  P->row_tiles = static_cast<int32_t>((m + P->cols - 1) / P->cols);
+  P->tiles = P->row_tiles * static_cast<int32_t>((n + feat - 1) / feat);
+  // as many CTAs per tile as run at the same time, of four blocks at least
+  P->split = 1;
+  for (int s = 2; s * ctas <= 8; ++s)
+    if (P->tiles <= most[s * ctas] && P->blocks >= 4 * s) P->split = s;
+  const int stage = (kFeat + P->cols / ctas) * 128;
+  P->stages = std::min({kMaxStages, (kSmem - 1024) / stage, std::max(2, P->blocks / P->split + 1)});
+  P->tmem_cols = 2 * columns_of(P->cols);
+  return ctas * std::min(P->tiles * P->split, most[ctas]);
+}
+
+// With more than 128 rows what a CTA copies per block, its weights and all rows, takes
+// longer than its products: a pair halves the rows (4096 rows, 4096 -> 12288: 264 us,
+// with pairs 223).  Few tiles do better one by one if that keeps more CTAs busy, a
+// quarter more (250 rows, 4096 -> 4096: 128 CTAs 17.1 us, 48 pairs 18.8).
+void choose(LinearParams* P, const int (&most)[9]) {
+  const int single = choose(P, most, 1);
+  if (P->cols <= 128 || P->io.n_out <= kFeat) return;
+  if (choose(P, most, 2) * 5 < single * 4) choose(P, most, 1);
+}
+
+template <class T, bool PAIR>
+mk_status launch(const LinearParams& P, const CUtensorMap& w, const CUtensorMap& x, const int (&most)[9],
+                 cudaStream_t s) {
+  constexpr int kCtas = PAIR ? 2 : 1;
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = P.split;
+  attr[1].val.clusterDim.x = P.split * kCtas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
-  lc.numAttrs = P.split > 1 ? 2 : 1;
+  lc.numAttrs = P.split * kCtas > 1 ? 2 : 1;
   lc.stream = s;
-  lc.gridDim = dim3(P.split > 1 ? P.tiles * P.split : std::min(P.tiles, sms));
+  lc.gridDim = dim3(P.split > 1 ? P.tiles * P.split * kCtas : std::min(P.tiles, most[kCtas]) * kCtas);
   lc.blockDim = dim3(kThreads);
-  const int stage = (kFeat + P.cols) * 128;
   // (a split tile's sums lie where the stages were)
-  lc.dynamicSmemBytes = std::max(P.stages * stage, P.split > 1 ? P.cols * kFeat * 4 : 0) + 1024;
-  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_linear<T>, P, w, x));
+  lc.dynamicSmemBytes = std::max(P.stages * (kFeat + P.cols / kCtas) * 128, P.split > 1 ? P.cols * kFeat * 4 : 0) + 1024;
+  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_linear<T, PAIR>, P, w, x));
   return MK_OK;
+}
+
+template <class T>
+mk_status linear(LinearParams* P, int device, int sms, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};  // (once per device: it takes as long as a launch)
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_linear<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_linear<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  int most[9] = {};
+  mk_status st = max_clusters<T>(device, sms, most);
+  if (st != MK_OK) return st;
+  choose(P, most);
+  const mk_linear_io& io = P->io;
+  // M, N of a product; fp16 is type 0, bf16 type 1
+  P->idesc = idesc_bf16(P->pair ? 2 * kFeat : kFeat, P->cols);
+  if (io.dtype == MK_FP16) P->idesc &= ~((1u << 7) | (1u << 10));
+  CUtensorMap w, x;
+  st = encode_tmap(&w, io.dtype, io.w, io.n_in, io.n_out, io.w_stride, kFeat);
+  if (st != MK_OK) return st;
+  st = encode_tmap(&x, io.dtype, io.x, io.n_in, io.n_rows, io.x_stride, P->pair ? P->cols / 2 : P->cols);
+  if (st != MK_OK) return st;
+  return P->pair ? launch<T, true>(*P, w, x, most, s) : launch<T, false>(*P, w, x, most, s);
 }
 
 mk_status check_shapes(const mk_linear_io* io) {
@@ -425,17 +588,9 @@ mk_status mk_linear(const mk_linear_io* io, void* workspace, int64_t workspace_b
   LinearParams P;
   P.io = *io;
   P.status = static_cast<uint32_t*>(workspace);
-  choose(&P, sms);
-  // M 128, N the tile's columns; fp16 is type 0, bf16 type 1
-  P.idesc = io->dtype == MK_BF16 ? idesc_bf16(kFeat, P.cols) : idesc_bf16(kFeat, P.cols) & ~((1u << 7) | (1u << 10));
   P.vec = n % 4 == 0 && io->out_stride % 4 == 0 && !misaligned(io->out, 8) &&
           (!io->residual || (io->residual_stride % 4 == 0 && !misaligned(io->residual, 8)));
-  CUtensorMap w, x;
-  st = encode_tmap(&w, io->dtype, io->w, k, n, io->w_stride, kFeat);
-  if (st != MK_OK) return st;
-  st = encode_tmap(&x, io->dtype, io->x, k, m, io->x_stride, P.cols);
-  if (st != MK_OK) return st;
-  return io->dtype == MK_BF16 ? launch<__nv_bfloat16>(P, w, x, device, sms, s) : launch<__half>(P, w, x, device, sms, s);
+  return io->dtype == MK_BF16 ? linear<__nv_bfloat16>(&P, device, sms, s) : linear<__half>(&P, device, sms, s);
 }
 
 mk_status mk_linear_status(const void* workspace) {

@@ -546,7 +546,8 @@ def check_linear(mk, rng, m, k, n, dtype, bias=False, act="none", residual=False
 @pytest.mark.parametrize("m,k,n", [
     (1, 8, 1), (1, 64, 128), (2, 256, 384), (3, 72, 130), (16, 4096, 256), (17, 1000, 129), (31, 136, 100),
     (64, 2048, 640), (65, 520, 255), (100, 4096, 257), (127, 64, 127), (128, 128, 256), (129, 192, 513),
-    (250, 1024, 1031), (256, 320, 999), (257, 8, 7), (600, 264, 300), (1000, 512, 1500)])
+    (250, 1024, 1031), (256, 320, 999), (257, 8, 7), (600, 264, 300), (1000, 512, 1500), (2100, 136, 2600),
+    (90, 72, 23000)])
 def test_linear(cuda_lib, dtype, m, k, n):
     check_linear(cuda_lib, np.random.default_rng(m + k + n), m, k, n, dtype, bias=bool(n & 1), residual=bool(m & 1))
 
