@@ -25,7 +25,8 @@ namespace {
 constexpr int kFeat = 128;        // outputs of a tile
 constexpr int kBlock = 64;        // inputs of a block: 128 bytes, the width of the swizzle
 constexpr int kMaxStages = 12;
-constexpr int kThreads = 192;     // producer, MMA issuer, four warps of results
+constexpr int kOutWarps = 8;      // of results: two to 32 outputs, for every other 16 rows
+constexpr int kThreads = 32 * (2 + kOutWarps);  // producer, MMA issuer, these
 constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
 constexpr uint32_t kTimeout = 1;
 constexpr int kSmem = 222 * 1024;  // of a CTA, at most: one per SM
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&wmap);
     prefetch_tensormap(&xmap);
     for (int i = 0; i < P.stages; ++i) mbar_init(&B.full[i], 1), mbar_init(&B.empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&B.acc_full[i], 1), mbar_init(&B.acc_empty[i], 4 * kCtas);
+    for (int i = 0; i < 2; ++i) mbar_init(&B.acc_full[i], 1), mbar_init(&B.acc_empty[i], kOutWarps * kCtas);
     mbar_init(&B.drained, 1);
     B.abort = 0;
     fence_mbar_init();
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    const int quad = warp & 3;
+    const int quad = warp & 3, col0 = (warp - 2) / 4 * 16;
     const uint32_t lane_at = static_cast<uint32_t>(quad * 32) << 16;
     int n = 0;
     bool ok = true;
@@ -339,19 +340,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 16; ++i)
           to[i] = mine && col + i < rows ? res[static_cast<int64_t>(col + i) * io.residual_stride] : static_cast<T>(0.f);
       };
-      fetch(0, ahead[0]);
-      fetch(16, ahead[1]);
+      fetch(col0, ahead[0]);
+      fetch(col0 + 32, ahead[1]);
       ok = __all_sync(0xffffffffu, wait_bar(P, B, &B.acc_full[buf], (n >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
-      for (int col = 0; col < rows; col += 16) {
+      for (int col = col0; col < rows; col += 32) {
         float v[16], r[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           r[i] = static_cast<float>(ahead[0][i]);
           ahead[0][i] = ahead[1][i];
         }
-        fetch(col + 32, ahead[1]);
+        fetch(col + 64, ahead[1]);
         tmem_ld16(tmem + lane_at + buf * acc_cols + col, v);
         if (P.split > 1) {
 #pragma unroll
