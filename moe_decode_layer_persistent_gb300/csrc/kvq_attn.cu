@@ -506,10 +506,11 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
   }
 }
 
-// Joins the parts of a split item: part 2 w + 1 of the worker with the first and
-// parts 2 (w + 1), ... of those behind it.  A CTA takes R / gridDim.y of its rows: a
-// row per warp, or where there are many parts all warps one row after the other, the
-// parts shared out among them.
+// Joins the parts of items: part 2 w + 1 of the worker with the first and parts
+// 2 (w + 1), ... of those behind it.  A CTA takes R / gridDim.y rows of the items of
+// every gridDim.x-th worker (most have none: a CTA for each takes 7 us longer): a row
+// per warp, or where there are many parts all warps one row after the other, the parts
+// shared out among them.
 constexpr int kJoinWarps = 8, kFewParts = 12;
 template <class T, int D, int R>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_kvq_join(const __grid_constant__ KvqParams P) {
@@ -517,71 +518,76 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kvq_join(const __grid_const
   __shared__ float sum_o[kJoinWarps][D];
   __shared__ float2 sum_l[kJoinWarps];
   const mk_kvq_attn_io& io = P.io;
-  const int lane = lane_id(), warp = threadIdx.x / 32, worker = blockIdx.x;
+  const int lane = lane_id(), warp = threadIdx.x / 32;
   pdl_wait();
-  const Split sp = P.split[worker];
-  if (sp.parts == 0) return;
-  const int rows = R / gridDim.y, r0 = blockIdx.y * rows, n = sp.parts << sp.folded;
-  // adds up parts from, from + step, ...
-  auto add = [&](int r, int from, int step, float& top, float& all, float (&acc)[V]) {
-    top = kNoRef, all = 0.f;
+  const int mine = blockIdx.x + lane * gridDim.x;  // (the host sees to it that 32 are enough)
+  uint32_t todo = __ballot_sync(0xffffffffu, mine < P.workers && P.split[mine].parts != 0);
+  const int rows = R / gridDim.y, r0 = blockIdx.y * rows;
+  for (; todo; todo &= todo - 1) {
+    const int worker = blockIdx.x + (__ffs(todo) - 1) * gridDim.x;
+    const Split sp = P.split[worker];
+    const int n = sp.parts << sp.folded;
+    // adds up parts from, from + step, ...
+    auto add = [&](int r, int from, int step, float& top, float& all, float (&acc)[V]) {
+      top = kNoRef, all = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+      for (int v = 0; v < V; ++v) acc[v] = 0.f;
 #pragma unroll 4
-    for (int k = from; k < n; k += step) {
-      const int p = k >> sp.folded;
-      const int64_t at = (p ? 2ll * (worker + p) : 2ll * worker + 1) * R + r + (sp.folded & k) * (R / 2);
-      const float2 x = P.stat[at];
-      const float* o = P.o + at * D + lane * V;
-      float y[V];
-      if (V == 4) *reinterpret_cast<float4*>(y) = __ldcs(reinterpret_cast<const float4*>(o));
-      else *reinterpret_cast<float2*>(y) = __ldcs(reinterpret_cast<const float2*>(o));
-      const float next = fmaxf(top, x.x), old = exp2f(top - next), f = exp2f(x.x - next);
-      top = next;
-      all = all * old + x.y * f;
+      for (int k = from; k < n; k += step) {
+        const int p = k >> sp.folded;
+        const int64_t at = (p ? 2ll * (worker + p) : 2ll * worker + 1) * R + r + (sp.folded & k) * (R / 2);
+        const float2 x = P.stat[at];
+        const float* o = P.o + at * D + lane * V;
+        float y[V];
+        if (V == 4) *reinterpret_cast<float4*>(y) = __ldcs(reinterpret_cast<const float4*>(o));
+        else *reinterpret_cast<float2*>(y) = __ldcs(reinterpret_cast<const float2*>(o));
+        const float next = fmaxf(top, x.x), old = exp2f(top - next), f = exp2f(x.x - next);
+        top = next;
+        all = all * old + x.y * f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = acc[v] * old + y[v] * f;
-    }
-  };
-  auto write = [&](int fr, float top, float all, const float (&acc)[V]) {
-    const float inv = all != 0.f ? 1.f / all : 0.f;
-    const int i = quotient(fr, P.by_group), hq = sp.h * P.group + fr - i * P.group;
-    const int64_t row = sp.cu + i;
-    uint32_t y[V / 2];
-#pragma unroll
-    for (int v = 0; v < V; v += 2) y[v / 2] = Pack<T>::put(acc[v] * inv, acc[v + 1] * inv);
-    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<T*>(io.out) + row * io.out_stride + hq * D + lane * V);
-#pragma unroll
-    for (int v = 0; v < V / 2; ++v) to[v] = y[v];
-    if (lane == 0 && io.lse)
-      io.lse[row * io.n_q_heads + hq] = all != 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY;
-  };
-  float acc[V], top, all;
-  if (n <= kFewParts) {
-    for (int r = r0 + warp; r < r0 + rows && sp.first + r < sp.rows; r += kJoinWarps) {
-      add(r, 0, 1, top, all, acc);
-      write(sp.first + r, top, all, acc);
-    }
-    return;
-  }
-  for (int r = r0; r < r0 + rows && sp.first + r < sp.rows; ++r) {
-    add(r, warp, kJoinWarps, top, all, acc);
-#pragma unroll
-    for (int v = 0; v < V; ++v) sum_o[warp][lane * V + v] = acc[v];
-    if (lane == 0) sum_l[warp] = make_float2(top, all);
-    __syncthreads();
-    if (warp == 0) {
-      float m = kNoRef, s = 0.f, out[V] = {};
-      for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sum_l[w].x);
-      for (int w = 0; w < kJoinWarps; ++w) {
-        const float f = exp2f(sum_l[w].x - m);
-        s += sum_l[w].y * f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) out[v] += sum_o[w][lane * V + v] * f;
+        for (int v = 0; v < V; ++v) acc[v] = acc[v] * old + y[v] * f;
       }
-      write(sp.first + r, m, s, out);
+    };
+    auto write = [&](int fr, float top, float all, const float (&acc)[V]) {
+      const float inv = all != 0.f ? 1.f / all : 0.f;
+      const int i = quotient(fr, P.by_group), hq = sp.h * P.group + fr - i * P.group;
+      const int64_t row = sp.cu + i;
+      uint32_t y[V / 2];
+#pragma unroll
+      for (int v = 0; v < V; v += 2) y[v / 2] = Pack<T>::put(acc[v] * inv, acc[v + 1] * inv);
+      uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<T*>(io.out) + row * io.out_stride + hq * D + lane * V);
+#pragma unroll
+      for (int v = 0; v < V / 2; ++v) to[v] = y[v];
+      if (lane == 0 && io.lse)
+        io.lse[row * io.n_q_heads + hq] = all != 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY;
+    };
+    float acc[V], top, all;
+    if (n <= kFewParts) {
+      for (int r = r0 + warp; r < r0 + rows && sp.first + r < sp.rows; r += kJoinWarps) {
+        add(r, 0, 1, top, all, acc);
+        write(sp.first + r, top, all, acc);
+      }
+      continue;
     }
-    __syncthreads();
+    for (int r = r0; r < r0 + rows && sp.first + r < sp.rows; ++r) {
+      add(r, warp, kJoinWarps, top, all, acc);
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum_o[warp][lane * V + v] = acc[v];
+      if (lane == 0) sum_l[warp] = make_float2(top, all);
+      __syncthreads();
+      if (warp == 0) {
+        float m = kNoRef, s = 0.f, out[V] = {};
+        for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sum_l[w].x);
+        for (int w = 0; w < kJoinWarps; ++w) {
+          const float f = exp2f(sum_l[w].x - m);
+          s += sum_l[w].y * f;
+#pragma unroll
+          for (int v = 0; v < V; ++v) out[v] += sum_o[w][lane * V + v] * f;
+        }
+        write(sp.first + r, m, s, out);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -633,7 +639,8 @@ mk_status launch(const KvqParams& P, int device, int sms, cudaStream_t s) {
   }
   // few items, many parts each: rows on CTAs of their own
   const int64_t items = (static_cast<int64_t>(P.io.n_rows) * P.group / R + P.io.n_requests) * P.io.kvq.n_kv_heads;
-  lc.gridDim = dim3(P.workers, items * 16 < P.workers ? R : R == kWideRows ? R / 8 : 1);
+  const bool few = items * 16 < P.workers;
+  lc.gridDim = dim3(std::min(P.workers, (few ? 1 : 12) * sms), few ? R : R == kWideRows ? R / 8 : 1);
   lc.blockDim = dim3(kJoinWarps * 32);
   lc.dynamicSmemBytes = 0;
   MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_join<T, D, R>, P));
