@@ -1,5 +1,5 @@
-// attn_ptx.cuh -- device primitives of the attention kernels: tensor memory by rows,
-// products with operand A in tensor memory, pairs of float32 operations.
+// attn_ptx.cuh -- device primitives of the attention kernels and the cache writes: tensor
+// memory by rows, products with operand A in tensor memory, pairs of float32 operations.
 #pragma once
 #include "ptx.cuh"
 
@@ -69,6 +69,14 @@ MK_DEV float2 add2(float2 a, float2 b) {
   float2 d;
   asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
       " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+MK_DEV float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;

@@ -12,6 +12,7 @@
 #include <climits>
 #include <math_constants.h>
 
+#include "attn_ptx.cuh"
 #include "kvq.cuh"
 #include "rope.h"
 
@@ -60,40 +61,47 @@ MK_DEV uint4 pack8(const float (&y)[8]) {
 // What 8 values of every q head, or of every k head, of a row are multiplied with:
 // themselves by a, their partners by b.
 struct Turn {
-  float a[8], b[8];
-  bool turns;
-  float top, partner_top;  // bounds of |a| and |b|
+  float2 a[4], b[4];
 };
 
+// A thread's 8 norm weights and those of its values' partners with the sign that these
+// have in the rotation.
+struct Weights {
+  uint4 own, partner;
+};
 template <class T, int LAYOUT>
-MK_DEV Turn make_turn(const AppendParams& P, const void* weights, const float2* cs, int l, int from) {
+MK_DEV Weights load_weights(const AppendParams& P, const void* w, int l, int from) {
+  const uint32_t one = Pack<T>::put(1.f, 1.f);
+  Weights x;
+  x.own = x.partner = make_uint4(one, one, one, one);
+  if (w && l * 8 < P.d) {
+    x.own = reinterpret_cast<const uint4*>(w)[l];
+    if (LAYOUT == MK_ROPE_HALF) x.partner = reinterpret_cast<const uint4*>(w)[from];
+  }
+  if (LAYOUT == MK_ROPE_HALF) {
+    const uint32_t sign = l < P.rot / 16 ? 0x80008000u : 0u;
+    x.partner.x ^= sign, x.partner.y ^= sign, x.partner.z ^= sign, x.partner.w ^= sign;
+  } else {  // neighbours: the first of a pair takes away
+    const uint32_t* o = reinterpret_cast<const uint32_t*>(&x.own);
+    uint32_t* p = reinterpret_cast<uint32_t*>(&x.partner);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = __byte_perm(o[i], 0, 0x1032) ^ 0x8000u;
+  }
+  return x;
+}
+// cosines, sines: of the thread's pairs (8 or, of neighbours, 4).
+template <class T, int LAYOUT>
+MK_DEV Turn make_turn(const Weights& w, const float* cosines, const float* sines) {
+  const uint32_t own[4] = {w.own.x, w.own.y, w.own.z, w.own.w};
+  const uint32_t partner[4] = {w.partner.x, w.partner.y, w.partner.z, w.partner.w};
   Turn t;
-  float w[8], wp[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = wp[i] = 1.f;
-  const bool turns = t.turns = l < P.rot / 8;
-  if (weights && l * 8 < P.d) {
-    unpack8<T>(reinterpret_cast<const uint4*>(weights)[l], w);
-    if (LAYOUT == MK_ROPE_HALF) unpack8<T>(reinterpret_cast<const uint4*>(weights)[from], wp);
+  for (int i = 0; i < 4; ++i) {
+    const float2 c = LAYOUT == MK_ROPE_HALF ? make_float2(cosines[2 * i], cosines[2 * i + 1]) : make_float2(cosines[i], cosines[i]);
+    const float2 s = LAYOUT == MK_ROPE_HALF ? make_float2(sines[2 * i], sines[2 * i + 1]) : make_float2(sines[i], sines[i]);
+    t.a[i] = mul2(Pack<T>::get(own[i]), c);
+    t.b[i] = mul2(Pack<T>::get(partner[i]), s);
   }
-  if (LAYOUT == MK_ROPE_INTERLEAVED)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wp[i] = w[i ^ 1];
-  t.top = t.partner_top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    t.top = fmaxf(t.top, fabsf(w[i]));
-    t.partner_top = fmaxf(t.partner_top, fabsf(wp[i]));
-    t.a[i] = w[i];
-    t.b[i] = 0.f;
-    if (!turns) continue;
-    const bool second = LAYOUT == MK_ROPE_HALF ? l >= P.rot / 16 : i & 1;
-    const float2 c = cs[LAYOUT == MK_ROPE_HALF ? (second ? l - P.rot / 16 : l) * 8 + i : l * 4 + i / 2];
-    t.a[i] = w[i] * c.x;
-    t.b[i] = second ? wp[i] * c.y : -wp[i] * c.y;
-  }
-  if (turns) t.top *= P.m, t.partner_top *= P.m;
-  else t.partner_top = 0.f;
   return t;
 }
 
@@ -153,48 +161,54 @@ __device__ __noinline__ uint3 exact_group(const AppendParams& P, const T* x, con
 
 // Codes of 8 values (value i in bits 4 i) and the scale of their group; the lane's
 // neighbour has the group's other 8.  MADE: the values were computed, and are off by
-// `off` at most; near: this could tell.
+// `off` at most; near_border: this could tell.  Else they are given, in at most 11
+// bits, and ties between codes or scales are frequent among them: quotients come by
+// way of a reciprocal, whose error of 2^-20 would break the ties, and are rounded to
+// more than that and less than what lies between a tie and its neighbours first.
 template <bool MADE>
-MK_DEV uint2 quantise(const float (&z)[8], float off, bool* near_border) {
-  float top = 0.f;
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    nan |= z[i] != z[i];
-    top = fmaxf(top, fabsf(z[i]));
-  }
-  if (nan) top = CUDART_NAN_F;
-  const float other = __shfl_xor_sync(0xffffffffu, top, 1);
-  nan |= other != other;
-  top = fmaxf(top, other);
-  const float seventh = __fdiv_rn(top, 7.f);
-  const uint32_t scale = floats_to_e4m3x2(seventh, 0.f) & 0xFFu;
-  const float s = e4m3_to_float(scale);
-  uint32_t word = 0;
+MK_DEV uint2 quantise(const float (&z)[8], float top, float off, bool* near_border) {
+  top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const bool nan = top != top;
+  float seventh = top * (1.f / 7.f);
   bool near = false;
   if (MADE) {
     off = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, 1));
-    const uint32_t both = floats_to_e4m3x2(seventh - off, seventh + off);
+    // (the product is off by 2^-23)
+    const float room = off + seventh * 0x1p-22f;
+    const uint32_t both = floats_to_e4m3x2(seventh - room, seventh + room);
     near = (both & 0xFFu) != (both >> 8);
+  } else if (seventh < 1e30f) {
+    const float c = __fmul_rn(seventh, 4097.f);  // to 12 bits
+    seventh = __fsub_rn(c, __fsub_rn(c, seventh));
   }
-  // Given values are divided, as ties between codes are frequent among them; computed
-  // ones near a tie are worked out again anyway (a product with 1 / s is off by 2^-22
-  // of up to 8).
-  const float inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
-  const float room = 0.5f - off * inv - 0x1p-19f;
+  const uint32_t scale = floats_to_e4m3x2(seventh, 0.f) & 0xFFu;
+  const float s = e4m3_to_float(scale), inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  float dev = 0.f;
+  uint32_t word = 0;
+  constexpr float kWhole = 12582912.f;  // 1.5 2^23: what is added to it is rounded to a whole number
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = MADE ? z[i] * inv : s > 0.f ? __fdiv_rn(z[i], s) : 0.f;
-    const float n = rintf(t);
-    if (MADE) near |= !(fabsf(t - n) <= room) && fabsf(t) < 9.f;
-    word |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(n, -8.f), 7.f)) + 8) << (4 * i);
+  for (int i = 7; i >= 0; --i) {
+    float t = fminf(fmaxf(z[i] * inv, -8.25f), 7.25f);  // (what lies beyond are codes 0 and 15)
+    if (!MADE) t = __fsub_rn(__fadd_rn(t, 48.f), 48.f);  // to 2^-18
+    const float n = __fadd_rn(t, kWhole);
+    if (MADE) dev = fmaxf(dev, fabsf(t - __fsub_rn(n, kWhole)));
+    word = word * 16 + __float_as_uint(n);
   }
+  // of the eight 0x4B400000 + n (mod 2^32) to codes n + 8
+  word += 0x88888888u - 0x4B400000u * 0x11111111u;
   if (MADE) {
-    near = near && !nan;
+    near = (near || dev > 0.5f - off * inv - 0x1p-19f) && !nan;
     *near_border = __shfl_xor_sync(0xffffffffu, static_cast<int>(near), 1) || near;
   }
   if (nan) return make_uint2(0x88888888u, 0x7Fu);
   return make_uint2(word, scale);
+}
+
+MK_DEV float largest(const float (&z)[8]) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max_or_nan(top, fabsf(z[i]));
+  return top;
 }
 
 // Where the slot's row of a kv head starts in the pools of codes and scales, in rows.
@@ -202,98 +216,91 @@ MK_DEV int64_t kvq_row(const mk_kvq_cache& c, int page_shift, int64_t slot, int 
   return (((slot >> page_shift) * c.n_kv_heads + head) << page_shift) + (slot & (c.page_size - 1));
 }
 
-// One row per CTA (gridDim.y 3: a CTA each for its q, k and v heads).
+// A row per CTA (gridDim.y 3: a CTA each for its q, k and v heads).
 template <class T, int LAYOUT, int BITS, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid_constant__ AppendParams P) {
   const mk_qkv_append_io& io = P.io;
-  __shared__ float2 cs[128];
-  const int64_t row = blockIdx.x;
+  // of the row's pairs, and behind them those of values that pass: cosine 1, sine 0
+  __shared__ __align__(16) float cosines[128 + 8], sines[128 + 8];
   const int d = P.d, team = P.team;
   const int l = threadIdx.x & (team - 1), first = threadIdx.x / team, teams = THREADS / team;
+  const int warp_first = (threadIdx.x & ~31) / team;
   const bool some = l * 8 < d;
   const int parts = gridDim.y == 3 ? 1 << blockIdx.y : 7;
-  const int32_t pos = P.rot ? io.positions[row] : 0;
+  // lane of the partners, and where this thread's pairs lie
+  const int h16 = P.rot / 16;
+  const bool turns = l < P.rot / 8;
+  const int from = LAYOUT == MK_ROPE_HALF && turns ? (l < h16 ? l + h16 : l - h16) : l;
+  const int at_pairs = !turns ? 128 : LAYOUT == MK_ROPE_HALF ? (l < h16 ? l : l - h16) * 8 : l * 4;
+  const uint32_t passes = turns ? ~0u : 0u;  // (a partner that is none is 0: infinity times the sine 0 is NaN)
+  if (threadIdx.x < 8) cosines[128 + threadIdx.x] = 1.f, sines[128 + threadIdx.x] = 0.f;
+
+  // The normed and rotated values of a head.  For a cache in 4 bits: they are off by
+  // the angle's and the sine's rounding (2^-23.4 of the pair), those of the brackets
+  // and products (3 x 2^-24) and of r (2^-21.7 of the value), together less than 2^-20.5
+  // (|n_a| + |n_b|) m, which is at most sqrt 2 (|y_a| + |y_b|).
+  auto turned = [&](const uint4& raw, const Turn& t, bool norm, float (&y)[8]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float2 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = Pack<T>::get(w[i]);
+    float r = 1.f;
+    if (norm) {
+      const float2 ss = add2(fma2(x[1], x[1], mul2(x[0], x[0])), fma2(x[3], x[3], mul2(x[2], x[2])));
+      float sum = ss.x + ss.y;
+      for (int o = team / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      r = __frsqrt_rn(sum * P.by_d + io.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 p;
+      if (LAYOUT == MK_ROPE_HALF) p = Pack<T>::get(__shfl_sync(0xffffffffu, w[i], from, team) & passes);
+      else p = Pack<T>::get(__byte_perm(w[i], 0, 0x1032) & passes);
+      const float2 v = mul2(fma2(x[i], t.a[i], mul2(p, t.b[i])), make_float2(r, r));
+      y[2 * i] = v.x;
+      y[2 * i + 1] = v.y;
+    }
+  };
+
+  const int64_t row = blockIdx.x;
   int64_t slot = -1;
   if (io.k && (parts & 6)) {
     slot = io.slots[row];
     const int64_t most = BITS == 4 ? static_cast<int64_t>(io.kvq.n_pages) << P.page_shift : io.n_slots;
     if (slot >= most) slot = -1;
   }
+  const int32_t pos = P.rot ? io.positions[row] : 0;
   constexpr int kAhead = 4;
-  uint4 next[kAhead];
+  uint4 raw4[kAhead];
   // the first loads are on their way while the angles are made
   const T* q = static_cast<const T*>(io.q) + row * io.q_stride + l * 8;
   if (parts & 1)
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (some && first + u * teams < io.n_q_heads) next[u] = __ldcs(reinterpret_cast<const uint4*>(q + (first + u * teams) * d));
+      if (some && first + u * teams < io.n_q_heads) raw4[u] = __ldcs(reinterpret_cast<const uint4*>(q + (first + u * teams) * d));
   for (int i = threadIdx.x; i < P.rot / 2 && (parts & 3); i += THREADS) {
     const float2 c = cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[i]);
-    cs[i] = make_float2(c.x * P.m, c.y * P.m);
+    cosines[i] = c.x * P.m;
+    sines[i] = c.y * P.m;
   }
   __syncthreads();
-  // lane of the partners
-  const int h16 = P.rot / 16;
-  const int from = LAYOUT == MK_ROPE_HALF && l < 2 * h16 ? (l < h16 ? l + h16 : l - h16) : l;
-
-  // The normed and rotated values of a head; for a cache in 4 bits how far they
-  // may be off: the angle's and the sine's rounding (2^-23.4 of the pair), those of
-  // the brackets and products (3 x 2^-24) and of r (2^-21.7 of the value), together
-  // below 2^-20.5 (|n_a| + |n_b|) m.
-  auto turned = [&](const uint4& raw, const Turn& t, bool norm, float (&y)[8], float* off) {
-    float x[8], p[8];
-    unpack8<T>(raw, x);
-    float r = 1.f;
-    if (norm) {
-      float ss[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ss[i] = x[2 * i] * x[2 * i] + x[2 * i + 1] * x[2 * i + 1];
-      float sum = (ss[0] + ss[1]) + (ss[2] + ss[3]);
-      for (int o = team / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      r = __frsqrt_rn(sum * P.by_d + io.eps);
-    }
-    if (LAYOUT == MK_ROPE_HALF) {
-      uint4 other;
-      other.x = __shfl_sync(0xffffffffu, raw.x, from, team);
-      other.y = __shfl_sync(0xffffffffu, raw.y, from, team);
-      other.z = __shfl_sync(0xffffffffu, raw.z, from, team);
-      other.w = __shfl_sync(0xffffffffu, raw.w, from, team);
-      unpack8<T>(other, p);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
-    }
-    if (off) {
-      float top = 0.f, ptop = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i])), ptop = fmaxf(ptop, fabsf(p[i]));
-      *off = 0x1p-20f * r * (top * t.top + ptop * t.partner_top);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = (t.turns ? x[i] * t.a[i] + p[i] * t.b[i] : x[i] * t.a[i]) * r;
-  };
 
   if (parts & 1) {
     T* out = static_cast<T*>(io.q_out) + row * io.q_out_stride + l * 8;
-    const Turn t = make_turn<T, LAYOUT>(P, io.q_norm, cs, l, from);
+    const Turn t = make_turn<T, LAYOUT>(load_weights<T, LAYOUT>(P, io.q_norm, l, from), cosines + at_pairs, sines + at_pairs);
     // (the loop is the same for a whole warp: its teams meet in the shuffles)
-    const int warp_first = (threadIdx.x & ~31) / team;
     for (int at = 0; warp_first + at < io.n_q_heads; at += kAhead * teams) {
-      uint4 raw[kAhead];
+      if (at)
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) raw[u] = next[u];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int h = first + at + (kAhead + u) * teams;
-        if (some && h < io.n_q_heads) next[u] = __ldcs(reinterpret_cast<const uint4*>(q + h * d));
-      }
+        for (int u = 0; u < kAhead; ++u)
+          if (some && first + at + u * teams < io.n_q_heads) raw4[u] = __ldcs(reinterpret_cast<const uint4*>(q + (first + at + u * teams) * d));
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int h = first + at + u * teams;
-        if (!some || h >= io.n_q_heads) raw[u] = make_uint4(0, 0, 0, 0);
+        if (!some || h >= io.n_q_heads) raw4[u] = make_uint4(0, 0, 0, 0);
         if (warp_first + at + u * teams >= io.n_q_heads) break;
         float y[8];
-        turned(raw[u], t, io.q_norm != nullptr, y, nullptr);
+        turned(raw4[u], t, io.q_norm != nullptr, y);
         if (some && h < io.n_q_heads) *reinterpret_cast<uint4*>(out + h * d) = pack8<T>(y);
       }
     }
@@ -304,9 +311,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid
     const T* src = static_cast<const T*>(is_k ? io.k : io.v);
     if (!(parts >> part & 1) || !src || slot < 0) continue;
     src += row * (is_k ? io.k_stride : io.v_stride);
-    const int warp_first = (threadIdx.x & ~31) / team;
     Turn t;
-    if (is_k) t = make_turn<T, LAYOUT>(P, io.k_norm, cs, l, from);
+    if (is_k) t = make_turn<T, LAYOUT>(load_weights<T, LAYOUT>(P, io.k_norm, l, from), cosines + at_pairs, sines + at_pairs);
     for (int at = 0; warp_first + at < io.n_kv_heads; at += teams) {
       const int h = first + at;
       const bool mine = some && h < io.n_kv_heads;
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid
       if (BITS == 16) {
         if (is_k) {
           float y[8];
-          turned(raw, t, io.k_norm != nullptr, y, nullptr);
+          turned(raw, t, io.k_norm != nullptr, y);
           raw = pack8<T>(y);
         }
         if (mine)
@@ -328,15 +334,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid
       const float unit = pow2(-e);
       float z[8];
       uint2 code;
-      if (is_k) {
-        float off;
-        turned(raw, t, io.k_norm != nullptr, z, &off);
-        off *= unit;
+      if (is_k) turned(raw, t, io.k_norm != nullptr, z);
+      else unpack8<T>(raw, z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] *= unit;
+      for (int i = 0; i < 8; ++i) z[i] *= unit;
+      const float top = largest(z);
+      if (is_k && (P.rot || io.k_norm)) {
         bool near = false;
-        if (P.rot || io.k_norm) code = quantise<true>(z, off, &near);
-        else code = quantise<false>(z, 0.f, nullptr);
+        const float other = LAYOUT == MK_ROPE_HALF ? __shfl_sync(0xffffffffu, top, from, team) : top;
+        code = quantise<true>(z, top, 0x1p-20f * (top + other), &near);
         // groups near a border, one after the other (about one row of 40 has one)
         uint32_t todo = __ballot_sync(0xffffffffu, near && mine && !(l & 1));
         while (todo) {
@@ -350,10 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid
           if (mine_too == 1) code = make_uint2(x.y, x.z);
         }
       } else {
-        unpack8<T>(raw, z);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] *= unit;
-        code = quantise<false>(z, 0.f, nullptr);
+        code = quantise<false>(z, top, 0.f, nullptr);
       }
       if (!mine) continue;
       const int64_t to = kvq_row(io.kvq, P.page_shift, slot, h);
