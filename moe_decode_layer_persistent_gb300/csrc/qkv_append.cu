@@ -24,6 +24,7 @@ struct AppendParams {
   mk_qkv_append_io io;
   int32_t d, rot;     // rot 0: no rotation
   int32_t team;       // lanes per head: the power of two from d / 8 on
+  int32_t team_shift;
   int32_t page_shift;
   float m, by_d;  // by_d: 1 / d
   double m64;
@@ -223,8 +224,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid
   // of the row's pairs, and behind them those of values that pass: cosine 1, sine 0
   __shared__ __align__(16) float cosines[128 + 8], sines[128 + 8];
   const int d = P.d, team = P.team;
-  const int l = threadIdx.x & (team - 1), first = threadIdx.x / team, teams = THREADS / team;
-  const int warp_first = (threadIdx.x & ~31) / team;
+  const int l = threadIdx.x & (team - 1), first = threadIdx.x >> P.team_shift, teams = THREADS >> P.team_shift;
+  const int warp_first = (threadIdx.x & ~31) >> P.team_shift;
   const bool some = l * 8 < d;
   const int parts = gridDim.y == 3 ? 1 << blockIdx.y : 7;
   // lane of the partners, and where this thread's pairs lie
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid
 
   // The normed and rotated values of a head.  For a cache in 4 bits: they are off by
   // the angle's and the sine's rounding (2^-23.4 of the pair), those of the brackets
-  // and products (3 x 2^-24) and of r (2^-21.7 of the value), together less than 2^-20.5
+  // and products (3 x 2^-24) and of r (2^-21.4 of the value), together less than 2^-20.5
   // (|n_a| + |n_b|) m, which is at most sqrt 2 (|y_a| + |y_b|).
   auto turned = [&](const uint4& raw, const Turn& t, bool norm, float (&y)[8]) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -248,8 +249,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid
     if (norm) {
       const float2 ss = add2(fma2(x[1], x[1], mul2(x[0], x[0])), fma2(x[3], x[3], mul2(x[2], x[2])));
       float sum = ss.x + ss.y;
-      for (int o = team / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      r = __frsqrt_rn(sum * P.by_d + io.eps);
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+        if (o < team) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      r = rsqrtf(sum * P.by_d + io.eps);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -524,6 +527,7 @@ mk_status mk_qkv_append(const mk_rope* rope, const mk_qkv_append_io* io, void* s
   P.team = 1;
   while (P.team * 8 < d) P.team *= 2;
   if (io->bits == 4) P.team = std::max(P.team, 2);
+  P.team_shift = __builtin_ctz(static_cast<uint32_t>(P.team));
   P.page_shift = io->bits == 4 && io->n_kv_heads ? __builtin_ctz(static_cast<uint32_t>(io->kvq.page_size)) : 0;
   P.m = rope ? rope->m : 1.f;
   P.m64 = rope ? rope->m64 : 1.0;
