@@ -742,6 +742,8 @@ mk_status mk_kvq_attn(const mk_kvq_attn_io* io, void* workspace, int64_t workspa
     return MK_OK;
   }
   P.io = *io;
+  if (!c.n_pages)  // (a pool without pages is never read)
+    P.io.kvq.k_codes = P.io.kvq.v_codes = P.io.kvq.k_scales = P.io.kvq.v_scales = const_cast<void*>(io->q);
   P.scale_log2 = (io->scale != 0.f ? io->scale : 1.f / std::sqrt(static_cast<float>(d))) * (8.f * 1.4426950408889634f);
   P.group = io->n_q_heads / c.n_kv_heads;
   P.by_group = make_divisor(P.group);

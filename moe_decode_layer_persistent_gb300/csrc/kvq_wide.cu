@@ -53,7 +53,7 @@ __host__ __device__ constexpr uint32_t idesc_fp16(int N, bool b_along_n) {
 
 // Bounded waits of whole warps: false once any wait of the CTA has run out.
 template <int D>
-MK_DEV bool wait_bar(const KvqParams& P, WideSmem<D>& S, uint64_t* bar, uint32_t parity) {
+MK_DEV bool wait_warp(const KvqParams& P, WideSmem<D>& S, uint64_t* bar, uint32_t parity) {
   bool ok = mbar_try_wait(bar, parity);
   if (!ok) {
     const uint64_t t0 = globaltimer();
@@ -204,7 +204,7 @@ MK_DEV void convert(const KvqParams& P, WideSmem<D>& S, Walk walk, int w) {
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         uint64_t* empty = kv ? &S.v_empty[buf] : &S.k_empty[buf];
-        if (done >= 2 && !wait_bar(P, S, empty, ((done >> 1) - 1) & 1)) {
+        if (done >= 2 && !wait_warp(P, S, empty, ((done >> 1) - 1) & 1)) {
           cp_async_wait<0>();
           return;
         }
@@ -246,7 +246,7 @@ MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   // O += P V of a tile
   auto pv = [&](int at, bool first) {
     const int buf = at & 1;
-    if (!wait_bar(P, S, &S.v_full[buf], (at >> 1) & 1) || !wait_bar(P, S, &S.p_full[buf], (at >> 1) & 1)) return false;
+    if (!wait_warp(P, S, &S.v_full[buf], (at >> 1) & 1) || !wait_warp(P, S, &S.p_full[buf], (at >> 1) & 1)) return false;
     tc_fence_after();
     if (elect_one()) {
       const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(S.v[buf]), kKeys * 128);
@@ -262,10 +262,10 @@ MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   while (walk.next(P, it)) {
     const int n = it.tile_end - it.tile;
     if (n <= 0) continue;
-    if (!wait_bar(P, S, &S.q_full, items++ & 1)) return false;
+    if (!wait_warp(P, S, &S.q_full, items++ & 1)) return false;
     for (int t = 0; t < n; ++t, ++done) {
       const int buf = done & 1;
-      if (!wait_bar(P, S, &S.k_full[buf], (done >> 1) & 1)) return false;
+      if (!wait_warp(P, S, &S.k_full[buf], (done >> 1) & 1)) return false;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t kd = sdesc_kmajor_sw128(smem_u32(S.k[buf]));
@@ -351,6 +351,7 @@ MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r) {
   fence_proxy_async_smem();
   __syncwarp();
   if (lane_id() == 0) mbar_arrive(&S.q_full);
+  __syncwarp();
 }
 
 template <class T, int D>
@@ -368,7 +369,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
     float ref = kNoRef, l = 0.f;
     for (int t = 0; t < n; ++t, ++done) {
       const int buf = done & 1, k0 = (r.it.tile + t) * kKeys;
-      if (!wait_bar(P, S, &S.s_full[buf], (done >> 1) & 1)) return;
+      if (!wait_warp(P, S, &S.s_full[buf], (done >> 1) & 1)) return;
       tc_fence_after();
       const uint32_t ts = lanes + buf * 128;
       if (warp_valid && r.it.folded && (t & 1) != warp >> 1) {
@@ -425,7 +426,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
             ref = next;
             if (t && __any_sync(0xffffffffu, old != 1.f)) {
               // (the tile before is in O when its V is free)
-              if (!wait_bar(P, S, &S.v_empty[(done - 1) & 1], ((done - 1) >> 1) & 1)) return;
+              if (!wait_warp(P, S, &S.v_empty[(done - 1) & 1], ((done - 1) >> 1) & 1)) return;
               tc_fence_after();
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
@@ -466,6 +467,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.p_full[buf]);
+      __syncwarp();
     }
 
     // The next item's Q goes its way before this one's results: Q's last products, the
@@ -474,7 +476,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
     more = walk.next(P, r.it);
     if (more) take_row<T, D>(P, S, r);
     if (n > 0) {
-      if (!wait_bar(P, S, &S.v_empty[(done - 1) & 1], ((done - 1) >> 1) & 1)) return;
+      if (!wait_warp(P, S, &S.v_empty[(done - 1) & 1], ((done - 1) >> 1) & 1)) return;
       tc_fence_after();
     }
     if (!warp_valid) continue;

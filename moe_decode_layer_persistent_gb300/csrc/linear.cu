@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (half == 0) mbar_arrive(&B.acc_empty[buf]);
         else arrive_at(address_in(&B.acc_empty[buf], leader));
       }
+      __syncwarp();
     }
   }
   if (P.split > 1) {
@@ -495,6 +496,9 @@ mk_status launch(const LinearParams& P, const CUtensorMap& w, const CUtensorMap&
   lc.blockDim = dim3(kThreads);
   // (a split tile's sums lie where the stages were)
   lc.dynamicSmemBytes = std::max(P.stages * (kFeat + P.cols / kCtas) * 128, P.split > 1 ? P.cols * kFeat * 4 : 0) + 1024;
+  // (a pair takes tensor memory on two SMs: no two of them on one, of which each might
+  // wait for what the other holds)
+  if (PAIR) lc.dynamicSmemBytes = std::max<size_t>(lc.dynamicSmemBytes, 120 * 1024);
   MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_linear<T, PAIR>, P, w, x));
   return MK_OK;
 }

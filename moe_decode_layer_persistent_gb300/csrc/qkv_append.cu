@@ -43,6 +43,14 @@ MK_DEV float2 cos_sin(uint64_t phase) {
   return make_float2((quarter + 1) & 2 ? -x : x, quarter & 2 ? -y : y);
 }
 
+// A parameter at a place of each thread's own: as constants, 32 places are read one by
+// one.
+MK_DEV uint64_t load_param(const uint64_t* p) {
+  uint64_t x;
+  asm("ld.u64 %0, [%1];" : "=l"(x) : "l"(p));
+  return x;
+}
+
 template <class T>
 MK_DEV void unpack8(const uint4& raw, float (&x)[8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -282,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid
     for (int u = 0; u < kAhead; ++u)
       if (some && first + u * teams < io.n_q_heads) raw4[u] = __ldcs(reinterpret_cast<const uint4*>(q + (first + u * teams) * d));
   for (int i = threadIdx.x; i < P.rot / 2 && (parts & 3); i += THREADS) {
-    const float2 c = cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[i]);
+    const float2 c = cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos)) * load_param(&P.turns[i]));
     cosines[i] = c.x * P.m;
     sines[i] = c.y * P.m;
   }

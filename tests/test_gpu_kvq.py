@@ -508,6 +508,103 @@ def test_attn_on_streams_and_in_graphs(cuda_lib):
         del hide
 
 
+def test_attn_without_pages(cuda_lib):
+    """A table without columns, and a pool without pages, which reads as zeros."""
+    a = make_attn(np.random.default_rng(14), [0, 0], [1, 9], 8, 2, 128, "bf16", 16)
+    a["table"] = np.zeros((2, 0), int)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+    for new in (1, 9):
+        a = make_attn(np.random.default_rng(15), [40, 200], [1, new], 8, 2, 128, "bf16", 16)
+        a["pools"] = [p[:0] for p in a["pools"]]
+        call_attn(cuda_lib, a)
+        torch.cuda.synchronize()
+        assert bool((a["out"][:a["n"]] == 0).all())
+        want = np.log([40.0] + [200.0 - new + i + 1 for i in range(new)])
+        assert np.abs(np64(a["lse"])[:a["n"]] - want[:, None]).max() < 1e-5
+
+
+def test_attn_many_requests(cuda_lib):
+    """More requests than a CTA has threads, several per thread; rows for either kernel."""
+    rng = np.random.default_rng(16)
+    for news in ([int(i % 7 == 0) for i in range(3000)], [20 * int(i % 150 == 3) for i in range(1200)]):
+        lens = [int(n + rng.integers(0, 60)) if n else int(rng.integers(0, 60)) for n in news]
+        a = make_attn(rng, lens, news, 4, 1, 64, "fp16", 16)
+        call_attn(cuda_lib, a)
+        check_attn(cuda_lib, a)
+
+
+def far_pools(d, heads, page):
+    """Pools whose codes pass 4 GB, their last pages' numbers."""
+    pages = (1 << 32) // (heads * page * d // 2) + 40
+    big = [torch.empty(pages, heads, page, w, dtype=torch.uint8, device="cuda") for w in (d // 2, d // 16) * 2]
+    return big, pages
+
+
+@pytest.mark.parametrize("new", [1, 12])
+def test_attn_pages_beyond_four_gigabytes(cuda_lib, new):
+    a = make_attn(np.random.default_rng(17), [700, 333], [new, 1], 32, 8, 128, "bf16", 128)
+    big, pages = far_pools(128, 8, 128)
+    small = a["pools"][0].shape[0]
+    for b, p in zip(big, a["pools"]):
+        b[pages - small:] = torch.from_numpy(p).cuda()
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+    want, lse = a["out"].clone(), a["lse"].clone()
+    table = a["keep"][2] + (pages - small)
+    kvq = cuda_lib.make_kvq_cache(*big, *a["dev"][4:])
+    io = cuda_lib.make_kvq_attn_io(a["q"], kvq, a["out"], a["keep"][0], a["keep"][1], table, lse=a["lse"])
+    a["whole"].fill_(CANARY)
+    cuda_lib.mk_kvq_attn(io, a["workspace"])
+    torch.cuda.synchronize()
+    assert torch.equal(a["out"], want) and torch.equal(a["lse"], lse)
+
+
+def test_append_and_read_beyond_four_gigabytes(cuda_lib):
+    rng = np.random.default_rng(18)
+    big, pages = far_pools(128, 8, 64)
+    kvq = cuda_lib.make_kvq_cache(*big)
+    k0, k = rounded(rng, (5, 8, 128), "bf16")
+    v0, v = rounded(rng, (5, 8, 128), "bf16")
+    slots = dev([pages * 64 - 1, pages * 64 - 70, 3, pages * 64, pages * 32 + 17], torch.int64)
+    cuda_lib.mk_qkv_append(None, cuda_lib.make_qkv_append_io(None, None, k, v, None, slots, kvq=kvq))
+    out = [torch.empty(5, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    cuda_lib.mk_kvq_read(cuda_lib.make_kvq_read_io(kvq, slots, *out))
+    for x, got in ((k0, out[0]), (v0, out[1])):
+        want = ok.decode(*ok.encode(x))
+        want[3] = 0
+        assert np.array_equal(np64(got), want)
+
+
+def test_append_captured_and_replayed(cuda_lib):
+    """A captured call reads its tensors when it is replayed."""
+    rng = np.random.default_rng(19)
+    n, hq, hk, d = 40, 8, 2, 64
+    pools = pool(rng, 4, hk, 16, d) + pool(rng, 4, hk, 16, d)
+    kvq = cuda_lib.make_kvq_cache(*pools)
+    _, qkv = rounded(rng, (n, hq + 2 * hk, d), "bf16")
+    positions, slots = dev(np.arange(n)), dev(rng.permutation(64)[:n], torch.int64)
+    q_out = torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda")
+    rope = cuda_lib.mk_rope_create(cuda_lib.make_rope_config(d))
+    io = cuda_lib.make_qkv_append_io(qkv[:, :hq], q_out, qkv[:, hq:hq + hk], qkv[:, hq + hk:], positions, slots, kvq=kvq)
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        cuda_lib.mk_qkv_append(rope, io, torch.cuda.current_stream())
+    x, again = rounded(rng, (n, hq + 2 * hk, d), "bf16")
+    qkv.copy_(again)
+    positions += 1000
+    g.replay()
+    torch.cuda.synchronize()
+    f, m = ob.rope_frequencies(d)
+    y, _ = ok.norm_rope(x[:, hq:hq + hk], None, 0, np.arange(n) + 1000, d, "half", f, m)
+    codes, scales = ok.encode(y)
+    got = [p.transpose(1, 2).reshape(64, hk, -1)[slots].cpu().numpy() for p in pools[:2]]
+    cuda_lib.mk_rope_destroy(rope)
+    assert np.array_equal(got[0], codes) and np.array_equal(got[1], scales)
+
+
 # ----------------------------------------------------------------- linear
 
 def check_linear(mk, rng, m, k, n, dtype, bias=False, act="none", residual=False, in_place=False, gap=8, stream=None,
@@ -573,6 +670,58 @@ def test_linear_takes_infinities_and_nan_as_they_come(cuda_lib):
         torch.cuda.synchronize()
         assert bool(torch.isinf(out[3]).all()) and bool(torch.isnan(out[4]).all()) and bool((out[0] == 0).all())
         assert bool((out[7] > 1.7).all()) and bool(torch.isfinite(out[5:]).all())
+
+
+def test_linear_on_streams_and_in_graphs(cuda_lib):
+    """Calls of every kind side by side, then captured and replayed on other inputs."""
+    rng = np.random.default_rng(40)
+    calls = []
+    for m, k, n in ((3, 1024, 256), (300, 512, 700), (2100, 64, 2600), (40, 128, 24000)):
+        x0, x = rounded(rng, (m, k), "bf16")
+        w0, w = rounded(rng, (n, k), "bf16", k ** -0.5)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+        io = cuda_lib.make_linear_io(x, w, out, act="silu")
+        ws = torch.empty(cuda_lib.mk_linear_workspace(io), dtype=torch.uint8, device="cuda")
+        calls.append((x0, x, w0, w, out, io, ws))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(3):
+        for c, s in zip(calls, streams):
+            cuda_lib.mk_linear(c[5], c[6], s)
+    torch.cuda.synchronize()
+
+    def check():
+        for x0, _, w0, _, out, _, ws in calls:
+            assert cuda_lib.mk_linear_status(ws) == 0
+            want, s = ok.linear(x0, w0, act="silu")
+            k = x0.shape[1]
+            tol = 1.13 * s * (k / 16 + 64) * 2 * V + 2.0 ** -20 * (1 + np.abs(want)) + U["bf16"] * np.abs(want) + TINY["bf16"]
+            assert np.all(np.abs(np64(out) - want) <= tol)
+
+    check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for c in calls:
+            cuda_lib.mk_linear(c[5], c[6], torch.cuda.current_stream())
+    for i, c in enumerate(calls):
+        x0, x = rounded(rng, c[0].shape, "bf16")
+        c[1].copy_(x)
+        calls[i] = (x0,) + c[1:]
+    for c in calls:
+        c[4].fill_(CANARY)
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    check()
+
+
+def test_linear_without_rows(cuda_lib):
+    x, w = (torch.zeros(n, 64, dtype=torch.bfloat16, device="cuda") for n in (0, 5))
+    io = cuda_lib.make_linear_io(x, w, torch.zeros(0, 5, dtype=torch.bfloat16, device="cuda"))
+    ws = torch.full((cuda_lib.mk_linear_workspace(io),), 0xFF, dtype=torch.uint8, device="cuda")
+    cuda_lib.mk_linear(io, ws)
+    torch.cuda.synchronize()
+    assert cuda_lib.mk_linear_status(ws) == 0
 
 
 # ---------------------------------------------------------- all of them
