@@ -511,8 +511,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
 // every gridDim.x-th worker (most have none: a CTA for each takes 7 us longer): a row
 // per warp, or where there are many parts all warps one row after the other, the parts
 // shared out among them.
-constexpr int kJoinWarps = 8, kFewParts = 12;
-template <class T, int D, int R>
+constexpr int kFewParts = 12;
+template <class T, int D, int R, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_kvq_join(const __grid_constant__ KvqParams P) {
   constexpr int V = D / 32;
   __shared__ float sum_o[kJoinWarps][D];
@@ -641,9 +641,14 @@ mk_status launch(const KvqParams& P, int device, int sms, cudaStream_t s) {
   const int64_t items = (static_cast<int64_t>(P.io.n_rows) * P.group / R + P.io.n_requests) * P.io.kvq.n_kv_heads;
   const bool few = items * 16 < P.workers;
   lc.gridDim = dim3(std::min(P.workers, (few ? 1 : 12) * sms), few ? R : R == kWideRows ? R / 8 : 1);
-  lc.blockDim = dim3(kJoinWarps * 32);
   lc.dynamicSmemBytes = 0;
-  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_join<T, D, R>, P));
+  if (few) {
+    lc.blockDim = dim3(8 * 32);
+    MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_join<T, D, R, 8>, P));
+  } else {
+    lc.blockDim = dim3(4 * 32);
+    MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_join<T, D, R, 4>, P));
+  }
   return MK_OK;
 }
 template <class T, int D>

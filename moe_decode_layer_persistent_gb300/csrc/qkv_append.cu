@@ -384,54 +384,46 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_append(const __grid
 struct ReadParams {
   mk_kvq_read_io io;
   int32_t page_shift;
-  int64_t groups;  // of 16 values, of K and of V
+  int32_t group;   // rows of a CTA's piece of work
+  int64_t pieces;  // groups of rows by kv heads
+  Divisor per;     // of 8 values in a head
 };
 
-// A thread per group, in the order of the pools where every slot is read.
+// A CTA per group of rows and kv head, a thread per 8 values: in the order of the pools
+// where every slot is read.
 template <class T>
 __global__ void __launch_bounds__(256) k_read(const __grid_constant__ ReadParams P) {
   const mk_kvq_read_io& io = P.io;
   const mk_kvq_cache& c = io.kvq;
-  const int per = c.head_dim / 16;
   const bool is_k = blockIdx.y == 0;
   T* out = static_cast<T*>(is_k ? io.k_out : io.v_out);
   if (!out) return;
   const uint8_t* codes = static_cast<const uint8_t*>(is_k ? c.k_codes : c.v_codes);
   const uint8_t* scales = static_cast<const uint8_t*>(is_k ? c.k_scales : c.v_scales);
   const int32_t* exps = is_k ? c.k_exp : c.v_exp;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < P.groups; i += gridDim.x * 256ll) {
-    const int64_t r = i / per;
-    const int g = static_cast<int>(i - r * per);
-    int64_t row, slot;
-    int h;
-    if (io.slots) {
-      row = r / c.n_kv_heads;
-      h = static_cast<int>(r - row * c.n_kv_heads);
-      slot = io.slots[row];
-    } else {
-      const int64_t block = r >> P.page_shift, page = block / c.n_kv_heads;
-      h = static_cast<int>(block - page * c.n_kv_heads);
-      row = slot = (page << P.page_shift) + (r & (c.page_size - 1));
-      if (row >= io.n_rows) continue;
-    }
-    uint2 word = make_uint2(0x88888888u, 0x88888888u);
-    float s = 0.f;
-    if (slot >= 0 && slot < static_cast<int64_t>(c.n_pages) << P.page_shift) {
-      const int64_t at = kvq_row(c, P.page_shift, slot, h);
-      word = *reinterpret_cast<const uint2*>(codes + at * (c.head_dim / 2) + g * 8);
-      s = e4m3_to_float(scales[at * per + g]) * pow2(exps ? clamp_exp(exps[h]) : 0);
-    }
-    uint4 y[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
+  const int64_t slots = static_cast<int64_t>(c.n_pages) << P.page_shift;
+  for (int64_t piece = blockIdx.x; piece < P.pieces; piece += gridDim.x) {
+    const int64_t row0 = piece / c.n_kv_heads * P.group;
+    const int h = static_cast<int>(piece % c.n_kv_heads);
+    const float unit = pow2(exps ? clamp_exp(exps[h]) : 0);
+    for (uint32_t i = threadIdx.x; i < P.group * P.per.d; i += 256) {
+      const uint32_t r = quotient(i, P.per), g = i - r * P.per.d;
+      const int64_t row = row0 + r;
+      const bool there = row < io.n_rows;
+      const int64_t slot = !there ? -1 : io.slots ? io.slots[row] : row;
+      uint32_t word = 0x88888888u;
+      float s = 0.f;
+      if (slot >= 0 && slot < slots) {
+        const int64_t at = kvq_row(c, P.page_shift, slot, h);
+        word = *reinterpret_cast<const uint32_t*>(codes + at * (c.head_dim / 2) + g * 4);
+        s = e4m3_to_float(scales[at * (c.head_dim / 16) + g / 2]) * unit;
+      }
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = (static_cast<int>(((k ? word.y : word.x) >> (4 * j)) & 15u) - 8) * s;
-      y[k] = pack8<T>(v);
+      for (int j = 0; j < 8; ++j)  // (2^23 + n, less 2^23 + 8)
+        v[j] = (__uint_as_float(0x4B000000u | (word >> (4 * j) & 15u)) - 8388616.f) * s;
+      if (there) *reinterpret_cast<uint4*>(out + (row * c.n_kv_heads + h) * c.head_dim + g * 8) = pack8<T>(v);
     }
-    uint4* to = reinterpret_cast<uint4*>(out + (row * c.n_kv_heads + h) * c.head_dim + g * 16);
-    to[0] = y[0];
-    to[1] = y[1];
   }
 }
 
@@ -574,10 +566,10 @@ mk_status mk_kvq_read(const mk_kvq_read_io* io, void* stream) {
   ReadParams P;
   P.io = *io;
   P.page_shift = __builtin_ctz(static_cast<uint32_t>(c.page_size));
-  // (every slot: whole pages, of which the last may stand out)
-  const int64_t r = io->slots ? n : (n + c.page_size - 1) / c.page_size * c.page_size;
-  P.groups = r * c.n_kv_heads * (c.head_dim / 16);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((P.groups + 255) / 256, 16ll * sms)), 2);
+  P.group = std::min(64, c.page_size);
+  P.pieces = (n + P.group - 1) / P.group * c.n_kv_heads;
+  P.per = make_divisor(static_cast<uint32_t>(c.head_dim / 8));
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(P.pieces, 16ll * sms)), 2);
   if (io->dtype == MK_BF16) k_read<__nv_bfloat16><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(P);
   else k_read<__half><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(P);
   MK_CUDA_TRY(cudaGetLastError());
