@@ -430,8 +430,14 @@ __global__ void __launch_bounds__(256) k_read(const __grid_constant__ ReadParams
 template <class T, int LAYOUT, int BITS>
 void launch_append(const AppendParams& P, int sms, cudaStream_t s) {
   const unsigned n = static_cast<unsigned>(P.io.n_rows);
+  // Few rows: many threads for each, with q, k and v apart.  Many: a warp for each, as
+  // what a row's threads wait for in turn is hidden by other rows only, and a warp does
+  // least of what is the same for all heads (with the values read back, 32 + 2 x 8 heads
+  // of 128 into 4 bits: 8192 rows 67 us, with 64 threads for each part 68, with 128 for a
+  // row 75; 1024 rows 29 and 18 us).
   if (P.io.n_rows < 2 * sms) k_append<T, LAYOUT, BITS, 256><<<dim3(n, 3), 256, 0, s>>>(P);
-  else k_append<T, LAYOUT, BITS, 128><<<n, 128, 0, s>>>(P);
+  else if (P.io.n_rows < 24 * sms) k_append<T, LAYOUT, BITS, 64><<<dim3(n, 3), 64, 0, s>>>(P);
+  else k_append<T, LAYOUT, BITS, 32><<<n, 32, 0, s>>>(P);
 }
 template <class T>
 void launch_append(const AppendParams& P, bool half, int sms, cudaStream_t s) {

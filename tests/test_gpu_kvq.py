@@ -173,8 +173,10 @@ def test_append_head_of_eight(cuda_lib):
 def test_append_many_codes(cuda_lib):
     """Codes of a million values, some hundred of which lie near a border in 32 bits."""
     rng = np.random.default_rng(3)
-    check_append(cuda_lib, rng, 1000, 1, 8, 128, 128, "half", "bf16", rng.integers(0, 1 << 20, 1000), 4,
-                 scaling="parts", factor=8.0, orig_ctx=8192)
+    for n, layout in ((1000, "half"), (4100, "interleaved")):   # rows on CTAs of 64 threads and of a warp
+        check_append(cuda_lib, rng, n, 5, 3, 128, 128, layout, "bf16", rng.integers(0, 1 << 20, n), 4, scaling="parts",
+                     factor=8.0, orig_ctx=8192)
+    check_append(cuda_lib, rng, 4100, 33, 1, 64, 32, "half", "fp16", rng.integers(0, 1 << 20, 4100), 16)
 
 
 def test_append_ties_infinities_and_nan(cuda_lib):
