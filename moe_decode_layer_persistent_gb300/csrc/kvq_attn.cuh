@@ -21,8 +21,8 @@ constexpr float kNoRef = -1e30f;
 // 4, 6 and 10.
 constexpr int kLead = 3, kWideLead = 7;
 
-// An item that is joined, as the worker with its first key tile says: one whose
-// stretches lie in several workers, or whose rows a worker holds twice.
+// An item whose stretches lie in several workers, as the one with its first key tile
+// says.
 struct Split {
   int32_t parts;     // 0: none
   int32_t folded;    // row r lies in rows r and r + kWideRows / 2 of each part

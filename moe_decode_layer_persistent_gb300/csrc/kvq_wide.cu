@@ -39,7 +39,7 @@ struct alignas(1024) WideSmem {
   static constexpr int kCodes = 16 * D / 2, kScales = 16 * D / 16, kStage = 2 * (kCodes + kScales);
   uint8_t q[kTile], k[2][kTile], v[2][kTile];
   uint8_t raw[kConvert][kStages][kStage];  // of each 16 keys: K's codes, V's, K's scales, V's
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], q_full, drained;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], q_full, halves, drained;
   int64_t sum[kThreads / 32];
   int64_t first_at;
   int32_t first;
@@ -79,8 +79,8 @@ struct Item {
   int32_t parts;                                // workers that share it
   bool starts;                                  // this one has its first key tile
   // No more than half of the tile's rows: they are there twice, and the first half of
-  // the threads takes the even key tiles, the second the odd ones.  (The other half's
-  // weights are zeros.)  The weights of a tile are otherwise what takes longest.
+  // the threads takes the even key tiles, the second the odd ones (the other half's
+  // weights are zeros), so that the weights of two tiles are made at the same time.
   bool folded;
 };
 struct Walk {
@@ -359,7 +359,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   const mk_kvq_attn_io& io = P.io;
   const int lane = lane_id(), warp = threadIdx.x / 32, row = threadIdx.x;
   const uint32_t lanes = S.tmem + (static_cast<uint32_t>(warp * 32) << 16), to = lanes + 256;
-  int done = 0;
+  int done = 0, joined = 0;
   Row r;
   bool more = walk.next(P, r.it);
   if (more) take_row<T, D>(P, S, r);
@@ -479,47 +479,78 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
       if (!wait_warp(P, S, &S.v_empty[(done - 1) & 1], ((done - 1) >> 1) & 1)) return;
       tc_fence_after();
     }
-    if (!warp_valid) continue;
+    // An item that this CTA has whole is written from here.  If it is folded, the second
+    // half of the threads leaves its results in the CTA's own place of the workspace,
+    // where the first half takes them (nothing else is there: a part of a later item is
+    // left there only after this).
+    const bool whole = mine.it.parts == 1, twice = whole && mine.it.folded && n > 0, second = twice && warp >= 2;
     const float unit_v = 8.f * pow2(io.kvq.v_exp ? clamp_exp(io.kvq.v_exp[mine.it.h]) : 0);
-    const int64_t part = 2ll * blockIdx.x + mine.it.starts;
-    const bool whole = mine.it.parts == 1 && !mine.it.folded;
-    const float inv = whole ? (l != 0.f ? unit_v / l : 0.f) : unit_v;
-#pragma unroll 1
-    for (int q = 0; q < D / 32; ++q) {
-      float o[32];
-      if (n > 0) {
-        tmem_ld32(to + 32 * q, o);
-        tmem_ld_wait();
-      } else {
-#pragma unroll
-        for (int x = 0; x < 32; ++x) o[x] = 0.f;
-      }
+    const int64_t part = (2ll * blockIdx.x + mine.it.starts) * kRows;
+    float f1 = 1.f, f2 = 0.f;  // what this half's and the other one's O are multiplied with
+    if (twice && !second) {
+      if (!wait_warp(P, S, &S.halves, joined++ & 1)) return;
       if (mine.valid) {
-        // eight columns are the dimensions 0 4 1 5 2 6 3 7
-        if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(io.out) + mine.at * io.out_stride + mine.hq * D + 32 * q);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float* y = o + 8 * x;
-            dst[x] = make_uint4(Pack<T>::put(y[0] * inv, y[2] * inv), Pack<T>::put(y[4] * inv, y[6] * inv),
-                                Pack<T>::put(y[1] * inv, y[3] * inv), Pack<T>::put(y[5] * inv, y[7] * inv));
-          }
+        const float2 other = P.stat[part + row + kRows / 2];
+        const float top = fmaxf(ref, other.x);
+        f1 = exp2_approx(ref - top);
+        f2 = exp2_approx(other.x - top);
+        l = l * f1 + other.y * f2;
+        ref = top;
+      }
+    }
+    if (whole && !second) {
+      const float inv = l != 0.f ? unit_v / l : 0.f;
+      f1 *= inv;
+      f2 = l != 0.f ? f2 / l : 0.f;  // (the other half's are in the values' units)
+    } else {
+      f1 = unit_v;
+    }
+    if (warp_valid && !(whole && mine.it.folded && n <= 0 && warp >= 2)) {
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        float o[32];
+        if (n > 0) {
+          tmem_ld32(to + 32 * q, o);
+          tmem_ld_wait();
         } else {
-          float4* dst = reinterpret_cast<float4*>(P.o + (part * kRows + row) * D + 32 * q);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float* y = o + 8 * x;
-            dst[2 * x] = make_float4(y[0] * inv, y[2] * inv, y[4] * inv, y[6] * inv);
-            dst[2 * x + 1] = make_float4(y[1] * inv, y[3] * inv, y[5] * inv, y[7] * inv);
+          for (int x = 0; x < 32; ++x) o[x] = 0.f;
+        }
+        if (mine.valid) {
+          // eight columns are the dimensions 0 4 1 5 2 6 3 7
+          float y[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) y[x] = o[(x & ~7) + (x & 3) * 2 + (x >> 2 & 1)] * f1;
+          if (whole && !second) {
+            if (twice) {
+              const float4* from = reinterpret_cast<const float4*>(P.o + (part + row + kRows / 2) * D + 32 * q);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const float4 v = from[x];
+                y[4 * x] += v.x * f2, y[4 * x + 1] += v.y * f2, y[4 * x + 2] += v.z * f2, y[4 * x + 3] += v.w * f2;
+              }
+            }
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(io.out) + mine.at * io.out_stride + mine.hq * D + 32 * q);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              dst[x] = make_uint4(Pack<T>::put(y[8 * x], y[8 * x + 1]), Pack<T>::put(y[8 * x + 2], y[8 * x + 3]),
+                                  Pack<T>::put(y[8 * x + 4], y[8 * x + 5]), Pack<T>::put(y[8 * x + 6], y[8 * x + 7]));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(P.o + (part + row) * D + 32 * q);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) dst[x] = make_float4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
           }
         }
+        __syncwarp();
       }
-      __syncwarp();
+      if (mine.valid && (!whole || second)) P.stat[part + row] = make_float2(ref, l);
+      if (mine.valid && whole && !second && io.lse)
+        io.lse[mine.at * io.n_q_heads + mine.hq] = l != 0.f ? (ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
     tc_fence_before();
-    if (mine.valid && !whole) P.stat[part * kRows + row] = make_float2(ref, l);
-    if (mine.valid && whole && io.lse)
-      io.lse[mine.at * io.n_q_heads + mine.hq] = l != 0.f ? (ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    __syncwarp();
+    if (second && lane == 0) mbar_arrive(&S.halves);
+    __syncwarp();
   }
 }
 
@@ -540,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant_
       mbar_init(&S.p_full[i], 4);
     }
     mbar_init(&S.q_full, 4);
+    mbar_init(&S.halves, 2);
     mbar_init(&S.drained, 1);
     S.abort = 0;
     fence_mbar_init();
@@ -613,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant_
         // an item to join
         Item it;
         while (walk.next(P, it)) {
-          if (it.starts && (it.parts > 1 || it.folded) && lane == 0)
+          if (it.starts && it.parts > 1 && lane == 0)
             P.split[blockIdx.x] = {it.parts, it.folded, it.cu, it.rows, it.first, it.h};
         }
       }

@@ -370,6 +370,31 @@ def test_attn(cuda_lib, name):
     check_attn(cuda_lib, a)
 
 
+@pytest.mark.parametrize("name,lens,news,hq,hk,d,dtype,page,more", [
+    # many key tiles per worker, items whole and in parts one after the other
+    ("one_token", [2000 - 13 * i for i in range(64)], [1] * 64, 8, 8, 64, "bf16", 64, {}),
+    ("one_token_128", [1900 - 41 * i for i in range(40)], [1] * 40, 32, 8, 128, "fp16", 128, {}),
+    ("two_tokens", [1500 - 17 * i for i in range(50)], [2 + i % 2 for i in range(50)], 20, 4, 64, "fp16", 32, {}),
+    ("folded_whole", [130 + (37 * i) % 300 for i in range(300)], [8] * 300, 4, 1, 64, "bf16", 16, {}),
+    ("folded_128", [150 + (37 * i) % 700 for i in range(120)], [5 + i % 9 for i in range(120)], 4, 1, 128, "bf16", 32,
+     dict(tree=True)),
+    ("folded_long", [3000, 2500, 2900, 700, 5, 3100], [24] * 4 + [5, 24], 8, 8, 128, "fp16", 64, {}),
+    ("folded_window", [1400 - 9 * i for i in range(40)], [17] * 40, 4, 2, 64, "bf16", 16, dict(window=600)),
+    ("tiles_of_80_rows", [700 - 11 * i for i in range(18)], [80] * 18, 4, 4, 64, "bf16", 32, {}),
+    ("tiles_of_128_rows", [900 - 7 * i for i in range(12)], [150] * 12, 2, 2, 128, "fp16", 64, {}),
+    ("mixed", [40 + (53 * i) % 900 for i in range(90)], [(1, 30, 2, 70)[i % 4] for i in range(90)], 4, 2, 64, "bf16", 16, {}),
+])
+def test_attn_many_tiles_per_worker(cuda_lib, name, lens, news, hq, hk, d, dtype, page, more):
+    a = make_attn(np.random.default_rng(len(name)), lens, news, hq, hk, d, dtype, page, **more)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+    first, lse = a["out"].clone(), a["lse"].clone()
+    for _ in range(3):
+        cuda_lib.mk_kvq_attn(a["io"], a["workspace"])
+    torch.cuda.synchronize()
+    assert torch.equal(a["out"], first) and torch.equal(a["lse"], lse)
+
+
 def test_attn_scale_and_no_lse(cuda_lib):
     a = make_attn(np.random.default_rng(1), [30, 109], [2, 1], 4, 2, 64, "bf16", 16, exps=False)
     call_attn(cuda_lib, a, scale=0.03125)
