@@ -266,6 +266,9 @@ MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
     for (int t = 0; t < n; ++t, ++done) {
       const int buf = done & 1;
       if (!wait_warp(P, S, &S.k_full[buf], (done >> 1) & 1)) return false;
+      // (its scores go over weights that the product two tiles back reads; products with
+      // other sums need not run in order)
+      if (done >= 2 && !wait_warp(P, S, &S.v_empty[buf], ((done >> 1) - 1) & 1)) return false;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t kd = sdesc_kmajor_sw128(smem_u32(S.k[buf]));
