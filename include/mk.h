@@ -587,8 +587,11 @@ typedef struct mk_kvq_cache {
  * could tell, the group is worked out again in 64 bits.  A group that holds a NaN
  * gets the scale NaN (0x7F) and the codes 8; infinities saturate.
  * A row whose slot is outside the pool writes nothing there; slots are distinct.
+ * mean x^2 + eps has to be a normal number in 32 bits (squares up to 3e38).
  * q_out may be q itself (same stride); any other overlap of inputs and outputs is
- * not allowed, k and v in the very cache rows that slots names (bits 16) apart. */
+ * not allowed, k and v in the very cache rows that slots names (bits 16) apart.
+ * q and q_out may be views of the same rows as k and v; any other tensor counts as
+ * the stretch from its first value to its last. */
 typedef struct mk_qkv_append_io {
   int32_t n_rows;            /* >= 0; with 0 every tensor of rows may be NULL      */
   int32_t n_q_heads;         /* 0 iff q is NULL; <= 4096                           */
@@ -654,7 +657,10 @@ mk_status mk_kvq_read(const mk_kvq_read_io* io, void* stream);
  * and out is rounded once.  Two calls on the same inputs give the same bits.
  * lens outside 0 .. max_pages * page_size and cu_rows outside 0 .. n_rows are
  * taken as the nearer end, and a page outside 0 .. n_pages-1 reads as zeros.  A
- * cu_rows that falls leaves out and lse undefined. */
+ * cu_rows that falls leaves out and lse undefined.  Scores up to 2^26 are held to.
+ * A page's codes (n_kv_heads * page_size * d / 2 bytes) are less than 2^31.  No
+ * output may overlap an input; a tensor of rows counts from its first value to its
+ * last, what lies between its rows included. */
 typedef struct mk_kvq_attn_io {
   int32_t n_requests;          /* B, 1 .. 65536                                   */
   int32_t n_rows;              /* rows of q, >= 0                                 */
@@ -696,7 +702,7 @@ mk_status mk_kvq_attn_status(const void* workspace);
  * summed in 32 bits and rounded once.  MK_ACT_SILU: y / (1 + e^-y);
  * MK_ACT_GELU: y (1 + erf(y / sqrt 2)) / 2; MK_ACT_GELU_TANH: y (1 + tanh(sqrt(2 / pi)
  * (y + 0.044715 y^3))) / 2.  residual may be out itself (same stride); any other
- * overlap of an input with out is not allowed.  Two calls on the same inputs give
+ * overlap of an input with out, counted as for mk_kvq_attn, is not allowed.  Two calls on the same inputs give
  * the same bits. */
 typedef enum { MK_ACT_NONE = 0, MK_ACT_SILU = 1, MK_ACT_GELU = 2, MK_ACT_GELU_TANH = 3 } mk_act;
 

@@ -39,7 +39,7 @@ struct alignas(1024) WideSmem {
   static constexpr int kCodes = 16 * D / 2, kScales = 16 * D / 16, kStage = 2 * (kCodes + kScales);
   uint8_t q[kTile], k[2][kTile], v[2][kTile];
   uint8_t raw[kConvert][kStages][kStage];  // of each 16 keys: K's codes, V's, K's scales, V's
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], q_full, halves, drained;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], q_full, halves, taken, drained;
   int64_t sum[kThreads / 32];
   int64_t first_at;
   int32_t first;
@@ -484,14 +484,15 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
     }
     // An item that this CTA has whole is written from here.  If it is folded, the second
     // half of the threads leaves its results in the CTA's own place of the workspace,
-    // where the first half takes them (nothing else is there: a part of a later item is
-    // left there only after this).
+    // where the first half takes them before the second writes there again.
     const bool whole = mine.it.parts == 1, twice = whole && mine.it.folded && n > 0, second = twice && warp >= 2;
     const float unit_v = 8.f * pow2(io.kvq.v_exp ? clamp_exp(io.kvq.v_exp[mine.it.h]) : 0);
     const int64_t part = (2ll * blockIdx.x + mine.it.starts) * kRows;
     float f1 = 1.f, f2 = 0.f;  // what this half's and the other one's O are multiplied with
+    if (warp >= 2 && joined && !wait_warp(P, S, &S.taken, (joined - 1) & 1)) return;
+    joined += twice;
     if (twice && !second) {
-      if (!wait_warp(P, S, &S.halves, joined++ & 1)) return;
+      if (!wait_warp(P, S, &S.halves, (joined - 1) & 1)) return;
       if (mine.valid) {
         const float2 other = P.stat[part + row + kRows / 2];
         const float top = fmaxf(ref, other.x);
@@ -552,7 +553,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
     }
     tc_fence_before();
     __syncwarp();
-    if (second && lane == 0) mbar_arrive(&S.halves);
+    if (twice && lane == 0) mbar_arrive(second ? &S.halves : &S.taken);
     __syncwarp();
   }
 }
@@ -575,6 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant_
     }
     mbar_init(&S.q_full, 4);
     mbar_init(&S.halves, 2);
+    mbar_init(&S.taken, 2);
     mbar_init(&S.drained, 1);
     S.abort = 0;
     fence_mbar_init();

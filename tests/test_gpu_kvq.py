@@ -437,6 +437,18 @@ def test_attn_window_of_rows_that_see_one_another(cuda_lib, window, dtype, d):
     check_attn(cuda_lib, a)
 
 
+@pytest.mark.parametrize("n", [160, 270, 400])
+def test_attn_parts_below_every_window(cuda_lib, n):
+    """The same with many requests: an item that a CTA has whole, its rows twice in the
+    tile, and behind it the first part of one that no row sees any key of."""
+    a = make_attn(np.random.default_rng(n), [128 * (2 + i % 3) + 203 for i in range(n)], [40] * n, 1, 1, 64, "bf16", 16,
+                  window=64, tree=True)
+    a["words"] = [(1 << 40) - 1] * (40 * n) + [0] * 2
+    hide_unseen(a)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+
+
 def test_attn_rising_scores(cuda_lib):
     """Scores that rise along the keys by far more than fp16 holds: the reference
     that weights are taken against moves all the time."""
