@@ -29,17 +29,20 @@ constexpr int kRows = kWideRows;
 constexpr int kConvert = 8;      // warps that convert: 16 keys of a tile each
 constexpr int kThreads = 512;    // four warpgroups: rows, two that convert, products
 constexpr int kStages = 3;       // tiles of a converting warp's ring
+constexpr int kValues = 3;       // tiles of V
 constexpr float kMost = 32768.f; // a row's sum of weights over a tile
 constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
 constexpr uint32_t kTimeout = 1;
+// columns of tensor memory: two tiles of scores and weights, O, Q
+constexpr uint32_t kOutAt = 256, kQAt = 384;
 
 template <int D>
 struct alignas(1024) WideSmem {
   static constexpr int kTile = kKeys * D * 2;
   static constexpr int kCodes = 16 * D / 2, kScales = 16 * D / 16, kStage = 2 * (kCodes + kScales);
-  uint8_t q[kTile], k[2][kTile], v[2][kTile];
+  uint8_t k[2][kTile], v[kValues][kTile];
   uint8_t raw[kConvert][kStages][kStage];  // of each 16 keys: K's codes, V's, K's scales, V's
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], q_full, halves, taken, drained;
+  uint64_t k_full[2], k_empty[2], v_full[kValues], v_empty[kValues], s_full[2], p_full[2], q_full, halves, taken, drained;
   int64_t sum[kThreads / 32];
   int64_t first_at;
   int32_t first;
@@ -197,14 +200,13 @@ MK_DEV void convert(const KvqParams& P, WideSmem<D>& S, Walk walk, int w) {
       __syncwarp();
       issue(stage_in);
       stage_in = after(stage_in);
-      const int buf = done & 1;
       const uint8_t* st = S.raw[w][stage];
       const int j = tile * kKeys + row;
       const bool seen = j >= it.klo && j < it.khi;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        uint64_t* empty = kv ? &S.v_empty[buf] : &S.k_empty[buf];
-        if (done >= 2 && !wait_warp(P, S, empty, ((done >> 1) - 1) & 1)) {
+        const int of = kv ? kValues : 2, buf = done % of, round = done / of;
+        if (round && !wait_warp(P, S, kv ? &S.v_empty[buf] : &S.k_empty[buf], (round - 1) & 1)) {
           cp_async_wait<0>();
           return;
         }
@@ -226,10 +228,14 @@ MK_DEV void convert(const KvqParams& P, WideSmem<D>& S, Walk walk, int w) {
             *reinterpret_cast<uint4*>(to + (unit >> 3) * (kKeys * 128) + (((unit & 7) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kv ? &S.v_full[buf] : &S.k_full[buf]);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&S.k_full[done & 1]);
+        mbar_arrive(&S.v_full[done % kValues]);
+      }
+      __syncwarp();
     }
     cp_async_wait<0>();
     __syncwarp();
@@ -240,20 +246,19 @@ MK_DEV void convert(const KvqParams& P, WideSmem<D>& S, Walk walk, int w) {
 template <int D>
 MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   constexpr uint32_t kIdS = idesc_fp16(kKeys, false), kIdO = idesc_fp16(D, true);
-  const uint32_t tmem = S.tmem, to = tmem + 256;
-  const uint64_t qd = sdesc_kmajor_sw128(smem_u32(S.q));
+  const uint32_t tmem = S.tmem, to = tmem + kOutAt, tq = tmem + kQAt;
   int done = 0, items = 0;
   // O += P V of a tile
   auto pv = [&](int at, bool first) {
-    const int buf = at & 1;
-    if (!wait_warp(P, S, &S.v_full[buf], (at >> 1) & 1) || !wait_warp(P, S, &S.p_full[buf], (at >> 1) & 1)) return false;
+    const int buf = at & 1, vb = at % kValues;
+    if (!wait_warp(P, S, &S.v_full[vb], (at / kValues) & 1) || !wait_warp(P, S, &S.p_full[buf], (at >> 1) & 1)) return false;
     tc_fence_after();
     if (elect_one()) {
-      const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(S.v[buf]), kKeys * 128);
+      const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(S.v[vb]), kKeys * 128);
 #pragma unroll
       for (int k = 0; k < kKeys / 16; ++k)
         mma_ts(to, tmem + buf * 128 + 8 * k, vd + k * (16 * 128 >> 4), kIdO, !first || k > 0);
-      mma_commit(&S.v_empty[buf]);
+      mma_commit(&S.v_empty[vb]);
     }
     __syncwarp();
     return true;
@@ -268,14 +273,14 @@ MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
       if (!wait_warp(P, S, &S.k_full[buf], (done >> 1) & 1)) return false;
       // (its scores go over weights that the product two tiles back reads; products with
       // other sums need not run in order)
-      if (done >= 2 && !wait_warp(P, S, &S.v_empty[buf], ((done >> 1) - 1) & 1)) return false;
+      if (done >= 2 && !wait_warp(P, S, &S.v_empty[(done - 2) % kValues], ((done - 2) / kValues) & 1)) return false;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t kd = sdesc_kmajor_sw128(smem_u32(S.k[buf]));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint64_t at = (k >> 2) * (kKeys * 128 >> 4) + (k & 3) * 2;
-          mma_bf16(tmem + buf * 128, qd + at, kd + at, kIdS, k);
+          mma_ts(tmem + buf * 128, tq + 8 * k, kd + at, kIdS, k);
         }
         mma_commit(&S.s_full[buf]);
         mma_commit(&S.k_empty[buf]);
@@ -299,7 +304,7 @@ struct Row {
   bool valid;
 };
 
-// Brings the row's Q into shared memory, in fp16 relative to its largest value, the
+// Brings the row's Q into tensor memory, in fp16 relative to its largest value, the
 // pairs in the order of the codes'.
 template <class T, int D>
 MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r) {
@@ -348,10 +353,13 @@ MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r) {
   r.c = fmaxf(r.c, FLT_MIN);  // (a masked score, -infinity, must not meet 0)
 #pragma unroll
   for (int j = 0; j < D / 8; ++j)
-    *reinterpret_cast<uint4*>(S.q + (j >> 3) * (kRows * 128) + row * 128 + (((j & 7) ^ (row & 7)) << 4)) =
-        make_uint4(__byte_perm(raw[j].x, raw[j].z, 0x5410), __byte_perm(raw[j].x, raw[j].z, 0x7632),
-                   __byte_perm(raw[j].y, raw[j].w, 0x5410), __byte_perm(raw[j].y, raw[j].w, 0x7632));
-  fence_proxy_async_smem();
+    raw[j] = make_uint4(__byte_perm(raw[j].x, raw[j].z, 0x5410), __byte_perm(raw[j].x, raw[j].z, 0x7632),
+                        __byte_perm(raw[j].y, raw[j].w, 0x5410), __byte_perm(raw[j].y, raw[j].w, 0x7632));
+  const uint32_t to = S.tmem + (static_cast<uint32_t>(row & ~31) << 16) + kQAt;
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) tmem_st32(to + 32 * j, reinterpret_cast<const uint32_t*>(raw + 8 * j));
+  tmem_st_wait();
+  tc_fence_before();
   __syncwarp();
   if (lane_id() == 0) mbar_arrive(&S.q_full);
   __syncwarp();
@@ -361,7 +369,7 @@ template <class T, int D>
 MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   const mk_kvq_attn_io& io = P.io;
   const int lane = lane_id(), warp = threadIdx.x / 32, row = threadIdx.x;
-  const uint32_t lanes = S.tmem + (static_cast<uint32_t>(warp * 32) << 16), to = lanes + 256;
+  const uint32_t lanes = S.tmem + (static_cast<uint32_t>(warp * 32) << 16), to = lanes + kOutAt;
   int done = 0, joined = 0;
   Row r;
   bool more = walk.next(P, r.it);
@@ -429,7 +437,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
             ref = next;
             if (t && __any_sync(0xffffffffu, old != 1.f)) {
               // (the tile before is in O when its V is free)
-              if (!wait_warp(P, S, &S.v_empty[(done - 1) & 1], ((done - 1) >> 1) & 1)) return;
+              if (!wait_warp(P, S, &S.v_empty[(done - 1) % kValues], ((done - 1) / kValues) & 1)) return;
               tc_fence_after();
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
@@ -479,7 +487,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
     more = walk.next(P, r.it);
     if (more) take_row<T, D>(P, S, r);
     if (n > 0) {
-      if (!wait_warp(P, S, &S.v_empty[(done - 1) & 1], ((done - 1) >> 1) & 1)) return;
+      if (!wait_warp(P, S, &S.v_empty[(done - 1) % kValues], ((done - 1) / kValues) & 1)) return;
       tc_fence_after();
     }
     // An item that this CTA has whole is written from here.  If it is folded, the second
@@ -568,11 +576,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant_
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.k_full[i], kConvert);
-      mbar_init(&S.v_full[i], kConvert);
       mbar_init(&S.k_empty[i], 1);
-      mbar_init(&S.v_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_full[i], 4);
+    }
+    for (int i = 0; i < kValues; ++i) {
+      mbar_init(&S.v_full[i], kConvert);
+      mbar_init(&S.v_empty[i], 1);
     }
     mbar_init(&S.q_full, 4);
     mbar_init(&S.halves, 2);
