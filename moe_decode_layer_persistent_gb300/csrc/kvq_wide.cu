@@ -11,9 +11,17 @@
 //   4 warps  keep a row per thread: they bring Q, turn scores into weights, and write
 //            the results;
 //   1 warp   (of a fourth warpgroup) issues the products, the scores of the next tile before P V.
-// Two buffers of K, of V and of S keep the three busy at the same time.  Key tiles of
-// all items lie on one line, of which each CTA (one per SM) takes an equal stretch;
+// Two tiles of K and of S and three of V keep them busy at the same time; Q, S, P and
+// O are in tensor memory (two tiles of S: with three the time was the same).  Key tiles
+// of all items lie on one line, of which each CTA (one per SM) takes an equal stretch;
 // k_kvq_join joins what lies in several.
+//
+// What bounds it: a key tile takes the converting warps about 2300 cycles (issue of the
+// copies 600, K and V 700 each, fence and hand-off 300), the chain from S by way of the
+// weights to P V two thirds of that and more, the tensor cores 1024.  16 requests of up
+// to 16 rows (32 heads over 8) and 16384 keys of d 128: 87 us, 157 MB, the tensor pipe
+// active 34 % of the time; on row tiles of 16 without tcgen05 143 us.
+// Copies by warps of their own (bulk or cp.async) take 110 us, twelve converting warps 93.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

@@ -11,6 +11,10 @@
 // their sums meet in distributed shared memory, where each CTA adds up a part of
 // the rows in the order of the ranks.  Many tiles: one CTA per SM works through
 // them, the tensor cores on the next tile while the last one's results leave.
+//
+// What bounds it: 4096 rows, 4096 -> 12288, SiLU: 217 to 223 us, 1.85 to 1.9 PFLOP/s, the tensor
+// cores.  64 rows, 4096 -> 6144: 15 us (50 MB of weights), half of it start, first trip
+// and join; 250 rows, 4096 -> 4096: 17.6 us, of which 6 go for what each SM takes in.
 #include <algorithm>
 #include <atomic>
 #include <climits>

@@ -8,6 +8,11 @@
 //   y_b = r (x_b (w_b m cos t) + x_a (w_a m sin t)).
 // A team of lanes holds a head, 8 values each, so that the brackets are the same
 // for every head of a row that a thread works on: they are made once per row.
+//
+// What bounds it: of 8192 rows (32 + 2 x 8 heads of 128, norms, into 4 bits) the
+// instructions, 4290 per row: 52 us for 177 MB, where HBM would take 26.  Few rows: the
+// launch, and groups near a border one after the other in 64 bits (64 rows: 4 us more
+// than into 16 bits).  Reading those rows' values back: 13 us.
 #include <algorithm>
 #include <climits>
 #include <math_constants.h>
