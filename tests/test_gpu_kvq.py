@@ -165,6 +165,19 @@ def test_append_variants(cuda_lib, bits, kw):
     check_append(cuda_lib, rng, 50, 8, 2, 128, dtype="bf16", positions=rng.integers(0, 1 << 20, 50), bits=bits, **kw)
 
 
+@pytest.mark.parametrize("layout,d,rot,scaling", [
+    ("half", 128, 32, "none"), ("half", 64, 64, "none"), ("interleaved", 128, 24, "linear"), ("interleaved", 80, 8, "none"),
+    ("half", 128, 16, "parts")])
+@pytest.mark.parametrize("n", [60, 1100, 4000])
+def test_append_groups_as_given(cuda_lib, layout, d, rot, scaling, n):
+    """Without norms: groups that the rotation leaves out, wholly or in part, and rows at
+    position 0, whose values have few bits and are often on borders."""
+    rng = np.random.default_rng(n + d)
+    positions = rng.integers(0, 3, n) * rng.integers(0, 1 << 17, n)
+    check_append(cuda_lib, rng, n, 2, 2, d, rot, layout, "bf16", positions, 4, norm=False, scaling=scaling,
+                 factor=1.0 if scaling == "none" else 4.0, orig_ctx=4096 if scaling == "parts" else 0)
+
+
 def test_append_head_of_eight(cuda_lib):
     rng = np.random.default_rng(2)
     check_append(cuda_lib, rng, 70, 5, 3, 8, 8, "interleaved", "bf16", rng.integers(0, 4000, 70), 16)
@@ -647,14 +660,14 @@ def test_append_captured_and_replayed(cuda_lib):
 # ----------------------------------------------------------------- linear
 
 def check_linear(mk, rng, m, k, n, dtype, bias=False, act="none", residual=False, in_place=False, gap=8, stream=None,
-                 by=1.0):
+                 by=1.0, pad=3):
     x0, x = rounded(rng, (m, k + gap), dtype, by)
     w0, w = rounded(rng, (n, k + gap), dtype, k ** -0.5)
     x[:, k:], w[:, k:] = float("nan"), float("nan")          # what lies between the rows is not read
     b0, b = rounded(rng, (n,), dtype) if bias else (None, None)
-    whole = torch.full((m + 1, n + 3), CANARY, dtype=TORCH[dtype], device="cuda")
+    whole = torch.full((m + 1, n + pad), CANARY, dtype=TORCH[dtype], device="cuda")
     out = whole[:m, :n]
-    r0, r = rounded(rng, (m, n + 5), dtype) if residual else (None, None)
+    r0, r = rounded(rng, (m, n + pad + 2 * (pad & 1)), dtype) if residual else (None, None)
     if residual:
         r0, r = r0[:, :n], r[:, :n]
         if in_place:
@@ -695,6 +708,16 @@ def test_linear(cuda_lib, dtype, m, k, n):
     dict(act="silu", by=100.0), dict(act="gelu_tanh", by=100.0)])
 def test_linear_variants(cuda_lib, m, k, n, kw):
     check_linear(cuda_lib, np.random.default_rng(9), m, k, n, "bf16", **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,k,n", [
+    (1, 8, 4), (5, 200, 76), (64, 2048, 640), (127, 64, 132), (250, 1024, 1036), (257, 8, 12), (600, 264, 300),
+    (1000, 512, 1500), (2101, 136, 2604), (90, 72, 23000)])
+@pytest.mark.parametrize("kw", [
+    dict(), dict(residual=True, bias=True, act="gelu"), dict(residual=True, in_place=True, act="silu")])
+def test_linear_outputs_in_fours(cuda_lib, dtype, m, k, n, kw):
+    check_linear(cuda_lib, np.random.default_rng(m + k + n), m, k, n, dtype, pad=4, **kw)
 
 
 def test_linear_takes_infinities_and_nan_as_they_come(cuda_lib):
