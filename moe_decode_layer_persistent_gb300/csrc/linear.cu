@@ -19,6 +19,7 @@
 #include <atomic>
 #include <climits>
 
+#include "attn_ptx.cuh"
 #include "batch.h"
 #include "rope.h"
 
@@ -65,11 +66,30 @@ MK_DEV void activate(float (&y)[N], int act) {
     for (int i = 0; i < N; ++i) y[i] = __fdividef(y[i], 1.f + __expf(-y[i]));
   } else if (act == MK_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = 0.5f * y[i] * (1.f + erff(y[i] * 0.7071067811865476f));
+    for (int i = 0; i < N; ++i) {
+      // y (1 + erf(y / sqrt 2)) / 2 = max(y, 0) - |y| erfc(x) / 2 with x = |y| / sqrt 2, and
+      // erfc(x) e^(x^2) / 2 as t times a polynomial in t = 1 / (1 + 0.45 x), fitted for the
+      // least relative error up to x = 9.6: 2^-21.7, with the rounding 2^-18.9 for y > -6.
+      // (2935 rows, 360 -> 10456: 59 us, with erff, whose ranges
+      // diverge, 72.)
+      const float a = fminf(fabsf(y[i]), 15.f), t = __fdividef(1.f, fmaf(a, 0.31819805f, 1.f));
+      float q = 0.033216566f;
+      q = fmaf(q, t, -0.119189195f);
+      q = fmaf(q, t, 0.10271385f);
+      q = fmaf(q, t, 0.021787712f);
+      q = fmaf(q, t, 0.09341932f);
+      q = fmaf(q, t, 0.11432297f);
+      q = fmaf(q, t, 0.12677133f);
+      q = fmaf(q, t, 0.1269576f);
+      const float tail = (y[i] < 0.f ? -y[i] : a) * (q * t * exp2_approx(a * a * -0.72134752f));
+      y[i] = (y[i] < 0.f ? 0.f : y[i]) - tail;
+    }
   } else if (act == MK_ACT_GELU_TANH) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      y[i] = 0.5f * y[i] * (1.f + tanhf(0.7978845608028654f * (y[i] + 0.044715f * y[i] * y[i] * y[i])));
+    for (int i = 0; i < N; ++i) {  // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+      const float u = 0.7978845608028654f * fmaf(0.044715f * y[i] * y[i], y[i], y[i]);
+      y[i] = __fdividef(y[i], 1.f + __expf(-2.f * u));
+    }
   }
 }
 
@@ -151,7 +171,9 @@ MK_DEV void free_columns(uint32_t at, uint32_t cols) {
   else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
 }
 MK_DEV void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  // (relaxed: tensor memory has been read, and the arrival need not wait for what the
+  // thread has stored elsewhere: 2935 rows, 360 -> 10456, 46.5 us without, 42.6 with)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 MK_DEV void cluster_sync() {
@@ -167,6 +189,8 @@ MK_DEV float4 load_cluster(uint32_t addr, uint32_t rank) {
                : "memory");
   return v;
 }
+
+MK_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Of a split tile: adds up the ranks' sums of rows c0 .. c1-1 (four outputs per
 // lane, a row per warp at a time, kRows rows on their way) and writes the results.
@@ -344,6 +368,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 16; ++i)
           to[i] = mine && col + i < rows ? res[static_cast<int64_t>(col + i) * io.residual_stride] : static_cast<T>(0.f);
       };
+      // (the next tile's on its way into L2, as the loads here keep few bytes in flight)
+      if (io.residual && P.split == 1) {
+        for (int to = n ? tile + step : tile; to <= tile + step && to < P.tiles; to += step) {
+          const int f = to / P.row_tiles * kTileFeat + half * kFeat, r = to % P.row_tiles * P.cols;
+          const char* from = static_cast<const char*>(io.residual) + (static_cast<int64_t>(r) * io.residual_stride + f) * 2;
+          const int bytes = min(kFeat, io.n_out - f) * 2, count = min(P.cols, io.n_rows - r);
+          for (int i = threadIdx.x - 64; i < 2 * count; i += kOutWarps * 32)
+            if ((i & 1) * 128 < bytes) prefetch_l2(from + (i >> 1) * io.residual_stride * 2 + (i & 1) * 128);
+        }
+      }
       fetch(col0, ahead[0]);
       fetch(col0 + 32, ahead[1]);
       ok = __all_sync(0xffffffffu, wait_bar(P, B, &B.acc_full[buf], (n >> 1) & 1));

@@ -720,6 +720,35 @@ def test_linear_outputs_in_fours(cuda_lib, dtype, m, k, n, kw):
     check_linear(cuda_lib, np.random.default_rng(m + k + n), m, k, n, dtype, pad=4, **kw)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_linear_activations_over_their_range(cuda_lib, act, dtype):
+    """Every value of the type from -40 to 40, one by one, by way of a row with a single 1.
+    Each function has an exponential 2^E whose E is off by three roundings of itself, and is
+    off by 2^-18.5 beside that; the oracle's 1 + erf and 1 + tanh are off by 2^-53, and what
+    lies below 2^-126 may be zero."""
+    import torch as T
+    bits = T.arange(0, 1 << 16, dtype=T.int32, device="cuda").to(T.int16)
+    y = bits.view(TORCH[dtype])
+    y = y[T.isfinite(y) & (y.float().abs() <= 40)]
+    y = y[: y.numel() // 8 * 8]
+    n = y.numel()
+    w = T.zeros(n, 8, dtype=y.dtype, device="cuda")
+    w[:, 3] = y
+    x = T.zeros(1, 8, dtype=y.dtype, device="cuda")
+    x[0, 3] = 1.0
+    out = T.empty(1, n, dtype=y.dtype, device="cuda")
+    io = cuda_lib.make_linear_io(x, w, out, act=act)
+    ws = T.empty(cuda_lib.mk_linear_workspace(io), dtype=T.uint8, device="cuda")
+    cuda_lib.mk_linear(io, ws)
+    T.cuda.synchronize()
+    want, _ = ok.linear(np64(x), np64(w), None, act, None)
+    got, a = np64(out)[0], np.abs(np64(y))
+    e = math.log2(math.e) * {"silu": a, "gelu": a * a / 2, "gelu_tanh": 2 * 0.79789 * (a + 0.044716 * a ** 3)}[act]
+    tol = (2.0 ** -18.5 + 3 * np.minimum(e, 130.0) * V + U[dtype]) * np.abs(want[0]) + TINY[dtype] + (a + 1) * 2.0 ** -53
+    assert np.all(np.abs(got - want[0]) <= tol), (np.abs(got - want[0]) / tol).max()
+
+
 def test_linear_takes_infinities_and_nan_as_they_come(cuda_lib):
     x = torch.zeros(40, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(200, 64, dtype=torch.bfloat16, device="cuda")
