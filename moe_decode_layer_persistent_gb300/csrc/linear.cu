@@ -12,9 +12,9 @@
 // the rows in the order of the ranks.  Many tiles: one CTA per SM works through
 // them, the tensor cores on the next tile while the last one's results leave.
 //
-// What bounds it: 4096 rows, 4096 -> 12288, SiLU: 217 to 223 us, 1.85 to 1.9 PFLOP/s, the tensor
-// cores.  64 rows, 4096 -> 6144: 15 us (50 MB of weights), half of it start, first trip
-// and join; 250 rows, 4096 -> 4096: 17.6 us, of which 6 go for what each SM takes in.
+// What bounds it: 4096 rows, 4096 -> 12288, SiLU: 217 to 229 us, 1.8 to 1.9 PFLOP/s, the tensor
+// cores.  64 rows, 4096 -> 6144: 14.5 us, of which 50 MB of weights take 9; 250 rows,
+// 4096 -> 4096: 17.8 us, of which 6 go for what each SM takes in and 6 for the sums' way.
 #include <algorithm>
 #include <atomic>
 #include <climits>
