@@ -815,6 +815,22 @@ def test_linear_without_rows(cuda_lib):
     assert cuda_lib.mk_linear_status(ws) == 0
 
 
+@pytest.mark.parametrize("m,k,n", [
+    (1, 2048, 9771), (3, 72, 10068), (16, 512, 4900), (40, 4096, 1000), (70, 2500 * 4, 264), (128, 640, 2050), (200, 328, 1999),
+    (400, 256, 3300), (33, 24, 19000), (64, 4096, 6144)])
+@pytest.mark.parametrize("kw", [dict(pad=4, residual=True, act="silu"), dict(bias=True)])
+def test_linear_few_rows_and_many_outputs(cuda_lib, m, k, n, kw):
+    check_linear(cuda_lib, np.random.default_rng(m + k + n), m, k, n, "bf16", **kw)
+
+
+def test_attn_without_rows(cuda_lib):
+    a = make_attn(np.random.default_rng(23), [30, 9], [0, 0], 4, 1, 64, "bf16", 16)
+    a["q"], a["n"] = a["q"][:0], 0
+    call_attn(cuda_lib, a)
+    torch.cuda.synchronize()
+    assert cuda_lib.mk_kvq_attn_status(a["workspace"]) == 0
+
+
 # ---------------------------------------------------------- all of them
 
 def test_a_step_through_all_operators(cuda_lib):
