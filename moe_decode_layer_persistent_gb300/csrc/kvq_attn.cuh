@@ -16,10 +16,10 @@ namespace mk {
 constexpr float kRefBelow = 6.f, kRefMost = 15.f;
 constexpr float kNoRef = -1e30f;
 // What an item takes on top of its key tiles, in key tiles (of 32 keys and of 128).
-// 200 requests of one token over up to 2000 keys: 70 us with 1, 61 with 2 or 5, 59 with
-// 3; token trees of 60 requests over up to 4000 keys: 132, 114, 100 and 101 us with 2,
-// 4, 6 and 10.
-constexpr int kLead = 3, kWideLead = 7;
+// 200 requests of one token over up to 2000 keys: 69 us with 1, 60 with 2, 58 with 3, 59
+// with 4; token trees of 60 requests over up to 4000 keys: 139, 121, 114, 104 and 108 us
+// with 3, 5, 7, 9 and 14 (of 16 over up to 16384 keys 100, 89, 88, 88 and 93).
+constexpr int kLead = 3, kWideLead = 9;
 
 // An item whose stretches lie in several workers, as the one with its first key tile
 // says.
