@@ -50,6 +50,17 @@ mk_status mk_selftest_attn_waits(const mk_prefix_attn_io* io, void* workspace,
                                  int64_t workspace_bytes, uint64_t wait_ns, int32_t withhold,
                                  int32_t which, void* stream);
 
+/* mk_linear (bf16) with its waits limited to `wait_ns` (1 .. 2e9; 2e9 in mk_linear
+ * itself) and, in every CTA, one hand-off withheld, so that the waits for it run out and
+ * the kernel gives up: withhold 1, the copies from block number `which` on; 2, a stage
+ * after the products of block number `which`; 3, the sums of tile number `which`; 4, the
+ * columns after the results of that tile; 0, nothing.  Of a pair of CTAs, 1 and 4 are of
+ * the one that `half` (0 or 1) names.  Synchronous; returns mk_linear_status:
+ * MK_ERR_TIMEOUT where some CTA came that far. */
+mk_status mk_selftest_linear_waits(const mk_linear_io* io, void* workspace, int64_t workspace_bytes,
+                                   uint64_t wait_ns, int32_t withhold, int32_t which, int32_t half,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

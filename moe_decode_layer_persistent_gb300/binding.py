@@ -218,6 +218,9 @@ _lib_mk_kvq_attn_status = _sig("mk_kvq_attn_status", _c.c_int, [_vp])
 _lib_mk_linear_workspace = _sig("mk_linear_workspace", _c.c_int,
                                 [_c.POINTER(mk_linear_io), _c.POINTER(_i64)])
 _lib_mk_linear = _sig("mk_linear", _c.c_int, [_c.POINTER(mk_linear_io), _vp, _i64, _vp])
+_lib_mk_selftest_linear_waits = _sig("mk_selftest_linear_waits", _c.c_int,
+                                     [_c.POINTER(mk_linear_io), _vp, _i64, _c.c_uint64, _i32, _i32,
+                                      _i32, _vp])
 _lib_mk_linear_status = _sig("mk_linear_status", _c.c_int, [_vp])
 
 EXPORTED = ["mk_layer_create", "mk_decode_step", "mk_decode_step_noalloc", "mk_layer_status", "mk_layer_clear_status",
@@ -228,7 +231,8 @@ EXPORTED = ["mk_layer_create", "mk_decode_step", "mk_decode_step_noalloc", "mk_l
             "mk_prefix_attn_workspace", "mk_prefix_attn", "mk_prefix_attn_status",
             "mk_qkv_append", "mk_kvq_read", "mk_kvq_attn_workspace", "mk_kvq_attn", "mk_kvq_attn_status",
             "mk_linear_workspace", "mk_linear", "mk_linear_status",
-            "mk_selftest_quantize", "mk_selftest_mma", "mk_selftest_sync", "mk_selftest_attn_waits"]
+            "mk_selftest_quantize", "mk_selftest_mma", "mk_selftest_sync", "mk_selftest_attn_waits",
+            "mk_selftest_linear_waits"]
 
 
 def _ptr(t):
@@ -832,3 +836,15 @@ def mk_linear(io, workspace, stream=None):
 
 def mk_linear_status(workspace):
     return _lib_mk_linear_status(_ptr(workspace))
+
+
+WITHHOLD_LINEAR = {"nothing": 0, "copies": 1, "stage": 2, "sums": 3, "columns": 4}
+
+
+def mk_selftest_linear_waits(io, workspace, wait_ns, withhold="nothing", which=0, half=0, stream=None):
+    """mk_linear with short waits and a hand-off withheld; returns the status."""
+    if not workspace.is_contiguous():
+        _refuse("mk_selftest_linear_waits")
+    return _lib_mk_selftest_linear_waits(
+        ctypes.byref(io), workspace.data_ptr(), workspace.numel() * workspace.element_size(), wait_ns,
+        WITHHOLD_LINEAR[withhold], which, half, _stream(stream))

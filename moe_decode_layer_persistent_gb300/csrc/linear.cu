@@ -19,6 +19,7 @@
 #include <atomic>
 #include <climits>
 
+#include "../../include/mk_selftest.h"
 #include "attn_ptx.cuh"
 #include "batch.h"
 #include "rope.h"
@@ -36,6 +37,10 @@ constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
 constexpr uint32_t kTimeout = 1;
 constexpr int kSmem = 222 * 1024;  // of a CTA, at most: one per SM
 
+// Hand-offs that a self-test withholds, so that waits run out: copies from a block on, a
+// stage after use, a tile's sums, a tile's columns after use.
+enum Withhold { kNothing = 0, kCopies = 1, kStage = 2, kSums = 3, kColumns = 4 };
+
 struct LinearParams {
   mk_linear_io io;
   uint32_t* status;
@@ -49,6 +54,10 @@ struct LinearParams {
   int32_t tmem_cols;   // allocated; two tiles' where a CTA has several
   uint32_t idesc;
   int32_t vec;         // out and residual take four values at a time
+  // of a self-test: limit of a wait; which hand-off to withhold, the how manieth, and of
+  // a pair in which CTA
+  uint64_t wait_ns;
+  int32_t withhold, withhold_at, withhold_half;
 };
 
 struct LinearBars {
@@ -56,6 +65,7 @@ struct LinearBars {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drained;
   uint32_t tmem, abort;
+  int32_t loads;  // blocks that the producer has brought
 };
 
 // y = act(y) of N values (the choice outside of the loop, so that their chains overlap).
@@ -93,7 +103,16 @@ MK_DEV void activate(float (&y)[N], int act) {
   }
 }
 
-// Bounded wait: false once any wait of the CTA has run out.
+// Pairs of CTAs: each holds half of a tile's outputs and brings half of the rows of x;
+// the first one's issuer multiplies for both.
+MK_DEV uint32_t address_in(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+// Bounded wait: false once any wait of the CTA, or of another one of its cluster, has run
+// out: they wait for one another, and none reads the sums of one that gave up.
+template <bool kTest>
 MK_DEV bool wait_bar(const LinearParams& P, LinearBars& B, uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
@@ -102,21 +121,21 @@ MK_DEV bool wait_bar(const LinearParams& P, LinearBars& B, uint64_t* bar, uint32
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*const_cast<volatile uint32_t*>(&B.abort)) return false;
-    if (globaltimer() - t0 > kWaitNs) {
-      *const_cast<volatile uint32_t*>(&B.abort) = 1;
+    if (globaltimer() - t0 > (kTest ? P.wait_ns : kWaitNs)) {
+      uint32_t ctas;
+      asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+      for (uint32_t r = 0; r < ctas; ++r)
+        asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(address_in(&B.abort, r)), "r"(1u) : "memory");
       atomicExch(P.status, kTimeout);
       return false;
     }
   }
 }
-
-// Pairs of CTAs: each holds half of a tile's outputs and brings half of the rows of x;
-// the first one's issuer multiplies for both.
-MK_DEV uint32_t address_in(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
+template <bool kTest>
+MK_DEV bool withheld(const LinearParams& P, int what, int at, int half) {
+  return kTest && P.withhold == what && P.withhold_at == at && P.withhold_half == half;
 }
+
 template <bool PAIR>
 MK_DEV void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, uint64_t policy, uint32_t leader) {
   if (!PAIR) {
@@ -176,8 +195,18 @@ MK_DEV void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Bytes of copies that do not come, as if they had.
+MK_DEV void complete_bytes(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 MK_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+MK_DEV int32_t load_cluster_word(const int32_t* p, uint32_t rank) {
+  int32_t v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(address_in(p, rank)) : "memory");
+  return v;
 }
 MK_DEV float4 load_cluster(uint32_t addr, uint32_t rank) {
   uint32_t a;
@@ -248,7 +277,7 @@ MK_DEV void join_sums(const LinearParams& P, uint32_t sums, int feat0, int row0,
   }
 }
 
-template <class T, bool PAIR>
+template <class T, bool PAIR, bool kTest>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear(const __grid_constant__ LinearParams P, const __grid_constant__ CUtensorMap wmap,
              const __grid_constant__ CUtensorMap xmap) {
@@ -288,29 +317,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
 
-  int loads = 0;  // of the producer
   if (warp == 0) {
     if (elect_one()) {
       const uint64_t keep = policy_evict_normal(), once = P.row_tiles == 1 ? policy_evict_first() : keep;
       bool ok = true;
+      int loads = 0;
       for (int tile = first; tile < P.tiles && ok; tile += step) {
         const int f = tile / P.row_tiles * kTileFeat + half * kFeat, r = tile % P.row_tiles * P.cols + half * x_rows;
         for (int k = k0; k < k1; ++k, ++loads) {
           const int st = loads % P.stages, round = loads / P.stages;
-          if (round && !wait_bar(P, B, &B.empty[st], (round - 1) & 1)) {
-            ok = false;
-            break;
-          }
+          ok = !withheld<kTest>(P, kCopies, loads, half) &&
+               (!round || wait_bar<kTest>(P, B, &B.empty[st], (round - 1) & 1));
+          if (!ok) break;
           uint8_t* a = smem + st * stage_bytes;
           if (half == 0) mbar_arrive_expect_tx(&B.full[st], stage_bytes * kCtas);
           load_box<PAIR>(a, &wmap, &B.full[st], k * kBlock, f, once, leader);
           load_box<PAIR>(a + kFeat * 128, &xmap, &B.full[st], k * kBlock, r, keep, leader);
         }
       }
-      // of work that was given up: the copies on their way, the last one into each stage
-      // (the second of a pair: the first one's barriers count its copies; it has waited long)
-      if (!ok && half == 0)
-        for (int i = max(0, loads - P.stages); i < loads; ++i) mbar_wait_bounded(&B.full[i % P.stages], (i / P.stages) & 1, kWaitNs);
+      // (what the products say about the stages comes before the CTA leaves)
+      for (int i = max(0, loads - P.stages); i < loads && ok; ++i)
+        ok = wait_bar<kTest>(P, B, &B.empty[i % P.stages], (i / P.stages) & 1);
+      B.loads = loads;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -319,14 +347,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int used = 0, n = 0;
       for (int tile = first; tile < P.tiles && ok; tile += step, ++n) {
         const int buf = n & 1;
-        if (n >= 2 && !wait_bar(P, B, &B.acc_empty[buf], ((n >> 1) - 1) & 1)) {
+        if (n >= 2 && !wait_bar<kTest>(P, B, &B.acc_empty[buf], ((n >> 1) - 1) & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
         for (int k = k0; k < k1; ++k, ++used) {
           const int st = used % P.stages;
-          if (!wait_bar(P, B, &B.full[st], (used / P.stages) & 1)) {
+          if (!wait_bar<kTest>(P, B, &B.full[st], (used / P.stages) & 1)) {
             ok = false;
             break;
           }
@@ -336,13 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kBlock / 16; ++i)  // 16 inputs: 32 bytes on in the swizzled rows
             multiply<PAIR>(tmem + buf * acc_cols, ad + 2 * i, bd + 2 * i, P.idesc, k > k0 || i > 0);
-          commit<PAIR>(&B.empty[st], both);
+          if (!withheld<kTest>(P, kStage, used, 0)) commit<PAIR>(&B.empty[st], both);
         }
-        if (ok) commit<PAIR>(&B.acc_full[buf], both);
-      }
-      if (!ok) {
-        commit<PAIR>(&B.drained, both);
-        mbar_wait_bounded(&B.drained, 0, kWaitNs);
+        if (ok && !withheld<kTest>(P, kSums, n, 0)) commit<PAIR>(&B.acc_full[buf], both);
       }
     }
     __syncwarp();
@@ -380,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fetch(col0, ahead[0]);
       fetch(col0 + 32, ahead[1]);
-      ok = __all_sync(0xffffffffu, wait_bar(P, B, &B.acc_full[buf], (n >> 1) & 1));
+      ok = __all_sync(0xffffffffu, wait_bar<kTest>(P, B, &B.acc_full[buf], (n >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
       for (int col = col0; col < rows; col += 32) {
@@ -414,30 +438,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
+      if (lane == 0 && !withheld<kTest>(P, kColumns, n, half)) {
         if (half == 0) mbar_arrive(&B.acc_empty[buf]);
         else arrive_at(address_in(&B.acc_empty[buf], leader));
       }
       __syncwarp();
     }
   }
-  if (P.split > 1) {
+  // Every warp of the CTA, of the whole cluster, is through: whether any of them gave up
+  // is settled, and the same in all of them.
+  const bool cluster = PAIR || P.split > 1;
+  auto meet = [&] {
     __syncwarp();
-    cluster_sync();
-    // (a CTA of a cluster has one tile)
-    if (!*const_cast<volatile uint32_t*>(&B.abort)) {
-      const int feat0 = first / P.row_tiles * kTileFeat + half * kFeat;
-      const int row0 = first % P.row_tiles * P.cols, rows = min(P.cols, io.n_rows - row0);
-      const int c0 = rows * rank / P.split, c1 = rows * (rank + 1) / P.split;
-      if (P.vec) join_sums<T, true>(P, smem_u32(smem), feat0, row0, c0, c1, half);
-      else join_sums<T, false>(P, smem_u32(smem), feat0, row0, c0, c1, half);
+    tc_fence_before();
+    if (cluster) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+  };
+  meet();
+  const bool gave_up = *const_cast<volatile uint32_t*>(&B.abort) != 0;
+  if (gave_up) {
+    // Whichever wait it was, and whoever was done by then: no copy may land and no product
+    // run on after the CTA has left.
+    if (warp == 0 && half == 0 && elect_one()) {
+      // (of a pair: this CTA's barriers count both CTAs' copies, and one may have brought
+      // blocks, fewer than there are stages, that the other has not)
+      const int mine = B.loads, other = PAIR ? load_cluster_word(&B.loads, leader + 1) : mine, most = max(mine, other);
+      for (int i = max(0, most - P.stages); i < most; ++i) {
+        uint64_t* bar = &B.full[i % P.stages];
+        if (i >= mine) mbar_arrive_expect_tx(bar, stage_bytes);
+        else if (i >= other) complete_bytes(bar, stage_bytes);
+        mbar_wait_bounded(bar, (i / P.stages) & 1, kWaitNs);
+      }
     }
-    __syncwarp();
+    if (warp == 1) {
+      if (half == 0 && elect_one()) commit<PAIR>(&B.drained, both);
+      __syncwarp();
+      mbar_wait_bounded(&B.drained, 0, kWaitNs);
+    }
+  } else if (P.split > 1) {
+    // (a CTA of a cluster has one tile)
+    const int feat0 = first / P.row_tiles * kTileFeat + half * kFeat;
+    const int row0 = first % P.row_tiles * P.cols, rows = min(P.cols, io.n_rows - row0);
+    const int c0 = rows * rank / P.split, c1 = rows * (rank + 1) / P.split;
+    if (P.vec) join_sums<T, true>(P, smem_u32(smem), feat0, row0, c0, c1, half);
+    else join_sums<T, false>(P, smem_u32(smem), feat0, row0, c0, c1, half);
   }
-  // no CTA leaves while another one reads its sums or arrives at its barriers
-  tc_fence_before();
-  if (PAIR || P.split > 1) cluster_sync();
-  __syncthreads();
+  // (no CTA leaves while another one reads its sums or its word, or copies into it)
+  if (gave_up || P.split > 1) meet();
+  __syncwarp();
   if (warp == 1) free_columns<PAIR>(tmem, P.tmem_cols);
 }
 
@@ -476,7 +525,7 @@ mk_status max_clusters(int device, int sms, int (&most)[9]) {
       lc.gridDim = dim3(c * sms);
       lc.blockDim = dim3(kThreads);
       lc.dynamicSmemBytes = kSmem;
-      MK_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_linear<T, false>, &lc));
+      MK_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_linear<T, false, false>, &lc));
       if (device < 64) known[device][c].store(n, std::memory_order_relaxed);
     }
     most[c] = n;
@@ -516,7 +565,7 @@ void choose(LinearParams* P, const int (&most)[9]) {
   if (choose(P, most, 2) * 5 < single * 4) choose(P, most, 1);
 }
 
-template <class T, bool PAIR>
+template <class T, bool PAIR, bool kTest>
 mk_status launch(const LinearParams& P, const CUtensorMap& w, const CUtensorMap& x, const int (&most)[9],
                  cudaStream_t s) {
   constexpr int kCtas = PAIR ? 2 : 1;
@@ -537,17 +586,17 @@ mk_status launch(const LinearParams& P, const CUtensorMap& w, const CUtensorMap&
   // (a pair takes tensor memory on two SMs: no two of them on one, of which each might
   // wait for what the other holds)
   if (PAIR) lc.dynamicSmemBytes = std::max<size_t>(lc.dynamicSmemBytes, 120 * 1024);
-  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_linear<T, PAIR>, P, w, x));
+  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_linear<T, PAIR, kTest>, P, w, x));
   return MK_OK;
 }
 
-template <class T>
+template <class T, bool kTest = false>
 mk_status linear(LinearParams* P, int device, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // (once per device: it takes as long as a launch)
   const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    MK_CUDA_TRY(cudaFuncSetAttribute(k_linear<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-    MK_CUDA_TRY(cudaFuncSetAttribute(k_linear<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_linear<T, false, kTest>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_linear<T, true, kTest>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   int most[9] = {};
@@ -563,7 +612,7 @@ mk_status linear(LinearParams* P, int device, int sms, cudaStream_t s) {
   if (st != MK_OK) return st;
   st = encode_tmap(&x, io.dtype, io.x, io.n_in, io.n_rows, io.x_stride, P->pair ? P->cols / 2 : P->cols);
   if (st != MK_OK) return st;
-  return P->pair ? launch<T, true>(*P, w, x, most, s) : launch<T, false>(*P, w, x, most, s);
+  return P->pair ? launch<T, true, kTest>(*P, w, x, most, s) : launch<T, false, kTest>(*P, w, x, most, s);
 }
 
 mk_status check_shapes(const mk_linear_io* io) {
@@ -579,24 +628,14 @@ mk_status check_shapes(const mk_linear_io* io) {
   return MK_OK;
 }
 
-}  // namespace
+// What a self-test sets about the waits.
+struct Waits {
+  uint64_t ns;
+  int32_t withhold, which, half;
+};
 
-}  // namespace mk
-
-using namespace mk;
-
-extern "C" {
-
-mk_status mk_linear_workspace(const mk_linear_io* io, int64_t* bytes) {
-  if (!bytes) return MK_ERR_INVALID_ARG;
-  *bytes = 0;
-  const mk_status st = check_shapes(io);
-  if (st != MK_OK) return st;
-  *bytes = 256;
-  return MK_OK;
-}
-
-mk_status mk_linear(const mk_linear_io* io, void* workspace, int64_t workspace_bytes, void* stream) {
+mk_status call_linear(const mk_linear_io* io, void* workspace, int64_t workspace_bytes, void* stream,
+                      const Waits* test) {
   mk_status st = check_shapes(io);
   if (st != MK_OK) return st;
   const int64_t m = io->n_rows, n = io->n_out, k = io->n_in;
@@ -633,7 +672,46 @@ mk_status mk_linear(const mk_linear_io* io, void* workspace, int64_t workspace_b
   P.status = static_cast<uint32_t*>(workspace);
   P.vec = n % 4 == 0 && io->out_stride % 4 == 0 && !misaligned(io->out, 8) &&
           (!io->residual || (io->residual_stride % 4 == 0 && !misaligned(io->residual, 8)));
+  P.wait_ns = test ? test->ns : kWaitNs;
+  P.withhold = test ? test->withhold : kNothing;
+  P.withhold_at = test ? test->which : 0;
+  P.withhold_half = test ? test->half : 0;
+  if (test) return linear<__nv_bfloat16, true>(&P, device, sms, s);
   return io->dtype == MK_BF16 ? linear<__nv_bfloat16>(&P, device, sms, s) : linear<__half>(&P, device, sms, s);
+}
+
+}  // namespace
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" {
+
+mk_status mk_linear_workspace(const mk_linear_io* io, int64_t* bytes) {
+  if (!bytes) return MK_ERR_INVALID_ARG;
+  *bytes = 0;
+  const mk_status st = check_shapes(io);
+  if (st != MK_OK) return st;
+  *bytes = 256;
+  return MK_OK;
+}
+
+mk_status mk_linear(const mk_linear_io* io, void* workspace, int64_t workspace_bytes, void* stream) {
+  return call_linear(io, workspace, workspace_bytes, stream, nullptr);
+}
+
+mk_status mk_selftest_linear_waits(const mk_linear_io* io, void* workspace, int64_t workspace_bytes,
+                                   uint64_t wait_ns, int32_t withhold, int32_t which, int32_t half, void* stream) {
+  if (!io || !wait_ns || wait_ns > kWaitNs || withhold < kNothing || withhold > kColumns || which < 0 ||
+      (half & ~1) || (half && (withhold == kStage || withhold == kSums)))
+    return MK_ERR_INVALID_ARG;
+  if (io->dtype != MK_BF16) return MK_ERR_UNSUPPORTED;
+  const Waits w{wait_ns, withhold, which, half};
+  const mk_status st = call_linear(io, workspace, workspace_bytes, stream, &w);
+  if (st != MK_OK) return st;
+  MK_CUDA_TRY(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
+  return mk_linear_status(workspace);
 }
 
 mk_status mk_linear_status(const void* workspace) {

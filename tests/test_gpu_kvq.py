@@ -900,3 +900,56 @@ def test_a_step_through_all_operators(cuda_lib):
         assert np.all(np.abs(np64(x_out) - want) <= s * (hq * d / 16 + 64) * 2 * V + U["bf16"] * np.abs(want) + 1e-6)
         assert np.array_equal(sl, slots.cpu().numpy())
     mk.mk_rope_destroy(rope)
+
+
+# ------------------------------------------------------- waits that run out
+
+LINEAR_WAITS = {  # one CTA per tile, several tiles each; clusters; pairs, several tiles each; clusters of pairs
+    "single": (40, 1024, 60000), "split": (3, 16384, 256), "pair": (2100, 1024, 9000), "split_pair": (250, 2048, 8192)}
+
+
+@pytest.fixture(scope="module", params=list(LINEAR_WAITS))
+def linear_waiting(cuda_lib, request):
+    m, k, n = LINEAR_WAITS[request.param]
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    x, w = ((torch.randn(r, k, generator=gen, device="cuda") * k ** -0.25).bfloat16() for r in (m, n))
+    out = torch.full((m, n), CANARY, dtype=torch.bfloat16, device="cuda")
+    io = cuda_lib.make_linear_io(x, w, out, act="silu")
+    room = torch.full((cuda_lib.mk_linear_workspace(io) + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    size = room.numel() - 4096
+    cuda_lib.mk_linear(io, room[:size])
+    torch.cuda.synchronize()
+    assert cuda_lib.mk_linear_status(room) == 0
+    return dict(name=request.param, io=io, ws=room[:size], guard=room[size:], out=out, want=out.clone(), keep=(x, w),
+                kept=(x.clone(), w.clone()))
+
+
+def test_linear_waits_that_do_not_run_out(cuda_lib, linear_waiting):
+    a = linear_waiting
+    a["out"].fill_(CANARY)
+    assert cuda_lib.mk_selftest_linear_waits(a["io"], a["ws"], 2 * 10 ** 9) == 0
+    assert torch.equal(a["out"], a["want"])
+
+
+@pytest.mark.parametrize("what,which,half", [
+    ("copies", 0, 0), ("copies", 2, 0), ("copies", 15, 0), ("copies", 0, 1), ("copies", 2, 1), ("copies", 15, 1),
+    ("stage", 0, 0), ("stage", 3, 0), ("stage", 15, 0), ("sums", 0, 0), ("sums", 1, 0), ("columns", 0, 0), ("columns", 0, 1)])
+def test_linear_gives_up_and_recovers(cuda_lib, linear_waiting, what, which, half):
+    """A hand-off that never comes: within the limit (2 ms) every warp of the CTA, and of
+    its cluster, gives up, the copies and products on their way are waited for, whoever
+    issued them, the status says so, nothing beside the output and the workspace is
+    touched; the next call on the same workspace is well, to the bit."""
+    a = linear_waiting
+    several = a["name"] in ("single", "pair")     # tiles per CTA
+    if half and "pair" not in a["name"] or not several and (what == "columns" or (what, which) == ("sums", 1)):
+        pytest.skip("no such hand-off")
+    status = cuda_lib.mk_selftest_linear_waits(a["io"], a["ws"], 2 * 10 ** 6, what, which, half)
+    assert cuda_lib.STATUS_NAMES[status] == "MK_ERR_TIMEOUT"
+    assert cuda_lib.mk_linear_status(a["ws"]) == status
+    assert bool((a["guard"] == 0x5A).all())
+    assert all(torch.equal(x, y) for x, y in zip(a["keep"], a["kept"]))
+    a["out"].fill_(CANARY)
+    cuda_lib.mk_linear(a["io"], a["ws"])
+    torch.cuda.synchronize()
+    assert cuda_lib.mk_linear_status(a["ws"]) == 0
+    assert torch.equal(a["out"], a["want"])

@@ -241,3 +241,23 @@ def test_packed_fields_are_the_structs(mk):
 @pytest.mark.parametrize("name", ["rows", "take_row", "convert", "issue_mmas"])
 def test_warps_meet_before_instructions_for_whole_warps(name):
     assert sources.breaches(sources.body("kvq_wide.cu", name)) == []
+
+
+@pytest.mark.parametrize("over,args,status", [
+    ({}, (0, 1, 0, 0), INVALID), ({}, (2 * 10 ** 9 + 1, 1, 0, 0), INVALID), ({}, (10 ** 6, 5, 0, 0), INVALID),
+    ({}, (10 ** 6, -1, 0, 0), INVALID), ({}, (10 ** 6, 1, -1, 0), INVALID), ({}, (10 ** 6, 1, 0, 2), INVALID),
+    ({}, (10 ** 6, 2, 0, 1), INVALID), (dict(dtype=1), (10 ** 6, 1, 0, 0), UNSUPPORTED), (dict(w=0), (10 ** 6, 1, 0, 0), INVALID)])
+def test_linear_waits_selftest_refusals(mk, over, args, status):
+    assert mk._lib_mk_selftest_linear_waits(linear_io(mk, **over), 64 * A, 1 << 20, *args, None) == status
+    assert mk._lib_mk_selftest_linear_waits(None, 64 * A, 1 << 20, 10 ** 6, 1, 0, 0, None) == INVALID
+
+
+def test_linear_settles_what_was_given_up_behind_a_barrier():
+    """The copies and products of work that was given up are waited for where every warp
+    is through, by the word that all of them write, not by what one warp went through."""
+    code = sources.body("linear.cu", "k_linear")
+    meets = [m.start() for m in sources.re.finditer(r"\bmeet\(\)", code)]
+    drains = [m.start() for m in sources.re.finditer(r"B\.drained|mbar_wait_bounded\(", code)]
+    settled = code.index("gave_up =")
+    assert len(meets) == 2 and meets[0] < settled < code.index("free_columns") and "B.abort" in code[settled:settled + 90]
+    assert len(drains) > 2 and all(meets[0] < d < meets[1] for d in drains[1:])      # (the first is its initialisation)
