@@ -61,6 +61,15 @@ mk_status mk_selftest_linear_waits(const mk_linear_io* io, void* workspace, int6
                                    uint64_t wait_ns, int32_t withhold, int32_t which, int32_t half,
                                    void* stream);
 
+/* mk_kvq_attn (bf16, head_dim 64, more than 16 rows per request and kv head on average)
+ * in the same way: withhold 1, the scores of each CTA's key tile number `which`; 2, its
+ * weights; 3, its keys; 4, its values; 5, the keys' buffer after use; 6, the values'; 7,
+ * row tile number `which`; 8 and 9, of a tile of up to 64 rows whose keys a CTA has all,
+ * the `which`-th such, the second half's results and their place after use; 0, nothing.
+ * Synchronous; returns mk_kvq_attn_status. */
+mk_status mk_selftest_kvq_waits(const mk_kvq_attn_io* io, void* workspace, int64_t workspace_bytes,
+                                uint64_t wait_ns, int32_t withhold, int32_t which, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

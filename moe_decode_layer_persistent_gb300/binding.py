@@ -218,6 +218,8 @@ _lib_mk_kvq_attn_status = _sig("mk_kvq_attn_status", _c.c_int, [_vp])
 _lib_mk_linear_workspace = _sig("mk_linear_workspace", _c.c_int,
                                 [_c.POINTER(mk_linear_io), _c.POINTER(_i64)])
 _lib_mk_linear = _sig("mk_linear", _c.c_int, [_c.POINTER(mk_linear_io), _vp, _i64, _vp])
+_lib_mk_selftest_kvq_waits = _sig("mk_selftest_kvq_waits", _c.c_int,
+                                  [_c.POINTER(mk_kvq_attn_io), _vp, _i64, _c.c_uint64, _i32, _i32, _vp])
 _lib_mk_selftest_linear_waits = _sig("mk_selftest_linear_waits", _c.c_int,
                                      [_c.POINTER(mk_linear_io), _vp, _i64, _c.c_uint64, _i32, _i32,
                                       _i32, _vp])
@@ -232,7 +234,7 @@ EXPORTED = ["mk_layer_create", "mk_decode_step", "mk_decode_step_noalloc", "mk_l
             "mk_qkv_append", "mk_kvq_read", "mk_kvq_attn_workspace", "mk_kvq_attn", "mk_kvq_attn_status",
             "mk_linear_workspace", "mk_linear", "mk_linear_status",
             "mk_selftest_quantize", "mk_selftest_mma", "mk_selftest_sync", "mk_selftest_attn_waits",
-            "mk_selftest_linear_waits"]
+            "mk_selftest_kvq_waits", "mk_selftest_linear_waits"]
 
 
 def _ptr(t):
@@ -848,3 +850,16 @@ def mk_selftest_linear_waits(io, workspace, wait_ns, withhold="nothing", which=0
     return _lib_mk_selftest_linear_waits(
         ctypes.byref(io), workspace.data_ptr(), workspace.numel() * workspace.element_size(), wait_ns,
         WITHHOLD_LINEAR[withhold], which, half, _stream(stream))
+
+
+WITHHOLD_KVQ = {"nothing": 0, "scores": 1, "weights": 2, "keys": 3, "values": 4, "keys_used": 5, "values_used": 6,
+                "row_tile": 7, "half": 8, "taken": 9}
+
+
+def mk_selftest_kvq_waits(io, workspace, wait_ns, withhold="nothing", which=0, stream=None):
+    """mk_kvq_attn with short waits and a hand-off withheld; returns the status."""
+    if not workspace.is_contiguous():
+        _refuse("mk_selftest_kvq_waits")
+    return _lib_mk_selftest_kvq_waits(
+        ctypes.byref(io), workspace.data_ptr(), workspace.numel() * workspace.element_size(), wait_ns,
+        WITHHOLD_KVQ[withhold], which, _stream(stream))

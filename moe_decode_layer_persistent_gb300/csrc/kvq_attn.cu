@@ -32,6 +32,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "../../include/mk_selftest.h"
 #include "kvq_attn.cuh"
 
 namespace mk {
@@ -675,29 +676,14 @@ mk_status check_shapes(const mk_kvq_attn_io* io) {
   return MK_OK;
 }
 
-}  // namespace
+// What a self-test sets about the waits.
+struct Waits {
+  uint64_t ns;
+  int32_t withhold, which;
+};
 
-}  // namespace mk
-
-using namespace mk;
-
-extern "C" {
-
-mk_status mk_kvq_attn_workspace(const mk_kvq_attn_io* io, int64_t* bytes) {
-  if (!bytes) return MK_ERR_INVALID_ARG;
-  *bytes = 0;
-  const mk_status st = check_shapes(io);
-  if (st != MK_OK) return st;
-  int dev = -1, sms = 0;
-  MK_CUDA_TRY(cudaGetDevice(&dev));
-  MK_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  KvqParams P;
-  const int rows = rows_of_tile(io);
-  *bytes = lay_out(workers_of(rows, sms), rows, io->kvq.head_dim, nullptr, &P);
-  return MK_OK;
-}
-
-mk_status mk_kvq_attn(const mk_kvq_attn_io* io, void* workspace, int64_t workspace_bytes, void* stream) {
+mk_status call_attn(const mk_kvq_attn_io* io, void* workspace, int64_t workspace_bytes, void* stream,
+                    const Waits* test) {
   mk_status st = check_shapes(io);
   if (st != MK_OK) return st;
   st = check_kvq(io->kvq, true);
@@ -758,9 +744,53 @@ mk_status mk_kvq_attn(const mk_kvq_attn_io* io, void* workspace, int64_t workspa
   P.by_group = make_divisor(P.group);
   P.page_shift = __builtin_ctz(static_cast<uint32_t>(c.page_size));
   P.page_bytes = static_cast<uint32_t>(page_bytes);
+  P.test = test != nullptr;
+  P.wait_ns = test ? test->ns : kKvqWaitNs;
+  P.withhold = test ? test->withhold : kKvqNothing;
+  P.withhold_at = test ? test->which : 0;
   if (io->dtype == MK_BF16)
     return d == 128 ? launch<__nv_bfloat16, 128>(P, tile, device, sms, s) : launch<__nv_bfloat16, 64>(P, tile, device, sms, s);
   return d == 128 ? launch<__half, 128>(P, tile, device, sms, s) : launch<__half, 64>(P, tile, device, sms, s);
+}
+
+}  // namespace
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" {
+
+mk_status mk_kvq_attn_workspace(const mk_kvq_attn_io* io, int64_t* bytes) {
+  if (!bytes) return MK_ERR_INVALID_ARG;
+  *bytes = 0;
+  const mk_status st = check_shapes(io);
+  if (st != MK_OK) return st;
+  int dev = -1, sms = 0;
+  MK_CUDA_TRY(cudaGetDevice(&dev));
+  MK_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  KvqParams P;
+  const int rows = rows_of_tile(io);
+  *bytes = lay_out(workers_of(rows, sms), rows, io->kvq.head_dim, nullptr, &P);
+  return MK_OK;
+}
+
+mk_status mk_kvq_attn(const mk_kvq_attn_io* io, void* workspace, int64_t workspace_bytes, void* stream) {
+  return call_attn(io, workspace, workspace_bytes, stream, nullptr);
+}
+
+mk_status mk_selftest_kvq_waits(const mk_kvq_attn_io* io, void* workspace, int64_t workspace_bytes,
+                                uint64_t wait_ns, int32_t withhold, int32_t which, void* stream) {
+  if (!wait_ns || wait_ns > kKvqWaitNs || withhold < kKvqNothing || withhold > kKvqTaken || which < 0)
+    return MK_ERR_INVALID_ARG;
+  mk_status st = check_shapes(io);
+  if (st != MK_OK) return st;
+  if (io->dtype != MK_BF16 || io->kvq.head_dim != 64 || rows_of_tile(io) != kWideRows) return MK_ERR_UNSUPPORTED;
+  const Waits w{wait_ns, withhold, which};
+  st = call_attn(io, workspace, workspace_bytes, stream, &w);
+  if (st != MK_OK) return st;
+  MK_CUDA_TRY(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
+  return mk_kvq_attn_status(workspace);
 }
 
 mk_status mk_kvq_attn_status(const void* workspace) {

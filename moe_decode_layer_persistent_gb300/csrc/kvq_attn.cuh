@@ -31,6 +31,14 @@ struct Split {
   int32_t h;
 };
 
+constexpr uint64_t kKvqWaitNs = 2000ull * 1000 * 1000;
+// Hand-offs of the kernel for row tiles of up to 128 rows that a self-test withholds, so
+// that waits run out: a tile's scores, its weights, its keys, its values, their buffers
+// after use, a row tile, the second half's results, its place after the first has them.
+enum KvqWithhold {
+  kKvqNothing, kKvqScores, kKvqWeights, kKvqKeys, kKvqValues, kKvqKeysUsed, kKvqValuesUsed, kKvqRowTile, kKvqHalf, kKvqTaken
+};
+
 struct KvqParams {
   mk_kvq_attn_io io;
   float scale_log2;  // scale * log2(e), times 8 (see Scales)
@@ -43,6 +51,10 @@ struct KvqParams {
   Split* split;      // [workers]
   float2* stat;      // (r, l) of the rows of part 2 w (begins inside an item), 2 w + 1
   float* o;          // [2 workers][rows][D]
+  // of a self-test: limit of a wait; which hand-off to withhold, and the how manieth
+  uint64_t wait_ns;
+  int32_t withhold, withhold_at;
+  bool test;
 };
 
 MK_DEV int clampi(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : static_cast<int>(v); }

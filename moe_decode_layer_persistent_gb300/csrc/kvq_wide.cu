@@ -39,7 +39,7 @@ constexpr int kThreads = 512;    // four warpgroups: rows, two that convert, pro
 constexpr int kStages = 3;       // tiles of a converting warp's ring
 constexpr int kValues = 3;       // tiles of V
 constexpr float kMost = 32768.f; // a row's sum of weights over a tile
-constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
+constexpr uint64_t kWaitNs = kKvqWaitNs;
 constexpr uint32_t kTimeout = 1;
 // columns of tensor memory: two tiles of scores and weights, O, Q
 constexpr uint32_t kOutAt = 256, kQAt = 384;
@@ -62,8 +62,14 @@ __host__ __device__ constexpr uint32_t idesc_fp16(int N, bool b_along_n) {
   return (1u << 4) | (b_along_n ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
 }
 
+// Whether a self-test withholds this hand-off.
+template <bool kTest>
+MK_DEV bool withheld(const KvqParams& P, KvqWithhold what, int at) {
+  return kTest && P.withhold == what && P.withhold_at == at;
+}
+
 // Bounded waits of whole warps: false once any wait of the CTA has run out.
-template <int D>
+template <bool kTest, int D>
 MK_DEV bool wait_warp(const KvqParams& P, WideSmem<D>& S, uint64_t* bar, uint32_t parity) {
   bool ok = mbar_try_wait(bar, parity);
   if (!ok) {
@@ -72,7 +78,7 @@ MK_DEV bool wait_warp(const KvqParams& P, WideSmem<D>& S, uint64_t* bar, uint32_
 #pragma unroll 1
       for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
       if (ok || *const_cast<volatile uint32_t*>(&S.abort)) break;
-      if (globaltimer() - t0 > kWaitNs) {
+      if (globaltimer() - t0 > (kTest ? P.wait_ns : kWaitNs)) {
         *const_cast<volatile uint32_t*>(&S.abort) = 1;
         atomicExch(P.status, kTimeout);
         break;
@@ -148,7 +154,7 @@ struct Walk {
 };
 
 // ---- converting warps
-template <int D>
+template <int D, bool kTest>
 MK_DEV void convert(const KvqParams& P, WideSmem<D>& S, Walk walk, int w) {
   using L = WideSmem<D>;
   const mk_kvq_attn_io& io = P.io;
@@ -214,7 +220,7 @@ MK_DEV void convert(const KvqParams& P, WideSmem<D>& S, Walk walk, int w) {
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const int of = kv ? kValues : 2, buf = done % of, round = done / of;
-        if (round && !wait_warp(P, S, kv ? &S.v_empty[buf] : &S.k_empty[buf], (round - 1) & 1)) {
+        if (round && !wait_warp<kTest>(P, S, kv ? &S.v_empty[buf] : &S.k_empty[buf], (round - 1) & 1)) {
           cp_async_wait<0>();
           return;
         }
@@ -240,8 +246,8 @@ MK_DEV void convert(const KvqParams& P, WideSmem<D>& S, Walk walk, int w) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&S.k_full[done & 1]);
-        mbar_arrive(&S.v_full[done % kValues]);
+        if (!withheld<kTest>(P, kKvqKeys, done)) mbar_arrive(&S.k_full[done & 1]);
+        if (!withheld<kTest>(P, kKvqValues, done)) mbar_arrive(&S.v_full[done % kValues]);
       }
       __syncwarp();
     }
@@ -251,7 +257,7 @@ MK_DEV void convert(const KvqParams& P, WideSmem<D>& S, Walk walk, int w) {
 }
 
 // ---- the products' issuer
-template <int D>
+template <int D, bool kTest>
 MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   constexpr uint32_t kIdS = idesc_fp16(kKeys, false), kIdO = idesc_fp16(D, true);
   const uint32_t tmem = S.tmem, to = tmem + kOutAt, tq = tmem + kQAt;
@@ -259,14 +265,14 @@ MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   // O += P V of a tile
   auto pv = [&](int at, bool first) {
     const int buf = at & 1, vb = at % kValues;
-    if (!wait_warp(P, S, &S.v_full[vb], (at / kValues) & 1) || !wait_warp(P, S, &S.p_full[buf], (at >> 1) & 1)) return false;
+    if (!wait_warp<kTest>(P, S, &S.v_full[vb], (at / kValues) & 1) || !wait_warp<kTest>(P, S, &S.p_full[buf], (at >> 1) & 1)) return false;
     tc_fence_after();
     if (elect_one()) {
       const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(S.v[vb]), kKeys * 128);
 #pragma unroll
       for (int k = 0; k < kKeys / 16; ++k)
         mma_ts(to, tmem + buf * 128 + 8 * k, vd + k * (16 * 128 >> 4), kIdO, !first || k > 0);
-      mma_commit(&S.v_empty[vb]);
+      if (!withheld<kTest>(P, kKvqValuesUsed, at)) mma_commit(&S.v_empty[vb]);
     }
     __syncwarp();
     return true;
@@ -275,13 +281,13 @@ MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   while (walk.next(P, it)) {
     const int n = it.tile_end - it.tile;
     if (n <= 0) continue;
-    if (!wait_warp(P, S, &S.q_full, items++ & 1)) return false;
+    if (!wait_warp<kTest>(P, S, &S.q_full, items++ & 1)) return false;
     for (int t = 0; t < n; ++t, ++done) {
       const int buf = done & 1;
-      if (!wait_warp(P, S, &S.k_full[buf], (done >> 1) & 1)) return false;
+      if (!wait_warp<kTest>(P, S, &S.k_full[buf], (done >> 1) & 1)) return false;
       // (its scores go over weights that the product two tiles back reads; products with
       // other sums need not run in order)
-      if (done >= 2 && !wait_warp(P, S, &S.v_empty[(done - 2) % kValues], ((done - 2) / kValues) & 1)) return false;
+      if (done >= 2 && !wait_warp<kTest>(P, S, &S.v_empty[(done - 2) % kValues], ((done - 2) / kValues) & 1)) return false;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t kd = sdesc_kmajor_sw128(smem_u32(S.k[buf]));
@@ -290,8 +296,8 @@ MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
           const uint64_t at = (k >> 2) * (kKeys * 128 >> 4) + (k & 3) * 2;
           mma_ts(tmem + buf * 128, tq + 8 * k, kd + at, kIdS, k);
         }
-        mma_commit(&S.s_full[buf]);
-        mma_commit(&S.k_empty[buf]);
+        if (!withheld<kTest>(P, kKvqScores, done)) mma_commit(&S.s_full[buf]);
+        if (!withheld<kTest>(P, kKvqKeysUsed, done)) mma_commit(&S.k_empty[buf]);
       }
       __syncwarp();
       if (t && !pv(done - 1, t == 1)) return false;
@@ -312,10 +318,10 @@ struct Row {
   bool valid;
 };
 
-// Brings the row's Q into tensor memory, in fp16 relative to its largest value, the
+// Brings the row's Q (the CTA's row tile number `taken`) into tensor memory, in fp16 relative to its largest value, the
 // pairs in the order of the codes'.
-template <class T, int D>
-MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r) {
+template <class T, int D, bool kTest>
+MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r, int taken) {
   const mk_kvq_attn_io& io = P.io;
   const mk_kvq_cache& c = io.kvq;
   const Item& it = r.it;
@@ -369,26 +375,26 @@ MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r) {
   tmem_st_wait();
   tc_fence_before();
   __syncwarp();
-  if (lane_id() == 0) mbar_arrive(&S.q_full);
+  if (lane_id() == 0 && !withheld<kTest>(P, kKvqRowTile, taken)) mbar_arrive(&S.q_full);
   __syncwarp();
 }
 
-template <class T, int D>
+template <class T, int D, bool kTest>
 MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   const mk_kvq_attn_io& io = P.io;
   const int lane = lane_id(), warp = threadIdx.x / 32, row = threadIdx.x;
   const uint32_t lanes = S.tmem + (static_cast<uint32_t>(warp * 32) << 16), to = lanes + kOutAt;
-  int done = 0, joined = 0;
+  int done = 0, joined = 0, items = 0;
   Row r;
   bool more = walk.next(P, r.it);
-  if (more) take_row<T, D>(P, S, r);
+  if (more) take_row<T, D, kTest>(P, S, r, items++);
   while (more) {
     const bool warp_valid = __any_sync(0xffffffffu, r.valid);
     const int n = r.it.tile_end - r.it.tile;
     float ref = kNoRef, l = 0.f;
     for (int t = 0; t < n; ++t, ++done) {
       const int buf = done & 1, k0 = (r.it.tile + t) * kKeys;
-      if (!wait_warp(P, S, &S.s_full[buf], (done >> 1) & 1)) return;
+      if (!wait_warp<kTest>(P, S, &S.s_full[buf], (done >> 1) & 1)) return;
       tc_fence_after();
       const uint32_t ts = lanes + buf * 128;
       if (warp_valid && r.it.folded && (t & 1) != warp >> 1) {
@@ -445,7 +451,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
             ref = next;
             if (t && __any_sync(0xffffffffu, old != 1.f)) {
               // (the tile before is in O when its V is free)
-              if (!wait_warp(P, S, &S.v_empty[(done - 1) % kValues], ((done - 1) / kValues) & 1)) return;
+              if (!wait_warp<kTest>(P, S, &S.v_empty[(done - 1) % kValues], ((done - 1) / kValues) & 1)) return;
               tc_fence_after();
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
@@ -485,7 +491,7 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.p_full[buf]);
+      if (lane == 0 && !withheld<kTest>(P, kKvqWeights, done)) mbar_arrive(&S.p_full[buf]);
       __syncwarp();
     }
 
@@ -493,9 +499,9 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
     // last tile's scores, are there.
     const Row mine = r;
     more = walk.next(P, r.it);
-    if (more) take_row<T, D>(P, S, r);
+    if (more) take_row<T, D, kTest>(P, S, r, items++);
     if (n > 0) {
-      if (!wait_warp(P, S, &S.v_empty[(done - 1) % kValues], ((done - 1) / kValues) & 1)) return;
+      if (!wait_warp<kTest>(P, S, &S.v_empty[(done - 1) % kValues], ((done - 1) / kValues) & 1)) return;
       tc_fence_after();
     }
     // An item that this CTA has whole is written from here.  If it is folded, the second
@@ -505,10 +511,10 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
     const float unit_v = 8.f * pow2(io.kvq.v_exp ? clamp_exp(io.kvq.v_exp[mine.it.h]) : 0);
     const int64_t part = (2ll * blockIdx.x + mine.it.starts) * kRows;
     float f1 = 1.f, f2 = 0.f;  // what this half's and the other one's O are multiplied with
-    if (warp >= 2 && joined && !wait_warp(P, S, &S.taken, (joined - 1) & 1)) return;
+    if (warp >= 2 && joined && !wait_warp<kTest>(P, S, &S.taken, (joined - 1) & 1)) return;
     joined += twice;
     if (twice && !second) {
-      if (!wait_warp(P, S, &S.halves, (joined - 1) & 1)) return;
+      if (!wait_warp<kTest>(P, S, &S.halves, (joined - 1) & 1)) return;
       if (mine.valid) {
         const float2 other = P.stat[part + row + kRows / 2];
         const float top = fmaxf(ref, other.x);
@@ -569,12 +575,13 @@ MK_DEV void rows(const KvqParams& P, WideSmem<D>& S, Walk walk) {
     }
     tc_fence_before();
     __syncwarp();
-    if (twice && lane == 0) mbar_arrive(second ? &S.halves : &S.taken);
+    if (twice && lane == 0 && !withheld<kTest>(P, second ? kKvqHalf : kKvqTaken, joined - 1))
+      mbar_arrive(second ? &S.halves : &S.taken);
     __syncwarp();
   }
 }
 
-template <class T, int D>
+template <class T, int D, bool kTest>
 __global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant__ KvqParams P) {
   extern __shared__ uint8_t raw_smem[];
   WideSmem<D>& S = *reinterpret_cast<WideSmem<D>*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
@@ -651,20 +658,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant_
   if (walk.pos < walk.end) {
     if (warp < 4) {
       reg_alloc<208>();
-      rows<T, D>(P, S, walk);
+      rows<T, D, kTest>(P, S, walk);
     } else if (warp < 4 + kConvert) {
       reg_dealloc<120>();
-      convert<D>(P, S, walk, warp - 4);
+      convert<D, kTest>(P, S, walk, warp - 4);
     } else {
       reg_dealloc<64>();
-      if (warp == 12) {
-      const bool ok = issue_mmas<D>(P, S, walk);
-      // of work that was given up: the products on their way
-      if (!ok) {
-        if (elect_one()) mma_commit(&S.drained);
-        __syncwarp();
-        mbar_wait_bounded(&S.drained, 0, kWaitNs);
-      } else {
+      if (warp == 12 && issue_mmas<D, kTest>(P, S, walk)) {
         // an item to join
         Item it;
         while (walk.next(P, it)) {
@@ -672,21 +672,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant_
             P.split[blockIdx.x] = {it.parts, it.folded, it.cu, it.rows, it.first, it.h};
         }
       }
-      }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) tmem_dealloc(S.tmem, 512);
+  tc_fence_after();
+  if (warp == 12) {
+    // A wait has run out (every warp is through: none writes the word any more).
+    // Whichever it was: no product may run on when the CTA leaves.  (The converting warps
+    // have waited for their own copies.)
+    if (*const_cast<volatile uint32_t*>(&S.abort)) {
+      if (elect_one()) mma_commit(&S.drained);
+      __syncwarp();
+      mbar_wait_bounded(&S.drained, 0, kWaitNs);
+      __syncwarp();
+    }
+    tmem_dealloc(S.tmem, 512);
+  }
 }
 
-template <class T, int D>
+template <class T, int D, bool kTest = false>
 mk_status launch(const KvqParams& P, int device, int sms, cudaStream_t s) {
   constexpr int smem = sizeof(WideSmem<D>) + 1024;
   static std::atomic<uint64_t> ready{0};  // (once per device: it takes as long as a launch)
   const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    MK_CUDA_TRY(cudaFuncSetAttribute(k_kvq_wide<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    MK_CUDA_TRY(cudaFuncSetAttribute(k_kvq_wide<T, D, kTest>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t lc = {};
@@ -699,7 +711,7 @@ mk_status launch(const KvqParams& P, int device, int sms, cudaStream_t s) {
   lc.gridDim = dim3(sms);
   lc.blockDim = dim3(kThreads);
   lc.dynamicSmemBytes = smem;
-  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_wide<T, D>, P));
+  MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_kvq_wide<T, D, kTest>, P));
   return MK_OK;
 }
 
@@ -707,6 +719,7 @@ mk_status launch(const KvqParams& P, int device, int sms, cudaStream_t s) {
 
 mk_status launch_kvq_wide(const KvqParams& P, int device, int sms, cudaStream_t s) {
   const bool d128 = P.io.kvq.head_dim == 128;
+  if (P.test) return launch<__nv_bfloat16, 64, true>(P, device, sms, s);
   if (P.io.dtype == MK_BF16)
     return d128 ? launch<__nv_bfloat16, 128>(P, device, sms, s) : launch<__nv_bfloat16, 64>(P, device, sms, s);
   return d128 ? launch<__half, 128>(P, device, sms, s) : launch<__half, 64>(P, device, sms, s);

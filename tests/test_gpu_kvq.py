@@ -953,3 +953,43 @@ def test_linear_gives_up_and_recovers(cuda_lib, linear_waiting, what, which, hal
     torch.cuda.synchronize()
     assert cuda_lib.mk_linear_status(a["ws"]) == 0
     assert torch.equal(a["out"], a["want"])
+
+
+@pytest.fixture(scope="module")
+def kvq_waiting(cuda_lib):
+    """Requests of 32 rows per kv head: several items per CTA, whole ones, held twice in
+    their tiles, and such as lie in two CTAs."""
+    n = 700
+    a = make_attn(np.random.default_rng(n), [130 + (37 * i) % 300 for i in range(n)], [8] * n, 4, 1, 64, "bf16", 16)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+    size = a["workspace"].numel()
+    room = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    a.update(ws=room[:size], guard=room[size:], want=(a["out"].clone(), a["lse"].clone()),
+             kept=[t.clone() for t in a["dev"] + [a["q"]]])
+    return a
+
+
+def test_attn_waits_that_do_not_run_out(cuda_lib, kvq_waiting):
+    a = kvq_waiting
+    a["whole"].fill_(CANARY)
+    assert cuda_lib.mk_selftest_kvq_waits(a["io"], a["ws"], 2 * 10 ** 9) == 0
+    assert torch.equal(a["out"][:a["n"]], a["want"][0][:a["n"]]) and torch.equal(a["lse"], a["want"][1])
+
+
+@pytest.mark.parametrize("what,which", [(w, i) for w in (
+    "scores", "weights", "keys", "values", "keys_used", "values_used") for i in (0, 1, 4)] + [
+    ("row_tile", 0), ("row_tile", 1), ("row_tile", 2), ("half", 0), ("half", 1), ("taken", 0)])
+def test_attn_gives_up_and_recovers(cuda_lib, kvq_waiting, what, which):
+    """A hand-off that never comes: as for the projection."""
+    a = kvq_waiting
+    status = cuda_lib.mk_selftest_kvq_waits(a["io"], a["ws"], 2 * 10 ** 6, what, which)
+    assert cuda_lib.STATUS_NAMES[status] == "MK_ERR_TIMEOUT"
+    assert cuda_lib.mk_kvq_attn_status(a["ws"]) == status
+    assert bool((a["guard"] == 0x5A).all()) and bool((a["whole"][a["n"]:] == CANARY).all())
+    assert all(torch.equal(x, y) for x, y in zip(a["dev"] + [a["q"]], a["kept"]))
+    a["whole"].fill_(CANARY)
+    cuda_lib.mk_kvq_attn(a["io"], a["ws"])
+    torch.cuda.synchronize()
+    assert cuda_lib.mk_kvq_attn_status(a["ws"]) == 0
+    assert torch.equal(a["out"][:a["n"]], a["want"][0][:a["n"]]) and torch.equal(a["lse"], a["want"][1])

@@ -261,3 +261,25 @@ def test_linear_settles_what_was_given_up_behind_a_barrier():
     settled = code.index("gave_up =")
     assert len(meets) == 2 and meets[0] < settled < code.index("free_columns") and "B.abort" in code[settled:settled + 90]
     assert len(drains) > 2 and all(meets[0] < d < meets[1] for d in drains[1:])      # (the first is its initialisation)
+
+
+@pytest.mark.parametrize("over,args,status", [
+    ({}, (0, 1, 0), INVALID), ({}, (2 * 10 ** 9 + 1, 1, 0), INVALID), ({}, (10 ** 6, 10, 0), INVALID),
+    ({}, (10 ** 6, -1, 0), INVALID), ({}, (10 ** 6, 1, -1), INVALID), (dict(dtype=1), (10 ** 6, 1, 0), UNSUPPORTED),
+    ({}, (10 ** 6, 1, 0), UNSUPPORTED), (dict(n_rows=100, n_q_heads=7), (10 ** 6, 1, 0), INVALID),
+    (dict(n_rows=100, lens=0), (10 ** 6, 1, 0), INVALID)])
+def test_attention_waits_selftest_refusals(mk, over, args, status):
+    kvq = pools(mk, head_dim=64)
+    assert mk._lib_mk_selftest_kvq_waits(attn_io(mk, kvq, **over), 64 * A, 1 << 30, *args, None) == status
+    assert mk._lib_mk_selftest_kvq_waits(attn_io(mk, n_rows=100), 64 * A, 1 << 30, 10 ** 6, 1, 0, None) == UNSUPPORTED
+    assert mk._lib_mk_selftest_kvq_waits(None, 64 * A, 1 << 30, 10 ** 6, 1, 0, None) == INVALID
+
+
+def test_attention_settles_what_was_given_up_behind_a_barrier():
+    """As for the projection: the products are waited for where every warp is through, by
+    the word that all of them write."""
+    code = sources.body("kvq_wide.cu", "k_kvq_wide")
+    last = code.rindex("__syncthreads()")
+    tail = code[last:]
+    assert code[:last].count("S.drained") == 1 and "mbar_wait_bounded" not in code[:last]      # its initialisation
+    assert tail.index("S.abort") < tail.index("mma_commit(&S.drained)") < tail.index("mbar_wait_bounded(&S.drained") < tail.index("tmem_dealloc")
