@@ -35,7 +35,10 @@ constexpr int kOutWarps = 8;      // of results: two to 32 outputs, for every ot
 constexpr int kThreads = 32 * (2 + kOutWarps);  // producer, MMA issuer, these
 constexpr uint64_t kWaitNs = 2000ull * 1000 * 1000;
 constexpr uint32_t kTimeout = 1;
-constexpr int kSmem = 222 * 1024;  // of a CTA, at most: one per SM
+constexpr int kSmem = 222 * 1024;  // of a CTA, at most
+// At least: more than half of an SM's, so that no two CTAs are on one. Clusters and pairs
+// take tensor memory on several SMs, and each of two might wait for what the other holds.
+constexpr int kSmemLeast = 120 * 1024;
 
 // Hand-offs that a self-test withholds, so that waits run out: copies from a block on, a
 // stage after use, a tile's sums, a tile's columns after use.
@@ -297,7 +300,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int k1 = static_cast<int>(static_cast<int64_t>(P.blocks) * (rank + 1) / P.split);
   const int acc_cols = P.cols <= 32 ? 32 : P.cols <= 64 ? 64 : P.cols <= 128 ? 128 : 256;
 
-  pdl_launch_dependents();
   if (warp == 0 && elect_one()) {
     prefetch_tensormap(&wmap);
     prefetch_tensormap(&xmap);
@@ -309,7 +311,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   if (PAIR) cluster_sync();  // (barriers that the other CTA arrives at)
-  if (warp == 1) alloc_columns<PAIR>(&B.tmem, P.tmem_cols);
+  if (warp == 1) {
+    alloc_columns<PAIR>(&B.tmem, P.tmem_cols);
+    // (not before: a dependent grid that took the columns first would wait for this one,
+    // which would wait for the columns)
+    pdl_launch_dependents();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -335,8 +342,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_box<PAIR>(a + kFeat * 128, &xmap, &B.full[st], k * kBlock, r, keep, leader);
         }
       }
-      // (what the products say about the stages comes before the CTA leaves)
-      for (int i = max(0, loads - P.stages); i < loads && ok; ++i)
+      // (what the first CTA's products say about the second one's stages comes before that
+      // one leaves)
+      for (int i = max(0, loads - P.stages); PAIR && i < loads && ok; ++i)
         ok = wait_bar<kTest>(P, B, &B.empty[i % P.stages], (i / P.stages) & 1);
       B.loads = loads;
     }
@@ -583,9 +591,7 @@ mk_status launch(const LinearParams& P, const CUtensorMap& w, const CUtensorMap&
   lc.blockDim = dim3(kThreads);
   // (a split tile's sums lie where the stages were)
   lc.dynamicSmemBytes = std::max(P.stages * (kFeat + P.cols / kCtas) * 128, P.split > 1 ? P.cols * kFeat * 4 : 0) + 1024;
-  // (a pair takes tensor memory on two SMs: no two of them on one, of which each might
-  // wait for what the other holds)
-  if (PAIR) lc.dynamicSmemBytes = std::max<size_t>(lc.dynamicSmemBytes, 120 * 1024);
+  lc.dynamicSmemBytes = std::max<size_t>(lc.dynamicSmemBytes, kSmemLeast);
   MK_CUDA_TRY(cudaLaunchKernelEx(&lc, k_linear<T, PAIR, kTest>, P, w, x));
   return MK_OK;
 }

@@ -283,3 +283,19 @@ def test_attention_settles_what_was_given_up_behind_a_barrier():
     tail = code[last:]
     assert code[:last].count("S.drained") == 1 and "mbar_wait_bounded" not in code[:last]      # its initialisation
     assert tail.index("S.abort") < tail.index("mma_commit(&S.drained)") < tail.index("mbar_wait_bounded(&S.drained") < tail.index("tmem_dealloc")
+
+
+def test_linear_holds_tensor_memory_before_another_grid_may_come():
+    """A dependent grid is let in behind the allocation, which waits without a limit, and
+    no launch leaves room for a second CTA on an SM (the 227 KB that one can have)."""
+    code = sources.body("linear.cu", "k_linear")
+    assert code.count("pdl_launch_dependents(") == 1
+    held = code[code.index("alloc_columns"):code.index("pdl_launch_dependents(")]
+    assert ";" in held and "{" not in held                        # by the warp that took them, next
+    text = open(sources.os.path.join(sources.CSRC, "linear.cu")).read()
+    least = int(sources.re.search(r"kSmemLeast = (\d+) \* 1024;", text).group(1))
+    assert 2 * (least + 1) > 227
+    launch = text[text.index("mk_status launch("):]
+    launch = launch[:launch.index("cudaLaunchKernelEx")]
+    sets = sources.re.findall(r"\n  (?:if [^\n]*)?lc\.dynamicSmemBytes = [^;]*;", launch)
+    assert "kSmemLeast" in sets[-1] and not sets[-1].startswith("\n  if")
