@@ -587,7 +587,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant_
   WideSmem<D>& S = *reinterpret_cast<WideSmem<D>*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
   const mk_kvq_attn_io& io = P.io;
   const int warp = threadIdx.x / 32, lane = lane_id(), Hk = io.kvq.n_kv_heads;
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.k_full[i], kConvert);
@@ -610,6 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kvq_wide(const __grid_constant_
     __syncwarp();
     tmem_alloc(&S.tmem, 512);
     tmem_relinquish();
+    // (not before: a dependent grid that took the columns first would wait for this one,
+    // which would wait for the columns)
+    pdl_launch_dependents();
   }
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;

@@ -299,3 +299,10 @@ def test_linear_holds_tensor_memory_before_another_grid_may_come():
     launch = launch[:launch.index("cudaLaunchKernelEx")]
     sets = sources.re.findall(r"\n  (?:if [^\n]*)?lc\.dynamicSmemBytes = [^;]*;", launch)
     assert "kSmemLeast" in sets[-1] and not sets[-1].startswith("\n  if")
+
+
+def test_attention_holds_tensor_memory_before_another_grid_may_come():
+    code = sources.body("kvq_wide.cu", "k_kvq_wide")
+    assert code.count("pdl_launch_dependents(") == 1
+    held = code[code.index("tmem_alloc"):code.index("pdl_launch_dependents(")]
+    assert "tmem_relinquish" in held and "{" not in held
