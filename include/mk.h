@@ -588,10 +588,11 @@ typedef struct mk_kvq_cache {
  * gets the scale NaN (0x7F) and the codes 8; infinities saturate.
  * A row whose slot is outside the pool writes nothing there; slots are distinct.
  * mean x^2 + eps has to be a normal number in 32 bits (squares up to 3e38).
- * q_out may be q itself (same stride); any other overlap of inputs and outputs is
- * not allowed, k and v in the very cache rows that slots names (bits 16) apart.
- * q and q_out may be views of the same rows as k and v; any other tensor counts as
- * the stretch from its first value to its last. */
+ * q_out may be q itself (same stride); any other overlap of an output with an input or
+ * another output is refused, each counted as the stretch from its first value to its
+ * last, with two exceptions: q_out may lie between the rows of k and v (at their stride),
+ * and with bits 16 k may be in the k_cache, v in the v_cache, in the very rows that slots
+ * names. */
 typedef struct mk_qkv_append_io {
   int32_t n_rows;            /* >= 0; with 0 every tensor of rows may be NULL      */
   int32_t n_q_heads;         /* 0 iff q is NULL; <= 4096                           */

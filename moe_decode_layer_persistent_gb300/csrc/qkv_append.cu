@@ -463,6 +463,19 @@ void launch_append(const AppendParams& P, bool half, int sms, cudaStream_t s) {
   }
 }
 
+// Whether n rows of `wa` 16-bit values, `sa` apart, and n of `wb`, `sb` apart, have a value
+// in common.  Rows of different strides count as having one where their stretches meet.
+bool rows_meet(const void* a, int64_t wa, int64_t sa, const void* b, int64_t wb, int64_t sb, int64_t n) {
+  if (!a || !b || !overlap(a, span_bytes(n, wa, sa, 2), b, span_bytes(n, wb, sb, 2))) return false;
+  if (n == 1 || sa != sb) return true;
+  // b's row j starts away - m s behind a's row j + m: within that row for m = q, or less than
+  // a row in front of it for m = q + 1
+  const int64_t s = sa * 2;
+  const int64_t away = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  const int64_t q = (away >= 0 ? away : away - s + 1) / s, r = away - q * s;
+  return (r < wa * 2 && q > -n && q < n) || (s - r < wb * 2 && q + 1 > -n && q + 1 < n);
+}
+
 }  // namespace
 
 }  // namespace mk
@@ -505,36 +518,51 @@ mk_status mk_qkv_append(const mk_rope* rope, const mk_qkv_append_io* io, void* s
     return MK_ERR_INVALID_ARG;
   if (io->k && (io->k_stride % 8 || io->k_stride < kw)) return MK_ERR_INVALID_ARG;
   if (io->v && (io->v_stride % 8 || io->v_stride < kw)) return MK_ERR_INVALID_ARG;
-  // what is written, against what is read (k and v may lie between the rows of q_out)
-  const int64_t q_out = io->q ? span_bytes(n, qw, io->q_out_stride, 2) : 0;
-  const int64_t q_in = io->q ? span_bytes(n, qw, io->q_stride, 2) : 0;
-  const int64_t k_in = io->k ? span_bytes(n, kw, io->k_stride, 2) : 0;
-  const int64_t v_in = io->v ? span_bytes(n, kw, io->v_stride, 2) : 0;
+  // What is written against what is read and against one another, each as the stretch from
+  // its first value to its last; but q_out may lie between the rows of k and v, and k and
+  // v in the rows of the 16-bit caches that they go to.
   struct Range { const void* p; int64_t n; };
+  const Range q = {io->q, io->q ? span_bytes(n, qw, io->q_stride, 2) : 0};
+  const Range q_out = {io->q_out, io->q ? span_bytes(n, qw, io->q_out_stride, 2) : 0};
+  const Range k = {io->k, io->k ? span_bytes(n, kw, io->k_stride, 2) : 0};
+  const Range v = {io->v, io->v ? span_bytes(n, kw, io->v_stride, 2) : 0};
   const bool in_place = io->q == io->q_out && io->q_stride == io->q_out_stride;
-  const Range in[] = {{in_place ? nullptr : io->q, q_in}, {rope ? io->positions : nullptr, n * 4},
-                      {io->k ? io->slots : nullptr, n * 8}, {io->q_norm, d * 2}, {io->k ? io->k_norm : nullptr, d * 2}};
-  Range out[5] = {{io->q_out, q_out}, {}, {}, {}, {}};
-  if (io->k && io->bits == 4) {
+  const bool four = io->bits == 4;
+  const Range in[] = {{rope ? io->positions : nullptr, n * 4}, {io->k ? io->slots : nullptr, n * 8},
+                      {io->q_norm, d * 2}, {io->k ? io->k_norm : nullptr, d * 2},
+                      {io->k && four ? io->kvq.k_exp : nullptr, io->n_kv_heads * 4ll},
+                      {io->k && four ? io->kvq.v_exp : nullptr, io->n_kv_heads * 4ll}};
+  Range pools[4] = {};  // codes and scales, or the cache, of k and of v
+  if (io->k && four) {
     const int64_t rows = static_cast<int64_t>(io->kvq.n_pages) * io->kvq.page_size * io->n_kv_heads;
-    out[1] = {io->kvq.k_codes, rows * (d / 2)};
-    out[2] = {io->kvq.k_scales, rows * (d / 16)};
+    pools[0] = {io->kvq.k_codes, rows * (d / 2)};
+    pools[1] = {io->kvq.k_scales, rows * (d / 16)};
     if (io->v) {
-      out[3] = {io->kvq.v_codes, rows * (d / 2)};
-      out[4] = {io->kvq.v_scales, rows * (d / 16)};
+      pools[2] = {io->kvq.v_codes, rows * (d / 2)};
+      pools[3] = {io->kvq.v_scales, rows * (d / 16)};
     }
-    for (int a = 1; a < 5; ++a) {
-      const Range more[] = {{io->kvq.k_exp, io->n_kv_heads * 4ll}, {io->kvq.v_exp, io->n_kv_heads * 4ll},
-                            {io->q, q_in}, {io->q_out, q_out}, {io->k, k_in}, {io->v, v_in}};
-      for (const Range& r : more)
-        if (overlap(r.p, r.n, out[a].p, out[a].n)) return MK_ERR_INVALID_ARG;
-      for (int b = a + 1; b < 5; ++b)
-        if (overlap(out[a].p, out[a].n, out[b].p, out[b].n)) return MK_ERR_INVALID_ARG;
-    }
+  } else if (io->k) {
+    if (io->n_slots > INT64_MAX / 2 / kw) return MK_ERR_INVALID_ARG;
+    pools[0] = {io->k_cache, io->n_slots * kw * 2};
+    if (io->v) pools[2] = {io->v_cache, io->n_slots * kw * 2};
   }
-  for (const Range& r : in)
-    for (const Range& w : out)
-      if (overlap(r.p, r.n, w.p, w.n)) return MK_ERR_INVALID_ARG;
+  auto meet = [](const Range& a, const Range& b) { return overlap(a.p, a.n, b.p, b.n); };
+  for (const Range& r : in) {
+    if (meet(r, q_out)) return MK_ERR_INVALID_ARG;
+    for (const Range& w : pools)
+      if (meet(r, w)) return MK_ERR_INVALID_ARG;
+  }
+  for (int a = 0; a < 4; ++a) {
+    if (meet(q, pools[a]) || meet(q_out, pools[a])) return MK_ERR_INVALID_ARG;
+    if ((four || a >= 2) && meet(k, pools[a])) return MK_ERR_INVALID_ARG;
+    if ((four || a < 2) && meet(v, pools[a])) return MK_ERR_INVALID_ARG;
+    for (int b = a + 1; b < 4; ++b)
+      if (meet(pools[a], pools[b])) return MK_ERR_INVALID_ARG;
+  }
+  if (!in_place && meet(q, q_out)) return MK_ERR_INVALID_ARG;
+  if (io->q && (rows_meet(io->q_out, qw, io->q_out_stride, io->k, kw, io->k_stride, n) ||
+                rows_meet(io->q_out, qw, io->q_out_stride, io->v, kw, io->v_stride, n)))
+    return MK_ERR_INVALID_ARG;
   int sms = 0;
   const mk_status st = check_device(io->q ? io->q_out : io->slots, nullptr, &sms);
   if (st != MK_OK) return st;

@@ -993,3 +993,66 @@ def test_attn_gives_up_and_recovers(cuda_lib, kvq_waiting, what, which):
     torch.cuda.synchronize()
     assert cuda_lib.mk_kvq_attn_status(a["ws"]) == 0
     assert torch.equal(a["out"][:a["n"]], a["want"][0][:a["n"]]) and torch.equal(a["lse"], a["want"][1])
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("n", [1, 9, 700])
+def test_append_takes_q_out_between_the_rows_of_k_and_v(cuda_lib, bits, n):
+    """q from elsewhere, q_out in a tensor that holds k and v too."""
+    mk, rng, hq, hk, d, page = cuda_lib, np.random.default_rng(n + bits), 4, 2, 64, 16
+    pages = n // page + 1
+    q0, q = rounded(rng, (n, hq, d), "bf16")
+    x0, x = rounded(rng, (n, hk + hq + hk, d), "bf16")
+    k, q_out, v = x[:, :hk], x[:, hk:hk + hq], x[:, hk + hq:]
+    slots = rng.permutation(pages * page)[:n]
+    if bits == 16:
+        caches = [torch.zeros(pages, page, hk, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        kw = dict(k_cache=caches[0], v_cache=caches[1])
+    else:
+        caches = pool(rng, pages, hk, page, d) + pool(rng, pages, hk, page, d)
+        kw = dict(kvq=mk.make_kvq_cache(*caches))
+    pos = rng.integers(0, 9000, n)
+    rope = mk.mk_rope_create(mk.make_rope_config(d))
+    at = dev(slots, torch.int64)
+    positions = dev(pos)
+    mk.mk_qkv_append(rope, mk.make_qkv_append_io(q, q_out, k, v, positions, at, **kw))
+    torch.cuda.synchronize()
+    mk.mk_rope_destroy(rope)
+    f, m = ob.rope_frequencies(d)
+    yq, mag = ok.norm_rope(q0, None, 0, pos, d, "half", f, m)
+    assert np.all(np.abs(np64(q_out) - yq) <= mag * 2.0 ** -20 + U["bf16"] * np.abs(yq) + TINY["bf16"])
+    assert np.array_equal(np64(k), x0[:, :hk]) and np.array_equal(np64(v), x0[:, hk + hq:])
+    yk, mag = ok.norm_rope(x0[:, :hk], None, 0, pos, d, "half", f, m)
+    if bits == 16:
+        got = np64(caches[0].view(-1, hk, d)[at])
+        assert np.all(np.abs(got - yk) <= mag * 2.0 ** -20 + U["bf16"] * np.abs(yk) + TINY["bf16"])
+        assert torch.equal(caches[1].view(-1, hk, d)[at], v)
+    else:
+        for y, i in ((yk, 0), (x0[:, hk + hq:], 2)):
+            codes, scales = ok.encode(y)
+            got = [p.transpose(1, 2).reshape(pages * page, hk, -1)[at].cpu().numpy() for p in caches[i:i + 2]]
+            assert np.array_equal(got[0], codes) and np.array_equal(got[1], scales)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("n", [5, 400, 4000])
+def test_append_in_the_rows_of_the_cache(cuda_lib, layout, n):
+    """k and v in the cache already, in the rows that they go to: rotated in place."""
+    mk, rng, hk, d, page = cuda_lib, np.random.default_rng(n), 2, 64, 16
+    pages = n // page + 2
+    held = [rounded(rng, (pages, page, hk, d), "fp16") for _ in range(2)]
+    first = 3
+    rows = [c.view(-1, hk, d)[first:first + n] for _, c in held]
+    pos = rng.integers(0, 9000, n)
+    rope = mk.mk_rope_create(mk.make_rope_config(d, layout=layout))
+    at, positions = dev(np.arange(first, first + n), torch.int64), dev(pos)
+    mk.mk_qkv_append(rope, mk.make_qkv_append_io(None, None, rows[0], rows[1], positions, at, k_cache=held[0][1], v_cache=held[1][1]))
+    torch.cuda.synchronize()
+    mk.mk_rope_destroy(rope)
+    f, m = ob.rope_frequencies(d)
+    k0 = held[0][0].reshape(-1, hk, d)
+    y, mag = ok.norm_rope(k0[first:first + n], None, 0, pos, d, layout, f, m)
+    got = np64(held[0][1].view(-1, hk, d))
+    assert np.all(np.abs(got[first:first + n] - y) <= mag * 2.0 ** -20 + U["fp16"] * np.abs(y) + TINY["fp16"])
+    assert np.array_equal(got[:first], k0[:first]) and np.array_equal(got[first + n:], k0[first + n:])
+    assert np.array_equal(np64(held[1][1]), held[1][0])

@@ -306,3 +306,31 @@ def test_attention_holds_tensor_memory_before_another_grid_may_come():
     assert code.count("pdl_launch_dependents(") == 1
     held = code[code.index("tmem_alloc"):code.index("pdl_launch_dependents(")]
     assert "tmem_relinquish" in held and "{" not in held
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("over", [
+    dict(q_out=A + 2048, q_out_stride=1536), dict(q_out=A + 2560, q_out_stride=1536),        # over k, over v
+    dict(q_out=A + 2048 - 2032, q_out_stride=1536, q=9 * A), dict(q_out=A + 3072 - 16, q_out_stride=1536, q=9 * A),
+    dict(q_out=A - 3072 + 1040, q_out_stride=1536, q=9 * A), dict(q_out=A, q_out_stride=1024, q=9 * A),
+    dict(n_rows=1, q_out=A + 1024, q=9 * A), dict(n_rows=1, q_out=A + 3056, q=9 * A)])
+def test_append_refuses_q_out_over_k_and_v(mk, bits, over):
+    refused(mk, lambda: mk.mk_qkv_append(None, append_io(mk, bits=bits, **over)), INVALID)
+
+
+@pytest.mark.parametrize("over", [
+    dict(v_cache=7 * A), dict(v_cache=7 * A + 16384), dict(k_cache=2 * A + 64), dict(v_cache=2 * A + 64), dict(k_cache=A),
+    dict(v_cache=A), dict(k_cache=A + 3056, q=9 * A), dict(slots=7 * A + 8), dict(slots=8 * A + 8), dict(positions=7 * A + 4),
+    dict(positions=8 * A + 32764), dict(q_norm=7 * A + 16), dict(k_norm=8 * A + 16), dict(v=7 * A, v_stride=256),
+    dict(k=8 * A, k_stride=256), dict(n_slots=1 << 61), dict(n_slots=1 << 20)])
+def test_append_refuses_what_overlaps_a_cache_in_16_bits(mk, over):
+    r = mk.mk_rope_create(mk.make_rope_config(128))
+    try:
+        refused(mk, lambda: mk.mk_qkv_append(r, append_io(mk, bits=16, **over)), INVALID)
+    finally:
+        mk.mk_rope_destroy(r)
+
+
+@pytest.mark.parametrize("over", [dict(k_exp=2 * A), dict(v_exp=2 * A + 64)])
+def test_append_refuses_exponents_under_q_out(mk, over):
+    refused(mk, lambda: mk.mk_qkv_append(None, append_io(mk, pools(mk, **over))), INVALID)
