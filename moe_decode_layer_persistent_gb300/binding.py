@@ -490,14 +490,15 @@ def _kind(fn, T, t):
 
 def _rows(fn, t, shape, dtype, dev):
     """(address, elements between rows) of a tensor [rows, heads, d] whose heads
-    lie side by side."""
+    lie side by side; of a single row, whose stride says nothing, one that every call
+    takes."""
     if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
         _refuse(fn)
     n, h, d = shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         _refuse(fn)
-    return t.data_ptr(), s0 if n > 1 else max(s0, h * d)
+    return t.data_ptr(), s0 if n > 1 or (s0 >= h * d and s0 % 8 == 0) else h * d
 
 
 def _table(fn, t, dtype, dev):
@@ -798,13 +799,14 @@ def mk_kvq_attn_status(workspace):
 
 
 def _matrix(fn, t, rows, cols, dtype, dev):
-    """(address, elements between rows) of a [rows, cols] matrix with contiguous rows."""
+    """(address, elements between rows) of a [rows, cols] matrix with contiguous rows; of
+    a single row, whose stride says nothing, one that every call takes."""
     if t.shape != (rows, cols) or t.dtype is not dtype or t.get_device() != dev:
         _refuse(fn)
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
         _refuse(fn)
-    return t.data_ptr(), s0 if rows > 1 else max(s0, -(-cols // 8) * 8)
+    return t.data_ptr(), s0 if rows > 1 or (s0 >= cols and s0 % 8 == 0) else -(-cols // 8) * 8
 
 
 def make_linear_io(x, w, out, bias=None, act="none", residual=None):

@@ -654,7 +654,7 @@ mk_status call_linear(const mk_linear_io* io, void* workspace, int64_t workspace
     if (!io->x || !io->out || io->x_stride < k || io->out_stride < n) return MK_ERR_INVALID_ARG;
     if (io->residual && io->residual_stride < n) return MK_ERR_INVALID_ARG;
     const int64_t to = span_bytes(m, n, io->out_stride, 2);
-    const bool in_place = io->residual == io->out && io->residual_stride == io->out_stride;
+    const bool in_place = io->residual == io->out && (m == 1 || io->residual_stride == io->out_stride);
     struct Range { const void* p; int64_t n; };
     const Range in[] = {{io->x, span_bytes(m, k, io->x_stride, 2)}, {io->w, span_bytes(n, k, io->w_stride, 2)},
                         {io->bias, n * 2}, {io->residual, span_bytes(m, n, io->residual_stride, 2)}};

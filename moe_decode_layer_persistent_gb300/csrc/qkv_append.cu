@@ -526,7 +526,7 @@ mk_status mk_qkv_append(const mk_rope* rope, const mk_qkv_append_io* io, void* s
   const Range q_out = {io->q_out, io->q ? span_bytes(n, qw, io->q_out_stride, 2) : 0};
   const Range k = {io->k, io->k ? span_bytes(n, kw, io->k_stride, 2) : 0};
   const Range v = {io->v, io->v ? span_bytes(n, kw, io->v_stride, 2) : 0};
-  const bool in_place = io->q == io->q_out && io->q_stride == io->q_out_stride;
+  const bool in_place = io->q == io->q_out && (n == 1 || io->q_stride == io->q_out_stride);
   const bool four = io->bits == 4;
   const Range in[] = {{rope ? io->positions : nullptr, n * 4}, {io->k ? io->slots : nullptr, n * 8},
                       {io->q_norm, d * 2}, {io->k ? io->k_norm : nullptr, d * 2},

@@ -1056,3 +1056,28 @@ def test_append_in_the_rows_of_the_cache(cuda_lib, layout, n):
     assert np.all(np.abs(got[first:first + n] - y) <= mag * 2.0 ** -20 + U["fp16"] * np.abs(y) + TINY["fp16"])
     assert np.array_equal(got[:first], k0[:first]) and np.array_equal(got[first + n:], k0[first + n:])
     assert np.array_equal(np64(held[1][1]), held[1][0])
+
+
+def test_one_row_of_tensors_with_odd_rows(cuda_lib):
+    """x, w and the residual, q, k and v as single rows of tensors whose stride no call
+    would take, and a residual that is the output under another stride."""
+    mk, rng = cuda_lib, np.random.default_rng(41)
+    x0, x = (a[2:3, :256] for a in rounded(rng, (3, 260), "bf16"))     # 16-byte aligned, as 2 * 260 is a multiple of 8
+    w0, w = (a[2:3, :256] for a in rounded(rng, (3, 260), "bf16", 1 / 16))
+    r0, r = rounded(rng, (1, 1), "bf16")
+    out = torch.empty(1, 7, dtype=torch.bfloat16, device="cuda")[:, :1]
+    out.copy_(r)
+    io = mk.make_linear_io(x, w, out, residual=out.as_strided((1, 1), (24, 1)))
+    ws = torch.empty(mk.mk_linear_workspace(io), dtype=torch.uint8, device="cuda")
+    mk.mk_linear(io, ws)
+    want, s = ok.linear(x0, w0, None, "none", r0)
+    assert abs(np64(out) - want) <= s * (16 + 64) * 2 * V + U["bf16"] * abs(want)
+
+    t0, t = rounded(rng, (2, 260), "bf16")
+    q, k, v = (t[:1, a:b].unflatten(1, (-1, 64)) for a, b in ((0, 128), (128, 192), (192, 256)))
+    pools = pool(rng, 1, 1, 16, 64) + pool(rng, 1, 1, 16, 64)
+    slots = dev([5], torch.int64)
+    mk.mk_qkv_append(None, mk.make_qkv_append_io(q, q, k, v, None, slots, kvq=mk.make_kvq_cache(*pools)))
+    for i, a in ((0, 128), (2, 192)):
+        codes, scales = ok.encode(t0[0, a:a + 64])
+        assert np.array_equal(pools[i][0, 0, 5].cpu().numpy(), codes) and np.array_equal(pools[i + 1][0, 0, 5].cpu().numpy(), scales)

@@ -334,3 +334,28 @@ def test_append_refuses_what_overlaps_a_cache_in_16_bits(mk, over):
 @pytest.mark.parametrize("over", [dict(k_exp=2 * A), dict(v_exp=2 * A + 64)])
 def test_append_refuses_exponents_under_q_out(mk, over):
     refused(mk, lambda: mk.mk_qkv_append(None, append_io(mk, pools(mk, **over))), INVALID)
+
+
+def test_a_single_row_has_no_stride(mk):
+    """A view of one row of a tensor whose rows no call would take: nothing is between rows."""
+    import torch
+    x = torch.zeros(6, 60, dtype=torch.bfloat16)
+    for one in (x[3:4, :16], x[3:4].expand(1, 60)[:, :16], x[3].as_strided((1, 16), (0, 1))):
+        address, stride = mk._matrix("f", one, 1, 16, x.dtype, -1)
+        assert address == one.data_ptr() and stride >= 16 and stride % 8 == 0
+        address, stride = mk._rows("f", one.view(1, 2, 8), (1, 2, 8), x.dtype, -1)
+        assert address == one.data_ptr() and stride >= 16 and stride % 8 == 0
+    assert mk._matrix("f", x[:2, :16], 2, 16, x.dtype, -1)[1] == 60
+    assert mk._rows("f", x[:2, :16].view(2, 2, 8), (2, 2, 8), x.dtype, -1)[1] == 60
+
+
+def test_one_row_in_place_whatever_its_strides_say(mk):
+    """Nothing to refuse (what follows is the GPU's absence or presence)."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not memory")
+    for call in (lambda: mk._check("f", mk._lib_mk_linear(linear_io(mk, n_rows=1, out=4 * A, out_stride=400), 64 * A, 1 << 20, None)),
+                 lambda: mk.mk_qkv_append(None, append_io(mk, n_rows=1, q_out=A))):
+        with pytest.raises(mk.MkError) as e:
+            call()
+        assert e.value.status not in (INVALID, UNSUPPORTED)
