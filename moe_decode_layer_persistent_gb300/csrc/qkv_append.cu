@@ -493,7 +493,7 @@ mk_status mk_qkv_append(const mk_rope* rope, const mk_qkv_append_io* io, void* s
   if (d < 8 || d > 256 || d % 8) return MK_ERR_UNSUPPORTED;
   if (rope && rope->cfg.head_dim != d) return MK_ERR_INVALID_ARG;
   if (io->n_q_heads > 4096 || io->n_kv_heads > 4096) return MK_ERR_UNSUPPORTED;
-  if (!(io->eps >= 0.f && io->eps <= 1e30f)) return MK_ERR_INVALID_ARG;
+  if ((io->q_norm || io->k_norm) && !(io->eps >= 0.f && io->eps <= 1e30f)) return MK_ERR_INVALID_ARG;
   if (io->bits == 4 && io->n_kv_heads) {
     const mk_status st = check_kvq(io->kvq, true);
     if (st != MK_OK) return st;

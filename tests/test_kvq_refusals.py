@@ -359,3 +359,11 @@ def test_one_row_in_place_whatever_its_strides_say(mk):
         with pytest.raises(mk.MkError) as e:
             call()
         assert e.value.status not in (INVALID, UNSUPPORTED)
+
+
+@pytest.mark.parametrize("eps", [float("nan"), -1.0, float("inf")])
+def test_append_looks_at_eps_with_a_norm_only(mk, eps):
+    empty = dict(n_rows=0, q=0, q_out=0, k=0, v=0, positions=0, slots=0, eps=eps)
+    mk.mk_qkv_append(None, append_io(mk, **empty, q_norm=0, k_norm=0))
+    for norms in (dict(q_norm=0), dict(k_norm=0), {}):
+        refused(mk, lambda: mk.mk_qkv_append(None, append_io(mk, **empty, **norms)), INVALID)
