@@ -181,7 +181,6 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
       }
       const int rows = rq.n * P.group;  // (checked by the host to be an int)
       int klo = INT_MAX, khi = 0;
-      const float unit_k = pow2(c.k_exp ? clamp_exp(c.k_exp[h]) : 0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int f = rt * R + nt * 8 + g;
@@ -236,10 +235,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
           full_hi = min(full_hi, my_hi);
         }
         if (t == 0) at.lo[nt * 8 + g] = my_lo, at.hi[nt * 8 + g] = my_hi;
-        // (not 0, which a masked score, -infinity, must not meet)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          c_row[nt][k] = fmaxf(P.scale_log2 * __shfl_sync(0xffffffffu, factor, 8 * t + 4 * k) * unit_k, FLT_MIN);
+        for (int k = 0; k < 2; ++k) c_row[nt][k] = score_factor(P, __shfl_sync(0xffffffffu, factor, 8 * t + 4 * k), h);
       }
       klo = __reduce_min_sync(0xffffffffu, klo);
       khi = __reduce_max_sync(0xffffffffu, khi);
@@ -739,7 +736,7 @@ mk_status call_attn(const mk_kvq_attn_io* io, void* workspace, int64_t workspace
   P.io = *io;
   if (!c.n_pages)  // (a pool without pages is never read)
     P.io.kvq.k_codes = P.io.kvq.v_codes = P.io.kvq.k_scales = P.io.kvq.v_scales = const_cast<void*>(io->q);
-  P.scale_log2 = (io->scale != 0.f ? io->scale : 1.f / std::sqrt(static_cast<float>(d))) * (8.f * 1.4426950408889634f);
+  P.scale_log2 = (io->scale != 0.f ? io->scale : 1.f / std::sqrt(static_cast<float>(d))) * 1.4426950408889634f;
   P.group = io->n_q_heads / c.n_kv_heads;
   P.by_group = make_divisor(P.group);
   P.page_shift = __builtin_ctz(static_cast<uint32_t>(c.page_size));

@@ -41,7 +41,7 @@ enum KvqWithhold {
 
 struct KvqParams {
   mk_kvq_attn_io io;
-  float scale_log2;  // scale * log2(e), times 8 (see Scales)
+  float scale_log2;  // scale * log2(e)
   int32_t group;
   int32_t page_shift;
   uint32_t page_bytes;  // of codes
@@ -58,6 +58,14 @@ struct KvqParams {
 };
 
 MK_DEV int clampi(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : static_cast<int>(v); }
+
+// What a row's products are multiplied with to become scores in units of log2; factor: what
+// its q was divided by.  (The 8: see Scales.)  Neither 0, which a masked score, -infinity,
+// must not meet, nor infinity, which a score of 0 must not.
+MK_DEV float score_factor(const KvqParams& P, float factor, int h) {
+  const mk_kvq_cache& c = P.io.kvq;
+  return fminf(fmaxf(P.scale_log2 * factor * (8.f * pow2(c.k_exp ? clamp_exp(c.k_exp[h]) : 0)), FLT_MIN), FLT_MAX);
+}
 
 // One request's lengths, made safe, and its place on the line: for each kv head and
 // row tile an item of its key tiles, in front of them `lead` units for what an item

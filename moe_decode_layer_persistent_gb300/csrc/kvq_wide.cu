@@ -323,14 +323,12 @@ struct Row {
 template <class T, int D, bool kTest>
 MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r, int taken) {
   const mk_kvq_attn_io& io = P.io;
-  const mk_kvq_cache& c = io.kvq;
   const Item& it = r.it;
   const int row = threadIdx.x, f = it.first + (it.folded ? row & (kRows / 2 - 1) : row);
   r.valid = f < it.rows;
   const int i = quotient(r.valid ? f : 0, P.by_group);
   r.hq = it.h * P.group + (r.valid ? f - i * P.group : 0);
   r.at = it.cu + i;
-  r.c = P.scale_log2 * pow2(c.k_exp ? clamp_exp(c.k_exp[it.h]) : 0);
   r.lo = r.hi = 0;
   r.tree = 0;
   if (r.valid) {
@@ -340,6 +338,7 @@ MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r, int taken) {
     r.hi = io.tree_mask ? min(it.len, it.base) : min(it.len, it.base + i + 1);
   }
   if (it.tile >= it.tile_end) return;
+  float factor = 1.f;
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(io.q) + r.at * io.q_stride + r.hq * D);
   uint4 raw[D / 8];
 #pragma unroll
@@ -353,7 +352,7 @@ MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r, int taken) {
     top = max(top & 0xFFFFu, top >> 16);
     const int e = min(max(static_cast<int>(top >> 7), 1), 253);
     const float inv = top < 0x7F80u ? __int_as_float((254 - e) << 23) : 1.f;
-    r.c *= top < 0x7F80u ? __int_as_float(e << 23) : 1.f;
+    factor = top < 0x7F80u ? __int_as_float(e << 23) : 1.f;
 #pragma unroll
     for (int j = 0; j < D / 8; ++j) {
       uint32_t* x = reinterpret_cast<uint32_t*>(&raw[j]);
@@ -364,7 +363,7 @@ MK_DEV void take_row(const KvqParams& P, WideSmem<D>& S, Row& r, int taken) {
       }
     }
   }
-  r.c = fmaxf(r.c, FLT_MIN);  // (a masked score, -infinity, must not meet 0)
+  r.c = score_factor(P, factor, it.h);
 #pragma unroll
   for (int j = 0; j < D / 8; ++j)
     raw[j] = make_uint4(__byte_perm(raw[j].x, raw[j].z, 0x5410), __byte_perm(raw[j].x, raw[j].z, 0x7632),

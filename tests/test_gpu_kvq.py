@@ -1081,3 +1081,14 @@ def test_one_row_of_tensors_with_odd_rows(cuda_lib):
     for i, a in ((0, 128), (2, 192)):
         codes, scales = ok.encode(t0[0, a:a + 64])
         assert np.array_equal(pools[i][0, 0, 5].cpu().numpy(), codes) and np.array_equal(pools[i + 1][0, 0, 5].cpu().numpy(), scales)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_attn_scales_up_to_the_largest(cuda_lib, new, dtype):
+    """The largest scale that is taken, with rows of zeros, whose scores are 0; and with
+    rows so small that their scores are ordinary ones."""
+    for scale, by in ((1.7e38, 0.0), (2.0 ** 126, 2.0 ** -126 if dtype == "bf16" else 0.0), (2.0 ** 100, 2.0 ** -100 if dtype == "bf16" else 0.0)):
+        a = make_attn(np.random.default_rng(new), [50, 200], [new, new], 4, 1, 64, dtype, 16, q_scale=by)
+        call_attn(cuda_lib, a, scale=scale)
+        check_attn(cuda_lib, a, scale=scale)
