@@ -97,7 +97,8 @@ MK_DEV Req read_req(const KvqParams& P, int b) {
   r.n = clampi(io.cu_rows[b + 1], r.cu, io.n_rows) - r.cu;
   r.len = clampi(io.lens[b], 0, io.max_pages << P.page_shift);
   r.base = max(0, r.len - r.n);
-  const int low = io.window ? max(0, r.base - io.window + 1) : 0;
+  // (a row with an empty tree word is at base - 1)
+  const int low = io.window ? max(0, r.base - io.window + (io.tree_mask ? 0 : 1)) : 0;
   r.tile0 = low / KEYS;
   r.lead = KEYS == 32 ? kLead : kWideLead;
   // (at least one, so that rows without keys are written)

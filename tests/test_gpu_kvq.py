@@ -1092,3 +1092,17 @@ def test_attn_scales_up_to_the_largest(cuda_lib, new, dtype):
         a = make_attn(np.random.default_rng(new), [50, 200], [new, new], 4, 1, 64, dtype, 16, q_scale=by)
         call_attn(cuda_lib, a, scale=scale)
         check_attn(cuda_lib, a, scale=scale)
+
+
+@pytest.mark.parametrize("news", [[3, 5, 2], [24, 40, 30]])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp16", 128)])
+def test_attn_empty_tree_words_under_a_window(cuda_lib, news, dtype, d):
+    """A row with an empty word (a padded one) is at base - 1: its window begins a key
+    earlier than all others', which here is the last of a key tile."""
+    # (made without window and words, which would hide the key that the empty word's row sees)
+    a = make_attn(np.random.default_rng(d), [base + n for base, n in zip((95, 191, 319), news)], news, 4, 1, d, dtype, 16)
+    a["window"] = 64
+    a["words"] = [0 if i == n // 2 else (1 << n) - 1 for n in news for i in range(n)] + [0] * 2
+    hide_unseen(a)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
