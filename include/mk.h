@@ -678,7 +678,9 @@ typedef struct mk_kvq_attn_io {
   const int32_t* block_table;  /* [B, max_pages]                                  */
   const int32_t* lens;         /* [B]                                             */
   const int32_t* cu_rows;      /* [B + 1]                                         */
-  const uint64_t* tree_mask;   /* optional [n_rows], as for mk_prefix_attn        */
+  const uint64_t* tree_mask;   /* optional [n_rows], as for mk_prefix_attn; here a
+                                  word may leave its own row out or be empty, as
+                                  of a padded row                                 */
   void* out;                   /* [n_rows, n_q_heads, d]; not q                   */
   int64_t out_stride;          /* elements between rows, a multiple of 8          */
   float* lse;                  /* optional [n_rows, n_q_heads]                    */

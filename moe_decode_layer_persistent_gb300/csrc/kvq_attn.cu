@@ -60,6 +60,7 @@ struct Layout {
 template <int R>
 struct Stretch {
   int64_t pos, begin, part;
+  uint64_t tree;  // bits of all rows' tree words
   int32_t b, h, cu, rows, first, base, whole, klo, khi;
   int32_t lo[R], hi[R];  // keys that each row sees (of a tree: those before its own)
 };
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
       }
       const int rows = rq.n * P.group;  // (checked by the host to be an int)
       int klo = INT_MAX, khi = 0;
+      uint64_t tree = 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int f = rt * R + nt * 8 + g;
@@ -226,7 +228,9 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
         }
         int my_lo = 0, my_hi = 0;
         if (valid) {
-          const int p = rq.base + (io.tree_mask ? __popcll(io.tree_mask[row]) - 1 : i);
+          const uint64_t word = io.tree_mask ? io.tree_mask[row] : 0;
+          tree |= word;
+          const int p = rq.base + (io.tree_mask ? __popcll(word) - 1 : i);
           my_lo = io.window ? max(0, p - io.window + 1) : 0;
           my_hi = io.tree_mask ? min(rq.len, rq.base) : min(rq.len, rq.base + i + 1);
           klo = min(klo, my_lo);
@@ -240,6 +244,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
       }
       klo = __reduce_min_sync(0xffffffffu, klo);
       khi = __reduce_max_sync(0xffffffffu, khi);
+      tree = bits_of_all(tree);
       full_lo = __reduce_max_sync(0xffffffffu, full_lo);
       full_hi = __reduce_min_sync(0xffffffffu, full_hi);
       tile = max(rq.tile0 + ta, min(klo, khi) / kKeys);
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
         at.pos = to;
         at.begin = begin;
         at.b = b, at.h = h, at.cu = rq.cu, at.rows = rows, at.first = rt * R, at.base = rq.base;
-        at.whole = whole, at.klo = klo, at.khi = khi;
+        at.whole = whole, at.klo = klo, at.khi = khi, at.tree = tree;
         at.part = 2ll * worker + (ta == 0);
         if (ta == 0 && !whole) P.split[worker] = {parts_of(rq, start, share), 0, rq.cu, rows, rt * R, h};
       }
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
       __syncwarp();
       issue(ring32 + stage_in);
       stage_in = next_stage(stage_in);
-      const uint8_t* st = ring + stage;
+      uint8_t* st = ring + stage;
       stage = next_stage(stage);
       float sc[2][NT][4];
       // scores: of each block rows g and g + 8 are the keys key_g and key_g + 8
@@ -362,6 +367,14 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
       }
       const bool edge = tile * kKeys < full_lo || tile * kKeys + kKeys > full_hi;
       if (edge) {
+        // keys that no row sees may hold anything: a weight of 0 must meet a number
+        const int j = tile * kKeys + lane;
+        if (j < at.klo || j >= at.khi || (io.tree_mask && j >= at.base && !(at.tree >> (j - at.base) & 1))) {
+          uint8_t* scales = st + (lane >> 4) * L::kBlock + L::kVs + (lane & 15) * (D / 16);
+          if (D == 128) *reinterpret_cast<uint2*>(scales) = make_uint2(0, 0);
+          else *reinterpret_cast<uint32_t*>(scales) = 0;
+        }
+        __syncwarp();
 #pragma unroll 1
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -441,11 +454,6 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) k_kvq_attn(const __grid_co
             w[2 * k][0] = *reinterpret_cast<const uint32_t*>(sb + L::kV + ka * 32 + g * 4);
             w[2 * k + 1][0] = *reinterpret_cast<const uint32_t*>(sb + L::kV + kb * 32 + g * 4);
             sa = sb[L::kVs + ka * 4 + g / 2], sb8 = sb[L::kVs + kb * 4 + g / 2];
-          }
-          if (edge) {  // keys that no row sees may hold anything
-            const int j0 = tile * kKeys + blk * 16, lo = at.klo, hi = at.khi;
-            if (j0 + ka < lo || j0 + ka >= hi) sa = 0;
-            if (j0 + kb < lo || j0 + kb >= hi) sb8 = 0;
           }
           f[k] = make_scales(sa | sb8 << 8);
         }

@@ -57,6 +57,12 @@ struct KvqParams {
   bool test;
 };
 
+// The bits that any lane has.
+MK_DEV uint64_t bits_of_all(uint64_t x) {
+  const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x));
+  const uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x >> 32));
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
 MK_DEV int clampi(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : static_cast<int>(v); }
 
 // What a row's products are multiplied with to become scores in units of log2; factor: what

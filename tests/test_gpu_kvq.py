@@ -1106,3 +1106,22 @@ def test_attn_empty_tree_words_under_a_window(cuda_lib, news, dtype, d):
     hide_unseen(a)
     call_attn(cuda_lib, a)
     check_attn(cuda_lib, a)
+
+
+@pytest.mark.parametrize("news", [[3, 1, 2], [24, 64, 30], [2, 16, 9]])
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp16", 128)])
+def test_attn_tree_keys_that_no_row_sees(cuda_lib, news, window, dtype, d):
+    """Words that leave their own row out, some of them empty (padded rows): what no row
+    sees between the tree's keys has NaN scales like any other such key."""
+    rng = np.random.default_rng(sum(news) + d)
+    a = make_attn(rng, [base + n for base, n in zip((95, 141, 0), news)], news, 4, 1, d, dtype, 16)
+    a["window"] = window
+    words = []
+    for n in news:
+        kept = int(rng.integers(0, 1 << 62)) & ((1 << n) - 1)
+        words += [kept & int(rng.integers(0, 1 << 62)) if i % 3 else 0 for i in range(n)]
+    a["words"] = words + [0] * 2
+    hide_unseen(a)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
