@@ -1125,3 +1125,39 @@ def test_attn_tree_keys_that_no_row_sees(cuda_lib, news, window, dtype, d):
     hide_unseen(a)
     call_attn(cuda_lib, a)
     check_attn(cuda_lib, a)
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_attn_pages_of_65536_keys(cuda_lib, new):
+    """The largest page: requests that end inside it, and one that goes on into another."""
+    a = make_attn(np.random.default_rng(new), [66000, 300, 65536], [new, 2, 1], 4, 1, 64, "bf16", 65536)
+    call_attn(cuda_lib, a)
+    check_attn(cuda_lib, a)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_append_to_pages_of_65536_keys(cuda_lib, bits):
+    rng = np.random.default_rng(42)
+    check_append(cuda_lib, rng, 60, 4, 2, 64, 64, "half", "bf16", rng.integers(0, 1 << 20, 60), bits, page=65536)
+
+
+def test_attention_takes_the_largest_page(cuda_lib):
+    """Four kv heads of 128 in one page of 65536 keys: 16 MB of codes."""
+    rng = np.random.default_rng(43)
+    pools = pool(rng, 1, 4, 65536, 128) + pool(rng, 1, 4, 65536, 128)
+    kvq = cuda_lib.make_kvq_cache(*pools)
+    q0, q = rounded(rng, (2, 8, 128), "bf16")
+    out, lse = torch.empty_like(q), torch.empty(2, 8, device="cuda")
+    lens, cu, table = dev([700, 65536]), dev([0, 1, 2]), dev([[0], [0]])
+    for s in pools[1::2]:
+        s.copy_(torch.from_numpy(rng.integers(16, 32, s.shape, dtype=np.uint8)))
+    io = cuda_lib.make_kvq_attn_io(q, kvq, out, lens, cu, table, lse=lse)
+    ws = torch.empty(cuda_lib.mk_kvq_attn_workspace(io), dtype=torch.uint8, device="cuda")
+    cuda_lib.mk_kvq_attn(io, ws)
+    k, v = (ok.decode_pool(pools[i].cpu().numpy(), pools[i + 1].cpu().numpy(), np.zeros(4, int)) for i in (0, 2))
+    want, want_lse, weight = ob.prefix_attn(q0, k, v, [], 0, np.zeros((2, 1), int), np.array([700, 65536]), np.array([0, 1, 2]))
+    size = lambda x: float(np.sqrt((x * x).sum(-1).max()))  # noqa: E731
+    e_s = 3 * 128 ** 0.5 * V * size(q0) * size(k) + 2.0 ** -19
+    tol = weight * (2.0 ** -11 + 2 * e_s + (65536 / 16 + 64) * 2 * V) + 65536 * 2.0 ** -25 * np.abs(v).max() + U["bf16"] * np.abs(want) + TINY["bf16"]
+    assert np.all(np.abs(np64(out) - want) <= tol)
+    assert np.all(np.abs(np64(lse) - want_lse) <= e_s + (65536 + 64) * V + 4 * V * np.abs(want_lse))
