@@ -517,7 +517,7 @@ mk_status encode_tmap(CUtensorMap* map, int dtype, const void* base, uint64_t in
 
 // How many clusters of 2 .. 8 CTAs, one CTA per SM, run at the same time: less than
 // the SMs divided by their size, as a cluster's SMs lie side by side.
-template <class T>
+template <class T, bool kTest>
 mk_status max_clusters(int device, int sms, int (&most)[9]) {
   static std::atomic<int> known[64][9];
   for (int c = 1; c <= 8; ++c) {
@@ -533,7 +533,7 @@ mk_status max_clusters(int device, int sms, int (&most)[9]) {
       lc.gridDim = dim3(c * sms);
       lc.blockDim = dim3(kThreads);
       lc.dynamicSmemBytes = kSmem;
-      MK_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_linear<T, false, false>, &lc));
+      MK_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_linear<T, false, kTest>, &lc));
       if (device < 64) known[device][c].store(n, std::memory_order_relaxed);
     }
     most[c] = n;
@@ -606,7 +606,7 @@ mk_status linear(LinearParams* P, int device, int sms, cudaStream_t s) {
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   int most[9] = {};
-  mk_status st = max_clusters<T>(device, sms, most);
+  mk_status st = max_clusters<T, kTest>(device, sms, most);
   if (st != MK_OK) return st;
   choose(P, most);
   const mk_linear_io& io = P->io;
