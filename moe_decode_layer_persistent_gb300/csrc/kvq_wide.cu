@@ -266,21 +266,23 @@ MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
   int done = 0, items = 0;
   Item it;
   uint64_t hidden = 0;  // keys from it.base on that no row's tree word has
+  int hidden_from = INT_MAX;  // first key tile with such
   // O += P V of a tile
   auto pv = [&](int at, int tile) {
     const int buf = at & 1, vb = at % kValues;
     const bool first = tile == it.tile;
-    if (!wait_warp<kTest>(P, S, &S.v_full[vb], (at / kValues) & 1) || !wait_warp<kTest>(P, S, &S.p_full[buf], (at >> 1) & 1)) return false;
-    const int j0 = tile * kKeys;
-    if (hidden && j0 + kKeys > it.base) {
+    if (!wait_warp<kTest>(P, S, &S.v_full[vb], (at / kValues) & 1)) return false;
+    if (tile >= hidden_from) {
       // They may hold anything, and a weight of 0 must meet a number.  (Here 16 trees over
       // 16384 keys take 89 us, 88 without; by the warps that convert, 92 to 97.)
+      const int j0 = tile * kKeys;
       for (int j = max(j0, it.base); j < min(j0 + kKeys, it.khi); ++j)
         if (hidden >> (j - it.base) & 1 && lane_id() < D / 8)
           *reinterpret_cast<uint4*>(S.v[vb] + (lane_id() >> 3) * (kKeys * 128) + (j - j0) * 128 + (lane_id() & 7) * 16) = make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
     }
+    if (!wait_warp<kTest>(P, S, &S.p_full[buf], (at >> 1) & 1)) return false;
     tc_fence_after();
     if (elect_one()) {
       const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(S.v[vb]), kKeys * 128);
@@ -320,6 +322,7 @@ MK_DEV bool issue_mmas(const KvqParams& P, WideSmem<D>& S, Walk walk) {
         const int i1 = quotient(min(it.rows, it.first + kRows) - 1, P.by_group);
         for (int i = quotient(it.first, P.by_group) + static_cast<int>(lane_id()); i <= i1; i += 32) tree |= io.tree_mask[it.cu + i];
         hidden = ~bits_of_all(tree);
+        hidden_from = it.base / kKeys;
       }
       if (t && !pv(done - 1, it.tile + t - 1)) return false;
     }
