@@ -654,14 +654,17 @@ mk_status mk_kvq_read(const mk_kvq_read_io* io, void* stream);
  *
  * Keys and values come into the products exactly; q is held in 11 bits relative to
  * its row's largest value or better; the softmax weights are rounded to fp16 (11
- * bits) before they multiply v; scores, maxima, sums and out are held in 32 bits
- * and out is rounded once.  Two calls on the same inputs give the same bits.
+ * bits) before they multiply v, and those below 2^-31 of a row's largest count in its
+ * sum only; scores, maxima, sums and out are held in 32 bits and out is rounded once.  Two calls on the same inputs give the same bits.
  * lens outside 0 .. max_pages * page_size and cu_rows outside 0 .. n_rows are
  * taken as the nearer end, and a page outside 0 .. n_pages-1 reads as zeros.  A
  * cu_rows that falls leaves out and lse undefined.  Scores up to 2^26 are held to.
  * A page's codes (n_kv_heads * page_size * d / 2 bytes) are less than 2^31.  No
  * output may overlap an input; a tensor of rows counts from its first value to its
- * last, what lies between its rows included. */
+ * last, what lies between its rows included.
+ * A call goes through one kernel, by its requests' rows per kv head on average (up to 8,
+ * up to 16, more): single tokens beside long chunks take less time in a call of their
+ * own. */
 typedef struct mk_kvq_attn_io {
   int32_t n_requests;          /* B, 1 .. 65536                                   */
   int32_t n_rows;              /* rows of q, >= 0                                 */
@@ -702,11 +705,11 @@ mk_status mk_kvq_attn_status(const void* workspace);
 
 /* Projection with bias, activation and residual:
  *   out = act(x w^T + bias) + residual,
- * summed in 32 bits and rounded once.  MK_ACT_SILU: y / (1 + e^-y);
- * MK_ACT_GELU: y (1 + erf(y / sqrt 2)) / 2; MK_ACT_GELU_TANH: y (1 + tanh(sqrt(2 / pi)
- * (y + 0.044715 y^3))) / 2.  residual may be out itself (same stride); any other
- * overlap of an input with out, counted as for mk_kvq_attn, is not allowed.  Two calls on the same inputs give
- * the same bits. */
+ * summed in 32 bits and rounded once; an activation's result below 2^-119 may be 0.
+ * MK_ACT_SILU: y / (1 + e^-y); MK_ACT_GELU: y (1 + erf(y / sqrt 2)) / 2;
+ * MK_ACT_GELU_TANH: y (1 + tanh(sqrt(2 / pi) (y + 0.044715 y^3))) / 2.  residual may be
+ * out itself (same stride); any other overlap of an input with out, counted as for
+ * mk_kvq_attn, is not allowed.  Two calls on the same inputs give the same bits. */
 typedef enum { MK_ACT_NONE = 0, MK_ACT_SILU = 1, MK_ACT_GELU = 2, MK_ACT_GELU_TANH = 3 } mk_act;
 
 typedef struct mk_linear_io {

@@ -23,8 +23,15 @@
 // programmatic dependent launch, joins in the order of the line.
 //
 // What bounds it: 64 requests of one row and up to 8192 keys (32 heads over 8, d 128,
-// 304 MB) take 69 us with the join, 5.8 TB/s between start and end, at 2.3 instructions
-// per cycle and SM; the conversions issue while HBM is waited for, but not freely.
+// 304 MB) take 66 us with the join; what more keys add comes at 6.1 TB/s, and 17 us are
+// start, join and ends (twice the keys 116 us, four times 215).  2.1 instructions per cycle
+// and SM: the conversions issue while HBM is waited for, but not freely.
+//
+// A call takes one kernel, by its requests' rows on average: single tokens beside a long
+// chunk go the way of many rows (64 of those above, 66 us, and 512 rows over 8192 keys,
+// 102 us by themselves, take 267 us in one call), and a request of many rows among single
+// tokens is read once per 8 or 16 rows (60 rows in place of the 512: 31 us, in one call
+// 113).  Calls of their own take less there.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -615,7 +622,7 @@ int64_t lay_out(int workers, int rows, int d, uint8_t* base, KvqParams* P) {
   return align256(at + 2ll * workers * rows * d * 4);
 }
 
-// Rows per tile, by what the requests' rows of a kv head are on average.
+// Rows per tile, by what the requests' rows of a kv head are on average (see above).
 int rows_of_tile(const mk_kvq_attn_io* io) {
   const int64_t group = io->n_q_heads / io->kvq.n_kv_heads, rows = io->n_rows * group;
   return rows > 16ll * io->n_requests ? kWideRows : rows > 8ll * io->n_requests ? 16 : 8;

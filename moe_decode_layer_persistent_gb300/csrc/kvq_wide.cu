@@ -16,11 +16,12 @@
 // of all items lie on one line, of which each CTA (one per SM) takes an equal stretch;
 // k_kvq_join joins what lies in several.
 //
-// What bounds it: a key tile takes the converting warps about 2300 cycles (issue of the
-// copies 600, K and V 700 each, fence and hand-off 300), the chain from S by way of the
-// weights to P V two thirds of that and more, the tensor cores 1024.  16 requests of up
-// to 16 rows (32 heads over 8) and 16384 keys of d 128: 87 us, 157 MB, the tensor pipe
-// active 34 % of the time; on row tiles of 16 without tcgen05 143 us.
+// What bounds it: a key tile takes the converting warps about 2400 cycles (issue of the
+// copies 430, K and V 500 each and 200 each until their buffers are free, fence and
+// hand-off 420), the chain from S (920) by way of the weights (1630) to P V 3500 for two
+// tiles at a time, the tensor cores 1024 (by time stamps, which slow the kernel by a
+// seventh).  16 requests of up to 16 rows (32 heads over 8) and 16384 keys of d 128: 89 us,
+// 157 MB, the tensor pipe active 33 % of the time; on row tiles of 16 without tcgen05 143 us.
 // Copies by warps of their own (bulk or cp.async) take 110 us, twelve converting warps 93.
 #include <algorithm>
 #include <atomic>

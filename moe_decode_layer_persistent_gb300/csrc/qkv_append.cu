@@ -10,9 +10,11 @@
 // for every head of a row that a thread works on: they are made once per row.
 //
 // What bounds it: of 8192 rows (32 + 2 x 8 heads of 128, norms, into 4 bits) the
-// instructions, 4290 per row: 52 us for 177 MB, where HBM would take 26.  Few rows: the
-// launch, and groups near a border one after the other in 64 bits (64 rows: 4 us more
-// than into 16 bits).  Reading those rows' values back: 13 us.
+// instructions, 4290 per row at 2.6 a cycle and SM, of which 4 could issue: 53 us for 177
+// MB, where HBM would take 26 (into 16 bits 47 us for 30).  Few rows: the launch, and groups
+// near a border one after the other in 64 bits (64 rows: 4 us more than into 16 bits).
+// Reading those rows' values back, 12 us for 6.4: a word of codes and a scale per thread
+// and turn, four turns one after the other.
 #include <algorithm>
 #include <climits>
 #include <math_constants.h>
