@@ -311,8 +311,8 @@ def test_attention_holds_tensor_memory_before_another_grid_may_come():
 @pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("over", [
     dict(q_out=A + 2048, q_out_stride=1536), dict(q_out=A + 2560, q_out_stride=1536),        # over k, over v
-    dict(q_out=A + 2048 - 2032, q_out_stride=1536, q=9 * A), dict(q_out=A + 3072 - 16, q_out_stride=1536, q=9 * A),
-    dict(q_out=A - 3072 + 1040, q_out_stride=1536, q=9 * A), dict(q_out=A, q_out_stride=1024, q=9 * A),
+    dict(q_out=A + 2048 - 2032, q_out_stride=1536, q=9 * A), dict(q_out=A + 2 * 1536 - 16, q_out_stride=1536, q=9 * A),
+    dict(q_out=A - 2 * 1536 + 1040, q_out_stride=1536, q=9 * A), dict(q_out=A, q_out_stride=1024, q=9 * A),
     dict(n_rows=1, q_out=A + 1024, q=9 * A), dict(n_rows=1, q_out=A + 3056, q=9 * A)])
 def test_append_refuses_q_out_over_k_and_v(mk, bits, over):
     refused(mk, lambda: mk.mk_qkv_append(None, append_io(mk, bits=bits, **over)), INVALID)
